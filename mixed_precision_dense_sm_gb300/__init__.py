@@ -14,9 +14,14 @@ and ``gemm_layernorm_plan_query`` (LayerNorm after the linear layer),
 ``gemm_debug_set`` and ``gemm_run_noalloc``; and include/softmax_sm103.h: ``softmax_rows``,
 ``softmax_plan_query``, ``softmax_sync``, ``softmax_debug_set``; and
 include/conv_sm103.h: ``conv2d_fprop``, ``conv2d_plan_query``,
-``conv2d_output_dims``.
-``Gemm`` wraps a handle and adds ``__call__`` for torch tensors; ``softmax``
-does the same for the row softmax.
+``conv2d_output_dims``; include/glu_sm103.h (the gated linear layer):
+``glu_forward``, ``glu_backward``, ``glu_plan_query``; include/norm_sm103.h
+(norms around a block): ``norm_block_forward``, ``norm_block_backward``,
+``norm_block_backward_workspace``; include/grad_sm103.h (gradient norm and
+clipping): ``grad_clip_raw``, ``grad_clip_workspace``.
+``Gemm`` wraps a handle and adds ``__call__``, ``layernorm``, ``glu`` and
+``glu_backward`` for torch tensors; ``softmax``, ``norm_block``,
+``norm_block_backward`` and ``grad_clip`` do the same for the others.
 """
 from __future__ import annotations
 
@@ -27,7 +32,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgemm_sm103.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "gemm_sm103.h")
 HEADERS = [HEADER, os.path.join(os.path.dirname(HERE), "include", "softmax_sm103.h"),
-           os.path.join(os.path.dirname(HERE), "include", "conv_sm103.h")]
+           os.path.join(os.path.dirname(HERE), "include", "conv_sm103.h"),
+           os.path.join(os.path.dirname(HERE), "include", "glu_sm103.h"),
+           os.path.join(os.path.dirname(HERE), "include", "norm_sm103.h"),
+           os.path.join(os.path.dirname(HERE), "include", "grad_sm103.h")]
 
 GEMM_F16, GEMM_BF16, GEMM_F32 = 0, 1, 2
 STATUS = {0: "GEMM_OK", 1: "GEMM_ERR_INVALID_VALUE", 2: "GEMM_ERR_NOT_SUPPORTED",
@@ -54,6 +62,39 @@ class LayerNorm(ctypes.Structure):
     _fields_ = [("bias", ctypes.c_void_p), ("bias_dtype", ctypes.c_int32),
                 ("gamma", ctypes.c_void_p), ("shift", ctypes.c_void_p),
                 ("ln_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class GluForward(ctypes.Structure):
+    _fields_ = [("activation", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("bias_dtype", ctypes.c_int32), ("P", ctypes.c_void_p), ("ldp", ctypes.c_int64)]
+
+
+class GluBackward(ctypes.Structure):
+    _fields_ = [("activation", ctypes.c_int32), ("p_dtype", ctypes.c_int32),
+                ("dP", ctypes.c_void_p), ("lddp", ctypes.c_int64),
+                ("dX", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("dx_dtype", ctypes.c_int32),
+                ("dW", ctypes.c_void_p), ("lddw", ctypes.c_int64), ("dw_dtype", ctypes.c_int32),
+                ("beta_w", ctypes.c_float),
+                ("dbias", ctypes.c_void_p), ("dbias_dtype", ctypes.c_int32)]
+
+
+NORM_KINDS = {None: 0, "none": 0, "rms": 1, "layer": 2}
+NORM_MAX_N = 16384
+
+
+class NormBlock(ctypes.Structure):
+    _fields_ = [("pre", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("pre_weight", ctypes.c_void_p), ("pre_bias", ctypes.c_void_p),
+                ("post_weight", ctypes.c_void_p), ("post_bias", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("ld_gate", ctypes.c_int64),
+                ("gate_rows", ctypes.c_int64), ("vec_dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+class NormBlockGrads(ctypes.Structure):
+    _fields_ = [("d_pre_weight", ctypes.c_void_p), ("d_pre_bias", ctypes.c_void_p),
+                ("d_post_weight", ctypes.c_void_p), ("d_post_bias", ctypes.c_void_p),
+                ("d_gate", ctypes.c_void_p), ("grad_dtype", ctypes.c_int32)]
 
 
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
@@ -141,6 +182,26 @@ def _load():
     lib.conv2d_plan_query.restype = ctypes.c_int
     lib.conv2d_plan_query.argtypes = conv_geo + [ctypes.c_float, vp, vp, ctypes.c_float, vp,
                                                  Dtypes, i32, i32, ctypes.POINTER(Plan)]
+    glu_args = [i64, i64, i64, vp, i64, vp, i64, vp, i64, Dtypes, ctypes.POINTER(GluForward)]
+    lib.glu_forward.restype = ctypes.c_int
+    lib.glu_forward.argtypes = [vp] + glu_args + [vp]
+    lib.glu_plan_query.restype = ctypes.c_int
+    lib.glu_plan_query.argtypes = glu_args + [i32, i32, ctypes.POINTER(Plan)]
+    lib.glu_backward.restype = ctypes.c_int
+    lib.glu_backward.argtypes = [vp, i64, i64, i64, vp, i64, vp, i64, vp, i64, vp, i64, i32,
+                                 ctypes.POINTER(GluBackward), vp]
+    lib.norm_block_forward.restype = ctypes.c_int
+    lib.norm_block_forward.argtypes = [i64, i64] + [vp, i64] * 4 + [
+        i32, i32, ctypes.POINTER(NormBlock), vp]
+    lib.norm_block_backward.restype = ctypes.c_int
+    lib.norm_block_backward.argtypes = [i64, i64] + [vp, i64] * 6 + [
+        i32, i32, ctypes.POINTER(NormBlock), ctypes.POINTER(NormBlockGrads), vp, i64, vp]
+    lib.norm_block_backward_workspace.restype = i64
+    lib.norm_block_backward_workspace.argtypes = [i64, i64, i64, i32]
+    lib.grad_clip.restype = ctypes.c_int
+    lib.grad_clip.argtypes = [i64, vp, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp, vp, i64, vp]
+    lib.grad_clip_workspace.restype = i64
+    lib.grad_clip_workspace.argtypes = [i64, i32]
     lib.softmax_sync.restype = ctypes.c_int
     lib.softmax_sync.argtypes = [vp]
     lib.softmax_debug_set.restype = ctypes.c_int
@@ -257,12 +318,13 @@ def gemm_plan_query(transA, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc
 
 
 def declared_symbols():
-    """Function names declared in include/gemm_sm103.h and softmax_sm103.h."""
+    """Function names declared in the headers under include/."""
     import re
     names = set()
     for h in HEADERS:
         text = open(h).read()
-        names |= set(re.findall(r"^\s*(?:gemm_status_t|const char\*)\s+((?:gemm|softmax|conv2d)_\w+)\s*\(",
+        names |= set(re.findall(r"^\s*(?:gemm_status_t|const char\*|int64_t)\s+"
+                                r"((?:gemm|softmax|conv2d|glu|norm|grad)_\w+)\s*\(",
                                 text, flags=re.M))
     return sorted(names)
 
@@ -348,6 +410,295 @@ def softmax(X, Y=None, rows=None, cols=None, stream=None):
     if st != 0:
         raise GemmError(st, "softmax_rows")
     return Y
+
+
+# ----------------------------------------------------- the gated linear layer
+
+def glu_forward(h, M, F, K, X, ldx, W, ldw, H, ldh, dtypes, act=ACT_NONE, bias=0,
+                bias_dtype=GEMM_F32, P=0, ldp=0, stream=0) -> int:
+    """Raw C-ABI call (include/glu_sm103.h): H = act(X Wg^T + bg) * (X Wu^T + bu),
+    W = [Wg; Wu] stored 2F x K; P (0 for none) receives X W^T + bias.  Device
+    addresses; returns the gemm_status_t code."""
+    o = GluForward(act, bias or None, bias_dtype, P or None, ldp)
+    return lib.glu_forward(h, M, F, K, X, ldx, W, ldw, H, ldh, Dtypes(*dtypes), ctypes.byref(o),
+                           stream)
+
+
+def glu_plan_query(M, F, K, X, ldx, W, ldw, H, ldh, dtypes, act=ACT_NONE, bias=0,
+                   bias_dtype=GEMM_F32, P=0, ldp=0, num_sms=152, smem_optin=232448):
+    """(status, plan dict) glu_forward would use (host logic only)."""
+    o = GluForward(act, bias or None, bias_dtype, P or None, ldp)
+    plan = Plan()
+    st = lib.glu_plan_query(M, F, K, X, ldx, W, ldw, H, ldh, Dtypes(*dtypes), ctypes.byref(o),
+                            num_sms, smem_optin, ctypes.byref(plan))
+    return st, (plan.as_dict() if st == 0 else None)
+
+
+def glu_backward(h, M, F, K, dH, lddh, P, ldp, X, ldx, W, ldw, dtype, dP, lddp, act=ACT_NONE,
+                 p_dtype=None, dX=0, lddx=0, dx_dtype=GEMM_F32, dW=0, lddw=0, dw_dtype=GEMM_F32,
+                 beta_w=0.0, dbias=0, dbias_dtype=GEMM_F32, stream=0) -> int:
+    """Raw C-ABI call of the gated linear layer's backward pass; p_dtype None
+    means dtype.  Returns the gemm_status_t code."""
+    o = GluBackward(act, dtype if p_dtype is None else p_dtype, dP or None, lddp, dX or None, lddx,
+                    dx_dtype, dW or None, lddw, dw_dtype, beta_w, dbias or None, dbias_dtype)
+    return lib.glu_backward(h, M, F, K, dH or None, lddh, P or None, ldp, X or None, ldx,
+                            W or None, ldw, dtype, ctypes.byref(o), stream)
+
+
+# ------------------------------------------------------- norms around a block
+
+def norm_block_forward(M, N, X, ldx, Z, ldz, XO, ldxo, Y, ldy, x_dtype, z_dtype, block,
+                       stream=0) -> int:
+    """Raw C-ABI call (include/norm_sm103.h); `block` a NormBlock, addresses 0
+    for what is absent.  Returns the gemm_status_t code."""
+    return lib.norm_block_forward(M, N, X or None, ldx, Z or None, ldz, XO or None, ldxo, Y or None,
+                                  ldy, x_dtype, z_dtype, ctypes.byref(block), stream)
+
+
+def norm_block_backward_raw(M, N, XO, ldxo, Z, ldz, dY, lddy, dXO, lddxo, dX, lddx, dZ, lddz,
+                            x_dtype, z_dtype, block, grads, workspace, workspace_bytes,
+                            stream=0) -> int:
+    """Raw C-ABI call of norm_block_backward; `grads` a NormBlockGrads."""
+    return lib.norm_block_backward(M, N, XO or None, ldxo, Z or None, ldz, dY or None, lddy,
+                                   dXO or None, lddxo, dX or None, lddx, dZ or None, lddz, x_dtype,
+                                   z_dtype, ctypes.byref(block), ctypes.byref(grads),
+                                   workspace or None, workspace_bytes, stream)
+
+
+def norm_block_backward_workspace(M, N, gate_rows=1, num_sms=0) -> int:
+    """Bytes of workspace norm_block_backward needs (host logic when num_sms > 0)."""
+    return lib.norm_block_backward_workspace(M, N, gate_rows, num_sms)
+
+
+def _need_cuda(*tensors):
+    """Every tensor lives on the current CUDA device."""
+    import torch
+    cur = None
+    for t in tensors:
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError("tensors must be on the GPU")
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.device.index != cur:
+            raise ValueError("tensors must be on the current CUDA device")
+
+
+def _need_matrix(t, name, rows, cols, dtype=None):
+    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{name} must be 2-D with unit inner stride")
+    if t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be {rows} x {cols}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}")
+
+
+def _need_vector(t, name, n):
+    if t.dim() != 1 or t.shape[0] != n or t.stride(0) != 1 and n > 1:
+        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+
+
+def _ld(t):
+    """Row pitch of a 2-D tensor (torch may give any stride to a single row)."""
+    return max(t.stride(0), t.shape[1], 1) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _ptr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _norm_config(N, rows, pre, pre_weight, pre_bias, post, post_weight, post_bias, gate, gate_rows,
+                 scale, eps):
+    vec = None
+    for t, name in ((pre_weight, "pre_weight"), (pre_bias, "pre_bias"),
+                    (post_weight, "post_weight"), (post_bias, "post_bias"), (gate, "gate")):
+        if t is None:
+            continue
+        if name == "gate":
+            if gate_rows < 1:
+                raise ValueError("gate_rows must be at least 1")
+            _need_matrix(t, name, -(-rows // gate_rows), N)
+        else:
+            _need_vector(t, name, N)
+        if vec is not None and t.dtype != vec:
+            raise ValueError("weights, biases and gate must share a dtype")
+        vec = t.dtype
+    return NormBlock(NORM_KINDS[pre], NORM_KINDS[post], _ptr(pre_weight) or None,
+                     _ptr(pre_bias) or None, _ptr(post_weight) or None, _ptr(post_bias) or None,
+                     _ptr(gate) or None, _ld(gate) if gate is not None else 0, gate_rows,
+                     GEMM_F32 if vec is None else dtype_code(vec), scale, eps)
+
+
+def norm_block(X, Z=None, XO=None, Y=None, *, pre="rms", pre_weight=None, pre_bias=None, post=None,
+               post_weight=None, post_bias=None, gate=None, gate_rows=1, scale=1.0, eps=1e-5,
+               stream=None):
+    """Norms around a transformer block, on 2-D CUDA tensors: (XO, Y) with
+    XO = X + scale * gate * Norm_post(Z) and Y = Norm_pre(XO).
+
+    X (M x N) is the residual stream, Z the block's output; Z None gives
+    (None, Norm_pre(X)).  pre and post are "rms", "layer" or None; pre None
+    (with no pre_weight or pre_bias) skips Y.  The gate has one row of N for
+    every gate_rows rows of X.  XO may be X (in place); XO and Y are new
+    tensors where None."""
+    import torch
+    _need_cuda(X, Z, XO, Y, pre_weight, pre_bias, post_weight, post_bias, gate)
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D with unit inner stride")
+    M, N = X.shape
+    _need_matrix(X, "X", M, N)
+    want_y = Y is not None or pre not in (None, "none") or pre_weight is not None or pre_bias is not None
+    z_dtype = X.dtype
+    if Z is not None:
+        _need_matrix(Z, "Z", M, N)
+        z_dtype = Z.dtype
+        if XO is None:
+            XO = torch.empty((M, N), dtype=X.dtype, device=X.device)
+        _need_matrix(XO, "XO", M, N, X.dtype)
+    elif XO is not None:
+        raise ValueError("XO goes with Z")
+    elif Y is not None:
+        z_dtype = Y.dtype
+    if want_y:
+        if Y is None:
+            Y = torch.empty((M, N), dtype=z_dtype, device=X.device)
+        _need_matrix(Y, "Y", M, N, z_dtype)
+    block = _norm_config(N, M, pre, pre_weight, pre_bias, post, post_weight, post_bias, gate,
+                         gate_rows, scale, eps)
+    if stream is None:
+        stream = torch.cuda.current_stream().cuda_stream
+    st = norm_block_forward(M, N, X.data_ptr(), _ld(X), _ptr(Z), _ld(Z) if Z is not None else 0,
+                            _ptr(XO), _ld(XO) if XO is not None else 0, _ptr(Y),
+                            _ld(Y) if Y is not None else 0, dtype_code(X.dtype),
+                            dtype_code(z_dtype), block, stream)
+    if st != 0:
+        raise GemmError(st, "norm_block_forward")
+    return XO, Y
+
+
+def norm_block_backward(XO, dY=None, dXO=None, Z=None, *, pre="rms", pre_weight=None, post=None,
+                        post_weight=None, post_bias=None, gate=None, gate_rows=1, scale=1.0,
+                        eps=1e-5, dX=None, dZ=None, dgate=None, dpre_weight=None, dpre_bias=None,
+                        dpost_weight=None, dpost_bias=None, workspace=None, stream=None):
+    """Backward pass of norm_block into the given tensors (None: not wanted).
+
+    XO is norm_block's output (X where there was no Z), dY and dXO the
+    gradients with respect to Y and XO (None: zero).  dX may be dXO and dZ may
+    be Z.  The vector gradients share a dtype; dgate is contiguous, as the
+    gate.  workspace: a uint8 tensor of norm_block_backward_workspace bytes
+    (a new one of the caching allocator where None)."""
+    import torch
+    _need_cuda(XO, dY, dXO, Z, pre_weight, post_weight, post_bias, gate, dX, dZ, dgate, dpre_weight,
+               dpre_bias, dpost_weight, dpost_bias, workspace)
+    if XO.dim() != 2:
+        raise ValueError("XO must be 2-D with unit inner stride")
+    M, N = XO.shape
+    xt = XO.dtype
+    zt = next((t.dtype for t in (Z, dY, dZ) if t is not None), xt)
+    for t, name, dt in ((XO, "XO", xt), (dXO, "dXO", xt), (dX, "dX", xt), (Z, "Z", zt),
+                        (dY, "dY", zt), (dZ, "dZ", zt)):
+        if t is not None:
+            _need_matrix(t, name, M, N, dt)
+    block = _norm_config(N, M, pre, pre_weight, None, post, post_weight, post_bias, gate, gate_rows,
+                         scale, eps)
+    gt = None
+    for t, name in ((dpre_weight, "dpre_weight"), (dpre_bias, "dpre_bias"),
+                    (dpost_weight, "dpost_weight"), (dpost_bias, "dpost_bias"), (dgate, "dgate")):
+        if t is None:
+            continue
+        if name == "dgate":
+            if gate is None:
+                raise ValueError("dgate goes with gate")
+            _need_matrix(t, name, gate.shape[0], N)
+            if not t.is_contiguous():
+                raise ValueError("dgate must be contiguous")
+        else:
+            _need_vector(t, name, N)
+        if gt is not None and t.dtype != gt:
+            raise ValueError("the vector gradients must share a dtype")
+        gt = t.dtype
+    grads = NormBlockGrads(_ptr(dpre_weight) or None, _ptr(dpre_bias) or None,
+                           _ptr(dpost_weight) or None, _ptr(dpost_bias) or None,
+                           _ptr(dgate) or None, GEMM_F32 if gt is None else dtype_code(gt))
+    nbytes = 0
+    if gt is not None:
+        if workspace is None:
+            need = norm_block_backward_workspace(M, N, gate_rows if gate is not None else 1)
+            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=XO.device)
+            if stream is not None:
+                workspace.record_stream(torch.cuda.ExternalStream(stream))
+        nbytes = workspace.numel() * workspace.element_size()
+    if stream is None:
+        stream = torch.cuda.current_stream().cuda_stream
+    ld = [(_ptr(t), _ld(t) if t is not None else 0) for t in (XO, Z, dY, dXO, dX, dZ)]
+    st = norm_block_backward_raw(M, N, *[v for pair in ld for v in pair], dtype_code(xt),
+                                 dtype_code(zt), block, grads, _ptr(workspace), nbytes, stream)
+    if st != 0:
+        raise GemmError(st, "norm_block_backward")
+
+
+# ------------------------------------------------ gradient norm and clipping
+
+def grad_clip_workspace(count, num_sms=0) -> int:
+    """Bytes of workspace grad_clip needs (host logic when num_sms > 0)."""
+    return lib.grad_clip_workspace(count, num_sms)
+
+
+def grad_clip_raw(grads, outs, sizes, dtypes, max_norm, inv_scale, norm, workspace,
+                  workspace_bytes, stream=0) -> int:
+    """Raw C-ABI call (include/grad_sm103.h): lists of device addresses (outs
+    None: in place), element counts and type codes.  Returns the status code."""
+    n = len(grads)
+    a = (ctypes.c_uint64 * max(n, 1))(*grads)
+    o = None if outs is None else (ctypes.c_uint64 * max(n, 1))(*outs)
+    z = (ctypes.c_int64 * max(n, 1))(*sizes)
+    d = (ctypes.c_int32 * max(n, 1))(*dtypes)
+    return lib.grad_clip(n, ctypes.addressof(a), None if o is None else ctypes.addressof(o),
+                         ctypes.addressof(z), ctypes.addressof(d), max_norm, inv_scale,
+                         norm or None, workspace or None, workspace_bytes, stream)
+
+
+def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace=None, stream=None):
+    """Clips a list of gradient tensors (contiguous CUDA tensors of any shape;
+    FP16, BF16 or FP32) by their global norm, in place or into `outputs`:
+    out = g * inv_scale * min(1, max_norm / norm), with
+    norm = inv_scale * sqrt(sum of all g^2) returned as a 1-element FP32
+    tensor.  A norm that is not finite clips nothing."""
+    import torch
+    _need_cuda(*grads)
+    _need_cuda(norm, workspace)
+    if outputs is not None:
+        _need_cuda(*outputs)
+        if len(outputs) != len(grads):
+            raise ValueError("as many outputs as gradients")
+        for g, o in zip(grads, outputs):
+            if o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous():
+                raise ValueError("an output must be contiguous, of its gradient's dtype and size")
+    for g in grads:
+        if not g.is_contiguous():
+            raise ValueError("gradients must be contiguous")
+    dev = grads[0].device if len(grads) else torch.device("cuda", torch.cuda.current_device())
+    other = None if stream is None else torch.cuda.ExternalStream(stream)
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        if other is not None:
+            norm.record_stream(other)
+    elif norm.dtype != torch.float32 or norm.numel() != 1:
+        raise ValueError("norm must be one FP32 element")
+    if workspace is None:
+        workspace = torch.empty(grad_clip_workspace(len(grads)), dtype=torch.uint8, device=dev)
+        if other is not None:
+            workspace.record_stream(other)
+    if stream is None:
+        stream = torch.cuda.current_stream().cuda_stream
+    st = grad_clip_raw([g.data_ptr() for g in grads],
+                       None if outputs is None else [o.data_ptr() for o in outputs],
+                       [g.numel() for g in grads], [dtype_code(g.dtype) for g in grads], max_norm,
+                       inv_scale, norm.data_ptr(), workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size(), stream)
+    if st != 0:
+        raise GemmError(st, "grad_clip")
+    return norm
 
 
 _TORCH_CODE = None
@@ -443,6 +794,77 @@ class Gemm:
         if st != 0:
             raise GemmError(st, "gemm_run_layernorm")
         return C
+
+    def glu(self, X, W, H=None, act="silu", bias=None, P=None, stream=None):
+        """The gated linear layer: H = act(X Wg^T + bg) * (X Wu^T + bu), with
+        W = [Wg; Wu] (2F x K) and bias = [bg; bu] (2F) or None.  X is M x K, H
+        M x F (a new tensor of X's type where None).  P (M x 2F, H's type)
+        receives X W^T + bias for the backward pass."""
+        import torch
+        _need_cuda(X, W, H, bias, P)
+        if X.dim() != 2 or W.dim() != 2 or W.shape[0] % 2:
+            raise ValueError("X must be M x K and W 2F x K")
+        M, K = X.shape
+        F = W.shape[0] // 2
+        _need_matrix(X, "X", M, K)
+        _need_matrix(W, "W", 2 * F, K, X.dtype)
+        if H is None:
+            H = torch.empty((M, F), dtype=X.dtype, device=X.device)
+        _need_matrix(H, "H", M, F)
+        if bias is not None:
+            _need_vector(bias, "bias", 2 * F)
+        if P is not None:
+            _need_matrix(P, "P", M, 2 * F, H.dtype)
+        if stream is None:
+            stream = torch.cuda.current_stream().cuda_stream
+        xt = dtype_code(X.dtype)
+        st = glu_forward(self.h, M, F, K, X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), H.data_ptr(),
+                         _ld(H), (xt, xt, dtype_code(H.dtype)),
+                         ACTIVATIONS[act] if not isinstance(act, int) else act, _ptr(bias),
+                         dtype_code(bias.dtype) if bias is not None else GEMM_F32, _ptr(P),
+                         _ld(P) if P is not None else 0, stream)
+        if st != 0:
+            raise GemmError(st, "glu_forward")
+        return H
+
+    def glu_backward(self, dH, P, X, W, act="silu", dP=None, dX=None, dW=None, dbias=None,
+                     beta_w=0.0, stream=None):
+        """Backward pass of `glu` from dH (M x F) and the stored P (M x 2F):
+        dP (a new tensor where None; may be P itself), and dX (M x K),
+        dW (2F x K, beta_w * dW added) and dbias (2F) where given.  X may be
+        None without dW, W without dX.  Returns dP."""
+        import torch
+        _need_cuda(dH, P, X, W, dP, dX, dW, dbias)
+        if dH.dim() != 2:
+            raise ValueError("dH must be M x F")
+        M, F = dH.shape
+        t = dH.dtype
+        _need_matrix(dH, "dH", M, F)
+        _need_matrix(P, "P", M, 2 * F)
+        if dP is None:
+            dP = torch.empty((M, 2 * F), dtype=t, device=dH.device)
+        _need_matrix(dP, "dP", M, 2 * F, t)
+        if dX is not None and W is None or dW is not None and X is None:
+            raise ValueError("dX needs W and dW needs X")
+        K = next((v.shape[-1] for v in (X, W, dX, dW) if v is not None), 0)
+        for v, name, rows, dt in ((X, "X", M, t), (W, "W", 2 * F, t), (dX, "dX", M, None),
+                                  (dW, "dW", 2 * F, None)):
+            if v is not None:
+                _need_matrix(v, name, rows, K, dt)
+        if dbias is not None:
+            _need_vector(dbias, "dbias", 2 * F)
+        if stream is None:
+            stream = torch.cuda.current_stream().cuda_stream
+        code = lambda v: GEMM_F32 if v is None else dtype_code(v.dtype)   # noqa: E731
+        ld = lambda v: 0 if v is None else _ld(v)                          # noqa: E731
+        st = glu_backward(self.h, M, F, K, dH.data_ptr(), _ld(dH), P.data_ptr(), _ld(P), _ptr(X),
+                          ld(X) or max(K, 1), _ptr(W), ld(W) or max(K, 1), dtype_code(t),
+                          dP.data_ptr(), _ld(dP), ACTIVATIONS[act] if not isinstance(act, int) else act,
+                          dtype_code(P.dtype), _ptr(dX), ld(dX), code(dX), _ptr(dW), ld(dW), code(dW),
+                          beta_w, _ptr(dbias), code(dbias), stream)
+        if st != 0:
+            raise GemmError(st, "glu_backward")
+        return dP
 
     def sync(self, stream=None):
         import torch

@@ -20,7 +20,9 @@
 
 #include "gemm_sm103.h"
 #include "conv_sm103.h"
+#include "glu_sm103.h"
 #include "aux_kernels.cuh"
+#include "glu_kern.cuh"
 #include "launch.h"
 
 using namespace gemm103;
@@ -475,6 +477,8 @@ struct gemm_ctx {
     int* err_dev;         // device view of the same word
     void* ws;             // device workspace
     size_t ws_bytes;
+    bool ws_captured;     // a captured graph may hold ws's address
+    struct Retired { void* p; Retired* next; }* retired;   // outgrown, still in such a graph
     EncodeTiledFn encode;
     EncodeIm2colFn encode_im2col;
 };
@@ -615,8 +619,29 @@ bool encode_conv_filter(EncodeTiledFn encode, const ConvDesc& cd, CUtensorMap* m
     return r == CUDA_SUCCESS;
 }
 
-gemm_status_t ensure_workspace(gemm_ctx* h, size_t bytes) {
-    if (bytes <= h->ws_bytes) return GEMM_OK;
+// The handle's workspace of at least `bytes`.  Under stream capture it cannot
+// grow (an allocation would end the capture): ALLOC.  A buffer that a captured
+// graph may still address is kept until gemm_destroy when it is outgrown.
+gemm_status_t ensure_workspace(gemm_ctx* h, size_t bytes, cudaStream_t stream) {
+    if (bytes == 0) return GEMM_OK;
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) cudaGetLastError();
+    const bool capturing = cap != cudaStreamCaptureStatusNone;
+    if (bytes <= h->ws_bytes) {
+        h->ws_captured = h->ws_captured || capturing;
+        return GEMM_OK;
+    }
+    if (capturing) return GEMM_ERR_ALLOC;
+    if (h->ws && h->ws_captured) {
+        gemm_ctx::Retired* r = new (std::nothrow) gemm_ctx::Retired;
+        if (r == nullptr) return GEMM_ERR_ALLOC;
+        r->p = h->ws;
+        r->next = h->retired;
+        h->retired = r;
+        h->ws = nullptr;
+        h->ws_bytes = 0;
+        h->ws_captured = false;
+    }
     if (h->ws) {
         cudaFree(h->ws);          // implicit device synchronisation: no user of the old buffer remains
         h->ws = nullptr;
@@ -1174,6 +1199,12 @@ gemm_status_t gemm_destroy(gemm_handle_t h) {
     if (h == nullptr) return GEMM_OK;
     cudaDeviceSynchronize();
     if (h->ws) cudaFree(h->ws);
+    while (h->retired) {
+        gemm_ctx::Retired* r = h->retired;
+        h->retired = r->next;
+        cudaFree(r->p);
+        delete r;
+    }
     if (h->err_host) cudaFreeHost(h->err_host);
     delete h;
     cudaGetLastError();
@@ -1209,7 +1240,7 @@ gemm_status_t gemm_run_ex(gemm_handle_t h, char transA, char transB, int64_t M, 
     if (pl.pub.path == GEMM_PATH_NOOP) return GEMM_OK;
     if (pl.pub.path == GEMM_PATH_SCALE)
         return enqueue_scale(M, N, C, ldc, beta, dt, h->num_sms, stream, ep);
-    st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes));
+    st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
     return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, alpha,
                         beta, C, dt, stream, false, h->debug_flags, h->wait_limit_ns, ep);
@@ -1261,7 +1292,7 @@ gemm_status_t gemm_run_layernorm(gemm_handle_t h, char transA, char transB, int6
         return enqueue_ln_rows(M, N, C, ldc, dt, nullptr, 1, static_cast<int32_t>(N), ln,
                                h->num_sms, stream);
     }
-    st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes));
+    st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
     return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, alpha,
                         beta, C, dt, stream, false, h->debug_flags, h->wait_limit_ns, nullptr,
@@ -1465,10 +1496,198 @@ gemm_status_t conv2d_fprop(gemm_handle_t h, int64_t N, int64_t H, int64_t W, int
     if (pl.pub.path == GEMM_PATH_NOOP) return GEMM_OK;
     if (pl.pub.path == GEMM_PATH_SCALE)
         return enqueue_scale(cd.N * cd.P * cd.Q, K, Y, K, beta, dt, h->num_sms, stream, ep);
-    st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes));
+    st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
     return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, alpha,
                         beta, Y, dt, stream, false, h->debug_flags, h->wait_limit_ns, ep, &cd);
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The gated linear layer (include/glu_sm103.h).
+// ---------------------------------------------------------------------------
+namespace {
+
+// Slabs of rows of the dP kernel: enough CTAs for eight per SM, each slab at
+// least one row per warp.
+int64_t glu_slab_rows(int64_t M, int64_t F, int num_sms) {
+    const int64_t col_blocks = ceil_div(F, 256);
+    int64_t slabs = ceil_div(static_cast<int64_t>(num_sms) * 8, col_blocks);
+    const int64_t most = ceil_div(M, kGluBackWarps);
+    if (slabs > most) slabs = most;
+    if (slabs > 65535) slabs = 65535;
+    if (slabs < 1) slabs = 1;
+    return round_up(ceil_div(M, slabs), kGluBackWarps);
+}
+
+gemm_status_t check_glu(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W,
+                        int64_t ldw, const void* H, int64_t ldh, gemm_dtypes_t dt,
+                        const glu_forward_t* o) {
+    if (o == nullptr || F < 0 || F > INT32_MAX / 2) return GEMM_ERR_INVALID_VALUE;
+    gemm_status_t st = check_args('N', 'T', M, F, K, 1.0f, X, ldx, W, ldw, 0.0f, H, ldh, dt);
+    if (st != GEMM_OK) return st;
+    const gemm_epilogue_t ep{o->bias, o->bias_dtype, o->activation};
+    if (!epilogue_ok(&ep)) return GEMM_ERR_INVALID_VALUE;
+    if (o->bias && !aligned_to(o->bias, in_elem_bytes(o->bias_dtype))) return GEMM_ERR_INVALID_VALUE;
+    if (o->P && (o->ldp < max1(2 * F) || !aligned_to(o->P, out_elem_bytes(dt.c))))
+        return GEMM_ERR_INVALID_VALUE;
+    if (dt.a == GEMM_F32) return GEMM_ERR_NOT_SUPPORTED;
+    return GEMM_OK;
+}
+
+// The handle's device is current: its workspace and the caller's tensors
+// belong to it.
+bool device_current(const gemm_ctx* h) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return dev == h->device;
+}
+
+template <typename OutT>
+void launch_glu_gate(const float* S, const glu_forward_t* o, void* H, int64_t ldh, int64_t M,
+                     int64_t F, int num_sms, cudaStream_t stream) {
+    glu_gate_kernel<OutT><<<grid_for(M * F, num_sms), 256, 0, stream>>>(
+        S, o->bias, o->bias_dtype, o->activation, static_cast<OutT*>(H), ldh,
+        static_cast<OutT*>(o->P), o->ldp, M, F);
+}
+
+gemm_status_t enqueue_glu_gate(const float* S, const glu_forward_t* o, void* H, int64_t ldh,
+                               int64_t M, int64_t F, int32_t c_dtype, int num_sms,
+                               cudaStream_t stream) {
+    if (c_dtype == GEMM_F32) launch_glu_gate<float>(S, o, H, ldh, M, F, num_sms, stream);
+    else if (c_dtype == GEMM_F16) launch_glu_gate<__half>(S, o, H, ldh, M, F, num_sms, stream);
+    else launch_glu_gate<__nv_bfloat16>(S, o, H, ldh, M, F, num_sms, stream);
+    return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
+}
+
+template <typename T, typename PT>
+void launch_glu_back(const GluBackParams& p, dim3 grid, cudaStream_t stream) {
+    if (p.partials) glu_back_kernel<T, PT, true><<<grid, 32 * kGluBackWarps, 0, stream>>>(p);
+    else glu_back_kernel<T, PT, false><<<grid, 32 * kGluBackWarps, 0, stream>>>(p);
+}
+
+template <typename T>
+void launch_glu_back_p(const GluBackParams& p, int32_t p_dtype, dim3 grid, cudaStream_t stream) {
+    if (p_dtype == GEMM_F32) launch_glu_back<T, float>(p, grid, stream);
+    else if (p_dtype == GEMM_F16) launch_glu_back<T, __half>(p, grid, stream);
+    else launch_glu_back<T, __nv_bfloat16>(p, grid, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t glu_plan_query(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
+                             const void* W, int64_t ldw, const void* H, int64_t ldh,
+                             gemm_dtypes_t dt, const glu_forward_t* opt, int32_t num_sms,
+                             int32_t smem_optin, gemm_plan_t* out) {
+    if (out == nullptr) return GEMM_ERR_INVALID_VALUE;
+    gemm_status_t st = check_glu(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt);
+    if (st != GEMM_OK) return st;
+    Plan pl;
+    st = make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, H, max1(2 * F),
+                   gemm_dtypes_t{dt.a, dt.b, GEMM_F32}, num_sms, smem_optin, pl);
+    if (st != GEMM_OK) return st;
+    *out = pl.pub;
+    return GEMM_OK;
+}
+
+gemm_status_t glu_forward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, const void* X,
+                          int64_t ldx, const void* W, int64_t ldw, void* H, int64_t ldh,
+                          gemm_dtypes_t dt, const glu_forward_t* opt, gemm_stream_t stream_) {
+    if (h == nullptr || !device_current(h)) return GEMM_ERR_INVALID_VALUE;
+    gemm_status_t st = take_device_error(h);
+    if (st != GEMM_OK) return st;
+    st = check_glu(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt);
+    if (st != GEMM_OK) return st;
+    if (M == 0 || F == 0) return GEMM_OK;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (K == 0) return enqueue_glu_gate(nullptr, opt, H, ldh, M, F, dt.c, h->num_sms, stream);
+    const gemm_dtypes_t gdt{dt.a, dt.b, GEMM_F32};
+    Plan pl;
+    st = make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, reinterpret_cast<void*>(256),
+                   2 * F, gdt, h->num_sms, h->smem_optin, pl);
+    if (st != GEMM_OK) return st;
+    const int64_t at = round_up(pl.pub.workspace_bytes > 0 ? pl.pub.workspace_bytes : kWsHeaderBytes, 256);
+    st = ensure_workspace(h, static_cast<size_t>(at + M * 2 * F * 4), stream);
+    if (st != GEMM_OK) return st;
+    uint8_t* ws = static_cast<uint8_t*>(h->ws);
+    st = enqueue_plan(pl, h->encode, h->num_sms, ws, h->err_dev, 1.0f, 0.0f, ws + at, gdt, stream,
+                      false, h->debug_flags, h->wait_limit_ns);
+    if (st != GEMM_OK) return st;
+    return enqueue_glu_gate(reinterpret_cast<float*>(ws + at), opt, H, ldh, M, F, dt.c, h->num_sms,
+                            stream);
+}
+
+gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, const void* dH,
+                           int64_t lddh, const void* P, int64_t ldp, const void* X, int64_t ldx,
+                           const void* W, int64_t ldw, int32_t dtype, const glu_backward_t* o,
+                           gemm_stream_t stream_) {
+    if (h == nullptr || o == nullptr || !device_current(h)) return GEMM_ERR_INVALID_VALUE;
+    gemm_status_t st = take_device_error(h);
+    if (st != GEMM_OK) return st;
+    if (M < 0 || F < 0 || K < 0 || M > INT32_MAX || F > INT32_MAX / 2 || K > INT32_MAX)
+        return GEMM_ERR_INVALID_VALUE;
+    if (dtype != GEMM_F16 && dtype != GEMM_BF16)
+        return dtype == GEMM_F32 ? GEMM_ERR_NOT_SUPPORTED : GEMM_ERR_INVALID_VALUE;
+    if (!dtype16or32(o->p_dtype) || o->activation < GEMM_ACT_NONE || o->activation > GEMM_ACT_SILU)
+        return GEMM_ERR_INVALID_VALUE;
+    const bool some = M > 0 && F > 0;
+    if (lddh < max1(F) || ldp < max1(2 * F) || o->lddp < max1(2 * F)) return GEMM_ERR_INVALID_VALUE;
+    if (some && (dH == nullptr || P == nullptr || o->dP == nullptr || !aligned_to(dH, 2) ||
+                 !aligned_to(P, out_elem_bytes(o->p_dtype)) || !aligned_to(o->dP, 2)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (some && o->dP == P && (o->p_dtype != dtype || o->lddp != ldp)) return GEMM_ERR_INVALID_VALUE;
+    if (o->dbias && (!dtype16or32(o->dbias_dtype) || !aligned_to(o->dbias, out_elem_bytes(o->dbias_dtype))))
+        return GEMM_ERR_INVALID_VALUE;
+    // both products' arguments are checked before anything is enqueued
+    const gemm_dtypes_t xdt{dtype, dtype, o->dx_dtype}, wdt{dtype, dtype, o->dw_dtype};
+    if (o->dX) {
+        st = check_args('N', 'N', M, K, 2 * F, 1.0f, o->dP, o->lddp, W, ldw, 0.0f, o->dX, o->lddx, xdt);
+        if (st != GEMM_OK) return st;
+    }
+    if (o->dW) {
+        st = check_args('T', 'N', 2 * F, K, M, 1.0f, o->dP, o->lddp, X, ldx, o->beta_w, o->dW, o->lddw, wdt);
+        if (st != GEMM_OK) return st;
+    }
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    const int64_t slab_rows = some ? glu_slab_rows(M, F, h->num_sms) : 1;
+    const int64_t slabs = some ? ceil_div(M, slab_rows) : 0;
+    float* partials = nullptr;
+    if (some && o->dbias) {
+        st = ensure_workspace(h, static_cast<size_t>(kWsHeaderBytes + slabs * 2 * F * 4), stream);
+        if (st != GEMM_OK) return st;
+        partials = reinterpret_cast<float*>(static_cast<uint8_t*>(h->ws) + kWsHeaderBytes);
+    }
+    if (some) {
+        const int64_t pe = static_cast<int64_t>(out_elem_bytes(o->p_dtype));
+        GluBackParams p{dH, lddh, P, ldp, o->dP, o->lddp, M, F, o->activation, 0, slab_rows, partials};
+        p.vec = F % 8 == 0 && aligned16(dH) && aligned16(P) && aligned16(o->dP) && lddh % 8 == 0 &&
+                o->lddp % 8 == 0 && ldp * pe % 16 == 0;
+        const dim3 grid(static_cast<unsigned>(ceil_div(F, 256)), static_cast<unsigned>(slabs), 1);
+        if (dtype == GEMM_F16) launch_glu_back_p<__half>(p, o->p_dtype, grid, stream);
+        else launch_glu_back_p<__nv_bfloat16>(p, o->p_dtype, grid, stream);
+        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+    }
+    if (o->dbias && F > 0) {
+        const int64_t cols = 2 * F;
+        glu_dbias_kernel<<<static_cast<unsigned>(ceil_div(cols, 256)), 256, 0, stream>>>(
+            partials, static_cast<int32_t>(slabs), cols, o->dbias, o->dbias_dtype);
+        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+    }
+    if (o->dX) {
+        st = gemm_run(h, 'N', 'N', M, K, 2 * F, 1.0f, o->dP, o->lddp, W, ldw, 0.0f, o->dX, o->lddx,
+                      xdt, stream_);
+        if (st != GEMM_OK) return st;
+    }
+    if (o->dW)
+        st = gemm_run(h, 'T', 'N', 2 * F, K, M, 1.0f, o->dP, o->lddp, X, ldx, o->beta_w, o->dW,
+                      o->lddw, wdt, stream_);
+    return st;
 }
 
 }  // extern "C"

@@ -1,0 +1,458 @@
+// grad.cu -- the global gradient norm over many tensors, and clipping by it
+// (include/grad_sm103.h).
+//
+// Two kernels.  norm_partial_kernel reads every element once: the tensors are
+// cut into chunks of kChunk elements, numbered through all of a launch's
+// tensors, and CTA b takes chunks b, b + grid, ...; each CTA leaves one FP64
+// partial sum.  apply_kernel adds the partial sums (every CTA the same way:
+// a few hundred FP64 values out of L2, cheaper than a third launch or a
+// grid-wide wait), CTA 0 writes the norm, and each CTA scales its chunks.  The
+// second pass walks the chunks in the opposite order, so what the first pass
+// left in L2 is found there.  Bound by HBM: two reads and one write of the
+// gradients (one read where nothing is scaled in place, or where they fit in
+// L2).
+//
+// Squares are summed in FP32 over one batch of a thread (kVecs 16-byte
+// vectors: 16 or 32 elements) and then in FP64: one FP64 add per batch, as
+// FP64 arithmetic is scarce here.  A batch whose FP32 sum lies in
+// [2^-90, 2^127) lost at most 32 squares below 2^-126 -- under 2^-31 of it --
+// so it is kept; any other batch that is not all zeros is summed again in
+// FP64, where the square of no FP32, BF16 or FP16 value overflows or
+// underflows.
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <new>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "grad_sm103.h"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace gemm103;
+
+constexpr int kThreads = 256;
+constexpr int kCtasPerSm = 6;
+constexpr int kVecs = 4;                       // 16-byte vectors per thread and batch
+constexpr int64_t kChunk = 16384;              // elements per chunk
+constexpr int kPerLaunch = GRAD_TENSORS_PER_LAUNCH;
+
+template <int CAP>
+struct Tensors {
+    const void* src[CAP];
+    void* dst[CAP];
+    int64_t size[CAP];
+    int32_t first_chunk[CAP + 1];              // chunks before tensor t; [count] = all
+    uint8_t dtype[CAP];
+    int32_t count;
+};
+
+struct ApplyParams {
+    const double* partials;
+    int32_t num_partials;
+    float max_norm, inv_scale;
+    float* norm;
+    int32_t write_norm;
+};
+
+// Tensor that holds chunk `c` (the last t with first_chunk[t] <= c).
+template <int CAP>
+__device__ __forceinline__ int find_tensor(const Tensors<CAP>& t, int32_t c) {
+    int lo = 0, hi = t.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first_chunk[mid] <= c) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
+    return __bfloat162float(v);
+}
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+template <typename T>
+union Vec16 {
+    uint4 u;
+    T e[16 / sizeof(T)];
+};
+
+// The sum of squares of a batch (see above).
+template <typename T>
+__device__ __forceinline__ double batch_sum(const uint4 (&v)[kVecs]) {
+    constexpr int kPer = 16 / sizeof(T);
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    #pragma unroll
+    for (int q = 0; q < kVecs; ++q) {
+        Vec16<T> w;
+        w.u = v[q];
+        #pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const float x = to_f<T>(w.e[e]);
+            s[e & 3] = fmaf(x, x, s[e & 3]);
+        }
+    }
+    const float t = (s[0] + s[1]) + (s[2] + s[3]);
+    if (t >= 0x1p-90f && t < 0x1p127f) return static_cast<double>(t);
+    uint32_t any = 0;
+    #pragma unroll
+    for (int q = 0; q < kVecs; ++q) any |= v[q].x | v[q].y | v[q].z | v[q].w;
+    if (any == 0) return 0.0;
+    double d = 0.0;
+    #pragma unroll 1
+    for (int q = 0; q < kVecs; ++q) {
+        Vec16<T> w;
+        w.u = v[q];
+        #pragma unroll 1
+        for (int e = 0; e < kPer; ++e) {
+            const double x = static_cast<double>(to_f<T>(w.e[e]));
+            d = fma(x, x, d);
+        }
+    }
+    return d;
+}
+
+// Elements of a chunk before its first 16-byte boundary (at most n).
+template <typename T>
+__device__ __forceinline__ int32_t head_of(const T* p, int32_t n) {
+    const int32_t h = static_cast<int32_t>(((16u - (reinterpret_cast<uintptr_t>(p) & 15u)) & 15u) /
+                                           sizeof(T));
+    return h < n ? h : n;
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_sum(const T* p, int32_t n) {
+    constexpr int kPer = 16 / sizeof(T);
+    const int32_t head = head_of(p, n);
+    const int32_t nvec = (n - head) / kPer;
+    const uint4* v = reinterpret_cast<const uint4*>(p + head);
+    double acc = 0.0;
+    for (int32_t i = threadIdx.x; i < nvec; i += kVecs * kThreads) {
+        uint4 r[kVecs];
+        #pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+            const int32_t k = i + q * kThreads;
+            r[q] = k < nvec ? __ldg(v + k) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        acc += batch_sum<T>(r);
+    }
+    // the elements before and behind the vectors: at most 14
+    const int32_t tail0 = head + nvec * kPer;
+    const int32_t loose = head + (n - tail0);
+    if (static_cast<int32_t>(threadIdx.x) < loose) {
+        const int32_t k = static_cast<int32_t>(threadIdx.x) < head ? threadIdx.x
+                                                                   : tail0 + threadIdx.x - head;
+        const double x = static_cast<double>(to_f<T>(p[k]));
+        acc = fma(x, x, acc);
+    }
+    return acc;
+}
+
+// Sum over the CTA in a fixed order; every thread gets it.
+__device__ __forceinline__ double cta_sum(double v, double* red) {
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double t = 0.0;
+    #pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) t += red[w];
+    return t;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    norm_partial_kernel(const __grid_constant__ Tensors<CAP> t, double* __restrict__ partials) {
+    __shared__ double red[kThreads / 32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int32_t chunks = t.first_chunk[t.count];
+    double acc = 0.0;
+    for (int32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+        const int k = find_tensor(t, c);
+        const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * kChunk;
+        const int64_t left = t.size[k] - at;
+        const int32_t n = static_cast<int32_t>(left < kChunk ? left : kChunk);
+        if (t.dtype[k] == GEMM_F32)
+            acc += chunk_sum(static_cast<const float*>(t.src[k]) + at, n);
+        else if (t.dtype[k] == GEMM_BF16)
+            acc += chunk_sum(static_cast<const __nv_bfloat16*>(t.src[k]) + at, n);
+        else
+            acc += chunk_sum(static_cast<const __half*>(t.src[k]) + at, n);
+    }
+    const double s = cta_sum(acc, red);
+    if (threadIdx.x == 0) partials[blockIdx.x] = s;
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 scale_vec(uint4 u, float f) {
+    Vec16<T> w;
+    w.u = u;
+    #pragma unroll
+    for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) w.e[e] = from_f<T>(to_f<T>(w.e[e]) * f);
+    return w.u;
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_scale(const T* p, T* o, int32_t n, float f) {
+    constexpr int kPer = 16 / sizeof(T);
+    // vectors only where source and destination reach a 16-byte boundary together
+    const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15u) == 0;
+    if (!same) {
+        for (int32_t i = threadIdx.x; i < n; i += kThreads) o[i] = from_f<T>(to_f<T>(p[i]) * f);
+        return;
+    }
+    const int32_t head = head_of(p, n);
+    const int32_t nvec = (n - head) / kPer;
+    const uint4* v = reinterpret_cast<const uint4*>(p + head);
+    uint4* w = reinterpret_cast<uint4*>(o + head);
+    for (int32_t i = threadIdx.x; i < nvec; i += kVecs * kThreads) {
+        uint4 r[kVecs];
+        #pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+            const int32_t k = i + q * kThreads;
+            if (k < nvec) r[q] = __ldcs(v + k);
+        }
+        #pragma unroll
+        for (int q = 0; q < kVecs; ++q) {
+            const int32_t k = i + q * kThreads;
+            if (k < nvec) __stcs(w + k, scale_vec<T>(r[q], f));
+        }
+    }
+    const int32_t tail0 = head + nvec * kPer;
+    const int32_t loose = head + (n - tail0);
+    if (static_cast<int32_t>(threadIdx.x) < loose) {
+        const int32_t k = static_cast<int32_t>(threadIdx.x) < head ? threadIdx.x
+                                                                   : tail0 + threadIdx.x - head;
+        o[k] = from_f<T>(to_f<T>(p[k]) * f);
+    }
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads)
+    apply_kernel(const __grid_constant__ Tensors<CAP> t, const ApplyParams a) {
+    __shared__ double red[kThreads / 32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    double acc = 0.0;
+    for (int32_t i = threadIdx.x; i < a.num_partials; i += kThreads) acc += a.partials[i];
+    const double norm = sqrt(cta_sum(acc, red)) * static_cast<double>(a.inv_scale);
+    if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = static_cast<float>(norm);
+    double f = static_cast<double>(a.inv_scale);
+    if (isfinite(norm) && norm > static_cast<double>(a.max_norm))
+        f *= static_cast<double>(a.max_norm) / norm;
+    const float factor = static_cast<float>(f);
+    const int32_t chunks = t.first_chunk[t.count];
+    for (int32_t r = blockIdx.x; r < chunks; r += gridDim.x) {
+        const int32_t c = chunks - 1 - r;
+        const int k = find_tensor(t, c);
+        if (factor == 1.0f && t.dst[k] == t.src[k]) continue;
+        const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * kChunk;
+        const int64_t left = t.size[k] - at;
+        const int32_t n = static_cast<int32_t>(left < kChunk ? left : kChunk);
+        if (t.dtype[k] == GEMM_F32)
+            chunk_scale(static_cast<const float*>(t.src[k]) + at, static_cast<float*>(t.dst[k]) + at,
+                        n, factor);
+        else if (t.dtype[k] == GEMM_BF16)
+            chunk_scale(static_cast<const __nv_bfloat16*>(t.src[k]) + at,
+                        static_cast<__nv_bfloat16*>(t.dst[k]) + at, n, factor);
+        else
+            chunk_scale(static_cast<const __half*>(t.src[k]) + at,
+                        static_cast<__half*>(t.dst[k]) + at, n, factor);
+    }
+}
+
+bool dtype_ok(int32_t t) { return t == GEMM_F16 || t == GEMM_BF16 || t == GEMM_F32; }
+int64_t esize(int32_t t) { return t == GEMM_F32 ? 4 : 2; }
+
+// SMs of the current device; 0 off sm_103, -1 on a CUDA error.
+int device_sms() {
+    int dev = 0, major = 0, minor = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    return major == 10 && minor == 3 ? sms : 0;
+}
+
+int64_t launches_for(int64_t count) { return (count + kPerLaunch - 1) / kPerLaunch; }
+
+int64_t workspace_for(int64_t count, int32_t sms) {
+    const int64_t l = launches_for(count);
+    return (l < 1 ? 1 : l) * static_cast<int64_t>(sms) * kCtasPerSm * 8;
+}
+
+cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute* attr) {
+    attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr->val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
+}
+
+struct Call {
+    int64_t count;
+    const void* const* grads;
+    void* const* outs;
+    const int64_t* sizes;
+    const int32_t* dtypes;
+    float max_norm, inv_scale;
+    float* norm;
+    double* partials;
+    int max_grid;
+    cudaStream_t stream;
+};
+
+// Tensors [first, first + n) of the call that are not empty.
+template <int CAP>
+void fill(Tensors<CAP>& t, const Call& c, int64_t first, int64_t n) {
+    int32_t chunk = 0;
+    t.count = 0;
+    for (int64_t i = first; i < first + n; ++i) {
+        if (c.sizes[i] == 0) continue;
+        const int k = t.count++;
+        t.src[k] = c.grads[i];
+        t.dst[k] = c.outs ? c.outs[i] : const_cast<void*>(c.grads[i]);
+        t.size[k] = c.sizes[i];
+        t.dtype[k] = static_cast<uint8_t>(c.dtypes[i]);
+        t.first_chunk[k] = chunk;
+        chunk += static_cast<int32_t>((c.sizes[i] + kChunk - 1) / kChunk);
+    }
+    t.first_chunk[t.count] = chunk;
+}
+
+// Two capacities: a launch copies its parameters, and 64 tensors (2 KB) go out
+// faster than 512 (15 KB).
+template <int CAP>
+cudaError_t run(const Call& c) {
+    Tensors<CAP> t;
+    const int64_t parts = c.count > 0 ? (c.count + CAP - 1) / CAP : 1;
+    int32_t partials = 0;
+    cudaLaunchAttribute attr;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int64_t l = 0; l < parts; ++l) {
+            const int64_t first = l * CAP;
+            const int64_t n = c.count - first < CAP ? c.count - first : CAP;
+            fill(t, c, first, n);
+            const int32_t chunks = t.first_chunk[t.count];
+            int grid = chunks < c.max_grid ? chunks : c.max_grid;
+            if (pass == 0) {
+                if (grid == 0) continue;
+                cudaLaunchConfig_t cfg = config(grid, c.stream, &attr);
+                const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_partial_kernel<CAP>, t,
+                                                         c.partials + partials);
+                if (e != cudaSuccess) return e;
+                partials += grid;
+            } else {
+                // nothing to scale: only the norm is written, by one CTA
+                bool in_place = true;
+                for (int32_t k = 0; k < t.count; ++k) in_place = in_place && t.dst[k] == t.src[k];
+                if (in_place && c.inv_scale == 1.0f && std::isinf(c.max_norm)) t.first_chunk[t.count] = 0, grid = 0;
+                if (grid == 0) {
+                    if (l > 0) continue;
+                    grid = 1;
+                }
+                const ApplyParams a{c.partials, partials, c.max_norm, c.inv_scale, c.norm,
+                                    l == 0 ? 1 : 0};
+                cudaLaunchConfig_t cfg = config(grid, c.stream, &attr);
+                const cudaError_t e = cudaLaunchKernelEx(&cfg, apply_kernel<CAP>, t, a);
+                if (e != cudaSuccess) return e;
+            }
+        }
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t grad_clip_workspace(int64_t count, int32_t num_sms) {
+    if (count < 0 || count > (1ll << 40) || num_sms < 0) return -1;
+    if (num_sms == 0) {
+        const int s = device_sms();
+        if (s <= 0) return -1;
+        num_sms = s;
+    }
+    return workspace_for(count, num_sms);
+}
+
+gemm_status_t grad_clip(int64_t count, const void* const* grads, void* const* outs,
+                        const int64_t* sizes, const int32_t* dtypes, float max_norm,
+                        float inv_scale, float* norm, void* workspace, int64_t workspace_bytes,
+                        gemm_stream_t stream) {
+    if (count < 0 || (count > 0 && (grads == nullptr || sizes == nullptr || dtypes == nullptr)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!(max_norm > 0.0f) || !(inv_scale > 0.0f) || std::isinf(inv_scale))
+        return GEMM_ERR_INVALID_VALUE;
+    if (norm == nullptr || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0)
+        return GEMM_ERR_INVALID_VALUE;
+    int64_t in_place = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] < 0 || sizes[i] > (1ll << 40) || !dtype_ok(dtypes[i]))
+            return GEMM_ERR_INVALID_VALUE;
+        if (sizes[i] == 0) continue;
+        const uintptr_t m = static_cast<uintptr_t>(esize(dtypes[i])) - 1;
+        const void* o = outs ? outs[i] : grads[i];
+        if (grads[i] == nullptr || o == nullptr || (reinterpret_cast<uintptr_t>(grads[i]) & m) != 0 ||
+            (reinterpret_cast<uintptr_t>(o) & m) != 0)
+            return GEMM_ERR_INVALID_VALUE;
+        if (o == grads[i]) ++in_place;
+    }
+    // chunk numbers are 32-bit within a launch
+    for (int64_t l = 0; l * kPerLaunch < count; ++l) {
+        int64_t chunks = 0;
+        for (int64_t i = l * kPerLaunch; i < count && i < (l + 1) * kPerLaunch; ++i)
+            chunks += (sizes[i] + kChunk - 1) / kChunk;
+        if (chunks > (1ll << 30)) return GEMM_ERR_INVALID_VALUE;
+    }
+    // a tensor listed twice in place would be scaled by two CTAs at once
+    if (in_place > 1) {
+        const void** p = new (std::nothrow) const void*[in_place];
+        if (p == nullptr) return GEMM_ERR_ALLOC;
+        int64_t n = 0;
+        for (int64_t i = 0; i < count; ++i)
+            if (sizes[i] > 0 && (outs ? outs[i] : grads[i]) == grads[i]) p[n++] = grads[i];
+        std::sort(p, p + n);
+        const bool twice = std::adjacent_find(p, p + n) != p + n;
+        delete[] p;
+        if (twice) return GEMM_ERR_INVALID_VALUE;
+    }
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
+        return GEMM_ERR_INVALID_VALUE;
+    const int sms = device_sms();
+    if (sms < 0) return GEMM_ERR_LAUNCH;
+    if (sms == 0) return GEMM_ERR_NOT_SUPPORTED;
+    if (workspace_bytes < workspace_for(count, sms)) return GEMM_ERR_INVALID_VALUE;
+    const Call c{count, grads, outs, sizes, dtypes, max_norm, inv_scale, norm,
+                 static_cast<double*>(workspace), sms * kCtasPerSm,
+                 reinterpret_cast<cudaStream_t>(stream)};
+    const cudaError_t e = count <= 64 ? run<64>(c) : run<kPerLaunch>(c);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,341 @@
+// norm.cu -- host side of the norms around a block (include/norm_sm103.h):
+// argument checks, the work split and the launches.
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include <cuda_runtime.h>
+
+#include "norm_launch.h"
+#include "norm_sm103.h"
+
+namespace {
+
+using namespace gemm103;
+using namespace gemm103::nrm;
+
+constexpr int64_t kSmemPerCta = 227 * 1024 - 1024;
+constexpr int64_t kMaxColumnsPerCta = 8192;  // backward
+constexpr int kRowsPerCtaThreads = 256;     // CTA size where a row needs fewer threads
+
+bool dtype_ok(int32_t t) { return t == GEMM_F16 || t == GEMM_BF16 || t == GEMM_F32; }
+int64_t esize(int32_t t) { return t == GEMM_F32 ? 4 : 2; }
+bool kind_ok(int32_t k) { return k == NORM_NONE || k == NORM_RMS || k == NORM_LAYER; }
+bool aligned(const void* p, int64_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool pair_ok(int32_t x, int32_t z) { return x == z || x == GEMM_F32; }
+
+// A matrix the call uses: NULL is refused where it is needed.
+bool matrix_ok(const void* p, int64_t ld, int64_t N, int32_t dtype) {
+    return p != nullptr && ld >= N && aligned(p, esize(dtype));
+}
+
+bool vector16(const void* p, int64_t ld, int32_t dtype) {
+    return p == nullptr || (aligned(p, 16) && ld * esize(dtype) % 16 == 0);
+}
+
+// SMs of the current device; 0 off sm_103, -1 on a CUDA error.
+int device_sms() {
+    int dev = 0, major = 0, minor = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return -1;
+    }
+    return major == 10 && minor == 3 ? sms : 0;
+}
+
+gemm_status_t check_block(int64_t M, int64_t N, int32_t x_dtype, int32_t z_dtype,
+                          const norm_block_t* b) {
+    if (b == nullptr || M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX)
+        return GEMM_ERR_INVALID_VALUE;
+    if (!dtype_ok(x_dtype) || !dtype_ok(z_dtype) || !kind_ok(b->pre) || !kind_ok(b->post))
+        return GEMM_ERR_INVALID_VALUE;
+    if (!(b->eps > 0.0f) || std::isinf(b->eps) || !std::isfinite(b->scale))
+        return GEMM_ERR_INVALID_VALUE;
+    const void* vecs[] = {b->pre_weight, b->pre_bias, b->post_weight, b->post_bias, b->gate};
+    for (const void* v : vecs) {
+        if (v == nullptr) continue;
+        if (!dtype_ok(b->vec_dtype) || !aligned(v, esize(b->vec_dtype))) return GEMM_ERR_INVALID_VALUE;
+    }
+    if (b->gate != nullptr && (b->gate_rows < 1 || b->ld_gate < N)) return GEMM_ERR_INVALID_VALUE;
+    if (!pair_ok(x_dtype, z_dtype)) return GEMM_ERR_NOT_SUPPORTED;
+    if (N > NORM_MAX_N) return GEMM_ERR_NOT_SUPPORTED;
+    return GEMM_OK;
+}
+
+void fill_block(Params& p, int64_t M, int64_t N, const norm_block_t* b) {
+    p.M = M;
+    p.N = static_cast<int32_t>(N);
+    p.wpre = b->pre_weight;
+    p.bpre = b->pre_bias;
+    p.wpost = b->post_weight;
+    p.bpost = b->post_bias;
+    p.gate = b->gate;
+    p.ld_gate = b->gate ? b->ld_gate : 0;
+    p.gate_rows = b->gate ? b->gate_rows : 1;
+    p.vec_dtype = b->vec_dtype;
+    bool wide = true;
+    const void* vecs[] = {b->pre_weight, b->pre_bias, b->post_weight, b->post_bias};
+    for (const void* v : vecs) wide = wide && aligned(v, 16);
+    if (b->gate) wide = wide && vector16(b->gate, b->ld_gate, b->vec_dtype);
+    p.vec_aligned = wide ? 1 : 0;
+    p.pre = b->pre;
+    p.post = b->post;
+    p.scale = b->scale;
+    p.eps = b->eps;
+    p.inv_n = 1.0f / static_cast<float>(N);
+}
+
+// Threads per row: the fewest of 32, 64, ... whose `chunks8` chunks of 8 hold N.
+int threads_for(int64_t N, int chunks8) {
+    int t = 32;
+    while (static_cast<int64_t>(t) * 8 * chunks8 < N) t *= 2;
+    return t;
+}
+
+// Ring depth: as many slots as fit beside each other in `budget` bytes, 2 to
+// kMaxStages (1 where two do not fit).
+int stages_for(int64_t slot, int groups, int64_t budget) {
+    int64_t s = (budget - 4096) / (slot * groups);
+    if (s > kMaxStages) s = kMaxStages;
+    return s < 1 ? 1 : static_cast<int>(s);
+}
+
+struct Chunks {
+    int64_t group_rows, groups, per_group, rows;
+};
+
+// Rows cut into about two chunks per SM, each inside one group of the gate.
+Chunks chunks_for(int64_t M, int64_t gate_rows, int64_t sms) {
+    Chunks c;
+    c.group_rows = (gate_rows > 1 && gate_rows < M) ? gate_rows : (M > 0 ? M : 1);
+    c.groups = ceil_div(M > 0 ? M : 1, c.group_rows);
+    int64_t per = ceil_div(2 * sms, c.groups);
+    if (per > c.group_rows) per = c.group_rows;
+    c.rows = ceil_div(c.group_rows, per);
+    c.per_group = ceil_div(c.group_rows, c.rows);
+    return c;
+}
+
+gemm_status_t status_of(cudaError_t e) {
+    if (e == cudaSuccess) return GEMM_OK;
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+}
+
+cudaError_t run_forward(int32_t x, int32_t z, const Launch& l) {
+    if (x == GEMM_F16) return forward_f16_f16(l);
+    if (x == GEMM_BF16) return forward_bf16_bf16(l);
+    if (z == GEMM_F16) return forward_f32_f16(l);
+    if (z == GEMM_BF16) return forward_f32_bf16(l);
+    return forward_f32_f32(l);
+}
+
+cudaError_t run_backward(int32_t x, int32_t z, const Launch& l) {
+    if (x == GEMM_F16) return backward_f16_f16(l);
+    if (x == GEMM_BF16) return backward_bf16_bf16(l);
+    if (z == GEMM_F16) return backward_f32_f16(l);
+    if (z == GEMM_BF16) return backward_f32_bf16(l);
+    return backward_f32_f32(l);
+}
+
+cudaError_t run_sum(const SumParams& s, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(s.N, 32)), 1, 1);
+    cfg.blockDim = dim3(32 * kSumY, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, sum_kernel, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ldx,
+                                 const void* Z, int64_t ldz, void* XO, int64_t ldxo,
+                                 void* Y, int64_t ldy, int32_t x_dtype, int32_t z_dtype,
+                                 const norm_block_t* block, gemm_stream_t stream) {
+    gemm_status_t st = check_block(M, N, x_dtype, z_dtype, block);
+    if (st == GEMM_ERR_INVALID_VALUE) return st;
+    const bool some = M > 0 && N > 0;         // of nothing, the pointers are not looked at
+    if (some && ((Z == nullptr) != (XO == nullptr) || (Z == nullptr && Y == nullptr)))
+        return GEMM_ERR_INVALID_VALUE;
+    if (some &&
+        (!matrix_ok(X, ldx, N, x_dtype) || (Z && !matrix_ok(Z, ldz, N, z_dtype)) ||
+         (XO && !matrix_ok(XO, ldxo, N, x_dtype)) || (Y && !matrix_ok(Y, ldy, N, z_dtype))))
+        return GEMM_ERR_INVALID_VALUE;
+    if (st != GEMM_OK) return st;
+    if (M == 0 || N == 0) return GEMM_OK;
+    const int sms = device_sms();
+    if (sms < 0) return GEMM_ERR_LAUNCH;
+    if (sms == 0) return GEMM_ERR_NOT_SUPPORTED;
+
+    Launch l;
+    std::memset(&l, 0, sizeof l);
+    Params& p = l.p;
+    fill_block(p, M, N, block);
+    p.X = X;
+    p.ldx = ldx;
+    p.Z = Z;
+    p.ldz = ldz;
+    p.XO = XO;
+    p.ldxo = ldxo;
+    p.Y = Y;
+    p.ldy = ldy;
+    p.vec = N % 8 == 0 && vector16(X, ldx, x_dtype) && vector16(Z, ldz, z_dtype) &&
+            vector16(XO, ldxo, x_dtype) && vector16(Y, ldy, z_dtype);
+    l.chunks8 = N > 8192 ? 2 : (M <= sms || N <= 256) ? 1 : 2;
+    p.T = threads_for(N, l.chunks8);
+    l.threads = p.T < kRowsPerCtaThreads ? kRowsPerCtaThreads : p.T;
+    const int groups = l.threads / p.T;
+    int64_t grid = ceil_div(M, groups);
+    const int64_t per_sm = 1024 / l.threads;              // resident CTAs
+    if (grid > sms * per_sm) grid = sms * per_sm;
+    const int64_t rows_each = ceil_div(M, grid * groups);
+    p.slot_bytes = static_cast<uint32_t>(l.chunks8 * 8 * p.T * (esize(x_dtype) + (Z ? esize(z_dtype) : 0)));
+    p.stages = stages_for(p.slot_bytes, groups, kSmemPerCta / per_sm);
+    if (p.stages > rows_each) p.stages = static_cast<int32_t>(rows_each);
+    l.grid = static_cast<int>(grid);
+    l.smem = static_cast<size_t>(groups) * (p.T / 32 * 32 + p.stages * static_cast<size_t>(p.slot_bytes));
+    l.stream = reinterpret_cast<cudaStream_t>(stream);
+    return status_of(run_forward(x_dtype, z_dtype, l));
+}
+
+int64_t norm_block_backward_workspace(int64_t M, int64_t N, int64_t gate_rows, int32_t num_sms) {
+    if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX || gate_rows < 1 || num_sms < 0) return -1;
+    if (num_sms == 0) {
+        num_sms = device_sms();
+        if (num_sms <= 0) return -1;
+    }
+    const Chunks c = chunks_for(M, gate_rows, num_sms);
+    return 4 * c.groups * c.per_group * N * 4;
+}
+
+gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t ldxo,
+                                  const void* Z, int64_t ldz, const void* dY, int64_t lddy,
+                                  const void* dXO, int64_t lddxo, void* dX, int64_t lddx,
+                                  void* dZ, int64_t lddz, int32_t x_dtype, int32_t z_dtype,
+                                  const norm_block_t* block, const norm_block_grads_t* grads,
+                                  void* workspace, int64_t workspace_bytes,
+                                  gemm_stream_t stream) {
+    gemm_status_t st = check_block(M, N, x_dtype, z_dtype, block);
+    if (st == GEMM_ERR_INVALID_VALUE) return st;
+    norm_block_grads_t none;
+    std::memset(&none, 0, sizeof none);
+    const norm_block_grads_t& gr = grads ? *grads : none;
+    void* const outs[] = {gr.d_pre_weight, gr.d_pre_bias, gr.d_post_weight, gr.d_post_bias, gr.d_gate};
+    bool sums = false;
+    for (void* o : outs) {
+        if (o == nullptr) continue;
+        sums = true;
+        if (!dtype_ok(gr.grad_dtype) || !aligned(o, esize(gr.grad_dtype))) return GEMM_ERR_INVALID_VALUE;
+    }
+    const bool some = M > 0 && N > 0;         // of nothing, the pointers are not looked at
+    if (some && Z == nullptr && (dZ || gr.d_post_weight || gr.d_post_bias || gr.d_gate))
+        return GEMM_ERR_INVALID_VALUE;
+    if (some && gr.d_gate && block->gate == nullptr) return GEMM_ERR_INVALID_VALUE;
+    if (some) {
+        if (!matrix_ok(XO, ldxo, N, x_dtype) || (Z && !matrix_ok(Z, ldz, N, z_dtype)) ||
+            (dY && !matrix_ok(dY, lddy, N, z_dtype)) || (dXO && !matrix_ok(dXO, lddxo, N, x_dtype)) ||
+            (dX && !matrix_ok(dX, lddx, N, x_dtype)) || (dZ && !matrix_ok(dZ, lddz, N, z_dtype)))
+            return GEMM_ERR_INVALID_VALUE;
+        if (sums && (workspace == nullptr || !aligned(workspace, 16))) return GEMM_ERR_INVALID_VALUE;
+    }
+    if (st != GEMM_OK) return st;
+    if (N == 0) return GEMM_OK;
+    const int sms = device_sms();
+    if (sms < 0) return GEMM_ERR_LAUNCH;
+    if (sms == 0) return GEMM_ERR_NOT_SUPPORTED;
+    const bool token = block->gate != nullptr && block->gate_rows == 1;
+    const Chunks ch = chunks_for(M, block->gate ? block->gate_rows : 1, sms);
+    const int64_t chunks = M > 0 ? ch.groups * ch.per_group : 0;
+    if (M > 0 && sums && workspace_bytes < 4 * chunks * N * 4) return GEMM_ERR_INVALID_VALUE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+
+    Launch l;
+    std::memset(&l, 0, sizeof l);
+    Params& p = l.p;
+    fill_block(p, M, N, block);
+    p.X = XO;
+    p.ldx = ldxo;
+    p.Z = Z;
+    p.ldz = ldz;
+    p.dY = dY;
+    p.lddy = lddy;
+    p.dXO = dXO;
+    p.lddxo = lddxo;
+    p.dX = dX;
+    p.lddx = lddx;
+    p.dZ = dZ;
+    p.lddz = lddz;
+    p.vec = N % 8 == 0 && vector16(XO, ldxo, x_dtype) && vector16(Z, ldz, z_dtype) &&
+            vector16(dY, lddy, z_dtype) && vector16(dXO, lddxo, x_dtype) &&
+            vector16(dX, lddx, x_dtype) && vector16(dZ, lddz, z_dtype);
+    p.token_gate = token ? 1 : 0;
+    p.chunk_group_rows = ch.group_rows;
+    p.chunks_per_group = static_cast<int32_t>(ch.per_group);
+    p.chunk_rows = ch.rows;
+    p.partials = sums ? static_cast<float*>(workspace) : nullptr;
+    p.part_stride = chunks * N;
+    p.dgate = token ? gr.d_gate : nullptr;
+    p.grad_dtype = gr.grad_dtype;
+    l.bias = gr.d_pre_bias || gr.d_post_bias || (!token && gr.d_gate && block->post_bias);
+    if (M > 0) {
+        // 8192 columns fill a CTA's registers: wider rows take a pair of CTAs
+        l.chunks8 = N > 2048 ? 2 : 1;
+        p.cluster = N > kMaxColumnsPerCta ? 2 : 1;
+        p.T = threads_for(N < kMaxColumnsPerCta ? N : kMaxColumnsPerCta, l.chunks8);
+        l.threads = p.T < kRowsPerCtaThreads ? kRowsPerCtaThreads : p.T;
+        const int groups = l.threads / p.T;
+        p.slot_bytes = static_cast<uint32_t>(
+            l.chunks8 * 8 * p.T *
+            (esize(x_dtype) * (dXO ? 2 : 1) + (Z ? esize(z_dtype) : 0) + (dY ? esize(z_dtype) : 0)));
+        const int64_t per_sm = l.threads == 256 ? 2 : 1;
+        p.stages = stages_for(p.slot_bytes, groups, kSmemPerCta / per_sm);
+        // the groups' column sums pass through the ring's memory
+        const size_t ring = static_cast<size_t>(groups) * p.stages * p.slot_bytes;
+        const size_t line = static_cast<size_t>(p.T) * l.chunks8 * 8 * 4;
+        l.smem = static_cast<size_t>(groups) * (p.T / 32 * 32) + (ring > line ? ring : line);
+        if (l.smem > static_cast<size_t>(kSmemPerCta)) return GEMM_ERR_NOT_SUPPORTED;
+        l.grid = static_cast<int>(chunks * p.cluster);
+        l.stream = s;
+        st = status_of(run_backward(x_dtype, z_dtype, l));
+        if (st != GEMM_OK) return st;
+    }
+    if (!sums) return GEMM_OK;
+    if (gr.d_gate && token && !(gr.d_pre_weight || gr.d_pre_bias || gr.d_post_weight || gr.d_post_bias))
+        return GEMM_OK;                                   // written row by row
+    SumParams sp;
+    std::memset(&sp, 0, sizeof sp);
+    sp.partials = p.partials;
+    sp.part_stride = p.part_stride;
+    sp.N = static_cast<int32_t>(N);
+    sp.groups = static_cast<int32_t>(M > 0 ? ch.groups : 1);
+    sp.chunks_per_group = M > 0 ? p.chunks_per_group : 0;
+    sp.token_gate = p.token_gate;
+    sp.bias = l.bias ? 1 : 0;
+    sp.wpost = p.wpost;
+    sp.bpost = p.bpost;
+    sp.gate = M > 0 ? p.gate : nullptr;
+    sp.ld_gate = p.ld_gate;
+    sp.vec_dtype = p.vec_dtype;
+    sp.grad_dtype = gr.grad_dtype;
+    sp.scale = p.scale;
+    sp.d_pre_weight = gr.d_pre_weight;
+    sp.d_pre_bias = gr.d_pre_bias;
+    sp.d_post_weight = gr.d_post_weight;
+    sp.d_post_bias = gr.d_post_bias;
+    sp.d_gate = (token || M == 0) ? nullptr : gr.d_gate;
+    return status_of(run_sum(sp, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,75 @@
+// norm_inst.cuh -- instantiates the norm kernels for one pair of types
+// (NORM_XT, NORM_ZT) behind plain launchers.
+#pragma once
+#include <mutex>
+
+#include "norm_launch.h"
+
+#define NORM_CAT2(a, b) a##b
+#define NORM_CAT(a, b) NORM_CAT2(a, b)
+
+namespace gemm103 {
+namespace nrm {
+
+template <typename K>
+static cudaError_t launch_kernel(K kern, const Launch& l, std::mutex& mu, size_t& raised_to) {
+    {
+        // raised once per size: a host call worth avoiding on every launch
+        std::lock_guard<std::mutex> g(mu);
+        if (l.smem > raised_to) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l.smem));
+            if (e != cudaSuccess) return e;
+            raised_to = l.smem;
+        }
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(l.grid, 1, 1);
+    cfg.blockDim = dim3(l.threads, 1, 1);
+    cfg.dynamicSmemBytes = l.smem;
+    cfg.stream = l.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = l.p.cluster == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, l.p);
+}
+
+template <int C>
+static cudaError_t forward_c(const Launch& l) {
+    static std::mutex mu;
+    static size_t raised_to = 0;
+    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, C>, l, mu, raised_to);
+}
+
+template <int C, bool BIAS, int THREADS>
+static cudaError_t backward_c(const Launch& l) {
+    static std::mutex mu;
+    static size_t raised_to = 0;
+    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, C, BIAS, THREADS>, l, mu, raised_to);
+}
+
+cudaError_t NORM_CAT(forward_, NORM_SUFFIX)(const Launch& l) {
+    return l.chunks8 == 1 ? forward_c<1>(l) : forward_c<2>(l);
+}
+
+template <bool BIAS>
+static cudaError_t backward_b(const Launch& l) {
+    switch (l.threads) {
+        case 256: return l.chunks8 == 1 ? backward_c<1, BIAS, 256>(l) : backward_c<2, BIAS, 256>(l);
+        case 512: return backward_c<2, BIAS, 512>(l);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t NORM_CAT(backward_, NORM_SUFFIX)(const Launch& l) {
+    return l.bias ? backward_b<true>(l) : backward_b<false>(l);
+}
+
+}  // namespace nrm
+}  // namespace gemm103

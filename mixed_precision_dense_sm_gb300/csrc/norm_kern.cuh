@@ -1,0 +1,926 @@
+// norm_kern.cuh -- the norms before and after a block, fused with its gate,
+// residual scale and residual add (include/norm_sm103.h): forward and
+// backward row kernels, and the backward's sum over rows.
+//
+// Both row kernels are bound by HBM: each matrix element is read once and
+// written once.  A row belongs to a group of T threads of a CTA (a warp for
+// narrow rows, the whole CTA for wide ones); each thread owns C chunks of 8
+// elements.  A thread copies its own elements of the next rows to shared
+// memory with cp.async while the group works on the current one, into a ring
+// of slots that only this thread reads: no barrier guards the copies, and no
+// registers hold loads in flight.  What the group shares are the sums of a
+// row: a butterfly in each warp, one shared-memory exchange, one barrier.
+//
+// Rows that are not 16-byte aligned, or N not a multiple of 8, go element by
+// element: a thread's 8 elements are then 32 apart, so a warp's accesses stay
+// contiguous.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+
+namespace gemm103 {
+namespace nrm {
+
+enum : int { kNone = 0, kRms = 1, kLayer = 2 };
+constexpr int kMaxStages = 4;
+
+struct Params {
+    // forward: X, Z in, XO, Y out; backward: X = XO, Z, dY, dXO in, dX, dZ out
+    const void* X; int64_t ldx;
+    const void* Z; int64_t ldz;
+    void* XO; int64_t ldxo;
+    void* Y; int64_t ldy;
+    const void* dY; int64_t lddy;
+    const void* dXO; int64_t lddxo;
+    void* dX; int64_t lddx;
+    void* dZ; int64_t lddz;
+    const void* wpre; const void* bpre; const void* wpost; const void* bpost;
+    const void* gate; int64_t ld_gate; int64_t gate_rows;
+    int32_t vec_dtype;
+    int32_t vec_aligned;        // weights, biases and gate rows are 16-byte aligned
+    int32_t vec;                // rows are 16-byte aligned and N a multiple of 8
+    int32_t pre, post;
+    float scale, eps, inv_n;
+    int64_t M;
+    int32_t N;
+    int32_t T;                  // threads per row
+    int32_t stages;             // slots of the ring
+    uint32_t slot_bytes;        // of one row of one group
+    // backward: rows are cut into chunks, one CTA each, that lie in one group
+    // of the gate (token gates, gate_rows == 1, count as one group)
+    int64_t chunk_group_rows;   // rows of a gate group (M where rows do not share one)
+    int32_t chunks_per_group;
+    int64_t chunk_rows;
+    int32_t token_gate;         // the gate's row changes with every row
+    int32_t cluster;            // CTAs that share a row (1 or 2), each half its columns
+    float* partials;            // [4][chunks][N]: sums of dY xhat, q zhat, dY, q (the last two: BIAS)
+    int64_t part_stride;        // chunks * N
+    void* dgate;                // written directly for token gates
+    int32_t grad_dtype;
+};
+
+// ------------------------------------------------------------------ elements
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
+    return __bfloat162float(v);
+}
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+// Where a thread's 8 elements of chunk c lie in the row: element e at
+// base + e * step.
+struct Spot {
+    int32_t base, step;
+};
+
+__device__ __forceinline__ Spot spot_of(bool vec, int T, int t, int c, int32_t first = 0) {
+    if (vec) return {first + (c * T + t) * 8, 1};
+    return {first + (c * T + (t & ~31)) * 8 + (t & 31), 32};
+}
+
+// 8 elements of a vector parameter (weight, bias, gate row) of type dtype.
+__device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool wide, Spot s,
+                                            int32_t N, float (&o)[8]) {
+    if (wide && s.step == 1) {
+        if (s.base >= N) {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = 0.0f;
+            return;
+        }
+        if (dtype == 2) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(v) + s.base);
+            const float4 a = __ldg(p), b = __ldg(p + 1);
+            o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+            o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+        } else {
+            union {
+                uint4 u;
+                __half h[8];
+                __nv_bfloat16 b[8];
+            } w;
+            w.u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(v) + s.base));
+            if (dtype == 1) {
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __bfloat162float(w.b[e]);
+            } else {
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __half2float(w.h[e]);
+            }
+        }
+        return;
+    }
+    #pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int32_t i = s.base + e * s.step;
+        o[e] = 0.0f;
+        if (i < N) {
+            if (dtype == 2) o[e] = __ldg(static_cast<const float*>(v) + i);
+            else if (dtype == 1) o[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(v)[i]);
+            else o[e] = __half2float(static_cast<const __half*>(v)[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ void store_elem(void* p, int32_t dtype, int64_t i, float v) {
+    if (dtype == 2) static_cast<float*>(p)[i] = v;
+    else if (dtype == 1) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most `n` of this thread's copy groups are in flight.
+__device__ __forceinline__ void cp_async_wait(int n) {
+    switch (n) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    }
+}
+
+// A thread's chunk c in a slot: 8 elements, 16-byte pieces strided by the
+// group's threads so that a warp's accesses are contiguous.
+template <typename E>
+__device__ __forceinline__ uint8_t* slot_at(uint8_t* slot, int T, int t, int c) {
+    constexpr int kPieces = sizeof(E) / 2;            // 16-byte pieces per 8 elements
+    return slot + (static_cast<uint32_t>(c * kPieces) * T + t) * 16u;
+}
+
+// Starts the copy of 8 elements of a row into this thread's part of a slot.
+template <typename E>
+__device__ __forceinline__ void fetch8(uint8_t* slot, int T, int t, int c, const E* row, Spot s,
+                                       int32_t N) {
+    constexpr int kPieces = sizeof(E) / 2;
+    uint8_t* d = slot_at<E>(slot, T, t, c);
+    if (s.step == 1) {
+        if (s.base < N) {
+            #pragma unroll
+            for (int q = 0; q < kPieces; ++q)
+                cp_async16(d + q * T * 16, row + s.base + q * (8 / kPieces));
+        }
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int32_t i = s.base + e * 32;
+            E* p = reinterpret_cast<E*>(d + (e / (8 / kPieces)) * T * 16) + e % (8 / kPieces);
+            if (i < N) {
+                if constexpr (sizeof(E) == 4) cp_async4(p, row + i);
+                else *p = row[i];                     // no 2-byte cp.async
+            }
+        }
+    }
+}
+
+// The 8 elements of this thread's part of a slot as FP32, 0 past column N.
+template <typename E>
+__device__ __forceinline__ void take8(uint8_t* slot, int T, int t, int c, Spot s, int32_t N,
+                                      float (&o)[8]) {
+    constexpr int kPieces = sizeof(E) / 2;
+    constexpr int kPer = 8 / kPieces;
+    const uint8_t* d = slot_at<E>(slot, T, t, c);
+    #pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+        union {
+            uint4 u;
+            E e[kPer];
+        } w;
+        w.u = *reinterpret_cast<const uint4*>(d + q * T * 16);
+        #pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            const int k = q * kPer + e;
+            o[k] = s.base + k * s.step < N ? to_f<E>(w.e[e]) : 0.0f;
+        }
+    }
+}
+
+template <typename E>
+__device__ __forceinline__ void store8(E* row, Spot s, int32_t N, const float (&v)[8]) {
+    constexpr int kPieces = sizeof(E) / 2;
+    constexpr int kPer = 8 / kPieces;
+    if (s.step == 1) {
+        if (s.base >= N) return;
+        #pragma unroll
+        for (int q = 0; q < kPieces; ++q) {
+            union {
+                uint4 u;
+                E e[kPer];
+            } w;
+            #pragma unroll
+            for (int e = 0; e < kPer; ++e) w.e[e] = from_f<E>(v[q * kPer + e]);
+            *reinterpret_cast<uint4*>(row + s.base + q * kPer) = w.u;
+        }
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (s.base + e * 32 < N) row[s.base + e * 32] = from_f<E>(v[e]);
+    }
+}
+
+// The group of threads that shares a row: T threads of the CTA, `warps` warps.
+struct Group {
+    int T, t, index, warps;     // threads, this thread's number, the group's number
+    float* red;                 // [2][warps][4] exchange buffer of this group
+    int parity;
+    float* pair;                // [2][2][4] exchange buffer of a CTA pair, or NULL
+    uint32_t rank;              // this CTA's number in the pair
+};
+
+__device__ __forceinline__ void group_barrier(const Group& g) {
+    if (g.T == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.T) : "memory");
+}
+
+// Sums of K values over the group, in the same order on every run; every
+// thread gets them.  One barrier: consecutive sums use alternate buffers.
+template <int K>
+__device__ __forceinline__ void group_sum(Group& g, float (&v)[K]) {
+    static_assert(K <= 4, "exchange buffer");
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        #pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+    if (g.T == 32) return;
+    float* r = g.red + g.parity * g.warps * 4;
+    g.parity ^= 1;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) {
+        #pragma unroll
+        for (int k = 0; k < K; ++k) r[(g.t >> 5) * 4 + k] = v[k];
+    }
+    group_barrier(g);
+    #pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = lane < g.warps ? r[lane * 4 + k] : 0.0f;
+    // warps is a power of two at most 32
+    for (int o = g.warps >> 1; o > 0; o >>= 1) {
+        #pragma unroll
+        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    }
+    #pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
+    if (g.pair == nullptr) return;
+    // the other half of the row: each CTA leaves its sums in both CTAs' shared
+    // memory, and both add them in rank order.  The buffer of this parity is
+    // written again only two sums on, behind the next sum's cluster barrier.
+    float* x = g.pair + (g.parity * 2 + g.rank) * 4;
+    if (g.t == 0) {
+        const uint32_t peer = map_to_rank(smem_addr(x), g.rank ^ 1u);
+        #pragma unroll
+        for (int k = 0; k < K; ++k) {
+            x[k] = v[k];
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer + 4u * k), "f"(v[k])
+                         : "memory");
+        }
+    }
+    cluster_sync_all();
+    const float* y = g.pair + g.parity * 8;
+    #pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = y[k] + y[4 + k];
+}
+
+__device__ __forceinline__ Group make_group(const Params& p, uint8_t* smem) {
+    Group g;
+    g.T = p.T;
+    g.index = static_cast<int>(threadIdx.x) / p.T;
+    g.t = static_cast<int>(threadIdx.x) - g.index * p.T;
+    g.warps = p.T >> 5;
+    g.red = reinterpret_cast<float*>(smem) + g.index * (2 * 4 * g.warps);
+    g.parity = 0;
+    g.pair = nullptr;
+    g.rank = 0;
+    return g;
+}
+
+// ------------------------------------------------------------------- forward
+
+// Rows go to groups round robin over the grid.
+template <typename XT, typename ZT, int C>
+__global__ void __launch_bounds__(1024)
+    forward_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Group g = make_group(p, smem);
+    const int groups = static_cast<int>(blockDim.x) / p.T;
+    uint8_t* ring = smem + groups * g.warps * 32 +
+                    static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
+    const uint32_t x_bytes = static_cast<uint32_t>(C) * 8u * sizeof(XT) * p.T;
+    const bool has_z = p.Z != nullptr;
+    const bool vec = p.vec != 0, wide = p.vec_aligned != 0;
+    const int32_t N = p.N;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + g.index;
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < p.M) {
+            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot sp = spot_of(vec, g.T, g.t, c);
+                fetch8<XT>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+                if (has_z)
+                    fetch8<ZT>(s + x_bytes, g.T, g.t, c,
+                               static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+            }
+        }
+        cp_async_commit();
+    };
+    for (int s = 0; s < p.stages - 1; ++s) fetch(first + s * step, s);
+    int slot = 0;
+    for (int64_t row = first; row < p.M; row += step) {
+        {
+            int ahead = slot + p.stages - 1;
+            if (ahead >= p.stages) ahead -= p.stages;
+            fetch(row + (p.stages - 1) * step, ahead);
+        }
+        cp_async_wait(p.stages - 1);
+        uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+        if (++slot == p.stages) slot = 0;
+
+        float x[C][8];
+        #pragma unroll
+        for (int c = 0; c < C; ++c)
+            take8<XT>(s, g.T, g.t, c, spot_of(vec, g.T, g.t, c), N, x[c]);
+        if (has_z) {
+            float z[C][8];
+            float mean = 0.0f, r = 1.0f;
+            #pragma unroll
+            for (int c = 0; c < C; ++c)
+                take8<ZT>(s + x_bytes, g.T, g.t, c, spot_of(vec, g.T, g.t, c), N, z[c]);
+            if (p.post == kLayer) {
+                float v[1] = {0.0f};
+                #pragma unroll
+                for (int c = 0; c < C; ++c)
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[0] += z[c][e];
+                group_sum(g, v);
+                mean = v[0] * p.inv_n;
+            }
+            if (p.post != kNone) {
+                float v[1] = {0.0f};
+                #pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const Spot sp = spot_of(vec, g.T, g.t, c);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float d = sp.base + e * sp.step < N ? z[c][e] - mean : 0.0f;
+                        v[0] = fmaf(d, d, v[0]);
+                    }
+                }
+                group_sum(g, v);
+                r = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
+            }
+            const int64_t grow = p.gate_rows > 1 ? row / p.gate_rows : row;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot sp = spot_of(vec, g.T, g.t, c);
+                float w[8];
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) z[c][e] = (z[c][e] - mean) * r;
+                if (p.wpost != nullptr) {
+                    load_param8(p.wpost, p.vec_dtype, wide, sp, N, w);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) z[c][e] *= w[e];
+                }
+                if (p.bpost != nullptr) {
+                    load_param8(p.bpost, p.vec_dtype, wide, sp, N, w);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) z[c][e] += w[e];
+                }
+                if (p.gate != nullptr) {
+                    const int64_t at = grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
+                    load_param8(static_cast<const uint8_t*>(p.gate) + at, p.vec_dtype, wide, sp, N, w);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) z[c][e] *= w[e];
+                }
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    // the stream as its type holds it: what is stored is what
+                    // the next norm sees
+                    x[c][e] = to_f<XT>(from_f<XT>(fmaf(p.scale, z[c][e], x[c][e])));
+                    if (sp.base + e * sp.step >= N) x[c][e] = 0.0f;
+                }
+                store8<XT>(static_cast<XT*>(p.XO) + row * p.ldxo, sp, N, x[c]);
+            }
+        }
+        if (p.Y != nullptr) {
+            float mean = 0.0f, r = 1.0f;
+            if (p.pre == kLayer) {
+                float v[1] = {0.0f};
+                #pragma unroll
+                for (int c = 0; c < C; ++c)
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[0] += x[c][e];
+                group_sum(g, v);
+                mean = v[0] * p.inv_n;
+            }
+            if (p.pre != kNone) {
+                float v[1] = {0.0f};
+                #pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const Spot sp = spot_of(vec, g.T, g.t, c);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float d = sp.base + e * sp.step < N ? x[c][e] - mean : 0.0f;
+                        v[0] = fmaf(d, d, v[0]);
+                    }
+                }
+                group_sum(g, v);
+                r = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
+            }
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot sp = spot_of(vec, g.T, g.t, c);
+                float w[8];
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) x[c][e] = (x[c][e] - mean) * r;
+                if (p.wpre != nullptr) {
+                    load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) x[c][e] *= w[e];
+                }
+                if (p.bpre != nullptr) {
+                    load_param8(p.bpre, p.vec_dtype, wide, sp, N, w);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) x[c][e] += w[e];
+                }
+                store8<ZT>(static_cast<ZT*>(p.Y) + row * p.ldy, sp, N, x[c]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+
+// The rows of chunk `b`: [row0, row1) inside one group of the gate.
+__device__ __forceinline__ void chunk_span(const Params& p, int64_t b, int64_t& row0, int64_t& row1,
+                                           int64_t& group) {
+    group = b / p.chunks_per_group;
+    const int64_t base = group * p.chunk_group_rows;
+    int64_t end = base + p.chunk_group_rows;
+    if (end > p.M) end = p.M;
+    row0 = base + (b - group * p.chunks_per_group) * p.chunk_rows;
+    row1 = row0 + p.chunk_rows;
+    if (row1 > end) row1 = end;
+}
+
+// One CTA per chunk of rows (or a pair of CTAs, each with half the columns of
+// rows wider than one CTA's registers hold), its groups taking the chunk's rows in turn.  Per
+// row: the statistics of XO and Z, the sums that the pre-norm's Jacobian
+// needs, then those of the post-norm's; per column, in registers, the sums
+// over the chunk's rows of dY xhat, dY, q zhat and q, with q = dXO' (the gate
+// is constant over a chunk and joins in the sum over chunks) or, for token
+// gates, q = scale gate dXO'.  The groups' sums meet in shared memory (in
+// group order) and go to the chunk's line of partials.
+template <typename XT, typename ZT, int C, bool BIAS, int THREADS>
+__global__ void __launch_bounds__(THREADS)
+    backward_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Group g = make_group(p, smem);
+    const int groups = static_cast<int>(blockDim.x) / p.T;
+    uint8_t* rings = smem + groups * g.warps * 32;
+    uint8_t* ring = rings + static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
+    // a slot: [XO][dXO][Z][dY], the absent ones left out
+    const uint32_t xb = static_cast<uint32_t>(C) * 8u * sizeof(XT) * p.T;
+    const uint32_t zb = static_cast<uint32_t>(C) * 8u * sizeof(ZT) * p.T;
+    const bool has_z = p.Z != nullptr, has_dy = p.dY != nullptr, has_dxo = p.dXO != nullptr;
+    const uint32_t o_dxo = xb, o_z = o_dxo + (has_dxo ? xb : 0u), o_dy = o_z + (has_z ? zb : 0u);
+    const bool vec = p.vec != 0, wide = p.vec_aligned != 0;
+    const int32_t N = p.N;
+    __shared__ float pair[16];
+    int32_t col0 = 0;
+    int64_t chunk = blockIdx.x;
+    if (p.cluster == 2) {
+        g.rank = cluster_ctarank();
+        g.pair = pair;
+        col0 = static_cast<int32_t>(g.rank) * p.T * C * 8;
+        chunk >>= 1;
+    }
+    int64_t row0, row1, group;
+    chunk_span(p, chunk, row0, row1, group);
+    if (p.cluster == 2) cluster_sync_all();     // the other CTA's shared memory is there
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < row1) {
+            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+                fetch8<XT>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+                if (has_dxo)
+                    fetch8<XT>(s + o_dxo, g.T, g.t, c,
+                               static_cast<const XT*>(p.dXO) + row * p.lddxo, sp, N);
+                if (has_z)
+                    fetch8<ZT>(s + o_z, g.T, g.t, c,
+                               static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+                if (has_dy)
+                    fetch8<ZT>(s + o_dy, g.T, g.t, c,
+                               static_cast<const ZT*>(p.dY) + row * p.lddy, sp, N);
+            }
+        }
+        cp_async_commit();
+    };
+
+    float a_yx[C][8], a_y[BIAS ? C : 1][8], a_qz[C][8], a_q[BIAS ? C : 1][8];
+    #pragma unroll
+    for (int c = 0; c < C; ++c) {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a_yx[c][e] = a_qz[c][e] = 0.0f;
+            if constexpr (BIAS) a_y[c][e] = a_q[c][e] = 0.0f;
+        }
+    }
+
+    for (int s = 0; s < p.stages - 1; ++s) fetch(row0 + g.index + static_cast<int64_t>(s) * groups, s);
+    int slot = 0;
+    for (int64_t row = row0 + g.index; row < row1; row += groups) {
+        {
+            int ahead = slot + p.stages - 1;
+            if (ahead >= p.stages) ahead -= p.stages;
+            fetch(row + static_cast<int64_t>(p.stages - 1) * groups, ahead);
+        }
+        cp_async_wait(p.stages - 1);
+        uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+        if (++slot == p.stages) slot = 0;
+
+        // ---- statistics of XO and Z, and the sums with g = dY * wpre
+        float mx = 0.0f, mz = 0.0f, gsum = 0.0f;
+        if (p.pre == kLayer || p.post == kLayer) {
+            float v[3] = {0.0f, 0.0f, 0.0f};
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+                float b[8], w[8];
+                if (p.pre == kLayer) {
+                    take8<XT>(s, g.T, g.t, c, sp, N, b);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[0] += b[e];
+                    if (has_dy) {
+                        take8<ZT>(s + o_dy, g.T, g.t, c, sp, N, b);
+                        if (p.wpre != nullptr) {
+                            load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
+                            #pragma unroll
+                            for (int e = 0; e < 8; ++e) v[1] = fmaf(b[e], w[e], v[1]);
+                        } else {
+                            #pragma unroll
+                            for (int e = 0; e < 8; ++e) v[1] += b[e];
+                        }
+                    }
+                }
+                if (has_z && p.post == kLayer) {
+                    take8<ZT>(s + o_z, g.T, g.t, c, sp, N, b);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[2] += b[e];
+                }
+            }
+            group_sum(g, v);
+            mx = v[0] * p.inv_n;
+            gsum = v[1] * p.inv_n;
+            mz = v[2] * p.inv_n;
+        }
+        float rx = 1.0f, rz = 1.0f, gx = 0.0f;      // gx: mean of g xhat
+        {
+            float v[3] = {0.0f, 0.0f, 0.0f};
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+                float b[8], w[8], x[8];
+                if (has_dy && p.pre != kNone) {
+                    take8<XT>(s, g.T, g.t, c, sp, N, x);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x[e] = sp.base + e * sp.step < N ? x[e] - mx : 0.0f;
+                        v[0] = fmaf(x[e], x[e], v[0]);
+                    }
+                    take8<ZT>(s + o_dy, g.T, g.t, c, sp, N, b);
+                    if (p.wpre != nullptr) {
+                        load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) b[e] *= w[e];
+                    }
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) v[1] = fmaf(b[e], x[e], v[1]);
+                }
+                if (has_z && p.post != kNone) {
+                    take8<ZT>(s + o_z, g.T, g.t, c, sp, N, b);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float d = sp.base + e * sp.step < N ? b[e] - mz : 0.0f;
+                        v[2] = fmaf(d, d, v[2]);
+                    }
+                }
+            }
+            if (p.pre != kNone || p.post != kNone) group_sum(g, v);
+            if (p.pre != kNone) rx = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
+            if (p.post != kNone) rz = 1.0f / sqrtf(fmaf(v[2], p.inv_n, p.eps));
+            gx = v[1] * rx * p.inv_n;
+        }
+
+        // ---- dXO' and its column sums; the post-norm's sums
+        float d[C][8];                               // dXO', then gz = dn * wpost
+        float v2[2] = {0.0f, 0.0f};
+        const int64_t grow = p.token_gate ? row : group;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+            float b[8], w[8];
+            if (has_dxo) {
+                take8<XT>(s + o_dxo, g.T, g.t, c, sp, N, d[c]);
+            } else {
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) d[c][e] = 0.0f;
+            }
+            if (has_dy) {
+                float x[8];
+                take8<XT>(s, g.T, g.t, c, sp, N, x);
+                take8<ZT>(s + o_dy, g.T, g.t, c, sp, N, b);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    x[e] = sp.base + e * sp.step < N ? (x[e] - mx) * rx : 0.0f;
+                    a_yx[c][e] = fmaf(b[e], x[e], a_yx[c][e]);
+                    if constexpr (BIAS) a_y[c][e] += b[e];
+                }
+                if (p.wpre != nullptr) {
+                    load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) b[e] *= w[e];
+                }
+                if (p.pre != kNone) {
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        b[e] = sp.base + e * sp.step < N ? (b[e] - gsum - x[e] * gx) * rx : 0.0f;
+                }
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) d[c][e] += b[e];
+            }
+            if (p.dX != nullptr)
+                store8<XT>(static_cast<XT*>(p.dX) + row * p.lddx, sp, N, d[c]);
+            if (has_z) {
+                float z[8], gt[8];
+                take8<ZT>(s + o_z, g.T, g.t, c, sp, N, z);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    z[e] = sp.base + e * sp.step < N ? (z[e] - mz) * rz : 0.0f;
+                    gt[e] = p.scale;
+                }
+                if (p.gate != nullptr) {
+                    const int64_t at = grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
+                    load_param8(static_cast<const uint8_t*>(p.gate) + at, p.vec_dtype, wide, sp, N, gt);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) gt[e] *= p.scale;
+                }
+                if (p.token_gate && p.dgate != nullptr) {
+                    // scale * dXO' * n, one row of the gate per row
+                    float n[8];
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) n[e] = z[e];
+                    if (p.wpost != nullptr) {
+                        load_param8(p.wpost, p.vec_dtype, wide, sp, N, w);
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) n[e] *= w[e];
+                    }
+                    if (p.bpost != nullptr) {
+                        load_param8(p.bpost, p.vec_dtype, wide, sp, N, w);
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) n[e] += w[e];
+                    }
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int32_t i = sp.base + e * sp.step;
+                        if (i < N) store_elem(p.dgate, p.grad_dtype, row * N + i, p.scale * d[c][e] * n[e]);
+                    }
+                }
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float q = p.token_gate ? d[c][e] * gt[e] : d[c][e];
+                    a_qz[c][e] = fmaf(q, z[e], a_qz[c][e]);
+                    if constexpr (BIAS) a_q[c][e] += q;
+                    d[c][e] *= gt[e];
+                }
+                if (p.wpost != nullptr) {
+                    load_param8(p.wpost, p.vec_dtype, wide, sp, N, w);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) d[c][e] *= w[e];
+                }
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    v2[0] = fmaf(d[c][e], z[e], v2[0]);
+                    v2[1] += d[c][e];
+                }
+            }
+        }
+        if (has_z && p.dZ != nullptr) {
+            float gz = 0.0f, gm = 0.0f;
+            if (p.post != kNone) {
+                group_sum(g, v2);
+                gz = v2[0] * p.inv_n;
+                gm = p.post == kLayer ? v2[1] * p.inv_n : 0.0f;
+            }
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+                if (p.post != kNone) {
+                    float z[8];
+                    take8<ZT>(s + o_z, g.T, g.t, c, sp, N, z);
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        d[c][e] = (d[c][e] - gm - (z[e] - mz) * rz * gz) * rz;
+                }
+                store8<ZT>(static_cast<ZT*>(p.dZ) + row * p.lddz, sp, N, d[c]);
+            }
+        }
+    }
+
+    // ---- the chunk's column sums: the groups' sums meet in the slots' memory
+    if (p.partials == nullptr) return;
+    cp_async_wait(0);
+    const int kinds = BIAS ? 4 : 2;                  // 0 dY xhat, 1 q zhat, 2 dY, 3 q
+    float* line = reinterpret_cast<float*>(rings);   // one group's sums: T * C * 8 floats
+    for (int k = 0; k < kinds; ++k) {
+        for (int gi = 1; gi < groups; ++gi) {
+            __syncthreads();
+            if (g.index == gi) {
+                #pragma unroll
+                for (int c = 0; c < C; ++c)
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float v = k == 0 ? a_yx[c][e] : a_qz[c][e];
+                        if constexpr (BIAS) v = k == 2 ? a_y[c][e] : k == 3 ? a_q[c][e] : v;
+                        line[(c * 8 + e) * p.T + g.t] = v;
+                    }
+            }
+            __syncthreads();
+            if (g.index == 0) {
+                #pragma unroll
+                for (int c = 0; c < C; ++c)
+                    #pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = line[(c * 8 + e) * p.T + g.t];
+                        if (k == 0) a_yx[c][e] += v;
+                        else if (k == 1) a_qz[c][e] += v;
+                        if constexpr (BIAS) {
+                            if (k == 2) a_y[c][e] += v;
+                            else if (k == 3) a_q[c][e] += v;
+                        }
+                    }
+            }
+        }
+    }
+    if (g.index == 0) {
+        float* out = p.partials + chunk * N;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int32_t i = sp.base + e * sp.step;
+                if (i >= N) continue;
+                out[i] = a_yx[c][e];
+                out[p.part_stride + i] = a_qz[c][e];
+                if constexpr (BIAS) {
+                    out[2 * p.part_stride + i] = a_y[c][e];
+                    out[3 * p.part_stride + i] = a_q[c][e];
+                }
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------- the sum over the chunks
+
+struct SumParams {
+    const float* partials;
+    int64_t part_stride;
+    int32_t N;
+    int32_t groups, chunks_per_group, token_gate;
+    int32_t bias;               // the sums of dY and q were taken
+    const void* wpost; const void* bpost; const void* gate;
+    int64_t ld_gate;
+    int32_t vec_dtype, grad_dtype;
+    float scale;
+    void* d_pre_weight; void* d_pre_bias; void* d_post_weight; void* d_post_bias; void* d_gate;
+};
+
+__device__ __forceinline__ float param_elem(const void* v, int32_t dtype, int64_t i, float absent) {
+    if (v == nullptr) return absent;
+    if (dtype == 2) return static_cast<const float*>(v)[i];
+    if (dtype == 1) return __bfloat162float(static_cast<const __nv_bfloat16*>(v)[i]);
+    return __half2float(static_cast<const __half*>(v)[i]);
+}
+
+constexpr int kSumY = 16;
+
+// Sums over the chunks: 32 columns per CTA, kSumY lines of threads.  With few
+// gate groups the lines share each group's chunks and a group's lines are
+// added in order; with many, each line takes whole groups.  The gate joins
+// here: it is constant over a group.
+static __global__ void __launch_bounds__(32 * kSumY)
+    sum_kernel(const __grid_constant__ SumParams p) {
+    __shared__ float red[4][kSumY][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int32_t col = static_cast<int32_t>(blockIdx.x) * 32 + tx;
+    const bool in = col < p.N;
+    grid_dependency_wait();
+    grid_dependents_launch();
+    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // dY xhat, q zhat, dY, q over all chunks
+    // sums of chunks first, first + step, ... of group gr
+    auto add = [&](int32_t gr, int32_t first, int32_t step, float (&a)[4]) {
+        const float* base = p.partials + static_cast<int64_t>(gr) * p.chunks_per_group * p.N + col;
+        #pragma unroll 4
+        for (int32_t c = first; c < p.chunks_per_group; c += step) {
+            const float* q = base + static_cast<int64_t>(c) * p.N;
+            a[0] += q[0];
+            a[1] += q[p.part_stride];
+            if (p.bias) {
+                a[2] += q[2 * p.part_stride];
+                a[3] += q[3 * p.part_stride];
+            }
+        }
+    };
+    // a group's sums: the gate's gradient, and the gated part of the totals
+    auto take = [&](int32_t gr, const float (&s)[4]) {
+        float gt = 1.0f;
+        if (!p.token_gate) {
+            gt = p.scale * param_elem(p.gate, p.vec_dtype, gr * p.ld_gate + col, 1.0f);
+            if (p.d_gate != nullptr) {
+                float v = s[1] * param_elem(p.wpost, p.vec_dtype, col, 1.0f);
+                if (p.bpost != nullptr) v = fmaf(s[3], param_elem(p.bpost, p.vec_dtype, col, 0.0f), v);
+                store_elem(p.d_gate, p.grad_dtype, static_cast<int64_t>(gr) * p.N + col, p.scale * v);
+            }
+        }
+        t[0] += s[0];
+        t[1] = fmaf(gt, s[1], t[1]);
+        t[2] += s[2];
+        t[3] = fmaf(gt, s[3], t[3]);
+    };
+    const bool by_group = p.groups >= kSumY;
+    if (by_group) {
+        if (in) {
+            for (int32_t gr = ty; gr < p.groups; gr += kSumY) {
+                float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                add(gr, 0, 1, a);
+                take(gr, a);
+            }
+        }
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) red[k][ty][tx] = t[k];
+        __syncthreads();
+        if (ty == 0) {
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                t[k] = 0.0f;
+                #pragma unroll
+                for (int y = 0; y < kSumY; ++y) t[k] += red[k][y][tx];
+            }
+        }
+    } else {
+        for (int32_t gr = 0; gr < p.groups; ++gr) {
+            float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (in) add(gr, ty, kSumY, a);
+            #pragma unroll
+            for (int k = 0; k < 4; ++k) red[k][ty][tx] = a[k];
+            __syncthreads();
+            if (ty == 0 && in) {
+                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                #pragma unroll
+                for (int y = 0; y < kSumY; ++y) {
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) s[k] += red[k][y][tx];
+                }
+                take(gr, s);
+            }
+            __syncthreads();
+        }
+    }
+    if (ty == 0 && in) {
+        if (p.d_pre_weight) store_elem(p.d_pre_weight, p.grad_dtype, col, t[0]);
+        if (p.d_post_weight) store_elem(p.d_post_weight, p.grad_dtype, col, t[1]);
+        if (p.d_pre_bias) store_elem(p.d_pre_bias, p.grad_dtype, col, t[2]);
+        if (p.d_post_bias) store_elem(p.d_post_bias, p.grad_dtype, col, t[3]);
+    }
+}
+
+}  // namespace nrm
+}  // namespace gemm103
