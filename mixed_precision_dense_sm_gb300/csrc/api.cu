@@ -146,7 +146,8 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
                         const void* C, int64_t ldc, gemm_dtypes_t dt, int32_t num_sms,
                         int32_t smem_optin, Plan& pl, bool allow_swap = true, bool ln = false,
                         int32_t max_kc = kMaxKc, int32_t min_kc2_stages = 3,
-                        bool allow_sk = true, int32_t max_sk_units = 0, bool mh2 = false) {
+                        bool allow_sk = true, int32_t max_sk_units = 0, bool mh2 = false,
+                        bool glu = false) {
     gemm_status_t st = check_args(transA, transB, M, N, K, alpha, A, lda, B, ldb, beta, C, ldc, dt);
     if (st != GEMM_OK) return st;
     if (num_sms < 1 || smem_optin < 64 * 1024) return GEMM_ERR_INVALID_VALUE;
@@ -348,7 +349,9 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     // not use is left to the L1 cache).
     const bool c_stage_ok = pl.pub.c_vector && !ln && !use_mh2;
     const int64_t avail_all = smem_optin - 1024 - barrier_bytes - static_bytes;
-    const int64_t avail = avail_all - (c_stage_ok ? kCStageBytes : 0);
+    // (the swapped gated layer exchanges its halves through the same area)
+    const bool exchange = glu && swap;
+    const int64_t avail = avail_all - (c_stage_ok || exchange ? kCStageBytes : 0);
     pl.kc = (kc2_ok && avail / (2 * static_cast<int64_t>(chunk_bytes)) >= min_kc2_stages) ? 2 : 1;
     const int64_t block_k = chunk_k * pl.kc;
     pl.k_blocks = static_cast<int32_t>(ceil_div(K, block_k));
@@ -402,10 +405,11 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     // that the steps' latency after a lone or last tile is small beside its
     // mainloop; with a residual (beta != 0) the reads of C come first and the
     // steps' barriers serialise them: row stores there.
-    pl.c_tma = c_stage_ok && beta == 0.0f &&
+    // (A gated 64-wide tile has 32 output columns, half a staging box.)
+    pl.c_tma = c_stage_ok && beta == 0.0f && !(glu && bn == 64) &&
                ((dt.c == GEMM_F32 && K >= 2048) || (!stream_k && tiles >= 2 * (num_sms / cg)));
     pl.pub.c_tma = pl.c_tma ? 1 : 0;
-    if (pl.c_tma) {
+    if (pl.c_tma || exchange) {
         pl.smem_bytes += kCStageBytes;
     } else if (c_stage_ok) {
         int64_t s_all = avail_all / stage_bytes;
@@ -463,6 +467,12 @@ struct ConvDesc {
     const void* X;
     const void* Wt;
     EncodeIm2colFn encode_im2col;
+};
+
+// A gated linear layer on the plan of the M x 2F product.
+struct GluDesc {
+    int64_t M, F, ldh;
+    const glu_forward_t* opt;
 };
 
 }  // namespace
@@ -619,6 +629,55 @@ bool encode_conv_filter(EncodeTiledFn encode, const ConvDesc& cd, CUtensorMap* m
     return r == CUDA_SUCCESS;
 }
 
+// The gated layer's W (2F x K, row pitch ld) with its halves as a dimension:
+// (K, F, 2), or with `chunks` > 1 (K a whole number of 128-byte chunks)
+// (chunk, F, 2, K / chunk).  A box is `rows` rows of `parts` halves -- in
+// shared memory, per chunk, the gate's rows and behind them the up
+// projection's.  Rows past F read zeros.
+bool encode_glu_weights(EncodeTiledFn encode, CUtensorMap* map, int32_t dtype, const void* ptr,
+                        int64_t K, int64_t F, int64_t ld, uint32_t rows, uint32_t parts,
+                        int32_t chunks) {
+    const CUtensorMapDataType ty = dtype == GEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t row = static_cast<cuuint64_t>(ld * 2), half = static_cast<cuuint64_t>(F * ld * 2);
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r;
+    if (chunks == 1) {
+        const cuuint64_t dims[3] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(F), 2};
+        const cuuint64_t strides[2] = {row, half};
+        const cuuint32_t box[3] = {64, rows, parts};
+        r = encode(map, ty, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    } else {
+        if (K % 64 != 0) return false;
+        const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(F), 2, static_cast<cuuint64_t>(K / 64)};
+        const cuuint64_t strides[3] = {row, half, 128};
+        const cuuint32_t box[4] = {64, rows, parts, static_cast<cuuint32_t>(chunks)};
+        r = encode(map, ty, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    }
+    return r == CUDA_SUCCESS;
+}
+
+// P (M x 2F, row pitch ld) as (F, M, 2) for the epilogue's TMA stores: a box
+// is 128 bytes of one half by 128 rows, clipped at F and M.
+bool encode_glu_store(EncodeTiledFn encode, CUtensorMap* map, int32_t dtype, void* ptr, int64_t F,
+                      int64_t M, int64_t ld) {
+    const int64_t es = out_elem_bytes(dtype);
+    const CUtensorMapDataType ty = dtype == GEMM_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : dtype == GEMM_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(F), static_cast<cuuint64_t>(M), 2};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld * es), static_cast<cuuint64_t>(F * es)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(kBlockM), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return encode(map, ty, 3, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The handle's workspace of at least `bytes`.  Under stream capture it cannot
 // grow (an allocation would end the capture): ALLOC.  A buffer that a captured
 // graph may still address is kept until gemm_destroy when it is outgrown.
@@ -724,6 +783,12 @@ gemm_status_t enqueue_ln_rows(int64_t M, int64_t N, void* C, int64_t ldc, gemm_d
     return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
+// P's rows and both its halves start on 16-byte boundaries.
+bool glu_p_vector(int64_t F, const glu_forward_t* o, int32_t c_dtype) {
+    const int64_t es = static_cast<int64_t>(out_elem_bytes(c_dtype));
+    return aligned16(o->P) && o->ldp * es % 16 == 0 && F * es % 16 == 0;
+}
+
 // Everything gemm_run enqueues after planning: the optional pack pre-passes,
 // the TMA descriptors and the GEMM kernel.  `ws` is the workspace laid out as
 // [tile counters (4 KB)][packed A][packed B][partial slots]; with
@@ -732,7 +797,8 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
                            int* err_dev, float alpha, float beta, void* C, gemm_dtypes_t dt,
                            cudaStream_t stream, bool clear_counters, uint32_t debug_flags = 0,
                            uint64_t wait_limit_ns = 0, const gemm_epilogue_t* ep = nullptr,
-                           const ConvDesc* conv = nullptr, const gemm_layernorm_t* ln = nullptr) {
+                           const ConvDesc* conv = nullptr, const gemm_layernorm_t* ln = nullptr,
+                           const GluDesc* glu = nullptr) {
     // kind::tf32 reads K-major operands only; the planner transposes the rest.
     if (pl.esize == 4 && (pl.a.mn_major || pl.b.mn_major)) return GEMM_ERR_NOT_SUPPORTED;
     int* counters = reinterpret_cast<int*>(ws);
@@ -811,6 +877,16 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
             ok = ok && encode_operand(encode, &l.tmB, dt.b, conv->Wt, conv->R * conv->S * conv->C,
                                       conv->K, conv->R * conv->S * conv->C,
                                       static_cast<uint32_t>(bn / cg), pl.kc);
+    } else if (glu != nullptr) {
+        // W is the kernel's A where swapped, its B otherwise
+        const bool sw = pl.pub.swap_ab != 0;
+        const OperandDesc& w = sw ? pl.a : pl.b;
+        const OperandDesc& x = sw ? pl.b : pl.a;
+        const uint32_t w_rows = sw ? 64u : static_cast<uint32_t>(bn / 2);
+        ok = encode_glu_weights(encode, sw ? &l.tmA : &l.tmB, dt.a, sw ? a_ptr : b_ptr, pl.K, glu->F,
+                                w.packed_ld, w_rows, cg == 2 ? 1u : 2u, pl.kc);
+        ok = ok && encode_operand(encode, sw ? &l.tmB : &l.tmA, dt.a, sw ? b_ptr : a_ptr, x.cols,
+                                  x.rows, x.packed_ld, static_cast<uint32_t>(sw ? bn : kBlockM), pl.kc);
     } else {
         ok = encode_operand(encode, &l.tmA, dt.a, a_ptr, pl.a.cols, pl.a.rows, pl.a.packed_ld,
                             pl.a.mn_major ? mn_box : static_cast<uint32_t>(kBlockM * pl.mh),
@@ -821,7 +897,17 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
                                   pl.b.mn_major ? 1 : pl.kc);
     }
     if (!ok) return GEMM_ERR_LAUNCH;
-    const bool c_tma = pl.c_tma && encode_c_store(encode, &l.tmC, dt.c, C, pl.Nk, pl.Mk, pl.c_rs);
+    bool c_tma;
+    if (glu != nullptr) {
+        const glu_forward_t* o = glu->opt;
+        c_tma = pl.c_tma && encode_c_store(encode, &l.tmC, dt.c, C, glu->F, glu->M, glu->ldh) &&
+                (o->P == nullptr ||
+                 encode_glu_store(encode, &l.glu.tmP, dt.c, o->P, glu->F, glu->M, o->ldp));
+        // the shared-memory layout follows the plan
+        if (pl.c_tma && !c_tma) return GEMM_ERR_LAUNCH;
+    } else {
+        c_tma = pl.c_tma && encode_c_store(encode, &l.tmC, dt.c, C, pl.Nk, pl.Mk, pl.c_rs);
+    }
 
     TcParams& p = l.p;
     p.M = static_cast<int32_t>(pl.Mk);
@@ -917,6 +1003,24 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
             p.halo_stage_bytes = pl.halo_stage_bytes;
         }
     }
+    if (glu != nullptr) {
+        const glu_forward_t* o = glu->opt;
+        const bool sw = pl.pub.swap_ab != 0;
+        l.epi = kEpiGlu;
+        p.M = static_cast<int32_t>(sw ? glu->F : glu->M);
+        p.N = static_cast<int32_t>(sw ? glu->M : glu->F);
+        p.c_rs = sw ? 1 : glu->ldh;
+        p.c_cs = sw ? glu->ldh : 1;
+        p.bias = o->bias;
+        p.bias_dtype = o->bias ? o->bias_dtype : GEMM_F32;
+        p.act = o->activation;
+        l.glu.P = o->P;
+        l.glu.ldp = o->ldp;
+        l.glu.F = static_cast<int32_t>(glu->F);
+        l.glu.swap = sw ? 1 : 0;
+        l.glu.p_vector = glu_p_vector(glu->F, o, dt.c) ? 1 : 0;
+        static_cast<TcParams&>(l.glu) = p;
+    }
     l.grid = pl.pub.grid;
     l.cta_group = cg;
     l.block_n = bn;
@@ -931,6 +1035,10 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
         if (dt.c == GEMM_F32) e = launch_tc_tf32_f32(l);
         else if (dt.c == GEMM_F16) e = launch_tc_tf32_f16(l);
         else e = launch_tc_tf32_bf16(l);
+    } else if (glu != nullptr) {
+        if (dt.c == GEMM_F32) e = launch_glu_f32(l);
+        else if (dt.c == GEMM_F16) e = launch_glu_f16(l);
+        else e = launch_glu_bf16(l);
     } else {
         if (dt.c == GEMM_F32) e = launch_tc_f32(l);
         else if (dt.c == GEMM_F16) e = launch_tc_f16(l);
@@ -1547,20 +1655,35 @@ bool device_current(const gemm_ctx* h) {
     return dev == h->device;
 }
 
+// The plan of the M x 2F product whose tiles hold gate and up columns (or,
+// swapped, rows) in equal parts; H's rows decide how the epilogue stores
+// (element by element where P could not follow by vectors).
+gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W,
+                       int64_t ldw, const void* H, int64_t ldh, gemm_dtypes_t dt,
+                       const glu_forward_t* o, int32_t num_sms, int32_t smem_optin, Plan& pl) {
+    const int64_t es = static_cast<int64_t>(out_elem_bytes(dt.c));
+    const bool vec = aligned16(H) && ldh * es % 16 == 0 && (o->P == nullptr || glu_p_vector(F, o, dt.c));
+    // any output row of 2F elements with that alignment stands for H's
+    const void* c = M > 0 && F > 0 ? reinterpret_cast<const void*>(static_cast<uintptr_t>(vec ? 256 : es))
+                                   : H;
+    return make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, c, round_up(max1(2 * F), 8), dt,
+                     num_sms, smem_optin, pl, true, false, kMaxKc, 3, true, 0, false, true);
+}
+
 template <typename OutT>
-void launch_glu_gate(const float* S, const glu_forward_t* o, void* H, int64_t ldh, int64_t M,
-                     int64_t F, int num_sms, cudaStream_t stream) {
+void launch_glu_gate(const glu_forward_t* o, void* H, int64_t ldh, int64_t M, int64_t F, int num_sms,
+                     cudaStream_t stream) {
     glu_gate_kernel<OutT><<<grid_for(M * F, num_sms), 256, 0, stream>>>(
-        S, o->bias, o->bias_dtype, o->activation, static_cast<OutT*>(H), ldh,
+        o->bias, o->bias_dtype, o->activation, static_cast<OutT*>(H), ldh,
         static_cast<OutT*>(o->P), o->ldp, M, F);
 }
 
-gemm_status_t enqueue_glu_gate(const float* S, const glu_forward_t* o, void* H, int64_t ldh,
-                               int64_t M, int64_t F, int32_t c_dtype, int num_sms,
-                               cudaStream_t stream) {
-    if (c_dtype == GEMM_F32) launch_glu_gate<float>(S, o, H, ldh, M, F, num_sms, stream);
-    else if (c_dtype == GEMM_F16) launch_glu_gate<__half>(S, o, H, ldh, M, F, num_sms, stream);
-    else launch_glu_gate<__nv_bfloat16>(S, o, H, ldh, M, F, num_sms, stream);
+// K == 0: P = bias.
+gemm_status_t enqueue_glu_gate(const glu_forward_t* o, void* H, int64_t ldh, int64_t M, int64_t F,
+                               int32_t c_dtype, int num_sms, cudaStream_t stream) {
+    if (c_dtype == GEMM_F32) launch_glu_gate<float>(o, H, ldh, M, F, num_sms, stream);
+    else if (c_dtype == GEMM_F16) launch_glu_gate<__half>(o, H, ldh, M, F, num_sms, stream);
+    else launch_glu_gate<__nv_bfloat16>(o, H, ldh, M, F, num_sms, stream);
     return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
@@ -1589,8 +1712,7 @@ gemm_status_t glu_plan_query(int64_t M, int64_t F, int64_t K, const void* X, int
     gemm_status_t st = check_glu(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt);
     if (st != GEMM_OK) return st;
     Plan pl;
-    st = make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, H, max1(2 * F),
-                   gemm_dtypes_t{dt.a, dt.b, GEMM_F32}, num_sms, smem_optin, pl);
+    st = glu_plan(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt, num_sms, smem_optin, pl);
     if (st != GEMM_OK) return st;
     *out = pl.pub;
     return GEMM_OK;
@@ -1606,21 +1728,16 @@ gemm_status_t glu_forward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, cons
     if (st != GEMM_OK) return st;
     if (M == 0 || F == 0) return GEMM_OK;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-    if (K == 0) return enqueue_glu_gate(nullptr, opt, H, ldh, M, F, dt.c, h->num_sms, stream);
-    const gemm_dtypes_t gdt{dt.a, dt.b, GEMM_F32};
+    if (K == 0) return enqueue_glu_gate(opt, H, ldh, M, F, dt.c, h->num_sms, stream);
     Plan pl;
-    st = make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, reinterpret_cast<void*>(256),
-                   2 * F, gdt, h->num_sms, h->smem_optin, pl);
+    st = glu_plan(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt, h->num_sms, h->smem_optin, pl);
     if (st != GEMM_OK) return st;
-    const int64_t at = round_up(pl.pub.workspace_bytes > 0 ? pl.pub.workspace_bytes : kWsHeaderBytes, 256);
-    st = ensure_workspace(h, static_cast<size_t>(at + M * 2 * F * 4), stream);
+    st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
-    uint8_t* ws = static_cast<uint8_t*>(h->ws);
-    st = enqueue_plan(pl, h->encode, h->num_sms, ws, h->err_dev, 1.0f, 0.0f, ws + at, gdt, stream,
-                      false, h->debug_flags, h->wait_limit_ns);
-    if (st != GEMM_OK) return st;
-    return enqueue_glu_gate(reinterpret_cast<float*>(ws + at), opt, H, ldh, M, F, dt.c, h->num_sms,
-                            stream);
+    const GluDesc glu{M, F, ldh, opt};
+    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, 1.0f, 0.0f,
+                        H, dt, stream, false, h->debug_flags, h->wait_limit_ns, nullptr, nullptr,
+                        nullptr, &glu);
 }
 
 gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, const void* dH,

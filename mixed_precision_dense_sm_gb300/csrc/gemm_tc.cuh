@@ -163,6 +163,24 @@ struct TcParams {
     float2* ln_stats;
 };
 
+// The gated linear layer (kernels instantiated with EPI == kEpiGlu): W holds
+// the gate's F rows and the up projection's F rows, and each tile takes as
+// many of both.  Not swapped, a tile's first BN / 2 columns are the gate's and
+// the others the up projection's (B is loaded from a map with the half as a
+// dimension; in a CTA pair each CTA loads one half), so a thread holds both
+// values of an output column; N = F and tile column tn starts at output column
+// tn * BN / 2.  Swapped, rows 0-63 are the gate's and 64-127 the up
+// projection's, M = F, and tile row tm starts at output column tm * 64; the
+// halves meet through shared memory.
+struct GluParams : TcParams {
+    alignas(64) CUtensorMap tmP;    // P (F, M, 2) for TMA stores
+    void* P;                        // pre-activations, or nullptr
+    int64_t ldp;
+    int32_t F;
+    int32_t swap;
+    int32_t p_vector;               // P's rows and halves are 16-byte aligned
+};
+
 enum : int { kL2EvictLast = 0, kL2EvictFirst = 1, kL2EvictNormal = 2 };
 
 __device__ __forceinline__ uint64_t l2_policy(int32_t which) {
@@ -508,6 +526,10 @@ __device__ __forceinline__ bool epilogue_all(bool ok) {
 
 constexpr int kEpiPlain = 0;
 constexpr int kEpiLayerNorm = 1;
+constexpr int kEpiGlu = 2;
+
+template <int EPI> struct ParamsOf { using type = TcParams; };
+template <> struct ParamsOf<kEpiGlu> { using type = GluParams; };
 
 // A value as the output type holds it (rounded to nearest even, read back).
 template <typename OutT>
@@ -675,6 +697,180 @@ __device__ __forceinline__ void ln_tile(const TcParams& p, uint32_t t_row, int32
     }
 }
 
+// ------------------------------------------------- the gated linear layer
+
+// 32 values of one row at columns c0.. (the columns < cols), cast to the
+// output type, from `base` on; vector stores when the chunk is whole and `vec`.
+template <typename OutT>
+__device__ __forceinline__ void glu_store32(OutT* base, bool vec, int32_t c0, int32_t cols,
+                                            const float (&v)[32]) {
+    if (vec && c0 + 32 <= cols) {
+        constexpr int kPer16 = 16 / sizeof(OutT);
+        #pragma unroll
+        for (int q = 0; q < 32 / kPer16; ++q) {
+            uint4 pack;
+            OutT* pk = reinterpret_cast<OutT*>(&pack);
+            #pragma unroll
+            for (int e = 0; e < kPer16; ++e) pk[e] = cvt_out<OutT>(v[q * kPer16 + e]);
+            *reinterpret_cast<uint4*>(base + c0 + q * kPer16) = pack;
+        }
+    } else {
+        #pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (c0 + j < cols) base[c0 + j] = cvt_out<OutT>(v[j]);
+    }
+}
+
+__device__ __forceinline__ const void* glu_up_bias(const GluParams& p) {
+    return static_cast<const uint8_t*>(p.bias) + static_cast<int64_t>(p.F) * (p.bias_dtype == 2 ? 4 : 2);
+}
+
+// The tile's accumulator (plus, for a stream-K finisher, the other
+// contributors' sums in the spare buffer), 32 columns of this warp's rows.
+__device__ __forceinline__ void glu_sums(uint32_t t_row, uint32_t t_spare, bool finisher, int chunk,
+                                         float (&v)[32]) {
+    tmem_row32(t_row + chunk * 32, v);
+    if (finisher) {
+        float o[32];
+        tmem_row32(t_spare + chunk * 32, o);
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = o[j] + v[j];
+    }
+}
+
+// Output tile of a problem that is not swapped: g and u of 32 output columns
+// at a time in each thread, H = act(g) u, rounded once.  With c_tma the two
+// warps of a lane quarter fill 64 columns (16-bit outputs) of a staging box
+// that one thread stores; P's two halves go the same way before H.
+template <typename OutT, int BN>
+__device__ __forceinline__ void glu_tile(const GluParams& p, const CUtensorMap* tmC, uint32_t t_row,
+                                         uint32_t t_spare, bool finisher, int32_t row, int row_in_cta,
+                                         int half, int32_t tn, uint8_t* cstage, uint32_t& cstep) {
+    constexpr int kChunks = BN / 64;              // 32-column chunks of the output tile
+    const int32_t col0 = tn * (BN / 2);
+    const bool first = threadIdx.x == 64;         // lane 0 of warp 2
+    // one 64-column step (32 columns per half) through the staging boxes
+    auto put = [&](const CUtensorMap* map, bool is_p, int32_t part, int step, const float (&v)[32]) {
+        uint8_t* box;
+        int u0;
+        if constexpr (sizeof(OutT) == 4) {
+            box = cstage + half * kCBoxBytes;
+            u0 = 0;
+        } else {
+            box = cstage + (cstep & 1u) * kCBoxBytes;
+            u0 = 4 * half;
+        }
+        if (first) {
+            if constexpr (sizeof(OutT) == 4) bulk_wait_group_read<0>();
+            else bulk_wait_group_read<1>();
+        }
+        epilogue_bar_sync();
+        stage_row32<OutT>(box, row_in_cta, u0, v);
+        fence_proxy_async_shared();
+        epilogue_bar_sync();
+        if (first) {
+            const int32_t y = row - row_in_cta;                   // the CTA's first row
+            const int32_t x = col0 + step * 64;
+            constexpr int kBoxes = sizeof(OutT) == 4 ? 2 : 1;
+            if (y < p.M) {
+                #pragma unroll
+                for (int b = 0; b < kBoxes; ++b) {
+                    const uint8_t* src = sizeof(OutT) == 4 ? cstage + b * kCBoxBytes : box;
+                    if (x + b * 32 < p.F) {
+                        if (is_p) tma_store_3d(map, src, x + b * 32, y, part);
+                        else tma_store_2d(map, src, x + b * 32, y);
+                    }
+                }
+            }
+            bulk_commit_group();
+        }
+        ++cstep;
+    };
+    #pragma unroll 1
+    for (int ch = half; ch < kChunks; ch += 2) {
+        const int32_t c0 = col0 + ch * 32;
+        float g[32], u[32];
+        glu_sums(t_row, t_spare, finisher, ch, g);
+        glu_sums(t_row, t_spare, finisher, ch + kChunks, u);
+        if (p.bias != nullptr && c0 < p.F) {
+            float b[32];
+            load_col_vec32(p.bias, p.bias_dtype, c0, p.F, b);
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] += b[j];
+            load_col_vec32(glu_up_bias(p), p.bias_dtype, c0, p.F, b);
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) u[j] += b[j];
+        }
+        if (p.c_tma) {
+            if (p.P != nullptr) {
+                put(&p.tmP, true, 0, ch >> 1, g);
+                put(&p.tmP, true, 1, ch >> 1, u);
+            }
+            act32(p.act, g);
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] *= u[j];
+            put(tmC, false, 0, ch >> 1, g);
+        } else if (row < p.M && c0 < p.F) {
+            if (p.P != nullptr) {
+                OutT* prow = static_cast<OutT*>(p.P) + static_cast<int64_t>(row) * p.ldp;
+                glu_store32<OutT>(prow, p.p_vector != 0, c0, p.F, g);
+                glu_store32<OutT>(prow + p.F, p.p_vector != 0, c0, p.F, u);
+            }
+            act32(p.act, g);
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] *= u[j];
+            glu_store32<OutT>(static_cast<OutT*>(p.C) + static_cast<int64_t>(row) * p.c_rs,
+                              p.c_vector != 0, c0, p.F, g);
+        }
+    }
+}
+
+constexpr int kGluXPitch = 33;     // floats per row of the exchange buffer: no bank conflicts
+
+// Output tile of a swapped problem: thread = one row of W, columns = tokens.
+// The up warps (TMEM lanes 64-127) leave their values in shared memory, the
+// gate warps (lanes 0-63) multiply and store.  H(token, n) = C[token * c_cs + n].
+template <typename OutT, int BN>
+__device__ __forceinline__ void glu_tile_swapped(const GluParams& p, uint32_t t_row, uint32_t t_spare,
+                                                 bool finisher, int row_in_cta, int half, int32_t tm,
+                                                 int32_t tn, float* xchg) {
+    const bool up = row_in_cta >= 64;
+    const int r = row_in_cta & 63;
+    const int32_t n = tm * 64 + r;
+    const bool in = n < p.F;
+    float* x = xchg + (half * 64 + r) * kGluXPitch;
+    float b = 0.0f;
+    if (p.bias != nullptr && in)
+        b = load_bias_elem(up ? glu_up_bias(p) : p.bias, p.bias_dtype, n);
+    #pragma unroll 1
+    for (int ch = half; ch < BN / 32; ch += 2) {
+        const int32_t c0 = tn * BN + ch * 32;
+        float v[32];
+        glu_sums(t_row, t_spare, finisher, ch, v);
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += b;
+        if (p.P != nullptr && in) {
+            OutT* dst = static_cast<OutT*>(p.P) + static_cast<int64_t>(c0) * p.ldp + (up ? p.F : 0) + n;
+            #pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c0 + j < p.N) dst[j * p.ldp] = cvt_out<OutT>(v[j]);
+        }
+        if (up) {
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = v[j];
+        }
+        epilogue_bar_sync();
+        if (!up && in) {
+            act32(p.act, v);
+            OutT* dst = static_cast<OutT*>(p.C) + static_cast<int64_t>(c0) * p.c_cs + n;
+            #pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c0 + j < p.N) dst[j * p.c_cs] = cvt_out<OutT>(v[j] * x[j]);
+        }
+        epilogue_bar_sync();                          // the buffer is written again
+    }
+}
+
 // MH = 2 (single CTA, plain epilogue, BN <= 128, data-parallel schedules):
 //   a 256 x BN tile in one CTA, as two M = 128 halves.  One A box of 256 rows
 //   per K chunk feeds both halves' MMAs, which share the chunk's B tile and
@@ -684,9 +880,10 @@ __device__ __forceinline__ void ln_tile(const TcParams& p, uint32_t t_row, int32
 template <int CG, int BN, typename OutT, int ES, int EPI = kEpiPlain, int KC = 1, int MH = 1>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmC, const __grid_constant__ TcParams p) {
+                   const __grid_constant__ CUtensorMap tmC,
+                   const __grid_constant__ typename ParamsOf<EPI>::type p) {
     static_assert(BN == 64 || BN == 128 || BN == 256, "BN");
-    static_assert(EPI == kEpiPlain || EPI == kEpiLayerNorm, "epilogue");
+    static_assert(EPI == kEpiPlain || EPI == kEpiLayerNorm || (EPI == kEpiGlu && ES == 2), "epilogue");
     static_assert(KC == 1 || KC == 2, "K chunks per stage");
     static_assert(CG == 1 || (CG == 2 && BN >= 128), "CG");
     static_assert(ES == 2 || ES == 4, "element size");
@@ -720,7 +917,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t a_region = halo ? p.halo_a_region : kATile;
     // [stages][C staging, when C is stored by TMA][barriers]
     uint8_t* cstage = smem + S * stage_bytes;
-    uint64_t* full = reinterpret_cast<uint64_t*>(cstage + (p.c_tma ? kCStageBytes : 0u));
+    bool staging = p.c_tma != 0;
+    if constexpr (EPI == kEpiGlu) staging = staging || p.swap;    // the exchange buffer
+    uint64_t* full = reinterpret_cast<uint64_t*>(cstage + (staging ? kCStageBytes : 0u));
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;
     uint64_t* acc_empty = acc_full + 2;
@@ -797,12 +996,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // matrix only feed outputs that are never stored: not loaded.
                 // tile_bytes(r) is what CTA r of the pair loads per k-block.
                 auto a_parts = [&](int32_t m_first) {
+                    if constexpr (EPI == kEpiGlu) {
+                        if (p.swap) return 1;
+                    }
                     if (!p.a_mn_major) return (m_first < p.M) ? 1 : 0;
                     int n = 0;
                     for (int c = 0; c < kARows / kMNChunk; ++c) n += (m_first + kMNChunk * c < p.M);
                     return n;
                 };
                 auto b_parts = [&](int32_t n_first) {
+                    if constexpr (EPI == kEpiGlu) return 1;
                     if (!p.b_mn_major) return (n_first < p.N) ? 1 : 0;
                     int n = 0;
                     for (int c = 0; c < static_cast<int>(kBRows) / kMNChunk; ++c)
@@ -867,7 +1070,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         continue;
                     }
-                    if (MH == 2 && halo) {
+                    if constexpr (EPI == kEpiGlu) {
+                        // W's box: the tile's gate rows and up rows (in a CTA
+                        // pair this CTA's half of them), kc chunks of K
+                        const int32_t c = kb * kc;
+                        if constexpr (CG == 1) {
+                            mbar_arrive_expect_tx(&full[stage], bytes);
+                            if (p.swap) {
+                                if constexpr (kc == 1) {
+                                    tma_load_3d(sa, &tmA, &full[stage], k0, tm * 64, 0, pol_a);
+                                    tma_load_2d(sb, &tmB, &full[stage], k0, n0, pol_b);
+                                } else {
+                                    tma_load_4d(sa, &tmA, &full[stage], 0, tm * 64, 0, c, pol_a);
+                                    tma_load_3d(sb, &tmB, &full[stage], 0, n0, c, pol_b);
+                                }
+                            } else {
+                                const int32_t w0 = tn * (BN / 2);
+                                if constexpr (kc == 1) {
+                                    if (na) tma_load_2d(sa, &tmA, &full[stage], k0, m0, pol_a);
+                                    tma_load_3d(sb, &tmB, &full[stage], k0, w0, 0, pol_b);
+                                } else {
+                                    if (na) tma_load_3d(sa, &tmA, &full[stage], 0, m0, c, pol_a);
+                                    tma_load_4d(sb, &tmB, &full[stage], 0, w0, 0, c, pol_b);
+                                }
+                            }
+                        } else {
+                            const uint32_t fb = map_to_rank(smem_addr(&full[stage]), 0);
+                            if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+                            const int32_t w0 = tn * (BN / 2);
+                            const int32_t part = static_cast<int32_t>(rank);
+                            if constexpr (kc == 1) {
+                                if (na) tma_load_2d_pair(sa, &tmA, fb, k0, m0, pol_a);
+                                tma_load_3d_pair(sb, &tmB, fb, k0, w0, part, pol_b);
+                            } else {
+                                if (na) tma_load_3d_pair(sa, &tmA, fb, 0, m0, c, pol_a);
+                                tma_load_4d_pair(sb, &tmB, fb, 0, w0, part, c, pol_b);
+                            }
+                        }
+                    } else if (MH == 2 && halo) {
                         // filter column s, channel block cb: the halo box, then
                         // the column's R taps (3-D filter map, one box per tap)
                         if constexpr (CG == 1 && MH == 2) {
@@ -1211,8 +1451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             ok = ok && wait_or_abort(&acc_full[buf], (acc_i >> 1) & 1u, &abort_flag, p.wait_limit_ns);
-            // stream-K, LayerNorm and the TMA store of C use named barriers below
-            if (p.stream_k || EPI == kEpiLayerNorm || p.c_tma) ok = epilogue_all(ok);
+            // stream-K, the LayerNorm and gated epilogues and the TMA store of C
+            // use named barriers below
+            if (p.stream_k || EPI != kEpiPlain || p.c_tma) ok = epilogue_all(ok);
             if (!ok) {
                 record_error(p, kErrTimeoutEpilogue, &abort_flag);
                 break;
@@ -1221,6 +1462,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (EPI == kEpiLayerNorm) {
                 // data-parallel only (the planner gives LayerNorm no stream-K)
                 ln_tile<OutT, BN>(p, t_row, row, row_in_cta, half, col0, tn, ln_red);
+            } else if (EPI == kEpiGlu && (sg.slot < 0 || finisher)) {
+                if constexpr (EPI == kEpiGlu) {
+                    if (CG == 1 && BN <= 128 && p.swap)
+                        glu_tile_swapped<OutT, BN>(p, t_row, t_spare, finisher, row_in_cta, half, tm, tn,
+                                                   reinterpret_cast<float*>(cstage));
+                    else
+                        glu_tile<OutT, BN>(p, &tmC, t_row, t_spare, finisher, row, row_in_cta, half, tn,
+                                           cstage, cstep);
+                }
             } else {
                 float* my_slot = (MH == 1 && sg.slot >= 0 && !finisher)
                                      ? p.partials + static_cast<int64_t>(sg.slot) * BM * BN

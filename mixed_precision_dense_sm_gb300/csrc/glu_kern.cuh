@@ -55,22 +55,17 @@ template <> __device__ __forceinline__ __nv_bfloat16 glu_from_f<__nv_bfloat16>(f
     return __float2bfloat16_rn(v);
 }
 
-// H = act(G) * U and P = [G U] from S (M x 2F, FP32, row pitch 2F; NULL: 0)
-// and the bias.
+// K == 0: P = [G U] is the bias (0 where there is none), H = act(G) * U.
 template <typename OutT>
 __global__ void __launch_bounds__(256)
-    glu_gate_kernel(const float* __restrict__ S, const void* bias, int32_t bias_dtype, int32_t act,
-                    OutT* __restrict__ H, int64_t ldh, OutT* P, int64_t ldp, int64_t M, int64_t F) {
+    glu_gate_kernel(const void* bias, int32_t bias_dtype, int32_t act, OutT* __restrict__ H,
+                    int64_t ldh, OutT* P, int64_t ldp, int64_t M, int64_t F) {
     const int64_t total = M * F;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t r = i / F, c = i - r * F;
-        float g = S ? S[r * 2 * F + c] : 0.0f;
-        float u = S ? S[r * 2 * F + F + c] : 0.0f;
-        if (bias != nullptr) {
-            g += load_bias_elem(bias, bias_dtype, c);
-            u += load_bias_elem(bias, bias_dtype, F + c);
-        }
+        const float g = bias ? load_bias_elem(bias, bias_dtype, c) : 0.0f;
+        const float u = bias ? load_bias_elem(bias, bias_dtype, F + c) : 0.0f;
         if (P != nullptr) {
             P[r * ldp + c] = glu_from_f<OutT>(g);
             P[r * ldp + F + c] = glu_from_f<OutT>(u);

@@ -6,7 +6,8 @@
 // 256-row single-CTA tiles of width 64/128 (MH = 2, used by convolutions).  Each with
 // one K chunk per stage, and those whose three stages of two chunks fit in
 // shared memory also with two; the plain single-CTA 256-wide tile also with
-// two (two stages, used by convolutions).
+// two (two stages, used by convolutions).  With KERN_GLU defined, the gated
+// linear layer's kernels instead.
 #pragma once
 #include <mutex>
 
@@ -17,9 +18,16 @@
 
 namespace gemm103 {
 
+template <int EPI>
+static const typename ParamsOf<EPI>::type& params_of(const TcLaunch& l) {
+    if constexpr (EPI == kEpiGlu) return l.glu;
+    else return l.p;
+}
+
 template <int CG, int BN, int EPI = kEpiPlain, int KC = 1, int MH = 1>
 static cudaError_t launch_tc_cfg(const TcLaunch& l) {
     auto kern = gemm_tc_kernel<CG, BN, KERN_OUT_T, KERN_ES, EPI, KC, MH>;
+    const auto& params = params_of<EPI>(l);
     {
         // The dynamic shared-memory limit is raised once per size (a host
         // call worth avoiding on every launch of a microsecond-scale GEMM).
@@ -47,7 +55,7 @@ static cudaError_t launch_tc_cfg(const TcLaunch& l) {
     cfg.numAttrs = 1;
     if constexpr (CG == 1) {
         cfg.gridDim = dim3(l.grid, 1, 1);
-        return cudaLaunchKernelEx(&cfg, kern, l.tmA, l.tmB, l.tmC, l.p);
+        return cudaLaunchKernelEx(&cfg, kern, l.tmA, l.tmB, l.tmC, params);
     } else {
         attr[1].id = cudaLaunchAttributeClusterDimension;
         attr[1].val.clusterDim.x = 2;
@@ -82,9 +90,36 @@ static cudaError_t launch_tc_cfg(const TcLaunch& l) {
             if (clusters > 0 && grid > 2 * clusters) grid = 2 * clusters;
         }
         cfg.gridDim = dim3(grid, 1, 1);
-        return cudaLaunchKernelEx(&cfg, kern, l.tmA, l.tmB, l.tmC, l.p);
+        return cudaLaunchKernelEx(&cfg, kern, l.tmA, l.tmB, l.tmC, params);
     }
 }
+
+#ifdef KERN_GLU
+
+// Single-CTA tiles of width 64 / 128 / 256 and CTA-pair tiles of width 256;
+// the single-CTA 256-wide tile with one K chunk per stage.
+template <int KC>
+static cudaError_t launch_glu_kc(const TcLaunch& l) {
+    if (l.cta_group == 2)
+        return l.block_n == 256 ? launch_tc_cfg<2, 256, kEpiGlu, KC>(l) : cudaErrorInvalidValue;
+    switch (l.block_n) {
+        case 64: return launch_tc_cfg<1, 64, kEpiGlu, KC>(l);
+        case 128: return launch_tc_cfg<1, 128, kEpiGlu, KC>(l);
+        case 256:
+            if constexpr (KC == 1) return launch_tc_cfg<1, 256, kEpiGlu, 1>(l);
+            return cudaErrorInvalidValue;
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+cudaError_t GEMM103_CAT(launch_glu_, KERN_SUFFIX)(const TcLaunch& l) {
+    if (l.esize != KERN_ES || l.epi != kEpiGlu || l.mh != 1) return cudaErrorInvalidValue;
+    if (l.kc == 1) return launch_glu_kc<1>(l);
+    if (l.kc == 2) return launch_glu_kc<2>(l);
+    return cudaErrorInvalidValue;
+}
+
+#else
 
 template <int KC>
 static cudaError_t launch_tc_kc(const TcLaunch& l) {
@@ -136,5 +171,7 @@ cudaError_t GEMM103_CAT(launch_tc_, KERN_SUFFIX)(const TcLaunch& l) {
     if (l.kc == 2) return launch_tc_kc<2>(l);
     return cudaErrorInvalidValue;
 }
+
+#endif  // KERN_GLU
 
 }  // namespace gemm103

@@ -17,7 +17,8 @@ struct TcLaunch {
     int cta_group;      // 1: single-CTA tiles, 2: CTA-pair tiles
     int block_n;
     int esize;          // input element bytes: 2 (FP16/BF16) or 4 (FP32 used as TF32)
-    int epi;            // kEpiPlain or kEpiLayerNorm (16-bit inputs only)
+    int epi;            // kEpiPlain, or with 16-bit inputs kEpiLayerNorm or kEpiGlu
+    GluParams glu;      // kEpiGlu: its own fields (the TcParams part is taken from p)
     int kc;             // K chunks per stage: 1, or 2 (tiles whose 3 stages fit)
     int mh;             // M halves per single-CTA tile: 1 (128 rows) or 2 (256 rows, BN <= 128)
     size_t smem_bytes;
@@ -32,5 +33,9 @@ cudaError_t launch_tc_bf16(const TcLaunch& l);
 cudaError_t launch_tc_tf32_f32(const TcLaunch& l);
 cudaError_t launch_tc_tf32_f16(const TcLaunch& l);
 cudaError_t launch_tc_tf32_bf16(const TcLaunch& l);
+// The gated linear layer, per output type.
+cudaError_t launch_glu_f32(const TcLaunch& l);
+cudaError_t launch_glu_f16(const TcLaunch& l);
+cudaError_t launch_glu_bf16(const TcLaunch& l);
 
 }  // namespace gemm103
