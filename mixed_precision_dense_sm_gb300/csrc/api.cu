@@ -367,9 +367,13 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     // Stream-K spreads the K loop of too few tiles (or of a badly filled last
     // wave, above) over all SMs.  It pays for itself only when the tiles are
     // long in K; the swapped skinny path (a weight-streaming GEMM) always uses it.
+    // The gated layer's skinny tiles (64 output columns each) outnumber the SMs
+    // sooner: a badly filled last wave is balanced there too (64 tokens,
+    // 4096 -> 14336: 224 tiles, 1.5 waves).
+    const bool exchange_sk = exchange && k_chunks >= 4 && wave_fill(tiles, num_sms) < kMinWaveFill;
     const bool stream_k = allow_sk && !use_mh2 && work < INT32_MAX &&
                           (pair_sk || (!pairs && !ln && (tiles <= kMaxCounterTiles) &&
-                                       (balance_sk || ((tiles < num_sms) &&
+                                       (balance_sk || exchange_sk || ((tiles < num_sms) &&
                                         (swap ? k_chunks >= 4 : (tiles < half_wave && long_k))))));
     if (stream_k) {
         int64_t units = num_sms / cg;                  // CTAs or CTA pairs

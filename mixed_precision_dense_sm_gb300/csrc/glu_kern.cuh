@@ -11,34 +11,42 @@
 
 namespace gemm103 {
 
-// act(x) and act'(x):
+// act(x) and act'(x) of 8 values, the choice made outside the element loops:
 //   SiLU  s = 1 / (1 + e^-x):  x s,  s (1 + x (1 - s))
 //   GELU  Phi = erfc(-x / sqrt 2) / 2:  x Phi,  Phi + x e^(-x^2 / 2) / sqrt(2 pi)
 //   ReLU  max(x, 0),  1 for x > 0 else 0
-__device__ __forceinline__ void act_and_slope(int act, float x, float& a, float& d) {
-    switch (act) {
-        case kActRelu:
-            a = relu(x);
-            d = x > 0.0f ? 1.0f : 0.0f;
-            break;
-        case kActGelu: {
-            const float e = 0.5f * erfc_nr(fabsf(x) * 0.70710678118654752f);
-            const float phi = x >= 0.0f ? 1.0f - e : e;
-            a = x * phi;
+__device__ __forceinline__ void act_and_slope8(int act, const float (&x)[8], float (&a)[8],
+                                               float (&d)[8]) {
+    if (act == kActSilu) {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = __fdividef(1.0f, 1.0f + __expf(-x[e]));
+            a[e] = x[e] * s;
+            d[e] = s * fmaf(x[e], 1.0f - s, 1.0f);
+        }
+    } else if (act == kActGelu) {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float h = 0.5f * erfc_nr(fabsf(x[e]) * 0.70710678118654752f);
+            const float phi = x[e] >= 0.0f ? 1.0f - h : h;
+            a[e] = x[e] * phi;
             // e^(-x^2/2) is 0 in FP32 beyond |x| = 15, where x times it would be inf * 0 for x = inf
-            const float g = fabsf(x) < 15.0f ? x * __expf(-0.5f * x * x) * 0.39894228040143268f : 0.0f;
-            d = phi + g;
-            break;
+            const float g = fabsf(x[e]) < 15.0f
+                                ? x[e] * __expf(-0.5f * x[e] * x[e]) * 0.39894228040143268f : 0.0f;
+            d[e] = phi + g;
         }
-        case kActSilu: {
-            const float s = __fdividef(1.0f, 1.0f + __expf(-x));
-            a = x * s;
-            d = s * fmaf(x, 1.0f - s, 1.0f);
-            break;
+    } else if (act == kActRelu) {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] = relu(x[e]);
+            d[e] = x[e] > 0.0f ? 1.0f : 0.0f;
         }
-        default:
-            a = x;
-            d = 1.0f;
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            a[e] = x[e];
+            d[e] = 1.0f;
+        }
     }
 }
 
@@ -161,12 +169,12 @@ __global__ void __launch_bounds__(32 * kGluBackWarps)
         glu_load8<T>(static_cast<const T*>(p.dH) + r * p.lddh, vec, base, p.F, h);
         glu_load8<PT>(prow, vec, base, p.F, g);
         glu_load8<PT>(prow + p.F, vec, base, p.F, u);
+        float a[8], d[8];
+        act_and_slope8(p.act, g, a, d);
         #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            float a, d;
-            act_and_slope(p.act, g[e], a, d);
-            g[e] = h[e] * u[e] * d;
-            u[e] = h[e] * a;
+            g[e] = h[e] * u[e] * d[e];
+            u[e] = h[e] * a[e];
             if constexpr (SUMS) {
                 sg[e] += g[e];
                 su[e] += u[e];

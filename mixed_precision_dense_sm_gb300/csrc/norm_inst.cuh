@@ -40,35 +40,40 @@ static cudaError_t launch_kernel(K kern, const Launch& l, std::mutex& mu, size_t
     return cudaLaunchKernelEx(&cfg, kern, l.p);
 }
 
-template <int C>
+template <int C, bool VEC>
 static cudaError_t forward_c(const Launch& l) {
     static std::mutex mu;
     static size_t raised_to = 0;
-    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, C>, l, mu, raised_to);
+    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, C, VEC>, l, mu, raised_to);
 }
 
-template <int C, bool BIAS, int THREADS>
+template <int C, bool VEC, bool BIAS, int THREADS>
 static cudaError_t backward_c(const Launch& l) {
     static std::mutex mu;
     static size_t raised_to = 0;
-    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, C, BIAS, THREADS>, l, mu, raised_to);
+    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, C, VEC, BIAS, THREADS>, l, mu, raised_to);
 }
 
 cudaError_t NORM_CAT(forward_, NORM_SUFFIX)(const Launch& l) {
-    return l.chunks8 == 1 ? forward_c<1>(l) : forward_c<2>(l);
+    if (l.p.vec) return l.chunks8 == 1 ? forward_c<1, true>(l) : forward_c<2, true>(l);
+    return l.chunks8 == 1 ? forward_c<1, false>(l) : forward_c<2, false>(l);
 }
 
-template <bool BIAS>
+template <bool VEC, bool BIAS>
 static cudaError_t backward_b(const Launch& l) {
     switch (l.threads) {
-        case 256: return l.chunks8 == 1 ? backward_c<1, BIAS, 256>(l) : backward_c<2, BIAS, 256>(l);
-        case 512: return backward_c<2, BIAS, 512>(l);
+        case 256:
+            return l.chunks8 == 1 ? backward_c<1, VEC, BIAS, 256>(l) : backward_c<2, VEC, BIAS, 256>(l);
+        case 512: return backward_c<2, VEC, BIAS, 512>(l);
         default: return cudaErrorInvalidValue;
     }
 }
 
+// Rows that are not vectors take the kernel with all four sums (fewer kernels;
+// the two that are not wanted are not added up).
 cudaError_t NORM_CAT(backward_, NORM_SUFFIX)(const Launch& l) {
-    return l.bias ? backward_b<true>(l) : backward_b<false>(l);
+    if (!l.p.vec) return backward_b<false, true>(l);
+    return l.bias ? backward_b<true, true>(l) : backward_b<true, false>(l);
 }
 
 }  // namespace nrm

@@ -25,7 +25,7 @@ namespace gemm103 {
 namespace nrm {
 
 enum : int { kNone = 0, kRms = 1, kLayer = 2 };
-constexpr int kMaxStages = 4;
+constexpr int kMaxStages = 2;
 
 struct Params {
     // forward: X, Z in, XO, Y out; backward: X = XO, Z, dY, dXO in, dX, dZ out
@@ -78,20 +78,25 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float
 }
 
 // Where a thread's 8 elements of chunk c lie in the row: element e at
-// base + e * step.
+// base + e with VEC (all 8 of them inside the row or none), else at
+// base + 32 e.
+template <bool VEC>
 struct Spot {
-    int32_t base, step;
+    int32_t base;
+    __device__ __forceinline__ int32_t at(int e) const { return VEC ? base + e : base + 32 * e; }
+    __device__ __forceinline__ bool in(int e, int32_t N) const { return VEC ? base < N : at(e) < N; }
 };
 
-__device__ __forceinline__ Spot spot_of(bool vec, int T, int t, int c, int32_t first = 0) {
-    if (vec) return {first + (c * T + t) * 8, 1};
-    return {first + (c * T + (t & ~31)) * 8 + (t & 31), 32};
+template <bool VEC>
+__device__ __forceinline__ Spot<VEC> spot_of(int T, int t, int c, int32_t first = 0) {
+    return {first + (VEC ? (c * T + t) * 8 : (c * T + (t & ~31)) * 8 + (t & 31))};
 }
 
 // 8 elements of a vector parameter (weight, bias, gate row) of type dtype.
-__device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool wide, Spot s,
+template <bool VEC>
+__device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool wide, Spot<VEC> s,
                                             int32_t N, float (&o)[8]) {
-    if (wide && s.step == 1) {
+    if (VEC && wide) {
         if (s.base >= N) {
             #pragma unroll
             for (int e = 0; e < 8; ++e) o[e] = 0.0f;
@@ -121,9 +126,9 @@ __device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool w
     }
     #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        const int32_t i = s.base + e * s.step;
+        const int32_t i = s.at(e);
         o[e] = 0.0f;
-        if (i < N) {
+        if (s.in(e, N)) {
             if (dtype == 2) o[e] = __ldg(static_cast<const float*>(v) + i);
             else if (dtype == 1) o[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(v)[i]);
             else o[e] = __half2float(static_cast<const __half*>(v)[i]);
@@ -167,33 +172,56 @@ __device__ __forceinline__ uint8_t* slot_at(uint8_t* slot, int T, int t, int c) 
 }
 
 // Starts the copy of 8 elements of a row into this thread's part of a slot.
-template <typename E>
-__device__ __forceinline__ void fetch8(uint8_t* slot, int T, int t, int c, const E* row, Spot s,
+// Single 16-bit elements cannot be copied asynchronously: those are loaded by
+// hold8 into registers while the previous row is worked on, and put8 writes
+// them to the slot.
+template <typename E, bool VEC>
+__device__ __forceinline__ void fetch8(uint8_t* slot, int T, int t, int c, const E* row, Spot<VEC> s,
                                        int32_t N) {
     constexpr int kPieces = sizeof(E) / 2;
     uint8_t* d = slot_at<E>(slot, T, t, c);
-    if (s.step == 1) {
+    if constexpr (VEC) {
         if (s.base < N) {
             #pragma unroll
             for (int q = 0; q < kPieces; ++q)
                 cp_async16(d + q * T * 16, row + s.base + q * (8 / kPieces));
         }
-    } else {
+    } else if constexpr (sizeof(E) == 4) {
         #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int32_t i = s.base + e * 32;
-            E* p = reinterpret_cast<E*>(d + (e / (8 / kPieces)) * T * 16) + e % (8 / kPieces);
-            if (i < N) {
-                if constexpr (sizeof(E) == 4) cp_async4(p, row + i);
-                else *p = row[i];                     // no 2-byte cp.async
-            }
+        for (int e = 0; e < 8; ++e)
+            if (s.in(e, N)) cp_async4(d + (e / 4) * T * 16 + (e % 4) * 4, row + s.at(e));
+    }
+}
+
+// 16-bit elements held in registers on the way to a slot (VEC false only).
+template <typename E, bool VEC>
+struct Held {
+    static constexpr bool kUsed = !VEC && sizeof(E) == 2;
+    uint32_t w[kUsed ? 4 : 1];
+};
+
+template <typename E, bool VEC>
+__device__ __forceinline__ void hold8(Held<E, VEC>& h, const E* row, Spot<VEC> s, int32_t N) {
+    if constexpr (Held<E, VEC>::kUsed) {
+        const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
+        #pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint32_t lo = s.in(2 * q, N) ? r[s.at(2 * q)] : 0u;
+            const uint32_t hi = s.in(2 * q + 1, N) ? r[s.at(2 * q + 1)] : 0u;
+            h.w[q] = lo | hi << 16;
         }
     }
 }
 
+template <typename E, bool VEC>
+__device__ __forceinline__ void put8(uint8_t* slot, int T, int t, int c, const Held<E, VEC>& h) {
+    if constexpr (Held<E, VEC>::kUsed)
+        *reinterpret_cast<uint4*>(slot_at<E>(slot, T, t, c)) = make_uint4(h.w[0], h.w[1], h.w[2], h.w[3]);
+}
+
 // The 8 elements of this thread's part of a slot as FP32, 0 past column N.
-template <typename E>
-__device__ __forceinline__ void take8(uint8_t* slot, int T, int t, int c, Spot s, int32_t N,
+template <typename E, bool VEC>
+__device__ __forceinline__ void take8(uint8_t* slot, int T, int t, int c, Spot<VEC> s, int32_t N,
                                       float (&o)[8]) {
     constexpr int kPieces = sizeof(E) / 2;
     constexpr int kPer = 8 / kPieces;
@@ -208,16 +236,16 @@ __device__ __forceinline__ void take8(uint8_t* slot, int T, int t, int c, Spot s
         #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             const int k = q * kPer + e;
-            o[k] = s.base + k * s.step < N ? to_f<E>(w.e[e]) : 0.0f;
+            o[k] = s.in(k, N) ? to_f<E>(w.e[e]) : 0.0f;
         }
     }
 }
 
-template <typename E>
-__device__ __forceinline__ void store8(E* row, Spot s, int32_t N, const float (&v)[8]) {
+template <typename E, bool VEC>
+__device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, const float (&v)[8]) {
     constexpr int kPieces = sizeof(E) / 2;
     constexpr int kPer = 8 / kPieces;
-    if (s.step == 1) {
+    if constexpr (VEC) {
         if (s.base >= N) return;
         #pragma unroll
         for (int q = 0; q < kPieces; ++q) {
@@ -232,7 +260,7 @@ __device__ __forceinline__ void store8(E* row, Spot s, int32_t N, const float (&
     } else {
         #pragma unroll
         for (int e = 0; e < 8; ++e)
-            if (s.base + e * 32 < N) row[s.base + e * 32] = from_f<E>(v[e]);
+            if (s.in(e, N)) row[s.at(e)] = from_f<E>(v[e]);
     }
 }
 
@@ -314,7 +342,7 @@ __device__ __forceinline__ Group make_group(const Params& p, uint8_t* smem) {
 // ------------------------------------------------------------------- forward
 
 // Rows go to groups round robin over the grid.
-template <typename XT, typename ZT, int C>
+template <typename XT, typename ZT, int C, bool VEC>
 __global__ void __launch_bounds__(1024)
     forward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -324,7 +352,7 @@ __global__ void __launch_bounds__(1024)
                     static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
     const uint32_t x_bytes = static_cast<uint32_t>(C) * 8u * sizeof(XT) * p.T;
     const bool has_z = p.Z != nullptr;
-    const bool vec = p.vec != 0, wide = p.vec_aligned != 0;
+    const bool wide = p.vec_aligned != 0;
     const int32_t N = p.N;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + g.index;
@@ -336,18 +364,39 @@ __global__ void __launch_bounds__(1024)
             uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot sp = spot_of(vec, g.T, g.t, c);
-                fetch8<XT>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
+                fetch8<XT, VEC>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
                 if (has_z)
-                    fetch8<ZT>(s + x_bytes, g.T, g.t, c,
+                    fetch8<ZT, VEC>(s + x_bytes, g.T, g.t, c,
                                static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
             }
         }
         cp_async_commit();
     };
+    Held<XT, VEC> hx[C];
+    Held<ZT, VEC> hz[C];
+    auto hold = [&](int64_t row) {
+        if (row >= p.M) return;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
+            hold8<XT, VEC>(hx[c], static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+            if (has_z) hold8<ZT, VEC>(hz[c], static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+        }
+    };
     for (int s = 0; s < p.stages - 1; ++s) fetch(first + s * step, s);
+    if constexpr (!VEC) hold(first);
     int slot = 0;
     for (int64_t row = first; row < p.M; row += step) {
+        if constexpr (!VEC) {
+            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                put8<XT, VEC>(s, g.T, g.t, c, hx[c]);
+                if (has_z) put8<ZT, VEC>(s + x_bytes, g.T, g.t, c, hz[c]);
+            }
+            hold(row + step);
+        }
         {
             int ahead = slot + p.stages - 1;
             if (ahead >= p.stages) ahead -= p.stages;
@@ -360,13 +409,13 @@ __global__ void __launch_bounds__(1024)
         float x[C][8];
         #pragma unroll
         for (int c = 0; c < C; ++c)
-            take8<XT>(s, g.T, g.t, c, spot_of(vec, g.T, g.t, c), N, x[c]);
+            take8<XT, VEC>(s, g.T, g.t, c, spot_of<VEC>(g.T, g.t, c), N, x[c]);
         if (has_z) {
             float z[C][8];
             float mean = 0.0f, r = 1.0f;
             #pragma unroll
             for (int c = 0; c < C; ++c)
-                take8<ZT>(s + x_bytes, g.T, g.t, c, spot_of(vec, g.T, g.t, c), N, z[c]);
+                take8<ZT, VEC>(s + x_bytes, g.T, g.t, c, spot_of<VEC>(g.T, g.t, c), N, z[c]);
             if (p.post == kLayer) {
                 float v[1] = {0.0f};
                 #pragma unroll
@@ -380,10 +429,10 @@ __global__ void __launch_bounds__(1024)
                 float v[1] = {0.0f};
                 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const Spot sp = spot_of(vec, g.T, g.t, c);
+                    const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float d = sp.base + e * sp.step < N ? z[c][e] - mean : 0.0f;
+                        const float d = sp.in(e, N) ? z[c][e] - mean : 0.0f;
                         v[0] = fmaf(d, d, v[0]);
                     }
                 }
@@ -393,7 +442,7 @@ __global__ void __launch_bounds__(1024)
             const int64_t grow = p.gate_rows > 1 ? row / p.gate_rows : row;
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot sp = spot_of(vec, g.T, g.t, c);
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
                 float w[8];
                 #pragma unroll
                 for (int e = 0; e < 8; ++e) z[c][e] = (z[c][e] - mean) * r;
@@ -418,9 +467,9 @@ __global__ void __launch_bounds__(1024)
                     // the stream as its type holds it: what is stored is what
                     // the next norm sees
                     x[c][e] = to_f<XT>(from_f<XT>(fmaf(p.scale, z[c][e], x[c][e])));
-                    if (sp.base + e * sp.step >= N) x[c][e] = 0.0f;
+                    if (!sp.in(e, N)) x[c][e] = 0.0f;
                 }
-                store8<XT>(static_cast<XT*>(p.XO) + row * p.ldxo, sp, N, x[c]);
+                store8<XT, VEC>(static_cast<XT*>(p.XO) + row * p.ldxo, sp, N, x[c]);
             }
         }
         if (p.Y != nullptr) {
@@ -438,10 +487,10 @@ __global__ void __launch_bounds__(1024)
                 float v[1] = {0.0f};
                 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const Spot sp = spot_of(vec, g.T, g.t, c);
+                    const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float d = sp.base + e * sp.step < N ? x[c][e] - mean : 0.0f;
+                        const float d = sp.in(e, N) ? x[c][e] - mean : 0.0f;
                         v[0] = fmaf(d, d, v[0]);
                     }
                 }
@@ -450,7 +499,7 @@ __global__ void __launch_bounds__(1024)
             }
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot sp = spot_of(vec, g.T, g.t, c);
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
                 float w[8];
                 #pragma unroll
                 for (int e = 0; e < 8; ++e) x[c][e] = (x[c][e] - mean) * r;
@@ -464,7 +513,7 @@ __global__ void __launch_bounds__(1024)
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) x[c][e] += w[e];
                 }
-                store8<ZT>(static_cast<ZT*>(p.Y) + row * p.ldy, sp, N, x[c]);
+                store8<ZT, VEC>(static_cast<ZT*>(p.Y) + row * p.ldy, sp, N, x[c]);
             }
         }
     }
@@ -492,7 +541,7 @@ __device__ __forceinline__ void chunk_span(const Params& p, int64_t b, int64_t& 
 // is constant over a chunk and joins in the sum over chunks) or, for token
 // gates, q = scale gate dXO'.  The groups' sums meet in shared memory (in
 // group order) and go to the chunk's line of partials.
-template <typename XT, typename ZT, int C, bool BIAS, int THREADS>
+template <typename XT, typename ZT, int C, bool VEC, bool BIAS, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     backward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -505,7 +554,7 @@ __global__ void __launch_bounds__(THREADS)
     const uint32_t zb = static_cast<uint32_t>(C) * 8u * sizeof(ZT) * p.T;
     const bool has_z = p.Z != nullptr, has_dy = p.dY != nullptr, has_dxo = p.dXO != nullptr;
     const uint32_t o_dxo = xb, o_z = o_dxo + (has_dxo ? xb : 0u), o_dy = o_z + (has_z ? zb : 0u);
-    const bool vec = p.vec != 0, wide = p.vec_aligned != 0;
+    const bool wide = p.vec_aligned != 0;
     const int32_t N = p.N;
     __shared__ float pair[16];
     int32_t col0 = 0;
@@ -527,16 +576,16 @@ __global__ void __launch_bounds__(THREADS)
             uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
-                fetch8<XT>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+                fetch8<XT, VEC>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
                 if (has_dxo)
-                    fetch8<XT>(s + o_dxo, g.T, g.t, c,
+                    fetch8<XT, VEC>(s + o_dxo, g.T, g.t, c,
                                static_cast<const XT*>(p.dXO) + row * p.lddxo, sp, N);
                 if (has_z)
-                    fetch8<ZT>(s + o_z, g.T, g.t, c,
+                    fetch8<ZT, VEC>(s + o_z, g.T, g.t, c,
                                static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
                 if (has_dy)
-                    fetch8<ZT>(s + o_dy, g.T, g.t, c,
+                    fetch8<ZT, VEC>(s + o_dy, g.T, g.t, c,
                                static_cast<const ZT*>(p.dY) + row * p.lddy, sp, N);
             }
         }
@@ -553,9 +602,34 @@ __global__ void __launch_bounds__(THREADS)
         }
     }
 
+    Held<XT, VEC> hx[C], hd[C];
+    Held<ZT, VEC> hz[C], hy[C];
+    auto hold = [&](int64_t row) {
+        if (row >= row1) return;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+            hold8<XT, VEC>(hx[c], static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+            if (has_dxo) hold8<XT, VEC>(hd[c], static_cast<const XT*>(p.dXO) + row * p.lddxo, sp, N);
+            if (has_z) hold8<ZT, VEC>(hz[c], static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+            if (has_dy) hold8<ZT, VEC>(hy[c], static_cast<const ZT*>(p.dY) + row * p.lddy, sp, N);
+        }
+    };
     for (int s = 0; s < p.stages - 1; ++s) fetch(row0 + g.index + static_cast<int64_t>(s) * groups, s);
+    if constexpr (!VEC) hold(row0 + g.index);
     int slot = 0;
     for (int64_t row = row0 + g.index; row < row1; row += groups) {
+        if constexpr (!VEC) {
+            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                put8<XT, VEC>(s, g.T, g.t, c, hx[c]);
+                if (has_dxo) put8<XT, VEC>(s + o_dxo, g.T, g.t, c, hd[c]);
+                if (has_z) put8<ZT, VEC>(s + o_z, g.T, g.t, c, hz[c]);
+                if (has_dy) put8<ZT, VEC>(s + o_dy, g.T, g.t, c, hy[c]);
+            }
+            hold(row + groups);
+        }
         {
             int ahead = slot + p.stages - 1;
             if (ahead >= p.stages) ahead -= p.stages;
@@ -571,14 +645,14 @@ __global__ void __launch_bounds__(THREADS)
             float v[3] = {0.0f, 0.0f, 0.0f};
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
                 float b[8], w[8];
                 if (p.pre == kLayer) {
-                    take8<XT>(s, g.T, g.t, c, sp, N, b);
+                    take8<XT, VEC>(s, g.T, g.t, c, sp, N, b);
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) v[0] += b[e];
                     if (has_dy) {
-                        take8<ZT>(s + o_dy, g.T, g.t, c, sp, N, b);
+                        take8<ZT, VEC>(s + o_dy, g.T, g.t, c, sp, N, b);
                         if (p.wpre != nullptr) {
                             load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
                             #pragma unroll
@@ -590,7 +664,7 @@ __global__ void __launch_bounds__(THREADS)
                     }
                 }
                 if (has_z && p.post == kLayer) {
-                    take8<ZT>(s + o_z, g.T, g.t, c, sp, N, b);
+                    take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, b);
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) v[2] += b[e];
                 }
@@ -605,16 +679,16 @@ __global__ void __launch_bounds__(THREADS)
             float v[3] = {0.0f, 0.0f, 0.0f};
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
                 float b[8], w[8], x[8];
                 if (has_dy && p.pre != kNone) {
-                    take8<XT>(s, g.T, g.t, c, sp, N, x);
+                    take8<XT, VEC>(s, g.T, g.t, c, sp, N, x);
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        x[e] = sp.base + e * sp.step < N ? x[e] - mx : 0.0f;
+                        x[e] = sp.in(e, N) ? x[e] - mx : 0.0f;
                         v[0] = fmaf(x[e], x[e], v[0]);
                     }
-                    take8<ZT>(s + o_dy, g.T, g.t, c, sp, N, b);
+                    take8<ZT, VEC>(s + o_dy, g.T, g.t, c, sp, N, b);
                     if (p.wpre != nullptr) {
                         load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
                         #pragma unroll
@@ -624,10 +698,10 @@ __global__ void __launch_bounds__(THREADS)
                     for (int e = 0; e < 8; ++e) v[1] = fmaf(b[e], x[e], v[1]);
                 }
                 if (has_z && p.post != kNone) {
-                    take8<ZT>(s + o_z, g.T, g.t, c, sp, N, b);
+                    take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, b);
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float d = sp.base + e * sp.step < N ? b[e] - mz : 0.0f;
+                        const float d = sp.in(e, N) ? b[e] - mz : 0.0f;
                         v[2] = fmaf(d, d, v[2]);
                     }
                 }
@@ -644,21 +718,21 @@ __global__ void __launch_bounds__(THREADS)
         const int64_t grow = p.token_gate ? row : group;
         #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
             float b[8], w[8];
             if (has_dxo) {
-                take8<XT>(s + o_dxo, g.T, g.t, c, sp, N, d[c]);
+                take8<XT, VEC>(s + o_dxo, g.T, g.t, c, sp, N, d[c]);
             } else {
                 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[c][e] = 0.0f;
             }
             if (has_dy) {
                 float x[8];
-                take8<XT>(s, g.T, g.t, c, sp, N, x);
-                take8<ZT>(s + o_dy, g.T, g.t, c, sp, N, b);
+                take8<XT, VEC>(s, g.T, g.t, c, sp, N, x);
+                take8<ZT, VEC>(s + o_dy, g.T, g.t, c, sp, N, b);
                 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    x[e] = sp.base + e * sp.step < N ? (x[e] - mx) * rx : 0.0f;
+                    x[e] = sp.in(e, N) ? (x[e] - mx) * rx : 0.0f;
                     a_yx[c][e] = fmaf(b[e], x[e], a_yx[c][e]);
                     if constexpr (BIAS) a_y[c][e] += b[e];
                 }
@@ -670,19 +744,19 @@ __global__ void __launch_bounds__(THREADS)
                 if (p.pre != kNone) {
                     #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        b[e] = sp.base + e * sp.step < N ? (b[e] - gsum - x[e] * gx) * rx : 0.0f;
+                        b[e] = sp.in(e, N) ? (b[e] - gsum - x[e] * gx) * rx : 0.0f;
                 }
                 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[c][e] += b[e];
             }
             if (p.dX != nullptr)
-                store8<XT>(static_cast<XT*>(p.dX) + row * p.lddx, sp, N, d[c]);
+                store8<XT, VEC>(static_cast<XT*>(p.dX) + row * p.lddx, sp, N, d[c]);
             if (has_z) {
                 float z[8], gt[8];
-                take8<ZT>(s + o_z, g.T, g.t, c, sp, N, z);
+                take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, z);
                 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    z[e] = sp.base + e * sp.step < N ? (z[e] - mz) * rz : 0.0f;
+                    z[e] = sp.in(e, N) ? (z[e] - mz) * rz : 0.0f;
                     gt[e] = p.scale;
                 }
                 if (p.gate != nullptr) {
@@ -708,8 +782,8 @@ __global__ void __launch_bounds__(THREADS)
                     }
                     #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const int32_t i = sp.base + e * sp.step;
-                        if (i < N) store_elem(p.dgate, p.grad_dtype, row * N + i, p.scale * d[c][e] * n[e]);
+                        if (sp.in(e, N))
+                            store_elem(p.dgate, p.grad_dtype, row * N + sp.at(e), p.scale * d[c][e] * n[e]);
                     }
                 }
                 #pragma unroll
@@ -740,15 +814,15 @@ __global__ void __launch_bounds__(THREADS)
             }
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
                 if (p.post != kNone) {
                     float z[8];
-                    take8<ZT>(s + o_z, g.T, g.t, c, sp, N, z);
+                    take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, z);
                     #pragma unroll
                     for (int e = 0; e < 8; ++e)
                         d[c][e] = (d[c][e] - gm - (z[e] - mz) * rz * gz) * rz;
                 }
-                store8<ZT>(static_cast<ZT*>(p.dZ) + row * p.lddz, sp, N, d[c]);
+                store8<ZT, VEC>(static_cast<ZT*>(p.dZ) + row * p.lddz, sp, N, d[c]);
             }
         }
     }
@@ -792,11 +866,11 @@ __global__ void __launch_bounds__(THREADS)
         float* out = p.partials + chunk * N;
         #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const Spot sp = spot_of(vec, g.T, g.t, c, col0);
+            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
             #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int32_t i = sp.base + e * sp.step;
-                if (i >= N) continue;
+                const int32_t i = sp.at(e);
+                if (!sp.in(e, N)) continue;
                 out[i] = a_yx[c][e];
                 out[p.part_stride + i] = a_qz[c][e];
                 if constexpr (BIAS) {
