@@ -64,17 +64,71 @@ struct Params {
 
 // ------------------------------------------------------------------ elements
 
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
-    return __bfloat162float(v);
+// Two FP32 values in a 64-bit register: the packed FP32 instructions do two
+// lanes' work in one issue slot, and these kernels were bound by issue slots
+// (64 instructions per element in scalar form, about 12 in this one).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 mk2(float lo, float hi) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+    return r;
 }
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
+__device__ __forceinline__ F2 mk2(float x) { return mk2(x, x); }
+__device__ __forceinline__ void get2(F2 a, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ float sum2(F2 a) {
+    float lo, hi;
+    get2(a, lo, hi);
+    return lo + hi;
+}
+
+// 8 consecutive or strided elements as 4 pairs.
+typedef F2 F8[4];
+
+__device__ __forceinline__ void set8(F8& o, float x) {
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = mk2(x);
+}
+
+// A pair of 16-bit elements (low half first) as FP32, and back, rounded.
+template <typename E> __device__ __forceinline__ F2 unpack2(uint32_t w);
+template <> __device__ __forceinline__ F2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return mk2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+template <> __device__ __forceinline__ F2 unpack2<__half>(uint32_t w) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return mk2(f.x, f.y);
+}
+template <typename E> __device__ __forceinline__ uint32_t pack2(F2 a);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(F2 a) {
+    float lo, hi;
+    get2(a, lo, hi);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <> __device__ __forceinline__ uint32_t pack2<__half>(F2 a) {
+    float lo, hi;
+    get2(a, lo, hi);
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Where a thread's 8 elements of chunk c lie in the row: element e at
@@ -85,6 +139,8 @@ struct Spot {
     int32_t base;
     __device__ __forceinline__ int32_t at(int e) const { return VEC ? base + e : base + 32 * e; }
     __device__ __forceinline__ bool in(int e, int32_t N) const { return VEC ? base < N : at(e) < N; }
+    // whether there is anything to do for the chunk
+    __device__ __forceinline__ bool some(int32_t N) const { return base < N; }
 };
 
 template <bool VEC>
@@ -92,48 +148,79 @@ __device__ __forceinline__ Spot<VEC> spot_of(int T, int t, int c, int32_t first 
     return {first + (VEC ? (c * T + t) * 8 : (c * T + (t & ~31)) * 8 + (t & 31))};
 }
 
-// 8 elements of a vector parameter (weight, bias, gate row) of type dtype.
+// 8 elements of a vector parameter (weight, bias, gate row) of type dtype; 0
+// past column N.
 template <bool VEC>
 __device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool wide, Spot<VEC> s,
-                                            int32_t N, float (&o)[8]) {
+                                            int32_t N, F8& o) {
     if (VEC && wide) {
-        if (s.base >= N) {
-            #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-            return;
-        }
         if (dtype == 2) {
-            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(v) + s.base);
-            const float4 a = __ldg(p), b = __ldg(p + 1);
-            o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-            o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+            const ulonglong2* p = reinterpret_cast<const ulonglong2*>(static_cast<const float*>(v) + s.base);
+            const ulonglong2 a = __ldg(p), b = __ldg(p + 1);
+            o[0].v = a.x; o[1].v = a.y; o[2].v = b.x; o[3].v = b.y;
         } else {
-            union {
-                uint4 u;
-                __half h[8];
-                __nv_bfloat16 b[8];
-            } w;
-            w.u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(v) + s.base));
-            if (dtype == 1) {
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __bfloat162float(w.b[e]);
-            } else {
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __half2float(w.h[e]);
-            }
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(v) + s.base));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            #pragma unroll
+            for (int q = 0; q < 4; ++q)
+                o[q] = dtype == 1 ? unpack2<__nv_bfloat16>(w[q]) : unpack2<__half>(w[q]);
         }
         return;
     }
+    float f[8];
     #pragma unroll
     for (int e = 0; e < 8; ++e) {
         const int32_t i = s.at(e);
-        o[e] = 0.0f;
+        f[e] = 0.0f;
         if (s.in(e, N)) {
-            if (dtype == 2) o[e] = __ldg(static_cast<const float*>(v) + i);
-            else if (dtype == 1) o[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(v)[i]);
-            else o[e] = __half2float(static_cast<const __half*>(v)[i]);
+            if (dtype == 2) f[e] = __ldg(static_cast<const float*>(v) + i);
+            else if (dtype == 1) f[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(v)[i]);
+            else f[e] = __half2float(static_cast<const __half*>(v)[i]);
         }
     }
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = mk2(f[2 * q], f[2 * q + 1]);
+}
+
+// o *= parameter, o += parameter, where there is one.
+template <bool VEC>
+__device__ __forceinline__ void scale_by(F8& o, const void* v, int32_t dtype, bool wide, Spot<VEC> s,
+                                         int32_t N) {
+    if (v == nullptr) return;
+    F8 w;
+    load_param8<VEC>(v, dtype, wide, s, N, w);
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = mul2(o[q], w[q]);
+}
+template <bool VEC>
+__device__ __forceinline__ void shift_by(F8& o, const void* v, int32_t dtype, bool wide, Spot<VEC> s,
+                                         int32_t N) {
+    if (v == nullptr) return;
+    F8 w;
+    load_param8<VEC>(v, dtype, wide, s, N, w);
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = add2(o[q], w[q]);
+}
+
+// Elements past column N as 0 (a chunk with VEC has none).
+template <bool VEC>
+__device__ __forceinline__ void mask8(F8& o, Spot<VEC> s, int32_t N) {
+    if constexpr (!VEC) {
+        #pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float lo, hi;
+            get2(o[q], lo, hi);
+            o[q] = mk2(s.in(2 * q, N) ? lo : 0.0f, s.in(2 * q + 1, N) ? hi : 0.0f);
+        }
+    }
+}
+
+// o - mean, 0 past column N.
+template <bool VEC>
+__device__ __forceinline__ void center8(F8& o, float mean, Spot<VEC> s, int32_t N) {
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = add2(o[q], mk2(-mean));
+    mask8<VEC>(o, s, N);
 }
 
 __device__ __forceinline__ void store_elem(void* p, int32_t dtype, int64_t i, float v) {
@@ -187,6 +274,7 @@ __device__ __forceinline__ void fetch8(uint8_t* slot, int T, int t, int c, const
                 cp_async16(d + q * T * 16, row + s.base + q * (8 / kPieces));
         }
     } else if constexpr (sizeof(E) == 4) {
+        // the elements past column N stay as they are: 0 (zero_ring)
         #pragma unroll
         for (int e = 0; e < 8; ++e)
             if (s.in(e, N)) cp_async4(d + (e / 4) * T * 16 + (e % 4) * 4, row + s.at(e));
@@ -219,63 +307,81 @@ __device__ __forceinline__ void put8(uint8_t* slot, int T, int t, int c, const H
         *reinterpret_cast<uint4*>(slot_at<E>(slot, T, t, c)) = make_uint4(h.w[0], h.w[1], h.w[2], h.w[3]);
 }
 
-// The 8 elements of this thread's part of a slot as FP32, 0 past column N.
-template <typename E, bool VEC>
-__device__ __forceinline__ void take8(uint8_t* slot, int T, int t, int c, Spot<VEC> s, int32_t N,
-                                      float (&o)[8]) {
-    constexpr int kPieces = sizeof(E) / 2;
-    constexpr int kPer = 8 / kPieces;
-    const uint8_t* d = slot_at<E>(slot, T, t, c);
-    #pragma unroll
-    for (int q = 0; q < kPieces; ++q) {
-        union {
-            uint4 u;
-            E e[kPer];
-        } w;
-        w.u = *reinterpret_cast<const uint4*>(d + q * T * 16);
-        #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const int k = q * kPer + e;
-            o[k] = s.in(k, N) ? to_f<E>(w.e[e]) : 0.0f;
-        }
+// This thread's parts of the group's ring as 0: what lies past column N in a
+// chunk that has columns of the row is never copied and has to read as 0.
+template <bool VEC>
+__device__ __forceinline__ void zero_ring(uint8_t* ring, uint32_t bytes, int T, int t) {
+    if constexpr (!VEC) {
+        for (uint32_t i = t * 16u; i < bytes; i += T * 16u)
+            *reinterpret_cast<uint4*>(ring + i) = make_uint4(0u, 0u, 0u, 0u);
     }
 }
 
-template <typename E, bool VEC>
-__device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, const float (&v)[8]) {
-    constexpr int kPieces = sizeof(E) / 2;
-    constexpr int kPer = 8 / kPieces;
-    if constexpr (VEC) {
-        if (s.base >= N) return;
-        #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            union {
-                uint4 u;
-                E e[kPer];
-            } w;
+// The 8 elements of this thread's part of a slot as FP32.
+template <typename E>
+__device__ __forceinline__ void take8(uint8_t* slot, int T, int t, int c, F8& o) {
+    const uint8_t* d = slot_at<E>(slot, T, t, c);
+    if constexpr (sizeof(E) == 4) {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(d);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(d + T * 16);
+        o[0].v = a.x; o[1].v = a.y; o[2].v = b.x; o[3].v = b.y;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(d);
+        o[0] = unpack2<E>(u.x);
+        o[1] = unpack2<E>(u.y);
+        o[2] = unpack2<E>(u.z);
+        o[3] = unpack2<E>(u.w);
+    }
+}
+
+// Stores 8 elements rounded to E (the columns < N); with KEEP v becomes what
+// was stored.
+template <typename E, bool VEC, bool KEEP = false>
+__device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, F8& v) {
+    if constexpr (sizeof(E) == 4) {
+        if constexpr (VEC) {
+            *reinterpret_cast<ulonglong2*>(row + s.base) = make_ulonglong2(v[0].v, v[1].v);
+            *reinterpret_cast<ulonglong2*>(row + s.base + 4) = make_ulonglong2(v[2].v, v[3].v);
+        } else {
             #pragma unroll
-            for (int e = 0; e < kPer; ++e) w.e[e] = from_f<E>(v[q * kPer + e]);
-            *reinterpret_cast<uint4*>(row + s.base + q * kPer) = w.u;
+            for (int q = 0; q < 4; ++q) {
+                float lo, hi;
+                get2(v[q], lo, hi);
+                if (s.in(2 * q, N)) row[s.at(2 * q)] = lo;
+                if (s.in(2 * q + 1, N)) row[s.at(2 * q + 1)] = hi;
+            }
         }
     } else {
+        uint32_t w[4];
         #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (s.in(e, N)) row[s.at(e)] = from_f<E>(v[e]);
+        for (int q = 0; q < 4; ++q) {
+            w[q] = pack2<E>(v[q]);
+            if constexpr (KEEP) v[q] = unpack2<E>(w[q]);
+        }
+        if constexpr (VEC) {
+            *reinterpret_cast<uint4*>(row + s.base) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            uint16_t* r = reinterpret_cast<uint16_t*>(row);
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (s.in(2 * q, N)) r[s.at(2 * q)] = static_cast<uint16_t>(w[q] & 0xFFFFu);
+                if (s.in(2 * q + 1, N)) r[s.at(2 * q + 1)] = static_cast<uint16_t>(w[q] >> 16);
+            }
+        }
     }
 }
 
 // The group of threads that shares a row: T threads of the CTA, `warps` warps.
 struct Group {
     int T, t, index, warps;     // threads, this thread's number, the group's number
-    float* red;                 // [2][warps][4] exchange buffer of this group
+    float* red;                 // [2][4][warps] exchange buffer of this group
     int parity;
     float* pair;                // [2][2][4] exchange buffer of a CTA pair, or NULL
     uint32_t rank;              // this CTA's number in the pair
 };
 
 __device__ __forceinline__ void group_barrier(const Group& g) {
-    if (g.T == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.T) : "memory");
+    asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.T) : "memory");
 }
 
 // Sums of K values over the group, in the same order on every run; every
@@ -291,21 +397,24 @@ __device__ __forceinline__ void group_sum(Group& g, float (&v)[K]) {
     if (g.T == 32) return;
     float* r = g.red + g.parity * g.warps * 4;
     g.parity ^= 1;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) {
+    if ((threadIdx.x & 31) == 0) {
         #pragma unroll
-        for (int k = 0; k < K; ++k) r[(g.t >> 5) * 4 + k] = v[k];
+        for (int k = 0; k < K; ++k) r[k * g.warps + (g.t >> 5)] = v[k];
     }
     group_barrier(g);
     #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = lane < g.warps ? r[lane * 4 + k] : 0.0f;
-    // warps is a power of two at most 32
-    for (int o = g.warps >> 1; o > 0; o >>= 1) {
-        #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int k = 0; k < K; ++k) {
+        const float* q = r + k * g.warps;
+        if (g.warps == 2) {
+            v[k] = q[0] + q[1];
+        } else {
+            v[k] = 0.0f;
+            for (int w = 0; w < g.warps; w += 4) {      // a power of two, 4 at least
+                const float4 x = *reinterpret_cast<const float4*>(q + w);
+                v[k] += (x.x + x.y) + (x.z + x.w);
+            }
+        }
     }
-    #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, v[k], 0);
     if (g.pair == nullptr) return;
     // the other half of the row: each CTA leaves its sums in both CTAs' shared
     // memory, and both add them in rank order.  The buffer of this parity is
@@ -341,6 +450,36 @@ __device__ __forceinline__ Group make_group(const Params& p, uint8_t* smem) {
 
 // ------------------------------------------------------------------- forward
 
+// Mean and 1 / size of a row whose chunks are in v; v becomes v - mean.
+template <int C, bool VEC>
+__device__ __forceinline__ float norm_stats(Group& g, const Params& p, int kind, F8 (&v)[C]) {
+    if (kind == kNone) return 1.0f;
+    if (kind == kLayer) {
+        F2 a = mk2(0.0f);
+        #pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (spot_of<VEC>(g.T, g.t, c).some(p.N)) {
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) a = add2(a, v[c][q]);
+            }
+        float s[1] = {sum2(a)};
+        group_sum(g, s);
+        const float mean = s[0] * p.inv_n;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) center8<VEC>(v[c], mean, spot_of<VEC>(g.T, g.t, c), p.N);
+    }
+    F2 a = mk2(0.0f);
+    #pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (spot_of<VEC>(g.T, g.t, c).some(p.N)) {
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) a = fma2(v[c][q], v[c][q], a);
+        }
+    float s[1] = {sum2(a)};
+    group_sum(g, s);
+    return 1.0f / sqrtf(fmaf(s[0], p.inv_n, p.eps));
+}
+
 // Rows go to groups round robin over the grid.
 template <typename XT, typename ZT, int C, bool VEC>
 __global__ void __launch_bounds__(1024)
@@ -356,6 +495,7 @@ __global__ void __launch_bounds__(1024)
     const int32_t N = p.N;
     const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + g.index;
+    zero_ring<VEC>(ring, p.stages * p.slot_bytes, g.T, g.t);
     grid_dependency_wait();
     grid_dependents_launch();
 
@@ -368,7 +508,7 @@ __global__ void __launch_bounds__(1024)
                 fetch8<XT, VEC>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
                 if (has_z)
                     fetch8<ZT, VEC>(s + x_bytes, g.T, g.t, c,
-                               static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+                                    static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
             }
         }
         cp_async_commit();
@@ -406,113 +546,47 @@ __global__ void __launch_bounds__(1024)
         uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
         if (++slot == p.stages) slot = 0;
 
-        float x[C][8];
-        #pragma unroll
-        for (int c = 0; c < C; ++c)
-            take8<XT, VEC>(s, g.T, g.t, c, spot_of<VEC>(g.T, g.t, c), N, x[c]);
+        F8 x[C];
         if (has_z) {
-            float z[C][8];
-            float mean = 0.0f, r = 1.0f;
+            F8 z[C];
             #pragma unroll
-            for (int c = 0; c < C; ++c)
-                take8<ZT, VEC>(s + x_bytes, g.T, g.t, c, spot_of<VEC>(g.T, g.t, c), N, z[c]);
-            if (p.post == kLayer) {
-                float v[1] = {0.0f};
-                #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[0] += z[c][e];
-                group_sum(g, v);
-                mean = v[0] * p.inv_n;
+            for (int c = 0; c < C; ++c) take8<ZT>(s + x_bytes, g.T, g.t, c, z[c]);
+            const float r = norm_stats<C, VEC>(g, p, p.post, z);
+            const void* gate = nullptr;
+            if (p.gate != nullptr) {
+                const int64_t grow = p.gate_rows > 1 ? row / p.gate_rows : row;
+                gate = static_cast<const uint8_t*>(p.gate) + grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
             }
-            if (p.post != kNone) {
-                float v[1] = {0.0f};
-                #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float d = sp.in(e, N) ? z[c][e] - mean : 0.0f;
-                        v[0] = fmaf(d, d, v[0]);
-                    }
-                }
-                group_sum(g, v);
-                r = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
-            }
-            const int64_t grow = p.gate_rows > 1 ? row / p.gate_rows : row;
             #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-                float w[8];
+                if (!sp.some(N)) continue;
+                take8<XT>(s, g.T, g.t, c, x[c]);
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[c][e] = (z[c][e] - mean) * r;
-                if (p.wpost != nullptr) {
-                    load_param8(p.wpost, p.vec_dtype, wide, sp, N, w);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[c][e] *= w[e];
-                }
-                if (p.bpost != nullptr) {
-                    load_param8(p.bpost, p.vec_dtype, wide, sp, N, w);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[c][e] += w[e];
-                }
-                if (p.gate != nullptr) {
-                    const int64_t at = grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
-                    load_param8(static_cast<const uint8_t*>(p.gate) + at, p.vec_dtype, wide, sp, N, w);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) z[c][e] *= w[e];
-                }
+                for (int q = 0; q < 4; ++q) z[c][q] = mul2(z[c][q], mk2(r));
+                scale_by<VEC>(z[c], p.wpost, p.vec_dtype, wide, sp, N);
+                shift_by<VEC>(z[c], p.bpost, p.vec_dtype, wide, sp, N);
+                scale_by<VEC>(z[c], gate, p.vec_dtype, wide, sp, N);
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    // the stream as its type holds it: what is stored is what
-                    // the next norm sees
-                    x[c][e] = to_f<XT>(from_f<XT>(fmaf(p.scale, z[c][e], x[c][e])));
-                    if (!sp.in(e, N)) x[c][e] = 0.0f;
-                }
-                store8<XT, VEC>(static_cast<XT*>(p.XO) + row * p.ldxo, sp, N, x[c]);
+                for (int q = 0; q < 4; ++q) x[c][q] = fma2(mk2(p.scale), z[c][q], x[c][q]);
+                // the stream as its type holds it: what is stored is what the
+                // next norm sees
+                store8<XT, VEC, true>(static_cast<XT*>(p.XO) + row * p.ldxo, sp, N, x[c]);
             }
+        } else {
+            #pragma unroll
+            for (int c = 0; c < C; ++c) take8<XT>(s, g.T, g.t, c, x[c]);
         }
         if (p.Y != nullptr) {
-            float mean = 0.0f, r = 1.0f;
-            if (p.pre == kLayer) {
-                float v[1] = {0.0f};
-                #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[0] += x[c][e];
-                group_sum(g, v);
-                mean = v[0] * p.inv_n;
-            }
-            if (p.pre != kNone) {
-                float v[1] = {0.0f};
-                #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float d = sp.in(e, N) ? x[c][e] - mean : 0.0f;
-                        v[0] = fmaf(d, d, v[0]);
-                    }
-                }
-                group_sum(g, v);
-                r = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
-            }
+            const float r = norm_stats<C, VEC>(g, p, p.pre, x);
             #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-                float w[8];
+                if (!sp.some(N)) continue;
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[c][e] = (x[c][e] - mean) * r;
-                if (p.wpre != nullptr) {
-                    load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[c][e] *= w[e];
-                }
-                if (p.bpre != nullptr) {
-                    load_param8(p.bpre, p.vec_dtype, wide, sp, N, w);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[c][e] += w[e];
-                }
+                for (int q = 0; q < 4; ++q) x[c][q] = mul2(x[c][q], mk2(r));
+                scale_by<VEC>(x[c], p.wpre, p.vec_dtype, wide, sp, N);
+                shift_by<VEC>(x[c], p.bpre, p.vec_dtype, wide, sp, N);
                 store8<ZT, VEC>(static_cast<ZT*>(p.Y) + row * p.ldy, sp, N, x[c]);
             }
         }
@@ -534,13 +608,14 @@ __device__ __forceinline__ void chunk_span(const Params& p, int64_t b, int64_t& 
 }
 
 // One CTA per chunk of rows (or a pair of CTAs, each with half the columns of
-// rows wider than one CTA's registers hold), its groups taking the chunk's rows in turn.  Per
-// row: the statistics of XO and Z, the sums that the pre-norm's Jacobian
-// needs, then those of the post-norm's; per column, in registers, the sums
-// over the chunk's rows of dY xhat, dY, q zhat and q, with q = dXO' (the gate
-// is constant over a chunk and joins in the sum over chunks) or, for token
-// gates, q = scale gate dXO'.  The groups' sums meet in shared memory (in
-// group order) and go to the chunk's line of partials.
+// rows wider than one CTA's registers hold), its groups taking the chunk's
+// rows in turn.  Per row: the statistics of XO and Z with the sums that the
+// pre-norm's Jacobian needs (one exchange; two where a mean comes first), then
+// the post-norm's (one more); per column, in registers, the sums over the
+// chunk's rows of dY xhat, q zhat, and with BIAS dY and q, where q = dXO' (the
+// gate is constant over a chunk and joins in the sum over chunks) or, for
+// token gates, q = scale gate dXO'.  The groups' sums meet in shared memory
+// (in group order) and go to the chunk's line of partials.
 template <typename XT, typename ZT, int C, bool VEC, bool BIAS, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     backward_kernel(const __grid_constant__ Params p) {
@@ -567,6 +642,7 @@ __global__ void __launch_bounds__(THREADS)
     }
     int64_t row0, row1, group;
     chunk_span(p, chunk, row0, row1, group);
+    zero_ring<VEC>(ring, p.stages * p.slot_bytes, g.T, g.t);
     if (p.cluster == 2) cluster_sync_all();     // the other CTA's shared memory is there
     grid_dependency_wait();
     grid_dependents_launch();
@@ -580,28 +656,17 @@ __global__ void __launch_bounds__(THREADS)
                 fetch8<XT, VEC>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
                 if (has_dxo)
                     fetch8<XT, VEC>(s + o_dxo, g.T, g.t, c,
-                               static_cast<const XT*>(p.dXO) + row * p.lddxo, sp, N);
+                                    static_cast<const XT*>(p.dXO) + row * p.lddxo, sp, N);
                 if (has_z)
                     fetch8<ZT, VEC>(s + o_z, g.T, g.t, c,
-                               static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+                                    static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
                 if (has_dy)
                     fetch8<ZT, VEC>(s + o_dy, g.T, g.t, c,
-                               static_cast<const ZT*>(p.dY) + row * p.lddy, sp, N);
+                                    static_cast<const ZT*>(p.dY) + row * p.lddy, sp, N);
             }
         }
         cp_async_commit();
     };
-
-    float a_yx[C][8], a_y[BIAS ? C : 1][8], a_qz[C][8], a_q[BIAS ? C : 1][8];
-    #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            a_yx[c][e] = a_qz[c][e] = 0.0f;
-            if constexpr (BIAS) a_y[c][e] = a_q[c][e] = 0.0f;
-        }
-    }
-
     Held<XT, VEC> hx[C], hd[C];
     Held<ZT, VEC> hz[C], hy[C];
     auto hold = [&](int64_t row) {
@@ -615,6 +680,19 @@ __global__ void __launch_bounds__(THREADS)
             if (has_dy) hold8<ZT, VEC>(hy[c], static_cast<const ZT*>(p.dY) + row * p.lddy, sp, N);
         }
     };
+
+    F8 a_yx[C], a_qz[C], a_y[BIAS ? C : 1], a_q[BIAS ? C : 1];
+    #pragma unroll
+    for (int c = 0; c < C; ++c) {
+        set8(a_yx[c], 0.0f);
+        set8(a_qz[c], 0.0f);
+        if constexpr (BIAS) {
+            set8(a_y[c], 0.0f);
+            set8(a_q[c], 0.0f);
+        }
+    }
+    const bool pre_layer = p.pre == kLayer, post_layer = p.post == kLayer;
+
     for (int s = 0; s < p.stages - 1; ++s) fetch(row0 + g.index + static_cast<int64_t>(s) * groups, s);
     if constexpr (!VEC) hold(row0 + g.index);
     int slot = 0;
@@ -639,188 +717,170 @@ __global__ void __launch_bounds__(THREADS)
         uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
         if (++slot == p.stages) slot = 0;
 
-        // ---- statistics of XO and Z, and the sums with g = dY * wpre
+        // ---- means, where a norm has one: of XO, g = dY wpre, Z
         float mx = 0.0f, mz = 0.0f, gsum = 0.0f;
-        if (p.pre == kLayer || p.post == kLayer) {
-            float v[3] = {0.0f, 0.0f, 0.0f};
+        if (pre_layer || post_layer) {
+            F2 sx = mk2(0.0f), sg = mk2(0.0f), sz = mk2(0.0f);
             #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
-                float b[8], w[8];
-                if (p.pre == kLayer) {
-                    take8<XT, VEC>(s, g.T, g.t, c, sp, N, b);
+                if (!sp.some(N)) continue;
+                F8 b;
+                if (pre_layer && has_dy) {
+                    take8<XT>(s, g.T, g.t, c, b);
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[0] += b[e];
-                    if (has_dy) {
-                        take8<ZT, VEC>(s + o_dy, g.T, g.t, c, sp, N, b);
-                        if (p.wpre != nullptr) {
-                            load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
-                            #pragma unroll
-                            for (int e = 0; e < 8; ++e) v[1] = fmaf(b[e], w[e], v[1]);
-                        } else {
-                            #pragma unroll
-                            for (int e = 0; e < 8; ++e) v[1] += b[e];
-                        }
-                    }
+                    for (int q = 0; q < 4; ++q) sx = add2(sx, b[q]);
+                    take8<ZT>(s + o_dy, g.T, g.t, c, b);
+                    scale_by<VEC>(b, p.wpre, p.vec_dtype, wide, sp, N);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) sg = add2(sg, b[q]);
                 }
-                if (has_z && p.post == kLayer) {
-                    take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, b);
+                if (has_z && post_layer) {
+                    take8<ZT>(s + o_z, g.T, g.t, c, b);
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[2] += b[e];
+                    for (int q = 0; q < 4; ++q) sz = add2(sz, b[q]);
                 }
             }
+            float v[3] = {sum2(sx), sum2(sg), sum2(sz)};
             group_sum(g, v);
             mx = v[0] * p.inv_n;
             gsum = v[1] * p.inv_n;
             mz = v[2] * p.inv_n;
         }
-        float rx = 1.0f, rz = 1.0f, gx = 0.0f;      // gx: mean of g xhat
-        {
-            float v[3] = {0.0f, 0.0f, 0.0f};
+        // ---- sizes of XO and Z, and the mean of g xhat
+        float rx = 1.0f, rz = 1.0f, gx = 0.0f;
+        if (p.pre != kNone || p.post != kNone) {
+            F2 sx = mk2(0.0f), sg = mk2(0.0f), sz = mk2(0.0f);
             #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
-                float b[8], w[8], x[8];
+                if (!sp.some(N)) continue;
+                F8 b, x;
                 if (has_dy && p.pre != kNone) {
-                    take8<XT, VEC>(s, g.T, g.t, c, sp, N, x);
+                    take8<XT>(s, g.T, g.t, c, x);
+                    if (pre_layer) center8<VEC>(x, mx, sp, N);
+                    take8<ZT>(s + o_dy, g.T, g.t, c, b);
+                    scale_by<VEC>(b, p.wpre, p.vec_dtype, wide, sp, N);
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        x[e] = sp.in(e, N) ? x[e] - mx : 0.0f;
-                        v[0] = fmaf(x[e], x[e], v[0]);
+                    for (int q = 0; q < 4; ++q) {
+                        sx = fma2(x[q], x[q], sx);
+                        sg = fma2(b[q], x[q], sg);
                     }
-                    take8<ZT, VEC>(s + o_dy, g.T, g.t, c, sp, N, b);
-                    if (p.wpre != nullptr) {
-                        load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) b[e] *= w[e];
-                    }
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[1] = fmaf(b[e], x[e], v[1]);
                 }
                 if (has_z && p.post != kNone) {
-                    take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, b);
+                    take8<ZT>(s + o_z, g.T, g.t, c, b);
+                    if (post_layer) center8<VEC>(b, mz, sp, N);
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float d = sp.in(e, N) ? b[e] - mz : 0.0f;
-                        v[2] = fmaf(d, d, v[2]);
-                    }
+                    for (int q = 0; q < 4; ++q) sz = fma2(b[q], b[q], sz);
                 }
             }
-            if (p.pre != kNone || p.post != kNone) group_sum(g, v);
-            if (p.pre != kNone) rx = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
+            float v[3] = {sum2(sx), sum2(sg), sum2(sz)};
+            group_sum(g, v);
+            if (p.pre != kNone) {
+                rx = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
+                gx = v[1] * rx * p.inv_n;
+            }
             if (p.post != kNone) rz = 1.0f / sqrtf(fmaf(v[2], p.inv_n, p.eps));
-            gx = v[1] * rx * p.inv_n;
         }
 
-        // ---- dXO' and its column sums; the post-norm's sums
-        float d[C][8];                               // dXO', then gz = dn * wpost
-        float v2[2] = {0.0f, 0.0f};
+        // ---- dXO' and the column sums; the post-norm's sums
+        F8 d[C];                                     // dXO', then gz = dn wpost
+        F2 sgz = mk2(0.0f), sgm = mk2(0.0f);
         const int64_t grow = p.token_gate ? row : group;
+        const void* gate = p.gate == nullptr ? nullptr
+                           : static_cast<const uint8_t*>(p.gate) +
+                                 grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
         #pragma unroll
         for (int c = 0; c < C; ++c) {
             const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
-            float b[8], w[8];
-            if (has_dxo) {
-                take8<XT, VEC>(s + o_dxo, g.T, g.t, c, sp, N, d[c]);
-            } else {
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) d[c][e] = 0.0f;
-            }
+            if (!sp.some(N)) continue;
+            if (has_dxo) take8<XT>(s + o_dxo, g.T, g.t, c, d[c]);
+            else set8(d[c], 0.0f);
             if (has_dy) {
-                float x[8];
-                take8<XT, VEC>(s, g.T, g.t, c, sp, N, x);
-                take8<ZT, VEC>(s + o_dy, g.T, g.t, c, sp, N, b);
+                F8 x, b;
+                take8<XT>(s, g.T, g.t, c, x);
+                take8<ZT>(s + o_dy, g.T, g.t, c, b);
+                if (pre_layer) center8<VEC>(x, mx, sp, N);
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    x[e] = sp.in(e, N) ? (x[e] - mx) * rx : 0.0f;
-                    a_yx[c][e] = fmaf(b[e], x[e], a_yx[c][e]);
-                    if constexpr (BIAS) a_y[c][e] += b[e];
+                for (int q = 0; q < 4; ++q) {
+                    x[q] = mul2(x[q], mk2(rx));
+                    a_yx[c][q] = fma2(b[q], x[q], a_yx[c][q]);
+                    if constexpr (BIAS) a_y[c][q] = add2(a_y[c][q], b[q]);
                 }
-                if (p.wpre != nullptr) {
-                    load_param8(p.wpre, p.vec_dtype, wide, sp, N, w);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) b[e] *= w[e];
-                }
+                scale_by<VEC>(b, p.wpre, p.vec_dtype, wide, sp, N);
                 if (p.pre != kNone) {
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        b[e] = sp.in(e, N) ? (b[e] - gsum - x[e] * gx) * rx : 0.0f;
+                    for (int q = 0; q < 4; ++q) b[q] = fma2(x[q], mk2(-gx), b[q]);
+                    if (pre_layer) center8<VEC>(b, gsum, sp, N);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) d[c][q] = fma2(b[q], mk2(rx), d[c][q]);
+                } else {
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) d[c][q] = add2(d[c][q], b[q]);
                 }
-                #pragma unroll
-                for (int e = 0; e < 8; ++e) d[c][e] += b[e];
             }
             if (p.dX != nullptr)
                 store8<XT, VEC>(static_cast<XT*>(p.dX) + row * p.lddx, sp, N, d[c]);
             if (has_z) {
-                float z[8], gt[8];
-                take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, z);
+                F8 z;
+                take8<ZT>(s + o_z, g.T, g.t, c, z);
+                if (post_layer) center8<VEC>(z, mz, sp, N);
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    z[e] = sp.in(e, N) ? (z[e] - mz) * rz : 0.0f;
-                    gt[e] = p.scale;
-                }
-                if (p.gate != nullptr) {
-                    const int64_t at = grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
-                    load_param8(static_cast<const uint8_t*>(p.gate) + at, p.vec_dtype, wide, sp, N, gt);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) gt[e] *= p.scale;
-                }
+                for (int q = 0; q < 4; ++q) z[q] = mul2(z[q], mk2(rz));
                 if (p.token_gate && p.dgate != nullptr) {
                     // scale * dXO' * n, one row of the gate per row
-                    float n[8];
+                    F8 n;
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) n[e] = z[e];
-                    if (p.wpost != nullptr) {
-                        load_param8(p.wpost, p.vec_dtype, wide, sp, N, w);
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) n[e] *= w[e];
-                    }
-                    if (p.bpost != nullptr) {
-                        load_param8(p.bpost, p.vec_dtype, wide, sp, N, w);
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) n[e] += w[e];
-                    }
+                    for (int q = 0; q < 4; ++q) n[q] = z[q];
+                    scale_by<VEC>(n, p.wpost, p.vec_dtype, wide, sp, N);
+                    shift_by<VEC>(n, p.bpost, p.vec_dtype, wide, sp, N);
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (sp.in(e, N))
-                            store_elem(p.dgate, p.grad_dtype, row * N + sp.at(e), p.scale * d[c][e] * n[e]);
+                    for (int q = 0; q < 4; ++q) {
+                        float lo, hi;
+                        get2(mul2(mul2(mk2(p.scale), d[c][q]), n[q]), lo, hi);
+                        if (sp.in(2 * q, N)) store_elem(p.dgate, p.grad_dtype, row * N + sp.at(2 * q), lo);
+                        if (sp.in(2 * q + 1, N)) store_elem(p.dgate, p.grad_dtype, row * N + sp.at(2 * q + 1), hi);
                     }
                 }
+                F8 dn;
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float q = p.token_gate ? d[c][e] * gt[e] : d[c][e];
-                    a_qz[c][e] = fmaf(q, z[e], a_qz[c][e]);
-                    if constexpr (BIAS) a_q[c][e] += q;
-                    d[c][e] *= gt[e];
-                }
-                if (p.wpost != nullptr) {
-                    load_param8(p.wpost, p.vec_dtype, wide, sp, N, w);
-                    #pragma unroll
-                    for (int e = 0; e < 8; ++e) d[c][e] *= w[e];
-                }
+                for (int q = 0; q < 4; ++q) dn[q] = mul2(d[c][q], mk2(p.scale));
+                scale_by<VEC>(dn, gate, p.vec_dtype, wide, sp, N);
                 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    v2[0] = fmaf(d[c][e], z[e], v2[0]);
-                    v2[1] += d[c][e];
+                for (int q = 0; q < 4; ++q) {
+                    const F2 v = p.token_gate ? dn[q] : d[c][q];
+                    a_qz[c][q] = fma2(v, z[q], a_qz[c][q]);
+                    if constexpr (BIAS) a_q[c][q] = add2(a_q[c][q], v);
+                    d[c][q] = dn[q];
+                }
+                scale_by<VEC>(d[c], p.wpost, p.vec_dtype, wide, sp, N);
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    sgz = fma2(d[c][q], z[q], sgz);
+                    sgm = add2(sgm, d[c][q]);
                 }
             }
         }
         if (has_z && p.dZ != nullptr) {
             float gz = 0.0f, gm = 0.0f;
             if (p.post != kNone) {
-                group_sum(g, v2);
-                gz = v2[0] * p.inv_n;
-                gm = p.post == kLayer ? v2[1] * p.inv_n : 0.0f;
+                float v[2] = {sum2(sgz), sum2(sgm)};
+                group_sum(g, v);
+                gz = v[0] * p.inv_n;
+                gm = post_layer ? v[1] * p.inv_n : 0.0f;
             }
             #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+                if (!sp.some(N)) continue;
                 if (p.post != kNone) {
-                    float z[8];
-                    take8<ZT, VEC>(s + o_z, g.T, g.t, c, sp, N, z);
+                    // rz (gz_j - mean gz - zhat mean(gz zhat)), zhat = (z - mz) rz
+                    F8 z;
+                    take8<ZT>(s + o_z, g.T, g.t, c, z);
+                    const F2 k = mk2(-rz * gz), a = mk2(rz * gz * mz - gm);
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        d[c][e] = (d[c][e] - gm - (z[e] - mz) * rz * gz) * rz;
+                    for (int q = 0; q < 4; ++q)
+                        d[c][q] = mul2(add2(fma2(z[q], k, d[c][q]), a), mk2(rz));
                 }
                 store8<ZT, VEC>(static_cast<ZT*>(p.dZ) + row * p.lddz, sp, N, d[c]);
             }
@@ -830,8 +890,16 @@ __global__ void __launch_bounds__(THREADS)
     // ---- the chunk's column sums: the groups' sums meet in the slots' memory
     if (p.partials == nullptr) return;
     cp_async_wait(0);
-    const int kinds = BIAS ? 4 : 2;                  // 0 dY xhat, 1 q zhat, 2 dY, 3 q
-    float* line = reinterpret_cast<float*>(rings);   // one group's sums: T * C * 8 floats
+    constexpr int kinds = BIAS ? 4 : 2;              // dY xhat, q zhat, dY, q
+    F2* line = reinterpret_cast<F2*>(rings);         // one group's sums: T * C * 4 pairs
+    auto sums = [&](int k, int c, int q) -> F2& {
+        if constexpr (BIAS) {
+            if (k == 2) return a_y[c][q];
+            if (k == 3) return a_q[c][q];
+        }
+        return k == 0 ? a_yx[c][q] : a_qz[c][q];
+    };
+    #pragma unroll
     for (int k = 0; k < kinds; ++k) {
         for (int gi = 1; gi < groups; ++gi) {
             __syncthreads();
@@ -839,43 +907,31 @@ __global__ void __launch_bounds__(THREADS)
                 #pragma unroll
                 for (int c = 0; c < C; ++c)
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float v = k == 0 ? a_yx[c][e] : a_qz[c][e];
-                        if constexpr (BIAS) v = k == 2 ? a_y[c][e] : k == 3 ? a_q[c][e] : v;
-                        line[(c * 8 + e) * p.T + g.t] = v;
-                    }
+                    for (int q = 0; q < 4; ++q) line[(c * 4 + q) * p.T + g.t] = sums(k, c, q);
             }
             __syncthreads();
             if (g.index == 0) {
                 #pragma unroll
                 for (int c = 0; c < C; ++c)
                     #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = line[(c * 8 + e) * p.T + g.t];
-                        if (k == 0) a_yx[c][e] += v;
-                        else if (k == 1) a_qz[c][e] += v;
-                        if constexpr (BIAS) {
-                            if (k == 2) a_y[c][e] += v;
-                            else if (k == 3) a_q[c][e] += v;
-                        }
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        sums(k, c, q) = add2(sums(k, c, q), line[(c * 4 + q) * p.T + g.t]);
             }
         }
     }
     if (g.index == 0) {
         float* out = p.partials + chunk * N;
         #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+        for (int k = 0; k < kinds; ++k) {
             #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int32_t i = sp.at(e);
-                if (!sp.in(e, N)) continue;
-                out[i] = a_yx[c][e];
-                out[p.part_stride + i] = a_qz[c][e];
-                if constexpr (BIAS) {
-                    out[2 * p.part_stride + i] = a_y[c][e];
-                    out[3 * p.part_stride + i] = a_q[c][e];
+            for (int c = 0; c < C; ++c) {
+                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float lo, hi;
+                    get2(sums(k, c, q), lo, hi);
+                    if (sp.in(2 * q, N)) out[k * p.part_stride + sp.at(2 * q)] = lo;
+                    if (sp.in(2 * q + 1, N)) out[k * p.part_stride + sp.at(2 * q + 1)] = hi;
                 }
             }
         }
