@@ -14,9 +14,9 @@ namespace {
 using namespace gemm103;
 using namespace gemm103::nrm;
 
-constexpr int64_t kSmemPerCta = 227 * 1024 - 1024;
-constexpr int64_t kMaxColumnsPerCta = 8192;  // backward
-constexpr int kRowsPerCtaThreads = 256;     // CTA size where a row needs fewer threads
+constexpr int64_t kSmemPerCta = 227 * 1024 - 256;
+constexpr int64_t kSmemPerSm = 228 * 1024;
+constexpr int64_t kMaxColumnsPerCta = 8192;
 
 bool dtype_ok(int32_t t) { return t == GEMM_F16 || t == GEMM_BF16 || t == GEMM_F32; }
 int64_t esize(int32_t t) { return t == GEMM_F32 ? 4 : 2; }
@@ -76,7 +76,6 @@ void fill_block(Params& p, int64_t M, int64_t N, const norm_block_t* b) {
     p.bpost = b->post_bias;
     p.gate = b->gate;
     p.ld_gate = b->gate ? b->ld_gate : 0;
-    p.gate_rows = b->gate ? b->gate_rows : 1;
     p.vec_dtype = b->vec_dtype;
     bool wide = true;
     const void* vecs[] = {b->pre_weight, b->pre_bias, b->post_weight, b->post_bias};
@@ -97,28 +96,57 @@ int threads_for(int64_t N, int chunks8) {
     return t;
 }
 
-// Ring depth: as many slots as fit beside each other in `budget` bytes, 2 to
-// kMaxStages (1 where two do not fit).
-int stages_for(int64_t slot, int groups, int64_t budget) {
-    int64_t s = (budget - 4096) / (slot * groups);
-    if (s > kMaxStages) s = kMaxStages;
-    return s < 1 ? 1 : static_cast<int>(s);
-}
-
 struct Chunks {
     int64_t group_rows, groups, per_group, rows;
 };
 
-// Rows cut into about two chunks per SM, each inside one group of the gate.
-Chunks chunks_for(int64_t M, int64_t gate_rows, int64_t sms) {
+// Rows cut into about `target` chunks, each inside one group of the gate.
+Chunks chunks_for(int64_t M, int64_t gate_rows, int64_t target) {
     Chunks c;
     c.group_rows = (gate_rows > 1 && gate_rows < M) ? gate_rows : (M > 0 ? M : 1);
     c.groups = ceil_div(M > 0 ? M : 1, c.group_rows);
-    int64_t per = ceil_div(2 * sms, c.groups);
+    int64_t per = ceil_div(target, c.groups);
     if (per > c.group_rows) per = c.group_rows;
     c.rows = ceil_div(c.group_rows, per);
     c.per_group = ceil_div(c.group_rows, c.rows);
     return c;
+}
+
+void set_chunks(Params& p, const Chunks& c) {
+    p.chunk_group_rows = c.group_rows;
+    p.chunks_per_group = static_cast<int32_t>(c.per_group);
+    p.chunk_rows = c.rows;
+}
+
+// Shared memory of a CTA of `groups` groups: exchange buffers, the n_par
+// vectors, the groups' rings.
+int64_t smem_for(const Params& p, int chunks8, int groups, int stages) {
+    return groups * static_cast<int64_t>(p.T) + static_cast<int64_t>(p.n_par) * chunks8 * 32 * p.T +
+           static_cast<int64_t>(groups) * stages * p.slot_bytes;
+}
+
+// Groups per CTA and slots per group: the most rows in flight per SM among
+// CTAs of up to `most` threads whose threads all fit an SM's `resident`, with
+// a second slot where it fits; the smallest such CTA.  Returns CTAs per SM, 0
+// where nothing fits.
+int choose_cta(Params& p, int chunks8, int most, int resident, int& groups) {
+    int best = 0, ctas = 0;
+    for (int stages = kMaxStages; stages >= 1 && best == 0; --stages) {
+        // (named barriers number the groups of more than a warp: 15 at most)
+        for (int g = 1; g * p.T <= most && (g <= 15 || p.T == 32); g *= 2) {
+            const int64_t bytes = smem_for(p, chunks8, g, stages);
+            if (bytes > kSmemPerCta) continue;
+            int64_t n = kSmemPerSm / (bytes + 1024);
+            if (n > resident / (g * p.T)) n = resident / (g * p.T);
+            if (n > 0 && n * g > best) {
+                best = static_cast<int>(n * g);
+                ctas = static_cast<int>(n);
+                groups = g;
+                p.stages = stages;
+            }
+        }
+    }
+    return ctas;
 }
 
 gemm_status_t status_of(cudaError_t e) {
@@ -193,19 +221,30 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     p.ldy = ldy;
     p.vec = N % 8 == 0 && vector16(X, ldx, x_dtype) && vector16(Z, ldz, z_dtype) &&
             vector16(XO, ldxo, x_dtype) && vector16(Y, ldy, z_dtype);
-    l.chunks8 = N > 8192 ? 2 : (M <= sms || N <= 256) ? 1 : 2;
-    p.T = threads_for(N, l.chunks8);
-    l.threads = p.T < kRowsPerCtaThreads ? kRowsPerCtaThreads : p.T;
-    const int groups = l.threads / p.T;
-    int64_t grid = ceil_div(M, groups);
-    const int64_t per_sm = 1024 / l.threads;              // resident CTAs
-    if (grid > sms * per_sm) grid = sms * per_sm;
-    const int64_t rows_each = ceil_div(M, grid * groups);
+    p.token_gate = Z && block->gate && block->gate_rows == 1 ? 1 : 0;
+    p.i_ws = p.i_bs = p.i_wpre = p.i_bpre = -1;
+    if (Z) p.i_ws = p.n_par++;
+    if (Z && block->post_bias) p.i_bs = p.n_par++;
+    if (Y) p.i_wpre = p.n_par++;
+    if (Y && block->pre_bias) p.i_bpre = p.n_par++;
+    // 16 elements per thread where rows are many, 8 where they are few (one
+    // row's latency counts) or narrow
+    l.chunks8 = N > kMaxColumnsPerCta ? 2 : (M <= sms || N <= 1024) ? 1 : 2;
+    p.cluster = N > kMaxColumnsPerCta ? 2 : 1;
+    p.T = threads_for(N < kMaxColumnsPerCta ? N : kMaxColumnsPerCta, l.chunks8);
     p.slot_bytes = static_cast<uint32_t>(l.chunks8 * 8 * p.T * (esize(x_dtype) + (Z ? esize(z_dtype) : 0)));
-    p.stages = stages_for(p.slot_bytes, groups, kSmemPerCta / per_sm);
-    if (p.stages > rows_each) p.stages = static_cast<int32_t>(rows_each);
-    l.grid = static_cast<int>(grid);
-    l.smem = static_cast<size_t>(groups) * (p.T / 32 * 32 + p.stages * static_cast<size_t>(p.slot_bytes));
+    int groups = 1;
+    // 64 registers per thread
+    const int ctas = choose_cta(p, l.chunks8, p.T > 512 ? p.T : 512, 1024, groups);
+    if (ctas == 0) return GEMM_ERR_NOT_SUPPORTED;
+    const Chunks ch = chunks_for(M, Z && block->gate ? block->gate_rows : 1,
+                                 static_cast<int64_t>(sms) * ctas / p.cluster);
+    set_chunks(p, ch);
+    // no more groups than a chunk has rows
+    while (groups > 1 && groups / 2 >= ch.rows) groups /= 2;
+    l.threads = groups * p.T;
+    l.grid = static_cast<int>(ch.groups * ch.per_group * p.cluster);
+    l.smem = static_cast<size_t>(smem_for(p, l.chunks8, groups, p.stages));
     l.stream = reinterpret_cast<cudaStream_t>(stream);
     return status_of(run_forward(x_dtype, z_dtype, l));
 }
@@ -279,11 +318,14 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
     p.lddz = lddz;
     p.vec = N % 8 == 0 && vector16(XO, ldxo, x_dtype) && vector16(Z, ldz, z_dtype) &&
             vector16(dY, lddy, z_dtype) && vector16(dXO, lddxo, x_dtype) &&
-            vector16(dX, lddx, x_dtype) && vector16(dZ, lddz, z_dtype);
+            vector16(dX, lddx, x_dtype) && vector16(dZ, lddz, z_dtype) &&
+            (!token || vector16(gr.d_gate, N, gr.grad_dtype));
     p.token_gate = token ? 1 : 0;
-    p.chunk_group_rows = ch.group_rows;
-    p.chunks_per_group = static_cast<int32_t>(ch.per_group);
-    p.chunk_rows = ch.rows;
+    set_chunks(p, ch);
+    p.i_ws = p.i_bs = p.i_wpre = p.i_bpre = -1;
+    if (Z) p.i_ws = p.n_par++;
+    if (dY) p.i_wpre = p.n_par++;
+    if (token && gr.d_gate && block->post_bias) p.i_bs = p.n_par++;
     p.partials = sums ? static_cast<float*>(workspace) : nullptr;
     p.part_stride = chunks * N;
     p.dgate = token ? gr.d_gate : nullptr;
@@ -294,17 +336,18 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
         l.chunks8 = N > 2048 ? 2 : 1;
         p.cluster = N > kMaxColumnsPerCta ? 2 : 1;
         p.T = threads_for(N < kMaxColumnsPerCta ? N : kMaxColumnsPerCta, l.chunks8);
-        l.threads = p.T < kRowsPerCtaThreads ? kRowsPerCtaThreads : p.T;
-        const int groups = l.threads / p.T;
         p.slot_bytes = static_cast<uint32_t>(
             l.chunks8 * 8 * p.T *
             (esize(x_dtype) * (dXO ? 2 : 1) + (Z ? esize(z_dtype) : 0) + (dY ? esize(z_dtype) : 0)));
-        const int64_t per_sm = l.threads == 256 ? 2 : 1;
-        p.stages = stages_for(p.slot_bytes, groups, kSmemPerCta / per_sm);
+        int groups = 1;
+        if (choose_cta(p, l.chunks8, kBackThreads, kBackThreads, groups) == 0) return GEMM_ERR_NOT_SUPPORTED;
+        while (groups > 1 && groups / 2 >= ch.rows) groups /= 2;
+        l.threads = groups * p.T;
+        l.smem = static_cast<size_t>(smem_for(p, l.chunks8, groups, p.stages));
         // the groups' column sums pass through the ring's memory
-        const size_t ring = static_cast<size_t>(groups) * p.stages * p.slot_bytes;
-        const size_t line = static_cast<size_t>(p.T) * l.chunks8 * 8 * 4;
-        l.smem = static_cast<size_t>(groups) * (p.T / 32 * 32) + (ring > line ? ring : line);
+        const size_t line = static_cast<size_t>(smem_for(p, l.chunks8, groups, 0)) +
+                            static_cast<size_t>(p.T) * l.chunks8 * 32;
+        if (l.smem < line) l.smem = line;
         if (l.smem > static_cast<size_t>(kSmemPerCta)) return GEMM_ERR_NOT_SUPPORTED;
         l.grid = static_cast<int>(chunks * p.cluster);
         l.stream = s;

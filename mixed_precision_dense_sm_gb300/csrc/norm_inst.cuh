@@ -40,40 +40,57 @@ static cudaError_t launch_kernel(K kern, const Launch& l, std::mutex& mu, size_t
     return cudaLaunchKernelEx(&cfg, kern, l.p);
 }
 
-template <int C, bool VEC>
+template <int TT, int C, bool VEC>
 static cudaError_t forward_c(const Launch& l) {
     static std::mutex mu;
     static size_t raised_to = 0;
-    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, C, VEC>, l, mu, raised_to);
+    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, TT, C, VEC>, l, mu, raised_to);
 }
 
-template <int C, bool VEC, bool BIAS, int THREADS>
+template <int TT, int C, bool VEC, bool BIAS>
 static cudaError_t backward_c(const Launch& l) {
     static std::mutex mu;
     static size_t raised_to = 0;
-    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, C, VEC, BIAS, THREADS>, l, mu, raised_to);
+    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, BIAS>, l, mu, raised_to);
 }
 
+// Rows of vectors have the threads per row compiled in for the common widths;
+// the others share one kernel per C.
 cudaError_t NORM_CAT(forward_, NORM_SUFFIX)(const Launch& l) {
-    if (l.p.vec) return l.chunks8 == 1 ? forward_c<1, true>(l) : forward_c<2, true>(l);
-    return l.chunks8 == 1 ? forward_c<1, false>(l) : forward_c<2, false>(l);
+    if (!l.p.vec) return l.chunks8 == 1 ? forward_c<0, 1, false>(l) : forward_c<0, 2, false>(l);
+    if (l.chunks8 == 1) {
+        switch (l.p.T) {
+            case 32: return forward_c<32, 1, true>(l);
+            case 128: return forward_c<128, 1, true>(l);
+            default: return forward_c<0, 1, true>(l);
+        }
+    }
+    switch (l.p.T) {
+        case 256: return forward_c<256, 2, true>(l);
+        default: return forward_c<0, 2, true>(l);
+    }
 }
 
-template <bool VEC, bool BIAS>
-static cudaError_t backward_b(const Launch& l) {
-    switch (l.threads) {
-        case 256:
-            return l.chunks8 == 1 ? backward_c<1, VEC, BIAS, 256>(l) : backward_c<2, VEC, BIAS, 256>(l);
-        case 512: return backward_c<2, VEC, BIAS, 512>(l);
-        default: return cudaErrorInvalidValue;
+template <bool BIAS>
+static cudaError_t backward_v(const Launch& l) {
+    if (l.chunks8 == 1) {
+        switch (l.p.T) {
+            case 32: return backward_c<32, 1, true, BIAS>(l);
+            case 128: return backward_c<128, 1, true, BIAS>(l);
+            default: return backward_c<0, 1, true, BIAS>(l);
+        }
+    }
+    switch (l.p.T) {
+        case 256: return backward_c<256, 2, true, BIAS>(l);
+        default: return backward_c<512, 2, true, BIAS>(l);
     }
 }
 
 // Rows that are not vectors take the kernel with all four sums (fewer kernels;
 // the two that are not wanted are not added up).
 cudaError_t NORM_CAT(backward_, NORM_SUFFIX)(const Launch& l) {
-    if (!l.p.vec) return backward_b<false, true>(l);
-    return l.bias ? backward_b<true, true>(l) : backward_b<true, false>(l);
+    if (!l.p.vec) return l.chunks8 == 1 ? backward_c<0, 1, false, true>(l) : backward_c<0, 2, false, true>(l);
+    return l.bias ? backward_v<true>(l) : backward_v<false>(l);
 }
 
 }  // namespace nrm

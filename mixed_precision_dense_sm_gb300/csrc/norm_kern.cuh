@@ -5,11 +5,14 @@
 // Both row kernels are bound by HBM: each matrix element is read once and
 // written once.  A row belongs to a group of T threads of a CTA (a warp for
 // narrow rows, the whole CTA for wide ones); each thread owns C chunks of 8
-// elements.  A thread copies its own elements of the next rows to shared
+// elements.  A thread copies its own elements of the next row to shared
 // memory with cp.async while the group works on the current one, into a ring
 // of slots that only this thread reads: no barrier guards the copies, and no
 // registers hold loads in flight.  What the group shares are the sums of a
-// row: a butterfly in each warp, one shared-memory exchange, one barrier.
+// row: a butterfly in each warp, one shared-memory exchange, one barrier.  A
+// CTA takes a chunk of consecutive rows that see the same row of the gate, so
+// the weights, the gate and the scale fold into vectors that it converts to
+// FP32 in shared memory once.
 //
 // Rows that are not 16-byte aligned, or N not a multiple of 8, go element by
 // element: a thread's 8 elements are then 32 apart, so a warp's accesses stay
@@ -26,6 +29,7 @@ namespace nrm {
 
 enum : int { kNone = 0, kRms = 1, kLayer = 2 };
 constexpr int kMaxStages = 2;
+constexpr int kBackThreads = 512;    // of a backward CTA: 128 registers each, one CTA per SM
 
 struct Params {
     // forward: X, Z in, XO, Y out; backward: X = XO, Z, dY, dXO in, dX, dZ out
@@ -38,7 +42,7 @@ struct Params {
     void* dX; int64_t lddx;
     void* dZ; int64_t lddz;
     const void* wpre; const void* bpre; const void* wpost; const void* bpost;
-    const void* gate; int64_t ld_gate; int64_t gate_rows;
+    const void* gate; int64_t ld_gate;
     int32_t vec_dtype;
     int32_t vec_aligned;        // weights, biases and gate rows are 16-byte aligned
     int32_t vec;                // rows are 16-byte aligned and N a multiple of 8
@@ -49,13 +53,18 @@ struct Params {
     int32_t T;                  // threads per row
     int32_t stages;             // slots of the ring
     uint32_t slot_bytes;        // of one row of one group
-    // backward: rows are cut into chunks, one CTA each, that lie in one group
+    // Row-invariant vectors, kept in shared memory as FP32 (their numbers
+    // there, -1 where absent): ws multiplies the post-norm (scale gate wpost,
+    // or wpost for token gates), bs is added to it (scale gate bpost, or bpost)
+    int32_t i_ws, i_bs, i_wpre, i_bpre, n_par;
+    // rows are cut into chunks, one CTA (or pair) each, that lie in one group
     // of the gate (token gates, gate_rows == 1, count as one group)
     int64_t chunk_group_rows;   // rows of a gate group (M where rows do not share one)
     int32_t chunks_per_group;
     int64_t chunk_rows;
     int32_t token_gate;         // the gate's row changes with every row
     int32_t cluster;            // CTAs that share a row (1 or 2), each half its columns
+    // backward
     float* partials;            // [4][chunks][N]: sums of dY xhat, q zhat, dY, q (the last two: BIAS)
     int64_t part_stride;        // chunks * N
     void* dgate;                // written directly for token gates
@@ -371,45 +380,51 @@ __device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, F8& v) {
     }
 }
 
-// The group of threads that shares a row: T threads of the CTA, `warps` warps.
+// The group of threads that shares a row: T threads of the CTA (a compile-time
+// number for TT > 0).
+template <int TT>
 struct Group {
-    int T, t, index, warps;     // threads, this thread's number, the group's number
+    int T_, t, index;           // threads, this thread's number, the group's number
     float* red;                 // [2][4][warps] exchange buffer of this group
     int parity;
     float* pair;                // [2][2][4] exchange buffer of a CTA pair, or NULL
     uint32_t rank;              // this CTA's number in the pair
+    __device__ __forceinline__ int T() const { return TT > 0 ? TT : T_; }
+    __device__ __forceinline__ int warps() const { return T() >> 5; }
 };
 
-__device__ __forceinline__ void group_barrier(const Group& g) {
-    asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.T) : "memory");
+template <int TT>
+__device__ __forceinline__ void group_barrier(const Group<TT>& g) {
+    asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.T()) : "memory");
 }
 
 // Sums of K values over the group, in the same order on every run; every
 // thread gets them.  One barrier: consecutive sums use alternate buffers.
-template <int K>
-__device__ __forceinline__ void group_sum(Group& g, float (&v)[K]) {
+template <int K, int TT>
+__device__ __forceinline__ void group_sum(Group<TT>& g, float (&v)[K]) {
     static_assert(K <= 4, "exchange buffer");
     #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         #pragma unroll
         for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
     }
-    if (g.T == 32) return;
-    float* r = g.red + g.parity * g.warps * 4;
+    if (g.T() == 32) return;
+    float* r = g.red + g.parity * g.warps() * 4;
     g.parity ^= 1;
     if ((threadIdx.x & 31) == 0) {
         #pragma unroll
-        for (int k = 0; k < K; ++k) r[k * g.warps + (g.t >> 5)] = v[k];
+        for (int k = 0; k < K; ++k) r[k * g.warps() + (g.t >> 5)] = v[k];
     }
     group_barrier(g);
     #pragma unroll
     for (int k = 0; k < K; ++k) {
-        const float* q = r + k * g.warps;
-        if (g.warps == 2) {
+        const float* q = r + k * g.warps();
+        if (g.warps() == 2) {
             v[k] = q[0] + q[1];
         } else {
             v[k] = 0.0f;
-            for (int w = 0; w < g.warps; w += 4) {      // a power of two, 4 at least
+            #pragma unroll
+            for (int w = 0; w < g.warps(); w += 4) {    // a power of two, 4 at least
                 const float4 x = *reinterpret_cast<const float4*>(q + w);
                 v[k] += (x.x + x.y) + (x.z + x.w);
             }
@@ -435,165 +450,18 @@ __device__ __forceinline__ void group_sum(Group& g, float (&v)[K]) {
     for (int k = 0; k < K; ++k) v[k] = y[k] + y[4 + k];
 }
 
-__device__ __forceinline__ Group make_group(const Params& p, uint8_t* smem) {
-    Group g;
-    g.T = p.T;
-    g.index = static_cast<int>(threadIdx.x) / p.T;
-    g.t = static_cast<int>(threadIdx.x) - g.index * p.T;
-    g.warps = p.T >> 5;
-    g.red = reinterpret_cast<float*>(smem) + g.index * (2 * 4 * g.warps);
+template <int TT>
+__device__ __forceinline__ Group<TT> make_group(const Params& p, uint8_t* smem) {
+    Group<TT> g;
+    g.T_ = p.T;
+    g.index = static_cast<int>(threadIdx.x) / g.T();
+    g.t = static_cast<int>(threadIdx.x) - g.index * g.T();
+    g.red = reinterpret_cast<float*>(smem) + g.index * (2 * 4 * g.warps());
     g.parity = 0;
     g.pair = nullptr;
     g.rank = 0;
     return g;
 }
-
-// ------------------------------------------------------------------- forward
-
-// Mean and 1 / size of a row whose chunks are in v; v becomes v - mean.
-template <int C, bool VEC>
-__device__ __forceinline__ float norm_stats(Group& g, const Params& p, int kind, F8 (&v)[C]) {
-    if (kind == kNone) return 1.0f;
-    if (kind == kLayer) {
-        F2 a = mk2(0.0f);
-        #pragma unroll
-        for (int c = 0; c < C; ++c)
-            if (spot_of<VEC>(g.T, g.t, c).some(p.N)) {
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) a = add2(a, v[c][q]);
-            }
-        float s[1] = {sum2(a)};
-        group_sum(g, s);
-        const float mean = s[0] * p.inv_n;
-        #pragma unroll
-        for (int c = 0; c < C; ++c) center8<VEC>(v[c], mean, spot_of<VEC>(g.T, g.t, c), p.N);
-    }
-    F2 a = mk2(0.0f);
-    #pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (spot_of<VEC>(g.T, g.t, c).some(p.N)) {
-            #pragma unroll
-            for (int q = 0; q < 4; ++q) a = fma2(v[c][q], v[c][q], a);
-        }
-    float s[1] = {sum2(a)};
-    group_sum(g, s);
-    return 1.0f / sqrtf(fmaf(s[0], p.inv_n, p.eps));
-}
-
-// Rows go to groups round robin over the grid.
-template <typename XT, typename ZT, int C, bool VEC>
-__global__ void __launch_bounds__(1024)
-    forward_kernel(const __grid_constant__ Params p) {
-    extern __shared__ __align__(16) uint8_t smem[];
-    Group g = make_group(p, smem);
-    const int groups = static_cast<int>(blockDim.x) / p.T;
-    uint8_t* ring = smem + groups * g.warps * 32 +
-                    static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
-    const uint32_t x_bytes = static_cast<uint32_t>(C) * 8u * sizeof(XT) * p.T;
-    const bool has_z = p.Z != nullptr;
-    const bool wide = p.vec_aligned != 0;
-    const int32_t N = p.N;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + g.index;
-    zero_ring<VEC>(ring, p.stages * p.slot_bytes, g.T, g.t);
-    grid_dependency_wait();
-    grid_dependents_launch();
-
-    auto fetch = [&](int64_t row, int slot) {
-        if (row < p.M) {
-            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
-            #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-                fetch8<XT, VEC>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
-                if (has_z)
-                    fetch8<ZT, VEC>(s + x_bytes, g.T, g.t, c,
-                                    static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
-            }
-        }
-        cp_async_commit();
-    };
-    Held<XT, VEC> hx[C];
-    Held<ZT, VEC> hz[C];
-    auto hold = [&](int64_t row) {
-        if (row >= p.M) return;
-        #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-            hold8<XT, VEC>(hx[c], static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
-            if (has_z) hold8<ZT, VEC>(hz[c], static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
-        }
-    };
-    for (int s = 0; s < p.stages - 1; ++s) fetch(first + s * step, s);
-    if constexpr (!VEC) hold(first);
-    int slot = 0;
-    for (int64_t row = first; row < p.M; row += step) {
-        if constexpr (!VEC) {
-            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
-            #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                put8<XT, VEC>(s, g.T, g.t, c, hx[c]);
-                if (has_z) put8<ZT, VEC>(s + x_bytes, g.T, g.t, c, hz[c]);
-            }
-            hold(row + step);
-        }
-        {
-            int ahead = slot + p.stages - 1;
-            if (ahead >= p.stages) ahead -= p.stages;
-            fetch(row + (p.stages - 1) * step, ahead);
-        }
-        cp_async_wait(p.stages - 1);
-        uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
-        if (++slot == p.stages) slot = 0;
-
-        F8 x[C];
-        if (has_z) {
-            F8 z[C];
-            #pragma unroll
-            for (int c = 0; c < C; ++c) take8<ZT>(s + x_bytes, g.T, g.t, c, z[c]);
-            const float r = norm_stats<C, VEC>(g, p, p.post, z);
-            const void* gate = nullptr;
-            if (p.gate != nullptr) {
-                const int64_t grow = p.gate_rows > 1 ? row / p.gate_rows : row;
-                gate = static_cast<const uint8_t*>(p.gate) + grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
-            }
-            #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-                if (!sp.some(N)) continue;
-                take8<XT>(s, g.T, g.t, c, x[c]);
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) z[c][q] = mul2(z[c][q], mk2(r));
-                scale_by<VEC>(z[c], p.wpost, p.vec_dtype, wide, sp, N);
-                shift_by<VEC>(z[c], p.bpost, p.vec_dtype, wide, sp, N);
-                scale_by<VEC>(z[c], gate, p.vec_dtype, wide, sp, N);
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) x[c][q] = fma2(mk2(p.scale), z[c][q], x[c][q]);
-                // the stream as its type holds it: what is stored is what the
-                // next norm sees
-                store8<XT, VEC, true>(static_cast<XT*>(p.XO) + row * p.ldxo, sp, N, x[c]);
-            }
-        } else {
-            #pragma unroll
-            for (int c = 0; c < C; ++c) take8<XT>(s, g.T, g.t, c, x[c]);
-        }
-        if (p.Y != nullptr) {
-            const float r = norm_stats<C, VEC>(g, p, p.pre, x);
-            #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c);
-                if (!sp.some(N)) continue;
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) x[c][q] = mul2(x[c][q], mk2(r));
-                scale_by<VEC>(x[c], p.wpre, p.vec_dtype, wide, sp, N);
-                shift_by<VEC>(x[c], p.bpre, p.vec_dtype, wide, sp, N);
-                store8<ZT, VEC>(static_cast<ZT*>(p.Y) + row * p.ldy, sp, N, x[c]);
-            }
-        }
-    }
-}
-
-// ------------------------------------------------------------------ backward
 
 // The rows of chunk `b`: [row0, row1) inside one group of the gate.
 __device__ __forceinline__ void chunk_span(const Params& p, int64_t b, int64_t& row0, int64_t& row1,
@@ -607,29 +475,115 @@ __device__ __forceinline__ void chunk_span(const Params& p, int64_t b, int64_t& 
     if (row1 > end) row1 = end;
 }
 
-// One CTA per chunk of rows (or a pair of CTAs, each with half the columns of
-// rows wider than one CTA's registers hold), its groups taking the chunk's
-// rows in turn.  Per row: the statistics of XO and Z with the sums that the
-// pre-norm's Jacobian needs (one exchange; two where a mean comes first), then
-// the post-norm's (one more); per column, in registers, the sums over the
-// chunk's rows of dY xhat, q zhat, and with BIAS dY and q, where q = dXO' (the
-// gate is constant over a chunk and joins in the sum over chunks) or, for
-// token gates, q = scale gate dXO'.  The groups' sums meet in shared memory
-// (in group order) and go to the chunk's line of partials.
-template <typename XT, typename ZT, int C, bool VEC, bool BIAS, int THREADS>
-__global__ void __launch_bounds__(THREADS)
-    backward_kernel(const __grid_constant__ Params p) {
+__device__ __forceinline__ const void* gate_row(const Params& p, int64_t row) {
+    return static_cast<const uint8_t*>(p.gate) + row * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
+}
+
+// This thread's part of vector k in shared memory: as a slot of FP32 elements.
+template <int C>
+__device__ __forceinline__ uint8_t* par_at(uint8_t* par, int k, int T) {
+    return par + static_cast<uint32_t>(k) * (C * 32u) * T;
+}
+
+// Fills the vectors in shared memory; every group reads them, the group
+// numbered 0 writes them.
+template <int C, bool VEC, int TT>
+__device__ __forceinline__ void fill_vectors(const Params& p, const Group<TT>& g, uint8_t* par,
+                                             int64_t group, int32_t col0) {
+    if (g.index == 0) {
+        const bool wide = p.vec_aligned != 0;
+        #pragma unroll 1
+        for (int c = 0; c < C; ++c) {
+            const Spot<VEC> sp = spot_of<VEC>(g.T(), g.t, c, col0);
+            if (!sp.some(p.N)) continue;
+            auto put = [&](int k, const F8& v) {
+                uint8_t* d = slot_at<float>(par_at<C>(par, k, g.T()), g.T(), g.t, c);
+                *reinterpret_cast<ulonglong2*>(d) = make_ulonglong2(v[0].v, v[1].v);
+                *reinterpret_cast<ulonglong2*>(d + g.T() * 16) = make_ulonglong2(v[2].v, v[3].v);
+            };
+            F8 gs, v;                               // scale * gate
+            set8(gs, p.token_gate ? 1.0f : p.scale);
+            if (p.gate != nullptr && !p.token_gate)
+                scale_by<VEC>(gs, gate_row(p, group), p.vec_dtype, wide, sp, p.N);
+            if (p.i_ws >= 0) {
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = gs[q];
+                scale_by<VEC>(v, p.wpost, p.vec_dtype, wide, sp, p.N);
+                put(p.i_ws, v);
+            }
+            if (p.i_bs >= 0) {
+                load_param8<VEC>(p.bpost, p.vec_dtype, wide, sp, p.N, v);
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = mul2(v[q], gs[q]);
+                put(p.i_bs, v);
+            }
+            if (p.i_wpre >= 0) {
+                set8(v, 1.0f);
+                scale_by<VEC>(v, p.wpre, p.vec_dtype, wide, sp, p.N);
+                put(p.i_wpre, v);
+            }
+            if (p.i_bpre >= 0) {
+                load_param8<VEC>(p.bpre, p.vec_dtype, wide, sp, p.N, v);
+                put(p.i_bpre, v);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// 1 / sqrt(mean + eps): the hardware's approximation and one Newton step.
+__device__ __forceinline__ float inv_size(float sum, const Params& p) {
+    const float a = fmaf(sum, p.inv_n, p.eps);
+    const float r = rsqrtf(a);
+    return a < 3e38f ? r * fmaf(-0.5f * a * r, r, 1.5f) : r;     // (0 for infinity)
+}
+
+// ------------------------------------------------------------------- forward
+
+// 1 / size of a row whose chunks are in v; v becomes v - mean for LayerNorm.
+template <int C, bool VEC, int TT>
+__device__ __forceinline__ float norm_stats(Group<TT>& g, const Params& p, int kind, int32_t col0,
+                                            F8 (&v)[C]) {
+    if (kind == kNone) return 1.0f;
+    if (kind == kLayer) {
+        F2 a = mk2(0.0f);
+        #pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (spot_of<VEC>(g.T(), g.t, c, col0).some(p.N)) {
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) a = add2(a, v[c][q]);
+            }
+        float s[1] = {sum2(a)};
+        group_sum(g, s);
+        const float mean = s[0] * p.inv_n;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) center8<VEC>(v[c], mean, spot_of<VEC>(g.T(), g.t, c, col0), p.N);
+    }
+    F2 a = mk2(0.0f);
+    #pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (spot_of<VEC>(g.T(), g.t, c, col0).some(p.N)) {
+            #pragma unroll
+            for (int q = 0; q < 4; ++q) a = fma2(v[c][q], v[c][q], a);
+        }
+    float s[1] = {sum2(a)};
+    group_sum(g, s);
+    return inv_size(s[0], p);
+}
+
+// One CTA (or a pair, for rows wider than kMaxColumnsPerCta) per chunk of rows,
+// its groups taking the rows in turn.
+template <typename XT, typename ZT, int TT, int C, bool VEC>
+__global__ void __launch_bounds__(1024)
+    forward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    Group g = make_group(p, smem);
-    const int groups = static_cast<int>(blockDim.x) / p.T;
-    uint8_t* rings = smem + groups * g.warps * 32;
-    uint8_t* ring = rings + static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
-    // a slot: [XO][dXO][Z][dY], the absent ones left out
-    const uint32_t xb = static_cast<uint32_t>(C) * 8u * sizeof(XT) * p.T;
-    const uint32_t zb = static_cast<uint32_t>(C) * 8u * sizeof(ZT) * p.T;
-    const bool has_z = p.Z != nullptr, has_dy = p.dY != nullptr, has_dxo = p.dXO != nullptr;
-    const uint32_t o_dxo = xb, o_z = o_dxo + (has_dxo ? xb : 0u), o_dy = o_z + (has_z ? zb : 0u);
-    const bool wide = p.vec_aligned != 0;
+    Group<TT> g = make_group<TT>(p, smem);
+    const int T = g.T(), t = g.t;
+    const int groups = static_cast<int>(blockDim.x) / T;
+    uint8_t* par = smem + groups * g.warps() * 32;
+    uint8_t* ring = par_at<C>(par, p.n_par, T) + static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
+    const uint32_t x_bytes = static_cast<uint32_t>(C) * 8u * sizeof(XT) * T;
+    const bool has_z = p.Z != nullptr;
     const int32_t N = p.N;
     __shared__ float pair[16];
     int32_t col0 = 0;
@@ -637,12 +591,12 @@ __global__ void __launch_bounds__(THREADS)
     if (p.cluster == 2) {
         g.rank = cluster_ctarank();
         g.pair = pair;
-        col0 = static_cast<int32_t>(g.rank) * p.T * C * 8;
+        col0 = static_cast<int32_t>(g.rank) * T * C * 8;
         chunk >>= 1;
     }
     int64_t row0, row1, group;
     chunk_span(p, chunk, row0, row1, group);
-    zero_ring<VEC>(ring, p.stages * p.slot_bytes, g.T, g.t);
+    zero_ring<VEC>(ring, p.stages * p.slot_bytes, T, t);
     if (p.cluster == 2) cluster_sync_all();     // the other CTA's shared memory is there
     grid_dependency_wait();
     grid_dependents_launch();
@@ -652,16 +606,164 @@ __global__ void __launch_bounds__(THREADS)
             uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
-                fetch8<XT, VEC>(s, g.T, g.t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
+                fetch8<XT, VEC>(s, T, t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+                if (has_z)
+                    fetch8<ZT, VEC>(s + x_bytes, T, t, c,
+                                    static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+            }
+        }
+        cp_async_commit();
+    };
+    Held<XT, VEC> hx[C];
+    Held<ZT, VEC> hz[C];
+    auto hold = [&](int64_t row) {
+        if (row >= row1) return;
+        #pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
+            hold8<XT, VEC>(hx[c], static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
+            if (has_z) hold8<ZT, VEC>(hz[c], static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
+        }
+    };
+    const int64_t first = row0 + g.index;
+    for (int s = 0; s < p.stages - 1; ++s) fetch(first + static_cast<int64_t>(s) * groups, s);
+    if constexpr (!VEC) hold(first);
+    fill_vectors<C, VEC>(p, g, par, group, col0);
+    int slot = 0;
+    for (int64_t row = first; row < row1; row += groups) {
+        if constexpr (!VEC) {
+            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                put8<XT, VEC>(s, T, t, c, hx[c]);
+                if (has_z) put8<ZT, VEC>(s + x_bytes, T, t, c, hz[c]);
+            }
+            hold(row + groups);
+        }
+        {
+            int ahead = slot + p.stages - 1;
+            if (ahead >= p.stages) ahead -= p.stages;
+            fetch(row + static_cast<int64_t>(p.stages - 1) * groups, ahead);
+        }
+        cp_async_wait(p.stages - 1);
+        uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+        if (++slot == p.stages) slot = 0;
+
+        F8 x[C];
+        if (has_z) {
+            F8 z[C];
+            #pragma unroll
+            for (int c = 0; c < C; ++c) take8<ZT>(s + x_bytes, T, t, c, z[c]);
+            const F2 r = mk2(norm_stats<C, VEC>(g, p, p.post, col0, z));
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
+                if (!sp.some(N)) continue;
+                F8 w;
+                take8<XT>(s, T, t, c, x[c]);
+                take8<float>(par_at<C>(par, p.i_ws, T), T, t, c, w);
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) z[c][q] = mul2(mul2(z[c][q], r), w[q]);
+                if (p.i_bs >= 0) {
+                    take8<float>(par_at<C>(par, p.i_bs, T), T, t, c, w);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) z[c][q] = add2(z[c][q], w[q]);
+                }
+                if (p.token_gate) {
+                    load_param8<VEC>(gate_row(p, row), p.vec_dtype, p.vec_aligned != 0, sp, N, w);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) z[c][q] = mul2(z[c][q], mul2(w[q], mk2(p.scale)));
+                }
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) x[c][q] = add2(x[c][q], z[c][q]);
+                // the stream as its type holds it: what is stored is what the
+                // next norm sees
+                store8<XT, VEC, true>(static_cast<XT*>(p.XO) + row * p.ldxo, sp, N, x[c]);
+            }
+        } else {
+            #pragma unroll
+            for (int c = 0; c < C; ++c) take8<XT>(s, T, t, c, x[c]);
+        }
+        if (p.Y != nullptr) {
+            const F2 r = mk2(norm_stats<C, VEC>(g, p, p.pre, col0, x));
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
+                if (!sp.some(N)) continue;
+                F8 w;
+                take8<float>(par_at<C>(par, p.i_wpre, T), T, t, c, w);
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) x[c][q] = mul2(mul2(x[c][q], r), w[q]);
+                if (p.i_bpre >= 0) {
+                    take8<float>(par_at<C>(par, p.i_bpre, T), T, t, c, w);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) x[c][q] = add2(x[c][q], w[q]);
+                }
+                store8<ZT, VEC>(static_cast<ZT*>(p.Y) + row * p.ldy, sp, N, x[c]);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ backward
+
+// One CTA per chunk of rows (or a pair of CTAs, each with half the columns of
+// rows wider than one CTA's registers hold), its groups taking the chunk's
+// rows in turn.  Per row: the statistics of XO and Z with the sums that the
+// pre-norm's Jacobian needs (one exchange; two where a mean comes first), then
+// the post-norm's (one more); per column, in registers, the sums over the
+// chunk's rows of dY xhat, q zhat, and with BIAS dY and q, where q = dXO' (the
+// gate is constant over a chunk and joins in the sum over chunks) or, for
+// token gates, q = scale gate dXO'.  The groups' sums meet in shared memory
+// (in group order) and go to the chunk's line of partials.
+template <typename XT, typename ZT, int TT, int C, bool VEC, bool BIAS>
+__global__ void __launch_bounds__(kBackThreads)
+    backward_kernel(const __grid_constant__ Params p) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    Group<TT> g = make_group<TT>(p, smem);
+    const int T = g.T(), t = g.t;
+    const int groups = static_cast<int>(blockDim.x) / T;
+    uint8_t* par = smem + groups * g.warps() * 32;
+    uint8_t* rings = par_at<C>(par, p.n_par, T);
+    uint8_t* ring = rings + static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
+    // a slot: [XO][dXO][Z][dY], the absent ones left out
+    const uint32_t xb = static_cast<uint32_t>(C) * 8u * sizeof(XT) * T;
+    const uint32_t zb = static_cast<uint32_t>(C) * 8u * sizeof(ZT) * T;
+    const bool has_z = p.Z != nullptr, has_dy = p.dY != nullptr, has_dxo = p.dXO != nullptr;
+    const uint32_t o_dxo = xb, o_z = o_dxo + (has_dxo ? xb : 0u), o_dy = o_z + (has_z ? zb : 0u);
+    const int32_t N = p.N;
+    __shared__ float pair[16];
+    int32_t col0 = 0;
+    int64_t chunk = blockIdx.x;
+    if (p.cluster == 2) {
+        g.rank = cluster_ctarank();
+        g.pair = pair;
+        col0 = static_cast<int32_t>(g.rank) * T * C * 8;
+        chunk >>= 1;
+    }
+    int64_t row0, row1, group;
+    chunk_span(p, chunk, row0, row1, group);
+    zero_ring<VEC>(ring, p.stages * p.slot_bytes, T, t);
+    if (p.cluster == 2) cluster_sync_all();     // the other CTA's shared memory is there
+    grid_dependency_wait();
+    grid_dependents_launch();
+
+    auto fetch = [&](int64_t row, int slot) {
+        if (row < row1) {
+            uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
+            #pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
+                fetch8<XT, VEC>(s, T, t, c, static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
                 if (has_dxo)
-                    fetch8<XT, VEC>(s + o_dxo, g.T, g.t, c,
+                    fetch8<XT, VEC>(s + o_dxo, T, t, c,
                                     static_cast<const XT*>(p.dXO) + row * p.lddxo, sp, N);
                 if (has_z)
-                    fetch8<ZT, VEC>(s + o_z, g.T, g.t, c,
+                    fetch8<ZT, VEC>(s + o_z, T, t, c,
                                     static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
                 if (has_dy)
-                    fetch8<ZT, VEC>(s + o_dy, g.T, g.t, c,
+                    fetch8<ZT, VEC>(s + o_dy, T, t, c,
                                     static_cast<const ZT*>(p.dY) + row * p.lddy, sp, N);
             }
         }
@@ -673,7 +775,7 @@ __global__ void __launch_bounds__(THREADS)
         if (row >= row1) return;
         #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+            const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
             hold8<XT, VEC>(hx[c], static_cast<const XT*>(p.X) + row * p.ldx, sp, N);
             if (has_dxo) hold8<XT, VEC>(hd[c], static_cast<const XT*>(p.dXO) + row * p.lddxo, sp, N);
             if (has_z) hold8<ZT, VEC>(hz[c], static_cast<const ZT*>(p.Z) + row * p.ldz, sp, N);
@@ -695,16 +797,17 @@ __global__ void __launch_bounds__(THREADS)
 
     for (int s = 0; s < p.stages - 1; ++s) fetch(row0 + g.index + static_cast<int64_t>(s) * groups, s);
     if constexpr (!VEC) hold(row0 + g.index);
+    fill_vectors<C, VEC>(p, g, par, group, col0);
     int slot = 0;
     for (int64_t row = row0 + g.index; row < row1; row += groups) {
         if constexpr (!VEC) {
             uint8_t* s = ring + static_cast<uint32_t>(slot) * p.slot_bytes;
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                put8<XT, VEC>(s, g.T, g.t, c, hx[c]);
-                if (has_dxo) put8<XT, VEC>(s + o_dxo, g.T, g.t, c, hd[c]);
-                if (has_z) put8<ZT, VEC>(s + o_z, g.T, g.t, c, hz[c]);
-                if (has_dy) put8<ZT, VEC>(s + o_dy, g.T, g.t, c, hy[c]);
+                put8<XT, VEC>(s, T, t, c, hx[c]);
+                if (has_dxo) put8<XT, VEC>(s + o_dxo, T, t, c, hd[c]);
+                if (has_z) put8<ZT, VEC>(s + o_z, T, t, c, hz[c]);
+                if (has_dy) put8<ZT, VEC>(s + o_dy, T, t, c, hy[c]);
             }
             hold(row + groups);
         }
@@ -723,20 +826,21 @@ __global__ void __launch_bounds__(THREADS)
             F2 sx = mk2(0.0f), sg = mk2(0.0f), sz = mk2(0.0f);
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
                 if (!sp.some(N)) continue;
                 F8 b;
                 if (pre_layer && has_dy) {
-                    take8<XT>(s, g.T, g.t, c, b);
+                    take8<XT>(s, T, t, c, b);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) sx = add2(sx, b[q]);
-                    take8<ZT>(s + o_dy, g.T, g.t, c, b);
-                    scale_by<VEC>(b, p.wpre, p.vec_dtype, wide, sp, N);
+                    take8<ZT>(s + o_dy, T, t, c, b);
+                    F8 w;
+                    take8<float>(par_at<C>(par, p.i_wpre, T), T, t, c, w);
                     #pragma unroll
-                    for (int q = 0; q < 4; ++q) sg = add2(sg, b[q]);
+                    for (int q = 0; q < 4; ++q) sg = fma2(b[q], w[q], sg);
                 }
                 if (has_z && post_layer) {
-                    take8<ZT>(s + o_z, g.T, g.t, c, b);
+                    take8<ZT>(s + o_z, T, t, c, b);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) sz = add2(sz, b[q]);
                 }
@@ -753,22 +857,23 @@ __global__ void __launch_bounds__(THREADS)
             F2 sx = mk2(0.0f), sg = mk2(0.0f), sz = mk2(0.0f);
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
                 if (!sp.some(N)) continue;
                 F8 b, x;
                 if (has_dy && p.pre != kNone) {
-                    take8<XT>(s, g.T, g.t, c, x);
+                    take8<XT>(s, T, t, c, x);
                     if (pre_layer) center8<VEC>(x, mx, sp, N);
-                    take8<ZT>(s + o_dy, g.T, g.t, c, b);
-                    scale_by<VEC>(b, p.wpre, p.vec_dtype, wide, sp, N);
+                    take8<ZT>(s + o_dy, T, t, c, b);
+                    F8 w;
+                    take8<float>(par_at<C>(par, p.i_wpre, T), T, t, c, w);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         sx = fma2(x[q], x[q], sx);
-                        sg = fma2(b[q], x[q], sg);
+                        sg = fma2(mul2(b[q], w[q]), x[q], sg);
                     }
                 }
                 if (has_z && p.post != kNone) {
-                    take8<ZT>(s + o_z, g.T, g.t, c, b);
+                    take8<ZT>(s + o_z, T, t, c, b);
                     if (post_layer) center8<VEC>(b, mz, sp, N);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) sz = fma2(b[q], b[q], sz);
@@ -777,29 +882,26 @@ __global__ void __launch_bounds__(THREADS)
             float v[3] = {sum2(sx), sum2(sg), sum2(sz)};
             group_sum(g, v);
             if (p.pre != kNone) {
-                rx = 1.0f / sqrtf(fmaf(v[0], p.inv_n, p.eps));
+                rx = inv_size(v[0], p);
                 gx = v[1] * rx * p.inv_n;
             }
-            if (p.post != kNone) rz = 1.0f / sqrtf(fmaf(v[2], p.inv_n, p.eps));
+            if (p.post != kNone) rz = inv_size(v[2], p);
         }
 
         // ---- dXO' and the column sums; the post-norm's sums
         F8 d[C];                                     // dXO', then gz = dn wpost
         F2 sgz = mk2(0.0f), sgm = mk2(0.0f);
-        const int64_t grow = p.token_gate ? row : group;
-        const void* gate = p.gate == nullptr ? nullptr
-                           : static_cast<const uint8_t*>(p.gate) +
-                                 grow * p.ld_gate * (p.vec_dtype == 2 ? 4 : 2);
         #pragma unroll
         for (int c = 0; c < C; ++c) {
-            const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+            const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
             if (!sp.some(N)) continue;
-            if (has_dxo) take8<XT>(s + o_dxo, g.T, g.t, c, d[c]);
+            if (has_dxo) take8<XT>(s + o_dxo, T, t, c, d[c]);
             else set8(d[c], 0.0f);
             if (has_dy) {
-                F8 x, b;
-                take8<XT>(s, g.T, g.t, c, x);
-                take8<ZT>(s + o_dy, g.T, g.t, c, b);
+                F8 x, b, w;
+                take8<XT>(s, T, t, c, x);
+                take8<ZT>(s + o_dy, T, t, c, b);
+                take8<float>(par_at<C>(par, p.i_wpre, T), T, t, c, w);
                 if (pre_layer) center8<VEC>(x, mx, sp, N);
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -807,55 +909,53 @@ __global__ void __launch_bounds__(THREADS)
                     a_yx[c][q] = fma2(b[q], x[q], a_yx[c][q]);
                     if constexpr (BIAS) a_y[c][q] = add2(a_y[c][q], b[q]);
                 }
-                scale_by<VEC>(b, p.wpre, p.vec_dtype, wide, sp, N);
-                if (p.pre != kNone) {
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) b[q] = fma2(x[q], mk2(-gx), b[q]);
-                    if (pre_layer) center8<VEC>(b, gsum, sp, N);
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) d[c][q] = fma2(b[q], mk2(rx), d[c][q]);
-                } else {
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) d[c][q] = add2(d[c][q], b[q]);
-                }
+                // rx (g - mean g - xhat mean(g xhat)), g = dY wpre; gx, gsum are 0
+                // and rx is 1 where there is no norm
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) b[q] = fma2(x[q], mk2(-gx), mul2(b[q], w[q]));
+                if (pre_layer) center8<VEC>(b, gsum, sp, N);
+                #pragma unroll
+                for (int q = 0; q < 4; ++q) d[c][q] = fma2(b[q], mk2(rx), d[c][q]);
             }
             if (p.dX != nullptr)
                 store8<XT, VEC>(static_cast<XT*>(p.dX) + row * p.lddx, sp, N, d[c]);
             if (has_z) {
-                F8 z;
-                take8<ZT>(s + o_z, g.T, g.t, c, z);
+                F8 z, w;
+                take8<ZT>(s + o_z, T, t, c, z);
+                take8<float>(par_at<C>(par, p.i_ws, T), T, t, c, w);
                 if (post_layer) center8<VEC>(z, mz, sp, N);
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) z[q] = mul2(z[q], mk2(rz));
-                if (p.token_gate && p.dgate != nullptr) {
-                    // scale * dXO' * n, one row of the gate per row
-                    F8 n;
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) n[q] = z[q];
-                    scale_by<VEC>(n, p.wpost, p.vec_dtype, wide, sp, N);
-                    shift_by<VEC>(n, p.bpost, p.vec_dtype, wide, sp, N);
-                    #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float lo, hi;
-                        get2(mul2(mul2(mk2(p.scale), d[c][q]), n[q]), lo, hi);
-                        if (sp.in(2 * q, N)) store_elem(p.dgate, p.grad_dtype, row * N + sp.at(2 * q), lo);
-                        if (sp.in(2 * q + 1, N)) store_elem(p.dgate, p.grad_dtype, row * N + sp.at(2 * q + 1), hi);
+                if (p.token_gate) {
+                    F8 n, gt;
+                    if (p.dgate != nullptr) {
+                        // scale * dXO' * n, one row of the gate per row
+                        #pragma unroll
+                        for (int q = 0; q < 4; ++q) n[q] = mul2(z[q], w[q]);
+                        if (p.i_bs >= 0) {
+                            F8 b;
+                            take8<float>(par_at<C>(par, p.i_bs, T), T, t, c, b);
+                            #pragma unroll
+                            for (int q = 0; q < 4; ++q) n[q] = add2(n[q], b[q]);
+                        }
+                        #pragma unroll
+                        for (int q = 0; q < 4; ++q) n[q] = mul2(mul2(mk2(p.scale), d[c][q]), n[q]);
+                        if (p.grad_dtype == 2)
+                            store8<float, VEC>(static_cast<float*>(p.dgate) + row * N, sp, N, n);
+                        else if (p.grad_dtype == 1)
+                            store8<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(p.dgate) + row * N, sp, N, n);
+                        else
+                            store8<__half, VEC>(static_cast<__half*>(p.dgate) + row * N, sp, N, n);
                     }
+                    load_param8<VEC>(gate_row(p, row), p.vec_dtype, p.vec_aligned != 0, sp, N, gt);
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) d[c][q] = mul2(d[c][q], mul2(gt[q], mk2(p.scale)));
                 }
-                F8 dn;
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) dn[q] = mul2(d[c][q], mk2(p.scale));
-                scale_by<VEC>(dn, gate, p.vec_dtype, wide, sp, N);
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const F2 v = p.token_gate ? dn[q] : d[c][q];
-                    a_qz[c][q] = fma2(v, z[q], a_qz[c][q]);
-                    if constexpr (BIAS) a_q[c][q] = add2(a_q[c][q], v);
-                    d[c][q] = dn[q];
-                }
-                scale_by<VEC>(d[c], p.wpost, p.vec_dtype, wide, sp, N);
-                #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                    a_qz[c][q] = fma2(d[c][q], z[q], a_qz[c][q]);
+                    if constexpr (BIAS) a_q[c][q] = add2(a_q[c][q], d[c][q]);
+                    d[c][q] = mul2(d[c][q], w[q]);
                     sgz = fma2(d[c][q], z[q], sgz);
                     sgm = add2(sgm, d[c][q]);
                 }
@@ -871,12 +971,12 @@ __global__ void __launch_bounds__(THREADS)
             }
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
                 if (!sp.some(N)) continue;
                 if (p.post != kNone) {
                     // rz (gz_j - mean gz - zhat mean(gz zhat)), zhat = (z - mz) rz
                     F8 z;
-                    take8<ZT>(s + o_z, g.T, g.t, c, z);
+                    take8<ZT>(s + o_z, T, t, c, z);
                     const F2 k = mk2(-rz * gz), a = mk2(rz * gz * mz - gm);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -907,7 +1007,7 @@ __global__ void __launch_bounds__(THREADS)
                 #pragma unroll
                 for (int c = 0; c < C; ++c)
                     #pragma unroll
-                    for (int q = 0; q < 4; ++q) line[(c * 4 + q) * p.T + g.t] = sums(k, c, q);
+                    for (int q = 0; q < 4; ++q) line[(c * 4 + q) * T + t] = sums(k, c, q);
             }
             __syncthreads();
             if (g.index == 0) {
@@ -915,7 +1015,7 @@ __global__ void __launch_bounds__(THREADS)
                 for (int c = 0; c < C; ++c)
                     #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        sums(k, c, q) = add2(sums(k, c, q), line[(c * 4 + q) * p.T + g.t]);
+                        sums(k, c, q) = add2(sums(k, c, q), line[(c * 4 + q) * T + t]);
             }
         }
     }
@@ -925,7 +1025,7 @@ __global__ void __launch_bounds__(THREADS)
         for (int k = 0; k < kinds; ++k) {
             #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const Spot<VEC> sp = spot_of<VEC>(g.T, g.t, c, col0);
+                const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     float lo, hi;
