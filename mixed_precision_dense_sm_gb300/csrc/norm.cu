@@ -127,9 +127,9 @@ int64_t smem_for(const Params& p, int chunks8, int groups, int stages) {
 
 // Groups per CTA and slots per group: the most rows in flight per SM among
 // CTAs of up to `most` threads whose threads all fit an SM's `resident`, with
-// a second slot where it fits; the smallest such CTA.  Returns CTAs per SM, 0
-// where nothing fits.
-int choose_cta(Params& p, int chunks8, int most, int resident, int& groups) {
+// a second slot where it fits; the smallest such CTA.  Returns CTAs per SM (at
+// most `per_sm`), 0 where nothing fits.
+int choose_cta(Params& p, int chunks8, int most, int resident, int per_sm, int& groups) {
     int best = 0, ctas = 0;
     for (int stages = kMaxStages; stages >= 1 && best == 0; --stages) {
         // (named barriers number the groups of more than a warp: 15 at most)
@@ -138,6 +138,7 @@ int choose_cta(Params& p, int chunks8, int most, int resident, int& groups) {
             if (bytes > kSmemPerCta) continue;
             int64_t n = kSmemPerSm / (bytes + 1024);
             if (n > resident / (g * p.T)) n = resident / (g * p.T);
+            if (n > per_sm) n = per_sm;
             if (n > 0 && n * g > best) {
                 best = static_cast<int>(n * g);
                 ctas = static_cast<int>(n);
@@ -176,7 +177,8 @@ cudaError_t run_sum(const SumParams& s, cudaStream_t stream) {
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(s.N, 32)), 1, 1);
+    const int64_t groups = s.d_gate ? (s.groups < kSumGroups ? s.groups : kSumGroups) : 0;
+    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(s.N, 32)), static_cast<unsigned>(1 + groups), 1);
     cfg.blockDim = dim3(32 * kSumY, 1, 1);
     cfg.stream = stream;
     cfg.attrs = &attr;
@@ -235,7 +237,7 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     p.slot_bytes = static_cast<uint32_t>(l.chunks8 * 8 * p.T * (esize(x_dtype) + (Z ? esize(z_dtype) : 0)));
     int groups = 1;
     // 64 registers per thread
-    const int ctas = choose_cta(p, l.chunks8, p.T > 512 ? p.T : 512, 1024, groups);
+    const int ctas = choose_cta(p, l.chunks8, p.T > 512 ? p.T : 512, 1024, 32, groups);
     if (ctas == 0) return GEMM_ERR_NOT_SUPPORTED;
     const Chunks ch = chunks_for(M, Z && block->gate ? block->gate_rows : 1,
                                  static_cast<int64_t>(sms) * ctas / p.cluster);
@@ -340,7 +342,7 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
             l.chunks8 * 8 * p.T *
             (esize(x_dtype) * (dXO ? 2 : 1) + (Z ? esize(z_dtype) : 0) + (dY ? esize(z_dtype) : 0)));
         int groups = 1;
-        if (choose_cta(p, l.chunks8, kBackThreads, kBackThreads, groups) == 0) return GEMM_ERR_NOT_SUPPORTED;
+        if (choose_cta(p, l.chunks8, kBackThreads, kBackThreads, 1, groups) == 0) return GEMM_ERR_NOT_SUPPORTED;
         while (groups > 1 && groups / 2 >= ch.rows) groups /= 2;
         l.threads = groups * p.T;
         l.smem = static_cast<size_t>(smem_for(p, l.chunks8, groups, p.stages));

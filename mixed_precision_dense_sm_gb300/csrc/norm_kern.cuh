@@ -1060,12 +1060,13 @@ __device__ __forceinline__ float param_elem(const void* v, int32_t dtype, int64_
     return __half2float(static_cast<const __half*>(v)[i]);
 }
 
-constexpr int kSumY = 16;
+constexpr int kSumY = 32;
+constexpr int kSumGroups = 2048;    // CTAs along the gate's groups at most
 
-// Sums over the chunks: 32 columns per CTA, kSumY lines of threads.  With few
-// gate groups the lines share each group's chunks and a group's lines are
-// added in order; with many, each line takes whole groups.  The gate joins
-// here: it is constant over a group.
+// Sums over the chunks, 32 columns per CTA, kSumY lines of threads that take
+// the chunks in turn and are added in line order.  CTAs with blockIdx.y == 0
+// make the totals, the gate's row joining chunk by chunk; the others (where
+// the gate's gradient is wanted) one group's sums each.
 static __global__ void __launch_bounds__(32 * kSumY)
     sum_kernel(const __grid_constant__ SumParams p) {
     __shared__ float red[4][kSumY][33];
@@ -1074,81 +1075,63 @@ static __global__ void __launch_bounds__(32 * kSumY)
     const bool in = col < p.N;
     grid_dependency_wait();
     grid_dependents_launch();
-    float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};         // dY xhat, q zhat, dY, q over all chunks
-    // sums of chunks first, first + step, ... of group gr
-    auto add = [&](int32_t gr, int32_t first, int32_t step, float (&a)[4]) {
-        const float* base = p.partials + static_cast<int64_t>(gr) * p.chunks_per_group * p.N + col;
-        #pragma unroll 4
-        for (int32_t c = first; c < p.chunks_per_group; c += step) {
-            const float* q = base + static_cast<int64_t>(c) * p.N;
-            a[0] += q[0];
-            a[1] += q[p.part_stride];
-            if (p.bias) {
-                a[2] += q[2 * p.part_stride];
-                a[3] += q[3 * p.part_stride];
-            }
-        }
-    };
-    // a group's sums: the gate's gradient, and the gated part of the totals
-    auto take = [&](int32_t gr, const float (&s)[4]) {
-        float gt = 1.0f;
-        if (!p.token_gate) {
-            gt = p.scale * param_elem(p.gate, p.vec_dtype, gr * p.ld_gate + col, 1.0f);
-            if (p.d_gate != nullptr) {
-                float v = s[1] * param_elem(p.wpost, p.vec_dtype, col, 1.0f);
-                if (p.bpost != nullptr) v = fmaf(s[3], param_elem(p.bpost, p.vec_dtype, col, 0.0f), v);
-                store_elem(p.d_gate, p.grad_dtype, static_cast<int64_t>(gr) * p.N + col, p.scale * v);
-            }
-        }
-        t[0] += s[0];
-        t[1] = fmaf(gt, s[1], t[1]);
-        t[2] += s[2];
-        t[3] = fmaf(gt, s[3], t[3]);
-    };
-    const bool by_group = p.groups >= kSumY;
-    if (by_group) {
+    // sums of this line's part of chunks [first, last); with GATED q's are
+    // weighted by the gate of the chunk's group
+    auto add = [&](int32_t first, int32_t last, bool gated, float (&a)[4]) {
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = 0.0f;
         if (in) {
-            for (int32_t gr = ty; gr < p.groups; gr += kSumY) {
-                float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                add(gr, 0, 1, a);
-                take(gr, a);
+            const float* base = p.partials + col;
+            #pragma unroll 4
+            for (int32_t c = first + ty; c < last; c += kSumY) {
+                const float* q = base + static_cast<int64_t>(c) * p.N;
+                float gt = 1.0f;
+                if (gated && p.gate != nullptr)
+                    gt = param_elem(p.gate, p.vec_dtype, (c / p.chunks_per_group) * p.ld_gate + col, 1.0f);
+                a[0] += q[0];
+                a[1] = fmaf(gt, q[p.part_stride], a[1]);
+                if (p.bias) {
+                    a[2] += q[2 * p.part_stride];
+                    a[3] = fmaf(gt, q[3 * p.part_stride], a[3]);
+                }
             }
         }
         #pragma unroll
-        for (int k = 0; k < 4; ++k) red[k][ty][tx] = t[k];
+        for (int k = 0; k < 4; ++k) red[k][ty][tx] = a[k];
         __syncthreads();
-        if (ty == 0) {
+        // line k < 4 adds the k-th sum over the lines; line 0 collects them
+        float s = 0.0f;
+        if (ty < 4) {
             #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                t[k] = 0.0f;
-                #pragma unroll
-                for (int y = 0; y < kSumY; ++y) t[k] += red[k][y][tx];
-            }
+            for (int y = 0; y < kSumY; ++y) s += red[ty][y][tx];
         }
-    } else {
-        for (int32_t gr = 0; gr < p.groups; ++gr) {
-            float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (in) add(gr, ty, kSumY, a);
-            #pragma unroll
-            for (int k = 0; k < 4; ++k) red[k][ty][tx] = a[k];
-            __syncthreads();
-            if (ty == 0 && in) {
-                float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                #pragma unroll
-                for (int y = 0; y < kSumY; ++y) {
-                    #pragma unroll
-                    for (int k = 0; k < 4; ++k) s[k] += red[k][y][tx];
-                }
-                take(gr, s);
-            }
-            __syncthreads();
+        __syncthreads();
+        if (ty < 4) red[ty][0][tx] = s;
+        __syncthreads();
+        #pragma unroll
+        for (int k = 0; k < 4; ++k) a[k] = red[k][0][tx];
+        __syncthreads();
+    };
+    float a[4];
+    if (blockIdx.y == 0) {
+        add(0, p.groups * p.chunks_per_group, !p.token_gate, a);
+        if (ty == 0 && in) {
+            const float f = p.token_gate ? 1.0f : p.scale;
+            if (p.d_pre_weight) store_elem(p.d_pre_weight, p.grad_dtype, col, a[0]);
+            if (p.d_post_weight) store_elem(p.d_post_weight, p.grad_dtype, col, f * a[1]);
+            if (p.d_pre_bias) store_elem(p.d_pre_bias, p.grad_dtype, col, a[2]);
+            if (p.d_post_bias) store_elem(p.d_post_bias, p.grad_dtype, col, f * a[3]);
         }
+        return;
     }
-    if (ty == 0 && in) {
-        if (p.d_pre_weight) store_elem(p.d_pre_weight, p.grad_dtype, col, t[0]);
-        if (p.d_post_weight) store_elem(p.d_post_weight, p.grad_dtype, col, t[1]);
-        if (p.d_pre_bias) store_elem(p.d_pre_bias, p.grad_dtype, col, t[2]);
-        if (p.d_post_bias) store_elem(p.d_post_bias, p.grad_dtype, col, t[3]);
+    for (int32_t gr = static_cast<int32_t>(blockIdx.y) - 1; gr < p.groups;
+         gr += static_cast<int32_t>(gridDim.y) - 1) {
+        add(gr * p.chunks_per_group, (gr + 1) * p.chunks_per_group, false, a);
+        if (ty == 0 && in) {
+            float v = a[1] * param_elem(p.wpost, p.vec_dtype, col, 1.0f);
+            if (p.bpost != nullptr) v = fmaf(a[3], param_elem(p.bpost, p.vec_dtype, col, 0.0f), v);
+            store_elem(p.d_gate, p.grad_dtype, static_cast<int64_t>(gr) * p.N + col, p.scale * v);
+        }
     }
 }
 
