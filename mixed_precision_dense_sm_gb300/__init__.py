@@ -25,8 +25,11 @@ clipping): ``grad_clip_raw``, ``grad_clip_workspace``.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
+
+import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgemm_sm103.so")
@@ -470,64 +473,83 @@ def norm_block_backward_workspace(M, N, gate_rows=1, num_sms=0) -> int:
     return lib.norm_block_backward_workspace(M, N, gate_rows, num_sms)
 
 
-def _need_cuda(*tensors):
-    """Every tensor lives on the current CUDA device."""
-    import torch
-    cur = None
-    for t in tensors:
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError("tensors must be on the GPU")
-        if cur is None:
-            cur = torch.cuda.current_device()
-        if t.device.index != cur:
-            raise ValueError("tensors must be on the current CUDA device")
+# Every launch of a small problem waits for these checks, so they look at each
+# tensor once and with few calls; what is wrong is spelled out by _refuse.
 
-
-def _need_matrix(t, name, rows, cols, dtype=None):
-    if t.dim() != 2 or t.stride(1) != 1 and t.shape[1] > 1:
-        raise ValueError(f"{name} must be 2-D with unit inner stride")
-    if t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be {rows} x {cols}")
+def _refuse(t, name, shape, dtype, dev):
+    if t.get_device() < 0:
+        raise ValueError(f"{name} must be on the GPU")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}")
+    raise ValueError(f"{name} must be {' x '.join(map(str, shape))}, with unit inner stride")
 
 
-def _need_vector(t, name, n):
-    if t.dim() != 1 or t.shape[0] != n or t.stride(0) != 1 and n > 1:
-        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
+def _device(t, name):
+    """The current CUDA device, which the tensor has to be on."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
+        _refuse(t, name, t.shape, None, -1)
+    return dev
 
 
-def _ld(t):
-    """Row pitch of a 2-D tensor (torch may give any stride to a single row)."""
-    return max(t.stride(0), t.shape[1], 1) if t.shape[0] > 1 else max(t.shape[1], 1)
+def _mat(t, name, rows, cols, dtype, dev):
+    """(address, row pitch) of a rows x cols matrix; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    if t.shape != (rows, cols) or dtype is not None and t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, name, (rows, cols), dtype, dev)
+    st = t.stride()
+    if st[1] != 1 and cols > 1:
+        _refuse(t, name, (rows, cols), dtype, dev)
+    # torch may give any stride to a single row
+    return t.data_ptr(), (st[0] if rows > 1 else cols) or 1
 
 
-def _ptr(t):
-    return 0 if t is None else t.data_ptr()
+def _vec(t, name, n, dtype, dev):
+    """Address of a vector of n elements; 0 for None."""
+    if t is None:
+        return 0
+    if t.shape != (n,) or dtype is not None and t.dtype is not dtype or t.get_device() != dev or \
+            n > 1 and t.stride(0) != 1:
+        _refuse(t, name, (n,), dtype, dev)
+    return t.data_ptr()
 
 
-def _norm_config(N, rows, pre, pre_weight, pre_bias, post, post_weight, post_bias, gate, gate_rows,
-                 scale, eps):
-    vec = None
-    for t, name in ((pre_weight, "pre_weight"), (pre_bias, "pre_bias"),
-                    (post_weight, "post_weight"), (post_bias, "post_bias"), (gate, "gate")):
-        if t is None:
-            continue
-        if name == "gate":
-            if gate_rows < 1:
-                raise ValueError("gate_rows must be at least 1")
-            _need_matrix(t, name, -(-rows // gate_rows), N)
-        else:
-            _need_vector(t, name, N)
-        if vec is not None and t.dtype != vec:
-            raise ValueError("weights, biases and gate must share a dtype")
-        vec = t.dtype
-    return NormBlock(NORM_KINDS[pre], NORM_KINDS[post], _ptr(pre_weight) or None,
-                     _ptr(pre_bias) or None, _ptr(post_weight) or None, _ptr(post_bias) or None,
-                     _ptr(gate) or None, _ld(gate) if gate is not None else 0, gate_rows,
-                     GEMM_F32 if vec is None else dtype_code(vec), scale, eps)
+def _stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _scratch(nbytes, t, stream):
+    """A workspace of the caching allocator for a call on `stream` (None: the
+    current one)."""
+    w = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
+    if stream is not None:
+        w.record_stream(torch.cuda.ExternalStream(stream))
+    return w
+
+
+def _first_dtype(*tensors):
+    for t in tensors:
+        if t is not None:
+            return t.dtype
+    return None
+
+
+def _norm_config(N, rows, dev, pre, pre_weight, pre_bias, post, post_weight, post_bias, gate,
+                 gate_rows, scale, eps):
+    vec = _first_dtype(pre_weight, pre_bias, post_weight, post_bias, gate)
+    gp = ld = 0
+    if gate is not None:
+        if gate_rows < 1:
+            raise ValueError("gate_rows must be at least 1")
+        gp, ld = _mat(gate, "gate", -(-rows // gate_rows), N, vec, dev)
+    return NormBlock(NORM_KINDS[pre], NORM_KINDS[post], _vec(pre_weight, "pre_weight", N, vec, dev),
+                     _vec(pre_bias, "pre_bias", N, vec, dev),
+                     _vec(post_weight, "post_weight", N, vec, dev),
+                     _vec(post_bias, "post_bias", N, vec, dev), gp, ld, gate_rows,
+                     GEMM_F32 if vec is None else _CODE[vec], scale, eps)
 
 
 def norm_block(X, Z=None, XO=None, Y=None, *, pre="rms", pre_weight=None, pre_bias=None, post=None,
@@ -540,37 +562,31 @@ def norm_block(X, Z=None, XO=None, Y=None, *, pre="rms", pre_weight=None, pre_bi
     (None, Norm_pre(X)).  pre and post are "rms", "layer" or None; pre None
     (with no pre_weight or pre_bias) skips Y.  The gate has one row of N for
     every gate_rows rows of X.  XO may be X (in place); XO and Y are new
-    tensors where None."""
-    import torch
-    _need_cuda(X, Z, XO, Y, pre_weight, pre_bias, post_weight, post_bias, gate)
+    tensors where None.  Weights, biases and gate share a dtype."""
+    dev = _device(X, "X")
     if X.dim() != 2:
         raise ValueError("X must be 2-D with unit inner stride")
     M, N = X.shape
-    _need_matrix(X, "X", M, N)
+    xt = X.dtype
+    x, ldx = _mat(X, "X", M, N, xt, dev)
     want_y = Y is not None or pre not in (None, "none") or pre_weight is not None or pre_bias is not None
-    z_dtype = X.dtype
     if Z is not None:
-        _need_matrix(Z, "Z", M, N)
-        z_dtype = Z.dtype
+        zt = Z.dtype
         if XO is None:
-            XO = torch.empty((M, N), dtype=X.dtype, device=X.device)
-        _need_matrix(XO, "XO", M, N, X.dtype)
+            XO = torch.empty((M, N), dtype=xt, device=X.device)
     elif XO is not None:
         raise ValueError("XO goes with Z")
-    elif Y is not None:
-        z_dtype = Y.dtype
-    if want_y:
-        if Y is None:
-            Y = torch.empty((M, N), dtype=z_dtype, device=X.device)
-        _need_matrix(Y, "Y", M, N, z_dtype)
-    block = _norm_config(N, M, pre, pre_weight, pre_bias, post, post_weight, post_bias, gate,
+    else:
+        zt = xt if Y is None else Y.dtype
+    if want_y and Y is None:
+        Y = torch.empty((M, N), dtype=zt, device=X.device)
+    z, ldz = _mat(Z, "Z", M, N, zt, dev)
+    xo, ldxo = _mat(XO, "XO", M, N, xt, dev)
+    y, ldy = _mat(Y, "Y", M, N, zt, dev)
+    block = _norm_config(N, M, dev, pre, pre_weight, pre_bias, post, post_weight, post_bias, gate,
                          gate_rows, scale, eps)
-    if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
-    st = norm_block_forward(M, N, X.data_ptr(), _ld(X), _ptr(Z), _ld(Z) if Z is not None else 0,
-                            _ptr(XO), _ld(XO) if XO is not None else 0, _ptr(Y),
-                            _ld(Y) if Y is not None else 0, dtype_code(X.dtype),
-                            dtype_code(z_dtype), block, stream)
+    st = norm_block_forward(M, N, x, ldx, z, ldz, xo, ldxo, y, ldy, dtype_code(xt), dtype_code(zt),
+                            block, _stream(dev) if stream is None else stream)
     if st != 0:
         raise GemmError(st, "norm_block_forward")
     return XO, Y
@@ -587,52 +603,40 @@ def norm_block_backward(XO, dY=None, dXO=None, Z=None, *, pre="rms", pre_weight=
     be Z.  The vector gradients share a dtype; dgate is contiguous, as the
     gate.  workspace: a uint8 tensor of norm_block_backward_workspace bytes
     (a new one of the caching allocator where None)."""
-    import torch
-    _need_cuda(XO, dY, dXO, Z, pre_weight, post_weight, post_bias, gate, dX, dZ, dgate, dpre_weight,
-               dpre_bias, dpost_weight, dpost_bias, workspace)
+    dev = _device(XO, "XO")
     if XO.dim() != 2:
         raise ValueError("XO must be 2-D with unit inner stride")
     M, N = XO.shape
     xt = XO.dtype
-    zt = next((t.dtype for t in (Z, dY, dZ) if t is not None), xt)
-    for t, name, dt in ((XO, "XO", xt), (dXO, "dXO", xt), (dX, "dX", xt), (Z, "Z", zt),
-                        (dY, "dY", zt), (dZ, "dZ", zt)):
-        if t is not None:
-            _need_matrix(t, name, M, N, dt)
-    block = _norm_config(N, M, pre, pre_weight, None, post, post_weight, post_bias, gate, gate_rows,
-                         scale, eps)
-    gt = None
-    for t, name in ((dpre_weight, "dpre_weight"), (dpre_bias, "dpre_bias"),
-                    (dpost_weight, "dpost_weight"), (dpost_bias, "dpost_bias"), (dgate, "dgate")):
-        if t is None:
-            continue
-        if name == "dgate":
-            if gate is None:
-                raise ValueError("dgate goes with gate")
-            _need_matrix(t, name, gate.shape[0], N)
-            if not t.is_contiguous():
-                raise ValueError("dgate must be contiguous")
-        else:
-            _need_vector(t, name, N)
-        if gt is not None and t.dtype != gt:
-            raise ValueError("the vector gradients must share a dtype")
-        gt = t.dtype
-    grads = NormBlockGrads(_ptr(dpre_weight) or None, _ptr(dpre_bias) or None,
-                           _ptr(dpost_weight) or None, _ptr(dpost_bias) or None,
-                           _ptr(dgate) or None, GEMM_F32 if gt is None else dtype_code(gt))
-    nbytes = 0
+    zt = _first_dtype(Z, dY, dZ) or xt
+    mats = _mat(XO, "XO", M, N, xt, dev) + _mat(Z, "Z", M, N, zt, dev) + \
+        _mat(dY, "dY", M, N, zt, dev) + _mat(dXO, "dXO", M, N, xt, dev) + \
+        _mat(dX, "dX", M, N, xt, dev) + _mat(dZ, "dZ", M, N, zt, dev)
+    block = _norm_config(N, M, dev, pre, pre_weight, None, post, post_weight, post_bias, gate,
+                         gate_rows, scale, eps)
+    gt = _first_dtype(dpre_weight, dpre_bias, dpost_weight, dpost_bias, dgate)
+    dg = 0
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate goes with gate")
+        dg, _ = _mat(dgate, "dgate", gate.shape[0], N, gt, dev)
+        if not dgate.is_contiguous():
+            raise ValueError("dgate must be contiguous")
+    grads = NormBlockGrads(_vec(dpre_weight, "dpre_weight", N, gt, dev),
+                           _vec(dpre_bias, "dpre_bias", N, gt, dev),
+                           _vec(dpost_weight, "dpost_weight", N, gt, dev),
+                           _vec(dpost_bias, "dpost_bias", N, gt, dev), dg,
+                           GEMM_F32 if gt is None else dtype_code(gt))
+    ws = nbytes = 0
     if gt is not None:
         if workspace is None:
-            need = norm_block_backward_workspace(M, N, gate_rows if gate is not None else 1)
-            workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=XO.device)
-            if stream is not None:
-                workspace.record_stream(torch.cuda.ExternalStream(stream))
-        nbytes = workspace.numel() * workspace.element_size()
-    if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
-    ld = [(_ptr(t), _ld(t) if t is not None else 0) for t in (XO, Z, dY, dXO, dX, dZ)]
-    st = norm_block_backward_raw(M, N, *[v for pair in ld for v in pair], dtype_code(xt),
-                                 dtype_code(zt), block, grads, _ptr(workspace), nbytes, stream)
+            need = lib.norm_block_backward_workspace(M, N, gate_rows if gate is not None else 1, 0)
+            workspace = _scratch(max(need, 16), XO, stream)
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous, on the current CUDA device")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    st = norm_block_backward_raw(M, N, *mats, dtype_code(xt), dtype_code(zt), block, grads, ws,
+                                 nbytes, _stream(dev) if stream is None else stream)
     if st != 0:
         raise GemmError(st, "norm_block_backward")
 
@@ -648,14 +652,13 @@ def grad_clip_raw(grads, outs, sizes, dtypes, max_norm, inv_scale, norm, workspa
                   workspace_bytes, stream=0) -> int:
     """Raw C-ABI call (include/grad_sm103.h): lists of device addresses (outs
     None: in place), element counts and type codes.  Returns the status code."""
-    n = len(grads)
-    a = (ctypes.c_uint64 * max(n, 1))(*grads)
-    o = None if outs is None else (ctypes.c_uint64 * max(n, 1))(*outs)
-    z = (ctypes.c_int64 * max(n, 1))(*sizes)
-    d = (ctypes.c_int32 * max(n, 1))(*dtypes)
-    return lib.grad_clip(n, ctypes.addressof(a), None if o is None else ctypes.addressof(o),
-                         ctypes.addressof(z), ctypes.addressof(d), max_norm, inv_scale,
-                         norm or None, workspace or None, workspace_bytes, stream)
+    a = array.array("Q", grads)
+    o = None if outs is None else array.array("Q", outs)
+    z = array.array("q", sizes)
+    d = array.array("i", dtypes)
+    return lib.grad_clip(len(grads), a.buffer_info()[0], None if o is None else o.buffer_info()[0],
+                         z.buffer_info()[0], d.buffer_info()[0], max_norm, inv_scale, norm or None,
+                         workspace or None, workspace_bytes, stream)
 
 
 def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace=None, stream=None):
@@ -664,53 +667,47 @@ def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace
     out = g * inv_scale * min(1, max_norm / norm), with
     norm = inv_scale * sqrt(sum of all g^2) returned as a 1-element FP32
     tensor.  A norm that is not finite clips nothing."""
-    import torch
-    _need_cuda(*grads)
-    _need_cuda(norm, workspace)
+    dev = _device(grads[0], "gradients") if len(grads) else torch.cuda.current_device()
+    ptrs, sizes, codes = [], [], []
+    for g in grads:
+        if g.get_device() != dev or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous, on the current CUDA device")
+        ptrs.append(g.data_ptr())
+        sizes.append(g.numel())
+        codes.append(_CODE[g.dtype])
+    outs = None
     if outputs is not None:
-        _need_cuda(*outputs)
         if len(outputs) != len(grads):
             raise ValueError("as many outputs as gradients")
-        for g, o in zip(grads, outputs):
-            if o.dtype != g.dtype or o.numel() != g.numel() or not o.is_contiguous():
-                raise ValueError("an output must be contiguous, of its gradient's dtype and size")
-    for g in grads:
-        if not g.is_contiguous():
-            raise ValueError("gradients must be contiguous")
-    dev = grads[0].device if len(grads) else torch.device("cuda", torch.cuda.current_device())
+        outs = []
+        for o, n, c in zip(outputs, sizes, codes):
+            if o.numel() != n or _CODE.get(o.dtype) != c or o.get_device() != dev or not o.is_contiguous():
+                raise ValueError("an output must be contiguous, of its gradient's dtype, size and device")
+            outs.append(o.data_ptr())
     other = None if stream is None else torch.cuda.ExternalStream(stream)
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=dev)
+        norm = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", dev))
         if other is not None:
             norm.record_stream(other)
-    elif norm.dtype != torch.float32 or norm.numel() != 1:
-        raise ValueError("norm must be one FP32 element")
+    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != dev:
+        raise ValueError("norm must be one FP32 element on the current CUDA device")
     if workspace is None:
-        workspace = torch.empty(grad_clip_workspace(len(grads)), dtype=torch.uint8, device=dev)
-        if other is not None:
-            workspace.record_stream(other)
-    if stream is None:
-        stream = torch.cuda.current_stream().cuda_stream
-    st = grad_clip_raw([g.data_ptr() for g in grads],
-                       None if outputs is None else [o.data_ptr() for o in outputs],
-                       [g.numel() for g in grads], [dtype_code(g.dtype) for g in grads], max_norm,
-                       inv_scale, norm.data_ptr(), workspace.data_ptr(),
-                       workspace.numel() * workspace.element_size(), stream)
+        workspace = _scratch(lib.grad_clip_workspace(len(ptrs), 0), norm, stream)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous, on the current CUDA device")
+    st = grad_clip_raw(ptrs, outs, sizes, codes, max_norm, inv_scale, norm.data_ptr(),
+                       workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                       _stream(dev) if stream is None else stream)
     if st != 0:
         raise GemmError(st, "grad_clip")
     return norm
 
 
-_TORCH_CODE = None
+_CODE = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16, torch.float32: GEMM_F32}
 
 
 def dtype_code(t) -> int:
-    global _TORCH_CODE
-    if _TORCH_CODE is None:
-        import torch
-        _TORCH_CODE = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16,
-                       torch.float32: GEMM_F32}
-    return _TORCH_CODE[t]
+    return _CODE[t]
 
 
 class Gemm:
@@ -800,29 +797,24 @@ class Gemm:
         W = [Wg; Wu] (2F x K) and bias = [bg; bu] (2F) or None.  X is M x K, H
         M x F (a new tensor of X's type where None).  P (M x 2F, H's type)
         receives X W^T + bias for the backward pass."""
-        import torch
-        _need_cuda(X, W, H, bias, P)
+        dev = _device(X, "X")
         if X.dim() != 2 or W.dim() != 2 or W.shape[0] % 2:
             raise ValueError("X must be M x K and W 2F x K")
         M, K = X.shape
         F = W.shape[0] // 2
-        _need_matrix(X, "X", M, K)
-        _need_matrix(W, "W", 2 * F, K, X.dtype)
+        xt = X.dtype
         if H is None:
-            H = torch.empty((M, F), dtype=X.dtype, device=X.device)
-        _need_matrix(H, "H", M, F)
-        if bias is not None:
-            _need_vector(bias, "bias", 2 * F)
-        if P is not None:
-            _need_matrix(P, "P", M, 2 * F, H.dtype)
-        if stream is None:
-            stream = torch.cuda.current_stream().cuda_stream
-        xt = dtype_code(X.dtype)
-        st = glu_forward(self.h, M, F, K, X.data_ptr(), _ld(X), W.data_ptr(), _ld(W), H.data_ptr(),
-                         _ld(H), (xt, xt, dtype_code(H.dtype)),
-                         ACTIVATIONS[act] if not isinstance(act, int) else act, _ptr(bias),
-                         dtype_code(bias.dtype) if bias is not None else GEMM_F32, _ptr(P),
-                         _ld(P) if P is not None else 0, stream)
+            H = torch.empty((M, F), dtype=xt, device=X.device)
+        x, ldx = _mat(X, "X", M, K, xt, dev)
+        w, ldw = _mat(W, "W", 2 * F, K, xt, dev)
+        hp, ldh = _mat(H, "H", M, F, None, dev)
+        pp, ldp = _mat(P, "P", M, 2 * F, H.dtype, dev)
+        c = _CODE[xt]
+        st = glu_forward(self.h, M, F, K, x, ldx, w, ldw, hp, ldh, (c, c, _CODE[H.dtype]),
+                         act if isinstance(act, int) else ACTIVATIONS[act],
+                         _vec(bias, "bias", 2 * F, None, dev),
+                         GEMM_F32 if bias is None else _CODE[bias.dtype], pp, ldp,
+                         _stream(dev) if stream is None else stream)
         if st != 0:
             raise GemmError(st, "glu_forward")
         return H
@@ -833,35 +825,30 @@ class Gemm:
         dP (a new tensor where None; may be P itself), and dX (M x K),
         dW (2F x K, beta_w * dW added) and dbias (2F) where given.  X may be
         None without dW, W without dX.  Returns dP."""
-        import torch
-        _need_cuda(dH, P, X, W, dP, dX, dW, dbias)
+        dev = _device(dH, "dH")
         if dH.dim() != 2:
             raise ValueError("dH must be M x F")
         M, F = dH.shape
         t = dH.dtype
-        _need_matrix(dH, "dH", M, F)
-        _need_matrix(P, "P", M, 2 * F)
         if dP is None:
             dP = torch.empty((M, 2 * F), dtype=t, device=dH.device)
-        _need_matrix(dP, "dP", M, 2 * F, t)
         if dX is not None and W is None or dW is not None and X is None:
             raise ValueError("dX needs W and dW needs X")
         K = next((v.shape[-1] for v in (X, W, dX, dW) if v is not None), 0)
-        for v, name, rows, dt in ((X, "X", M, t), (W, "W", 2 * F, t), (dX, "dX", M, None),
-                                  (dW, "dW", 2 * F, None)):
-            if v is not None:
-                _need_matrix(v, name, rows, K, dt)
-        if dbias is not None:
-            _need_vector(dbias, "dbias", 2 * F)
-        if stream is None:
-            stream = torch.cuda.current_stream().cuda_stream
-        code = lambda v: GEMM_F32 if v is None else dtype_code(v.dtype)   # noqa: E731
-        ld = lambda v: 0 if v is None else _ld(v)                          # noqa: E731
-        st = glu_backward(self.h, M, F, K, dH.data_ptr(), _ld(dH), P.data_ptr(), _ld(P), _ptr(X),
-                          ld(X) or max(K, 1), _ptr(W), ld(W) or max(K, 1), dtype_code(t),
-                          dP.data_ptr(), _ld(dP), ACTIVATIONS[act] if not isinstance(act, int) else act,
-                          dtype_code(P.dtype), _ptr(dX), ld(dX), code(dX), _ptr(dW), ld(dW), code(dW),
-                          beta_w, _ptr(dbias), code(dbias), stream)
+        h_, ldh = _mat(dH, "dH", M, F, t, dev)
+        p, ldp = _mat(P, "P", M, 2 * F, None, dev)
+        dp, lddp = _mat(dP, "dP", M, 2 * F, t, dev)
+        x, ldx = _mat(X, "X", M, K, t, dev)
+        w, ldw = _mat(W, "W", 2 * F, K, t, dev)
+        dx, lddx = _mat(dX, "dX", M, K, None, dev)
+        dw, lddw = _mat(dW, "dW", 2 * F, K, None, dev)
+        st = glu_backward(self.h, M, F, K, h_, ldh, p, ldp, x, ldx or max(K, 1), w, ldw or max(K, 1),
+                          _CODE[t], dp, lddp, act if isinstance(act, int) else ACTIVATIONS[act],
+                          _CODE[P.dtype], dx, lddx, GEMM_F32 if dX is None else _CODE[dX.dtype], dw,
+                          lddw, GEMM_F32 if dW is None else _CODE[dW.dtype], beta_w,
+                          _vec(dbias, "dbias", 2 * F, None, dev),
+                          GEMM_F32 if dbias is None else _CODE[dbias.dtype],
+                          _stream(dev) if stream is None else stream)
         if st != 0:
             raise GemmError(st, "glu_backward")
         return dP
