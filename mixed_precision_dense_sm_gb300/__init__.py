@@ -43,7 +43,8 @@ HEADERS = [HEADER, os.path.join(os.path.dirname(HERE), "include", "softmax_sm103
 GEMM_F16, GEMM_BF16, GEMM_F32 = 0, 1, 2
 STATUS = {0: "GEMM_OK", 1: "GEMM_ERR_INVALID_VALUE", 2: "GEMM_ERR_NOT_SUPPORTED",
           3: "GEMM_ERR_ALLOC", 4: "GEMM_ERR_LAUNCH", 5: "GEMM_ERR_DEVICE_TIMEOUT"}
-PATHS = {0: "noop", 1: "scale", 2: "tiled_1sm", 3: "tiled_2sm", 4: "skinny"}
+PATHS = {0: "noop", 1: "scale", 2: "tiled_1sm", 3: "tiled_2sm", 4: "skinny",
+         5: "dot"}
 
 
 class GemmError(RuntimeError):

@@ -349,8 +349,9 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     // not use is left to the L1 cache).
     const bool c_stage_ok = pl.pub.c_vector && !ln && !use_mh2;
     const int64_t avail_all = smem_optin - 1024 - barrier_bytes - static_bytes;
-    // (the swapped gated layer exchanges its halves through the same area)
-    const bool exchange = glu && swap;
+    // (the gated layer exchanges its halves where swapped, and turns rows that
+    // are not aligned, through the same area)
+    const bool exchange = glu && (swap || !pl.pub.c_vector);
     const int64_t avail = avail_all - (c_stage_ok || exchange ? kCStageBytes : 0);
     pl.kc = (kc2_ok && avail / (2 * static_cast<int64_t>(chunk_bytes)) >= min_kc2_stages) ? 2 : 1;
     const int64_t block_k = chunk_k * pl.kc;
@@ -370,7 +371,7 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     // The gated layer's skinny tiles (64 output columns each) outnumber the SMs
     // sooner: a badly filled last wave is balanced there too (64 tokens,
     // 4096 -> 14336: 224 tiles, 1.5 waves).
-    const bool exchange_sk = exchange && k_chunks >= 4 && wave_fill(tiles, num_sms) < kMinWaveFill;
+    const bool exchange_sk = glu && swap && k_chunks >= 4 && wave_fill(tiles, num_sms) < kMinWaveFill;
     const bool stream_k = allow_sk && !use_mh2 && work < INT32_MAX &&
                           (pair_sk || (!pairs && !ln && (tiles <= kMaxCounterTiles) &&
                                        (balance_sk || exchange_sk || ((tiles < num_sms) &&
@@ -796,13 +797,14 @@ bool glu_p_vector(int64_t F, const glu_forward_t* o, int32_t c_dtype) {
 // Everything gemm_run enqueues after planning: the optional pack pre-passes,
 // the TMA descriptors and the GEMM kernel.  `ws` is the workspace laid out as
 // [tile counters (4 KB)][packed A][packed B][partial slots]; with
-// clear_counters the counters are zeroed on the stream first.
+// clear_counters the counters are zeroed on the stream first.  body_offset: bytes
+// behind the counters that the caller uses itself.
 gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, uint8_t* ws,
                            int* err_dev, float alpha, float beta, void* C, gemm_dtypes_t dt,
                            cudaStream_t stream, bool clear_counters, uint32_t debug_flags = 0,
                            uint64_t wait_limit_ns = 0, const gemm_epilogue_t* ep = nullptr,
                            const ConvDesc* conv = nullptr, const gemm_layernorm_t* ln = nullptr,
-                           const GluDesc* glu = nullptr) {
+                           const GluDesc* glu = nullptr, int64_t body_offset = 0) {
     // kind::tf32 reads K-major operands only; the planner transposes the rest.
     if (pl.esize == 4 && (pl.a.mn_major || pl.b.mn_major)) return GEMM_ERR_NOT_SUPPORTED;
     int* counters = reinterpret_cast<int*>(ws);
@@ -811,7 +813,7 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
         cudaGetLastError();
         return GEMM_ERR_LAUNCH;
     }
-    uint8_t* ws_a = ws + kWsHeaderBytes;
+    uint8_t* ws_a = ws + kWsHeaderBytes + body_offset;
     uint8_t* ws_b = ws_a + round_up(pl.pack_a_bytes, 256);
     float* ws_part = reinterpret_cast<float*>(ws_b + round_up(pl.pack_b_bytes, 256));
     float2* ws_stats = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ws_part) +
@@ -841,13 +843,30 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
                 static_cast<const uint16_t*>(o.ptr), o.ld, o.rows, o.cols,
                 reinterpret_cast<uint16_t*>(dst), o.packed_ld);
     };
-    if (pl.a.pack) {
-        pack(pl.a, ws_a);
+    if (glu != nullptr && pl.a.pack && pl.b.pack) {
+        // both in one launch: small problems wait for launches
+        PackPair pp;
+        const OperandDesc* o[2] = {&pl.a, &pl.b};
+        uint8_t* dst[2] = {ws_a, ws_b};
+        int grid = 1;
+        for (int i = 0; i < 2; ++i) {
+            pp.d[i] = PackDesc{static_cast<const uint16_t*>(o[i]->ptr), reinterpret_cast<uint16_t*>(dst[i]),
+                               o[i]->ld, o[i]->rows, o[i]->cols, o[i]->packed_ld};
+            const int g = grid_for(o[i]->rows * o[i]->packed_ld / 8, num_sms);
+            if (g > grid) grid = g;
+        }
+        pack_pair_kernel<<<dim3(grid, 2, 1), 256, 0, stream>>>(pp);
         a_ptr = ws_a;
-    }
-    if (pl.b.pack) {
-        pack(pl.b, ws_b);
         b_ptr = ws_b;
+    } else {
+        if (pl.a.pack) {
+            pack(pl.a, ws_a);
+            a_ptr = ws_a;
+        }
+        if (pl.b.pack) {
+            pack(pl.b, ws_b);
+            b_ptr = ws_b;
+        }
     }
     if ((pl.a.pack || pl.b.pack) && cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
 
@@ -1621,6 +1640,9 @@ gemm_status_t conv2d_fprop(gemm_handle_t h, int64_t N, int64_t H, int64_t W, int
 // ---------------------------------------------------------------------------
 namespace {
 
+// Tokens the dot-product kernel takes (its instances go to 4).
+constexpr int64_t kGluDotTokens = 4;
+
 // Slabs of rows of the dP kernel: enough CTAs for eight per SM, each slab at
 // least one row per warp.
 int64_t glu_slab_rows(int64_t M, int64_t F, int num_sms) {
@@ -1691,17 +1713,99 @@ gemm_status_t enqueue_glu_gate(const glu_forward_t* o, void* H, int64_t ldh, int
     return cudaGetLastError() == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
-template <typename T, typename PT>
-void launch_glu_back(const GluBackParams& p, dim3 grid, cudaStream_t stream) {
-    if (p.partials) glu_back_kernel<T, PT, true><<<grid, 32 * kGluBackWarps, 0, stream>>>(p);
-    else glu_back_kernel<T, PT, false><<<grid, 32 * kGluBackWarps, 0, stream>>>(p);
+// A few tokens whose rows and weights are vectors go to the dot-product kernel.
+bool glu_dot_ok(int64_t M, int64_t K, const void* X, int64_t ldx, const void* W, int64_t ldw) {
+    return M <= kGluDotTokens && K % 8 == 0 && aligned16(X) && aligned16(W) && ldx % 8 == 0 && ldw % 8 == 0;
+}
+
+int32_t glu_dot_grid(int64_t F, int num_sms) {
+    const int64_t want = ceil_div(F, kGluDotThreads / 32);
+    const int64_t most = static_cast<int64_t>(num_sms) * kGluDotCtas;
+    return static_cast<int32_t>(want < most ? want : most);
 }
 
 template <typename T>
-void launch_glu_back_p(const GluBackParams& p, int32_t p_dtype, dim3 grid, cudaStream_t stream) {
-    if (p_dtype == GEMM_F32) launch_glu_back<T, float>(p, grid, stream);
-    else if (p_dtype == GEMM_F16) launch_glu_back<T, __half>(p, grid, stream);
-    else launch_glu_back<T, __nv_bfloat16>(p, grid, stream);
+cudaError_t launch_glu_dot(const GluDotParams& p, int64_t M, int grid, cudaStream_t stream) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, 1, 1);
+    cfg.blockDim = dim3(kGluDotThreads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    switch (M) {
+        case 1: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 1>, p);
+        case 2: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 2>, p);
+        case 3: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 3>, p);
+        default: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 4>, p);
+    }
+}
+
+gemm_status_t enqueue_glu_dot(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
+                              const void* W, int64_t ldw, void* H, int64_t ldh, gemm_dtypes_t dt,
+                              const glu_forward_t* o, int num_sms, cudaStream_t stream) {
+    const GluDotParams p{X, ldx, W, ldw, H, ldh, o->P, o->ldp, o->bias, o->bias_dtype, o->activation,
+                         dt.c, static_cast<int32_t>(F), static_cast<int32_t>(K)};
+    const int grid = glu_dot_grid(F, num_sms);
+    const cudaError_t e = dt.a == GEMM_F16 ? launch_glu_dot<__half>(p, M, grid, stream)
+                                           : launch_glu_dot<__nv_bfloat16>(p, M, grid, stream);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+template <typename T, typename PT>
+void launch_glu_back(const GluBackParams& p, bool vec, dim3 grid, cudaStream_t stream) {
+    constexpr int kT = 32 * kGluBackWarps;
+    if (p.partials) {
+        if (vec) glu_back_kernel<T, PT, true, true><<<grid, kT, 0, stream>>>(p);
+        else glu_back_kernel<T, PT, false, true><<<grid, kT, 0, stream>>>(p);
+    } else {
+        if (vec) glu_back_kernel<T, PT, true, false><<<grid, kT, 0, stream>>>(p);
+        else glu_back_kernel<T, PT, false, false><<<grid, kT, 0, stream>>>(p);
+    }
+}
+
+template <typename T>
+void launch_glu_back_p(const GluBackParams& p, bool vec, int32_t p_dtype, dim3 grid,
+                       cudaStream_t stream) {
+    if (p_dtype == GEMM_F32) launch_glu_back<T, float>(p, vec, grid, stream);
+    else if (p_dtype == GEMM_F16) launch_glu_back<T, __half>(p, vec, grid, stream);
+    else launch_glu_back<T, __nv_bfloat16>(p, vec, grid, stream);
+}
+
+// Rows that the GEMM's loads and stores take as they are.
+bool rows_aligned(const void* p, int64_t ld, int64_t es) { return aligned16(p) && ld * es % 16 == 0; }
+
+// One of the backward pass's products on a workspace whose first `used` bytes
+// behind the counters are the caller's; *need: the bytes behind those.
+struct Product {
+    char ta, tb;
+    int64_t M, N, K;
+    const void* A; int64_t lda;
+    const void* B; int64_t ldb;
+    float beta;
+    void* C; int64_t ldc;
+    gemm_dtypes_t dt;
+};
+
+gemm_status_t plan_product(const gemm_ctx* h, const Product& g, Plan& pl) {
+    return make_plan(g.ta, g.tb, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C, g.ldc, g.dt,
+                     h->num_sms, h->smem_optin, pl);
+}
+
+gemm_status_t enqueue_product(gemm_ctx* h, const Product& g, const Plan& pl, int64_t used,
+                              cudaStream_t stream) {
+    if (pl.pub.path == GEMM_PATH_NOOP) return GEMM_OK;
+    if (pl.pub.path == GEMM_PATH_SCALE)
+        return enqueue_scale(g.M, g.N, g.C, g.ldc, g.beta, g.dt, h->num_sms, stream);
+    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, 1.0f, g.beta,
+                        g.C, g.dt, stream, false, h->debug_flags, h->wait_limit_ns, nullptr, nullptr,
+                        nullptr, nullptr, used);
 }
 
 }  // namespace
@@ -1718,6 +1822,12 @@ gemm_status_t glu_plan_query(int64_t M, int64_t F, int64_t K, const void* X, int
     Plan pl;
     st = glu_plan(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt, num_sms, smem_optin, pl);
     if (st != GEMM_OK) return st;
+    if (M > 0 && F > 0 && K > 0 && glu_dot_ok(M, K, X, ldx, W, ldw)) {
+        std::memset(&pl.pub, 0, sizeof pl.pub);
+        pl.pub.path = GEMM_PATH_DOT;
+        pl.pub.split_k = 1;
+        pl.pub.grid = glu_dot_grid(F, num_sms);
+    }
     *out = pl.pub;
     return GEMM_OK;
 }
@@ -1733,6 +1843,8 @@ gemm_status_t glu_forward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, cons
     if (M == 0 || F == 0) return GEMM_OK;
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     if (K == 0) return enqueue_glu_gate(opt, H, ldh, M, F, dt.c, h->num_sms, stream);
+    if (glu_dot_ok(M, K, X, ldx, W, ldw))
+        return enqueue_glu_dot(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt, h->num_sms, stream);
     Plan pl;
     st = glu_plan(M, F, K, X, ldx, W, ldw, H, ldh, dt, opt, h->num_sms, h->smem_optin, pl);
     if (st != GEMM_OK) return st;
@@ -1778,37 +1890,132 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     const int64_t slab_rows = some ? glu_slab_rows(M, F, h->num_sms) : 1;
     const int64_t slabs = some ? ceil_div(M, slab_rows) : 0;
-    float* partials = nullptr;
-    if (some && o->dbias) {
-        st = ensure_workspace(h, static_cast<size_t>(kWsHeaderBytes + slabs * 2 * F * 4), stream);
+
+    // The workspace behind the counters: [column sums][aligned copies of dP, W,
+    // X where theirs are not][aligned dX, dW on their way to rows that are
+    // not][the products' own].  Laid out and grown before anything is enqueued.
+    int64_t used = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t at = used;
+        used += round_up(bytes, 256);
+        return at;
+    };
+    const bool dx_some = o->dX && M > 0 && K > 0, dw_some = o->dW && F > 0 && K > 0;
+    const bool copy_p = some && (dx_some || dw_some) && !rows_aligned(o->dP, o->lddp, 2);
+    const bool copy_w = some && dx_some && !rows_aligned(W, ldw, 2);
+    const bool copy_x = some && dw_some && !rows_aligned(X, ldx, 2);
+    const int64_t dx_es = static_cast<int64_t>(out_elem_bytes(o->dx_dtype));
+    const int64_t dw_es = static_cast<int64_t>(out_elem_bytes(o->dw_dtype));
+    // (an accumulated dW is read too: it stays in place)
+    const bool out_x = some && dx_some && !rows_aligned(o->dX, o->lddx, dx_es);
+    const bool out_w = some && dw_some && o->beta_w == 0.0f && !rows_aligned(o->dW, o->lddw, dw_es);
+    const int64_t ldp8 = round_up(2 * F, 8), ldk8 = round_up(K, 8);
+    const int64_t at_sums = some && o->dbias ? take(slabs * 2 * F * 4) : 0;
+    const int64_t at_p = copy_p ? take(M * ldp8 * 2) : 0;
+    const int64_t at_w = copy_w ? take(2 * F * ldk8 * 2) : 0;
+    const int64_t at_x = copy_x ? take(M * ldk8 * 2) : 0;
+    const int64_t at_dx = out_x ? take(M * ldk8 * dx_es) : 0;
+    const int64_t at_dw = out_w ? take(2 * F * ldk8 * dw_es) : 0;
+    // planned with stand-in addresses: only alignment counts
+    void* const any = reinterpret_cast<void*>(static_cast<uintptr_t>(256));
+    Product gx{'N', 'N', M, K, 2 * F, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_w ? any : W,
+               copy_w ? ldk8 : ldw, 0.0f, out_x ? any : o->dX, out_x ? ldk8 : o->lddx, xdt};
+    Product gw{'T', 'N', 2 * F, K, M, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_x ? any : X,
+               copy_x ? ldk8 : ldx, o->beta_w, out_w ? any : o->dW, out_w ? ldk8 : o->lddw, wdt};
+    Plan px, pw;
+    int64_t own = 0;
+    if (dx_some) {
+        st = plan_product(h, gx, px);
         if (st != GEMM_OK) return st;
-        partials = reinterpret_cast<float*>(static_cast<uint8_t*>(h->ws) + kWsHeaderBytes);
+        if (px.pub.workspace_bytes > own) own = px.pub.workspace_bytes;
     }
+    if (dw_some) {
+        st = plan_product(h, gw, pw);
+        if (st != GEMM_OK) return st;
+        if (pw.pub.workspace_bytes > own) own = pw.pub.workspace_bytes;
+    }
+    if (used > 0 || own > 0) {
+        st = ensure_workspace(h, static_cast<size_t>(kWsHeaderBytes + used + own), stream);
+        if (st != GEMM_OK) return st;
+    }
+    uint8_t* body = static_cast<uint8_t*>(h->ws) + kWsHeaderBytes;
+    float* partials = some && o->dbias ? reinterpret_cast<float*>(body + at_sums) : nullptr;
+    if (copy_p) gx.A = gw.A = body + at_p;
+    if (copy_w) gx.B = body + at_w;
+    if (copy_x) gw.B = body + at_x;
+    if (out_x) gx.C = body + at_dx;
+    if (out_w) gw.C = body + at_dw;
+    px.a.ptr = gx.A;
+    px.b.ptr = gx.B;
+    pw.a.ptr = gw.A;
+    pw.b.ptr = gw.B;
+    if (dx_some && px.pub.swap_ab) {
+        px.a.ptr = gx.B;
+        px.b.ptr = gx.A;
+    }
+    if (dw_some && pw.pub.swap_ab) {
+        pw.a.ptr = gw.B;
+        pw.b.ptr = gw.A;
+    }
+
     if (some) {
         const int64_t pe = static_cast<int64_t>(out_elem_bytes(o->p_dtype));
-        GluBackParams p{dH, lddh, P, ldp, o->dP, o->lddp, M, F, o->activation, 0, slab_rows, partials};
-        p.vec = F % 8 == 0 && aligned16(dH) && aligned16(P) && aligned16(o->dP) && lddh % 8 == 0 &&
-                o->lddp % 8 == 0 && ldp * pe % 16 == 0;
+        GluBackParams p{dH, lddh, P, ldp, o->dP, o->lddp, copy_p ? body + at_p : nullptr, ldp8, M, F,
+                        o->activation, slab_rows, partials};
+        const bool vec = F % 8 == 0 && rows_aligned(dH, lddh, 2) && rows_aligned(P, ldp, pe) &&
+                         rows_aligned(o->dP, o->lddp, 2);
         const dim3 grid(static_cast<unsigned>(ceil_div(F, 256)), static_cast<unsigned>(slabs), 1);
-        if (dtype == GEMM_F16) launch_glu_back_p<__half>(p, o->p_dtype, grid, stream);
-        else launch_glu_back_p<__nv_bfloat16>(p, o->p_dtype, grid, stream);
+        if (dtype == GEMM_F16) launch_glu_back_p<__half>(p, vec, o->p_dtype, grid, stream);
+        else launch_glu_back_p<__nv_bfloat16>(p, vec, o->p_dtype, grid, stream);
         if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
     }
     if (o->dbias && F > 0) {
         const int64_t cols = 2 * F;
-        glu_dbias_kernel<<<static_cast<unsigned>(ceil_div(cols, 256)), 256, 0, stream>>>(
+        glu_dbias_kernel<<<static_cast<unsigned>(ceil_div(cols, 32)), 1024, 0, stream>>>(
             partials, static_cast<int32_t>(slabs), cols, o->dbias, o->dbias_dtype);
         if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
     }
-    if (o->dX) {
-        st = gemm_run(h, 'N', 'N', M, K, 2 * F, 1.0f, o->dP, o->lddp, W, ldw, 0.0f, o->dX, o->lddx,
-                      xdt, stream_);
+    if (copy_w || copy_x) {
+        PackPair pp;
+        std::memset(&pp, 0, sizeof pp);
+        int n = 0, grid = 1;
+        auto add = [&](const void* src, int64_t ld, int64_t rows, int64_t at) {
+            pp.d[n++] = PackDesc{static_cast<const uint16_t*>(src), reinterpret_cast<uint16_t*>(body + at),
+                                 ld, rows, K, ldk8};
+            const int g = grid_for(rows * ldk8 / 8, h->num_sms);
+            if (g > grid) grid = g;
+        };
+        if (copy_w) add(W, ldw, 2 * F, at_w);
+        if (copy_x) add(X, ldx, M, at_x);
+        pack_pair_kernel<<<dim3(grid, n, 1), 256, 0, stream>>>(pp);
+        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+    }
+    if (dx_some) {
+        st = enqueue_product(h, gx, px, used, stream);
         if (st != GEMM_OK) return st;
     }
-    if (o->dW)
-        st = gemm_run(h, 'T', 'N', 2 * F, K, M, 1.0f, o->dP, o->lddp, X, ldx, o->beta_w, o->dW,
-                      o->lddw, wdt, stream_);
-    return st;
+    if (dw_some) {
+        st = enqueue_product(h, gw, pw, used, stream);
+        if (st != GEMM_OK) return st;
+    }
+    if (out_x || out_w) {
+        UnpackPair up;
+        std::memset(&up, 0, sizeof up);
+        int n = 0;
+        int64_t rows = 1;
+        auto add = [&](int64_t at, void* dst, int64_t r, int64_t ld, int64_t es) {
+            up.d[n++] = UnpackDesc{body + at, dst, ldk8, r, K, ld, static_cast<int32_t>(es)};
+            if (r > rows) rows = r;
+        };
+        if (out_x) add(at_dx, o->dX, M, o->lddx, dx_es);
+        if (out_w) add(at_dw, o->dW, 2 * F, o->lddw, dw_es);
+        int64_t grid = ceil_div(rows, 8);
+        const int64_t cap = static_cast<int64_t>(h->num_sms) * 8;
+        if (grid > cap) grid = cap;
+        unpack_pair_kernel<<<dim3(static_cast<unsigned>(grid), n, 1), 256, 0, stream>>>(up);
+        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
 }
 
 }  // extern "C"

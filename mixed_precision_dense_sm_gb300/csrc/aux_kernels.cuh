@@ -49,6 +49,66 @@ __global__ void __launch_bounds__(256)
     }
 }
 
+// Two such copies of 16-bit matrices in one launch (blockIdx.y picks one).
+struct PackDesc {
+    const uint16_t* src;
+    uint16_t* dst;
+    int64_t src_ld, rows, cols, dst_ld;
+};
+struct PackPair {
+    PackDesc d[2];
+};
+static __global__ void __launch_bounds__(256)
+    pack_pair_kernel(const __grid_constant__ PackPair p) {
+    const PackDesc& d = p.d[blockIdx.y];
+    const int64_t vec_per_row = d.dst_ld / 8;
+    const int64_t total = d.rows * vec_per_row;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t r = i / vec_per_row;
+        const int64_t c0 = (i - r * vec_per_row) * 8;
+        const uint16_t* s = d.src + r * d.src_ld;
+        union {
+            uint16_t e[8];
+            uint4 u;
+        } v;
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) v.e[e] = (c0 + e < d.cols) ? s[c0 + e] : static_cast<uint16_t>(0);
+        *reinterpret_cast<uint4*>(d.dst + r * d.dst_ld + c0) = v.u;
+    }
+}
+
+// Copies rows out of the workspace to rows of any alignment (elements of 2 or
+// 4 bytes), up to two matrices in one launch; one warp per row at a time.
+struct UnpackDesc {
+    const void* src;
+    void* dst;
+    int64_t src_ld, rows, cols, dst_ld;
+    int32_t esize;
+};
+struct UnpackPair {
+    UnpackDesc d[2];
+};
+static __global__ void __launch_bounds__(256)
+    unpack_pair_kernel(const __grid_constant__ UnpackPair p) {
+    const UnpackDesc& d = p.d[blockIdx.y];
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < d.rows; r += warps) {
+        if (d.esize == 4) {
+            const uint32_t* s = static_cast<const uint32_t*>(d.src) + r * d.src_ld;
+            uint32_t* o = static_cast<uint32_t*>(d.dst) + r * d.dst_ld;
+            #pragma unroll 4
+            for (int64_t c = lane; c < d.cols; c += 32) o[c] = s[c];
+        } else {
+            const uint16_t* s = static_cast<const uint16_t*>(d.src) + r * d.src_ld;
+            uint16_t* o = static_cast<uint16_t*>(d.dst) + r * d.dst_ld;
+            #pragma unroll 4
+            for (int64_t c = lane; c < d.cols; c += 32) o[c] = s[c];
+        }
+    }
+}
+
 // dst[n][k] = src[k][n] for k < K, n < MN; dst's columns K..dst_ld-1 are
 // written as zeros (dst_ld <= K rounded up to 32).  One 32 x 32 tile per
 // iteration through shared memory (padded against bank conflicts), so the

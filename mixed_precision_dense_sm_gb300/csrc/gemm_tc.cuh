@@ -738,6 +738,29 @@ __device__ __forceinline__ void glu_sums(uint32_t t_row, uint32_t t_spare, bool 
     }
 }
 
+// The same for a warp's 32 rows (the first at `base`) that are not 16-byte
+// aligned: turned through 4 KB of shared memory, so that each store
+// instruction writes 32 consecutive elements of one row and not one element
+// of 32 rows (a ragged 1000 x 777 -> 1023 problem 45 -> 17 us).  Element
+// (r, c) lies at word r * 32 + (c ^ r): no bank conflicts either way.
+template <typename OutT>
+__device__ __forceinline__ void glu_store_turned(float* buf, OutT* base, int64_t ld, int32_t rows,
+                                                 int32_t c0, int32_t cols, const float (&v)[32]) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+    #pragma unroll
+    for (int j = 0; j < 32; ++j) buf[lane * 32 + (j ^ lane)] = v[j];
+    __syncwarp();
+    if (c0 + lane < cols) {
+        OutT* dst = base + c0 + lane;
+        #pragma unroll 8
+        for (int r = 0; r < 32; ++r) {
+            if (r >= rows) break;
+            dst[r * ld] = cvt_out<OutT>(buf[r * 32 + (lane ^ r)]);
+        }
+    }
+}
+
 // Output tile of a problem that is not swapped: g and u of 32 output columns
 // at a time in each thread, H = act(g) u, rounded once.  With c_tma the two
 // warps of a lane quarter fill 64 columns (16-bit outputs) of a staging box
@@ -810,6 +833,22 @@ __device__ __forceinline__ void glu_tile(const GluParams& p, const CUtensorMap* 
             #pragma unroll
             for (int j = 0; j < 32; ++j) g[j] *= u[j];
             put(tmC, false, 0, ch >> 1, g);
+        } else if (!p.c_vector) {
+            const int lane = threadIdx.x & 31;
+            const int32_t r0 = row - lane;                        // the warp's first row
+            const int32_t rows = p.M - r0;
+            float* buf = reinterpret_cast<float*>(cstage) + ((threadIdx.x >> 5) - 2) * 1024;
+            if (rows <= 0 || c0 >= p.F) continue;                 // (the same for the whole warp)
+            if (p.P != nullptr) {
+                OutT* prow = static_cast<OutT*>(p.P) + static_cast<int64_t>(r0) * p.ldp;
+                glu_store_turned<OutT>(buf, prow, p.ldp, rows, c0, p.F, g);
+                glu_store_turned<OutT>(buf, prow + p.F, p.ldp, rows, c0, p.F, u);
+            }
+            act32(p.act, g);
+            #pragma unroll
+            for (int j = 0; j < 32; ++j) g[j] *= u[j];
+            glu_store_turned<OutT>(buf, static_cast<OutT*>(p.C) + static_cast<int64_t>(r0) * p.c_rs,
+                                   p.c_rs, rows, c0, p.F, g);
         } else if (row < p.M && c0 < p.F) {
             if (p.P != nullptr) {
                 OutT* prow = static_cast<OutT*>(p.P) + static_cast<int64_t>(row) * p.ldp;
@@ -918,7 +957,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // [stages][C staging, when C is stored by TMA][barriers]
     uint8_t* cstage = smem + S * stage_bytes;
     bool staging = p.c_tma != 0;
-    if constexpr (EPI == kEpiGlu) staging = staging || p.swap;    // the exchange buffer
+    // the gated layer exchanges its halves, or turns its rows, there
+    if constexpr (EPI == kEpiGlu) staging = staging || p.swap || !p.c_vector;
     uint64_t* full = reinterpret_cast<uint64_t*>(cstage + (staging ? kCStageBytes : 0u));
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;

@@ -7,6 +7,7 @@
 #include <cuda_fp16.h>
 
 #include "epilogue_ops.cuh"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 
 namespace gemm103 {
@@ -86,107 +87,123 @@ struct GluBackParams {
     const void* dH; int64_t lddh;
     const void* P; int64_t ldp;
     void* dP; int64_t lddp;
+    void* dPa; int64_t ldpa;  // a second copy of dP whose rows are 16-byte aligned, or NULL
     int64_t M;
     int64_t F;
     int32_t act;
-    int32_t vec;             // rows of dH, P, dP and their halves 16-byte aligned, F a multiple of 8
     int64_t slab_rows;       // rows per CTA (blockIdx.y)
     float* partials;         // [slabs][2F] column sums of dP, or NULL
 };
 
 constexpr int kGluBackWarps = 8;
+constexpr int kGluBackRows = 2;     // rows whose loads a warp has in flight together
 
-template <typename T>
-union GluVec {
-    uint4 u[sizeof(T) / 2];
-    T e[8];
-};
-
-// 8 elements at p + base + e * step; 0 past column F.
-template <typename T>
-__device__ __forceinline__ void glu_load8(const T* p, bool vec, int64_t base, int64_t F, float (&o)[8]) {
-    if (vec) {
-        if (base >= F) {
+// 8 elements of a row as they lie in memory (VEC: consecutive; else 32 apart).
+template <typename T, bool VEC>
+struct Raw8 {
+    union {
+        uint4 u[sizeof(T) / 2];
+        T e[8];
+    };
+    // the loads; element i is at p + base + i (VEC) or p + base + 32 i
+    __device__ __forceinline__ void load(const T* p, int64_t base, int64_t F) {
+        if constexpr (VEC) {
+            if (base < F) {
+                #pragma unroll
+                for (int q = 0; q < static_cast<int>(sizeof(T) / 2); ++q)
+                    u[q] = __ldcs(reinterpret_cast<const uint4*>(p + base) + q);
+            }
+        } else {
             #pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] = 0.0f;
-            return;
+            for (int i = 0; i < 8; ++i)
+                if (base + i * 32 < F) e[i] = p[base + i * 32];
         }
-        GluVec<T> v;
-        #pragma unroll
-        for (int q = 0; q < static_cast<int>(sizeof(T) / 2); ++q)
-            v.u[q] = __ldcs(reinterpret_cast<const uint4*>(p + base) + q);
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = glu_to_f<T>(v.e[e]);
-    } else {
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) o[e] = base + e * 32 < F ? glu_to_f<T>(p[base + e * 32]) : 0.0f;
     }
-}
-
-template <typename T>
-__device__ __forceinline__ void glu_store8(T* p, bool vec, int64_t base, int64_t F, const float (&v)[8]) {
-    if (vec) {
-        if (base >= F) return;
-        GluVec<T> w;
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) w.e[e] = glu_from_f<T>(v[e]);
-        #pragma unroll
-        for (int q = 0; q < static_cast<int>(sizeof(T) / 2); ++q)
-            reinterpret_cast<uint4*>(p + base)[q] = w.u[q];
-    } else {
-        #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (base + e * 32 < F) p[base + e * 32] = glu_from_f<T>(v[e]);
+    __device__ __forceinline__ void store(T* p, int64_t base, int64_t F) const {
+        if constexpr (VEC) {
+            if (base < F) {
+                #pragma unroll
+                for (int q = 0; q < static_cast<int>(sizeof(T) / 2); ++q)
+                    reinterpret_cast<uint4*>(p + base)[q] = u[q];
+            }
+        } else {
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (base + i * 32 < F) p[base + i * 32] = e[i];
+        }
     }
-}
+};
 
 // dG = dH U act'(G), dU = dH act(G).  A CTA covers 256 columns of each half
 // (8 per lane) by slab_rows rows, its warps taking the rows in turn; bound by
-// HBM: 3 reads and 2 writes per element of H.  A thread reads P's elements
-// before it writes dP's, so dP may be P.  Column sums of the FP32 values: per
-// thread over its rows, then over the warps in order, then over the slabs by
-// glu_dbias_kernel.  The stores of dP are kept in L2 (the products read it next).
-template <typename T, typename PT, bool SUMS>
-__global__ void __launch_bounds__(32 * kGluBackWarps)
+// HBM (3 reads and 2 writes per element of H) once enough loads are in flight:
+// each warp issues those of kGluBackRows rows before it works on them.  A
+// thread reads P's elements before it writes dP's, so dP may be P.  Column
+// sums of the FP32 values: per thread over its rows, then over the warps in
+// order, then over the slabs by glu_dbias_kernel.
+template <typename T, typename PT, bool VEC, bool SUMS>
+__global__ void __launch_bounds__(32 * kGluBackWarps, VEC ? 4 : 2)
     glu_back_kernel(const __grid_constant__ GluBackParams p) {
     __shared__ float red[SUMS ? kGluBackWarps : 1][SUMS ? 512 : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool vec = p.vec != 0;
     const int64_t col0 = static_cast<int64_t>(blockIdx.x) * 256;
-    const int64_t base = col0 + (vec ? lane * 8 : lane);
+    const int64_t base = col0 + (VEC ? lane * 8 : lane);
     const int64_t row0 = static_cast<int64_t>(blockIdx.y) * p.slab_rows;
     int64_t row1 = row0 + p.slab_rows;
     if (row1 > p.M) row1 = p.M;
     grid_dependency_wait();
-    float sg[8], su[8];
-    #pragma unroll
-    for (int e = 0; e < 8; ++e) sg[e] = su[e] = 0.0f;
-    #pragma unroll 2
-    for (int64_t r = row0 + warp; r < row1; r += kGluBackWarps) {
-        float h[8], g[8], u[8];
-        const PT* prow = static_cast<const PT*>(p.P) + r * p.ldp;
-        T* drow = static_cast<T*>(p.dP) + r * p.lddp;
-        glu_load8<T>(static_cast<const T*>(p.dH) + r * p.lddh, vec, base, p.F, h);
-        glu_load8<PT>(prow, vec, base, p.F, g);
-        glu_load8<PT>(prow + p.F, vec, base, p.F, u);
-        float a[8], d[8];
-        act_and_slope8(p.act, g, a, d);
+    float sg[SUMS ? 8 : 1], su[SUMS ? 8 : 1];
+    if constexpr (SUMS) {
         #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            g[e] = h[e] * u[e] * d[e];
-            u[e] = h[e] * a[e];
-            if constexpr (SUMS) {
-                sg[e] += g[e];
-                su[e] += u[e];
+        for (int e = 0; e < 8; ++e) sg[e] = su[e] = 0.0f;
+    }
+    for (int64_t r = row0 + warp; r < row1; r += kGluBackWarps * kGluBackRows) {
+        Raw8<T, VEC> h[kGluBackRows];
+        Raw8<PT, VEC> gu[kGluBackRows][2];
+        #pragma unroll
+        for (int k = 0; k < kGluBackRows; ++k) {
+            const int64_t rk = r + k * kGluBackWarps;
+            if (rk < row1) {
+                const PT* prow = static_cast<const PT*>(p.P) + rk * p.ldp;
+                h[k].load(static_cast<const T*>(p.dH) + rk * p.lddh, base, p.F);
+                gu[k][0].load(prow, base, p.F);
+                gu[k][1].load(prow + p.F, base, p.F);
             }
         }
-        glu_store8<T>(drow, vec, base, p.F, g);
-        glu_store8<T>(drow + p.F, vec, base, p.F, u);
+        #pragma unroll
+        for (int k = 0; k < kGluBackRows; ++k) {
+            const int64_t rk = r + k * kGluBackWarps;
+            if (rk >= row1) break;
+            float g[8], a[8], d[8];
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] = glu_to_f<PT>(gu[k][0].e[e]);
+            act_and_slope8(p.act, g, a, d);
+            Raw8<T, VEC> og, ou;
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float x = glu_to_f<T>(h[k].e[e]);
+                const float dg = x * glu_to_f<PT>(gu[k][1].e[e]) * d[e], du = x * a[e];
+                og.e[e] = glu_from_f<T>(dg);
+                ou.e[e] = glu_from_f<T>(du);
+                if constexpr (SUMS) {
+                    sg[e] += dg;                       // (columns past F are not looked at)
+                    su[e] += du;
+                }
+            }
+            T* drow = static_cast<T*>(p.dP) + rk * p.lddp;
+            og.store(drow, base, p.F);
+            ou.store(drow + p.F, base, p.F);
+            if (!VEC && p.dPa != nullptr) {
+                T* arow = static_cast<T*>(p.dPa) + rk * p.ldpa;
+                og.store(arow, base, p.F);
+                ou.store(arow + p.F, base, p.F);
+            }
+        }
     }
     if constexpr (SUMS) {
         #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int c = vec ? lane * 8 + e : lane + e * 32;
+            const int c = VEC ? lane * 8 + e : lane + e * 32;
             red[warp][c] = sg[e];
             red[warp][256 + c] = su[e];
         }
@@ -202,19 +219,130 @@ __global__ void __launch_bounds__(32 * kGluBackWarps)
     }
 }
 
-// dbias = sum over the slabs, in order.
-static __global__ void __launch_bounds__(256)
+// dbias = sum over the slabs: 32 columns per CTA, 32 lines of threads that
+// take the slabs in turn and are added in line order.
+static __global__ void __launch_bounds__(1024)
     glu_dbias_kernel(const float* __restrict__ partials, int32_t slabs, int64_t cols, void* dbias,
                      int32_t dtype) {
+    __shared__ float red[32][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + tx;
     grid_dependency_wait();
-    const int64_t c = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (c >= cols) return;
     float t = 0.0f;
-    #pragma unroll 8
-    for (int32_t s = 0; s < slabs; ++s) t += partials[static_cast<int64_t>(s) * cols + c];
+    if (c < cols) {
+        #pragma unroll 4
+        for (int32_t s = ty; s < slabs; s += 32) t += partials[static_cast<int64_t>(s) * cols + c];
+    }
+    red[ty][tx] = t;
+    __syncthreads();
+    if (ty != 0 || c >= cols) return;
+    t = 0.0f;
+    #pragma unroll
+    for (int y = 0; y < 32; ++y) t += red[y][tx];
     if (dtype == 2) static_cast<float*>(dbias)[c] = t;
     else if (dtype == 1) static_cast<__nv_bfloat16*>(dbias)[c] = __float2bfloat16_rn(t);
     else static_cast<__half*>(dbias)[c] = __float2half_rn(t);
+}
+
+// -------------------------------------------------------- a few tokens (decode)
+
+struct GluDotParams {
+    const void* X; int64_t ldx;
+    const void* W; int64_t ldw;
+    void* H; int64_t ldh;
+    void* P; int64_t ldp;
+    const void* bias;
+    int32_t bias_dtype, act, h_dtype;
+    int32_t F, K;
+};
+
+constexpr int kGluDotThreads = 256;
+constexpr int kGluDotCtas = 4;          // per SM
+constexpr int kGluDotAhead = 4;         // 256-element pieces of both rows in flight per warp
+
+__device__ __forceinline__ void glu_put(void* p, int32_t dtype, int64_t i, float v) {
+    if (dtype == 2) static_cast<float*>(p)[i] = v;
+    else if (dtype == 1) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
+
+// The gated layer of MT tokens (1 to 4): bound by the stream of W.  A warp
+// takes one gate row and its up row at a time, 16 bytes per lane and load,
+// kGluDotAhead pieces of both rows in flight; X (a few KB) comes from L1.
+// Against the tensor-core path there is no tile to fill, no pipeline to start
+// and no split of K to join: what a problem of a few microseconds spends its
+// time on.  FP32 sums in pairs, joined over the lanes by a butterfly.
+// K is a multiple of 8; rows of X and W are 16-byte aligned.
+template <typename T, int MT>
+__global__ void __launch_bounds__(kGluDotThreads, kGluDotCtas)
+    glu_dot_kernel(const __grid_constant__ GluDotParams p) {
+    const int lane = threadIdx.x & 31;
+    const int32_t warp = static_cast<int32_t>(blockIdx.x) * (kGluDotThreads / 32) +
+                         static_cast<int32_t>(threadIdx.x >> 5);
+    const int32_t warps = static_cast<int32_t>(gridDim.x) * (kGluDotThreads / 32);
+    const T* X = static_cast<const T*>(p.X);
+    grid_dependency_wait();
+    grid_dependents_launch();
+    for (int32_t f = warp; f < p.F; f += warps) {
+        const T* wg = static_cast<const T*>(p.W) + static_cast<int64_t>(f) * p.ldw;
+        const T* wu = wg + static_cast<int64_t>(p.F) * p.ldw;
+        F2 ag[MT], au[MT];
+        #pragma unroll
+        for (int m = 0; m < MT; ++m) ag[m] = au[m] = mk2(0.0f);
+        for (int32_t k0 = lane * 8; k0 < p.K; k0 += 256 * kGluDotAhead) {
+            uint4 g[kGluDotAhead], u[kGluDotAhead];
+            #pragma unroll
+            for (int i = 0; i < kGluDotAhead; ++i) {
+                const int32_t k = k0 + i * 256;
+                const bool in = k < p.K;
+                g[i] = in ? __ldcs(reinterpret_cast<const uint4*>(wg + k)) : make_uint4(0u, 0u, 0u, 0u);
+                u[i] = in ? __ldcs(reinterpret_cast<const uint4*>(wu + k)) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            #pragma unroll
+            for (int i = 0; i < kGluDotAhead; ++i) {
+                const int32_t k = k0 + i * 256;
+                if (k >= p.K) break;
+                const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+                const uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                #pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(X + m * p.ldx + k));
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                    #pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const F2 xv = unpack2<T>(xw[q]);
+                        ag[m] = fma2(unpack2<T>(gw[q]), xv, ag[m]);
+                        au[m] = fma2(unpack2<T>(uw[q]), xv, au[m]);
+                    }
+                }
+            }
+        }
+        float mine_g = 0.0f, mine_u = 0.0f;              // lane m keeps token m's sums
+        #pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float sg = sum2(ag[m]), su = sum2(au[m]);
+            #pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                sg += __shfl_xor_sync(0xffffffffu, sg, o);
+                su += __shfl_xor_sync(0xffffffffu, su, o);
+            }
+            if (lane == m) {
+                mine_g = sg;
+                mine_u = su;
+            }
+        }
+        if (lane < MT) {
+            if (p.bias != nullptr) {
+                mine_g += load_bias_elem(p.bias, p.bias_dtype, f);
+                mine_u += load_bias_elem(p.bias, p.bias_dtype, static_cast<int64_t>(p.F) + f);
+            }
+            if (p.P != nullptr) {
+                glu_put(p.P, p.h_dtype, lane * p.ldp + f, mine_g);
+                glu_put(p.P, p.h_dtype, lane * p.ldp + p.F + f, mine_u);
+            }
+            glu_put(p.H, p.h_dtype, lane * p.ldh + f, activate(p.act, mine_g) * mine_u);
+        }
+    }
 }
 
 }  // namespace gemm103

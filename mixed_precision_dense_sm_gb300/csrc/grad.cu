@@ -112,11 +112,11 @@ __device__ __forceinline__ double batch_sum(const uint4 (&v)[kVecs]) {
     for (int q = 0; q < kVecs; ++q) any |= v[q].x | v[q].y | v[q].z | v[q].w;
     if (any == 0) return 0.0;
     double d = 0.0;
-    #pragma unroll 1
+    #pragma unroll                      // (indexed by constants: the batch stays in registers)
     for (int q = 0; q < kVecs; ++q) {
         Vec16<T> w;
         w.u = v[q];
-        #pragma unroll 1
+        #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             const double x = static_cast<double>(to_f<T>(w.e[e]));
             d = fma(x, x, d);
@@ -145,7 +145,7 @@ __device__ __forceinline__ double chunk_sum(const T* p, int32_t n) {
         #pragma unroll
         for (int q = 0; q < kVecs; ++q) {
             const int32_t k = i + q * kThreads;
-            r[q] = k < nvec ? __ldg(v + k) : make_uint4(0u, 0u, 0u, 0u);
+            r[q] = k < nvec ? __ldcg(v + k) : make_uint4(0u, 0u, 0u, 0u);
         }
         acc += batch_sum<T>(r);
     }

@@ -22,6 +22,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "f32x2.cuh"
 #include "ptx.cuh"
 
 namespace gemm103 {
@@ -73,71 +74,12 @@ struct Params {
 
 // ------------------------------------------------------------------ elements
 
-// Two FP32 values in a 64-bit register: the packed FP32 instructions do two
-// lanes' work in one issue slot, and these kernels were bound by issue slots
-// (64 instructions per element in scalar form, about 12 in this one).
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 mk2(float lo, float hi) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ F2 mk2(float x) { return mk2(x, x); }
-__device__ __forceinline__ void get2(F2 a, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    F2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-__device__ __forceinline__ float sum2(F2 a) {
-    float lo, hi;
-    get2(a, lo, hi);
-    return lo + hi;
-}
-
 // 8 consecutive or strided elements as 4 pairs.
 typedef F2 F8[4];
 
 __device__ __forceinline__ void set8(F8& o, float x) {
     #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = mk2(x);
-}
-
-// A pair of 16-bit elements (low half first) as FP32, and back, rounded.
-template <typename E> __device__ __forceinline__ F2 unpack2(uint32_t w);
-template <> __device__ __forceinline__ F2 unpack2<__nv_bfloat16>(uint32_t w) {
-    return mk2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-template <> __device__ __forceinline__ F2 unpack2<__half>(uint32_t w) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
-    return mk2(f.x, f.y);
-}
-template <typename E> __device__ __forceinline__ uint32_t pack2(F2 a);
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(F2 a) {
-    float lo, hi;
-    get2(a, lo, hi);
-    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <> __device__ __forceinline__ uint32_t pack2<__half>(F2 a) {
-    float lo, hi;
-    get2(a, lo, hi);
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // Where a thread's 8 elements of chunk c lie in the row: element e at
