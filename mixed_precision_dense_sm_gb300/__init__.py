@@ -669,22 +669,20 @@ def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace
     norm = inv_scale * sqrt(sum of all g^2) returned as a 1-element FP32
     tensor.  A norm that is not finite clips nothing."""
     dev = _device(grads[0], "gradients") if len(grads) else torch.cuda.current_device()
-    ptrs, sizes, codes = [], [], []
-    for g in grads:
-        if g.get_device() != dev or not g.is_contiguous():
-            raise ValueError("gradients must be contiguous, on the current CUDA device")
-        ptrs.append(g.data_ptr())
-        sizes.append(g.numel())
-        codes.append(_CODE[g.dtype])
+    T = torch.Tensor                      # (mapped methods: a list may hold hundreds of tensors)
+    if not set(map(T.get_device, grads)) <= {dev} or not all(map(T.is_contiguous, grads)):
+        raise ValueError("gradients must be contiguous, on the current CUDA device")
+    ptrs, sizes = list(map(T.data_ptr, grads)), list(map(T.numel, grads))
+    dtypes = [g.dtype for g in grads]
+    codes = [_CODE[t] for t in dtypes]
     outs = None
     if outputs is not None:
         if len(outputs) != len(grads):
             raise ValueError("as many outputs as gradients")
-        outs = []
-        for o, n, c in zip(outputs, sizes, codes):
-            if o.numel() != n or _CODE.get(o.dtype) != c or o.get_device() != dev or not o.is_contiguous():
-                raise ValueError("an output must be contiguous, of its gradient's dtype, size and device")
-            outs.append(o.data_ptr())
+        if list(map(T.numel, outputs)) != sizes or [o.dtype for o in outputs] != dtypes or \
+                not set(map(T.get_device, outputs)) <= {dev} or not all(map(T.is_contiguous, outputs)):
+            raise ValueError("an output must be contiguous, of its gradient's dtype, size and device")
+        outs = list(map(T.data_ptr, outputs))
     other = None if stream is None else torch.cuda.ExternalStream(stream)
     if norm is None:
         norm = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", dev))

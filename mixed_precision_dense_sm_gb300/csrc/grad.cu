@@ -7,8 +7,9 @@
 // partial sum.  apply_kernel adds the partial sums (every CTA the same way:
 // a few hundred FP64 values out of L2, cheaper than a third launch or a
 // grid-wide wait), CTA 0 writes the norm, and each CTA scales its chunks.  The
-// second pass walks the chunks in the opposite order, so what the first pass
-// left in L2 is found there.  Bound by HBM: two reads and one write of the
+// second pass gives each CTA the chunks it had in the first, in the opposite
+// order, so what the first pass left last in L2 (in the half of it that
+// belongs to the CTA's die) is found there.  Bound by HBM: two reads and one write of the
 // gradients (one read where nothing is scaled in place, or where they fit in
 // L2).
 //
@@ -36,9 +37,9 @@ namespace {
 using namespace gemm103;
 
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 6;
+constexpr int kCtasPerSm = 4;                  // all resident at once
 constexpr int kVecs = 4;                       // 16-byte vectors per thread and batch
-constexpr int64_t kChunk = 16384;              // elements per chunk
+constexpr int64_t kChunk = 8192;               // elements per chunk
 constexpr int kPerLaunch = GRAD_TENSORS_PER_LAUNCH;
 
 template <int CAP>
@@ -174,7 +175,7 @@ __device__ __forceinline__ double cta_sum(double v, double* red) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     norm_partial_kernel(const __grid_constant__ Tensors<CAP> t, double* __restrict__ partials) {
     __shared__ double red[kThreads / 32];
     grid_dependency_wait();
@@ -242,7 +243,7 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int32_t n, float f
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     apply_kernel(const __grid_constant__ Tensors<CAP> t, const ApplyParams a) {
     __shared__ double red[kThreads / 32];
     grid_dependency_wait();
@@ -256,8 +257,12 @@ __global__ void __launch_bounds__(kThreads)
         f *= static_cast<double>(a.max_norm) / norm;
     const float factor = static_cast<float>(f);
     const int32_t chunks = t.first_chunk[t.count];
-    for (int32_t r = blockIdx.x; r < chunks; r += gridDim.x) {
-        const int32_t c = chunks - 1 - r;
+    // this CTA's chunks of the first pass, the last one first
+    const int32_t mine = chunks > static_cast<int32_t>(blockIdx.x)
+                             ? (chunks - 1 - static_cast<int32_t>(blockIdx.x)) / static_cast<int32_t>(gridDim.x)
+                             : -1;
+    for (int32_t r = mine; r >= 0; --r) {
+        const int32_t c = static_cast<int32_t>(blockIdx.x) + r * static_cast<int32_t>(gridDim.x);
         const int k = find_tensor(t, c);
         if (factor == 1.0f && t.dst[k] == t.src[k]) continue;
         const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * kChunk;

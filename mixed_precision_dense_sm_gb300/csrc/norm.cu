@@ -125,13 +125,16 @@ int64_t smem_for(const Params& p, int chunks8, int groups, int stages) {
            static_cast<int64_t>(groups) * stages * p.slot_bytes;
 }
 
-// Groups per CTA and slots per group: the most rows in flight per SM among
-// CTAs of up to `most` threads whose threads all fit an SM's `resident`, with
-// a second slot where it fits; the smallest such CTA.  Returns CTAs per SM (at
-// most `per_sm`), 0 where nothing fits.
+// Groups per CTA and slots per group: the most rows worked on per SM among
+// CTAs of up to `most` threads, all resident within `resident` threads, that
+// have a second slot per group; of those the deepest rings, then the smallest
+// CTA.  One slot only where two fit nowhere.  Returns CTAs per SM (at most
+// `per_sm`), 0 where nothing fits.
 int choose_cta(Params& p, int chunks8, int most, int resident, int per_sm, int& groups) {
-    int best = 0, ctas = 0;
-    for (int stages = kMaxStages; stages >= 1 && best == 0; --stages) {
+    int64_t best = 0;
+    int ctas = 0;
+    for (int stages = kMaxStages; stages >= 1; --stages) {
+        if (stages == 1 && best > 0) break;
         // (named barriers number the groups of more than a warp: 15 at most)
         for (int g = 1; g * p.T <= most && (g <= 15 || p.T == 32); g *= 2) {
             const int64_t bytes = smem_for(p, chunks8, g, stages);
@@ -139,8 +142,8 @@ int choose_cta(Params& p, int chunks8, int most, int resident, int per_sm, int& 
             int64_t n = kSmemPerSm / (bytes + 1024);
             if (n > resident / (g * p.T)) n = resident / (g * p.T);
             if (n > per_sm) n = per_sm;
-            if (n > 0 && n * g > best) {
-                best = static_cast<int>(n * g);
+            if (n * g > best) {
+                best = n * g;
                 ctas = static_cast<int>(n);
                 groups = g;
                 p.stages = stages;
@@ -237,7 +240,7 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     p.slot_bytes = static_cast<uint32_t>(l.chunks8 * 8 * p.T * (esize(x_dtype) + (Z ? esize(z_dtype) : 0)));
     int groups = 1;
     // 64 registers per thread
-    const int ctas = choose_cta(p, l.chunks8, p.T > 512 ? p.T : 512, 1024, 32, groups);
+    const int ctas = choose_cta(p, l.chunks8, 1024, 1024, 32, groups);
     if (ctas == 0) return GEMM_ERR_NOT_SUPPORTED;
     const Chunks ch = chunks_for(M, Z && block->gate ? block->gate_rows : 1,
                                  static_cast<int64_t>(sms) * ctas / p.cluster);

@@ -29,7 +29,7 @@ namespace gemm103 {
 namespace nrm {
 
 enum : int { kNone = 0, kRms = 1, kLayer = 2 };
-constexpr int kMaxStages = 2;
+constexpr int kMaxStages = 3;
 constexpr int kBackThreads = 512;    // of a backward CTA: 128 registers each, one CTA per SM
 
 struct Params {
@@ -82,6 +82,19 @@ __device__ __forceinline__ void set8(F8& o, float x) {
     for (int q = 0; q < 4; ++q) o[q] = mk2(x);
 }
 
+__device__ __forceinline__ void set8(F8& o, float4 a, float4 b) {
+    o[0] = mk2(a.x, a.y);
+    o[1] = mk2(a.z, a.w);
+    o[2] = mk2(b.x, b.y);
+    o[3] = mk2(b.z, b.w);
+}
+__device__ __forceinline__ float4 join2(F2 a, F2 b) {
+    float4 r;
+    get2(a, r.x, r.y);
+    get2(b, r.z, r.w);
+    return r;
+}
+
 // Where a thread's 8 elements of chunk c lie in the row: element e at
 // base + e with VEC (all 8 of them inside the row or none), else at
 // base + 32 e.
@@ -106,9 +119,8 @@ __device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool w
                                             int32_t N, F8& o) {
     if (VEC && wide) {
         if (dtype == 2) {
-            const ulonglong2* p = reinterpret_cast<const ulonglong2*>(static_cast<const float*>(v) + s.base);
-            const ulonglong2 a = __ldg(p), b = __ldg(p + 1);
-            o[0].v = a.x; o[1].v = a.y; o[2].v = b.x; o[3].v = b.y;
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(v) + s.base);
+            set8(o, __ldg(p), __ldg(p + 1));
         } else {
             const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(v) + s.base));
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -273,9 +285,7 @@ template <typename E>
 __device__ __forceinline__ void take8(uint8_t* slot, int T, int t, int c, F8& o) {
     const uint8_t* d = slot_at<E>(slot, T, t, c);
     if constexpr (sizeof(E) == 4) {
-        const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(d);
-        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(d + T * 16);
-        o[0].v = a.x; o[1].v = a.y; o[2].v = b.x; o[3].v = b.y;
+        set8(o, *reinterpret_cast<const float4*>(d), *reinterpret_cast<const float4*>(d + T * 16));
     } else {
         const uint4 u = *reinterpret_cast<const uint4*>(d);
         o[0] = unpack2<E>(u.x);
@@ -291,8 +301,8 @@ template <typename E, bool VEC, bool KEEP = false>
 __device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, F8& v) {
     if constexpr (sizeof(E) == 4) {
         if constexpr (VEC) {
-            *reinterpret_cast<ulonglong2*>(row + s.base) = make_ulonglong2(v[0].v, v[1].v);
-            *reinterpret_cast<ulonglong2*>(row + s.base + 4) = make_ulonglong2(v[2].v, v[3].v);
+            *reinterpret_cast<float4*>(row + s.base) = join2(v[0], v[1]);
+            *reinterpret_cast<float4*>(row + s.base + 4) = join2(v[2], v[3]);
         } else {
             #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -440,8 +450,8 @@ __device__ __forceinline__ void fill_vectors(const Params& p, const Group<TT>& g
             if (!sp.some(p.N)) continue;
             auto put = [&](int k, const F8& v) {
                 uint8_t* d = slot_at<float>(par_at<C>(par, k, g.T()), g.T(), g.t, c);
-                *reinterpret_cast<ulonglong2*>(d) = make_ulonglong2(v[0].v, v[1].v);
-                *reinterpret_cast<ulonglong2*>(d + g.T() * 16) = make_ulonglong2(v[2].v, v[3].v);
+                *reinterpret_cast<float4*>(d) = join2(v[0], v[1]);
+                *reinterpret_cast<float4*>(d + g.T() * 16) = join2(v[2], v[3]);
             };
             F8 gs, v;                               // scale * gate
             set8(gs, p.token_gate ? 1.0f : p.scale);
@@ -1024,11 +1034,12 @@ static __global__ void __launch_bounds__(32 * kSumY)
         for (int k = 0; k < 4; ++k) a[k] = 0.0f;
         if (in) {
             const float* base = p.partials + col;
+            const float one = gated && p.groups == 1 ? param_elem(p.gate, p.vec_dtype, col, 1.0f) : 1.0f;
             #pragma unroll 4
             for (int32_t c = first + ty; c < last; c += kSumY) {
                 const float* q = base + static_cast<int64_t>(c) * p.N;
-                float gt = 1.0f;
-                if (gated && p.gate != nullptr)
+                float gt = one;
+                if (gated && p.gate != nullptr && p.groups > 1)
                     gt = param_elem(p.gate, p.vec_dtype, (c / p.chunks_per_group) * p.ld_gate + col, 1.0f);
                 a[0] += q[0];
                 a[1] = fmaf(gt, q[p.part_stride], a[1]);
