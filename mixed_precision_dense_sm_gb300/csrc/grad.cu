@@ -2,14 +2,14 @@
 // (include/grad_sm103.h).
 //
 // Two kernels.  norm_partial_kernel reads every element once: the tensors are
-// cut into chunks of kChunk elements, numbered through all of a launch's
+// cut into chunks of 8192 or 16384 elements, numbered through all of a launch's
 // tensors, and CTA b takes chunks b, b + grid, ...; each CTA leaves one FP64
 // partial sum.  apply_kernel adds the partial sums (every CTA the same way:
 // a few hundred FP64 values out of L2, cheaper than a third launch or a
 // grid-wide wait), CTA 0 writes the norm, and each CTA scales its chunks.  The
-// second pass gives each CTA the chunks it had in the first, in the opposite
-// order, so what the first pass left last in L2 (in the half of it that
-// belongs to the CTA's die) is found there.  Bound by HBM: two reads and one write of the
+// second pass walks the chunks in the opposite order, each SM those it had in
+// the first (the grids are multiples of the SMs), and what the first pass read
+// last it marked to stay in L2 (kKeepBytes).  Bound by HBM: two reads and one write of the
 // gradients (one read where nothing is scaled in place, or where they fit in
 // L2).
 //
@@ -37,9 +37,16 @@ namespace {
 using namespace gemm103;
 
 constexpr int kThreads = 256;
-constexpr int kCtasPerSm = 4;                  // all resident at once
+constexpr int kSumCtas = 6;                    // per SM, all resident at once
+constexpr int kApplyCtas = 3;                  // (4 would spill: 122 against 112 us for 120M bf16)
 constexpr int kVecs = 4;                       // 16-byte vectors per thread and batch
-constexpr int64_t kChunk = 8192;               // elements per chunk
+// Elements per chunk; the smaller where the larger would give an SM fewer than
+// four (60 FP32 tensors of 900k elements in all: 14.5 us by 16384, 12.4 by
+// 8192, 18.6 by 2048).
+constexpr int32_t kMostChunk = 16384, kLeastChunk = 8192;
+// About this much of what is read last is kept in L2 for the second pass, the
+// rest makes room for it (0 to 100 MB measured: 115, 112, 115 us at 0, 64, 96 MB).
+constexpr int64_t kKeepBytes = 64 << 20;
 constexpr int kPerLaunch = GRAD_TENSORS_PER_LAUNCH;
 
 template <int CAP>
@@ -50,6 +57,7 @@ struct Tensors {
     int32_t first_chunk[CAP + 1];              // chunks before tensor t; [count] = all
     uint8_t dtype[CAP];
     int32_t count;
+    int32_t chunk;                             // elements per chunk
 };
 
 struct ApplyParams {
@@ -91,15 +99,35 @@ union Vec16 {
     T e[16 / sizeof(T)];
 };
 
-// The sum of squares of a batch (see above).
+// A batch again in FP64, from memory: rare, and out of line so that it costs
+// the fast path no registers.
 template <typename T>
-__device__ __forceinline__ double batch_sum(const uint4 (&v)[kVecs]) {
+__device__ __noinline__ double batch_again(const uint4* v, int32_t i, int32_t nvec) {
+    double d = 0.0;
+    for (int q = 0; q < kVecs; ++q) {
+        const int32_t k = i + q * kThreads;
+        if (k >= nvec) break;
+        Vec16<T> w;
+        w.u = v[k];
+        #pragma unroll
+        for (int e = 0; e < static_cast<int>(16 / sizeof(T)); ++e) {
+            const double x = static_cast<double>(to_f<T>(w.e[e]));
+            d = fma(x, x, d);
+        }
+    }
+    return d;
+}
+
+// The sum of squares of a batch (see above): vectors i, i + kThreads, ... of v.
+template <typename T>
+__device__ __forceinline__ double batch_sum(const uint4 (&r)[kVecs], const uint4* v, int32_t i,
+                                            int32_t nvec) {
     constexpr int kPer = 16 / sizeof(T);
     float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     #pragma unroll
     for (int q = 0; q < kVecs; ++q) {
         Vec16<T> w;
-        w.u = v[q];
+        w.u = r[q];
         #pragma unroll
         for (int e = 0; e < kPer; ++e) {
             const float x = to_f<T>(w.e[e]);
@@ -110,20 +138,8 @@ __device__ __forceinline__ double batch_sum(const uint4 (&v)[kVecs]) {
     if (t >= 0x1p-90f && t < 0x1p127f) return static_cast<double>(t);
     uint32_t any = 0;
     #pragma unroll
-    for (int q = 0; q < kVecs; ++q) any |= v[q].x | v[q].y | v[q].z | v[q].w;
-    if (any == 0) return 0.0;
-    double d = 0.0;
-    #pragma unroll                      // (indexed by constants: the batch stays in registers)
-    for (int q = 0; q < kVecs; ++q) {
-        Vec16<T> w;
-        w.u = v[q];
-        #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const double x = static_cast<double>(to_f<T>(w.e[e]));
-            d = fma(x, x, d);
-        }
-    }
-    return d;
+    for (int q = 0; q < kVecs; ++q) any |= r[q].x | r[q].y | r[q].z | r[q].w;
+    return any == 0 ? 0.0 : batch_again<T>(v, i, nvec);
 }
 
 // Elements of a chunk before its first 16-byte boundary (at most n).
@@ -134,8 +150,17 @@ __device__ __forceinline__ int32_t head_of(const T* p, int32_t n) {
     return h < n ? h : n;
 }
 
+// 16 bytes with an L2 policy.
+__device__ __forceinline__ uint4 load_hint(const uint4* p, uint64_t policy) {
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0, %1, %2, %3}, [%4], %5;"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p), "l"(policy));
+    return r;
+}
+
 template <typename T>
-__device__ __forceinline__ double chunk_sum(const T* p, int32_t n) {
+__device__ __forceinline__ double chunk_sum(const T* p, int32_t n, uint64_t policy) {
     constexpr int kPer = 16 / sizeof(T);
     const int32_t head = head_of(p, n);
     const int32_t nvec = (n - head) / kPer;
@@ -146,9 +171,9 @@ __device__ __forceinline__ double chunk_sum(const T* p, int32_t n) {
         #pragma unroll
         for (int q = 0; q < kVecs; ++q) {
             const int32_t k = i + q * kThreads;
-            r[q] = k < nvec ? __ldcg(v + k) : make_uint4(0u, 0u, 0u, 0u);
+            r[q] = k < nvec ? load_hint(v + k, policy) : make_uint4(0u, 0u, 0u, 0u);
         }
-        acc += batch_sum<T>(r);
+        acc += batch_sum<T>(r, v, i, nvec);
     }
     // the elements before and behind the vectors: at most 14
     const int32_t tail0 = head + nvec * kPer;
@@ -175,24 +200,27 @@ __device__ __forceinline__ double cta_sum(double v, double* red) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, kSumCtas)
     norm_partial_kernel(const __grid_constant__ Tensors<CAP> t, double* __restrict__ partials) {
     __shared__ double red[kThreads / 32];
     grid_dependency_wait();
     grid_dependents_launch();
     const int32_t chunks = t.first_chunk[t.count];
     double acc = 0.0;
+    const uint64_t last = l2_policy_evict_last(), early = l2_policy_evict_first();
     for (int32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
         const int k = find_tensor(t, c);
-        const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * kChunk;
+        const int64_t behind = static_cast<int64_t>(chunks - c) * t.chunk * (t.dtype[k] == GEMM_F32 ? 4 : 2);
+        const uint64_t pol = behind <= kKeepBytes ? last : early;
+        const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * t.chunk;
         const int64_t left = t.size[k] - at;
-        const int32_t n = static_cast<int32_t>(left < kChunk ? left : kChunk);
+        const int32_t n = static_cast<int32_t>(left < t.chunk ? left : t.chunk);
         if (t.dtype[k] == GEMM_F32)
-            acc += chunk_sum(static_cast<const float*>(t.src[k]) + at, n);
+            acc += chunk_sum(static_cast<const float*>(t.src[k]) + at, n, pol);
         else if (t.dtype[k] == GEMM_BF16)
-            acc += chunk_sum(static_cast<const __nv_bfloat16*>(t.src[k]) + at, n);
+            acc += chunk_sum(static_cast<const __nv_bfloat16*>(t.src[k]) + at, n, pol);
         else
-            acc += chunk_sum(static_cast<const __half*>(t.src[k]) + at, n);
+            acc += chunk_sum(static_cast<const __half*>(t.src[k]) + at, n, pol);
     }
     const double s = cta_sum(acc, red);
     if (threadIdx.x == 0) partials[blockIdx.x] = s;
@@ -243,7 +271,7 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int32_t n, float f
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__(kThreads, kApplyCtas)
     apply_kernel(const __grid_constant__ Tensors<CAP> t, const ApplyParams a) {
     __shared__ double red[kThreads / 32];
     grid_dependency_wait();
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         f *= static_cast<double>(a.max_norm) / norm;
     const float factor = static_cast<float>(f);
     const int32_t chunks = t.first_chunk[t.count];
-    // this CTA's chunks of the first pass, the last one first
+    // this CTA's chunks, the last one first
     const int32_t mine = chunks > static_cast<int32_t>(blockIdx.x)
                              ? (chunks - 1 - static_cast<int32_t>(blockIdx.x)) / static_cast<int32_t>(gridDim.x)
                              : -1;
@@ -265,9 +293,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         const int32_t c = static_cast<int32_t>(blockIdx.x) + r * static_cast<int32_t>(gridDim.x);
         const int k = find_tensor(t, c);
         if (factor == 1.0f && t.dst[k] == t.src[k]) continue;
-        const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * kChunk;
+        const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * t.chunk;
         const int64_t left = t.size[k] - at;
-        const int32_t n = static_cast<int32_t>(left < kChunk ? left : kChunk);
+        const int32_t n = static_cast<int32_t>(left < t.chunk ? left : t.chunk);
         if (t.dtype[k] == GEMM_F32)
             chunk_scale(static_cast<const float*>(t.src[k]) + at, static_cast<float*>(t.dst[k]) + at,
                         n, factor);
@@ -300,7 +328,7 @@ int64_t launches_for(int64_t count) { return (count + kPerLaunch - 1) / kPerLaun
 
 int64_t workspace_for(int64_t count, int32_t sms) {
     const int64_t l = launches_for(count);
-    return (l < 1 ? 1 : l) * static_cast<int64_t>(sms) * kCtasPerSm * 8;
+    return (l < 1 ? 1 : l) * static_cast<int64_t>(sms) * kSumCtas * 8;
 }
 
 cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute* attr) {
@@ -324,7 +352,7 @@ struct Call {
     float max_norm, inv_scale;
     float* norm;
     double* partials;
-    int max_grid;
+    int sms;
     cudaStream_t stream;
 };
 
@@ -341,7 +369,7 @@ void fill(Tensors<CAP>& t, const Call& c, int64_t first, int64_t n) {
         t.size[k] = c.sizes[i];
         t.dtype[k] = static_cast<uint8_t>(c.dtypes[i]);
         t.first_chunk[k] = chunk;
-        chunk += static_cast<int32_t>((c.sizes[i] + kChunk - 1) / kChunk);
+        chunk += static_cast<int32_t>((c.sizes[i] + t.chunk - 1) / t.chunk);
     }
     t.first_chunk[t.count] = chunk;
 }
@@ -358,9 +386,14 @@ cudaError_t run(const Call& c) {
         for (int64_t l = 0; l < parts; ++l) {
             const int64_t first = l * CAP;
             const int64_t n = c.count - first < CAP ? c.count - first : CAP;
+            int64_t total = 0;
+            for (int64_t i = first; i < first + n; ++i) total += c.sizes[i];
+            t.chunk = kMostChunk;
+            while (t.chunk > kLeastChunk && total / t.chunk < 4 * c.sms) t.chunk /= 2;
             fill(t, c, first, n);
             const int32_t chunks = t.first_chunk[t.count];
-            int grid = chunks < c.max_grid ? chunks : c.max_grid;
+            const int most = c.sms * (pass == 0 ? kSumCtas : kApplyCtas);
+            int grid = chunks < most ? chunks : most;
             if (pass == 0) {
                 if (grid == 0) continue;
                 cudaLaunchConfig_t cfg = config(grid, c.stream, &attr);
@@ -428,7 +461,7 @@ gemm_status_t grad_clip(int64_t count, const void* const* grads, void* const* ou
     for (int64_t l = 0; l * kPerLaunch < count; ++l) {
         int64_t chunks = 0;
         for (int64_t i = l * kPerLaunch; i < count && i < (l + 1) * kPerLaunch; ++i)
-            chunks += (sizes[i] + kChunk - 1) / kChunk;
+            chunks += (sizes[i] + kLeastChunk - 1) / kLeastChunk;
         if (chunks > (1ll << 30)) return GEMM_ERR_INVALID_VALUE;
     }
     // a tensor listed twice in place would be scaled by two CTAs at once
@@ -450,7 +483,7 @@ gemm_status_t grad_clip(int64_t count, const void* const* grads, void* const* ou
     if (sms == 0) return GEMM_ERR_NOT_SUPPORTED;
     if (workspace_bytes < workspace_for(count, sms)) return GEMM_ERR_INVALID_VALUE;
     const Call c{count, grads, outs, sizes, dtypes, max_norm, inv_scale, norm,
-                 static_cast<double*>(workspace), sms * kCtasPerSm,
+                 static_cast<double*>(workspace), sms,
                  reinterpret_cast<cudaStream_t>(stream)};
     const cudaError_t e = count <= 64 ? run<64>(c) : run<kPerLaunch>(c);
     if (e != cudaSuccess) {
