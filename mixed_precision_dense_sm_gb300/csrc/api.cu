@@ -71,6 +71,7 @@ struct OperandDesc {
     bool pack;          // needs a 16-byte-aligned copy
     bool transpose;     // the copy also transposes (FP32 MN-major -> K-major)
     int64_t packed_ld;
+    int64_t src_cols;   // columns the source has, where the copy pads them with zeros (0: cols)
 };
 
 struct Plan {
@@ -851,7 +852,8 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
         int grid = 1;
         for (int i = 0; i < 2; ++i) {
             pp.d[i] = PackDesc{static_cast<const uint16_t*>(o[i]->ptr), reinterpret_cast<uint16_t*>(dst[i]),
-                               o[i]->ld, o[i]->rows, o[i]->cols, o[i]->packed_ld};
+                               o[i]->ld, o[i]->rows, o[i]->src_cols ? o[i]->src_cols : o[i]->cols,
+                               o[i]->packed_ld};
             const int g = grid_for(o[i]->rows * o[i]->packed_ld / 8, num_sms);
             if (g > grid) grid = g;
         }
@@ -1640,6 +1642,9 @@ gemm_status_t conv2d_fprop(gemm_handle_t h, int64_t N, int64_t H, int64_t W, int
 // ---------------------------------------------------------------------------
 namespace {
 
+// Rows that the GEMM's loads and stores take as they are.
+bool rows_aligned(const void* p, int64_t ld, int64_t es) { return aligned16(p) && ld * es % 16 == 0; }
+
 // Tokens the dot-product kernel takes (its instances go to 4).
 constexpr int64_t kGluDotTokens = 4;
 
@@ -1692,8 +1697,36 @@ gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t l
     // any output row of 2F elements with that alignment stands for H's
     const void* c = M > 0 && F > 0 ? reinterpret_cast<const void*>(static_cast<uintptr_t>(vec ? 256 : es))
                                    : H;
-    return make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, c, round_up(max1(2 * F), 8), dt,
-                     num_sms, smem_optin, pl, true, false, kMaxKc, 3, true, 0, false, true);
+    const int64_t ldc = round_up(max1(2 * F), 8);
+    // Where both operands are copied to aligned rows, the copies are padded
+    // with zeros to whole pairs of K chunks: two chunks per stage, half the
+    // TMA operations.
+    const bool pad = M > 0 && F > 0 && K > 0 && !rows_aligned(X, ldx, 2) && !rows_aligned(W, ldw, 2);
+    if (!pad)
+        return make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, c, ldc, dt, num_sms,
+                         smem_optin, pl, true, false, kMaxKc, 3, true, 0, false, true);
+    const int64_t kp = round_up(K, 128);
+    const void* any = reinterpret_cast<const void*>(static_cast<uintptr_t>(256));
+    const gemm_status_t st = make_plan('N', 'T', M, 2 * F, kp, 1.0f, any, kp, any, kp, 0.0f, c, ldc, dt,
+                                       num_sms, smem_optin, pl, true, false, kMaxKc, 3, true, 0, false, true);
+    if (st != GEMM_OK) return st;
+    const bool sw = pl.pub.swap_ab != 0;
+    OperandDesc* o2[2] = {sw ? &pl.b : &pl.a, sw ? &pl.a : &pl.b};       // X, W
+    const void* ptr[2] = {X, W};
+    const int64_t ld[2] = {ldx, ldw};
+    for (int i = 0; i < 2; ++i) {
+        o2[i]->ptr = ptr[i];
+        o2[i]->ld = ld[i];
+        o2[i]->pack = true;
+        o2[i]->packed_ld = kp;
+        o2[i]->src_cols = K;
+    }
+    pl.pub.pack_a = pl.pub.pack_b = 1;
+    pl.pack_a_bytes = pl.a.rows * kp * 2;
+    pl.pack_b_bytes = pl.b.rows * kp * 2;
+    pl.pub.workspace_bytes = kWsHeaderBytes + round_up(pl.pack_a_bytes, 256) +
+                             round_up(pl.pack_b_bytes, 256) + round_up(pl.partial_bytes, 256);
+    return GEMM_OK;
 }
 
 template <typename OutT>
@@ -1778,9 +1811,6 @@ void launch_glu_back_p(const GluBackParams& p, bool vec, int32_t p_dtype, dim3 g
     else launch_glu_back<T, __nv_bfloat16>(p, vec, grid, stream);
 }
 
-// Rows that the GEMM's loads and stores take as they are.
-bool rows_aligned(const void* p, int64_t ld, int64_t es) { return aligned16(p) && ld * es % 16 == 0; }
-
 // One of the backward pass's products on a workspace whose first `used` bytes
 // behind the counters are the caller's; *need: the bytes behind those.
 struct Product {
@@ -1793,9 +1823,19 @@ struct Product {
     gemm_dtypes_t dt;
 };
 
+// The GEMM's plan; where that is stream-K on less than half the SMs (few wide
+// tiles, too short in K to be split far), the data-parallel plan of smaller
+// tiles if it fills more of them (1000 x 777 from K = 2046, 16 pair tiles
+// against 104 tiles: 22 -> 11 us).
 gemm_status_t plan_product(const gemm_ctx* h, const Product& g, Plan& pl) {
-    return make_plan(g.ta, g.tb, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C, g.ldc, g.dt,
-                     h->num_sms, h->smem_optin, pl);
+    gemm_status_t st = make_plan(g.ta, g.tb, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C,
+                                 g.ldc, g.dt, h->num_sms, h->smem_optin, pl);
+    if (st != GEMM_OK || pl.sk_len == 0 || pl.pub.swap_ab || 2 * pl.pub.grid >= h->num_sms) return st;
+    Plan dp;
+    st = make_plan(g.ta, g.tb, g.M, g.N, g.K, 1.0f, g.A, g.lda, g.B, g.ldb, g.beta, g.C, g.ldc, g.dt,
+                   h->num_sms, h->smem_optin, dp, true, false, kMaxKc, 3, false);
+    if (st == GEMM_OK && dp.pub.grid > 2 * pl.pub.grid) pl = dp;
+    return GEMM_OK;
 }
 
 gemm_status_t enqueue_product(gemm_ctx* h, const Product& g, const Plan& pl, int64_t used,
@@ -1909,7 +1949,8 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
     // (an accumulated dW is read too: it stays in place)
     const bool out_x = some && dx_some && !rows_aligned(o->dX, o->lddx, dx_es);
     const bool out_w = some && dw_some && o->beta_w == 0.0f && !rows_aligned(o->dW, o->lddw, dw_es);
-    const int64_t ldp8 = round_up(2 * F, 8), ldk8 = round_up(K, 8);
+    // the copy of dP is padded with zeros to whole pairs of K chunks
+    const int64_t ldp8 = round_up(2 * F, 128), ldk8 = round_up(K, 8);
     const int64_t at_sums = some && o->dbias ? take(slabs * 2 * F * 4) : 0;
     const int64_t at_p = copy_p ? take(M * ldp8 * 2) : 0;
     const int64_t at_w = copy_w ? take(2 * F * ldk8 * 2) : 0;
@@ -1918,7 +1959,7 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
     const int64_t at_dw = out_w ? take(2 * F * ldk8 * dw_es) : 0;
     // planned with stand-in addresses: only alignment counts
     void* const any = reinterpret_cast<void*>(static_cast<uintptr_t>(256));
-    Product gx{'N', 'N', M, K, 2 * F, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_w ? any : W,
+    Product gx{'N', 'N', M, K, copy_p ? ldp8 : 2 * F, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_w ? any : W,
                copy_w ? ldk8 : ldw, 0.0f, out_x ? any : o->dX, out_x ? ldk8 : o->lddx, xdt};
     Product gw{'T', 'N', 2 * F, K, M, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_x ? any : X,
                copy_x ? ldk8 : ldx, o->beta_w, out_w ? any : o->dW, out_w ? ldk8 : o->lddw, wdt};
@@ -1947,6 +1988,8 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
     if (out_w) gw.C = body + at_dw;
     px.a.ptr = gx.A;
     px.b.ptr = gx.B;
+    // W has 2F rows, whatever dP's copy is padded to: the rest reads zeros
+    if (dx_some) (px.pub.swap_ab ? px.a : px.b).rows = 2 * F;
     pw.a.ptr = gw.A;
     pw.b.ptr = gw.B;
     if (dx_some && px.pub.swap_ab) {
@@ -2002,14 +2045,14 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
         UnpackPair up;
         std::memset(&up, 0, sizeof up);
         int n = 0;
-        int64_t rows = 1;
+        int64_t units = 1;
         auto add = [&](int64_t at, void* dst, int64_t r, int64_t ld, int64_t es) {
             up.d[n++] = UnpackDesc{body + at, dst, ldk8, r, K, ld, static_cast<int32_t>(es)};
-            if (r > rows) rows = r;
+            if (r * ceil_div(K, 256) > units) units = r * ceil_div(K, 256);
         };
         if (out_x) add(at_dx, o->dX, M, o->lddx, dx_es);
         if (out_w) add(at_dw, o->dW, 2 * F, o->lddw, dw_es);
-        int64_t grid = ceil_div(rows, 8);
+        int64_t grid = ceil_div(units, 8);
         const int64_t cap = static_cast<int64_t>(h->num_sms) * 8;
         if (grid > cap) grid = cap;
         unpack_pair_kernel<<<dim3(static_cast<unsigned>(grid), n, 1), 256, 0, stream>>>(up);

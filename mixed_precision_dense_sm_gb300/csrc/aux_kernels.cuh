@@ -79,7 +79,8 @@ static __global__ void __launch_bounds__(256)
 }
 
 // Copies rows out of the workspace to rows of any alignment (elements of 2 or
-// 4 bytes), up to two matrices in one launch; one warp per row at a time.
+// 4 bytes), up to two matrices in one launch.  A warp takes 256 elements of a
+// row at a time, 8 per lane, all loads before the stores.
 struct UnpackDesc {
     const void* src;
     void* dst;
@@ -94,17 +95,28 @@ static __global__ void __launch_bounds__(256)
     const UnpackDesc& d = p.d[blockIdx.y];
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
-    for (int64_t r = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); r < d.rows; r += warps) {
+    const int64_t segs = (d.cols + 255) / 256, units = d.rows * segs;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < units; i += warps) {
+        const int64_t r = i / segs;
+        const int64_t c0 = (i - r * segs) * 256 + lane;
         if (d.esize == 4) {
             const uint32_t* s = static_cast<const uint32_t*>(d.src) + r * d.src_ld;
             uint32_t* o = static_cast<uint32_t*>(d.dst) + r * d.dst_ld;
-            #pragma unroll 4
-            for (int64_t c = lane; c < d.cols; c += 32) o[c] = s[c];
+            uint32_t v[8];
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c0 + e * 32 < d.cols ? s[c0 + e * 32] : 0u;
+            #pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c0 + e * 32 < d.cols) o[c0 + e * 32] = v[e];
         } else {
             const uint16_t* s = static_cast<const uint16_t*>(d.src) + r * d.src_ld;
             uint16_t* o = static_cast<uint16_t*>(d.dst) + r * d.dst_ld;
-            #pragma unroll 4
-            for (int64_t c = lane; c < d.cols; c += 32) o[c] = s[c];
+            uint16_t v[8];
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = c0 + e * 32 < d.cols ? s[c0 + e * 32] : static_cast<uint16_t>(0);
+            #pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c0 + e * 32 < d.cols) o[c0 + e * 32] = v[e];
         }
     }
 }

@@ -87,7 +87,7 @@ struct GluBackParams {
     const void* dH; int64_t lddh;
     const void* P; int64_t ldp;
     void* dP; int64_t lddp;
-    void* dPa; int64_t ldpa;  // a second copy of dP whose rows are 16-byte aligned, or NULL
+    void* dPa; int64_t ldpa;  // a second copy of dP in aligned rows, zeros behind column 2F, or NULL
     int64_t M;
     int64_t F;
     int32_t act;
@@ -197,6 +197,8 @@ __global__ void __launch_bounds__(32 * kGluBackWarps, VEC ? 4 : 2)
                 T* arow = static_cast<T*>(p.dPa) + rk * p.ldpa;
                 og.store(arow, base, p.F);
                 ou.store(arow + p.F, base, p.F);
+                if (blockIdx.x == 0)
+                    for (int64_t c = 2 * p.F + lane; c < p.ldpa; c += 32) arow[c] = glu_from_f<T>(0.0f);
             }
         }
     }
