@@ -721,6 +721,25 @@ __device__ __forceinline__ void glu_store32(OutT* base, bool vec, int32_t c0, in
     }
 }
 
+// v[j] += vec[c0 + j]: by vectors where they are whole and aligned; else one
+// element per lane, handed round (32 single loads by every lane took 2 us of a
+// lone tile's epilogue).
+__device__ __forceinline__ void glu_add_bias(const void* vec, int32_t dtype, int32_t c0, int32_t cols,
+                                             float (&v)[32]) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(vec) + static_cast<uintptr_t>(c0) * (dtype == 2 ? 4 : 2);
+    if (c0 + 32 <= cols && (at & 15u) == 0) {
+        float b[32];
+        load_col_vec32(vec, dtype, c0, cols, b);
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += b[j];
+    } else {
+        const int lane = threadIdx.x & 31;
+        const float b = c0 + lane < cols ? load_bias_elem(vec, dtype, c0 + lane) : 0.0f;
+        #pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] += __shfl_sync(0xffffffffu, b, j);
+    }
+}
+
 __device__ __forceinline__ const void* glu_up_bias(const GluParams& p) {
     return static_cast<const uint8_t*>(p.bias) + static_cast<int64_t>(p.F) * (p.bias_dtype == 2 ? 4 : 2);
 }
@@ -816,13 +835,8 @@ __device__ __forceinline__ void glu_tile(const GluParams& p, const CUtensorMap* 
         glu_sums(t_row, t_spare, finisher, ch, g);
         glu_sums(t_row, t_spare, finisher, ch + kChunks, u);
         if (p.bias != nullptr && c0 < p.F) {
-            float b[32];
-            load_col_vec32(p.bias, p.bias_dtype, c0, p.F, b);
-            #pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] += b[j];
-            load_col_vec32(glu_up_bias(p), p.bias_dtype, c0, p.F, b);
-            #pragma unroll
-            for (int j = 0; j < 32; ++j) u[j] += b[j];
+            glu_add_bias(p.bias, p.bias_dtype, c0, p.F, g);
+            glu_add_bias(glu_up_bias(p), p.bias_dtype, c0, p.F, u);
         }
         if (p.c_tma) {
             if (p.P != nullptr) {
