@@ -246,7 +246,7 @@ typedef enum {
     GEMM_PATH_TILED_1SM = 2,  /* persistent tcgen05 kernel, one CTA per 128 x BN tile */
     GEMM_PATH_TILED_2SM = 3,  /* persistent tcgen05 kernel on 2-SM CTA pairs, 256 x BN tiles */
     GEMM_PATH_SKINNY = 4,     /* memory-bound small-M path (swap A/B, split-K) */
-    GEMM_PATH_DOT = 5         /* gated linear layer of up to 4 tokens: dot products, no tiles */
+    GEMM_PATH_DOT = 5         /* gated linear layer of 1 or 2 tokens: dot products, no tiles */
 } gemm_path_t;
 
 typedef struct {

@@ -93,6 +93,7 @@ struct Plan {
     bool ln;
     bool ln_fused;
     int64_t ln_stats_bytes;
+    bool glu_skinny;    // gated layer on the weight-streaming kernel
     // the plain epilogue stores C through shared memory by TMA (C rows
     // 16-byte aligned, not swapped): kCStageBytes of staging after the stages
     bool c_tma;
@@ -872,6 +873,35 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
     }
     if ((pl.a.pack || pl.b.pack) && cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
 
+    if (glu != nullptr && pl.glu_skinny) {
+        // W is the kernel's A
+        const glu_forward_t* o = glu->opt;
+        GluSkinnyLaunch s;
+        std::memset(&s, 0, sizeof s);
+        s.grid = pl.pub.grid;
+        s.block_n = pl.pub.block_n;
+        s.kc = pl.kc;
+        s.stream = stream;
+        if (!encode_glu_weights(encode, &s.tmW, dt.a, a_ptr, pl.K, glu->F, pl.a.packed_ld, 64, 2, pl.kc) ||
+            !encode_operand(encode, &s.tmX, dt.a, b_ptr, pl.b.cols, pl.b.rows, pl.b.packed_ld,
+                            static_cast<uint32_t>(s.block_n), pl.kc))
+            return GEMM_ERR_LAUNCH;
+        const uint32_t fmt = dt.a == GEMM_BF16 ? 1u : 0u;
+        int32_t log_per = 2;
+        while ((pl.pub.split_k << log_per) < s.block_n) ++log_per;
+        s.p = GluSkinnyParams{static_cast<int32_t>(glu->M), static_cast<int32_t>(glu->F), pl.k_blocks,
+                              pl.pub.split_k, log_per, pl.pub.stages,
+                              instr_desc(fmt, false, false, kBlockM, static_cast<uint32_t>(s.block_n)),
+                              C, glu->ldh, o->P, o->ldp, o->bias, o->bias ? o->bias_dtype : GEMM_F32,
+                              o->activation, dt.c, err_dev, wait_limit_ns ? wait_limit_ns : kWaitTimeoutNs,
+                              debug_flags};
+        if (launch_glu_skinny(s) != cudaSuccess) {
+            cudaGetLastError();
+            return GEMM_ERR_LAUNCH;
+        }
+        return GEMM_OK;
+    }
+
     TcLaunch l;
     std::memset(&l, 0, sizeof l);
     const int bn = pl.pub.block_n;
@@ -1645,8 +1675,11 @@ namespace {
 // Rows that the GEMM's loads and stores take as they are.
 bool rows_aligned(const void* p, int64_t ld, int64_t es) { return aligned16(p) && ld * es % 16 == 0; }
 
-// Tokens the dot-product kernel takes (its instances go to 4).
-constexpr int64_t kGluDotTokens = 4;
+// Tokens the dot-product kernel takes.  Against the weight-streaming kernel, for
+// 1 / 2 / 3 / 4 tokens and any number up to 16 on that one: 4.5 / 5.1 / 5.9 /
+// 7.3 and 6.7 us (1024 -> 4096), 12.6 / 13.6 / 15.7 / 20.2 and 14.6 us (4096 ->
+// 4096), 37.7 / 39.3 / 41.6 / 58.8 and 39.2 us (4096 -> 14336).
+constexpr int64_t kGluDotTokens = 2;
 
 // Slabs of rows of the dP kernel: enough CTAs for eight per SM, each slab at
 // least one row per warp.
@@ -1689,7 +1722,7 @@ bool device_current(const gemm_ctx* h) {
 // The plan of the M x 2F product whose tiles hold gate and up columns (or,
 // swapped, rows) in equal parts; H's rows decide how the epilogue stores
 // (element by element where P could not follow by vectors).
-gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W,
+gemm_status_t glu_tile_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W,
                        int64_t ldw, const void* H, int64_t ldh, gemm_dtypes_t dt,
                        const glu_forward_t* o, int32_t num_sms, int32_t smem_optin, Plan& pl) {
     const int64_t es = static_cast<int64_t>(out_elem_bytes(dt.c));
@@ -1726,6 +1759,49 @@ gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t l
     pl.pack_b_bytes = pl.b.rows * kp * 2;
     pl.pub.workspace_bytes = kWsHeaderBytes + round_up(pl.pack_a_bytes, 256) +
                              round_up(pl.pack_b_bytes, 256) + round_up(pl.partial_bytes, 256);
+    return GEMM_OK;
+}
+
+// The gated layer's plan: up to 64 tokens go to the weight-streaming kernel,
+// split over as many CTAs of a cluster (1, 2, 4 or 8) as two CTAs per SM hold,
+// each with two k-blocks at least.
+gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W,
+                       int64_t ldw, const void* H, int64_t ldh, gemm_dtypes_t dt,
+                       const glu_forward_t* o, int32_t num_sms, int32_t smem_optin, Plan& pl) {
+    const gemm_status_t st = glu_tile_plan(M, F, K, X, ldx, W, ldw, H, ldh, dt, o, num_sms, smem_optin, pl);
+    if (st != GEMM_OK || !pl.pub.swap_ab || M > 64) return st;
+    // Where the persistent tiles win: more tiles than two per SM would run in
+    // waves here, each with its own set-up and epilogue (64 tokens, 1024 ->
+    // 28672, 448 tiles: 24.4 us persistent, 32.8 here), and with many tokens the
+    // epilogues of all CTAs end together where tiles nearly fill that (4096 ->
+    // 14336, 224 tiles: 43.4 and 44.0, with GELU 45.4 and 48.7).  Elsewhere: 2048
+    // -> 10240, 160 tiles, 23.5 persistent and 22.5 here; 4096 -> 4096 21.8 and
+    // 17.0; 16 tokens 43.2 / 23.6 / 21.8 and 40.9 / 20.5 / 14.5.
+    const int64_t cols64 = ceil_div(F, 64);
+    if (cols64 > 2 * static_cast<int64_t>(num_sms) ||
+        (M > 32 && 4 * cols64 > 5 * static_cast<int64_t>(num_sms)))
+        return st;
+    pl.glu_skinny = true;
+    int bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    const int64_t tiles = ceil_div(F, 64);
+    int64_t splits = 1;
+    while (splits < 8 && tiles * splits * 2 <= 2 * static_cast<int64_t>(num_sms) &&
+           pl.k_blocks / (splits * 2) >= 2)
+        splits *= 2;
+    if (bn < 4 * splits) bn = static_cast<int>(4 * splits);      // each CTA finishes four tokens at least
+    pl.pub.block_n = bn;
+    pl.pub.stages = pl.kc == 2 ? (bn == 16 ? Skinny<16, 2>::kStages : bn == 32 ? Skinny<32, 2>::kStages
+                                                                              : Skinny<64, 2>::kStages)
+                               : (bn == 16 ? Skinny<16, 1>::kStages : bn == 32 ? Skinny<32, 1>::kStages
+                                                                              : Skinny<64, 1>::kStages);
+    pl.pub.split_k = static_cast<int32_t>(splits);
+    pl.pub.grid = static_cast<int32_t>(tiles * splits);
+    pl.pub.num_tiles = static_cast<int32_t>(tiles);
+    pl.pub.tiles_n = pl.tiles_n = 1;
+    pl.sk_len = pl.sk_max_seg = pl.pub.sk_len = pl.pub.sk_max_seg = 0;
+    pl.partial_bytes = 0;
+    const int64_t body = round_up(pl.pack_a_bytes, 256) + round_up(pl.pack_b_bytes, 256);
+    pl.pub.workspace_bytes = body > 0 ? kWsHeaderBytes + body : 0;
     return GEMM_OK;
 }
 
@@ -1768,12 +1844,8 @@ cudaError_t launch_glu_dot(const GluDotParams& p, int64_t M, int grid, cudaStrea
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    switch (M) {
-        case 1: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 1>, p);
-        case 2: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 2>, p);
-        case 3: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 3>, p);
-        default: return cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 4>, p);
-    }
+    return M == 1 ? cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 1>, p)
+                  : cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 2>, p);
 }
 
 gemm_status_t enqueue_glu_dot(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,

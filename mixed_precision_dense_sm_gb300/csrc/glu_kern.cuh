@@ -268,7 +268,7 @@ __device__ __forceinline__ void glu_put(void* p, int32_t dtype, int64_t i, float
     else static_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// The gated layer of MT tokens (1 to 4): bound by the stream of W.  A warp
+// The gated layer of MT tokens (1 or 2): bound by the stream of W.  A warp
 // takes one gate row and its up row at a time, 16 bytes per lane and load,
 // kGluDotAhead pieces of both rows in flight; X (a few KB) comes from L1.
 // Against the tensor-core path there is no tile to fill, no pipeline to start

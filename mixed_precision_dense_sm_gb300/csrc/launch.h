@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include "gemm_tc.cuh"
+#include "glu_skinny.cuh"
 
 namespace gemm103 {
 
@@ -37,5 +38,16 @@ cudaError_t launch_tc_tf32_bf16(const TcLaunch& l);
 cudaError_t launch_glu_f32(const TcLaunch& l);
 cudaError_t launch_glu_f16(const TcLaunch& l);
 cudaError_t launch_glu_bf16(const TcLaunch& l);
+
+// ... of up to 64 tokens.
+struct GluSkinnyLaunch {
+    CUtensorMap tmW, tmX;
+    GluSkinnyParams p;
+    int grid;
+    int block_n;        // 16, 32 or 64 tokens
+    int kc;             // K chunks per stage
+    cudaStream_t stream;
+};
+cudaError_t launch_glu_skinny(const GluSkinnyLaunch& l);
 
 }  // namespace gemm103

@@ -277,6 +277,37 @@ def test_capture_cannot_grow_the_workspace():
     h.close()
 
 
+@pytest.mark.parametrize("shape", [(300, 256, 512), (16, 640, 1024), (64, 20480, 256), (2048, 2048, 256)],
+                         ids=lambda s: "x".join(map(str, s)))
+def test_a_load_that_never_lands_is_reported(shape):
+    """The planted missing load (gemm_debug_set) on each tile path: the wait
+    runs out, the kernel winds down, the handle reports it and works again."""
+    import mixed_precision_dense_sm_gb300 as lib
+    h = lib.Gemm()
+    M, F, K = shape
+    X, W = torch.randn(M, K, device="cuda").to(BF), torch.randn(2 * F, K, device="cuda").to(BF)
+    want = h.glu(X, W)
+    h.sync()
+    assert lib.gemm_debug_set(h.h, lib.GEMM_DEBUG_SKIP_FIRST_LOAD, 20_000_000) == 0
+    h.glu(X, W)
+    with pytest.raises(lib.GemmError) as e:
+        h.sync()
+    assert e.value.status == 5
+    assert lib.gemm_debug_set(h.h, 0, 0) == 0
+    got = h.glu(X, W)
+    h.sync()
+    assert torch.equal(got, want)
+    h.close()
+
+
+# tokens around the few-token kernels' bounds, splits of K over 1 to 8 CTAs,
+# more tiles than two per SM
+@pytest.mark.parametrize("M", [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64])
+@pytest.mark.parametrize("F,K", [(64, 2048), (100, 520), (1024, 1024), (4100, 640), (20480, 128)])
+def test_forward_few_tokens(g, M, F, K):
+    forward_case(g, M, F, K, FP, "gelu", bias=F32, save=M % 2 == 1)
+
+
 def test_refusals_on_the_device(g):
     import mixed_precision_dense_sm_gb300 as lib
     X, W = torch.randn(8, 32, device="cuda").to(BF), torch.randn(16, 32, device="cuda").to(BF)
