@@ -14,6 +14,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <new>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -272,7 +273,10 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
         return static_cast<double>(tiles) / static_cast<double>(ceil_div(tiles, units) * units);
     };
     const int64_t pair_tiles = ceil_div(pl.Mk, 2 * kBlockM) * ceil_div(pl.Nk, 256);
-    bool pairs = !use_mh2 && !swap && pl.Mk >= 2 * kBlockM && pl.Nk >= 256 && num_sms >= 2 &&
+    // (the gated layer takes pairs from 129 rows on: 200 tokens, 4096 -> 14336,
+    // 94.8 us on single-CTA stream-K tiles, 51.7 on half-filled pairs)
+    const int64_t pair_rows = glu ? kBlockM + 1 : 2 * kBlockM;
+    bool pairs = !use_mh2 && !swap && pl.Mk >= pair_rows && pl.Nk >= 256 && num_sms >= 2 &&
                  pair_tiles >= num_sms / 2;
     if (ln && pl.Nk <= 128) pairs = false;
     bool balance_sk = false;
@@ -318,7 +322,7 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     // operand bytes of a single-CTA 128 x 256 tile, and that is the limit
     // once the operands come from L2 (each re-read by several tiles).
     bool pair_sk = false;
-    if (!use_mh2 && !pairs && !ln && !swap && bn == 256 && pl.Mk >= 2 * kBlockM && num_sms >= 2) {
+    if (!use_mh2 && !pairs && !ln && !swap && bn == 256 && pl.Mk >= pair_rows && num_sms >= 2) {
         const int64_t t1 = tiles_m * ceil_div(pl.Nk, bn);
         // one counter per tile and CTA of the pair
         const bool fits = pair_tiles * 2 <= kMaxCounterTiles;
@@ -1762,14 +1766,14 @@ gemm_status_t glu_tile_plan(int64_t M, int64_t F, int64_t K, const void* X, int6
     return GEMM_OK;
 }
 
-// The gated layer's plan: up to 64 tokens go to the weight-streaming kernel,
+// The gated layer's plan: up to 128 tokens go to the weight-streaming kernel,
 // split over as many CTAs of a cluster (1, 2, 4 or 8) as two CTAs per SM hold,
 // each with two k-blocks at least.
 gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx, const void* W,
                        int64_t ldw, const void* H, int64_t ldh, gemm_dtypes_t dt,
                        const glu_forward_t* o, int32_t num_sms, int32_t smem_optin, Plan& pl) {
     const gemm_status_t st = glu_tile_plan(M, F, K, X, ldx, W, ldw, H, ldh, dt, o, num_sms, smem_optin, pl);
-    if (st != GEMM_OK || !pl.pub.swap_ab || M > 64) return st;
+    if (st != GEMM_OK || M < 1 || M > 128 || 2 * F < 128 || K < 1) return st;
     // Where the persistent tiles win: more tiles than two per SM would run in
     // waves here, each with its own set-up and epilogue (64 tokens, 1024 ->
     // 28672, 448 tiles: 24.4 us persistent, 32.8 here), and with many tokens the
@@ -1779,10 +1783,21 @@ gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t l
     // 17.0; 16 tokens 43.2 / 23.6 / 21.8 and 40.9 / 20.5 / 14.5.
     const int64_t cols64 = ceil_div(F, 64);
     if (cols64 > 2 * static_cast<int64_t>(num_sms) ||
-        (M > 32 && 4 * cols64 > 5 * static_cast<int64_t>(num_sms)))
+        (M > 32 && 4 * cols64 > 5 * static_cast<int64_t>(num_sms)) ||
+        (M > 64 && K < 128 * cols64))
         return st;
     pl.glu_skinny = true;
-    int bn = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    if (!pl.pub.swap_ab) {
+        // W is the kernel's A
+        std::swap(pl.a, pl.b);
+        std::swap(pl.pack_a_bytes, pl.pack_b_bytes);
+        pl.pub.swap_ab = 1;
+    }
+    int bn = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    if (bn == 128 && pl.kc == 2) {               // stages of two chunks would leave one per CTA
+        pl.kc = 1;
+        pl.k_blocks = static_cast<int32_t>(ceil_div(pl.K, 64));
+    }
     const int64_t tiles = ceil_div(F, 64);
     int64_t splits = 1;
     while (splits < 8 && tiles * splits * 2 <= 2 * static_cast<int64_t>(num_sms) &&
@@ -1790,7 +1805,15 @@ gemm_status_t glu_plan(int64_t M, int64_t F, int64_t K, const void* X, int64_t l
         splits *= 2;
     if (bn < 4 * splits) bn = static_cast<int>(4 * splits);      // each CTA finishes four tokens at least
     pl.pub.block_n = bn;
-    pl.pub.stages = pl.kc == 2 ? (bn == 16 ? Skinny<16, 2>::kStages : bn == 32 ? Skinny<32, 2>::kStages
+    pl.pub.block_m = kBlockM;
+    pl.pub.block_k = 64 * pl.kc;
+    pl.pub.k_blocks = pl.k_blocks;
+    pl.pub.path = GEMM_PATH_SKINNY;
+    pl.pub.tiles_m = pl.tiles_m = static_cast<int32_t>(tiles);
+    pl.pub.c_tma = 0;
+    pl.c_tma = false;
+    pl.pub.stages = bn == 128 ? Skinny<128, 1>::kStages
+                    : pl.kc == 2 ? (bn == 16 ? Skinny<16, 2>::kStages : bn == 32 ? Skinny<32, 2>::kStages
                                                                               : Skinny<64, 2>::kStages)
                                : (bn == 16 ? Skinny<16, 1>::kStages : bn == 32 ? Skinny<32, 1>::kStages
                                                                               : Skinny<64, 1>::kStages);

@@ -42,6 +42,7 @@ cudaError_t launch_glu_skinny(const GluSkinnyLaunch& l) {
             case 16: return launch<16, 1>(l);
             case 32: return launch<32, 1>(l);
             case 64: return launch<64, 1>(l);
+            case 128: return launch<128, 1>(l);
         }
     } else {
         switch (l.block_n) {

@@ -1,12 +1,12 @@
-// glu_skinny.cuh -- the gated linear layer of up to 64 tokens
+// glu_skinny.cuh -- the gated linear layer of up to 128 tokens
 // (include/glu_sm103.h): a weight-streaming kernel.
 //
 // Swapped as the GEMM's skinny path is: the weights fill the tensor core's 128
 // rows (64 of the gate, the same 64 of the up projection), the tokens are the
-// MMA's N (16, 32 or 64).  What differs is the split of K.  A problem of few
+// MMA's N (16, 32, 64 or 128).  What differs is the split of K.  A problem of few
 // tiles is split over the S CTAs of a cluster, each streaming its own range of
 // K, and the sums meet through distributed shared memory: every CTA sends each
-// other one the columns (tokens) which that one finishes, one exchange of 32 KB
+// other one the columns (tokens) which that one finishes, one exchange of 64 KB
 // at most and two cluster barriers, where stream-K goes through global memory,
 // a counter and a second pass over tensor memory (4 to 5 us of a problem of
 // 10).  Two CTAs share an SM, so one's set-up and epilogue hide behind the

@@ -39,12 +39,12 @@ cudaError_t launch_glu_f32(const TcLaunch& l);
 cudaError_t launch_glu_f16(const TcLaunch& l);
 cudaError_t launch_glu_bf16(const TcLaunch& l);
 
-// ... of up to 64 tokens.
+// ... of up to 128 tokens.
 struct GluSkinnyLaunch {
     CUtensorMap tmW, tmX;
     GluSkinnyParams p;
     int grid;
-    int block_n;        // 16, 32 or 64 tokens
+    int block_n;        // 16, 32, 64 or (kc = 1) 128 tokens
     int kc;             // K chunks per stage
     cudaStream_t stream;
 };

@@ -36,6 +36,38 @@ def test_glu_arguments():
     assert lib.glu_backward(None, 1, 1, 1, 256, 1, 256, 2, 256, 1, 256, 1, BF16, 256, 2) == 1
 
 
+@pytest.mark.parametrize("seed", range(6))
+def test_glu_plans_cover_the_problem(seed):
+    """Invariants of the plan on random problems: every output tile and K block
+    is there once, the kernels' widths, and a split in K only where allowed."""
+    import random
+    rng = random.Random(seed)
+    for _ in range(300):
+        M, F, K = (int(2 ** rng.uniform(0, b)) for b in (13.5, 14.5, 13.5))
+        ld = K + rng.choice([0, 0, 1, 8])
+        st, p = plan(M=M, F=F, K=K, ldx=ld, ldw=K + rng.choice([0, 0, 1, 8]),
+                     ldh=F + rng.choice([0, 3, 8]), dt=(BF16, BF16, rng.choice([BF16, F16, F32])))
+        assert st == 0
+        if p["path_name"] == "dot":
+            assert M <= 2 and K % 8 == 0
+            continue
+        pad = p["pack_a"] and p["pack_b"]
+        kk = -(-K // 128) * 128 if pad else K
+        assert p["k_blocks"] == -(-kk // p["block_k"])
+        if p["swap_ab"]:
+            assert M <= 128 and p["tiles_m"] == -(-F // 64) and p["block_n"] * p["tiles_n"] >= M
+        else:
+            assert p["block_m"] * p["tiles_m"] >= M and p["block_n"] // 2 * p["tiles_n"] >= F
+            assert p["block_m"] * (p["tiles_m"] - 1) < M and p["block_n"] // 2 * (p["tiles_n"] - 1) < F
+        assert p["num_tiles"] == p["tiles_m"] * p["tiles_n"]
+        if p["path_name"] == "skinny" and p["sk_len"] == 0 and p["split_k"] > 1:
+            assert p["grid"] == p["num_tiles"] * p["split_k"] and p["split_k"] in (2, 4, 8)
+            assert p["block_n"] >= 4 * p["split_k"] and p["k_blocks"] >= 2 * p["split_k"]
+        if p["sk_len"]:
+            cg = 2 if p["path_name"] == "tiled_2sm" else 1
+            assert p["grid"] // cg * p["sk_len"] >= p["num_tiles"] * p["k_blocks"]
+
+
 def norm(M=4, N=64, X=256, Z=256, XO=256, Y=256, x=F32, z=BF16, ld=64, **kw):
     b = dict(pre=1, post=1, pre_weight=None, pre_bias=None, post_weight=None, post_bias=None, gate=None,
              ld_gate=64, gate_rows=1, vec_dtype=F32, scale=1.0, eps=1e-5)

@@ -302,8 +302,8 @@ def test_a_load_that_never_lands_is_reported(shape):
 
 # tokens around the few-token kernels' bounds, splits of K over 1 to 8 CTAs,
 # more tiles than two per SM
-@pytest.mark.parametrize("M", [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64])
-@pytest.mark.parametrize("F,K", [(64, 2048), (100, 520), (1024, 1024), (4100, 640), (20480, 128)])
+@pytest.mark.parametrize("M", [1, 2, 3, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129])
+@pytest.mark.parametrize("F,K", [(64, 2048), (100, 520), (1024, 1024), (4100, 640), (20480, 128), (200, 4096)])
 def test_forward_few_tokens(g, M, F, K):
     forward_case(g, M, F, K, FP, "gelu", bias=F32, save=M % 2 == 1)
 
