@@ -13,8 +13,12 @@ static cudaError_t launch(const GluSkinnyLaunch& l) {
         static bool raised = false;
         std::lock_guard<std::mutex> g(mu);
         if (!raised) {
-            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(Skinny<BN, KC>::kSmem));
+            // room for two CTAs per SM
+            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                 cudaSharedmemCarveoutMaxShared);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Skinny<BN, KC>::kSmem));
             if (e != cudaSuccess) return e;
             raised = true;
         }

@@ -23,6 +23,7 @@ int64_t esize(int32_t t) { return t == GEMM_F32 ? 4 : 2; }
 bool kind_ok(int32_t k) { return k == NORM_NONE || k == NORM_RMS || k == NORM_LAYER; }
 bool aligned(const void* p, int64_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 bool pair_ok(int32_t x, int32_t z) { return x == z || x == GEMM_F32; }
 
@@ -89,11 +90,12 @@ void fill_block(Params& p, int64_t M, int64_t N, const norm_block_t* b) {
     p.inv_n = 1.0f / static_cast<float>(N);
 }
 
-// Threads per row: the fewest of 32, 64, ... whose `chunks8` chunks of 8 hold N.
+// Threads per row: the fewest of 32, 64, ... (and 384) whose `chunks8` chunks
+// of 8 hold N.
 int threads_for(int64_t N, int chunks8) {
     int t = 32;
     while (static_cast<int64_t>(t) * 8 * chunks8 < N) t *= 2;
-    return t;
+    return t == 512 && N <= static_cast<int64_t>(384) * 8 * chunks8 ? 384 : t;
 }
 
 struct Chunks {
@@ -127,8 +129,9 @@ int64_t smem_for(const Params& p, int chunks8, int groups, int stages) {
 
 // Groups per CTA and slots per group: the most rows worked on per SM among
 // CTAs of up to `most` threads, all resident within `resident` threads, that
-// have a second slot per group; of those the deepest rings, then the smallest
-// CTA.  One slot only where two fit nowhere.  Returns CTAs per SM (at most
+// have a second slot per group; of those the deepest rings, then the largest
+// CTA (many small ones leave the driver's default split of an SM's memory with
+// room for few: 5 of 32 one-warp CTAs).  One slot only where two fit nowhere.  Returns CTAs per SM (at most
 // `per_sm`), 0 where nothing fits.
 int choose_cta(Params& p, int chunks8, int most, int resident, int per_sm, int& groups) {
     int64_t best = 0;
@@ -142,7 +145,7 @@ int choose_cta(Params& p, int chunks8, int most, int resident, int per_sm, int& 
             int64_t n = kSmemPerSm / (bytes + 1024);
             if (n > resident / (g * p.T)) n = resident / (g * p.T);
             if (n > per_sm) n = per_sm;
-            if (n * g > best) {
+            if (n * g > best || (n * g == best && stages == p.stages)) {
                 best = n * g;
                 ctas = static_cast<int>(n);
                 groups = g;
@@ -232,11 +235,11 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     if (Z && block->post_bias) p.i_bs = p.n_par++;
     if (Y) p.i_wpre = p.n_par++;
     if (Y && block->pre_bias) p.i_bpre = p.n_par++;
-    // 16 elements per thread where rows are many, 8 where they are few (one
-    // row's latency counts) or narrow
-    l.chunks8 = N > kMaxColumnsPerCta ? 2 : (M <= sms || N <= 1024) ? 1 : 2;
+    // 16 elements per thread, which halves what a row costs beside its
+    // elements; 8 where rows are few (one row's latency counts) or narrow
+    l.chunks8 = N > kMaxColumnsPerCta ? 2 : (M <= sms || N <= 256) ? 1 : 2;
     p.cluster = N > kMaxColumnsPerCta ? 2 : 1;
-    p.T = threads_for(N < kMaxColumnsPerCta ? N : kMaxColumnsPerCta, l.chunks8);
+    p.T = threads_for(ceil_div(round_up(N, 16 * p.cluster), p.cluster), l.chunks8);
     p.slot_bytes = static_cast<uint32_t>(l.chunks8 * 8 * p.T * (esize(x_dtype) + (Z ? esize(z_dtype) : 0)));
     int groups = 1;
     // 64 registers per thread
@@ -338,9 +341,9 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
     l.bias = gr.d_pre_bias || gr.d_post_bias || (!token && gr.d_gate && block->post_bias);
     if (M > 0) {
         // 8192 columns fill a CTA's registers: wider rows take a pair of CTAs
-        l.chunks8 = N > 2048 ? 2 : 1;
+        l.chunks8 = N > 256 ? 2 : 1;
         p.cluster = N > kMaxColumnsPerCta ? 2 : 1;
-        p.T = threads_for(N < kMaxColumnsPerCta ? N : kMaxColumnsPerCta, l.chunks8);
+        p.T = threads_for(ceil_div(round_up(N, 16 * p.cluster), p.cluster), l.chunks8);
         p.slot_bytes = static_cast<uint32_t>(
             l.chunks8 * 8 * p.T *
             (esize(x_dtype) * (dXO ? 2 : 1) + (Z ? esize(z_dtype) : 0) + (dY ? esize(z_dtype) : 0)));

@@ -54,35 +54,38 @@ static cudaError_t backward_c(const Launch& l) {
     return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, BIAS>, l, mu, raised_to);
 }
 
-// Rows of vectors have the threads per row compiled in for the common widths;
-// the others share one kernel per C.
+// Threads per row and chunks per thread: one chunk for rows of up to 256
+// columns (a warp each) and for few rows (norm.cu), else two.  Rows of vectors
+// have the threads compiled in; the others share a kernel per C.
 cudaError_t NORM_CAT(forward_, NORM_SUFFIX)(const Launch& l) {
     if (!l.p.vec) return l.chunks8 == 1 ? forward_c<0, 1, false>(l) : forward_c<0, 2, false>(l);
     if (l.chunks8 == 1) {
-        switch (l.p.T) {
-            case 32: return forward_c<32, 1, true>(l);
-            case 128: return forward_c<128, 1, true>(l);
-            default: return forward_c<0, 1, true>(l);
-        }
+        return l.p.T == 32    ? forward_c<32, 1, true>(l)
+               : l.p.T == 512 ? forward_c<512, 1, true>(l)
+                              : forward_c<0, 1, true>(l);
     }
     switch (l.p.T) {
+        case 32: return forward_c<32, 2, true>(l);
+        case 64: return forward_c<64, 2, true>(l);
+        case 128: return forward_c<128, 2, true>(l);
         case 256: return forward_c<256, 2, true>(l);
-        default: return forward_c<0, 2, true>(l);
+        case 384: return forward_c<384, 2, true>(l);
+        case 512: return forward_c<512, 2, true>(l);
+        default: return cudaErrorInvalidValue;
     }
 }
 
 template <bool BIAS>
 static cudaError_t backward_v(const Launch& l) {
-    if (l.chunks8 == 1) {
-        switch (l.p.T) {
-            case 32: return backward_c<32, 1, true, BIAS>(l);
-            case 128: return backward_c<128, 1, true, BIAS>(l);
-            default: return backward_c<0, 1, true, BIAS>(l);
-        }
-    }
+    if (l.chunks8 == 1) return backward_c<32, 1, true, BIAS>(l);
     switch (l.p.T) {
+        case 32: return backward_c<32, 2, true, BIAS>(l);
+        case 64: return backward_c<64, 2, true, BIAS>(l);
+        case 128: return backward_c<128, 2, true, BIAS>(l);
         case 256: return backward_c<256, 2, true, BIAS>(l);
-        default: return backward_c<512, 2, true, BIAS>(l);
+        case 384: return backward_c<384, 2, true, BIAS>(l);
+        case 512: return backward_c<512, 2, true, BIAS>(l);
+        default: return cudaErrorInvalidValue;
     }
 }
 
