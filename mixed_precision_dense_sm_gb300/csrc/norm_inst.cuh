@@ -89,10 +89,13 @@ static cudaError_t backward_v(const Launch& l) {
     }
 }
 
-// Rows that are not vectors take the kernel with all four sums (fewer kernels;
-// the two that are not wanted are not added up).
+// Rows that are not vectors and take two chunks per thread run the kernel with
+// all four sums (fewer kernels; the two that are not wanted are not added up).
 cudaError_t NORM_CAT(backward_, NORM_SUFFIX)(const Launch& l) {
-    if (!l.p.vec) return l.chunks8 == 1 ? backward_c<0, 1, false, true>(l) : backward_c<0, 2, false, true>(l);
+    if (!l.p.vec)
+        return l.chunks8 == 2 ? backward_c<0, 2, false, true>(l)
+               : l.bias       ? backward_c<0, 1, false, true>(l)
+                              : backward_c<0, 1, false, false>(l);
     return l.bias ? backward_v<true>(l) : backward_v<false>(l);
 }
 

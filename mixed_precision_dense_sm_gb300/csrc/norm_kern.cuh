@@ -131,15 +131,18 @@ __device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool w
         return;
     }
     float f[8];
-    #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int32_t i = s.at(e);
-        f[e] = 0.0f;
-        if (s.in(e, N)) {
-            if (dtype == 2) f[e] = __ldg(static_cast<const float*>(v) + i);
-            else if (dtype == 1) f[e] = __bfloat162float(static_cast<const __nv_bfloat16*>(v)[i]);
-            else f[e] = __half2float(static_cast<const __half*>(v)[i]);
-        }
+    if (dtype == 2) {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = s.in(e, N) ? __ldg(static_cast<const float*>(v) + s.at(e)) : 0.0f;
+    } else {
+        uint16_t u[8];
+        #pragma unroll
+        for (int e = 0; e < 8; ++e)
+            u[e] = s.in(e, N) ? __ldg(static_cast<const uint16_t*>(v) + s.at(e)) : static_cast<uint16_t>(0);
+        #pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[e] = dtype == 1 ? __bfloat162float(__ushort_as_bfloat16(u[e])) : __half2float(__ushort_as_half(u[e]));
     }
     #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = mk2(f[2 * q], f[2 * q + 1]);
@@ -304,7 +307,7 @@ __device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, F8& v) {
             *reinterpret_cast<float4*>(row + s.base) = join2(v[0], v[1]);
             *reinterpret_cast<float4*>(row + s.base + 4) = join2(v[2], v[3]);
         } else {
-            #pragma unroll
+                #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float lo, hi;
                 get2(v[q], lo, hi);
