@@ -28,7 +28,8 @@
  * Layout: row-major with leading dimensions in elements; every pointer
  * aligned to its element size; any leading dimension >= the row length (rows
  * that are not 16-byte aligned are copied to the handle's workspace first).
- * Padding columns are never touched.
+ * Padding columns are never touched.  Outputs must not overlap inputs or each
+ * other, but for dP, which may be P.
  *
  * Types: X, W, dH and dP are F16 or BF16, all the same; H and P share a type,
  * dX and dW have one each (F16, BF16 or F32).  FP32 (TF32) inputs return

@@ -22,8 +22,9 @@
  * place), and outs == NULL means in place for all.  In place, tensors are not
  * written when inv_scale * c is exactly 1.  max_norm = infinity (INFINITY)
  * never clips; with outs == NULL and inv_scale == 1 it only computes the norm.
- * A tensor listed twice counts twice in the norm; listed twice in place it
- * would be scaled twice by two overlapping CTAs: such a list is rejected.
+ * A tensor listed twice counts twice in the norm.  Outputs that overlap each
+ * other, or a gradient other than their own, are rejected (a CTA would write
+ * what another still reads), and so is a tensor listed twice in place.
  *
  * The arrays grads, outs, sizes and dtypes are HOST arrays, read during the
  * call only (they travel as kernel parameters, GRAD_TENSORS_PER_LAUNCH
@@ -36,8 +37,8 @@
  *
  * Errors: GEMM_ERR_INVALID_VALUE (negative count or size, NULL or misaligned
  * pointer of a tensor that is not empty, unknown type, max_norm not positive,
- * inv_scale not positive and finite, workspace too small, a repeated in-place
- * tensor; nothing is enqueued), GEMM_ERR_NOT_SUPPORTED (not sm_103),
+ * inv_scale not positive and finite, workspace too small, overlapping
+ * outputs; nothing is enqueued), GEMM_ERR_NOT_SUPPORTED (not sm_103),
  * GEMM_ERR_LAUNCH.
  */
 #ifndef GRAD_SM103_H_

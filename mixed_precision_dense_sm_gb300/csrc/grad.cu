@@ -331,6 +331,46 @@ int64_t workspace_for(int64_t count, int32_t sms) {
     return (l < 1 ? 1 : l) * static_cast<int64_t>(sms) * kSumCtas * 8;
 }
 
+// CTAs write the outputs while others still read gradients: the outputs have to
+// be apart from each other, and from every gradient but their own (where they
+// may be that gradient itself).  With the starts and the ends of the gradients
+// sorted, those that meet [s, e) are the starts before e less the ends up to s.
+gemm_status_t check_overlap(int64_t count, const void* const* grads, void* const* outs,
+                            const int64_t* sizes, const int32_t* dtypes) {
+    if (count < 2 && (outs == nullptr || count == 0 || outs[0] == grads[0])) return GEMM_OK;
+    uintptr_t* mem = new (std::nothrow) uintptr_t[4 * count];
+    if (mem == nullptr) return GEMM_ERR_ALLOC;
+    uintptr_t* gs = mem;                     // gradients' starts and ends
+    uintptr_t* ge = mem + count;
+    uintptr_t* os = mem + 2 * count;         // outputs', sorted apart: disjoint intervals keep their order
+    uintptr_t* oe = mem + 3 * count;
+    int64_t n = 0;
+    for (int64_t i = 0; i < count; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t bytes = static_cast<uintptr_t>(sizes[i] * esize(dtypes[i]));
+        gs[n] = reinterpret_cast<uintptr_t>(grads[i]);
+        ge[n] = gs[n] + bytes;
+        os[n] = outs ? reinterpret_cast<uintptr_t>(outs[i]) : gs[n];
+        oe[n] = os[n] + bytes;
+        ++n;
+    }
+    std::sort(gs, gs + n);
+    std::sort(ge, ge + n);
+    std::sort(os, os + n);
+    std::sort(oe, oe + n);
+    bool ok = true;
+    for (int64_t i = 0; i + 1 < n; ++i) ok = ok && oe[i] <= os[i + 1];
+    for (int64_t i = 0; i < count && ok; ++i) {
+        if (sizes[i] == 0) continue;
+        const uintptr_t s = reinterpret_cast<uintptr_t>(outs ? outs[i] : grads[i]);
+        const uintptr_t e = s + static_cast<uintptr_t>(sizes[i] * esize(dtypes[i]));
+        const int64_t meet = (std::lower_bound(gs, gs + n, e) - gs) - (std::upper_bound(ge, ge + n, s) - ge);
+        ok = meet == (s == reinterpret_cast<uintptr_t>(grads[i]) ? 1 : 0);
+    }
+    delete[] mem;
+    return ok ? GEMM_OK : GEMM_ERR_INVALID_VALUE;
+}
+
 cudaLaunchConfig_t config(int grid, cudaStream_t stream, cudaLaunchAttribute* attr) {
     attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr->val.programmaticStreamSerializationAllowed = 1;
@@ -445,7 +485,6 @@ gemm_status_t grad_clip(int64_t count, const void* const* grads, void* const* ou
         return GEMM_ERR_INVALID_VALUE;
     if (norm == nullptr || (reinterpret_cast<uintptr_t>(norm) & 3u) != 0)
         return GEMM_ERR_INVALID_VALUE;
-    int64_t in_place = 0;
     for (int64_t i = 0; i < count; ++i) {
         if (sizes[i] < 0 || sizes[i] > (1ll << 40) || !dtype_ok(dtypes[i]))
             return GEMM_ERR_INVALID_VALUE;
@@ -455,7 +494,6 @@ gemm_status_t grad_clip(int64_t count, const void* const* grads, void* const* ou
         if (grads[i] == nullptr || o == nullptr || (reinterpret_cast<uintptr_t>(grads[i]) & m) != 0 ||
             (reinterpret_cast<uintptr_t>(o) & m) != 0)
             return GEMM_ERR_INVALID_VALUE;
-        if (o == grads[i]) ++in_place;
     }
     // chunk numbers are 32-bit within a launch
     for (int64_t l = 0; l * kPerLaunch < count; ++l) {
@@ -464,18 +502,8 @@ gemm_status_t grad_clip(int64_t count, const void* const* grads, void* const* ou
             chunks += (sizes[i] + kLeastChunk - 1) / kLeastChunk;
         if (chunks > (1ll << 30)) return GEMM_ERR_INVALID_VALUE;
     }
-    // a tensor listed twice in place would be scaled by two CTAs at once
-    if (in_place > 1) {
-        const void** p = new (std::nothrow) const void*[in_place];
-        if (p == nullptr) return GEMM_ERR_ALLOC;
-        int64_t n = 0;
-        for (int64_t i = 0; i < count; ++i)
-            if (sizes[i] > 0 && (outs ? outs[i] : grads[i]) == grads[i]) p[n++] = grads[i];
-        std::sort(p, p + n);
-        const bool twice = std::adjacent_find(p, p + n) != p + n;
-        delete[] p;
-        if (twice) return GEMM_ERR_INVALID_VALUE;
-    }
+    const gemm_status_t st = check_overlap(count, grads, outs, sizes, dtypes);
+    if (st != GEMM_OK) return st;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
         return GEMM_ERR_INVALID_VALUE;
     const int sms = device_sms();

@@ -137,6 +137,11 @@ def test_clip_arguments():
                 dict(grads=(256, 256), sizes=(4, 4), dtypes=(F32, F32)),
                 dict(grads=(256, 512), outs=(256, 512), sizes=(4, -4), dtypes=(F32, F32))):
         assert clip(**bad) == 1, bad
+    # outputs that meet each other or another gradient
+    f = dict(sizes=(4, 4), dtypes=(F32, F32))
+    for g, o in (((256, 512), (1024, 1036)), ((256, 512), (512, 1024)), ((256, 512), (1024, 264)),
+                 ((256, 264), (256, 264)), ((256, 256), (1024, 1024)), ((256, 512), (260, 1024))):
+        assert clip(grads=g, outs=o, **f) == 1, (g, o)
     assert lib.lib.grad_clip(1, None, None, None, None, 1.0, 1.0, 256, 256, 1 << 20, None) == 1
     assert lib.lib.grad_clip(-1, None, None, None, None, 1.0, 1.0, 256, 256, 1 << 20, None) == 1
     assert lib.grad_clip_workspace(-1, 152) == -1 and lib.grad_clip_workspace(1, -1) == -1

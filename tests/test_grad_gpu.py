@@ -136,6 +136,21 @@ def test_capture(lib):
     assert torch.equal(norm, want)
 
 
+def test_apart_and_in_place_in_one_list(lib):
+    """Some outputs are their gradients, some lie right beside other tensors; a
+    gradient listed twice counts twice."""
+    flat = torch.randn(4000, device="cuda")
+    gs = [flat[:1000], flat[1000:1007], flat[2000:3000], flat[1000:1007]]
+    outs = [flat[:1000], torch.empty(7, device="cuda"), flat[3000:4000], torch.empty(7, device="cuda")]
+    ins = [t.cpu().double() for t in gs]
+    norm = math.sqrt(sum(float((t * t).sum()) for t in ins))
+    got = lib.grad_clip(gs, 1.0, outputs=outs)
+    assert abs(float(got) - norm) <= 8 * ref.U32 * norm
+    for o, t in zip(outs, ins):
+        r = t / norm
+        ref.check(o, r, 11 * ref.U32 * r.abs(), "out")
+
+
 def test_no_tensors(lib):
     assert float(lib.grad_clip([], 1.0)) == 0.0
 
