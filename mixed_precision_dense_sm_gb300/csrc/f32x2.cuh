@@ -1,11 +1,32 @@
-// f32x2.cuh -- FP32 arithmetic on pairs, and conversions between pairs and
-// packed 16-bit elements.
+// f32x2.cuh -- FP32 arithmetic on pairs, and conversions between FP32 and the
+// storage types: single elements, elements of a type chosen at run time, and
+// pairs of 16-bit elements.
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 namespace gemm103 {
+
+template <typename T> __device__ __forceinline__ float to_f(T v);
+template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
+template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
+    return __bfloat162float(v);
+}
+template <typename T> __device__ __forceinline__ T from_f(float v);
+template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
+template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
+    return __float2bfloat16_rn(v);
+}
+
+// p[i] = v rounded to type 0 = F16, 1 = BF16, 2 = F32.
+__device__ __forceinline__ void store_elem(void* p, int32_t dtype, int64_t i, float v) {
+    if (dtype == 2) static_cast<float*>(p)[i] = v;
+    else if (dtype == 1) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half*>(p)[i] = __float2half_rn(v);
+}
 
 // Two FP32 values in a 64-bit register: the packed FP32 instructions do two
 // lanes' work in one issue slot.  The element kernels here convert 16-bit

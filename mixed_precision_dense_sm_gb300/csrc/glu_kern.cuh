@@ -51,19 +51,6 @@ __device__ __forceinline__ void act_and_slope8(int act, const float (&x)[8], flo
     }
 }
 
-template <typename T> __device__ __forceinline__ float glu_to_f(T v);
-template <> __device__ __forceinline__ float glu_to_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ float glu_to_f<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float glu_to_f<__nv_bfloat16>(__nv_bfloat16 v) {
-    return __bfloat162float(v);
-}
-template <typename T> __device__ __forceinline__ T glu_from_f(float v);
-template <> __device__ __forceinline__ float glu_from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half glu_from_f<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 glu_from_f<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
-}
-
 // K == 0: P = [G U] is the bias (0 where there is none), H = act(G) * U.
 template <typename OutT>
 __global__ void __launch_bounds__(256)
@@ -76,10 +63,10 @@ __global__ void __launch_bounds__(256)
         const float g = bias ? load_bias_elem(bias, bias_dtype, c) : 0.0f;
         const float u = bias ? load_bias_elem(bias, bias_dtype, F + c) : 0.0f;
         if (P != nullptr) {
-            P[r * ldp + c] = glu_from_f<OutT>(g);
-            P[r * ldp + F + c] = glu_from_f<OutT>(u);
+            P[r * ldp + c] = from_f<OutT>(g);
+            P[r * ldp + F + c] = from_f<OutT>(u);
         }
-        H[r * ldh + c] = glu_from_f<OutT>(activate(act, g) * u);
+        H[r * ldh + c] = from_f<OutT>(activate(act, g) * u);
     }
 }
 
@@ -176,15 +163,15 @@ __global__ void __launch_bounds__(32 * kGluBackWarps, VEC ? 4 : 2)
             if (rk >= row1) break;
             float g[8], a[8], d[8];
             #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = glu_to_f<PT>(gu[k][0].e[e]);
+            for (int e = 0; e < 8; ++e) g[e] = to_f<PT>(gu[k][0].e[e]);
             act_and_slope8(p.act, g, a, d);
             Raw8<T, VEC> og, ou;
             #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float x = glu_to_f<T>(h[k].e[e]);
-                const float dg = x * glu_to_f<PT>(gu[k][1].e[e]) * d[e], du = x * a[e];
-                og.e[e] = glu_from_f<T>(dg);
-                ou.e[e] = glu_from_f<T>(du);
+                const float x = to_f<T>(h[k].e[e]);
+                const float dg = x * to_f<PT>(gu[k][1].e[e]) * d[e], du = x * a[e];
+                og.e[e] = from_f<T>(dg);
+                ou.e[e] = from_f<T>(du);
                 if constexpr (SUMS) {
                     sg[e] += dg;                       // (columns past F are not looked at)
                     su[e] += du;
@@ -198,7 +185,7 @@ __global__ void __launch_bounds__(32 * kGluBackWarps, VEC ? 4 : 2)
                 og.store(arow, base, p.F);
                 ou.store(arow + p.F, base, p.F);
                 if (blockIdx.x == 0)
-                    for (int64_t c = 2 * p.F + lane; c < p.ldpa; c += 32) arow[c] = glu_from_f<T>(0.0f);
+                    for (int64_t c = 2 * p.F + lane; c < p.ldpa; c += 32) arow[c] = from_f<T>(0.0f);
             }
         }
     }
@@ -241,9 +228,7 @@ static __global__ void __launch_bounds__(1024)
     t = 0.0f;
     #pragma unroll
     for (int y = 0; y < 32; ++y) t += red[y][tx];
-    if (dtype == 2) static_cast<float*>(dbias)[c] = t;
-    else if (dtype == 1) static_cast<__nv_bfloat16*>(dbias)[c] = __float2bfloat16_rn(t);
-    else static_cast<__half*>(dbias)[c] = __float2half_rn(t);
+    store_elem(dbias, dtype, c, t);
 }
 
 // -------------------------------------------------------- a few tokens (decode)
@@ -261,12 +246,6 @@ struct GluDotParams {
 constexpr int kGluDotThreads = 256;
 constexpr int kGluDotCtas = 4;          // per SM
 constexpr int kGluDotAhead = 4;         // 256-element pieces of both rows in flight per warp
-
-__device__ __forceinline__ void glu_put(void* p, int32_t dtype, int64_t i, float v) {
-    if (dtype == 2) static_cast<float*>(p)[i] = v;
-    else if (dtype == 1) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
 
 // The gated layer of MT tokens (1 or 2): bound by the stream of W.  A warp
 // takes one gate row and its up row at a time, 16 bytes per lane and load,
@@ -339,10 +318,10 @@ __global__ void __launch_bounds__(kGluDotThreads, kGluDotCtas)
                 mine_u += load_bias_elem(p.bias, p.bias_dtype, static_cast<int64_t>(p.F) + f);
             }
             if (p.P != nullptr) {
-                glu_put(p.P, p.h_dtype, lane * p.ldp + f, mine_g);
-                glu_put(p.P, p.h_dtype, lane * p.ldp + p.F + f, mine_u);
+                store_elem(p.P, p.h_dtype, lane * p.ldp + f, mine_g);
+                store_elem(p.P, p.h_dtype, lane * p.ldp + p.F + f, mine_u);
             }
-            glu_put(p.H, p.h_dtype, lane * p.ldh + f, activate(p.act, mine_g) * mine_u);
+            store_elem(p.H, p.h_dtype, lane * p.ldh + f, activate(p.act, mine_g) * mine_u);
         }
     }
 }

@@ -17,6 +17,7 @@
 #include <cuda.h>
 
 #include "epilogue_ops.cuh"
+#include "f32x2.cuh"
 #include "ptx.cuh"
 
 namespace gemm103 {
@@ -49,12 +50,6 @@ struct Skinny {
     static constexpr int kStages = static_cast<int>((112u * 1024u - 2048u) / kStage);
     static constexpr uint32_t kSmem = (kStages * kStage > kExchange ? kStages * kStage : kExchange) + 1024u + 128u;
 };
-
-__device__ __forceinline__ void skinny_put(void* p, int32_t dtype, int64_t i, float v) {
-    if (dtype == 2) static_cast<float*>(p)[i] = v;
-    else if (dtype == 1) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
 
 // Bounded wait that also gives up once another role has.
 __device__ __forceinline__ bool skinny_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -240,10 +235,10 @@ __global__ void __launch_bounds__(kSkinnyThreads)
                 for (int k = 0; k < 4; ++k) {
                     if (t + k >= p.M) break;
                     if (p.P != nullptr) {
-                        skinny_put(p.P, p.h_dtype, (t + k) * p.ldp + n, g[k]);
-                        skinny_put(p.P, p.h_dtype, (t + k) * p.ldp + p.F + n, u[k]);
+                        store_elem(p.P, p.h_dtype, (t + k) * p.ldp + n, g[k]);
+                        store_elem(p.P, p.h_dtype, (t + k) * p.ldp + p.F + n, u[k]);
                     }
-                    skinny_put(p.H, p.h_dtype, (t + k) * p.ldh + n, activate(p.act, g[k]) * u[k]);
+                    store_elem(p.H, p.h_dtype, (t + k) * p.ldh + n, activate(p.act, g[k]) * u[k]);
                 }
             }
         }

@@ -29,6 +29,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "device.h"
+#include "f32x2.cuh"
 #include "grad_sm103.h"
 #include "ptx.cuh"
 
@@ -78,19 +80,6 @@ __device__ __forceinline__ int find_tensor(const Tensors<CAP>& t, int32_t c) {
         else hi = mid - 1;
     }
     return lo;
-}
-
-template <typename T> __device__ __forceinline__ float to_f(T v);
-template <> __device__ __forceinline__ float to_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ float to_f<__half>(__half v) { return __half2float(v); }
-template <> __device__ __forceinline__ float to_f<__nv_bfloat16>(__nv_bfloat16 v) {
-    return __bfloat162float(v);
-}
-template <typename T> __device__ __forceinline__ T from_f(float v);
-template <> __device__ __forceinline__ float from_f<float>(float v) { return v; }
-template <> __device__ __forceinline__ __half from_f<__half>(float v) { return __float2half_rn(v); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
 }
 
 template <typename T>
@@ -310,19 +299,6 @@ __global__ void __launch_bounds__(kThreads, kApplyCtas)
 
 bool dtype_ok(int32_t t) { return t == GEMM_F16 || t == GEMM_BF16 || t == GEMM_F32; }
 int64_t esize(int32_t t) { return t == GEMM_F32 ? 4 : 2; }
-
-// SMs of the current device; 0 off sm_103, -1 on a CUDA error.
-int device_sms() {
-    int dev = 0, major = 0, minor = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return -1;
-    }
-    return major == 10 && minor == 3 ? sms : 0;
-}
 
 int64_t launches_for(int64_t count) { return (count + kPerLaunch - 1) / kPerLaunch; }
 

@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include "device.h"
 #include "norm_launch.h"
 #include "norm_sm103.h"
 
@@ -34,19 +35,6 @@ bool matrix_ok(const void* p, int64_t ld, int64_t N, int32_t dtype) {
 
 bool vector16(const void* p, int64_t ld, int32_t dtype) {
     return p == nullptr || (aligned(p, 16) && ld * esize(dtype) % 16 == 0);
-}
-
-// SMs of the current device; 0 off sm_103, -1 on a CUDA error.
-int device_sms() {
-    int dev = 0, major = 0, minor = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return -1;
-    }
-    return major == 10 && minor == 3 ? sms : 0;
 }
 
 gemm_status_t check_block(int64_t M, int64_t N, int32_t x_dtype, int32_t z_dtype,

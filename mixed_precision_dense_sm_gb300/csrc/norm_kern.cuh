@@ -189,12 +189,6 @@ __device__ __forceinline__ void center8(F8& o, float mean, Spot<VEC> s, int32_t 
     mask8<VEC>(o, s, N);
 }
 
-__device__ __forceinline__ void store_elem(void* p, int32_t dtype, int64_t i, float v) {
-    if (dtype == 2) static_cast<float*>(p)[i] = v;
-    else if (dtype == 1) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half*>(p)[i] = __float2half_rn(v);
-}
-
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
                  : "memory");
