@@ -86,20 +86,43 @@ int threads_for(int64_t N, int chunks8) {
     return t == 512 && N <= static_cast<int64_t>(384) * 8 * chunks8 ? 384 : t;
 }
 
+constexpr int64_t kChunkCost = 32768;
+
 struct Chunks {
     int64_t group_rows, groups, per_group, rows;
 };
 
-// Rows cut into about `target` chunks, each inside one group of the gate.
-Chunks chunks_for(int64_t M, int64_t gate_rows, int64_t target) {
+// Rows cut into chunks, each inside one group of the gate, for `resident` CTAs
+// that work at a time on one each.  The size is the one whose waves take the
+// shortest: a chunk costs its rows and, to fill its vectors and write its
+// sums, about kChunkCost elements more.  (8192 x 4096, backward, 16 groups of
+// the gate: 157 us in 160 chunks, two waves, 100 in 144.  512 groups: 148 in
+// chunks of half a group and 179 of a whole one, which a cost of 8192 takes.)
+Chunks chunks_for(int64_t M, int64_t N, int64_t gate_rows, int64_t resident) {
     Chunks c;
     c.group_rows = (gate_rows > 1 && gate_rows < M) ? gate_rows : (M > 0 ? M : 1);
     c.groups = ceil_div(M > 0 ? M : 1, c.group_rows);
-    int64_t per = ceil_div(target, c.groups);
-    if (per > c.group_rows) per = c.group_rows;
-    c.rows = ceil_div(c.group_rows, per);
+    int64_t per = ceil_div(resident, c.groups), best = INT64_MAX;
+    int64_t most = c.groups > 1 && per < 4 ? 4 : per;
+    if (most > c.group_rows) most = c.group_rows;
+    c.rows = ceil_div(c.group_rows, most);
+    for (int64_t i = c.groups > 1 ? (most > 64 ? most - 64 : 1) : most; i <= most; ++i) {
+        const int64_t rows = ceil_div(c.group_rows, i);
+        const int64_t waves = ceil_div(c.groups * ceil_div(c.group_rows, rows), resident);
+        const int64_t cost = waves * (rows * N + kChunkCost);
+        if (cost < best) {
+            best = cost;
+            c.rows = rows;
+        }
+    }
     c.per_group = ceil_div(c.group_rows, c.rows);
     return c;
+}
+
+// Of the backward pass: a CTA, or a pair of them, per SM.
+Chunks back_chunks(int64_t M, int64_t N, int64_t gate_rows, int sms) {
+    const int64_t resident = N > kMaxColumnsPerCta ? sms / 2 : sms;
+    return chunks_for(M, N, gate_rows, resident > 0 ? resident : 1);
 }
 
 void set_chunks(Params& p, const Chunks& c) {
@@ -166,18 +189,50 @@ cudaError_t run_backward(int32_t x, int32_t z, const Launch& l) {
     return backward_f32_f32(l);
 }
 
-cudaError_t run_sum(const SumParams& s, cudaStream_t stream) {
+template <typename K>
+cudaError_t launch_sum(K kern, dim3 grid, int threads, const SumParams& s, cudaStream_t stream) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    const int64_t groups = s.d_gate ? (s.groups < kSumGroups ? s.groups : kSumGroups) : 0;
-    cfg.gridDim = dim3(static_cast<unsigned>(ceil_div(s.N, 32)), static_cast<unsigned>(1 + groups), 1);
-    cfg.blockDim = dim3(32 * kSumY, 1, 1);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, sum_kernel, s);
+    return cudaLaunchKernelEx(&cfg, kern, s);
+}
+
+// The sums over the chunks: one step, or two where there are many chunks
+// (`lines`, kSumSplits of them, hold the first step's); the gate's gradient
+// beside it, or by its own kernel where it has many groups.
+cudaError_t run_sum(SumParams s, float* lines, int sms, cudaStream_t stream) {
+    const unsigned cols = static_cast<unsigned>(ceil_div(s.N, 32));
+    const bool two = s.chunks > kSumOneStep;
+    const bool own = s.d_gate != nullptr && (two || s.groups > kSumGroups);
+    cudaError_t e = cudaSuccess;
+    if (own) {
+        const int64_t want = ceil_div(static_cast<int64_t>(s.groups) * s.N, 256);
+        const int64_t most = static_cast<int64_t>(sms) * 8;
+        e = launch_sum(dgate_kernel, dim3(static_cast<unsigned>(want < most ? want : most), 1, 1), 256, s,
+                       stream);
+        if (e != cudaSuccess) return e;
+    }
+    const bool totals = s.d_pre_weight || s.d_pre_bias || s.d_post_weight || s.d_post_bias;
+    if (own && !totals) return e;
+    if (two) {
+        SumParams f = s;
+        f.lines = lines;
+        e = launch_sum(sum_kernel, dim3(cols, kSumSplits, 1), 32 * kSumY, f, stream);
+        if (e != cudaSuccess) return e;
+        s.partials = lines;
+        s.part_stride = static_cast<int64_t>(kSumSplits) * s.N;
+        s.chunks = kSumSplits;
+        s.gated = 0;
+        s.d_gate = nullptr;
+    }
+    const unsigned groups = s.d_gate && !own ? static_cast<unsigned>(s.groups) : 0u;
+    return launch_sum(sum_kernel, dim3(cols, 1 + groups, 1), 32 * kSumY, s, stream);
 }
 
 }  // namespace
@@ -235,7 +290,7 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     // 64 registers per thread
     const int ctas = choose_cta(p, l.chunks8, 1024, 1024, 32, groups);
     if (ctas == 0) return GEMM_ERR_NOT_SUPPORTED;
-    const Chunks ch = chunks_for(M, Z && block->gate ? block->gate_rows : 1,
+    const Chunks ch = chunks_for(M, N, Z && block->gate ? block->gate_rows : 1,
                                  static_cast<int64_t>(sms) * ctas / p.cluster);
     set_chunks(p, ch);
     // no more groups than a chunk has rows
@@ -253,8 +308,8 @@ int64_t norm_block_backward_workspace(int64_t M, int64_t N, int64_t gate_rows, i
         num_sms = device_sms();
         if (num_sms <= 0) return -1;
     }
-    const Chunks c = chunks_for(M, gate_rows, num_sms);
-    return 4 * c.groups * c.per_group * N * 4;
+    const Chunks c = back_chunks(M, N, gate_rows, num_sms);
+    return 4 * (c.groups * c.per_group + kSumSplits) * N * 4;
 }
 
 gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t ldxo,
@@ -293,9 +348,9 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
     if (sms < 0) return GEMM_ERR_LAUNCH;
     if (sms == 0) return GEMM_ERR_NOT_SUPPORTED;
     const bool token = block->gate != nullptr && block->gate_rows == 1;
-    const Chunks ch = chunks_for(M, block->gate ? block->gate_rows : 1, sms);
+    const Chunks ch = back_chunks(M, N, block->gate ? block->gate_rows : 1, sms);
     const int64_t chunks = M > 0 ? ch.groups * ch.per_group : 0;
-    if (M > 0 && sums && workspace_bytes < 4 * chunks * N * 4) return GEMM_ERR_INVALID_VALUE;
+    if (M > 0 && sums && workspace_bytes < 4 * (chunks + kSumSplits) * N * 4) return GEMM_ERR_INVALID_VALUE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
 
     Launch l;
@@ -363,6 +418,8 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
     sp.N = static_cast<int32_t>(N);
     sp.groups = static_cast<int32_t>(M > 0 ? ch.groups : 1);
     sp.chunks_per_group = M > 0 ? p.chunks_per_group : 0;
+    sp.chunks = sp.groups * sp.chunks_per_group;
+    sp.gated = token || M == 0 ? 0 : 1;    // (no rows: the gate has none either)
     sp.token_gate = p.token_gate;
     sp.bias = l.bias ? 1 : 0;
     sp.wpost = p.wpost;
@@ -377,7 +434,7 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
     sp.d_post_weight = gr.d_post_weight;
     sp.d_post_bias = gr.d_post_bias;
     sp.d_gate = (token || M == 0) ? nullptr : gr.d_gate;
-    return status_of(run_sum(sp, s));
+    return status_of(run_sum(sp, p.partials ? p.partials + 4 * p.part_stride : nullptr, sms, s));
 }
 
 }  // extern "C"

@@ -993,13 +993,17 @@ struct SumParams {
     const float* partials;
     int64_t part_stride;
     int32_t N;
+    int32_t chunks;             // lines to add
     int32_t groups, chunks_per_group, token_gate;
+    int32_t gated;              // q's sums are weighted by the gate of the chunk's group
     int32_t bias;               // the sums of dY and q were taken
     const void* wpost; const void* bpost; const void* gate;
     int64_t ld_gate;
     int32_t vec_dtype, grad_dtype;
     float scale;
     void* d_pre_weight; void* d_pre_bias; void* d_post_weight; void* d_post_bias; void* d_gate;
+    float* lines;               // first of two steps: CTA row y adds its share of the
+                                // chunks into line y of [4][kSumSplits][N]
 };
 
 __device__ __forceinline__ float param_elem(const void* v, int32_t dtype, int64_t i, float absent) {
@@ -1010,12 +1014,20 @@ __device__ __forceinline__ float param_elem(const void* v, int32_t dtype, int64_
 }
 
 constexpr int kSumY = 32;
-constexpr int kSumGroups = 2048;    // CTAs along the gate's groups at most
+constexpr int kSumSplits = 16;      // lines that many chunks are added to first
+// Chunks that one step adds.  (Backward, 8192 x 4096 / 65536 x 512: 4096 chunks
+// 497 / 344 us in one step, 462 / 279 in two; 1024 chunks 189 / 138 and 187 / 123.)
+constexpr int kSumOneStep = 1024;
+// Gate groups that get CTAs of their own; of more, dgate_kernel makes the
+// gate's gradient.  (The same: 2 groups 88 / 68 us beside, 93 / 72 by the
+// kernel; 32 groups 172 / 121 and 157 / 124; 1024 groups 714 / 186 and 189 / 138.)
+constexpr int kSumGroups = 16;
 
 // Sums over the chunks, 32 columns per CTA, kSumY lines of threads that take
 // the chunks in turn and are added in line order.  CTAs with blockIdx.y == 0
 // make the totals, the gate's row joining chunk by chunk; the others (where
-// the gate's gradient is wanted) one group's sums each.
+// the gate's gradient is wanted) one group's sums each.  With p.lines, CTA row
+// y adds its part of the chunks into line y instead.
 static __global__ void __launch_bounds__(32 * kSumY)
     sum_kernel(const __grid_constant__ SumParams p) {
     __shared__ float red[4][kSumY][33];
@@ -1024,64 +1036,86 @@ static __global__ void __launch_bounds__(32 * kSumY)
     const bool in = col < p.N;
     grid_dependency_wait();
     grid_dependents_launch();
-    // sums of this line's part of chunks [first, last); with GATED q's are
-    // weighted by the gate of the chunk's group
-    auto add = [&](int32_t first, int32_t last, bool gated, float (&a)[4]) {
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) a[k] = 0.0f;
-        if (in) {
-            const float* base = p.partials + col;
-            const float one = gated && p.groups == 1 ? param_elem(p.gate, p.vec_dtype, col, 1.0f) : 1.0f;
-            #pragma unroll 4
-            for (int32_t c = first + ty; c < last; c += kSumY) {
-                const float* q = base + static_cast<int64_t>(c) * p.N;
-                float gt = one;
-                if (gated && p.gate != nullptr && p.groups > 1)
-                    gt = param_elem(p.gate, p.vec_dtype, (c / p.chunks_per_group) * p.ld_gate + col, 1.0f);
-                a[0] += q[0];
-                a[1] = fmaf(gt, q[p.part_stride], a[1]);
-                if (p.bias) {
-                    a[2] += q[2 * p.part_stride];
-                    a[3] = fmaf(gt, q[3 * p.part_stride], a[3]);
-                }
+    int32_t first = 0, last = p.chunks;
+    bool gated = p.gated != 0;
+    const int32_t y = static_cast<int32_t>(blockIdx.y);
+    if (p.lines != nullptr) {
+        first = static_cast<int32_t>(static_cast<int64_t>(p.chunks) * y / kSumSplits);
+        last = static_cast<int32_t>(static_cast<int64_t>(p.chunks) * (y + 1) / kSumSplits);
+    } else if (y > 0) {
+        first = (y - 1) * p.chunks_per_group;
+        last = y * p.chunks_per_group;
+        gated = false;
+    }
+    float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (in) {
+        const float* base = p.partials + col;
+        const float one = gated && p.groups == 1 ? param_elem(p.gate, p.vec_dtype, col, 1.0f) : 1.0f;
+        #pragma unroll 4
+        for (int32_t c = first + ty; c < last; c += kSumY) {
+            const float* q = base + static_cast<int64_t>(c) * p.N;
+            float gt = one;
+            if (gated && p.gate != nullptr && p.groups > 1)
+                gt = param_elem(p.gate, p.vec_dtype, (c / p.chunks_per_group) * p.ld_gate + col, 1.0f);
+            a[0] += q[0];
+            a[1] = fmaf(gt, q[p.part_stride], a[1]);
+            if (p.bias) {
+                a[2] += q[2 * p.part_stride];
+                a[3] = fmaf(gt, q[3 * p.part_stride], a[3]);
             }
         }
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) red[k][ty][tx] = a[k];
-        __syncthreads();
-        // line k < 4 adds the k-th sum over the lines; line 0 collects them
-        float s = 0.0f;
-        if (ty < 4) {
-            #pragma unroll
-            for (int y = 0; y < kSumY; ++y) s += red[ty][y][tx];
-        }
-        __syncthreads();
-        if (ty < 4) red[ty][0][tx] = s;
-        __syncthreads();
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) a[k] = red[k][0][tx];
-        __syncthreads();
-    };
-    float a[4];
-    if (blockIdx.y == 0) {
-        add(0, p.groups * p.chunks_per_group, !p.token_gate, a);
-        if (ty == 0 && in) {
-            const float f = p.token_gate ? 1.0f : p.scale;
-            if (p.d_pre_weight) store_elem(p.d_pre_weight, p.grad_dtype, col, a[0]);
-            if (p.d_post_weight) store_elem(p.d_post_weight, p.grad_dtype, col, f * a[1]);
-            if (p.d_pre_bias) store_elem(p.d_pre_bias, p.grad_dtype, col, a[2]);
-            if (p.d_post_bias) store_elem(p.d_post_bias, p.grad_dtype, col, f * a[3]);
-        }
-        return;
     }
-    for (int32_t gr = static_cast<int32_t>(blockIdx.y) - 1; gr < p.groups;
-         gr += static_cast<int32_t>(gridDim.y) - 1) {
-        add(gr * p.chunks_per_group, (gr + 1) * p.chunks_per_group, false, a);
-        if (ty == 0 && in) {
-            float v = a[1] * param_elem(p.wpost, p.vec_dtype, col, 1.0f);
-            if (p.bpost != nullptr) v = fmaf(a[3], param_elem(p.bpost, p.vec_dtype, col, 0.0f), v);
-            store_elem(p.d_gate, p.grad_dtype, static_cast<int64_t>(gr) * p.N + col, p.scale * v);
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) red[k][ty][tx] = a[k];
+    __syncthreads();
+    // line k < 4 adds the k-th sum over the lines
+    if (ty < 4) {
+        float s = 0.0f;
+        #pragma unroll
+        for (int i = 0; i < kSumY; ++i) s += red[ty][i][tx];
+        red[ty][0][tx] = s;
+    }
+    __syncthreads();
+    if (ty != 0 || !in) return;
+    #pragma unroll
+    for (int k = 0; k < 4; ++k) a[k] = red[k][0][tx];
+    if (p.lines != nullptr) {
+        #pragma unroll
+        for (int k = 0; k < 4; ++k)
+            p.lines[(static_cast<int64_t>(k) * kSumSplits + y) * p.N + col] = a[k];
+    } else if (y == 0) {
+        const float f = p.token_gate ? 1.0f : p.scale;
+        if (p.d_pre_weight) store_elem(p.d_pre_weight, p.grad_dtype, col, a[0]);
+        if (p.d_post_weight) store_elem(p.d_post_weight, p.grad_dtype, col, f * a[1]);
+        if (p.d_pre_bias) store_elem(p.d_pre_bias, p.grad_dtype, col, a[2]);
+        if (p.d_post_bias) store_elem(p.d_post_bias, p.grad_dtype, col, f * a[3]);
+    } else {
+        float v = a[1] * param_elem(p.wpost, p.vec_dtype, col, 1.0f);
+        if (p.bpost != nullptr) v = fmaf(a[3], param_elem(p.bpost, p.vec_dtype, col, 0.0f), v);
+        store_elem(p.d_gate, p.grad_dtype, static_cast<int64_t>(y - 1) * p.N + col, p.scale * v);
+    }
+}
+
+// The gate's gradient where its groups are many (and so of few chunks each):
+// a thread per group and column adds the group's chunks.
+static __global__ void __launch_bounds__(256)
+    dgate_kernel(const __grid_constant__ SumParams p) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const int64_t total = static_cast<int64_t>(p.groups) * p.N;
+    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const int32_t gr = static_cast<int32_t>(i / p.N);
+        const int32_t col = static_cast<int32_t>(i - static_cast<int64_t>(gr) * p.N);
+        const float* q = p.partials + p.part_stride +
+                         static_cast<int64_t>(gr) * p.chunks_per_group * p.N + col;
+        float s = 0.0f, t = 0.0f;
+        for (int32_t c = 0; c < p.chunks_per_group; ++c) {
+            s += q[static_cast<int64_t>(c) * p.N];
+            if (p.bpost != nullptr) t += q[2 * p.part_stride + static_cast<int64_t>(c) * p.N];
         }
+        float v = s * param_elem(p.wpost, p.vec_dtype, col, 1.0f);
+        if (p.bpost != nullptr) v = fmaf(t, param_elem(p.bpost, p.vec_dtype, col, 0.0f), v);
+        store_elem(p.d_gate, p.grad_dtype, i, p.scale * v);
     }
 }
 

@@ -115,8 +115,8 @@ def test_norm_workspace():
     for M, N, rows, sms in itertools.product((0, 1, 5, 303, 304, 305, 8192, 100000), (1, 4096), (1, 2, 3, 100, 8192),
                                              (1, 16, 152)):
         b = w(M, N, rows, sms)
-        lines = b // (16 * N)
-        assert b == lines * 16 * N and lines >= 1
+        lines = b // (16 * N) - 16                  # (16 more for the second step of the sums)
+        assert b == (lines + 16) * 16 * N and lines >= 1
         # no more lines than rows or twice the SMs, but one for every gate group
         groups = -(-max(M, 1) // rows) if 1 < rows < M else 1
         assert lines <= max(M, 1) + groups and lines <= 2 * sms + 2 * groups

@@ -133,8 +133,9 @@ def test_kinds_and_gates(lib, pre, post, rows):
 
 
 def test_many_gate_groups(lib):
-    run_backward(lib, make(2000, 264, BF, BF, "rms", "rms", 3))
-    run_backward(lib, make(2000, 264, BF, BF, "rms", "rms", 3), biases=False)
+    for M, rows in ((2000, 3), (2000, 100), (2000, 150), (5000, 2), (4000, 4), (4100, 4)):
+        run_backward(lib, make(M, 264, BF, BF, "rms", "layer", rows))
+        run_backward(lib, make(M, 33, F32, BF, "layer", "rms", rows, bias=False), biases=False)
 
 
 @pytest.mark.parametrize("pad,off", [(8, 0), (8, 8), (3, 0), (0, 1), (16, 3)])
