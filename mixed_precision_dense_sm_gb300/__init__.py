@@ -504,8 +504,8 @@ def _mat(t, name, rows, cols, dtype, dev):
     st = t.stride()
     if st[1] != 1 and cols > 1:
         _refuse(t, name, (rows, cols), dtype, dev)
-    # torch may give any stride to a single row
-    return t.data_ptr(), (st[0] if rows > 1 else cols) or 1
+    # torch may give any stride to a single row, or to rows of nothing
+    return t.data_ptr(), st[0] if rows > 1 and cols > 0 else max(cols, 1)
 
 
 def _vec(t, name, n, dtype, dev):

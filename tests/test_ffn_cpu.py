@@ -160,3 +160,16 @@ def test_struct_layouts():
     """The ctypes structures are laid out as the C ones (size checked by natural alignment)."""
     assert ctypes.sizeof(lib.GluForward) == 40 and ctypes.sizeof(lib.GluBackward) == 88
     assert ctypes.sizeof(lib.NormBlock) == 80 and ctypes.sizeof(lib.NormBlockGrads) == 48
+
+
+@pytest.mark.parametrize("shape,stride,ld", [((4, 1), (0, 1), 0), ((4, 1), (0, 0), 0), ((4, 1), (3, 7), 3),
+                                             ((4, 8), (0, 1), 0), ((4, 8), (2, 1), 2), ((1, 8), (0, 1), 8),
+                                             ((1, 8), (99, 1), 8), ((1, 1), (0, 0), 1), ((4, 0), (0, 1), 1),
+                                             ((0, 8), (0, 1), 8), ((4, 8), (12, 1), 12)])
+def test_row_pitch_of_a_view(shape, stride, ld):
+    """Broadcast and overlapping rows keep a pitch below the row length, which
+    the library refuses."""
+    t = torch.empty(64).as_strided(shape, stride)
+    assert lib._mat(t, "t", *shape, torch.float32, -1) == (t.data_ptr(), ld)
+    if ld < max(shape[1], 1):
+        assert plan(M=shape[0], K=shape[1], ldx=ld or -1)[0] == 1
