@@ -522,13 +522,16 @@ def _stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _scratch(nbytes, t, stream):
-    """A workspace of the caching allocator for a call on `stream` (None: the
-    current one)."""
-    w = torch.empty(nbytes, dtype=torch.uint8, device=t.device)
-    if stream is not None:
-        w.record_stream(torch.cuda.ExternalStream(stream))
-    return w
+def _empty(shape, dtype, dev, stream):
+    """A new tensor of the caching allocator for a call on `stream` (None: the
+    current one), from that stream's own memory: what another stream freed may
+    still be in use there."""
+    where = torch.device("cuda", dev)
+    if stream is None or stream == _stream(dev):
+        return torch.empty(shape, dtype=dtype, device=where)
+    s = torch.cuda.ExternalStream(stream, where) if stream else torch.cuda.default_stream(where)
+    with torch.cuda.stream(s):
+        return torch.empty(shape, dtype=dtype, device=where)
 
 
 def _first_dtype(*tensors):
@@ -574,13 +577,13 @@ def norm_block(X, Z=None, XO=None, Y=None, *, pre="rms", pre_weight=None, pre_bi
     if Z is not None:
         zt = Z.dtype
         if XO is None:
-            XO = torch.empty((M, N), dtype=xt, device=X.device)
+            XO = _empty((M, N), xt, dev, stream)
     elif XO is not None:
         raise ValueError("XO goes with Z")
     else:
         zt = xt if Y is None else Y.dtype
     if want_y and Y is None:
-        Y = torch.empty((M, N), dtype=zt, device=X.device)
+        Y = _empty((M, N), zt, dev, stream)
     z, ldz = _mat(Z, "Z", M, N, zt, dev)
     xo, ldxo = _mat(XO, "XO", M, N, xt, dev)
     y, ldy = _mat(Y, "Y", M, N, zt, dev)
@@ -632,7 +635,7 @@ def norm_block_backward(XO, dY=None, dXO=None, Z=None, *, pre="rms", pre_weight=
     if gt is not None:
         if workspace is None:
             need = lib.norm_block_backward_workspace(M, N, gate_rows if gate is not None else 1, 0)
-            workspace = _scratch(max(need, 16), XO, stream)
+            workspace = _empty(max(need, 16), torch.uint8, dev, stream)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous, on the current CUDA device")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
@@ -683,15 +686,12 @@ def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace
                 not set(map(T.get_device, outputs)) <= {dev} or not all(map(T.is_contiguous, outputs)):
             raise ValueError("an output must be contiguous, of its gradient's dtype, size and device")
         outs = list(map(T.data_ptr, outputs))
-    other = None if stream is None else torch.cuda.ExternalStream(stream)
     if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", dev))
-        if other is not None:
-            norm.record_stream(other)
+        norm = _empty(1, torch.float32, dev, stream)
     elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != dev:
         raise ValueError("norm must be one FP32 element on the current CUDA device")
     if workspace is None:
-        workspace = _scratch(lib.grad_clip_workspace(len(ptrs), 0), norm, stream)
+        workspace = _empty(lib.grad_clip_workspace(len(ptrs), 0), torch.uint8, dev, stream)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous, on the current CUDA device")
     st = grad_clip_raw(ptrs, outs, sizes, codes, max_norm, inv_scale, norm.data_ptr(),
@@ -803,7 +803,7 @@ class Gemm:
         F = W.shape[0] // 2
         xt = X.dtype
         if H is None:
-            H = torch.empty((M, F), dtype=xt, device=X.device)
+            H = _empty((M, F), xt, dev, stream)
         x, ldx = _mat(X, "X", M, K, xt, dev)
         w, ldw = _mat(W, "W", 2 * F, K, xt, dev)
         hp, ldh = _mat(H, "H", M, F, None, dev)
@@ -830,7 +830,7 @@ class Gemm:
         M, F = dH.shape
         t = dH.dtype
         if dP is None:
-            dP = torch.empty((M, 2 * F), dtype=t, device=dH.device)
+            dP = _empty((M, 2 * F), t, dev, stream)
         if dX is not None and W is None or dW is not None and X is None:
             raise ValueError("dX needs W and dW needs X")
         K = next((v.shape[-1] for v in (X, W, dX, dW) if v is not None), 0)

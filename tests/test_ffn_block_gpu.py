@@ -176,3 +176,37 @@ def test_step_in_a_graph_beside_an_eager_one(lib):
         assert math.isfinite(float(norm))
     for b in (a, e):
         b.g.close()
+
+
+def test_new_tensors_on_another_stream():
+    """Tensors that a call on a given stream makes are not taken from memory
+    that the current stream has freed and still writes to."""
+    import mixed_precision_dense_sm_gb300 as lib
+    g = lib.Gemm()
+    gen = torch.Generator().manual_seed(8)
+    X = torch.randn(256, 512, generator=gen).to(torch.bfloat16).cuda()
+    W = torch.randn(1024, 512, generator=gen).to(torch.bfloat16).cuda()
+    v = torch.ones(512, device="cuda")
+    dv = torch.empty_like(v)
+
+    def calls(stream):
+        H = g.glu(X, W, stream=stream)
+        XO, Y = lib.norm_block(X, H, post="rms", pre_weight=v, stream=stream)
+        lib.norm_block_backward(XO, Y, Z=H, post="rms", pre_weight=v, dpre_weight=dv, stream=stream)
+        return [H, XO, Y, dv.clone() if stream is None else dv, lib.grad_clip([H, XO], 1.0, outputs=outs, stream=stream)]
+    outs = [torch.empty(256, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    want = [t.clone() for t in calls(None)]
+    dv.zero_()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(50_000_000)                # the current stream is late
+    tmp = [torch.empty(n, dtype=torch.uint8, device="cuda")
+           for n in (4, 512, 4096, 1 << 18, 1 << 18, 1 << 18, 1 << 20, 1 << 20, 1 << 22)]
+    for t in tmp:
+        t.fill_(255)
+    del tmp, t
+    got = calls(side.cuda_stream)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g.close()
