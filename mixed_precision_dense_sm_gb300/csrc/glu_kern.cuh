@@ -270,19 +270,21 @@ __global__ void __launch_bounds__(kGluDotThreads, kGluDotCtas)
         F2 ag[MT], au[MT];
         #pragma unroll
         for (int m = 0; m < MT; ++m) ag[m] = au[m] = mk2(0.0f);
-        for (int32_t k0 = lane * 8; k0 < p.K; k0 += 256 * kGluDotAhead) {
+        // (unsigned: K may end less than a step below 2^31)
+        const uint32_t K = static_cast<uint32_t>(p.K);
+        for (uint32_t k0 = lane * 8; k0 < K; k0 += 256 * kGluDotAhead) {
             uint4 g[kGluDotAhead], u[kGluDotAhead];
             #pragma unroll
             for (int i = 0; i < kGluDotAhead; ++i) {
-                const int32_t k = k0 + i * 256;
-                const bool in = k < p.K;
+                const uint32_t k = k0 + i * 256;
+                const bool in = k < K;
                 g[i] = in ? __ldcs(reinterpret_cast<const uint4*>(wg + k)) : make_uint4(0u, 0u, 0u, 0u);
                 u[i] = in ? __ldcs(reinterpret_cast<const uint4*>(wu + k)) : make_uint4(0u, 0u, 0u, 0u);
             }
             #pragma unroll
             for (int i = 0; i < kGluDotAhead; ++i) {
-                const int32_t k = k0 + i * 256;
-                if (k >= p.K) break;
+                const uint32_t k = k0 + i * 256;
+                if (k >= K) break;
                 const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
                 const uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
                 #pragma unroll

@@ -308,6 +308,26 @@ def test_forward_few_tokens(g, M, F, K):
     forward_case(g, M, F, K, FP, "gelu", bias=F32, save=M % 2 == 1)
 
 
+@pytest.mark.parametrize("M", [1, 2])
+def test_rows_of_almost_2_to_the_31(g, M):
+    """A few tokens of the longest rows: zeros but for the first and the last
+    elements, whose products are exact."""
+    K, F = 2 ** 31 - 8, 1
+    free, _ = torch.cuda.mem_get_info()
+    if free < 40 << 30:
+        pytest.skip("needs 40 GB")
+    X, W = torch.zeros(M, K, dtype=BF, device="cuda"), torch.zeros(2 * F, K, dtype=BF, device="cuda")
+    for t in (X, W):
+        t[:, :8] = 2
+        t[:, -8:] = torch.arange(1, 9, device="cuda").to(BF)
+    W[1] *= -1
+    H = g.glu(X, W, act="none")
+    P = 8 * 4 + sum(i * i for i in range(1, 9))            # 236
+    assert (H.float() == torch.tensor(-P * P, dtype=torch.float32).to(BF).float()).all()
+    del X, W
+    torch.cuda.empty_cache()
+
+
 def test_refusals_on_the_device(g):
     import mixed_precision_dense_sm_gb300 as lib
     X, W = torch.randn(8, 32, device="cuda").to(BF), torch.randn(16, 32, device="cuda").to(BF)
