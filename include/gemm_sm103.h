@@ -38,7 +38,9 @@
  *     or base address is not 16-byte aligned, split-K partial sums) and a
  *     device-visible error word.  The workspace grows on demand inside
  *     gemm_run (a cudaMalloc, which synchronises the device) and is released
- *     by gemm_destroy.
+ *     by gemm_destroy.  Under stream capture it grows too, without waiting; a
+ *     buffer that a captured graph may address stays allocated until
+ *     gemm_destroy, which therefore comes after the last replay.
  *   - gemm_run is asynchronous with respect to the host: it enqueues work on
  *     `stream` and returns.  A handle must not be used from two host threads
  *     at once; use one handle per thread or per stream.  Calls on one handle

@@ -37,12 +37,8 @@
  *
  * Ownership, threading, workspace and errors: as gemm_run (gemm_sm103.h), on the
  * handle's device, which has to be current (INVALID_VALUE otherwise): the
- * handle's workspace serves one stream at a time, and a call that grows it
- * allocates.  To capture calls into a CUDA graph, make the same calls once
- * before the capture (so that nothing allocates under it) and give each graph
- * that may run beside another its own handle; a buffer that the workspace has
- * outgrown stays allocated until gemm_destroy, so captured graphs keep
- * reading valid memory.
+ * handle's workspace serves one stream at a time.  Calls can be captured into a
+ * CUDA graph; give each graph that may run beside another its own handle.
  */
 #ifndef GLU_SM103_H_
 #define GLU_SM103_H_

@@ -689,9 +689,43 @@ bool encode_glu_store(EncodeTiledFn encode, CUtensorMap* map, int32_t dtype, voi
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The handle's workspace of at least `bytes`.  Under stream capture it cannot
-// grow (an allocation would end the capture): ALLOC.  A buffer that a captured
-// graph may still address is kept until gemm_destroy when it is outgrown.
+// A buffer of `want` bytes whose tile counters are zero, made while `capturing`
+// is under way on the calling thread: allocated in relaxed mode, as the graph
+// does not hold the allocation, and cleared on a stream of its own.
+void* workspace_buffer(size_t want, bool capturing) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    if (capturing && cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) {
+        cudaGetLastError();
+        return nullptr;
+    }
+    void* p = nullptr;
+    cudaError_t e = cudaMalloc(&p, want);
+    if (e != cudaSuccess) {
+        p = nullptr;
+    } else if (!capturing) {
+        e = cudaMemset(p, 0, kWsHeaderBytes);
+    } else {
+        cudaStream_t s;
+        e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+        if (e == cudaSuccess) {
+            e = cudaMemsetAsync(p, 0, kWsHeaderBytes, s);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+            cudaStreamDestroy(s);
+        }
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        if (p) cudaFree(p);
+        p = nullptr;
+    }
+    if (capturing) cudaThreadExchangeStreamCaptureMode(&mode);
+    return p;
+}
+
+// The handle's workspace of at least `bytes`.  A buffer that a captured graph
+// may still address, and any buffer outgrown under capture, where nothing can
+// wait for its users, is kept until gemm_destroy.  The stream-K tile counters
+// start at zero; every call leaves them at zero again.
 gemm_status_t ensure_workspace(gemm_ctx* h, size_t bytes, cudaStream_t stream) {
     if (bytes == 0) return GEMM_OK;
     cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
@@ -701,36 +735,20 @@ gemm_status_t ensure_workspace(gemm_ctx* h, size_t bytes, cudaStream_t stream) {
         h->ws_captured = h->ws_captured || capturing;
         return GEMM_OK;
     }
-    if (capturing) return GEMM_ERR_ALLOC;
-    if (h->ws && h->ws_captured) {
+    if (h->ws && (h->ws_captured || capturing)) {
         gemm_ctx::Retired* r = new (std::nothrow) gemm_ctx::Retired;
         if (r == nullptr) return GEMM_ERR_ALLOC;
         r->p = h->ws;
         r->next = h->retired;
         h->retired = r;
-        h->ws = nullptr;
-        h->ws_bytes = 0;
-        h->ws_captured = false;
-    }
-    if (h->ws) {
+    } else if (h->ws) {
         cudaFree(h->ws);          // implicit device synchronisation: no user of the old buffer remains
-        h->ws = nullptr;
-        h->ws_bytes = 0;
     }
-    size_t want = bytes + (bytes >> 2);
-    if (cudaMalloc(&h->ws, want) != cudaSuccess) {
-        cudaGetLastError();
-        h->ws = nullptr;
-        return GEMM_ERR_ALLOC;
-    }
-    // The stream-K tile counters must start at zero; every call leaves them
-    // at zero again.
-    if (cudaMemset(h->ws, 0, kWsHeaderBytes) != cudaSuccess) {
-        cudaGetLastError();
-        cudaFree(h->ws);
-        h->ws = nullptr;
-        return GEMM_ERR_ALLOC;
-    }
+    h->ws_bytes = 0;
+    h->ws_captured = capturing;
+    const size_t want = bytes + (bytes >> 2);
+    h->ws = workspace_buffer(want, capturing);
+    if (h->ws == nullptr) return GEMM_ERR_ALLOC;
     h->ws_bytes = want;
     return GEMM_OK;
 }

@@ -257,24 +257,39 @@ def test_capture_replays_with_new_inputs(g):
     assert all(torch.equal(a, b) for a, b in zip(got, (H, P, dP, dX, dW)))
 
 
-def test_capture_cannot_grow_the_workspace():
+@pytest.mark.parametrize("mode", ["global", "thread_local", "relaxed"])
+def test_capture_grows_the_workspace(mode):
+    """First calls of a handle under capture, each with more workspace than the
+    last; the graph stays right once larger calls have outgrown its buffers."""
     import mixed_precision_dense_sm_gb300 as lib
     h = lib.Gemm()
-    X = torch.randn(300, 1001, device="cuda").to(BF)
-    W = torch.randn(600, 1001, device="cuda").to(BF)
-    H = torch.empty(300, 300, dtype=BF, device="cuda")
-    a = torch.ones(8, device="cuda")
+    gen = torch.Generator().manual_seed(6)
+    Xs = [torch.randn(M, 1001, generator=gen).to(BF).cuda() for M in (30, 300, 600)]
+    W = (torch.randn(600, 1001, generator=gen) / 32).to(BF).cuda()
+    Hs = [torch.empty(X.shape[0], 300, dtype=BF, device="cuda") for X in Xs]
+    C = torch.empty(300, 600, dtype=BF, device="cuda")
+
+    def step():
+        for X, H in zip(Xs, Hs):
+            h.glu(X, W, H)                       # unaligned rows: copied to the workspace
+        h(Xs[1], W, C, transB="T")
     graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        a.mul_(2)
-        with pytest.raises(lib.GemmError) as e:
-            h.glu(X, W, H)                       # unaligned rows: needs workspace
-        a.add_(1)
-    assert e.value.status == 3
+    with torch.cuda.graph(graph, capture_error_mode=mode):
+        step()
+    h.glu(torch.cat(Xs * 4), W)                  # outgrows it again
+    for t in (*Hs, C):
+        t.zero_()
     graph.replay()
     torch.cuda.synchronize()
-    assert (a == 3).all()
-    h.close()
+    got = [t.clone() for t in (*Hs, C)]
+    other = lib.Gemm()
+    h, mine = other, h
+    step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, (*Hs, C)))
+    del graph
+    mine.close()
+    other.close()
 
 
 @pytest.mark.parametrize("shape", [(300, 256, 512), (16, 640, 1024), (64, 20480, 256), (2048, 2048, 256)],
