@@ -912,7 +912,7 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
         int32_t log_per = 2;
         while ((pl.pub.split_k << log_per) < s.block_n) ++log_per;
         s.p = GluSkinnyParams{static_cast<int32_t>(glu->M), static_cast<int32_t>(glu->F), pl.k_blocks,
-                              pl.pub.split_k, log_per, pl.pub.stages,
+                              pl.pub.split_k, log_per,
                               instr_desc(fmt, false, false, kBlockM, static_cast<uint32_t>(s.block_n)),
                               C, glu->ldh, o->P, o->ldp, o->bias, o->bias ? o->bias_dtype : GEMM_F32,
                               o->activation, dt.c, err_dev, wait_limit_ns ? wait_limit_ns : kWaitTimeoutNs,

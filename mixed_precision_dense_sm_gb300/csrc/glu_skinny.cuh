@@ -30,7 +30,6 @@ struct GluSkinnyParams {
     int32_t k_blocks;                    // of KC chunks
     int32_t splits;                      // CTAs per tile (the cluster's size): 1, 2, 4, 8, at most BN / 4
     int32_t log_per;                     // log2(BN / splits): tokens each CTA finishes
-    int32_t stages;
     uint32_t idesc;
     void* H; int64_t ldh;
     void* P; int64_t ldp;

@@ -86,7 +86,7 @@ int threads_for(int64_t N, int chunks8) {
     return t == 512 && N <= static_cast<int64_t>(384) * 8 * chunks8 ? 384 : t;
 }
 
-constexpr int64_t kChunkCost = 32768;
+constexpr double kChunkCost = 32768.0;
 
 struct Chunks {
     int64_t group_rows, groups, per_group, rows;
@@ -102,14 +102,15 @@ Chunks chunks_for(int64_t M, int64_t N, int64_t gate_rows, int64_t resident) {
     Chunks c;
     c.group_rows = (gate_rows > 1 && gate_rows < M) ? gate_rows : (M > 0 ? M : 1);
     c.groups = ceil_div(M > 0 ? M : 1, c.group_rows);
-    int64_t per = ceil_div(resident, c.groups), best = INT64_MAX;
+    const int64_t per = ceil_div(resident, c.groups);
+    double best = INFINITY;
     int64_t most = c.groups > 1 && per < 4 ? 4 : per;
     if (most > c.group_rows) most = c.group_rows;
     c.rows = ceil_div(c.group_rows, most);
     for (int64_t i = c.groups > 1 ? (most > 64 ? most - 64 : 1) : most; i <= most; ++i) {
         const int64_t rows = ceil_div(c.group_rows, i);
         const int64_t waves = ceil_div(c.groups * ceil_div(c.group_rows, rows), resident);
-        const int64_t cost = waves * (rows * N + kChunkCost);
+        const double cost = static_cast<double>(waves) * (static_cast<double>(rows) * static_cast<double>(N) + kChunkCost);
         if (cost < best) {
             best = cost;
             c.rows = rows;

@@ -148,7 +148,7 @@ __device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool w
     for (int q = 0; q < 4; ++q) o[q] = mk2(f[2 * q], f[2 * q + 1]);
 }
 
-// o *= parameter, o += parameter, where there is one.
+// o *= parameter, where there is one.
 template <bool VEC>
 __device__ __forceinline__ void scale_by(F8& o, const void* v, int32_t dtype, bool wide, Spot<VEC> s,
                                          int32_t N) {
@@ -157,15 +157,6 @@ __device__ __forceinline__ void scale_by(F8& o, const void* v, int32_t dtype, bo
     load_param8<VEC>(v, dtype, wide, s, N, w);
     #pragma unroll
     for (int q = 0; q < 4; ++q) o[q] = mul2(o[q], w[q]);
-}
-template <bool VEC>
-__device__ __forceinline__ void shift_by(F8& o, const void* v, int32_t dtype, bool wide, Spot<VEC> s,
-                                         int32_t N) {
-    if (v == nullptr) return;
-    F8 w;
-    load_param8<VEC>(v, dtype, wide, s, N, w);
-    #pragma unroll
-    for (int q = 0; q < 4; ++q) o[q] = add2(o[q], w[q]);
 }
 
 // Elements past column N as 0 (a chunk with VEC has none).
@@ -301,7 +292,7 @@ __device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, F8& v) {
             *reinterpret_cast<float4*>(row + s.base) = join2(v[0], v[1]);
             *reinterpret_cast<float4*>(row + s.base + 4) = join2(v[2], v[3]);
         } else {
-                #pragma unroll
+            #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float lo, hi;
                 get2(v[q], lo, hi);
@@ -373,7 +364,7 @@ __device__ __forceinline__ void group_sum(Group<TT>& g, float (&v)[K]) {
         } else {
             v[k] = 0.0f;
             #pragma unroll
-            for (int w = 0; w < g.warps(); w += 4) {    // a power of two, 4 at least
+            for (int w = 0; w < g.warps(); w += 4) {    // a multiple of 4
                 const float4 x = *reinterpret_cast<const float4*>(q + w);
                 v[k] += (x.x + x.y) + (x.z + x.w);
             }
