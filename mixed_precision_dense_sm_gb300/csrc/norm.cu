@@ -132,10 +132,10 @@ void set_chunks(Params& p, const Chunks& c) {
     p.chunk_rows = c.rows;
 }
 
-// Shared memory of a CTA of `groups` groups: exchange buffers, the n_par
-// vectors, the groups' rings.
-int64_t smem_for(const Params& p, int chunks8, int groups, int stages) {
-    return groups * static_cast<int64_t>(p.T) + static_cast<int64_t>(p.n_par) * chunks8 * 32 * p.T +
+// Shared memory of a CTA of `groups` groups: exchange buffers for `sums` values,
+// the n_par vectors, the groups' rings.
+int64_t smem_for(const Params& p, int sums, int chunks8, int groups, int stages) {
+    return groups * static_cast<int64_t>(p.T / 32 * 8 * sums) + static_cast<int64_t>(p.n_par) * chunks8 * 32 * p.T +
            static_cast<int64_t>(groups) * stages * p.slot_bytes;
 }
 
@@ -145,14 +145,14 @@ int64_t smem_for(const Params& p, int chunks8, int groups, int stages) {
 // CTA (many small ones leave the driver's default split of an SM's memory with
 // room for few: 5 of 32 one-warp CTAs).  One slot only where two fit nowhere.  Returns CTAs per SM (at most
 // `per_sm`), 0 where nothing fits.
-int choose_cta(Params& p, int chunks8, int most, int resident, int per_sm, int& groups) {
+int choose_cta(Params& p, int sums, int chunks8, int most, int resident, int per_sm, int& groups) {
     int64_t best = 0;
     int ctas = 0;
     for (int stages = kMaxStages; stages >= 1; --stages) {
         if (stages == 1 && best > 0) break;
         // (named barriers number the groups of more than a warp: 15 at most)
         for (int g = 1; g * p.T <= most && (g <= 15 || p.T == 32); g *= 2) {
-            const int64_t bytes = smem_for(p, chunks8, g, stages);
+            const int64_t bytes = smem_for(p, sums, chunks8, g, stages);
             if (bytes > kSmemPerCta) continue;
             int64_t n = kSmemPerSm / (bytes + 1024);
             if (n > resident / (g * p.T)) n = resident / (g * p.T);
@@ -289,7 +289,7 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     p.slot_bytes = static_cast<uint32_t>(l.chunks8 * 8 * p.T * (esize(x_dtype) + (Z ? esize(z_dtype) : 0)));
     int groups = 1;
     // 64 registers per thread
-    const int ctas = choose_cta(p, l.chunks8, 1024, 1024, 32, groups);
+    const int ctas = choose_cta(p, kForwardSums, l.chunks8, 1024, 1024, 32, groups);
     if (ctas == 0) return GEMM_ERR_NOT_SUPPORTED;
     const Chunks ch = chunks_for(M, N, Z && block->gate ? block->gate_rows : 1,
                                  static_cast<int64_t>(sms) * ctas / p.cluster);
@@ -298,7 +298,7 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     while (groups > 1 && groups / 2 >= ch.rows) groups /= 2;
     l.threads = groups * p.T;
     l.grid = static_cast<int>(ch.groups * ch.per_group * p.cluster);
-    l.smem = static_cast<size_t>(smem_for(p, l.chunks8, groups, p.stages));
+    l.smem = static_cast<size_t>(smem_for(p, kForwardSums, l.chunks8, groups, p.stages));
     l.stream = reinterpret_cast<cudaStream_t>(stream);
     return status_of(run_forward(x_dtype, z_dtype, l));
 }
@@ -395,12 +395,12 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
             l.chunks8 * 8 * p.T *
             (esize(x_dtype) * (dXO ? 2 : 1) + (Z ? esize(z_dtype) : 0) + (dY ? esize(z_dtype) : 0)));
         int groups = 1;
-        if (choose_cta(p, l.chunks8, kBackThreads, kBackThreads, 1, groups) == 0) return GEMM_ERR_NOT_SUPPORTED;
+        if (choose_cta(p, kBackwardSums, l.chunks8, kBackThreads, kBackThreads, 1, groups) == 0) return GEMM_ERR_NOT_SUPPORTED;
         while (groups > 1 && groups / 2 >= ch.rows) groups /= 2;
         l.threads = groups * p.T;
-        l.smem = static_cast<size_t>(smem_for(p, l.chunks8, groups, p.stages));
+        l.smem = static_cast<size_t>(smem_for(p, kBackwardSums, l.chunks8, groups, p.stages));
         // the groups' column sums pass through the ring's memory
-        const size_t line = static_cast<size_t>(smem_for(p, l.chunks8, groups, 0)) +
+        const size_t line = static_cast<size_t>(smem_for(p, kBackwardSums, l.chunks8, groups, 0)) +
                             static_cast<size_t>(p.T) * l.chunks8 * 32;
         if (l.smem < line) l.smem = line;
         if (l.smem > static_cast<size_t>(kSmemPerCta)) return GEMM_ERR_NOT_SUPPORTED;

@@ -321,40 +321,98 @@ __device__ __forceinline__ void store8(E* row, Spot<VEC> s, int32_t N, F8& v) {
 }
 
 // The group of threads that shares a row: T threads of the CTA (a compile-time
-// number for TT > 0).
-template <int TT>
+// number for TT > 0); KR: the most values summed together.
+template <int TT, int KR>
 struct Group {
+    static constexpr int kMost = KR;
     int T_, t, index;           // threads, this thread's number, the group's number
-    float* red;                 // [2][4][warps] exchange buffer of this group
+    float* red;                 // [2][KR][warps] exchange buffer of this group
     int parity;
-    float* pair;                // [2][2][4] exchange buffer of a CTA pair, or NULL
+    float* pair;                // [2][2][KR] exchange buffer of a CTA pair, or NULL
     uint32_t rank;              // this CTA's number in the pair
     __device__ __forceinline__ int T() const { return TT > 0 ? TT : T_; }
     __device__ __forceinline__ int warps() const { return T() >> 5; }
 };
 
-template <int TT>
-__device__ __forceinline__ void group_barrier(const Group<TT>& g) {
+template <class G>
+__device__ __forceinline__ void group_barrier(const G& g) {
     asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.T()) : "memory");
 }
 
+// Sums of v[0..K) over a warp by halving: at each step a lane keeps one half of
+// the values it still has (the upper half where its bit is set) and gives the
+// other away, so K values take about K + 3 exchanges instead of 5 K.  The lane
+// ends with the sum of value warp_slot<K>(lane) in v[0].
+template <int K, int O = 16, int L>
+__device__ __forceinline__ void warp_halve(float (&v)[L], int lane) {
+    constexpr int H = (K + 1) / 2;
+    if constexpr (K > 1) {
+        const bool up = (lane & O) != 0;
+        #pragma unroll
+        for (int k = 0; k < H; ++k) {
+            const float hi = k + H < K ? v[k + H] : 0.0f;
+            const float give = up ? v[k] : hi;
+            v[k] = (up ? hi : v[k]) + __shfl_xor_sync(0xffffffffu, give, O);
+        }
+    } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], O);
+    }
+    if constexpr (O > 1) warp_halve<H, O / 2>(v, lane);
+}
+// Number of the value that a lane ends with, -1 for none.
+template <int K>
+__host__ __device__ constexpr int warp_slot(int lane) {
+    int first = 0, count = K, held = K;
+    for (int o = 16; o > 0; o >>= 1) {
+        if (held <= 1) break;
+        const int h = (held + 1) / 2;
+        if (lane & o) {
+            first += h;
+            count -= h;
+        } else if (count > h) {
+            count = h;
+        }
+        held = h;
+    }
+    return count > 0 ? first : -1;
+}
+// Lanes that end with each value.
+template <int K>
+struct WarpLanes {
+    int at[K];
+    bool all;
+    __host__ __device__ constexpr WarpLanes() : at{}, all(true) {
+        for (int k = 0; k < K; ++k) {
+            at[k] = -1;
+            for (int l = 31; l >= 0; --l)
+                if (warp_slot<K>(l) == k) at[k] = l;
+            all = all && at[k] >= 0;
+        }
+    }
+};
+
 // Sums of K values over the group, in the same order on every run; every
 // thread gets them.  One barrier: consecutive sums use alternate buffers.
-template <int K, int TT>
-__device__ __forceinline__ void group_sum(Group<TT>& g, float (&v)[K]) {
-    static_assert(K <= 4, "exchange buffer");
-    #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        #pragma unroll
-        for (int k = 0; k < K; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+template <int K, class G>
+__device__ __forceinline__ void group_sum(G& g, float (&v)[K]) {
+    constexpr WarpLanes<K> lanes;
+    static_assert(K <= G::kMost, "exchange buffer");
+    static_assert(lanes.all, "every value ends somewhere");
+    const int lane = static_cast<int>(threadIdx.x) & 31;
+    warp_halve<K>(v, lane);
+    if (g.T() == 32) {
+        if constexpr (K > 1) {
+            const float mine = v[0];
+            #pragma unroll
+            for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, mine, lanes.at[k]);
+        }
+        return;
     }
-    if (g.T() == 32) return;
-    float* r = g.red + g.parity * g.warps() * 4;
+    float* r = g.red + g.parity * g.warps() * G::kMost;
     g.parity ^= 1;
-    if ((threadIdx.x & 31) == 0) {
-        #pragma unroll
-        for (int k = 0; k < K; ++k) r[k * g.warps() + (g.t >> 5)] = v[k];
-    }
+    // (lanes that end with the same value write the same bits)
+    const int slot = warp_slot<K>(lane);
+    if (slot >= 0) r[slot * g.warps() + (g.t >> 5)] = v[0];
     group_barrier(g);
     #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -374,7 +432,7 @@ __device__ __forceinline__ void group_sum(Group<TT>& g, float (&v)[K]) {
     // the other half of the row: each CTA leaves its sums in both CTAs' shared
     // memory, and both add them in rank order.  The buffer of this parity is
     // written again only two sums on, behind the next sum's cluster barrier.
-    float* x = g.pair + (g.parity * 2 + g.rank) * 4;
+    float* x = g.pair + (g.parity * 2 + g.rank) * G::kMost;
     if (g.t == 0) {
         const uint32_t peer = map_to_rank(smem_addr(x), g.rank ^ 1u);
         #pragma unroll
@@ -385,18 +443,20 @@ __device__ __forceinline__ void group_sum(Group<TT>& g, float (&v)[K]) {
         }
     }
     cluster_sync_all();
-    const float* y = g.pair + g.parity * 8;
+    const float* y = g.pair + g.parity * 2 * G::kMost;
     #pragma unroll
-    for (int k = 0; k < K; ++k) v[k] = y[k] + y[4 + k];
+    for (int k = 0; k < K; ++k) v[k] = y[k] + y[G::kMost + k];
 }
 
-template <int TT>
-__device__ __forceinline__ Group<TT> make_group(const Params& p, uint8_t* smem) {
-    Group<TT> g;
+constexpr int kForwardSums = 4, kBackwardSums = 4;
+
+template <class G>
+__device__ __forceinline__ G make_group(const Params& p, uint8_t* smem) {
+    G g;
     g.T_ = p.T;
     g.index = static_cast<int>(threadIdx.x) / g.T();
     g.t = static_cast<int>(threadIdx.x) - g.index * g.T();
-    g.red = reinterpret_cast<float*>(smem) + g.index * (2 * 4 * g.warps());
+    g.red = reinterpret_cast<float*>(smem) + g.index * (2 * G::kMost * g.warps());
     g.parity = 0;
     g.pair = nullptr;
     g.rank = 0;
@@ -427,8 +487,8 @@ __device__ __forceinline__ uint8_t* par_at(uint8_t* par, int k, int T) {
 
 // Fills the vectors in shared memory; every group reads them, the group
 // numbered 0 writes them.
-template <int C, bool VEC, int TT>
-__device__ __forceinline__ void fill_vectors(const Params& p, const Group<TT>& g, uint8_t* par,
+template <int C, bool VEC, class G>
+__device__ __forceinline__ void fill_vectors(const Params& p, const G& g, uint8_t* par,
                                              int64_t group, int32_t col0) {
     if (g.index == 0) {
         const bool wide = p.vec_aligned != 0;
@@ -481,8 +541,8 @@ __device__ __forceinline__ float inv_size(float sum, const Params& p) {
 // ------------------------------------------------------------------- forward
 
 // 1 / size of a row whose chunks are in v; v becomes v - mean for LayerNorm.
-template <int C, bool VEC, int TT>
-__device__ __forceinline__ float norm_stats(Group<TT>& g, const Params& p, int kind, int32_t col0,
+template <int C, bool VEC, class G>
+__device__ __forceinline__ float norm_stats(G& g, const Params& p, int kind, int32_t col0,
                                             F8 (&v)[C]) {
     if (kind == kNone) return 1.0f;
     if (kind == kLayer) {
@@ -517,15 +577,15 @@ template <typename XT, typename ZT, int TT, int C, bool VEC>
 __global__ void __launch_bounds__(1024)
     forward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    Group<TT> g = make_group<TT>(p, smem);
+    auto g = make_group<Group<TT, kForwardSums>>(p, smem);
     const int T = g.T(), t = g.t;
     const int groups = static_cast<int>(blockDim.x) / T;
-    uint8_t* par = smem + groups * g.warps() * 32;
+    uint8_t* par = smem + groups * g.warps() * (8 * kForwardSums);
     uint8_t* ring = par_at<C>(par, p.n_par, T) + static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
     const uint32_t x_bytes = static_cast<uint32_t>(C) * 8u * sizeof(XT) * T;
     const bool has_z = p.Z != nullptr;
     const int32_t N = p.N;
-    __shared__ float pair[16];
+    __shared__ float pair[4 * kForwardSums];
     int32_t col0 = 0;
     int64_t chunk = blockIdx.x;
     if (p.cluster == 2) {
@@ -661,10 +721,10 @@ template <typename XT, typename ZT, int TT, int C, bool VEC, bool BIAS>
 __global__ void __launch_bounds__(kBackThreads)
     backward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
-    Group<TT> g = make_group<TT>(p, smem);
+    auto g = make_group<Group<TT, kBackwardSums>>(p, smem);
     const int T = g.T(), t = g.t;
     const int groups = static_cast<int>(blockDim.x) / T;
-    uint8_t* par = smem + groups * g.warps() * 32;
+    uint8_t* par = smem + groups * g.warps() * (8 * kBackwardSums);
     uint8_t* rings = par_at<C>(par, p.n_par, T);
     uint8_t* ring = rings + static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
     // a slot: [XO][dXO][Z][dY], the absent ones left out
@@ -673,7 +733,7 @@ __global__ void __launch_bounds__(kBackThreads)
     const bool has_z = p.Z != nullptr, has_dy = p.dY != nullptr, has_dxo = p.dXO != nullptr;
     const uint32_t o_dxo = xb, o_z = o_dxo + (has_dxo ? xb : 0u), o_dy = o_z + (has_z ? zb : 0u);
     const int32_t N = p.N;
-    __shared__ float pair[16];
+    __shared__ float pair[4 * kBackwardSums];
     int32_t col0 = 0;
     int64_t chunk = blockIdx.x;
     if (p.cluster == 2) {
