@@ -171,7 +171,9 @@ struct TcParams {
 // values of an output column; N = F and tile column tn starts at output column
 // tn * BN / 2.  Swapped, rows 0-63 are the gate's and 64-127 the up
 // projection's, M = F, and tile row tm starts at output column tm * 64; the
-// halves meet through shared memory.
+// halves meet through shared memory.  Bound by the tensor cores: 8192 tokens,
+// 4096 -> 14336, bf16 with P stored, 1045 to 1175 us as the power cap allows
+// (1.64 to 1.84 PFLOP/s), the tensor pipe 86 % busy at 4096 tokens -> 8192.
 struct GluParams : TcParams {
     alignas(64) CUtensorMap tmP;    // P (F, M, 2) for TMA stores
     void* P;                        // pre-activations, or nullptr
@@ -760,7 +762,7 @@ __device__ __forceinline__ void glu_sums(uint32_t t_row, uint32_t t_spare, bool 
 // The same for a warp's 32 rows (the first at `base`) that are not 16-byte
 // aligned: turned through 4 KB of shared memory, so that each store
 // instruction writes 32 consecutive elements of one row and not one element
-// of 32 rows (a ragged 1000 x 777 -> 1023 problem 45 -> 17 us).  Element
+// of 32 rows (1000 tokens, 777 -> 1023, with what followed: 45 -> 21 us).  Element
 // (r, c) lies at word r * 32 + (c ^ r): no bank conflicts either way.
 template <typename OutT>
 __device__ __forceinline__ void glu_store_turned(float* buf, OutT* base, int64_t ld, int32_t rows,

@@ -11,7 +11,7 @@
 // the first (the grids are multiples of the SMs), and what the first pass read
 // last it marked to stay in L2 (kKeepBytes).  Bound by HBM: two reads and one write of the
 // gradients (one read where nothing is scaled in place, or where they fit in
-// L2).
+// L2).  120M bf16 elements: 115 us; three passes over them at copy speed are 106.
 //
 // Squares are summed in FP32 over one batch of a thread (kVecs 16-byte
 // vectors: 16 or 32 elements) and then in FP64: one FP64 add per batch, as

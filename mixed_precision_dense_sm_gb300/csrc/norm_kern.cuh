@@ -2,17 +2,24 @@
 // residual scale and residual add (include/norm_sm103.h): forward and
 // backward row kernels, and the backward's sum over rows.
 //
-// Both row kernels are bound by HBM: each matrix element is read once and
-// written once.  A row belongs to a group of T threads of a CTA (a warp for
-// narrow rows, the whole CTA for wide ones); each thread owns C chunks of 8
-// elements.  A thread copies its own elements of the next row to shared
-// memory with cp.async while the group works on the current one, into a ring
-// of slots that only this thread reads: no barrier guards the copies, and no
-// registers hold loads in flight.  What the group shares are the sums of a
-// row: a butterfly in each warp, one shared-memory exchange, one barrier.  A
-// CTA takes a chunk of consecutive rows that see the same row of the gate, so
-// the weights, the gate and the scale fold into vectors that it converts to
-// FP32 in shared memory once.
+// Each matrix element is read once and written once.  A row belongs to a group
+// of T threads of a CTA (a warp for narrow rows, the whole CTA for wide ones);
+// each thread owns C chunks of 8 elements.  A thread copies its own elements of
+// the next row to shared memory with cp.async while the group works on the
+// current one, into a ring of slots that only this thread reads: no barrier
+// guards the copies, and no registers hold loads in flight.  What the group
+// shares are the sums of a row: halving in each warp, one shared-memory
+// exchange, one barrier.  A CTA takes a chunk of consecutive rows that see the
+// same row of the gate, so the weights, the gate and the scale fold into
+// vectors that it converts to FP32 in shared memory once.
+//
+// 8192 x 4096 bf16, RMSNorm on both sides, a gate per channel.  Forward: 49 us,
+// 5.4 TB/s; issue slots 64 % and DRAM 60 % busy.  Backward: 84 us and 6 for the
+// sums, 4.5 TB/s; bound by its instructions, 51 per element (16-bit pairs are
+// unpacked again in each of its passes over a row), at the 16 warps per SM that
+// its registers leave: issue slots 54 % busy.  One exchange per row in place of
+// two (the post-norm's sums, from products known before the pre-norm's size)
+// costs more products than it saves: 93 us for 84.
 //
 // Rows that are not 16-byte aligned, or N not a multiple of 8, go element by
 // element: a thread's 8 elements are then 32 apart, so a warp's accesses stay
