@@ -47,11 +47,11 @@ static cudaError_t forward_c(const Launch& l) {
     return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, TT, C, VEC>, l, mu, raised_to);
 }
 
-template <int TT, int C, bool VEC, bool BIAS>
+template <int TT, int C, bool VEC, bool BIAS, int KIND>
 static cudaError_t backward_c(const Launch& l) {
     static std::mutex mu;
     static size_t raised_to = 0;
-    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, BIAS>, l, mu, raised_to);
+    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, BIAS, KIND>, l, mu, raised_to);
 }
 
 // Threads per row and chunks per thread: one chunk for rows of up to 256
@@ -75,28 +75,35 @@ cudaError_t NORM_CAT(forward_, NORM_SUFFIX)(const Launch& l) {
     }
 }
 
-template <bool BIAS>
-static cudaError_t backward_v(const Launch& l) {
-    if (l.chunks8 == 1) return backward_c<32, 1, true, BIAS>(l);
+template <bool BIAS, int KIND>
+static cudaError_t backward_k(const Launch& l) {
+    if (!l.p.vec) return backward_c<0, 1, false, BIAS, KIND>(l);
+    if (l.chunks8 == 1) return backward_c<32, 1, true, BIAS, KIND>(l);
     switch (l.p.T) {
-        case 32: return backward_c<32, 2, true, BIAS>(l);
-        case 64: return backward_c<64, 2, true, BIAS>(l);
-        case 128: return backward_c<128, 2, true, BIAS>(l);
-        case 256: return backward_c<256, 2, true, BIAS>(l);
-        case 384: return backward_c<384, 2, true, BIAS>(l);
-        case 512: return backward_c<512, 2, true, BIAS>(l);
+        case 32: return backward_c<32, 2, true, BIAS, KIND>(l);
+        case 64: return backward_c<64, 2, true, BIAS, KIND>(l);
+        case 128: return backward_c<128, 2, true, BIAS, KIND>(l);
+        case 256: return backward_c<256, 2, true, BIAS, KIND>(l);
+        case 384: return backward_c<384, 2, true, BIAS, KIND>(l);
+        case 512: return backward_c<512, 2, true, BIAS, KIND>(l);
         default: return cudaErrorInvalidValue;
     }
 }
 
-// Rows that are not vectors and take two chunks per thread run the kernel with
-// all four sums (fewer kernels; the two that are not wanted are not added up).
+// The kinds that are compiled in: RMSNorm without biases, LayerNorm with them,
+// each with the same norm behind the block or none.  Rows that are not vectors
+// and take two chunks per thread run the kernel with all four sums (fewer
+// kernels; the two that are not wanted are not added up).
 cudaError_t NORM_CAT(backward_, NORM_SUFFIX)(const Launch& l) {
-    if (!l.p.vec)
-        return l.chunks8 == 2 ? backward_c<0, 2, false, true>(l)
-               : l.bias       ? backward_c<0, 1, false, true>(l)
-                              : backward_c<0, 1, false, false>(l);
-    return l.bias ? backward_v<true>(l) : backward_v<false>(l);
+    const Params& p = l.p;
+    if (!p.vec && l.chunks8 == 2) return backward_c<0, 2, false, true, kAnyKind>(l);
+    if (p.Z && p.dY && p.dXO && p.dX && p.dZ && !p.token_gate) {
+        if (!l.bias && p.pre == kRms && p.post == kRms) return backward_k<false, kRmsRms>(l);
+        if (!l.bias && p.pre == kRms && p.post == kNone) return backward_k<false, kRmsPlain>(l);
+        if (l.bias && p.pre == kLayer && p.post == kLayer) return backward_k<true, kLayerLayer>(l);
+        if (l.bias && p.pre == kLayer && p.post == kNone) return backward_k<true, kLayerPlain>(l);
+    }
+    return l.bias ? backward_k<true, kAnyKind>(l) : backward_k<false, kAnyKind>(l);
 }
 
 }  // namespace nrm
