@@ -40,11 +40,11 @@ static cudaError_t launch_kernel(K kern, const Launch& l, std::mutex& mu, size_t
     return cudaLaunchKernelEx(&cfg, kern, l.p);
 }
 
-template <int TT, int C, bool VEC>
+template <int TT, int C, bool VEC, int KIND>
 static cudaError_t forward_c(const Launch& l) {
     static std::mutex mu;
     static size_t raised_to = 0;
-    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, TT, C, VEC>, l, mu, raised_to);
+    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, KIND>, l, mu, raised_to);
 }
 
 template <int TT, int C, bool VEC, bool BIAS, int KIND>
@@ -57,22 +57,37 @@ static cudaError_t backward_c(const Launch& l) {
 // Threads per row and chunks per thread: one chunk for rows of up to 256
 // columns (a warp each) and for few rows (norm.cu), else two.  Rows of vectors
 // have the threads compiled in; the others share a kernel per C.
-cudaError_t NORM_CAT(forward_, NORM_SUFFIX)(const Launch& l) {
-    if (!l.p.vec) return l.chunks8 == 1 ? forward_c<0, 1, false>(l) : forward_c<0, 2, false>(l);
+template <int KIND>
+static cudaError_t forward_k(const Launch& l) {
+    if (!l.p.vec) return l.chunks8 == 1 ? forward_c<0, 1, false, KIND>(l) : forward_c<0, 2, false, KIND>(l);
     if (l.chunks8 == 1) {
-        return l.p.T == 32    ? forward_c<32, 1, true>(l)
-               : l.p.T == 512 ? forward_c<512, 1, true>(l)
-                              : forward_c<0, 1, true>(l);
+        return l.p.T == 32    ? forward_c<32, 1, true, KIND>(l)
+               : l.p.T == 512 ? forward_c<512, 1, true, KIND>(l)
+                              : forward_c<0, 1, true, KIND>(l);
     }
     switch (l.p.T) {
-        case 32: return forward_c<32, 2, true>(l);
-        case 64: return forward_c<64, 2, true>(l);
-        case 128: return forward_c<128, 2, true>(l);
-        case 256: return forward_c<256, 2, true>(l);
-        case 384: return forward_c<384, 2, true>(l);
-        case 512: return forward_c<512, 2, true>(l);
+        case 32: return forward_c<32, 2, true, KIND>(l);
+        case 64: return forward_c<64, 2, true, KIND>(l);
+        case 128: return forward_c<128, 2, true, KIND>(l);
+        case 256: return forward_c<256, 2, true, KIND>(l);
+        case 384: return forward_c<384, 2, true, KIND>(l);
+        case 512: return forward_c<512, 2, true, KIND>(l);
         default: return cudaErrorInvalidValue;
     }
+}
+
+// The kinds that are compiled in: RMSNorm without biases, LayerNorm with them,
+// each with the same norm behind the block or none.
+cudaError_t NORM_CAT(forward_, NORM_SUFFIX)(const Launch& l) {
+    const Params& p = l.p;
+    if (p.Z && p.Y && !p.token_gate) {
+        const bool bs = p.i_bs >= 0, bpre = p.i_bpre >= 0;
+        if (!bs && !bpre && p.pre == kRms && p.post == kRms) return forward_k<kRmsRms>(l);
+        if (!bs && !bpre && p.pre == kRms && p.post == kNone) return forward_k<kRmsPlain>(l);
+        if (bs && bpre && p.pre == kLayer && p.post == kLayer) return forward_k<kLayerLayer>(l);
+        if (!bs && bpre && p.pre == kLayer && p.post == kNone) return forward_k<kLayerPlain>(l);
+    }
+    return forward_k<kAnyKind>(l);
 }
 
 template <bool BIAS, int KIND>
@@ -90,9 +105,8 @@ static cudaError_t backward_k(const Launch& l) {
     }
 }
 
-// The kinds that are compiled in: RMSNorm without biases, LayerNorm with them,
-// each with the same norm behind the block or none.  Rows that are not vectors
-// and take two chunks per thread run the kernel with all four sums (fewer
+// The same kinds (the biases' gradients standing for the biases).  Rows that
+// are not vectors and take two chunks per thread run the kernel with all four sums (fewer
 // kernels; the two that are not wanted are not added up).
 cudaError_t NORM_CAT(backward_, NORM_SUFFIX)(const Launch& l) {
     const Params& p = l.p;

@@ -37,10 +37,10 @@ namespace nrm {
 
 enum : int { kNone = 0, kRms = 1, kLayer = 2 };
 constexpr int kMaxStages = 3;
-// What the backward kernel has compiled in: the norms on both sides, that every
-// matrix is there and that the gate is not per token (or nothing).  Fewer
+// What a kernel has compiled in: the norms on both sides, that every matrix is
+// there and that the gate is not per token (or nothing of this).  Fewer
 // instructions and longer runs of them without a branch: 8192 x 4096 bf16,
-// RMSNorm on both sides, 84 us not compiled in, 76 compiled in.
+// RMSNorm on both sides, backward, 84 us not compiled in, 76 compiled in.
 enum : int { kAnyKind = 0, kRmsRms = 1, kRmsPlain = 2, kLayerLayer = 3, kLayerPlain = 4 };
 __host__ __device__ constexpr int kind_pre(int kind) { return kind <= kRmsPlain ? kRms : kLayer; }
 __host__ __device__ constexpr int kind_post(int kind) {
@@ -588,9 +588,12 @@ __device__ __forceinline__ float norm_stats(G& g, const Params& p, int kind, int
 }
 
 // One CTA (or a pair, for rows wider than kMaxColumnsPerCta) per chunk of rows,
-// its groups taking the rows in turn.
-template <typename XT, typename ZT, int TT, int C, bool VEC>
-__global__ void __launch_bounds__(1024)
+// its groups taking the rows in turn.  (The bound of one CTA per SM keeps the
+// compiler from spilling the narrowest rows' kernel to 32 registers: 33.5M bf16
+// elements, N = 128, LayerNorm before 73 us without it and 59 with.  The others
+// are left without: N = 5120 FP32, LayerNorm on both sides, 109 without, 150 with.)
+template <typename XT, typename ZT, int TT, int C, bool VEC, int KIND>
+__global__ void __launch_bounds__(1024, TT == 32 && C == 1 ? 1 : 0)
     forward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
     auto g = make_group<Group<TT, kForwardSums>>(p, smem);
@@ -599,7 +602,13 @@ __global__ void __launch_bounds__(1024)
     uint8_t* par = smem + groups * g.warps() * (8 * kForwardSums);
     uint8_t* ring = par_at<C>(par, p.n_par, T) + static_cast<uint32_t>(g.index) * p.stages * p.slot_bytes;
     const uint32_t x_bytes = static_cast<uint32_t>(C) * 8u * sizeof(XT) * T;
-    const bool has_z = p.Z != nullptr;
+    constexpr bool kAll = KIND != kAnyKind;
+    constexpr bool kBiases = kAll && kind_pre(KIND) == kLayer;
+    const bool has_z = kAll || p.Z != nullptr, has_y = kAll || p.Y != nullptr;
+    const bool has_bs = kAll ? kBiases && kind_post(KIND) == kLayer : p.i_bs >= 0;
+    const bool has_bpre = kAll ? kBiases : p.i_bpre >= 0;
+    const bool token_gate = !kAll && p.token_gate;
+    const int pre = kAll ? kind_pre(KIND) : p.pre, post = kAll ? kind_post(KIND) : p.post;
     const int32_t N = p.N;
     __shared__ float pair[4 * kForwardSums];
     int32_t col0 = 0;
@@ -671,7 +680,7 @@ __global__ void __launch_bounds__(1024)
             F8 z[C];
             #pragma unroll
             for (int c = 0; c < C; ++c) take8<ZT>(s + x_bytes, T, t, c, z[c]);
-            const F2 r = mk2(norm_stats<C, VEC>(g, p, p.post, col0, z));
+            const F2 r = mk2(norm_stats<C, VEC>(g, p, post, col0, z));
             #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
@@ -681,12 +690,12 @@ __global__ void __launch_bounds__(1024)
                 take8<float>(par_at<C>(par, p.i_ws, T), T, t, c, w);
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) z[c][q] = mul2(mul2(z[c][q], r), w[q]);
-                if (p.i_bs >= 0) {
+                if (has_bs) {
                     take8<float>(par_at<C>(par, p.i_bs, T), T, t, c, w);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) z[c][q] = add2(z[c][q], w[q]);
                 }
-                if (p.token_gate) {
+                if (token_gate) {
                     load_param8<VEC>(gate_row(p, row), p.vec_dtype, p.vec_aligned != 0, sp, N, w);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) z[c][q] = mul2(z[c][q], mul2(w[q], mk2(p.scale)));
@@ -701,8 +710,8 @@ __global__ void __launch_bounds__(1024)
             #pragma unroll
             for (int c = 0; c < C; ++c) take8<XT>(s, T, t, c, x[c]);
         }
-        if (p.Y != nullptr) {
-            const F2 r = mk2(norm_stats<C, VEC>(g, p, p.pre, col0, x));
+        if (has_y) {
+            const F2 r = mk2(norm_stats<C, VEC>(g, p, pre, col0, x));
             #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const Spot<VEC> sp = spot_of<VEC>(T, t, c, col0);
@@ -711,7 +720,7 @@ __global__ void __launch_bounds__(1024)
                 take8<float>(par_at<C>(par, p.i_wpre, T), T, t, c, w);
                 #pragma unroll
                 for (int q = 0; q < 4; ++q) x[c][q] = mul2(mul2(x[c][q], r), w[q]);
-                if (p.i_bpre >= 0) {
+                if (has_bpre) {
                     take8<float>(par_at<C>(par, p.i_bpre, T), T, t, c, w);
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) x[c][q] = add2(x[c][q], w[q]);
@@ -733,8 +742,11 @@ __global__ void __launch_bounds__(1024)
 // gate is constant over a chunk and joins in the sum over chunks) or, for
 // token gates, q = scale gate dXO'.  The groups' sums meet in shared memory
 // (in group order) and go to the chunk's line of partials.
+// (The bound of one CTA per SM where registers are not short: N = 5120 bf16,
+// RMSNorm on both sides, 96 us without it and 89 with; with the biases' sums
+// 2048 columns 90 and 95, rows that are not vectors 29 and 31 at 2000 x 1023.)
 template <typename XT, typename ZT, int TT, int C, bool VEC, bool BIAS, int KIND>
-__global__ void __launch_bounds__(kBackThreads)
+__global__ void __launch_bounds__(kBackThreads, VEC && !BIAS ? 1 : 0)
     backward_kernel(const __grid_constant__ Params p) {
     extern __shared__ __align__(16) uint8_t smem[];
     auto g = make_group<Group<TT, kBackwardSums>>(p, smem);
