@@ -151,7 +151,8 @@ int choose_cta(Params& p, int sums, int chunks8, int most, int resident, int per
     for (int stages = kMaxStages; stages >= 1; --stages) {
         if (stages == 1 && best > 0) break;
         // (named barriers number the groups of more than a warp: 15 at most)
-        for (int g = 1; g * p.T <= most && (g <= 15 || p.T == 32); g *= 2) {
+        // (a pair of CTAs has one exchange buffer and one barrier: one group)
+        for (int g = 1; g * p.T <= most && (g <= 15 || p.T == 32) && (g == 1 || p.cluster == 1); g *= 2) {
             const int64_t bytes = smem_for(p, sums, chunks8, g, stages);
             if (bytes > kSmemPerCta) continue;
             int64_t n = kSmemPerSm / (bytes + 1024);

@@ -132,6 +132,22 @@ def test_kinds_and_gates(lib, pre, post, rows):
     run_backward(lib, c, biases=False)
 
 
+# every width of a row group, for few rows and for many; the kinds that have
+# kernels of their own, and RMSNorm with biases and LayerNorm without, which do not
+@pytest.mark.parametrize("N", [40, 99, 256, 500, 512, 1016, 1023, 2048, 3000, 4096, 4097, 5120, 8192, 9001, 12288])
+@pytest.mark.parametrize("M", [20, 340])
+def test_kinds_by_width(lib, M, N):
+    kinds = [("rms", "rms", False), ("rms", None, False), ("layer", "layer", True), ("layer", None, True),
+             ("rms", "rms", True), ("layer", "layer", False)]
+    for i, (pre, post, bias) in enumerate(kinds):
+        xt, zt = PAIRS[(i + N + M) % len(PAIRS)]
+        c = make(M, N, xt, zt, pre, post, (0, M, 100)[(i + N) % 3], bias=bias)
+        if post is None:
+            c["bpost"] = None
+        run_forward(lib, c)
+        run_backward(lib, c, biases=bias)
+
+
 def test_many_gate_groups(lib):
     for M, rows in ((2000, 3), (2000, 100), (2000, 150), (5000, 2), (4000, 4), (4100, 4)):
         run_backward(lib, make(M, 264, BF, BF, "rms", "layer", rows))
