@@ -14,12 +14,13 @@
 // vectors that it converts to FP32 in shared memory once.
 //
 // 8192 x 4096 bf16, RMSNorm on both sides, a gate per channel.  Forward: 49 us,
-// 5.4 TB/s; issue slots 64 % and DRAM 60 % busy.  Backward: 84 us and 6 for the
-// sums, 4.5 TB/s; bound by its instructions, 51 per element (16-bit pairs are
-// unpacked again in each of its passes over a row), at the 16 warps per SM that
-// its registers leave: issue slots 54 % busy.  One exchange per row in place of
-// two (the post-norm's sums, from products known before the pre-norm's size)
-// costs more products than it saves: 93 us for 84.
+// 5.4 TB/s; issue slots 57 % and DRAM 61 % busy.  Backward: 72 us and 6 for the
+// sums, 5.2 TB/s; bound by its instructions, 39 per element (16-bit pairs are
+// unpacked again in each of its passes over a row), and the latency of shared
+// memory at the 16 warps per SM that its registers leave: issue slots 47 %
+// busy.  One exchange per row in place of two (the post-norm's sums, from
+// products known before the pre-norm's size) costs more products than it saves:
+// 93 us for 84, both without the kinds compiled in.
 //
 // Rows that are not 16-byte aligned, or N not a multiple of 8, go element by
 // element: a thread's 8 elements are then 32 apart, so a warp's accesses stay
