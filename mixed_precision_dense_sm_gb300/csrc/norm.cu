@@ -281,10 +281,14 @@ gemm_status_t norm_block_forward(int64_t M, int64_t N, const void* X, int64_t ld
     if (Y) p.i_wpre = p.n_par++;
     if (Y && block->pre_bias) p.i_bpre = p.n_par++;
     // 16 elements per thread, which halves what a row costs beside its
-    // elements; 8 where rows are few (one row's latency counts) or narrow
-    // (FP32 rows that are not vectors: 127 us by 16, 102 by 8 at 32800 x 1023)
-    l.chunks8 = N > kMaxColumnsPerCta ? 2
-                : (M <= sms || N <= 256 || (!p.vec && x_dtype == GEMM_F32)) ? 1 : 2;
+    // elements; 8 where rows are few (one row's latency counts) or narrow, and
+    // for rows that are not vectors, whose addresses take registers: FP32 ones
+    // (32800 x 1023, RMSNorm on both sides, 117 us by 16, 93 by 8) and 16-bit
+    // ones but where the post-norm has a mean to take first or rows are long
+    // (8194 x 4095 bf16 100 and 86, LayerNorm on both sides 124 and 140; 4096 x
+    // 8191 108 and 117)
+    const bool loose8 = !p.vec && (x_dtype == GEMM_F32 || (N <= 4096 && !(Z && block->post == kLayer)));
+    l.chunks8 = N > kMaxColumnsPerCta ? 2 : (M <= sms || N <= 256 || loose8) ? 1 : 2;
     p.cluster = N > kMaxColumnsPerCta ? 2 : 1;
     p.T = threads_for(ceil_div(round_up(N, 16 * p.cluster), p.cluster), l.chunks8);
     p.slot_bytes = static_cast<uint32_t>(l.chunks8 * 8 * p.T * (esize(x_dtype) + (Z ? esize(z_dtype) : 0)));
@@ -388,7 +392,7 @@ gemm_status_t norm_block_backward(int64_t M, int64_t N, const void* XO, int64_t 
     l.bias = gr.d_pre_bias || gr.d_post_bias || (!token && gr.d_gate && block->post_bias);
     if (M > 0) {
         // 8192 columns fill a CTA's registers: wider rows take a pair of CTAs
-        // (rows that are not vectors: 16 per thread spill, 285 us against 276 at 32800 x 1023)
+        // (rows that are not vectors: 16 per thread spill, 32800 x 1023 FP32 231 us against 171)
         l.chunks8 = N > (p.vec ? 256 : 4096) ? 2 : 1;
         p.cluster = N > kMaxColumnsPerCta ? 2 : 1;
         p.T = threads_for(ceil_div(round_up(N, 16 * p.cluster), p.cluster), l.chunks8);
