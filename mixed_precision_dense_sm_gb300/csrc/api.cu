@@ -818,6 +818,24 @@ bool glu_p_vector(int64_t F, const glu_forward_t* o, int32_t c_dtype) {
     return aligned16(o->P) && o->ldp * es % 16 == 0 && F * es % 16 == 0;
 }
 
+// A launch that may begin while the kernel before it ends; the kernel waits
+// for that one itself (grid_dependency_wait) before it touches memory.
+template <typename... A>
+cudaError_t launch_early(void (*kern)(A...), dim3 grid, int threads, cudaStream_t stream, const A&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e;
+}
+
 // Everything gemm_run enqueues after planning: the optional pack pre-passes,
 // the TMA descriptors and the GEMM kernel.  `ws` is the workspace laid out as
 // [tile counters (4 KB)][packed A][packed B][partial slots]; with
@@ -880,7 +898,8 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
             const int g = grid_for(o[i]->rows * o[i]->packed_ld / 8, num_sms);
             if (g > grid) grid = g;
         }
-        pack_pair_kernel<<<dim3(grid, 2, 1), 256, 0, stream>>>(pp);
+        if (launch_early(pack_pair_kernel, dim3(grid, 2, 1), 256, stream, pp) != cudaSuccess)
+            return GEMM_ERR_LAUNCH;
         a_ptr = ws_a;
         b_ptr = ws_b;
     } else {
@@ -1876,17 +1895,8 @@ int32_t glu_dot_grid(int64_t F, int num_sms) {
 
 template <typename T>
 cudaError_t launch_glu_dot(const GluDotParams& p, int64_t M, int grid, cudaStream_t stream) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, 1, 1);
-    cfg.blockDim = dim3(kGluDotThreads, 1, 1);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return M == 1 ? cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 1>, p)
-                  : cudaLaunchKernelEx(&cfg, glu_dot_kernel<T, 2>, p);
+    return launch_early(M == 1 ? glu_dot_kernel<T, 1> : glu_dot_kernel<T, 2>, dim3(grid, 1, 1),
+                        kGluDotThreads, stream, p);
 }
 
 gemm_status_t enqueue_glu_dot(int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
@@ -1897,31 +1907,23 @@ gemm_status_t enqueue_glu_dot(int64_t M, int64_t F, int64_t K, const void* X, in
     const int grid = glu_dot_grid(F, num_sms);
     const cudaError_t e = dt.a == GEMM_F16 ? launch_glu_dot<__half>(p, M, grid, stream)
                                            : launch_glu_dot<__nv_bfloat16>(p, M, grid, stream);
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        return GEMM_ERR_LAUNCH;
-    }
-    return GEMM_OK;
+    return e == cudaSuccess ? GEMM_OK : GEMM_ERR_LAUNCH;
 }
 
 template <typename T, typename PT>
-void launch_glu_back(const GluBackParams& p, bool vec, dim3 grid, cudaStream_t stream) {
+cudaError_t launch_glu_back(const GluBackParams& p, bool vec, dim3 grid, cudaStream_t stream) {
     constexpr int kT = 32 * kGluBackWarps;
-    if (p.partials) {
-        if (vec) glu_back_kernel<T, PT, true, true><<<grid, kT, 0, stream>>>(p);
-        else glu_back_kernel<T, PT, false, true><<<grid, kT, 0, stream>>>(p);
-    } else {
-        if (vec) glu_back_kernel<T, PT, true, false><<<grid, kT, 0, stream>>>(p);
-        else glu_back_kernel<T, PT, false, false><<<grid, kT, 0, stream>>>(p);
-    }
+    auto kern = p.partials ? (vec ? glu_back_kernel<T, PT, true, true> : glu_back_kernel<T, PT, false, true>)
+                           : (vec ? glu_back_kernel<T, PT, true, false> : glu_back_kernel<T, PT, false, false>);
+    return launch_early(kern, grid, kT, stream, p);
 }
 
 template <typename T>
-void launch_glu_back_p(const GluBackParams& p, bool vec, int32_t p_dtype, dim3 grid,
-                       cudaStream_t stream) {
-    if (p_dtype == GEMM_F32) launch_glu_back<T, float>(p, vec, grid, stream);
-    else if (p_dtype == GEMM_F16) launch_glu_back<T, __half>(p, vec, grid, stream);
-    else launch_glu_back<T, __nv_bfloat16>(p, vec, grid, stream);
+cudaError_t launch_glu_back_p(const GluBackParams& p, bool vec, int32_t p_dtype, dim3 grid,
+                              cudaStream_t stream) {
+    if (p_dtype == GEMM_F32) return launch_glu_back<T, float>(p, vec, grid, stream);
+    if (p_dtype == GEMM_F16) return launch_glu_back<T, __half>(p, vec, grid, stream);
+    return launch_glu_back<T, __nv_bfloat16>(p, vec, grid, stream);
 }
 
 // One of the backward pass's products on a workspace whose first `used` bytes
@@ -2121,15 +2123,17 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
         const bool vec = F % 8 == 0 && rows_aligned(dH, lddh, 2) && rows_aligned(P, ldp, pe) &&
                          rows_aligned(o->dP, o->lddp, 2);
         const dim3 grid(static_cast<unsigned>(ceil_div(F, 256)), static_cast<unsigned>(slabs), 1);
-        if (dtype == GEMM_F16) launch_glu_back_p<__half>(p, vec, o->p_dtype, grid, stream);
-        else launch_glu_back_p<__nv_bfloat16>(p, vec, o->p_dtype, grid, stream);
-        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+        const cudaError_t e = dtype == GEMM_F16
+                                  ? launch_glu_back_p<__half>(p, vec, o->p_dtype, grid, stream)
+                                  : launch_glu_back_p<__nv_bfloat16>(p, vec, o->p_dtype, grid, stream);
+        if (e != cudaSuccess) return GEMM_ERR_LAUNCH;
     }
     if (o->dbias && F > 0) {
         const int64_t cols = 2 * F;
-        glu_dbias_kernel<<<static_cast<unsigned>(ceil_div(cols, 32)), 1024, 0, stream>>>(
-            partials, static_cast<int32_t>(slabs), cols, o->dbias, o->dbias_dtype);
-        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+        if (launch_early(glu_dbias_kernel, dim3(static_cast<unsigned>(ceil_div(cols, 32)), 1, 1), 1024,
+                         stream, static_cast<const float*>(partials), static_cast<int32_t>(slabs), cols,
+                         o->dbias, o->dbias_dtype) != cudaSuccess)
+            return GEMM_ERR_LAUNCH;
     }
     if (copy_w || copy_x) {
         PackPair pp;
@@ -2143,8 +2147,8 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
         };
         if (copy_w) add(W, ldw, 2 * F, at_w);
         if (copy_x) add(X, ldx, M, at_x);
-        pack_pair_kernel<<<dim3(grid, n, 1), 256, 0, stream>>>(pp);
-        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+        if (launch_early(pack_pair_kernel, dim3(grid, n, 1), 256, stream, pp) != cudaSuccess)
+            return GEMM_ERR_LAUNCH;
     }
     if (dx_some) {
         st = enqueue_product(h, gx, px, used, stream);
@@ -2168,8 +2172,9 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
         int64_t grid = ceil_div(units, 8);
         const int64_t cap = static_cast<int64_t>(h->num_sms) * 8;
         if (grid > cap) grid = cap;
-        unpack_pair_kernel<<<dim3(static_cast<unsigned>(grid), n, 1), 256, 0, stream>>>(up);
-        if (cudaGetLastError() != cudaSuccess) return GEMM_ERR_LAUNCH;
+        if (launch_early(unpack_pair_kernel, dim3(static_cast<unsigned>(grid), n, 1), 256, stream, up) !=
+            cudaSuccess)
+            return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
 }

@@ -20,6 +20,7 @@
 #include <cuda_fp16.h>
 
 #include "epilogue_ops.cuh"
+#include "ptx.cuh"
 
 namespace gemm103 {
 
@@ -61,6 +62,8 @@ struct PackPair {
 static __global__ void __launch_bounds__(256)
     pack_pair_kernel(const __grid_constant__ PackPair p) {
     const PackDesc& d = p.d[blockIdx.y];
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int64_t vec_per_row = d.dst_ld / 8;
     const int64_t total = d.rows * vec_per_row;
     for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
@@ -93,6 +96,8 @@ struct UnpackPair {
 static __global__ void __launch_bounds__(256)
     unpack_pair_kernel(const __grid_constant__ UnpackPair p) {
     const UnpackDesc& d = p.d[blockIdx.y];
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int lane = threadIdx.x & 31;
     const int64_t warps = static_cast<int64_t>(gridDim.x) * 8;
     const int64_t segs = (d.cols + 255) / 256, units = d.rows * segs;

@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(32 * kGluBackWarps, VEC ? 4 : 2)
     int64_t row1 = row0 + p.slab_rows;
     if (row1 > p.M) row1 = p.M;
     grid_dependency_wait();
+    grid_dependents_launch();
     float sg[SUMS ? 8 : 1], su[SUMS ? 8 : 1];
     if constexpr (SUMS) {
         #pragma unroll
@@ -218,6 +219,7 @@ static __global__ void __launch_bounds__(1024)
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + tx;
     grid_dependency_wait();
+    grid_dependents_launch();
     float t = 0.0f;
     if (c < cols) {
         #pragma unroll 4

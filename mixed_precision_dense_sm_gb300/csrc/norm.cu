@@ -142,7 +142,7 @@ int64_t smem_for(const Params& p, int sums, int chunks8, int groups, int stages)
 // Groups per CTA and slots per group: the most rows worked on per SM among
 // CTAs of up to `most` threads, all resident within `resident` threads, that
 // have a second slot per group; of those the deepest rings, then the largest
-// CTA (many small ones leave the driver's default split of an SM's memory with
+// CTA (many small ones leave the default split of an SM's memory with
 // room for few: 5 of 32 one-warp CTAs).  One slot only where two fit nowhere.  Returns CTAs per SM (at most
 // `per_sm`), 0 where nothing fits.
 int choose_cta(Params& p, int sums, int chunks8, int most, int resident, int per_sm, int& groups) {
