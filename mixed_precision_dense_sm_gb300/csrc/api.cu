@@ -353,7 +353,10 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     // lines.  The K chunks per stage are chosen with the staging set aside;
     // without it the stages are counted again (shared memory the kernel does
     // not use is left to the L1 cache).
-    const bool c_stage_ok = pl.pub.c_vector && !ln && !use_mh2;
+    // A TMA store clips its box by 16-byte pieces, not by elements: it takes only
+    // rows of whole pieces, or it would write zeros into the padding behind them.
+    const bool c_pieces = (glu ? N / 2 : N) * static_cast<int64_t>(out_elem_bytes(dt.c)) % 16 == 0;
+    const bool c_stage_ok = pl.pub.c_vector && c_pieces && !ln && !use_mh2;
     const int64_t avail_all = smem_optin - 1024 - barrier_bytes - static_bytes;
     // (the gated layer exchanges its halves where swapped, and turns rows that
     // are not aligned, through the same area)

@@ -210,3 +210,22 @@ def test_new_tensors_on_another_stream():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     g.close()
+
+
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16, torch.float16], ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("N", [1, 25, 1001, 1002, 1003, 2388, 2389])
+def test_padding_behind_rows_of_odd_bytes(N, dt):
+    """The columns between N and an aligned pitch stay as they were, and what
+    lies behind a last row without padding, for the GEMM and the gated layer."""
+    import mixed_precision_dense_sm_gb300 as lib
+    g = lib.Gemm()
+    ld = -(-N // 8) * 8
+    for M, K in ((704, 3626), (5000, 2048), (20000, 64)):
+        A = torch.randn(M, K, device="cuda").to(torch.bfloat16)
+        W = torch.randn(2 * N, K, device="cuda").to(torch.bfloat16)
+        for f in (lambda C: g(A, W[:N], C, transB="T"), lambda C: g.glu(A, W, C)):
+            buf = torch.full((M * ld + 16,), 321.0, dtype=dt, device="cuda")
+            f(buf[:M * ld].view(M, ld)[:, :N])
+            g.sync()
+            assert (buf[:M * ld].view(M, ld)[:, N:] == 321).all() and (buf[M * ld:] == 321).all(), (M, K)
+    g.close()

@@ -173,3 +173,19 @@ def test_row_pitch_of_a_view(shape, stride, ld):
     assert lib._mat(t, "t", *shape, torch.float32, -1) == (t.data_ptr(), ld)
     if ld < max(shape[1], 1):
         assert plan(M=shape[0], K=shape[1], ldx=ld or -1)[0] == 1
+
+
+@pytest.mark.parametrize("c,es", [(lib.GEMM_F32, 4), (BF16, 2), (lib.GEMM_F16, 2)])
+def test_tma_stores_need_rows_of_whole_pieces(c, es):
+    """A TMA store clips by 16 bytes: only rows of whole 16-byte pieces take it,
+    whatever the pitch (of C, and of the gated layer's H)."""
+    seen = set()
+    for N in range(2384, 2401):
+        want = int(N * es % 16 == 0)
+        st, p = lib.gemm_plan_query("N", "T", 20000, N, 2048, 1.0, 256, 2048, 256, 2048, 0.0, 256, 2400,
+                                    (BF16, BF16, c))
+        assert st == 0 and p["c_tma"] == want, (N, p)
+        st, p = plan(M=20000, F=N, K=2048, ldh=2400, dt=(BF16, BF16, c))
+        assert st == 0 and p["c_tma"] == want, (N, p)
+        seen.add(want)
+    assert seen == {0, 1}
