@@ -344,7 +344,9 @@ __device__ __forceinline__ float load_bias(const TcParams& p, int64_t idx) {
 }
 
 // Elements c0..c0+31 of a per-column vector (bias, gamma, shift) of type
-// 0 = F16, 1 = BF16, 2 = F32; zeros past column N.
+// 0 = F16, 1 = BF16, 2 = F32; zeros past column N.  (Plain loads here and in the
+// other kernels that begin early: the read-only path is for memory that nothing
+// writes while the kernel lives, and the one before it still may.)
 __device__ __forceinline__ void load_col_vec32(const void* vec, int32_t dtype, int32_t c0,
                                                int32_t N, float (&b)[32]) {
     const int esize = dtype == 2 ? 4 : 2;
@@ -356,7 +358,7 @@ __device__ __forceinline__ void load_col_vec32(const void* vec, int32_t dtype, i
         if (dtype == 2) {
             #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const uint4 t = __ldg(src + q);
+                const uint4 t = src[q];
                 b[4 * q] = __uint_as_float(t.x);
                 b[4 * q + 1] = __uint_as_float(t.y);
                 b[4 * q + 2] = __uint_as_float(t.z);
@@ -365,7 +367,7 @@ __device__ __forceinline__ void load_col_vec32(const void* vec, int32_t dtype, i
         } else {
             #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 t = __ldg(src + q);
+                const uint4 t = src[q];
                 const uint32_t w[4] = {t.x, t.y, t.z, t.w};
                 #pragma unroll
                 for (int e = 0; e < 4; ++e) {

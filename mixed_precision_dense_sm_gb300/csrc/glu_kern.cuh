@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(32 * kGluBackWarps, VEC ? 4 : 2)
 // dbias = sum over the slabs: 32 columns per CTA, 32 lines of threads that
 // take the slabs in turn and are added in line order.
 static __global__ void __launch_bounds__(1024)
-    glu_dbias_kernel(const float* __restrict__ partials, int32_t slabs, int64_t cols, void* dbias,
+    glu_dbias_kernel(const float* partials, int32_t slabs, int64_t cols, void* dbias,
                      int32_t dtype) {
     __shared__ float red[32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -256,7 +256,8 @@ constexpr int kGluDotAhead = 4;         // 256-element pieces of both rows in fl
 // Against the tensor-core path there is no tile to fill, no pipeline to start
 // and no split of K to join: what a problem of a few microseconds spends its
 // time on.  FP32 sums in pairs, joined over the lanes by a butterfly.
-// K is a multiple of 8; rows of X and W are 16-byte aligned.
+// K is a multiple of 8; rows of X and W are 16-byte aligned.  X is read by plain
+// loads: the kernel before this one, still running when this one begins, writes it.
 // One token, 1024 -> 4096, bf16: 6.4 us with the launch, 2.5 us of which are W's 17 MB.
 template <typename T, int MT>
 __global__ void __launch_bounds__(kGluDotThreads, kGluDotCtas)
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kGluDotThreads, kGluDotCtas)
                 const uint32_t uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
                 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    const uint4 x = __ldg(reinterpret_cast<const uint4*>(X + m * p.ldx + k));
+                    const uint4 x = *reinterpret_cast<const uint4*>(X + m * p.ldx + k);
                     const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
                     #pragma unroll
                     for (int q = 0; q < 4; ++q) {

@@ -137,9 +137,9 @@ __device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool w
     if (VEC && wide) {
         if (dtype == 2) {
             const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(v) + s.base);
-            set8(o, __ldg(p), __ldg(p + 1));
+            set8(o, p[0], p[1]);
         } else {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(v) + s.base));
+            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(v) + s.base);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
             #pragma unroll
             for (int q = 0; q < 4; ++q)
@@ -151,12 +151,12 @@ __device__ __forceinline__ void load_param8(const void* v, int32_t dtype, bool w
     if (dtype == 2) {
         #pragma unroll
         for (int e = 0; e < 8; ++e)
-            f[e] = s.in(e, N) ? __ldg(static_cast<const float*>(v) + s.at(e)) : 0.0f;
+            f[e] = s.in(e, N) ? static_cast<const float*>(v)[s.at(e)] : 0.0f;
     } else {
         uint16_t u[8];
         #pragma unroll
         for (int e = 0; e < 8; ++e)
-            u[e] = s.in(e, N) ? __ldg(static_cast<const uint16_t*>(v) + s.at(e)) : static_cast<uint16_t>(0);
+            u[e] = s.in(e, N) ? static_cast<const uint16_t*>(v)[s.at(e)] : static_cast<uint16_t>(0);
         #pragma unroll
         for (int e = 0; e < 8; ++e)
             f[e] = dtype == 1 ? __bfloat162float(__ushort_as_bfloat16(u[e])) : __half2float(__ushort_as_half(u[e]));
