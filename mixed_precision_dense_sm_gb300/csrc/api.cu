@@ -25,6 +25,7 @@
 #include "aux_kernels.cuh"
 #include "glu_kern.cuh"
 #include "launch.h"
+#include "workspace.h"
 
 using namespace gemm103;
 
@@ -499,10 +500,7 @@ struct gemm_ctx {
     int smem_optin;
     int* err_host;        // mapped pinned error word (host view)
     int* err_dev;         // device view of the same word
-    void* ws;             // device workspace
-    size_t ws_bytes;
-    bool ws_captured;     // a captured graph may hold ws's address
-    struct Retired { void* p; Retired* next; }* retired;   // outgrown, still in such a graph
+    Workspace ws{kWsHeaderBytes};
     EncodeTiledFn encode;
     EncodeIm2colFn encode_im2col;
 };
@@ -692,77 +690,18 @@ bool encode_glu_store(EncodeTiledFn encode, CUtensorMap* map, int32_t dtype, voi
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A buffer of `want` bytes whose tile counters are zero, made while `capturing`
-// is under way on the calling thread: allocated in relaxed mode, as the graph
-// does not hold the allocation, and cleared on a stream of its own.
-void* workspace_buffer(size_t want, bool capturing) {
-    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-    if (capturing && cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) {
-        cudaGetLastError();
-        return nullptr;
-    }
-    void* p = nullptr;
-    cudaError_t e = cudaMalloc(&p, want);
-    if (e != cudaSuccess) {
-        p = nullptr;
-    } else if (!capturing) {
-        e = cudaMemset(p, 0, kWsHeaderBytes);
-    } else {
-        cudaStream_t s;
-        e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
-        if (e == cudaSuccess) {
-            e = cudaMemsetAsync(p, 0, kWsHeaderBytes, s);
-            if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-            cudaStreamDestroy(s);
-        }
-    }
-    if (e != cudaSuccess) {
-        cudaGetLastError();
-        if (p) cudaFree(p);
-        p = nullptr;
-    }
-    if (capturing) cudaThreadExchangeStreamCaptureMode(&mode);
-    return p;
-}
-
-// The handle's workspace of at least `bytes`.  A buffer that a captured graph
-// may still address, and any buffer outgrown under capture, where nothing can
-// wait for its users, is kept until gemm_destroy.  The stream-K tile counters
-// start at zero; every call leaves them at zero again.
 gemm_status_t ensure_workspace(gemm_ctx* h, size_t bytes, cudaStream_t stream) {
-    if (bytes == 0) return GEMM_OK;
-    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(stream, &cap) != cudaSuccess) cudaGetLastError();
-    const bool capturing = cap != cudaStreamCaptureStatusNone;
-    if (bytes <= h->ws_bytes) {
-        h->ws_captured = h->ws_captured || capturing;
-        return GEMM_OK;
-    }
-    if (h->ws && (h->ws_captured || capturing)) {
-        gemm_ctx::Retired* r = new (std::nothrow) gemm_ctx::Retired;
-        if (r == nullptr) return GEMM_ERR_ALLOC;
-        r->p = h->ws;
-        r->next = h->retired;
-        h->retired = r;
-    } else if (h->ws) {
-        cudaFree(h->ws);          // implicit device synchronisation: no user of the old buffer remains
-    }
-    h->ws_bytes = 0;
-    h->ws_captured = capturing;
-    const size_t want = bytes + (bytes >> 2);
-    h->ws = workspace_buffer(want, capturing);
-    if (h->ws == nullptr) return GEMM_ERR_ALLOC;
-    h->ws_bytes = want;
-    return GEMM_OK;
+    return h->ws.reserve(bytes, stream) ? GEMM_OK : GEMM_ERR_ALLOC;
 }
 
 gemm_status_t take_device_error(gemm_ctx* h) {
     volatile int* e = h->err_host;
     if (*e != 0) {
         // A kernel that gave up may have left stream-K tile counters
-        // half-counted: clear them before the handle is used again.
+        // half-counted: clear them before the handle is used again, or one of
+        // its graphs replayed.
         cudaDeviceSynchronize();
-        if (h->ws) cudaMemset(h->ws, 0, kWsHeaderBytes);
+        h->ws.clear_counters();
         cudaGetLastError();
         *e = 0;
         return GEMM_ERR_DEVICE_TIMEOUT;
@@ -1405,13 +1344,7 @@ gemm_status_t gemm_debug_set(gemm_handle_t h, uint32_t flags, uint64_t wait_limi
 gemm_status_t gemm_destroy(gemm_handle_t h) {
     if (h == nullptr) return GEMM_OK;
     cudaDeviceSynchronize();
-    if (h->ws) cudaFree(h->ws);
-    while (h->retired) {
-        gemm_ctx::Retired* r = h->retired;
-        h->retired = r->next;
-        cudaFree(r->p);
-        delete r;
-    }
+    h->ws.release();
     if (h->err_host) cudaFreeHost(h->err_host);
     delete h;
     cudaGetLastError();
@@ -1449,7 +1382,7 @@ gemm_status_t gemm_run_ex(gemm_handle_t h, char transA, char transB, int64_t M, 
         return enqueue_scale(M, N, C, ldc, beta, dt, h->num_sms, stream, ep);
     st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
-    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, alpha,
+    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws.data()), h->err_dev, alpha,
                         beta, C, dt, stream, false, h->debug_flags, h->wait_limit_ns, ep);
 }
 
@@ -1501,7 +1434,7 @@ gemm_status_t gemm_run_layernorm(gemm_handle_t h, char transA, char transB, int6
     }
     st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
-    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, alpha,
+    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws.data()), h->err_dev, alpha,
                         beta, C, dt, stream, false, h->debug_flags, h->wait_limit_ns, nullptr,
                         nullptr, ln);
 }
@@ -1705,7 +1638,7 @@ gemm_status_t conv2d_fprop(gemm_handle_t h, int64_t N, int64_t H, int64_t W, int
         return enqueue_scale(cd.N * cd.P * cd.Q, K, Y, K, beta, dt, h->num_sms, stream, ep);
     st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
-    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, alpha,
+    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws.data()), h->err_dev, alpha,
                         beta, Y, dt, stream, false, h->debug_flags, h->wait_limit_ns, ep, &cd);
 }
 
@@ -1961,7 +1894,7 @@ gemm_status_t enqueue_product(gemm_ctx* h, const Product& g, const Plan& pl, int
     if (pl.pub.path == GEMM_PATH_NOOP) return GEMM_OK;
     if (pl.pub.path == GEMM_PATH_SCALE)
         return enqueue_scale(g.M, g.N, g.C, g.ldc, g.beta, g.dt, h->num_sms, stream);
-    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, 1.0f, g.beta,
+    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws.data()), h->err_dev, 1.0f, g.beta,
                         g.C, g.dt, stream, false, h->debug_flags, h->wait_limit_ns, nullptr, nullptr,
                         nullptr, nullptr, used);
 }
@@ -2009,7 +1942,7 @@ gemm_status_t glu_forward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, cons
     st = ensure_workspace(h, static_cast<size_t>(pl.pub.workspace_bytes), stream);
     if (st != GEMM_OK) return st;
     const GluDesc glu{M, F, ldh, opt};
-    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws), h->err_dev, 1.0f, 0.0f,
+    return enqueue_plan(pl, h->encode, h->num_sms, static_cast<uint8_t*>(h->ws.data()), h->err_dev, 1.0f, 0.0f,
                         H, dt, stream, false, h->debug_flags, h->wait_limit_ns, nullptr, nullptr,
                         nullptr, &glu);
 }
@@ -2097,7 +2030,7 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
         st = ensure_workspace(h, static_cast<size_t>(kWsHeaderBytes + used + own), stream);
         if (st != GEMM_OK) return st;
     }
-    uint8_t* body = static_cast<uint8_t*>(h->ws) + kWsHeaderBytes;
+    uint8_t* body = static_cast<uint8_t*>(h->ws.data()) + kWsHeaderBytes;
     float* partials = some && o->dbias ? reinterpret_cast<float*>(body + at_sums) : nullptr;
     if (copy_p) gx.A = gw.A = body + at_p;
     if (copy_w) gx.B = body + at_w;
