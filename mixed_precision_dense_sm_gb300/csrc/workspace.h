@@ -27,6 +27,7 @@ public:
             captured_ = captured_ || capturing;
             return true;
         }
+        const Relaxed relaxed;
         if (p_ != nullptr && (captured_ || capturing)) {
             Retired* r = new (std::nothrow) Retired;
             if (r == nullptr) return false;
@@ -39,7 +40,7 @@ public:
         bytes_ = 0;
         captured_ = capturing;
         const size_t some = bytes + (bytes >> 2), want = some > header_ ? some : header_;
-        p_ = make(want, capturing);
+        p_ = make(want);
         if (p_ == nullptr) return false;
         bytes_ = want;
         return true;
@@ -49,10 +50,9 @@ public:
     // runs on them: a kernel that gave up may have left them half-counted, in the
     // buffer that its graph was captured with.
     bool clear_counters() {
-        bool ok = p_ == nullptr || cudaMemset(p_, 0, header_) == cudaSuccess;
-        for (Retired* r = retired_; r != nullptr; r = r->next)
-            ok = cudaMemset(r->p, 0, header_) == cudaSuccess && ok;
-        if (!ok) cudaGetLastError();
+        const Relaxed relaxed;
+        bool ok = p_ == nullptr || zero(p_);
+        for (Retired* r = retired_; r != nullptr; r = r->next) ok = zero(r->p) && ok;
         return ok;
     }
 
@@ -74,37 +74,39 @@ private:
         Retired* next;
     };
 
-    // A buffer of `want` bytes whose counters are zero, also while the calling
-    // thread captures: allocated in relaxed mode, as the graph does not hold the
-    // allocation, and cleared on a stream of its own.
-    void* make(size_t want, bool capturing) const {
+    // Calls that a capture under way, this thread's or another's, would forbid:
+    // the graph does not hold what they do.
+    struct Relaxed {
         cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-        if (capturing && cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) {
+        Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+        ~Relaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    };
+
+    // The counters at p as zero before it returns: on a stream of its own (cudaMemset
+    // would return early, on the legacy stream, which non-blocking streams do not
+    // wait for).
+    bool zero(void* p) const {
+        cudaStream_t s;
+        cudaError_t e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
+        if (e == cudaSuccess) {
+            e = cudaMemsetAsync(p, 0, header_, s);
+            if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+            cudaStreamDestroy(s);
+        }
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess;
+    }
+
+    // A buffer of `want` bytes whose counters are zero.
+    void* make(size_t want) const {
+        void* p = nullptr;
+        if (cudaMalloc(&p, want) != cudaSuccess) {
             cudaGetLastError();
             return nullptr;
         }
-        void* p = nullptr;
-        cudaError_t e = cudaMalloc(&p, want);
-        if (e != cudaSuccess) {
-            p = nullptr;
-        } else if (!capturing) {
-            e = cudaMemset(p, 0, header_);
-        } else {
-            cudaStream_t s;
-            e = cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking);
-            if (e == cudaSuccess) {
-                e = cudaMemsetAsync(p, 0, header_, s);
-                if (e == cudaSuccess) e = cudaStreamSynchronize(s);
-                cudaStreamDestroy(s);
-            }
-        }
-        if (e != cudaSuccess) {
-            cudaGetLastError();
-            if (p != nullptr) cudaFree(p);
-            p = nullptr;
-        }
-        if (capturing) cudaThreadExchangeStreamCaptureMode(&mode);
-        return p;
+        if (zero(p)) return p;
+        cudaFree(p);
+        return nullptr;
     }
 
     size_t header_;
