@@ -50,7 +50,8 @@
  * Errors: every entry point returns a gemm_status_t and never aborts.  Device
  * kernels never trap: every wait inside them is bounded, and a wait that runs
  * out records GEMM_ERR_DEVICE_TIMEOUT in the handle's error word, which the
- * next gemm_run or gemm_sync on that handle reports (and clears).
+ * next gemm_run or gemm_sync on that handle reports and clears (while a stream
+ * of the device is captured, which nothing can wait beside, it only reports it).
  */
 #ifndef GEMM_SM103_H_
 #define GEMM_SM103_H_

@@ -699,11 +699,8 @@ gemm_status_t take_device_error(gemm_ctx* h) {
     if (*e != 0) {
         // A kernel that gave up may have left stream-K tile counters
         // half-counted: clear them before the handle is used again, or one of
-        // its graphs replayed.
-        cudaDeviceSynchronize();
-        h->ws.clear_counters();
-        cudaGetLastError();
-        *e = 0;
+        // its graphs replayed.  Until that is done, every call says so.
+        if (h->ws.recover()) *e = 0;
         return GEMM_ERR_DEVICE_TIMEOUT;
     }
     return GEMM_OK;

@@ -46,6 +46,16 @@ public:
         return true;
     }
 
+    // After a kernel gave up: waits for the device and clears the counters.  False
+    // where it cannot, as while a stream is captured: to be tried again.
+    bool recover() {
+        if (cudaDeviceSynchronize() != cudaSuccess) {
+            cudaGetLastError();
+            return false;
+        }
+        return clear_counters();
+    }
+
     // Zeroes the counters of every buffer, the outgrown ones too, once nothing
     // runs on them: a kernel that gave up may have left them half-counted, in the
     // buffer that its graph was captured with.
