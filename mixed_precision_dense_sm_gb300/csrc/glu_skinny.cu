@@ -1,6 +1,5 @@
 // glu_skinny.cu -- instances of the weight-streaming gated layer.
-#include <mutex>
-
+#include "device_limits.h"
 #include "launch.h"
 
 namespace gemm103 {
@@ -8,21 +7,16 @@ namespace gemm103 {
 template <int BN, int KC>
 static cudaError_t launch(const GluSkinnyLaunch& l) {
     auto kern = glu_skinny_kernel<BN, KC>;
-    {
-        static std::mutex mu;
-        static bool raised = false;
-        std::lock_guard<std::mutex> g(mu);
-        if (!raised) {
-            // room for two CTAs per SM
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                                 cudaSharedmemCarveoutMaxShared);
-            if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Skinny<BN, KC>::kSmem));
-            if (e != cudaSuccess) return e;
-            raised = true;
-        }
-    }
+    static DeviceLimits limit;
+    const cudaError_t set = limit.raise(Skinny<BN, KC>::kSmem, [&] {
+        // room for two CTAs per SM
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                   cudaSharedmemCarveoutMaxShared);
+        return e != cudaSuccess ? e
+                                : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(Skinny<BN, KC>::kSmem));
+    });
+    if (set != cudaSuccess) return set;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -11,6 +11,7 @@
 #pragma once
 #include <mutex>
 
+#include "device_limits.h"
 #include "launch.h"
 
 #define GEMM103_CAT2(a, b) a##b
@@ -28,19 +29,12 @@ template <int CG, int BN, int EPI = kEpiPlain, int KC = 1, int MH = 1>
 static cudaError_t launch_tc_cfg(const TcLaunch& l) {
     auto kern = gemm_tc_kernel<CG, BN, KERN_OUT_T, KERN_ES, EPI, KC, MH>;
     const auto& params = params_of<EPI>(l);
-    {
-        // The dynamic shared-memory limit is raised once per size (a host
-        // call worth avoiding on every launch of a microsecond-scale GEMM).
-        static std::mutex mu;
-        static size_t raised_to = 0;
-        std::lock_guard<std::mutex> g(mu);
-        if (l.smem_bytes > raised_to) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(l.smem_bytes));
-            if (e != cudaSuccess) return e;
-            raised_to = l.smem_bytes;
-        }
-    }
+    static DeviceLimits limit;
+    const cudaError_t set = limit.raise(l.smem_bytes, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(l.smem_bytes));
+    });
+    if (set != cudaSuccess) return set;
     // Programmatic stream serialisation: the kernel's set-up may overlap the
     // tail of the previous kernel on the stream (the kernel waits for it with
     // griddepcontrol.wait before touching global memory).
@@ -66,13 +60,19 @@ static cudaError_t launch_tc_cfg(const TcLaunch& l) {
         if (!l.p.stream_k) {
             // A data-parallel schedule adapts to the grid: launch no more
             // pairs than can be resident at once (persistent CTAs).
+            struct Resident {
+                size_t smem;
+                int clusters;
+            };
             static std::mutex mu;
-            static size_t cached_smem = 0;
-            static int cached_clusters = 0;
+            static PerDevice<Resident> table;
             int clusters = 0;
             {
                 std::lock_guard<std::mutex> g(mu);
-                if (cached_smem != l.smem_bytes) {
+                Resident none{0, 0};
+                Resident* known = table.current();
+                if (known == nullptr) known = &none;
+                if (known->smem != l.smem_bytes) {
                     // the query takes the cluster shape alone
                     cudaLaunchConfig_t q = cfg;
                     q.gridDim = dim3(grid, 1, 1);
@@ -82,10 +82,9 @@ static cudaError_t launch_tc_cfg(const TcLaunch& l) {
                         cudaGetLastError();
                         clusters = 0;
                     }
-                    cached_smem = l.smem_bytes;
-                    cached_clusters = clusters;
+                    *known = Resident{l.smem_bytes, clusters};
                 }
-                clusters = cached_clusters;
+                clusters = known->clusters;
             }
             if (clusters > 0 && grid > 2 * clusters) grid = 2 * clusters;
         }

@@ -1,8 +1,7 @@
 // norm_inst.cuh -- instantiates the norm kernels for one pair of types
 // (NORM_XT, NORM_ZT) behind plain launchers.
 #pragma once
-#include <mutex>
-
+#include "device_limits.h"
 #include "norm_launch.h"
 
 #define NORM_CAT2(a, b) a##b
@@ -12,17 +11,12 @@ namespace gemm103 {
 namespace nrm {
 
 template <typename K>
-static cudaError_t launch_kernel(K kern, const Launch& l, std::mutex& mu, size_t& raised_to) {
-    {
-        // raised once per size: a host call worth avoiding on every launch
-        std::lock_guard<std::mutex> g(mu);
-        if (l.smem > raised_to) {
-            const cudaError_t e = cudaFuncSetAttribute(
-                kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l.smem));
-            if (e != cudaSuccess) return e;
-            raised_to = l.smem;
-        }
-    }
+static cudaError_t launch_kernel(K kern, const Launch& l, DeviceLimits& limit) {
+    const cudaError_t e = limit.raise(l.smem, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(l.smem));
+    });
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -42,16 +36,14 @@ static cudaError_t launch_kernel(K kern, const Launch& l, std::mutex& mu, size_t
 
 template <int TT, int C, bool VEC, int KIND>
 static cudaError_t forward_c(const Launch& l) {
-    static std::mutex mu;
-    static size_t raised_to = 0;
-    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, KIND>, l, mu, raised_to);
+    static DeviceLimits limit;
+    return launch_kernel(forward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, KIND>, l, limit);
 }
 
 template <int TT, int C, bool VEC, bool BIAS, int KIND>
 static cudaError_t backward_c(const Launch& l) {
-    static std::mutex mu;
-    static size_t raised_to = 0;
-    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, BIAS, KIND>, l, mu, raised_to);
+    static DeviceLimits limit;
+    return launch_kernel(backward_kernel<NORM_XT, NORM_ZT, TT, C, VEC, BIAS, KIND>, l, limit);
 }
 
 // Threads per row and chunks per thread: one chunk for rows of up to 256

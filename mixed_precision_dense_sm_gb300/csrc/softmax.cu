@@ -234,10 +234,10 @@ struct DeviceInfo {
 
 bool device_info(DeviceInfo& out) {
     static std::mutex mu;
-    static DeviceInfo cache[64];
-    static bool known[64] = {};
+    static DeviceInfo cache[gemm103::kMaxDevices];
+    static bool known[gemm103::kMaxDevices] = {};
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= gemm103::kMaxDevices) {
         cudaGetLastError();
         return false;
     }
@@ -290,9 +290,9 @@ uint64_t g_wait_limit_ns = 0;
 
 int* error_word(int dev) {
     static std::mutex mu;
-    static int* addr[64] = {};
+    static int* addr[gemm103::kMaxDevices] = {};
     std::lock_guard<std::mutex> g(mu);
-    if (dev < 0 || dev >= 64) return nullptr;
+    if (dev < 0 || dev >= gemm103::kMaxDevices) return nullptr;
     if (addr[dev] == nullptr) {
         void* p = nullptr;
         if (cudaGetSymbolAddress(&p, g_softmax_error) != cudaSuccess) {

@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "device_limits.h"
 #include "ptx.cuh"
 
 namespace smx {
@@ -330,11 +331,17 @@ cudaError_t launch_softmax(const SoftmaxParams& p, bool warp_rows, int threads, 
 // group, or clusters on the whole GPU (cached per shape).
 template <typename InT, typename OutT>
 int resident_groups(bool warp_rows, int threads, int cluster, int num_sms) {
+    struct Groups {
+        int n[2][2][kMaxCluster + 1];
+    };
     static std::mutex mu;
-    static int cache[2][2][kMaxCluster + 1] = {};
+    static gemm103::PerDevice<Groups> table;
     const int ti = threads > 256 ? 1 : 0;
     std::lock_guard<std::mutex> g(mu);
-    int& c = cache[warp_rows ? 1 : 0][ti][cluster];
+    Groups none = {};
+    Groups* known = table.current();
+    if (known == nullptr) known = &none;
+    int& c = known->n[warp_rows ? 1 : 0][ti][cluster];
     if (c > 0) return c;
     int n = 0;
     if (cluster <= 1) {

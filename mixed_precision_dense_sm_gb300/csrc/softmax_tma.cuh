@@ -795,20 +795,24 @@ cudaError_t launch_softmax_long(const TmaSoftmaxParams& p, int grid, size_t smem
     if (cl < 1 || cl > kMaxLongCluster || grid % cl != 0) return cudaErrorInvalidValue;
     int clusters_max = 0;                 // clusters of `cl` CTAs resident at once (cl > 1)
     {
+        static gemm103::DeviceLimits limit;
+        const cudaError_t set = limit.raise(smem, [&] {
+            const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                       static_cast<int>(smem));
+            return e != cudaSuccess
+                       ? e
+                       : cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        });
+        if (set != cudaSuccess) return set;
+        struct Resident {
+            int n[kMaxLongCluster + 1];
+        };
         static std::mutex mu;
-        static bool raised = false;
-        static int resident[kMaxLongCluster + 1] = {};
+        static gemm103::PerDevice<Resident> table;
         std::lock_guard<std::mutex> g(mu);
-        if (!raised) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-            if (cl > 1) {
-                e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-                if (e != cudaSuccess) return e;
-            }
-            raised = true;
-        }
+        Resident none = {};
+        Resident* known = table.current();
+        int* resident = known != nullptr ? known->n : none.n;
         if (cl > 1 && resident[cl] == 0) {
             cudaLaunchConfig_t q = {};
             cudaLaunchAttribute qa[1];
@@ -856,17 +860,11 @@ template <typename InT, typename OutT, int KV, bool WHOLE>
 cudaError_t launch_softmax_tma_kv(const TmaSoftmaxParams& p, int grid, size_t smem,
                                   cudaStream_t stream) {
     auto kern = softmax_tma_kernel<InT, OutT, KV, WHOLE>;
-    {
-        static std::mutex mu;
-        static size_t raised = 0;
-        std::lock_guard<std::mutex> g(mu);
-        if (smem > raised) {
-            cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem));
-            if (e != cudaSuccess) return e;
-            raised = smem;
-        }
-    }
+    static gemm103::DeviceLimits limit;
+    const cudaError_t set = limit.raise(smem, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    });
+    if (set != cudaSuccess) return set;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

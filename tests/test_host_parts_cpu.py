@@ -20,3 +20,20 @@ def test_host_part(name, tmp_path):
                     os.path.join(lib.HERE, "csrc"), os.path.join(HOST, name + ".cpp"), "-o", exe], check=True)
     out = subprocess.run([exe], capture_output=True, text=True, timeout=60)
     assert out.returncode == 0, out.stdout + out.stderr
+
+
+def test_launchers_remember_nothing_per_process():
+    """A function-local static of a launcher is a lock, a table of devices or a
+    limit per device: the attributes it stands for belong to a device."""
+    import re
+    csrc = os.path.join(lib.HERE, "csrc")
+    bad = []
+    for f in sorted(os.listdir(csrc)):
+        if not f.endswith((".cu", ".cuh", ".h")):
+            continue
+        for line in open(os.path.join(csrc, f)):
+            m = re.match(r"\s+static (?!constexpr|const |_?_?inline)([\w:<>\[\], ]+?)\s+\w+(\[[^\]]*\])*( = .*)?;", line)
+            if m and not re.match(r"(std::mutex|DeviceLimits|(gemm103::)?(DeviceLimits|PerDevice<.*>))$", m.group(1)):
+                if "kMaxDevices]" not in line:
+                    bad.append((f, line.strip()))
+    assert not bad, bad
