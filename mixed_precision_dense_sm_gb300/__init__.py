@@ -29,8 +29,6 @@ import array
 import ctypes
 import os
 
-import torch
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgemm_sm103.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "gemm_sm103.h")
@@ -474,6 +472,18 @@ def norm_block_backward_workspace(M, N, gate_rows=1, num_sms=0) -> int:
     return lib.norm_block_backward_workspace(M, N, gate_rows, num_sms)
 
 
+# The planner and the raw C calls need no torch: the first call that takes tensors imports it.
+torch = None
+_CODE = {}
+
+
+def _need_torch():
+    global torch
+    import torch as t
+    _CODE.update({t.float16: GEMM_F16, t.bfloat16: GEMM_BF16, t.float32: GEMM_F32})
+    torch = t
+
+
 # Every launch of a small problem waits for these checks, so they look at each
 # tensor once and with few calls; what is wrong is spelled out by _refuse.
 
@@ -489,6 +499,8 @@ def _refuse(t, name, shape, dtype, dev):
 
 def _device(t, name):
     """The current CUDA device, which the tensor has to be on."""
+    if torch is None:
+        _need_torch()
     dev = t.get_device()
     if dev < 0 or dev != torch._C._cuda_getDevice():
         _refuse(t, name, t.shape, None, -1)
@@ -671,6 +683,8 @@ def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace
     out = g * inv_scale * min(1, max_norm / norm), with
     norm = inv_scale * sqrt(sum of all g^2) returned as a 1-element FP32
     tensor.  A norm that is not finite clips nothing."""
+    if torch is None:
+        _need_torch()
     dev = _device(grads[0], "gradients") if len(grads) else torch.cuda.current_device()
     T = torch.Tensor                      # (mapped methods: a list may hold hundreds of tensors)
     if not set(map(T.get_device, grads)) <= {dev} or not all(map(T.is_contiguous, grads)):
@@ -702,10 +716,9 @@ def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace
     return norm
 
 
-_CODE = {torch.float16: GEMM_F16, torch.bfloat16: GEMM_BF16, torch.float32: GEMM_F32}
-
-
 def dtype_code(t) -> int:
+    if not _CODE:
+        _need_torch()
     return _CODE[t]
 
 
