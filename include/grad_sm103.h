@@ -24,7 +24,9 @@
  * never clips; with outs == NULL and inv_scale == 1 it only computes the norm.
  * A tensor listed twice counts twice in the norm.  Outputs that overlap each
  * other, or a gradient other than their own, are rejected (a CTA would write
- * what another still reads), and so is a tensor listed twice in place.
+ * what another still reads), and so is a tensor listed twice in place; where
+ * all are in place, max_norm is infinite and inv_scale is 1, nothing but the norm
+ * is written and tensors may overlap.
  *
  * The arrays grads, outs, sizes and dtypes are HOST arrays, read during the
  * call only (they travel as kernel parameters, GRAD_TENSORS_PER_LAUNCH

@@ -478,7 +478,11 @@ gemm_status_t grad_clip(int64_t count, const void* const* grads, void* const* ou
             chunks += (sizes[i] + kLeastChunk - 1) / kLeastChunk;
         if (chunks > (1ll << 30)) return GEMM_ERR_INVALID_VALUE;
     }
-    const gemm_status_t st = check_overlap(count, grads, outs, sizes, dtypes);
+    // in place, with nothing to scale: only the norm is written
+    bool norm_only = inv_scale == 1.0f && std::isinf(max_norm);
+    for (int64_t i = 0; outs != nullptr && norm_only && i < count; ++i)
+        norm_only = sizes[i] == 0 || outs[i] == grads[i];
+    const gemm_status_t st = norm_only ? GEMM_OK : check_overlap(count, grads, outs, sizes, dtypes);
     if (st != GEMM_OK) return st;
     if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0)
         return GEMM_ERR_INVALID_VALUE;
