@@ -6,15 +6,16 @@
  *     out_ti = round(g_ti * inv_scale * c),  c = max_norm / norm if norm > max_norm, else 1
  *
  * inv_scale undoes a loss scale (1 where there is none).  If the norm is not
- * finite (an infinity or NaN among the gradients), c = 1: the caller sees it
- * in *norm and skips the step.
+ * finite in FP32 (an infinity or NaN among the gradients, or a norm above FP32's
+ * range), c = 1: the caller sees it in *norm and skips the step.
  *
  * The squares are summed in FP32 over 32 or fewer elements at a time and from
  * there on in FP64; a group of elements whose FP32 sum left the range where
  * every square is exact to FP32 (overflow, or squares that underflow) is
  * summed again in FP64, so the norm is right to a few FP32 roundings for
- * every finite input.  The order of the sums is fixed: the same bits on every
- * run on the same device.  FP16 and BF16 subnormals count.
+ * every finite input (infinity where FP32 does not hold it).  The order of the
+ * sums is fixed: the same bits on every run on the same device.  FP16 and BF16
+ * subnormals count.
  *
  * Tensors: `count` device pointers with their element counts and types, each
  * pointer aligned to its element size, elements contiguous; a tensor may be

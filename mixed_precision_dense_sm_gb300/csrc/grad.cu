@@ -268,9 +268,11 @@ __global__ void __launch_bounds__(kThreads, kApplyCtas)
     double acc = 0.0;
     for (int32_t i = threadIdx.x; i < a.num_partials; i += kThreads) acc += a.partials[i];
     const double norm = sqrt(cta_sum(acc, red)) * static_cast<double>(a.inv_scale);
-    if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = static_cast<float>(norm);
+    // the caller, who decides by the stored norm, and the clipping agree on what is finite
+    const float stored = static_cast<float>(norm);
+    if (a.write_norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = stored;
     double f = static_cast<double>(a.inv_scale);
-    if (isfinite(norm) && norm > static_cast<double>(a.max_norm))
+    if (isfinite(stored) && norm > static_cast<double>(a.max_norm))
         f *= static_cast<double>(a.max_norm) / norm;
     const float factor = static_cast<float>(f);
     const int32_t chunks = t.first_chunk[t.count];

@@ -31,3 +31,22 @@ def test_the_norm_alone_over_overlapping_views(lib):
             lib.grad_clip(views, 1.0)
         assert e.value.status == 1
     assert torch.equal(flat, keep)
+
+
+@pytest.mark.parametrize("inv_scale", [1.0, 0.5])
+def test_a_norm_above_fp32(lib, inv_scale):
+    """Finite gradients whose norm FP32 does not hold: the caller sees an infinite
+    norm, and nothing is clipped (inv_scale applies, exactly where a power of two)."""
+    for n, v in ((2, 3e38), (1000, -1.0e38), (40, 3.38e38)):
+        g = torch.full((n,), v, device="cuda")
+        want = g * inv_scale
+        if inv_scale * math.sqrt(n) * abs(v) <= torch.finfo(F32).max:
+            continue
+        for in_place in (False, True):
+            t, out = g.clone(), torch.zeros_like(g)
+            got = lib.grad_clip([t], 1.0, outputs=None if in_place else [out], inv_scale=inv_scale)
+            assert math.isinf(float(got))
+            assert torch.equal(t if in_place else out, want)
+    g = torch.full((4,), 1.7e38, device="cuda")                   # 3.4e38: the largest that FP32 holds
+    got = lib.grad_clip([g], 1.0)
+    assert abs(float(got) - 3.4e38) <= 8 * ref.U32 * 3.4e38 and torch.allclose(g, torch.full_like(g, 0.5))
