@@ -259,6 +259,23 @@ __device__ __forceinline__ void chunk_scale(const T* p, T* o, int32_t n, float f
     }
 }
 
+// By a factor that FP32 holds as a subnormal, if at all: the products may be
+// normal numbers all the same, so they are made in FP64.  Rare, and out of line as
+// batch_again is.
+template <typename T>
+__device__ __noinline__ void chunk_scale_far(const T* p, T* o, int32_t n, double f) {
+    for (int32_t i = threadIdx.x; i < n; i += kThreads)
+        o[i] = from_f<T>(static_cast<float>(static_cast<double>(to_f<T>(p[i])) * f));
+}
+
+template <typename T>
+__device__ __forceinline__ void chunk_apply(const void* p, void* o, int64_t at, int32_t n, double f) {
+    const T* src = static_cast<const T*>(p) + at;
+    T* dst = static_cast<T*>(o) + at;
+    if (f < 0x1p-126) chunk_scale_far(src, dst, n, f);
+    else chunk_scale(src, dst, n, static_cast<float>(f));
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kApplyCtas)
     apply_kernel(const __grid_constant__ Tensors<CAP> t, const ApplyParams a) {
@@ -274,7 +291,6 @@ __global__ void __launch_bounds__(kThreads, kApplyCtas)
     double f = static_cast<double>(a.inv_scale);
     if (isfinite(stored) && norm > static_cast<double>(a.max_norm))
         f *= static_cast<double>(a.max_norm) / norm;
-    const float factor = static_cast<float>(f);
     const int32_t chunks = t.first_chunk[t.count];
     // this CTA's chunks, the last one first
     const int32_t mine = chunks > static_cast<int32_t>(blockIdx.x)
@@ -283,19 +299,13 @@ __global__ void __launch_bounds__(kThreads, kApplyCtas)
     for (int32_t r = mine; r >= 0; --r) {
         const int32_t c = static_cast<int32_t>(blockIdx.x) + r * static_cast<int32_t>(gridDim.x);
         const int k = find_tensor(t, c);
-        if (factor == 1.0f && t.dst[k] == t.src[k]) continue;
+        if (static_cast<float>(f) == 1.0f && t.dst[k] == t.src[k]) continue;
         const int64_t at = static_cast<int64_t>(c - t.first_chunk[k]) * t.chunk;
         const int64_t left = t.size[k] - at;
         const int32_t n = static_cast<int32_t>(left < t.chunk ? left : t.chunk);
-        if (t.dtype[k] == GEMM_F32)
-            chunk_scale(static_cast<const float*>(t.src[k]) + at, static_cast<float*>(t.dst[k]) + at,
-                        n, factor);
-        else if (t.dtype[k] == GEMM_BF16)
-            chunk_scale(static_cast<const __nv_bfloat16*>(t.src[k]) + at,
-                        static_cast<__nv_bfloat16*>(t.dst[k]) + at, n, factor);
-        else
-            chunk_scale(static_cast<const __half*>(t.src[k]) + at,
-                        static_cast<__half*>(t.dst[k]) + at, n, factor);
+        if (t.dtype[k] == GEMM_F32) chunk_apply<float>(t.src[k], t.dst[k], at, n, f);
+        else if (t.dtype[k] == GEMM_BF16) chunk_apply<__nv_bfloat16>(t.src[k], t.dst[k], at, n, f);
+        else chunk_apply<__half>(t.src[k], t.dst[k], at, n, f);
     }
 }
 

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import ffn_ref as ref
+import test_grad_gpu as clip
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +51,22 @@ def test_a_norm_above_fp32(lib, inv_scale):
     g = torch.full((4,), 1.7e38, device="cuda")                   # 3.4e38: the largest that FP32 holds
     got = lib.grad_clip([g], 1.0)
     assert abs(float(got) - 3.4e38) <= 8 * ref.U32 * 3.4e38 and torch.allclose(g, torch.full_like(g, 0.5))
+
+
+# the factor max_norm / norm: normal, subnormal in FP32, below all of FP32
+@pytest.mark.parametrize("max_norm", [1e-5, 1e-6, 1e-8, 1e-10, 1e-12, 1e-13, 1e-16])
+@pytest.mark.parametrize("dt", [BF, F32], ids=["bf16", "fp32"])
+def test_factors_below_the_normal_range(lib, dt, max_norm):
+    """Elements of about 1e30 clipped to a small norm stay normal numbers, though
+    the factor is not one: the same bound as for any other factor."""
+    gs = clip.tensors([5000, 100, 7], [dt], scale=1e30, off=1)
+    clip.run(lib, gs, max_norm)
+    clip.run(lib, gs, max_norm, inv_scale=0.5, outs=[torch.empty(t.numel() + 2, dtype=dt, device="cuda")[2:]
+                                                     for t in gs])
+    clip.run(lib, gs, max_norm, in_place=True)
+
+
+def test_a_small_scale_and_clipping(lib):
+    """inv_scale = 2^-140, a subnormal: exact where nothing is clipped, a bound as ever where it is."""
+    clip.run(lib, clip.tensors([3000], [F32], scale=1e34), 1e30, inv_scale=2.0 ** -140)
+    clip.run(lib, clip.tensors([3000], [F32], scale=1e34), 1e-7, inv_scale=2.0 ** -140)
