@@ -169,7 +169,7 @@ gemm_status_t make_plan(char transA, char transB, int64_t M, int64_t N, int64_t 
     }
 
     // Operand descriptions in the problem's own orientation.
-    OperandDesc opA, opB;
+    OperandDesc opA{}, opB{};
     opA.ptr = A;
     opA.mn_major = is_t(transA);            // stored K x M
     opA.rows = opA.mn_major ? K : M;

@@ -37,3 +37,13 @@ def test_launchers_remember_nothing_per_process():
                 if "kMaxDevices]" not in line:
                     bad.append((f, line.strip()))
     assert not bad, bad
+
+
+def test_operand_descriptors_start_from_zero():
+    """A field of an operand's description that a plan does not set reads as zero
+    (the paired copy takes the source's columns from one)."""
+    import re
+    text = open(os.path.join(lib.HERE, "csrc", "api.cu")).read()
+    local = re.findall(r"^ +OperandDesc (\w[^;(&*]*);", text, flags=re.M)
+    local = [d for decl in local for d in re.split(r",\s*", decl) if decl != "a, b"]
+    assert local and all(d.endswith("{}") for d in local), local
