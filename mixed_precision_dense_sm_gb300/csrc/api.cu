@@ -1053,7 +1053,6 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
         l.glu.ldp = o->ldp;
         l.glu.F = static_cast<int32_t>(glu->F);
         l.glu.swap = sw ? 1 : 0;
-        l.glu.p_vector = glu_p_vector(glu->F, o, dt.c) ? 1 : 0;
         static_cast<TcParams&>(l.glu) = p;
     }
     l.grid = pl.pub.grid;

@@ -180,7 +180,6 @@ struct GluParams : TcParams {
     int64_t ldp;
     int32_t F;
     int32_t swap;
-    int32_t p_vector;               // P's rows and halves are 16-byte aligned
 };
 
 enum : int { kL2EvictLast = 0, kL2EvictFirst = 1, kL2EvictNormal = 2 };
@@ -704,11 +703,11 @@ __device__ __forceinline__ void ln_tile(const TcParams& p, uint32_t t_row, int32
 // ------------------------------------------------- the gated linear layer
 
 // 32 values of one row at columns c0.. (the columns < cols), cast to the
-// output type, from `base` on; vector stores when the chunk is whole and `vec`.
+// output type, from `base` on (16-byte aligned); vector stores when the chunk is
+// whole.
 template <typename OutT>
-__device__ __forceinline__ void glu_store32(OutT* base, bool vec, int32_t c0, int32_t cols,
-                                            const float (&v)[32]) {
-    if (vec && c0 + 32 <= cols) {
+__device__ __forceinline__ void glu_store32(OutT* base, int32_t c0, int32_t cols, const float (&v)[32]) {
+    if (c0 + 32 <= cols) {
         constexpr int kPer16 = 16 / sizeof(OutT);
         #pragma unroll
         for (int q = 0; q < 32 / kPer16; ++q) {
@@ -867,17 +866,16 @@ __device__ __forceinline__ void glu_tile(const GluParams& p, const CUtensorMap* 
             for (int j = 0; j < 32; ++j) g[j] *= u[j];
             glu_store_turned<OutT>(buf, static_cast<OutT*>(p.C) + static_cast<int64_t>(r0) * p.c_rs,
                                    p.c_rs, rows, c0, p.F, g);
-        } else if (row < p.M && c0 < p.F) {
+        } else if (row < p.M && c0 < p.F) {      // (c_vector: H's and P's rows are 16-byte aligned)
             if (p.P != nullptr) {
                 OutT* prow = static_cast<OutT*>(p.P) + static_cast<int64_t>(row) * p.ldp;
-                glu_store32<OutT>(prow, p.p_vector != 0, c0, p.F, g);
-                glu_store32<OutT>(prow + p.F, p.p_vector != 0, c0, p.F, u);
+                glu_store32<OutT>(prow, c0, p.F, g);
+                glu_store32<OutT>(prow + p.F, c0, p.F, u);
             }
             act32(p.act, g);
             #pragma unroll
             for (int j = 0; j < 32; ++j) g[j] *= u[j];
-            glu_store32<OutT>(static_cast<OutT*>(p.C) + static_cast<int64_t>(row) * p.c_rs,
-                              p.c_vector != 0, c0, p.F, g);
+            glu_store32<OutT>(static_cast<OutT*>(p.C) + static_cast<int64_t>(row) * p.c_rs, c0, p.F, g);
         }
     }
 }
