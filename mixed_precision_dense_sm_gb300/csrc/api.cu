@@ -1706,8 +1706,9 @@ gemm_status_t glu_tile_plan(int64_t M, int64_t F, int64_t K, const void* X, int6
     const int64_t ldc = round_up(max1(2 * F), 8);
     // Where both operands are copied to aligned rows, the copies are padded
     // with zeros to whole pairs of K chunks: two chunks per stage, half the
-    // TMA operations.
-    const bool pad = M > 0 && F > 0 && K > 0 && !rows_aligned(X, ldx, 2) && !rows_aligned(W, ldw, 2);
+    // TMA operations.  (Not past the largest K.)
+    const bool pad = M > 0 && F > 0 && K > 0 && round_up(K, 128) <= INT32_MAX &&
+                     !rows_aligned(X, ldx, 2) && !rows_aligned(W, ldw, 2);
     if (!pad)
         return make_plan('N', 'T', M, 2 * F, K, 1.0f, X, ldx, W, ldw, 0.0f, c, ldc, dt, num_sms,
                          smem_optin, pl, true, false, kMaxKc, 3, true, 0, false, true);
@@ -1996,8 +1997,10 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
     // (an accumulated dW is read too: it stays in place)
     const bool out_x = some && dx_some && !rows_aligned(o->dX, o->lddx, dx_es);
     const bool out_w = some && dw_some && o->beta_w == 0.0f && !rows_aligned(o->dW, o->lddw, dw_es);
-    // the copy of dP is padded with zeros to whole pairs of K chunks
+    // the copy of dP is padded with zeros to whole pairs of K chunks, and dX's
+    // product runs over them (not past the largest K)
     const int64_t ldp8 = round_up(2 * F, 128), ldk8 = round_up(K, 8);
+    const int64_t p_cols = copy_p && ldp8 <= INT32_MAX ? ldp8 : 2 * F;
     const int64_t at_sums = some && o->dbias ? take(slabs * 2 * F * 4) : 0;
     const int64_t at_p = copy_p ? take(M * ldp8 * 2) : 0;
     const int64_t at_w = copy_w ? take(2 * F * ldk8 * 2) : 0;
@@ -2006,7 +2009,7 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
     const int64_t at_dw = out_w ? take(2 * F * ldk8 * dw_es) : 0;
     // planned with stand-in addresses: only alignment counts
     void* const any = reinterpret_cast<void*>(static_cast<uintptr_t>(256));
-    Product gx{'N', 'N', M, K, copy_p ? ldp8 : 2 * F, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_w ? any : W,
+    Product gx{'N', 'N', M, K, p_cols, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_w ? any : W,
                copy_w ? ldk8 : ldw, 0.0f, out_x ? any : o->dX, out_x ? ldk8 : o->lddx, xdt};
     Product gw{'T', 'N', 2 * F, K, M, copy_p ? any : o->dP, copy_p ? ldp8 : o->lddp, copy_x ? any : X,
                copy_x ? ldk8 : ldx, o->beta_w, out_w ? any : o->dW, out_w ? ldk8 : o->lddw, wdt};
