@@ -101,7 +101,7 @@ __device__ __forceinline__ void warp_merge(float& m, float& s) {
 // slice), so its lines stay in L2 (ld.global.cg); otherwise this is the last
 // read and they go first (ld.global.cs).
 template <typename InT, bool KEEP = false>
-__device__ __forceinline__ void load_chunk(const InT* __restrict__ x, int32_t base, int32_t end,
+__device__ __forceinline__ void load_chunk(const InT* x, int32_t base, int32_t end,
                                            bool vec, int t, int T, float (&v)[kE]) {
     constexpr int V = VecOf<InT>::V;
     if (vec) {
@@ -129,7 +129,7 @@ __device__ __forceinline__ void load_chunk(const InT* __restrict__ x, int32_t ba
 }
 
 template <typename InT, typename OutT>
-__device__ __forceinline__ void store_chunk(OutT* __restrict__ y, int32_t base, int32_t end,
+__device__ __forceinline__ void store_chunk(OutT* y, int32_t base, int32_t end,
                                             bool vec, int t, int T, const float (&v)[kE],
                                             float m, float inv_s) {
     // the register layout follows the input's vector width
@@ -197,8 +197,8 @@ __device__ __forceinline__ void chunk_stats(const float (&v)[kE], float& m, floa
 template <typename InT, typename OutT, bool WARP_ROWS>
 __global__ void __launch_bounds__(512)
     softmax_kernel(const __grid_constant__ SoftmaxParams p) {
-    const InT* __restrict__ X = static_cast<const InT*>(p.X);
-    OutT* __restrict__ Y = static_cast<OutT*>(p.Y);
+    const InT* X = static_cast<const InT*>(p.X);
+    OutT* Y = static_cast<OutT*>(p.Y);
     const bool vec = p.vec != 0;
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;

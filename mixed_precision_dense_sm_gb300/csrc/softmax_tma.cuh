@@ -208,7 +208,7 @@ __device__ __forceinline__ void issue_unit(const TmaSoftmaxParams& p, const InT*
 // most one tail element past the bulk-copied part.  WHOLE: every vector slot
 // is inside the row and there is no tail.
 template <typename InT, int KV, bool WHOLE>
-__device__ __forceinline__ void load_row(const uint8_t* srow, const InT* __restrict__ grow,
+__device__ __forceinline__ void load_row(const uint8_t* srow, const InT* grow,
                                          int32_t nvec, int32_t bulk_elems, int32_t cols, int t,
                                          int T, float (&x)[KV][VecOf<InT>::V], float& xt) {
     constexpr int V = VecOf<InT>::V;
@@ -245,7 +245,7 @@ __device__ __forceinline__ void load_row(const uint8_t* srow, const InT* __restr
 // abandoned unless it holds everywhere.  Returns that.
 template <typename InT, typename OutT, int KV, bool WHOLE>
 __device__ __forceinline__ bool finish_row(float (&x)[KV][VecOf<InT>::V], float xt, bool ok,
-                                           OutT* __restrict__ yrow, int32_t nvec,
+                                           OutT* yrow, int32_t nvec,
                                            int32_t bulk_elems, int32_t cols, int t, int T, int gw,
                                            int group, int warp, int lane, float* red_m,
                                            float* red_s) {
@@ -328,8 +328,8 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     // per warp (m_w, s_w) of a shared row, two buffers alternating by row
     __shared__ float red_m[2][kTmaComputeWarps], red_s[2][kTmaComputeWarps];
-    const InT* __restrict__ X = static_cast<const InT*>(p.X);
-    OutT* __restrict__ Y = static_cast<OutT*>(p.Y);
+    const InT* X = static_cast<const InT*>(p.X);
+    OutT* Y = static_cast<OutT*>(p.Y);
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int GW = p.group_warps;
@@ -568,8 +568,8 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
     __shared__ float recv_m[2][kMaxLongCluster], recv_s[2][kMaxLongCluster];
     __shared__ __align__(8) uint64_t xbar[2];
     __shared__ int abort_flag;
-    const InT* __restrict__ X = static_cast<const InT*>(p.X);
-    OutT* __restrict__ Y = static_cast<OutT*>(p.Y);
+    const InT* X = static_cast<const InT*>(p.X);
+    OutT* Y = static_cast<OutT*>(p.Y);
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int CL = p.cluster;
@@ -669,8 +669,8 @@ __global__ void __launch_bounds__(kTmaThreads, 1)
             if (lane == 0 && wok) gemm103::mbar_arrive(&empty[dd]);
         };
         for (int64_t row = cid; row < p.rows; row += nclusters, ++iter) {
-            const InT* __restrict__ xrow = X + row * p.ldx + e_lo;
-            OutT* __restrict__ yrow = Y + row * p.ldy + e_lo;
+            const InT* xrow = X + row * p.ldx + e_lo;
+            OutT* yrow = Y + row * p.ldy + e_lo;
             const int pb = static_cast<int>(iter & 1u);
             // pass 1: (m, s) of this thread's elements, chunk by chunk
             float m = -INFINITY, s = 0.0f;

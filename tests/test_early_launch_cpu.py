@@ -63,3 +63,8 @@ def test_no_read_only_loads():
             early = [code(f)]                      # (all, or a file of functions alone)
         bad += [(f, m.group(0)) for t in early for m in NC.finditer(t)]
     assert not bad, bad
+
+
+def test_softmax_promises_nothing_about_its_rows():
+    """Y may be X, and the kernel before it writes X: no pointer is __restrict__."""
+    assert not [f for f in sources() if f.startswith("softmax") and "__restrict__" in code(f)]

@@ -86,3 +86,28 @@ def test_training_chain(M, K, F):
         wait()
     compare(start, step)
     g.close()
+
+
+@pytest.mark.parametrize("rows,cols", [(64, 1000), (300, 1023), (40, 33), (8, 70001), (4, 300000)])
+@pytest.mark.parametrize("dt", [BF, torch.float32], ids=["bf16", "fp32"])
+def test_softmax_after_the_kernel_that_writes_its_rows(rows, cols, dt):
+    """Rows that clipping or a norm has just written, in place and apart."""
+    import mixed_precision_dense_sm_gb300 as lib
+    gen = torch.Generator().manual_seed(cols)
+    src = [randn(gen, rows, cols, scale=2.0, dtype=dt) for _ in range(3)]
+    start = {"X": randn(gen, rows, cols, dtype=dt), "Y": randn(gen, rows, cols, dtype=dt)}
+    norm = torch.empty(1, device="cuda")
+    ws = torch.empty(lib.grad_clip_workspace(1), dtype=torch.uint8, device="cuda")
+    small = cols <= lib.NORM_MAX_N
+
+    def step(s, i, wait):
+        lib.grad_clip([src[i % 3]], 10.0 + i % 7, outputs=[s["X"]], norm=norm, workspace=ws)
+        wait()
+        if small:
+            lib.norm_block(s["X"], s["Y"], s["X"], pre=None, post="rms")
+            wait()
+        lib.softmax(s["X"], s["Y"])
+        wait()
+        lib.softmax(s["X"], s["X"])
+        wait()
+    compare(start, step)
