@@ -6,12 +6,14 @@
  * the up projection's F rows -- and an optional bias of 2F elements:
  *     P = X W^T + bias                (M x 2F: columns 0..F-1 the gate's G, F..2F-1 U)
  *     H = act(G) * U                  (M x F)
- * Both projections, the activation and the product run in one tcgen05 kernel:
- * G and U of an output tile are accumulated side by side in tensor memory in
- * FP32, and H is rounded once.  Every problem runs on the GEMM's own tile
- * schedules (CTA pairs, single CTAs, stream-K, swapped skinny tiles for few
- * rows).  P is written (rounded once, from the same FP32 values) where the
- * caller asks for it, for the backward pass.
+ * Both projections, the activation and the product run in one kernel (behind
+ * copies of rows that are not 16-byte aligned): G and U of an output element are
+ * accumulated in FP32, and H is rounded once.  In general that is the GEMM's
+ * tcgen05 kernel on its own tile schedules (CTA pairs, single CTAs, stream-K,
+ * swapped tiles), with G and U of a tile side by side in tensor memory; up to 128
+ * rows go to a tcgen05 kernel that streams W where few tiles make it the faster
+ * one, and 1 or 2 aligned rows to FP32 dot products.  P is written (rounded once,
+ * from the same FP32 values) where the caller asks for it, for the backward pass.
  *
  * act is any gemm_activation_t, with the accuracy stated there.  act(G) * U
  * follows IEEE arithmetic (0 * inf and NaN give NaN).

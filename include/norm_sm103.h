@@ -55,8 +55,11 @@
  * device; the calls are asynchronous on `stream`, allocate nothing and keep
  * nothing.  The backward pass writes its partial sums to the caller's
  * workspace (norm_block_backward_workspace bytes, 16-byte aligned; its
- * contents need no preparation); two calls that may overlap on the GPU need
- * two workspaces.  Both calls can be captured into a CUDA graph.
+ * contents need no preparation): 16 N bytes for each chunk of rows, of which
+ * there are about as many as SMs but at least one for every group of the gate.
+ * With 1 < gate_rows < M that is at least 16 N ceil(M / gate_rows) bytes, for
+ * two rows per group and 16-bit rows four times the size of X.  Two calls that
+ * may overlap on the GPU need two workspaces.  Both calls can be captured into a CUDA graph.
  *
  * Errors: GEMM_ERR_INVALID_VALUE (bad size, leading dimension, type, kind,
  * NULL or misaligned pointer, eps not positive and finite, scale not finite,

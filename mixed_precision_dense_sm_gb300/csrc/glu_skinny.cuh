@@ -11,9 +11,10 @@
 // a counter and a second pass over tensor memory (4 to 5 us of a problem of
 // 10).  Two CTAs share an SM, so one's set-up and epilogue hide behind the
 // other's stream, and S = 1 suffices once there are about as many tiles as SMs:
-// HBM, which bounds all of this, divides itself evenly over the CTAs.  64 tokens,
-// 4096 -> 14336, fp16: 41 us between other work, 5.8 TB/s; 16 tokens, 4096 -> 4096:
-// 14.5 us.
+// HBM, which bounds all of this, divides itself evenly over the CTAs.  W not in
+// L2, one call after another: 16 tokens, 4096 -> 14336, 39.2 us, 6.0 TB/s; 4096 ->
+// 4096, 14.0 us, 4.8 TB/s; 64 tokens, 2048 -> 10240, 23.0 us, 3.6 TB/s.  (Of more
+// tokens and tiles the GEMM's persistent tiles are faster: glu_plan says where.)
 #pragma once
 #include <cstdint>
 #include <cuda.h>
