@@ -269,7 +269,7 @@ typedef struct {
     int32_t swap_ab;       /* 1: computed as C^T = op(B)^T op(A)^T */
     int32_t c_vector;      /* 1: C rows are 16-byte aligned (vector epilogue) */
     int32_t sk_len;        /* stream-K: k-blocks per CTA (0 = data-parallel) */
-    int32_t sk_max_seg;    /* stream-K: workspace slots per CTA */
+    int32_t sk_max_seg;    /* stream-K: tiles per CTA's range at most (slots held; its sums take one) */
     int32_t k_blocks;      /* ceil(K / block_k) */
     int32_t tiles_m;       /* tile rows (of the possibly swapped problem) */
     int32_t tiles_n;       /* tile columns */

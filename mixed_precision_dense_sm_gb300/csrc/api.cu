@@ -962,7 +962,6 @@ gemm_status_t enqueue_plan(const Plan& pl, EncodeTiledFn encode, int num_sms, ui
                          static_cast<uint32_t>(kBlockM * cg), static_cast<uint32_t>(bn));
     p.stream_k = pl.sk_len > 0 ? 1 : 0;
     p.sk_len = pl.sk_len;
-    p.sk_max_seg = pl.sk_max_seg;
     p.alpha = alpha;
     p.beta = beta;
     p.C = C;

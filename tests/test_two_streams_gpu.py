@@ -71,3 +71,29 @@ def test_two_streams(a, b):
             assert torch.isfinite(want[k].float()).all() and torch.equal(o[k], want[k]), k
     for w in works:
         w.g.close()
+
+
+@pytest.mark.parametrize("shapes", [((64, 14336, 4096), (64, 4096, 14336)), ((64, 16384, 8192), (3136, 512, 4608))])
+def test_stream_k_on_two_streams(shapes):
+    """Stream-K kernels of two streams share the SMs: a finisher waits only for
+    blocks started before it, so every call ends, with the bits it has alone."""
+    import mixed_precision_dense_sm_gb300 as lib
+    runs = []
+    for i, (M, N, K) in enumerate(shapes):
+        gen = torch.Generator().manual_seed(i)
+        st, p = lib.gemm_plan_query("N", "T", M, N, K, 1.0, 256, K, 256, K, 0.0, 256, N,
+                                    (lib.GEMM_BF16, lib.GEMM_BF16, lib.GEMM_F32))
+        assert st == 0 and p["sk_len"] > 0, p
+        A, B = torch.randn(M, K, generator=gen).to(BF).cuda(), torch.randn(N, K, generator=gen).to(BF).cuda()
+        C, h = torch.empty(M, N, device="cuda"), lib.Gemm()
+        h(A, B, C, transB="T")
+        h.sync()
+        runs.append((h, A, B, C, C.clone(), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(100):
+        for h, A, B, C, _, s in runs:
+            h(A, B, C, transB="T", stream=s.cuda_stream)
+    for h, A, B, C, want, s in runs:
+        h.sync(s.cuda_stream)
+        assert torch.equal(C, want)
+        h.close()
