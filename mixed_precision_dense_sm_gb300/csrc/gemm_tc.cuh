@@ -1461,19 +1461,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = (wait_ok != 0);
                 __threadfence();
                 if (ok) {
+                    // (The gated epilogue, which holds two values per output, has
+                    // registers for one slot: by two, pair tiles spilled 336 bytes
+                    // in stores, not 88; 1000 tokens, 777 -> 1023, 20.6 us, not 18.8.)
+                    constexpr int kFin = EPI == kEpiGlu ? 1 : kFinBatch;
                     #pragma unroll 1
                     for (int ch = half; ch < BN / 32; ch += 2) {
                         float acc[32];
                         #pragma unroll
                         for (int j = 0; j < 32; ++j) acc[j] = 0.0f;
-                        // 16 columns at a time, up to kFinBatch slots' loads in
+                        // 16 columns at a time, up to kFin slots' loads in
                         // flight together; each warp load is 512 contiguous bytes
                         #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            for (int32_t g0 = g_first + 1; g0 <= g_last; g0 += kFinBatch) {
-                                float x[kFinBatch][16];
+                            for (int32_t g0 = g_first + 1; g0 <= g_last; g0 += kFin) {
+                                float x[kFin][16];
                                 #pragma unroll
-                                for (int u = 0; u < kFinBatch; ++u) {
+                                for (int u = 0; u < kFin; ++u) {
                                     const int32_t g = g0 + u;
                                     if (g > g_last) continue;
                                     const int32_t slot = stream_k_unit(g, gridDim.x / CG);
@@ -1491,7 +1495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     }
                                 }
                                 #pragma unroll
-                                for (int u = 0; u < kFinBatch; ++u) {
+                                for (int u = 0; u < kFin; ++u) {
                                     if (g0 + u > g_last) break;
                                     #pragma unroll
                                     for (int j = 0; j < 16; ++j) acc[h * 16 + j] += x[u][j];
