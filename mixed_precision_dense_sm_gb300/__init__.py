@@ -18,10 +18,13 @@ include/conv_sm103.h: ``conv2d_fprop``, ``conv2d_plan_query``,
 ``glu_forward``, ``glu_backward``, ``glu_plan_query``; include/norm_sm103.h
 (norms around a block): ``norm_block_forward``, ``norm_block_backward``,
 ``norm_block_backward_workspace``; include/grad_sm103.h (gradient norm and
-clipping): ``grad_clip_raw``, ``grad_clip_workspace``.
+clipping): ``grad_clip_raw``, ``grad_clip_workspace``; include/expert_sm103.h
+(tokens sorted by expert and back): ``expert_sort_raw`` and ``expert_rows_raw``.
 ``Gemm`` wraps a handle and adds ``__call__``, ``layernorm``, ``glu`` and
 ``glu_backward`` for torch tensors; ``softmax``, ``norm_block``,
-``norm_block_backward`` and ``grad_clip`` do the same for the others.
+``norm_block_backward``, ``grad_clip``, ``expert_sort``, ``expert_gather``,
+``expert_combine``, ``expert_gather_backward`` and ``expert_combine_backward``
+do the same for the others.
 """
 from __future__ import annotations
 
@@ -36,7 +39,8 @@ HEADERS = [HEADER, os.path.join(os.path.dirname(HERE), "include", "softmax_sm103
            os.path.join(os.path.dirname(HERE), "include", "conv_sm103.h"),
            os.path.join(os.path.dirname(HERE), "include", "glu_sm103.h"),
            os.path.join(os.path.dirname(HERE), "include", "norm_sm103.h"),
-           os.path.join(os.path.dirname(HERE), "include", "grad_sm103.h")]
+           os.path.join(os.path.dirname(HERE), "include", "grad_sm103.h"),
+           os.path.join(os.path.dirname(HERE), "include", "expert_sm103.h")]
 
 GEMM_F16, GEMM_BF16, GEMM_F32 = 0, 1, 2
 STATUS = {0: "GEMM_OK", 1: "GEMM_ERR_INVALID_VALUE", 2: "GEMM_ERR_NOT_SUPPORTED",
@@ -99,6 +103,13 @@ class NormBlockGrads(ctypes.Structure):
                 ("d_gate", ctypes.c_void_p), ("grad_dtype", ctypes.c_int32)]
 
 
+class ExpertWeights(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("ldw", ctypes.c_int64),
+                ("weight_dtype", ctypes.c_int32), ("dweight", ctypes.c_void_p),
+                ("lddw", ctypes.c_int64), ("dweight_dtype", ctypes.c_int32)]
+
+
+EXPERT_MAX = 1024
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
 ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU,
                "silu": ACT_SILU}
@@ -204,6 +215,15 @@ def _load():
     lib.grad_clip.argtypes = [i64, vp, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp, vp, i64, vp]
     lib.grad_clip_workspace.restype = i64
     lib.grad_clip_workspace.argtypes = [i64, i32]
+    lib.expert_sort.restype = ctypes.c_int
+    lib.expert_sort.argtypes = [i64, i64, i64, vp, i64, i32, vp, vp, vp, vp]
+    for f in (lib.expert_gather, lib.expert_combine):
+        f.restype = ctypes.c_int
+        f.argtypes = [i64] * 4 + [vp, i64, vp, vp, i64, i32, ctypes.POINTER(ExpertWeights), vp]
+    for f in (lib.expert_gather_backward, lib.expert_combine_backward):
+        f.restype = ctypes.c_int
+        f.argtypes = [i64] * 4 + [vp, i64, vp, i64, vp, vp, i64, i32,
+                                  ctypes.POINTER(ExpertWeights), vp]
     lib.softmax_sync.restype = ctypes.c_int
     lib.softmax_sync.argtypes = [vp]
     lib.softmax_debug_set.restype = ctypes.c_int
@@ -326,7 +346,7 @@ def declared_symbols():
     for h in HEADERS:
         text = open(h).read()
         names |= set(re.findall(r"^\s*(?:gemm_status_t|const char\*|int64_t)\s+"
-                                r"((?:gemm|softmax|conv2d|glu|norm|grad)_\w+)\s*\(",
+                                r"((?:gemm|softmax|conv2d|glu|norm|grad|expert)_\w+)\s*\(",
                                 text, flags=re.M))
     return sorted(names)
 
@@ -714,6 +734,157 @@ def grad_clip(grads, max_norm, outputs=None, inv_scale=1.0, norm=None, workspace
     if st != 0:
         raise GemmError(st, "grad_clip")
     return norm
+
+
+# -------------------------------------------- tokens sorted by expert and back
+
+def expert_sort_raw(T, k, E, ids, ldids, id_bytes, pos, offsets, order=0, stream=0) -> int:
+    """Raw C-ABI call (include/expert_sm103.h); order 0: not wanted.  Returns the
+    gemm_status_t code."""
+    return lib.expert_sort(T, k, E, ids or None, ldids, id_bytes, pos or None, offsets or None,
+                           order or None, stream)
+
+
+def expert_rows_raw(name, T, k, D, rows, *args, weights=None, stream=0) -> int:
+    """Raw C-ABI call of ``name`` (expert_gather, expert_combine or one's backward
+    pass); args as in the header, between rows and w; `weights` an ExpertWeights."""
+    return getattr(lib, name)(T, k, D, rows, *args, None if weights is None else ctypes.byref(weights),
+                              stream)
+
+
+def expert_sort(ids, experts, pos=None, offsets=None, order=None, stream=None):
+    """Sorts the choices of T tokens by expert: (pos, offsets, order).
+
+    ids (T x k, int32 or int64) holds the experts' numbers, 0 .. experts - 1; others
+    (-1) choose none.  pos (T x k): the row of each choice, -1 for none; offsets
+    (experts + 1): the experts' first rows; order (T * k): the choice t * k + j of
+    each row, -1 behind the last.  int32 all, new tensors where None.  Rows are in
+    the order of the experts, and of the choices within one."""
+    dev = _device(ids, "ids")
+    if ids.dim() != 2 or ids.dtype is not torch.int64 and ids.dtype is not torch.int32:
+        raise ValueError("ids must be T x k of int32 or int64")
+    T, k = ids.shape
+    i, ldi = _mat(ids, "ids", T, k, None, dev)
+    if pos is None:
+        pos = _empty((T, k), torch.int32, dev, stream)
+    if offsets is None:
+        offsets = _empty((experts + 1,), torch.int32, dev, stream)
+    if order is None:
+        order = _empty((T * k,), torch.int32, dev, stream)
+    st = lib.expert_sort(T, k, experts, i, ldi, ids.element_size(), _pos(pos, T, k, dev),
+                         _vec(offsets, "offsets", experts + 1, torch.int32, dev),
+                         _vec(order, "order", T * k, torch.int32, dev),
+                         _stream(dev) if stream is None else stream)
+    if st != 0:
+        raise GemmError(st, "expert_sort")
+    return pos, offsets, order
+
+
+def _pos(pos, T, k, dev):
+    if pos.shape != (T, k) or pos.dtype is not torch.int32 or pos.get_device() != dev or \
+            not pos.is_contiguous():
+        if pos.is_contiguous():
+            _refuse(pos, "pos", (T, k), torch.int32, dev)
+        raise ValueError("pos must be contiguous")
+    return pos.data_ptr()
+
+
+def _expert_weights(weight, dweight, T, k, dev):
+    """The weights' argument; None where there are none."""
+    if weight is None and dweight is None:
+        return None
+    w, ldw = _mat(weight, "weight", T, k, None, dev)
+    dw, lddw = _mat(dweight, "dweight", T, k, None, dev)
+    return ctypes.byref(ExpertWeights(
+        w, ldw, GEMM_F32 if weight is None else dtype_code(weight.dtype), dw, lddw,
+        GEMM_F32 if dweight is None else dtype_code(dweight.dtype)))
+
+
+def _expert_shapes(tokens, pos, name):
+    dev = _device(tokens, name)
+    if tokens.dim() != 2 or pos.dim() != 2:
+        raise ValueError(f"{name} and pos must be 2-D")
+    return (dev, *tokens.shape, pos.shape[1])
+
+
+def expert_gather(X, pos, weight=None, Xs=None, stream=None):
+    """The tokens' rows to their experts: Xs[pos[t, j]] = weight[t, j] * X[t].
+
+    X is T x D, pos (T x k) expert_sort's, weight T x k or None (1).  Xs has X's
+    type and D columns (a new T * k x D tensor where None); rows that pos does not
+    name are left as they are.  Returns Xs."""
+    dev, T, D, k = _expert_shapes(X, pos, "X")
+    if Xs is None:
+        Xs = _empty((T * k, D), X.dtype, dev, stream)
+    x, ldx = _mat(X, "X", T, D, None, dev)
+    xs, ldxs = _mat(Xs, "Xs", Xs.shape[0], D, X.dtype, dev)
+    st = lib.expert_gather(T, k, D, Xs.shape[0], x, ldx, _pos(pos, T, k, dev), xs, ldxs,
+                           dtype_code(X.dtype), _expert_weights(weight, None, T, k, dev),
+                           _stream(dev) if stream is None else stream)
+    if st != 0:
+        raise GemmError(st, "expert_gather")
+    return Xs
+
+
+def expert_combine(Ys, pos, weight=None, Y=None, stream=None):
+    """The experts' rows back to the tokens: Y[t] = sum over j of
+    weight[t, j] * Ys[pos[t, j]], in FP32 and rounded once.
+
+    Ys has D columns, pos (T x k) is expert_sort's, weight T x k or None (1); Y is
+    T x D of Ys's type (a new tensor where None).  Returns Y."""
+    dev, rows, D, k = _expert_shapes(Ys, pos, "Ys")
+    T = pos.shape[0]
+    if Y is None:
+        Y = _empty((T, D), Ys.dtype, dev, stream)
+    ys, ldys = _mat(Ys, "Ys", rows, D, None, dev)
+    y, ldy = _mat(Y, "Y", T, D, Ys.dtype, dev)
+    st = lib.expert_combine(T, k, D, rows, ys, ldys, _pos(pos, T, k, dev), y, ldy,
+                            dtype_code(Ys.dtype), _expert_weights(weight, None, T, k, dev),
+                            _stream(dev) if stream is None else stream)
+    if st != 0:
+        raise GemmError(st, "expert_combine")
+    return Y
+
+
+def expert_gather_backward(dXs, pos, weight=None, X=None, dX=None, dweight=None, stream=None):
+    """Backward pass of expert_gather into the given tensors (None: not wanted):
+    dX[t] = sum over j of weight[t, j] * dXs[pos[t, j]] and
+    dweight[t, j] = X[t] . dXs[pos[t, j]] (0 where pos is -1); X only with dweight."""
+    dev, rows, D, k = _expert_shapes(dXs, pos, "dXs")
+    T = pos.shape[0]
+    if dweight is not None and X is None:
+        raise ValueError("dweight needs X")
+    if dX is None and dweight is None:
+        raise ValueError("one of dX and dweight has to be given")
+    g, ldg = _mat(dXs, "dXs", rows, D, None, dev)
+    x, ldx = _mat(X, "X", T, D, dXs.dtype, dev)
+    dx, lddx = _mat(dX, "dX", T, D, dXs.dtype, dev)
+    st = lib.expert_gather_backward(T, k, D, rows, g, ldg, x, ldx, _pos(pos, T, k, dev), dx, lddx,
+                                    dtype_code(dXs.dtype), _expert_weights(weight, dweight, T, k, dev),
+                                    _stream(dev) if stream is None else stream)
+    if st != 0:
+        raise GemmError(st, "expert_gather_backward")
+
+
+def expert_combine_backward(dY, pos, weight=None, Ys=None, dYs=None, dweight=None, stream=None):
+    """Backward pass of expert_combine into the given tensors (None: not wanted):
+    dYs[pos[t, j]] = weight[t, j] * dY[t] and dweight[t, j] = dY[t] . Ys[pos[t, j]]
+    (0 where pos is -1); Ys only with dweight.  dYs may be Ys; rows that pos does not
+    name are left as they are."""
+    dev, T, D, k = _expert_shapes(dY, pos, "dY")
+    if dweight is not None and Ys is None:
+        raise ValueError("dweight needs Ys")
+    if dYs is None and dweight is None:
+        raise ValueError("one of dYs and dweight has to be given")
+    rows = next((m.shape[0] for m in (dYs, Ys) if m is not None), 0)
+    g, ldg = _mat(dY, "dY", T, D, None, dev)
+    ys, ldys = _mat(Ys, "Ys", rows, D, dY.dtype, dev)
+    dys, lddys = _mat(dYs, "dYs", rows, D, dY.dtype, dev)
+    st = lib.expert_combine_backward(T, k, D, rows, g, ldg, ys, ldys, _pos(pos, T, k, dev), dys, lddys,
+                                     dtype_code(dY.dtype), _expert_weights(weight, dweight, T, k, dev),
+                                     _stream(dev) if stream is None else stream)
+    if st != 0:
+        raise GemmError(st, "expert_combine_backward")
 
 
 def dtype_code(t) -> int:
