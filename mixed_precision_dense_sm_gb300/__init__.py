@@ -19,9 +19,11 @@ include/conv_sm103.h: ``conv2d_fprop``, ``conv2d_plan_query``,
 (norms around a block): ``norm_block_forward``, ``norm_block_backward``,
 ``norm_block_backward_workspace``; include/grad_sm103.h (gradient norm and
 clipping): ``grad_clip_raw``, ``grad_clip_workspace``; include/expert_sm103.h
-(tokens sorted by expert and back): ``expert_sort_raw`` and ``expert_rows_raw``.
-``Gemm`` wraps a handle and adds ``__call__``, ``layernorm``, ``glu`` and
-``glu_backward`` for torch tensors; ``softmax``, ``norm_block``,
+(tokens sorted by expert and back): ``expert_sort_raw`` and ``expert_rows_raw``;
+include/ortho_sm103.h (the orthogonalised update): ``ortho_update``,
+``ortho_workspace``.
+``Gemm`` wraps a handle and adds ``__call__``, ``layernorm``, ``glu``,
+``glu_backward`` and ``orthogonalize`` for torch tensors; ``softmax``, ``norm_block``,
 ``norm_block_backward``, ``grad_clip``, ``expert_sort``, ``expert_gather``,
 ``expert_combine``, ``expert_gather_backward`` and ``expert_combine_backward``
 do the same for the others.
@@ -40,7 +42,8 @@ HEADERS = [HEADER, os.path.join(os.path.dirname(HERE), "include", "softmax_sm103
            os.path.join(os.path.dirname(HERE), "include", "glu_sm103.h"),
            os.path.join(os.path.dirname(HERE), "include", "norm_sm103.h"),
            os.path.join(os.path.dirname(HERE), "include", "grad_sm103.h"),
-           os.path.join(os.path.dirname(HERE), "include", "expert_sm103.h")]
+           os.path.join(os.path.dirname(HERE), "include", "expert_sm103.h"),
+           os.path.join(os.path.dirname(HERE), "include", "ortho_sm103.h")]
 
 GEMM_F16, GEMM_BF16, GEMM_F32 = 0, 1, 2
 STATUS = {0: "GEMM_OK", 1: "GEMM_ERR_INVALID_VALUE", 2: "GEMM_ERR_NOT_SUPPORTED",
@@ -110,6 +113,14 @@ class ExpertWeights(ctypes.Structure):
 
 
 EXPERT_MAX = 1024
+
+
+class OrthoUpdate(ctypes.Structure):
+    _fields_ = [("steps", ctypes.c_int32), ("coefficients", ctypes.c_void_p),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+ORTHO_MAX_STEPS, ORTHO_MAX_SIDE = 32, 65536
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU = 0, 1, 2, 3
 ACTIVATIONS = {None: ACT_NONE, "none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU,
                "silu": ACT_SILU}
@@ -224,6 +235,11 @@ def _load():
         f.restype = ctypes.c_int
         f.argtypes = [i64] * 4 + [vp, i64, vp, i64, vp, vp, i64, i32,
                                   ctypes.POINTER(ExpertWeights), vp]
+    lib.ortho_update.restype = ctypes.c_int
+    lib.ortho_update.argtypes = [vp, i64, i64, i64, vp, i64, i64, i32, vp, i64, i64,
+                                 ctypes.POINTER(OrthoUpdate), vp]
+    lib.ortho_workspace.restype = i64
+    lib.ortho_workspace.argtypes = [i64, i64, i64]
     lib.softmax_sync.restype = ctypes.c_int
     lib.softmax_sync.argtypes = [vp]
     lib.softmax_debug_set.restype = ctypes.c_int
@@ -346,7 +362,7 @@ def declared_symbols():
     for h in HEADERS:
         text = open(h).read()
         names |= set(re.findall(r"^\s*(?:gemm_status_t|const char\*|int64_t)\s+"
-                                r"((?:gemm|softmax|conv2d|glu|norm|grad|expert)_\w+)\s*\(",
+                                r"((?:gemm|softmax|conv2d|glu|norm|grad|expert|ortho)_\w+)\s*\(",
                                 text, flags=re.M))
     return sorted(names)
 
@@ -887,6 +903,23 @@ def expert_combine_backward(dY, pos, weight=None, Ys=None, dYs=None, dweight=Non
         raise GemmError(st, "expert_combine_backward")
 
 
+# ------------------------------------------------------ the orthogonalised update
+
+def ortho_update(h, batch, rows, cols, G, ldg, stride_g, g_dtype, O, ldo, stride_o, coefficients,
+                 eps=1e-7, scale=1.0, stream=0) -> int:
+    """Raw C-ABI call (include/ortho_sm103.h); coefficients: 3 floats per step.
+    Returns the gemm_status_t code."""
+    abc = array.array("f", coefficients)
+    o = OrthoUpdate(len(abc) // 3, abc.buffer_info()[0], eps, scale)
+    return lib.ortho_update(h, batch, rows, cols, G or None, ldg, stride_g, g_dtype, O or None, ldo,
+                            stride_o, ctypes.byref(o), stream)
+
+
+def ortho_workspace(batch, rows, cols) -> int:
+    """Bytes of the handle's workspace that ortho_update takes."""
+    return lib.ortho_workspace(batch, rows, cols)
+
+
 def dtype_code(t) -> int:
     if not _CODE:
         _need_torch()
@@ -1035,6 +1068,45 @@ class Gemm:
         if st != 0:
             raise GemmError(st, "glu_backward")
         return dP
+
+    def orthogonalize(self, G, O=None, steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7,
+                      scale=1.0, stream=None):
+        """The update G brought near orthonormal rows or columns by Newton-Schulz
+        steps (as the Muon optimiser does): X = G / (||G|| + eps), then `steps`
+        times X = a X + (b A + c A^2) X with A = X X^T (on the shorter side);
+        returns O = scale * X in BF16 (a new tensor where None).
+
+        G is rows x cols, or a batch of such, of any type; coefficients are one
+        (a, b, c) or one for each step.  O may be G."""
+        dev = _device(G, "G")
+        if G.dim() not in (2, 3):
+            raise ValueError("G must be rows x cols, or batch x rows x cols")
+        if O is None:
+            O = _empty(tuple(G.shape), torch.bfloat16, dev, stream)
+        if O.dim() != G.dim():
+            raise ValueError("O must have G's shape")
+        batch, sg, so, g, o = 1, 0, 0, G, O
+        if G.dim() == 3:
+            batch, sg, so = G.shape[0], G.stride(0), O.stride(0)
+            if O.shape != G.shape:
+                _refuse(O, "O", tuple(G.shape), torch.bfloat16, dev)
+            if batch == 0:
+                return O
+            g, o = G[0], O[0]
+        rows, cols = g.shape
+        gp, ldg = _mat(g, "G", rows, cols, None, dev)
+        op, ldo = _mat(o, "O", rows, cols, torch.bfloat16, dev)
+        if len(coefficients) == 3 and not hasattr(coefficients[0], "__len__"):
+            abc = tuple(coefficients) * steps
+        elif len(coefficients) == steps:
+            abc = [v for step in coefficients for v in step]
+        else:
+            raise ValueError("coefficients: one (a, b, c), or one for each step")
+        st = ortho_update(self.h, batch, rows, cols, gp, ldg, sg, dtype_code(G.dtype), op, ldo, so, abc, eps,
+                          scale, _stream(dev) if stream is None else stream)
+        if st != 0:
+            raise GemmError(st, "ortho_update")
+        return O
 
     def sync(self, stream=None):
         import torch

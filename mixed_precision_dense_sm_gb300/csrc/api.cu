@@ -25,6 +25,7 @@
 #include "aux_kernels.cuh"
 #include "glu_kern.cuh"
 #include "launch.h"
+#include "ortho_launch.h"
 #include "workspace.h"
 
 using namespace gemm103;
@@ -2111,6 +2112,43 @@ gemm_status_t glu_backward(gemm_handle_t h, int64_t M, int64_t F, int64_t K, con
             return GEMM_ERR_LAUNCH;
     }
     return GEMM_OK;
+}
+
+int64_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols) {
+    if (batch < 0 || rows < 0 || cols < 0 || batch > 65535 || rows > ORTHO_MAX_SIDE || cols > ORTHO_MAX_SIDE)
+        return -1;
+    if (batch == 0 || rows == 0 || cols == 0) return 0;
+    return kWsHeaderBytes + ortho_bytes(batch, rows, cols);
+}
+
+gemm_status_t ortho_update(gemm_handle_t h, int64_t batch, int64_t rows, int64_t cols, const void* G,
+                           int64_t ldg, int64_t stride_g, int32_t g_dtype, void* O, int64_t ldo,
+                           int64_t stride_o, const ortho_update_t* opt, gemm_stream_t stream_) {
+    if (h == nullptr || !device_current(h)) return GEMM_ERR_INVALID_VALUE;
+    gemm_status_t st = take_device_error(h);
+    if (st != GEMM_OK) return st;
+    const int64_t bytes = ortho_workspace(batch, rows, cols);
+    if (bytes < 0 || opt == nullptr || opt->coefficients == nullptr || opt->steps < 1 ||
+        opt->steps > ORTHO_MAX_STEPS || !(opt->eps >= 0.0f) || !std::isfinite(opt->eps) ||
+        !std::isfinite(opt->scale) || !dtype16or32(g_dtype))
+        return GEMM_ERR_INVALID_VALUE;
+    for (int32_t i = 0; i < 3 * opt->steps; ++i)
+        if (!std::isfinite(opt->coefficients[i])) return GEMM_ERR_INVALID_VALUE;
+    constexpr int64_t kMostLd = 1ll << 40;
+    if (ldg < max1(cols) || ldo < max1(cols) || ldg > kMostLd || ldo > kMostLd) return GEMM_ERR_INVALID_VALUE;
+    if (bytes == 0) return GEMM_OK;
+    if (batch > 1 && (stride_g < (rows - 1) * ldg + cols || stride_o < (rows - 1) * ldo + cols ||
+                      stride_g > INT64_MAX >> 20 || stride_o > INT64_MAX >> 20))
+        return GEMM_ERR_INVALID_VALUE;
+    if (G == nullptr || O == nullptr || !aligned_to(G, in_elem_bytes(g_dtype)) || !aligned_to(O, 2))
+        return GEMM_ERR_INVALID_VALUE;
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    st = ensure_workspace(h, static_cast<size_t>(bytes), stream);
+    if (st != GEMM_OK) return st;
+    return ortho_enqueue(OrthoCall{batch, rows, cols, G, ldg, stride_g, g_dtype, O, ldo, stride_o, opt, h->encode,
+                                   static_cast<uint8_t*>(h->ws.data()) + kWsHeaderBytes, h->num_sms, h->err_dev,
+                                   h->wait_limit_ns != 0 ? h->wait_limit_ns : kWaitTimeoutNs, h->debug_flags,
+                                   stream});
 }
 
 }  // extern "C"

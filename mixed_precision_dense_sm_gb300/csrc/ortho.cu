@@ -1,0 +1,452 @@
+// ortho.cu -- the orthogonalised update (include/ortho_sm103.h): the norm, the
+// scaled copy, and the schedule of the products (ortho_kern.cuh).
+#include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include "device_limits.h"
+#include "f32x2.cuh"
+#include "ortho_kern.cuh"
+#include "ortho_launch.h"
+
+namespace gemm103 {
+namespace {
+
+constexpr int kPrepThreads = 256;
+constexpr int kMostParts = 1024;             // partial sums of a matrix, at most
+
+struct PrepParams {
+    const void* G;
+    int64_t ldg, stride_g;
+    int32_t rows, cols, parts;               // as stored; CTAs that sum each matrix
+    int32_t vec;                             // G's rows are 16-byte vectors
+    int32_t np, mp;                          // padded sides, wide
+    double* sums;                            // [batch][parts]
+    float eps;
+    __half *hi, *lo;
+};
+
+// Eight elements of a row as FP32, zeros behind its end.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int32_t col, int32_t cols, bool vec, float (&f)[8]) {
+    constexpr int kPer = 16 / sizeof(T);
+    if (vec && col + 8 <= cols) {
+        #pragma unroll
+        for (int q = 0; q < 8 / kPer; ++q) {
+            const uint4 u = *reinterpret_cast<const uint4*>(row + col + q * kPer);
+            const T* e = reinterpret_cast<const T*>(&u);
+            #pragma unroll
+            for (int i = 0; i < kPer; ++i) f[q * kPer + i] = to_f<T>(e[i]);
+        }
+    } else {
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = col + i < cols ? to_f<T>(row[col + i]) : 0.0f;
+    }
+}
+
+// Sum over the CTA in a fixed order; every thread gets it.
+__device__ __forceinline__ double cta_sum(double v, double* red) {
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double t = 0.0;
+    #pragma unroll
+    for (int w = 0; w < kPrepThreads / 32; ++w) t += red[w];
+    return t;
+}
+
+// Partial sums of squares.  Eight elements in FP32, kept where the sum lies in
+// [2^-90, 2^127) (eight squares below 2^-126 are under 2^-33 of it), else again in
+// FP64; FP64 from there on, as FP64 arithmetic is scarce here.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const PrepParams p) {
+    __shared__ double red[kPrepThreads / 32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
+    const int32_t per_row = (p.cols + 7) >> 3;
+    const int64_t total = static_cast<int64_t>(p.rows) * per_row;
+    double acc = 0.0;
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; q < total;
+         q += static_cast<int64_t>(p.parts) * kPrepThreads) {
+        const uint32_t r = static_cast<uint32_t>(q) / static_cast<uint32_t>(per_row);
+        const int32_t col = static_cast<int32_t>(static_cast<uint32_t>(q) - r * per_row) * 8;
+        float f[8];
+        load8<T>(g + r * p.ldg, col, p.cols, p.vec, f);
+        float s = 0.0f, t = 0.0f;
+        #pragma unroll
+        for (int i = 0; i < 8; i += 2) s = fmaf(f[i], f[i], s), t = fmaf(f[i + 1], f[i + 1], t);
+        s += t;
+        if (s >= 0x1p-90f && s < 0x1p127f) {
+            acc += static_cast<double>(s);
+        } else {
+            #pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                const double d = static_cast<double>(f[i]);
+                acc = fma(d, d, acc);
+            }
+        }
+    }
+    const double s = cta_sum(acc, red);
+    if (threadIdx.x == 0) p.sums[static_cast<int64_t>(blockIdx.y) * p.parts + blockIdx.x] = s;
+}
+
+// kScale / (norm + eps).
+__device__ __forceinline__ double ortho_factor(const PrepParams& p, double* red) {
+    double s = 0.0;
+    for (int32_t i = threadIdx.x; i < p.parts; i += kPrepThreads)
+        s += p.sums[static_cast<int64_t>(blockIdx.y) * p.parts + i];
+    return static_cast<double>(kOrthoScale) / (sqrt(cta_sum(s, red)) + static_cast<double>(p.eps));
+}
+
+// x times the factor, in FP32 where that holds the factor.
+__device__ __forceinline__ float scaled(float x, double f, bool fits) {
+    return fits ? x * static_cast<float>(f) : static_cast<float>(static_cast<double>(x) * f);
+}
+__device__ __forceinline__ bool factor_fits(double f) { return f >= 0x1p-120 && f < 0x1p120; }
+
+__device__ __forceinline__ void store_pair8(const PrepParams& p, int64_t at, const float (&x)[8]) {
+    alignas(16) __half h[8], l[8];
+    #pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        h[i] = __float2half_rn(x[i]);
+        l[i] = __float2half_rn(x[i] - __half2float(h[i]));
+    }
+    *reinterpret_cast<uint4*>(p.hi + at) = *reinterpret_cast<const uint4*>(h);
+    *reinterpret_cast<uint4*>(p.lo + at) = *reinterpret_cast<const uint4*>(l);
+}
+
+// X = G times the factor, as hi + lo, padded with zeros.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) ortho_wide_kernel(const PrepParams p) {
+    __shared__ double red[kPrepThreads / 32];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const double f = ortho_factor(p, red);
+    const bool fits = factor_fits(f);
+    const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
+    const int64_t base = static_cast<int64_t>(blockIdx.y) * p.np * p.mp;
+    const uint32_t per_row = static_cast<uint32_t>(p.mp) >> 3;
+    const int64_t total = static_cast<int64_t>(p.np) * per_row;
+    for (int64_t q = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; q < total;
+         q += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
+        const int32_t r = static_cast<int32_t>(static_cast<uint32_t>(q) / per_row);
+        const int32_t col = static_cast<int32_t>(static_cast<uint32_t>(q) - r * per_row) * 8;
+        float x[8];
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+        if (r < p.rows && col < p.cols) {
+            load8<T>(g + r * p.ldg, col, p.cols, p.vec, x);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = scaled(x[i], f, fits);
+            // behind the row's end a factor that is not finite must not reach the padding
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + i >= p.cols) x[i] = 0.0f;
+        }
+        store_pair8(p, base + q * 8, x);
+    }
+}
+
+// The same, transposed, by tiles of 64 x 64.
+template <typename T>
+__global__ void __launch_bounds__(kPrepThreads) ortho_tall_kernel(const PrepParams p) {
+    __shared__ double red[kPrepThreads / 32];
+    __shared__ float tile[64][65];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const double f = ortho_factor(p, red);
+    const bool fits = factor_fits(f);
+    const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
+    const int64_t base = static_cast<int64_t>(blockIdx.y) * p.np * p.mp;
+    const int32_t across = p.np >> 6, tiles = across * (p.mp >> 6);
+    const int32_t sub = (static_cast<int32_t>(threadIdx.x) & 7) * 8, line = static_cast<int32_t>(threadIdx.x) >> 3;
+    for (int32_t k = blockIdx.x; k < tiles; k += gridDim.x) {
+        const int32_t r0 = k / across * 64, c0 = k % across * 64;       // of G
+        #pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+            const int32_t r = r0 + h + line;
+            float x[8];
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+            if (r < p.rows && c0 + sub < p.cols) load8<T>(g + r * p.ldg, c0 + sub, p.cols, p.vec, x);
+            #pragma unroll
+            for (int i = 0; i < 8; ++i)
+                tile[h + line][sub + i] = r < p.rows && c0 + sub + i < p.cols ? scaled(x[i], f, fits) : 0.0f;
+        }
+        __syncthreads();
+        #pragma unroll
+        for (int h = 0; h < 64; h += 32) {
+            float x[8];
+            #pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = tile[sub + i][h + line];
+            store_pair8(p, base + static_cast<int64_t>(c0 + h + line) * p.mp + r0 + sub, x);
+        }
+        __syncthreads();
+    }
+}
+
+int64_t pad64(int64_t v) { return (v + 63) & ~static_cast<int64_t>(63); }
+int64_t up256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
+
+// Where things lie in the workspace, in bytes.
+struct Layout {
+    int64_t np, mp;
+    int64_t hi[2], lo, a, b, sums, bytes;
+};
+Layout layout(int64_t batch, int64_t rows, int64_t cols) {
+    Layout l;
+    l.np = pad64(rows < cols ? rows : cols);
+    l.mp = pad64(rows < cols ? cols : rows);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up256(bytes);
+        return here;
+    };
+    const int64_t x = batch * l.np * l.mp * 2, s = batch * l.np * l.np * 2;
+    l.hi[0] = take(x);
+    l.hi[1] = take(x);
+    l.lo = take(x);
+    l.a = take(s);
+    l.b = take(s);
+    l.sums = take(batch * kMostParts * 8);
+    l.bytes = at;
+    return l;
+}
+
+// batch matrices of `rows` x `cols` halves, cols a multiple of 64, one behind the
+// other: (64 elements, row, chunk, matrix), boxes of 128 rows by two chunks.
+bool encode_map(const OrthoCall& c, CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols) {
+    const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
+                                static_cast<cuuint64_t>(c.batch)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(cols * 2), 128u, static_cast<cuuint64_t>(rows * cols * 2)};
+    const cuuint32_t box[4] = {64u, 128u, 2u, 1u};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return c.encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stream, cudaLaunchAttribute* attr,
+                          int cluster) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cfg;
+}
+
+template <int MODE>
+cudaError_t launch_pair(const OrthoCall& c, const CUtensorMap& a, const CUtensorMap& b, const OrthoParams& p) {
+    auto kern = ortho_pair_kernel<MODE>;
+    static DeviceLimits limit;
+    cudaError_t e = limit.raise(kOrthoSmem, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoSmem));
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    int64_t pairs = static_cast<int64_t>(p.batch) * p.tiles;
+    if (pairs > c.sms / 2) pairs = c.sms / 2;
+    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(2 * pairs), 1, 1), kOrthoPairThreads, kOrthoSmem, c.stream,
+                                    attr, 2);
+    // no more pairs than can be resident at once: they take the tiles in turns
+    static std::mutex mu;
+    static PerDevice<int> known;
+    int most = 0;
+    {
+        std::lock_guard<std::mutex> g(mu);
+        int* k = known.current();
+        if (k != nullptr) most = *k;
+        if (most == 0) {
+            cudaLaunchConfig_t q = cfg;
+            q.gridDim = dim3(static_cast<unsigned>(c.sms / 2 * 2), 1, 1);
+            q.attrs = &attr[1];
+            q.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&most, kern, &q) != cudaSuccess) {
+                cudaGetLastError();
+                most = 0;
+            }
+            if (k != nullptr) *k = most;
+        }
+    }
+    if (most > 0 && pairs > most) cfg.gridDim = dim3(static_cast<unsigned>(2 * most), 1, 1);
+    return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+}
+
+template <int MODE>
+cudaError_t launch_tile(const OrthoCall& c, const CUtensorMap& a, const CUtensorMap& b, const OrthoParams& p) {
+    auto kern = ortho_tile_kernel<MODE>;
+    static DeviceLimits limit;
+    const cudaError_t e = limit.raise(kOrthoSmem, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoSmem));
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(p.batch * p.tiles * p.splits), 1, 1), kOrthoTileThreads,
+                                    kOrthoSmem, c.stream, attr, p.splits);
+    return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+}
+
+struct Schedule {
+    bool pair;
+    int32_t tiles, tiles_i, splits;
+};
+
+// The faster schedule by a rough count of SM cycles.  A pair's 256 x 256 x 128 block
+// takes 1024 at the tensor core's rate; a single CTA's 128 x 128 x 128 block as
+// long, for it is bound by the 64 KB that it loads.  Beside the blocks a wave
+// costs about 4000 cycles (fill, drain, epilogue), the exchange of a split 2000.
+Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols, int64_t k_blocks) {
+    auto count = [&](int64_t side, int32_t& along) {
+        const int64_t i = (rows + side - 1) / side, j = (cols + side - 1) / side;
+        along = static_cast<int32_t>(i);
+        return symmetric ? i * (i + 1) / 2 : i * j;
+    };
+    Schedule s;
+    const int64_t big = count(256, s.tiles_i) * c.batch;
+    const int64_t pairs = c.sms / 2;
+    int64_t best = (big + pairs - 1) / pairs * (k_blocks * 1024) + 4000;
+    s.pair = true;
+    s.splits = 1;
+    int32_t along;
+    const int64_t small = count(128, along) * c.batch;
+    for (int32_t n = 1; n <= 8 && n <= k_blocks; n *= 2) {
+        const int64_t waves = (small * n + c.sms - 1) / c.sms;
+        const int64_t cost = waves * ((k_blocks + n - 1) / n * 1024 + 4000 + (n > 1 ? 2000 : 0));
+        if (cost < best) {
+            best = cost;
+            s.pair = false;
+            s.splits = n;
+        }
+    }
+    if (!s.pair) s.tiles_i = along;
+    s.tiles = static_cast<int32_t>((s.pair ? big : small) / c.batch);
+    return s;
+}
+
+template <int MODE>
+cudaError_t product(const OrthoCall& c, const Schedule& s, const CUtensorMap& a, const CUtensorMap& b,
+                    OrthoParams p) {
+    p.tiles = s.tiles;
+    p.tiles_i = s.tiles_i;
+    p.splits = s.splits;
+    p.log_width = 7;
+    for (int32_t n = s.splits; n > 1; n >>= 1) --p.log_width;
+    return s.pair ? launch_pair<MODE>(c, a, b, p) : launch_tile<MODE>(c, a, b, p);
+}
+
+template <typename T>
+cudaError_t prepare(const OrthoCall& c, PrepParams p) {
+    cudaLaunchAttribute attr[2];
+    const int64_t share = c.sms * 4 / c.batch > 1 ? c.sms * 4 / c.batch : 1;    // CTAs of a matrix
+    const int64_t pieces = static_cast<int64_t>(p.rows) * ((p.cols + 7) / 8);
+    int64_t parts = (pieces + 2 * kPrepThreads - 1) / (2 * kPrepThreads);
+    if (parts > share) parts = share;
+    if (parts > kMostParts) parts = kMostParts;
+    p.parts = static_cast<int32_t>(parts);
+    const unsigned batch = static_cast<unsigned>(c.batch);
+    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(parts), batch, 1), kPrepThreads, 0, c.stream, attr, 1);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, ortho_norm_kernel<T>, p);
+    if (e != cudaSuccess) return e;
+    if (p.rows > p.cols) {
+        int64_t grid = static_cast<int64_t>(p.np / 64) * (p.mp / 64);
+        if (grid > share) grid = share;
+        cfg.gridDim = dim3(static_cast<unsigned>(grid), batch, 1);
+        return cudaLaunchKernelEx(&cfg, ortho_tall_kernel<T>, p);
+    }
+    int64_t grid = (static_cast<int64_t>(p.np) * (p.mp / 8) + 2 * kPrepThreads - 1) / (2 * kPrepThreads);
+    if (grid > share) grid = share;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid), batch, 1);
+    return cudaLaunchKernelEx(&cfg, ortho_wide_kernel<T>, p);
+}
+
+cudaError_t run(const OrthoCall& c) {
+    const Layout l = layout(c.batch, c.rows, c.cols);
+    __half* hi[2] = {reinterpret_cast<__half*>(c.ws + l.hi[0]), reinterpret_cast<__half*>(c.ws + l.hi[1])};
+    __half* lo = reinterpret_cast<__half*>(c.ws + l.lo);
+    __half* a = reinterpret_cast<__half*>(c.ws + l.a);
+    __half* b = reinterpret_cast<__half*>(c.ws + l.b);
+    const bool tall = c.rows > c.cols;
+    const int64_t es = c.g_dtype == GEMM_F32 ? 4 : 2;
+    auto vector = [&](const void* q, int64_t ld, int64_t stride, int64_t bytes) {
+        return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ld * bytes % 16 == 0 &&
+               (c.batch == 1 || stride * bytes % 16 == 0);
+    };
+
+    PrepParams q = {};
+    q.G = c.G, q.ldg = c.ldg, q.stride_g = c.stride_g;
+    q.rows = static_cast<int32_t>(c.rows), q.cols = static_cast<int32_t>(c.cols);
+    q.vec = vector(c.G, c.ldg, c.stride_g, es);
+    q.np = static_cast<int32_t>(l.np), q.mp = static_cast<int32_t>(l.mp);
+    q.sums = reinterpret_cast<double*>(c.ws + l.sums);
+    q.eps = c.opt->eps;
+    q.hi = hi[0], q.lo = lo;
+    cudaError_t e = c.g_dtype == GEMM_F32    ? prepare<float>(c, q)
+                    : c.g_dtype == GEMM_BF16 ? prepare<__nv_bfloat16>(c, q)
+                                             : prepare<__half>(c, q);
+    if (e != cudaSuccess) return e;
+
+    CUtensorMap map_x[2], map_a, map_b;
+    bool ok = encode_map(c, &map_x[0], hi[0], l.np, l.mp) && encode_map(c, &map_a, a, l.np, l.np) &&
+              encode_map(c, &map_b, b, l.np, l.np);
+    if (c.opt->steps > 1) ok = ok && encode_map(c, &map_x[1], hi[1], l.np, l.mp);
+    if (!ok) return cudaErrorInvalidValue;
+
+    OrthoParams p = {};
+    p.batch = static_cast<int32_t>(c.batch);
+    p.np = q.np, p.mp = q.mp;
+    p.n = static_cast<int32_t>(tall ? c.cols : c.rows), p.m = static_cast<int32_t>(tall ? c.rows : c.cols);
+    p.tall = tall;
+    p.O = static_cast<__nv_bfloat16*>(c.O), p.ldo = c.ldo, p.stride_o = c.stride_o;
+    p.vec = vector(c.O, c.ldo, c.stride_o, 2);
+    p.scale = c.opt->scale;
+    p.err = c.err, p.wait_limit_ns = c.wait_limit_ns;
+    const int32_t kx = static_cast<int32_t>((l.mp + 127) / 128), kn = static_cast<int32_t>((l.np + 127) / 128);
+    const Schedule gram = schedule(c, true, l.np, l.np, kx), poly = schedule(c, true, l.np, l.np, kn),
+                   step = schedule(c, false, l.np, l.mp, kn);
+    for (int32_t i = 0; i < c.opt->steps; ++i) {
+        const float* abc = c.opt->coefficients + 3 * i;
+        p.a = abc[0], p.b = abc[1], p.c = abc[2];
+        const int from = i & 1;
+        p.debug_flags = i == 0 ? c.debug_flags : 0;
+        p.k_blocks = kx;
+        p.out = a;
+        e = product<kGram>(c, gram, map_x[from], map_x[from], p);
+        if (e != cudaSuccess) return e;
+        p.debug_flags = 0;
+        p.k_blocks = kn;
+        p.ah = a, p.out = b;
+        e = product<kPoly>(c, poly, map_a, map_a, p);
+        if (e != cudaSuccess) return e;
+        p.hi = hi[from], p.lo = lo, p.hi_out = hi[from ^ 1];
+        e = i + 1 < c.opt->steps ? product<kStep>(c, step, map_b, map_x[from], p)
+                                 : product<kLast>(c, step, map_b, map_x[from], p);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+int64_t ortho_bytes(int64_t batch, int64_t rows, int64_t cols) { return layout(batch, rows, cols).bytes; }
+
+gemm_status_t ortho_enqueue(const OrthoCall& c) {
+    if (run(c) != cudaSuccess) {
+        cudaGetLastError();
+        return GEMM_ERR_LAUNCH;
+    }
+    return GEMM_OK;
+}
+
+}  // namespace gemm103
