@@ -100,11 +100,24 @@ __device__ __forceinline__ double ortho_factor(const PrepParams& p, double* red)
     return static_cast<double>(kOrthoScale) / (sqrt(cta_sum(s, red)) + static_cast<double>(p.eps));
 }
 
-// x times the factor, in FP32 where that holds the factor.
-__device__ __forceinline__ float scaled(float x, double f, bool fits) {
-    return fits ? x * static_cast<float>(f) : static_cast<float>(static_cast<double>(x) * f);
+// x times the factor as x f g: the factor in FP32, or where that does not hold it
+// the two halves of its exponent range.  (A product in FP64 for every element, even
+// one that is not taken, made this pass 353 us for 59M elements, of 75.)
+struct Factor {
+    float f, g;
+};
+__device__ __forceinline__ Factor split_factor(double f) {
+    Factor r;
+    const bool fits = !(f >= 0x1p120) && !(f < 0x1p-120);       // (NaN and 0 go on as they are)
+    if (fits || f == 0.0) {
+        r.f = static_cast<float>(f), r.g = 1.0f;
+    } else {
+        const double h = f >= 1.0 ? 0x1p100 : 0x1p-100;
+        r.f = static_cast<float>(f / h), r.g = static_cast<float>(h);
+    }
+    return r;
 }
-__device__ __forceinline__ bool factor_fits(double f) { return f >= 0x1p-120 && f < 0x1p120; }
+__device__ __forceinline__ float scaled(float x, const Factor& f) { return x * f.f * f.g; }
 
 __device__ __forceinline__ void store_pair8(const PrepParams& p, int64_t at, const float (&x)[8]) {
     alignas(16) __half h[8], l[8];
@@ -123,8 +136,7 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_wide_kernel(const PrepPara
     __shared__ double red[kPrepThreads / 32];
     grid_dependency_wait();
     grid_dependents_launch();
-    const double f = ortho_factor(p, red);
-    const bool fits = factor_fits(f);
+    const Factor f = split_factor(ortho_factor(p, red));
     const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
     const int64_t base = static_cast<int64_t>(blockIdx.y) * p.np * p.mp;
     const uint32_t per_row = static_cast<uint32_t>(p.mp) >> 3;
@@ -139,7 +151,7 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_wide_kernel(const PrepPara
         if (r < p.rows && col < p.cols) {
             load8<T>(g + r * p.ldg, col, p.cols, p.vec, x);
             #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = scaled(x[i], f, fits);
+            for (int i = 0; i < 8; ++i) x[i] = scaled(x[i], f);
             // behind the row's end a factor that is not finite must not reach the padding
             #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -156,8 +168,7 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_tall_kernel(const PrepPara
     __shared__ float tile[64][65];
     grid_dependency_wait();
     grid_dependents_launch();
-    const double f = ortho_factor(p, red);
-    const bool fits = factor_fits(f);
+    const Factor f = split_factor(ortho_factor(p, red));
     const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
     const int64_t base = static_cast<int64_t>(blockIdx.y) * p.np * p.mp;
     const int32_t across = p.np >> 6, tiles = across * (p.mp >> 6);
@@ -173,7 +184,7 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_tall_kernel(const PrepPara
             if (r < p.rows && c0 + sub < p.cols) load8<T>(g + r * p.ldg, c0 + sub, p.cols, p.vec, x);
             #pragma unroll
             for (int i = 0; i < 8; ++i)
-                tile[h + line][sub + i] = r < p.rows && c0 + sub + i < p.cols ? scaled(x[i], f, fits) : 0.0f;
+                tile[h + line][sub + i] = r < p.rows && c0 + sub + i < p.cols ? scaled(x[i], f) : 0.0f;
         }
         __syncthreads();
         #pragma unroll
@@ -251,14 +262,14 @@ template <int MODE>
 cudaError_t launch_pair(const OrthoCall& c, const CUtensorMap& a, const CUtensorMap& b, const OrthoParams& p) {
     auto kern = ortho_pair_kernel<MODE>;
     static DeviceLimits limit;
-    cudaError_t e = limit.raise(kOrthoSmem, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoSmem));
+    cudaError_t e = limit.raise(kOrthoPairSmem, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoPairSmem));
     });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     int64_t pairs = static_cast<int64_t>(p.batch) * p.tiles;
     if (pairs > c.sms / 2) pairs = c.sms / 2;
-    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(2 * pairs), 1, 1), kOrthoPairThreads, kOrthoSmem, c.stream,
+    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(2 * pairs), 1, 1), kOrthoPairThreads, kOrthoPairSmem, c.stream,
                                     attr, 2);
     // no more pairs than can be resident at once: they take the tiles in turns
     static std::mutex mu;
@@ -288,13 +299,13 @@ template <int MODE>
 cudaError_t launch_tile(const OrthoCall& c, const CUtensorMap& a, const CUtensorMap& b, const OrthoParams& p) {
     auto kern = ortho_tile_kernel<MODE>;
     static DeviceLimits limit;
-    const cudaError_t e = limit.raise(kOrthoSmem, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoSmem));
+    const cudaError_t e = limit.raise(kOrthoTileSmem, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoTileSmem));
     });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(p.batch * p.tiles * p.splits), 1, 1), kOrthoTileThreads,
-                                    kOrthoSmem, c.stream, attr, p.splits);
+                                    kOrthoTileSmem, c.stream, attr, p.splits);
     return cudaLaunchKernelEx(&cfg, kern, a, b, p);
 }
 
@@ -304,9 +315,9 @@ struct Schedule {
 };
 
 // The faster schedule by a rough count of SM cycles.  A pair's 256 x 256 x 128 block
-// takes 1024 at the tensor core's rate; a single CTA's 128 x 128 x 128 block as
-// long, for it is bound by the 64 KB that it loads.  Beside the blocks a wave
-// costs about 4000 cycles (fill, drain, epilogue), the exchange of a split 2000.
+// takes 1024 at the tensor core's rate, a tile's epilogue 9000 beside the next
+// tile's blocks.  A single CTA's 128 x 128 x 128 block takes as long, for it is bound
+// by the 64 KB that it loads; its epilogue 5000, the exchange of a split 2000.
 Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols, int64_t k_blocks) {
     auto count = [&](int64_t side, int32_t& along) {
         const int64_t i = (rows + side - 1) / side, j = (cols + side - 1) / side;
@@ -316,14 +327,14 @@ Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols
     Schedule s;
     const int64_t big = count(256, s.tiles_i) * c.batch;
     const int64_t pairs = c.sms / 2;
-    int64_t best = (big + pairs - 1) / pairs * (k_blocks * 1024) + 4000;
+    int64_t best = (big + pairs - 1) / pairs * (k_blocks * 1024 > 9000 ? k_blocks * 1024 : 9000) + 9000;
     s.pair = true;
     s.splits = 1;
     int32_t along;
     const int64_t small = count(128, along) * c.batch;
     for (int32_t n = 1; n <= 8 && n <= k_blocks; n *= 2) {
         const int64_t waves = (small * n + c.sms - 1) / c.sms;
-        const int64_t cost = waves * ((k_blocks + n - 1) / n * 1024 + 4000 + (n > 1 ? 2000 : 0));
+        const int64_t cost = waves * ((k_blocks + n - 1) / n * 1024 + 5000 + (n > 1 ? 2000 : 0));
         if (cost < best) {
             best = cost;
             s.pair = false;

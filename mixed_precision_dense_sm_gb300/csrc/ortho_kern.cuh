@@ -36,7 +36,9 @@ constexpr float kOrthoScale = 2048.0f;
 constexpr int kOrthoStages = 3;
 constexpr uint32_t kOrthoBox = 32768;                // 128 rows x 128 bytes x 2 chunks
 constexpr uint32_t kOrthoStage = 2 * kOrthoBox;      // A's and B's
-constexpr uint32_t kOrthoSmem = kOrthoStages * kOrthoStage + 1024 + 256;
+constexpr uint32_t kOrthoTurn = 32768;                // pairs: 4 KB per epilogue warp behind the stages
+constexpr uint32_t kOrthoTileSmem = kOrthoStages * kOrthoStage + 1024 + 256;
+constexpr uint32_t kOrthoPairSmem = kOrthoTileSmem + kOrthoTurn;
 constexpr int kOrthoPairThreads = 320;               // warp 0 TMA, 1 MMA, 2-9 epilogue
 constexpr int kOrthoTileThreads = 192;               // warp 0 TMA, 1 MMA, 2-5 epilogue
 
@@ -93,110 +95,212 @@ __device__ __forceinline__ void half8(uint4 u, float* f) {
         f[2 * i + 1] = v.y;
     }
 }
+__device__ __forceinline__ uint4 pack8(const float* f) {
+    uint32_t w[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
 
-// What the epilogue reads of 16 columns: A (kPoly), or hi and lo.
+// The epilogue works on 8 columns of a row at a time, 8 rows by 32 columns a warp, four
+// neighbouring lanes a row: eight lanes, which the load/store unit takes at once, touch
+// two lines.  (With a row per lane, as the accumulator comes, or any other order of
+// the lanes, eight: 33 wavefronts an access for 8, and a tile's epilogue was longer
+// than its products up to a K of 2500.)  The sums take a turn through shared memory to
+// get there.
+
+// What it reads: A (kPoly), or hi and lo.
 template <int MODE>
 struct OrthoIn {
-    uint4 u[MODE == kGram ? 1 : MODE == kPoly ? 2 : 4];
+    uint4 x, y;
 };
+// Whether a row and a column lie in the padded matrix: with sides of multiples of 64,
+// whole blocks of 32 do or do not.
 template <int MODE>
 __device__ __forceinline__ bool ortho_inside(const OrthoParams& p, int32_t row, int32_t col) {
     return row < p.np && col < (MODE == kGram || MODE == kPoly ? p.np : p.mp);
 }
 template <int MODE>
 __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_t b, int32_t row, int32_t col) {
-    OrthoIn<MODE> in = {};
+    OrthoIn<MODE> in;
+    in.x = in.y = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (MODE == kPoly) {
-        const uint4* s = reinterpret_cast<const uint4*>(p.ah + (static_cast<int64_t>(b) * p.np + row) * p.np + col);
-        in.u[0] = s[0], in.u[1] = s[1];
+        in.x = *reinterpret_cast<const uint4*>(p.ah + (static_cast<int64_t>(b) * p.np + row) * p.np + col);
     } else if constexpr (MODE != kGram) {
         const int64_t at = (static_cast<int64_t>(b) * p.np + row) * p.mp + col;
-        const uint4* h = reinterpret_cast<const uint4*>(p.hi + at);
-        const uint4* l = reinterpret_cast<const uint4*>(p.lo + at);
-        in.u[0] = h[0], in.u[1] = h[1], in.u[2] = l[0], in.u[3] = l[1];
+        in.x = *reinterpret_cast<const uint4*>(p.hi + at);
+        in.y = *reinterpret_cast<const uint4*>(p.lo + at);
     }
     return in;
 }
 
-// 16 columns of one row: sums v (of scaled products) to the result, and out.
-// `mirror`: also to the transposed place.
+// Sums v (of scaled products) of 8 columns to the result, in v, and out to where it
+// is stored by rows.
 template <int MODE>
 __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t b, int32_t row, int32_t col,
-                                             const OrthoIn<MODE>& in, float (&v)[16], bool mirror) {
+                                             const OrthoIn<MODE>& in, float (&v)[8]) {
     constexpr float kDown = 1.0f / kOrthoScale;
     if constexpr (MODE == kGram || MODE == kPoly) {
         if constexpr (MODE == kPoly) {
-            float x[16];
-            half8(in.u[0], x);
-            half8(in.u[1], x + 8);
+            float x[8];
+            half8(in.x, x);
             const float c = p.c * kDown;
             #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = fmaf(p.b, x[i], c * v[i]);
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(p.b, x[i], c * v[i]);
         } else {
             #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] *= kDown;
+            for (int i = 0; i < 8; ++i) v[i] *= kDown;
         }
-        __half* base = p.out + static_cast<int64_t>(b) * p.np * p.np;
-        alignas(16) __half h[16];
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) h[i] = __float2half_rn(v[i]);
-        uint4* d = reinterpret_cast<uint4*>(base + static_cast<int64_t>(row) * p.np + col);
-        d[0] = reinterpret_cast<const uint4*>(h)[0];
-        d[1] = reinterpret_cast<const uint4*>(h)[1];
-        if (mirror) {
-            // (the lanes' rows are neighbours: 64 contiguous bytes per store)
-            __half* t = base + static_cast<int64_t>(col) * p.np + row;
-            #pragma unroll
-            for (int i = 0; i < 16; ++i) t[static_cast<int64_t>(i) * p.np] = h[i];
-        }
+        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * p.np + row) * p.np + col) = pack8(v);
     } else {
-        float x[16], y[8];
-        half8(in.u[0], x);
-        half8(in.u[1], x + 8);
+        float x[8], y[8];
+        half8(in.x, x);
+        half8(in.y, y);
         #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            half8(in.u[2 + q], y);
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) x[8 * q + i] += y[i];
-        }
-        #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = fmaf(p.a, x[i], v[i] * kDown);
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(p.a, x[i] + y[i], v[i] * kDown);
         if constexpr (MODE == kStep) {
-            alignas(16) __half h[16], l[16];
+            const uint4 h = pack8(v);
+            half8(h, x);
             #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                h[i] = __float2half_rn(v[i]);
-                l[i] = __float2half_rn(v[i] - __half2float(h[i]));
-            }
+            for (int i = 0; i < 8; ++i) y[i] = v[i] - x[i];
             const int64_t at = (static_cast<int64_t>(b) * p.np + row) * p.mp + col;
-            uint4* d = reinterpret_cast<uint4*>(p.hi_out + at);
-            d[0] = reinterpret_cast<const uint4*>(h)[0];
-            d[1] = reinterpret_cast<const uint4*>(h)[1];
-            d = reinterpret_cast<uint4*>(p.lo + at);
-            d[0] = reinterpret_cast<const uint4*>(l)[0];
-            d[1] = reinterpret_cast<const uint4*>(l)[1];
+            *reinterpret_cast<uint4*>(p.hi_out + at) = h;
+            *reinterpret_cast<uint4*>(p.lo + at) = pack8(y);
         } else {
-            if (row >= p.n) return;
             const float s = p.scale * kDown;
-            alignas(16) __nv_bfloat16 o[16];
             #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float2bfloat16_rn(v[i] * s);
-            __nv_bfloat16* base = p.O + b * p.stride_o;
-            if (p.tall) {
-                #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (col + i < p.m) base[(col + i) * p.ldo + row] = o[i];
-            } else if (p.vec && col + 16 <= p.m) {
-                uint4* d = reinterpret_cast<uint4*>(base + row * p.ldo + col);
-                d[0] = reinterpret_cast<const uint4*>(o)[0];
-                d[1] = reinterpret_cast<const uint4*>(o)[1];
-            } else {
-                #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (col + i < p.m) base[row * p.ldo + col + i] = o[i];
+            for (int i = 0; i < 8; ++i) v[i] *= s;
+            if (!p.tall && p.vec && row < p.n && col < p.m) {
+                __nv_bfloat16* d = p.O + b * p.stride_o + row * p.ldo + col;
+                if (col + 8 <= p.m) {
+                    uint32_t w[4];
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    #pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (col + i < p.m) d[i] = __float2bfloat16_rn(v[i]);
+                }
             }
         }
     }
+}
+
+// Whether the results are stored in another way too, or only: mirrored, transposed,
+// or as rows that are not vectors.
+template <int MODE>
+__device__ __forceinline__ bool ortho_again(const OrthoParams& p, const OrthoTile& t) {
+    if constexpr (MODE == kGram || MODE == kPoly) return t.i != t.j;
+    else return MODE == kLast && (p.tall || !p.vec);
+}
+// Four columns of one row to the result's transpose (lanes: neighbouring rows).
+template <int MODE>
+__device__ __forceinline__ void ortho_mirror(const OrthoParams& p, int32_t b, int32_t row, int32_t col, float4 v) {
+    if constexpr (MODE == kLast) {
+        if (row >= p.n) return;
+        __nv_bfloat16* d = p.O + b * p.stride_o + col * p.ldo + row;
+        if (col < p.m) d[0] = __float2bfloat16_rn(v.x);
+        if (col + 1 < p.m) d[p.ldo] = __float2bfloat16_rn(v.y);
+        if (col + 2 < p.m) d[2 * p.ldo] = __float2bfloat16_rn(v.z);
+        if (col + 3 < p.m) d[3 * p.ldo] = __float2bfloat16_rn(v.w);
+    } else {
+        __half* d = p.out + (static_cast<int64_t>(b) * p.np + col) * p.np + row;
+        d[0] = __float2half_rn(v.x);
+        d[p.np] = __float2half_rn(v.y);
+        d[2 * p.np] = __float2half_rn(v.z);
+        d[3 * p.np] = __float2half_rn(v.w);
+    }
+}
+
+// A warp's 32 rows (the first is row0) and 32 columns: `r` one row per lane, from
+// tensor memory; `in` four of eight rows.  `buf` is 4 KB of its own: row r's float4 u
+// lies at u ^ (r & 7), which no access of 8 lanes meets twice in a bank.
+template <int MODE>
+__device__ __forceinline__ void ortho_block(const OrthoParams& p, const OrthoTile& t, int32_t row0, int32_t col0,
+                                            const uint32_t (&r)[32], const OrthoIn<MODE> (&in)[4], float4* buf) {
+    const int lane = threadIdx.x & 31, l7 = lane & 7, g = lane & 3, line = lane >> 2;
+    __syncwarp();
+    #pragma unroll
+    for (int u = 0; u < 8; ++u)
+        buf[lane * 8 + (u ^ l7)] = make_float4(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1]),
+                                               __uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3]));
+    __syncwarp();
+    const bool again = ortho_again<MODE>(p, t);
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float4* at = buf + (q * 8 + line) * 8;
+        const float4 a = at[(2 * g) ^ line], b = at[(2 * g + 1) ^ line];
+        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        ortho_finish<MODE>(p, t.b, row0 + q * 8 + line, col0 + g * 8, in[q], v);
+        if (again) {
+            at[(2 * g) ^ line] = make_float4(v[0], v[1], v[2], v[3]);
+            at[(2 * g + 1) ^ line] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    if (!again) return;
+    __syncwarp();
+    if (MODE == kLast && !p.tall) {
+        // rows that are not vectors: a row at a time, one element per lane
+        if constexpr (MODE == kLast) {
+            const float* f = reinterpret_cast<const float*>(buf);
+            const int32_t col = col0 + lane;
+            __nv_bfloat16* d = p.O + t.b * p.stride_o + col;
+            #pragma unroll 4
+            for (int k = 0; k < 32; ++k)
+                if (row0 + k < p.n && col < p.m)
+                    d[(row0 + k) * p.ldo] = __float2bfloat16_rn(f[k * 32 + (((lane >> 2) ^ (k & 7)) << 2) + (lane & 3)]);
+        }
+    } else {
+        #pragma unroll 2
+        for (int u = 0; u < 8; ++u) ortho_mirror<MODE>(p, t.b, row0 + lane, col0 + 4 * u, buf[lane * 8 + (u ^ l7)]);
+    }
+}
+
+// The inputs of such a block.
+template <int MODE>
+__device__ __forceinline__ void ortho_read_block(const OrthoParams& p, int32_t b, int32_t row0, int32_t col0,
+                                                 OrthoIn<MODE> (&in)[4]) {
+    const int lane = threadIdx.x & 31;
+    #pragma unroll
+    for (int q = 0; q < 4; ++q) in[q] = ortho_read<MODE>(p, b, row0 + q * 8 + (lane >> 2), col0 + (lane & 3) * 8);
+}
+
+// A warp's 32 rows by up to 128 columns of a tile: `taddr` their accumulator; `in0`
+// and `in1` the inputs of the first two blocks, on their way since before the sums
+// were there.  Those of the next two follow when their registers are free (one at a
+// time, handed on, cost the latency of a load per block: 5 us of 10 a tile).  A loop,
+// and its body short: code that runs once per tile is bound by its fetching.
+template <int MODE>
+__device__ __forceinline__ void ortho_blocks(const OrthoParams& p, const OrthoTile& t, int32_t row0, int32_t col0,
+                                             int32_t blocks, uint32_t taddr, OrthoIn<MODE> (&in0)[4],
+                                             OrthoIn<MODE> (&in1)[4], float4* buf) {
+    #pragma unroll 1
+    for (int32_t c = 0; c < blocks; c += 2) {
+        uint32_t r[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(taddr + c * 32, r);
+        tmem_ld_wait();
+        ortho_block<MODE>(p, t, row0, col0 + c * 32, r, in0, buf);
+        if (c + 2 < blocks) ortho_read_block<MODE>(p, t.b, row0, col0 + c * 32 + 64, in0);
+        __syncwarp();
+        tmem_ld_32x32b_x32(taddr + c * 32 + 32, r);
+        tmem_ld_wait();
+        ortho_block<MODE>(p, t, row0, col0 + c * 32 + 32, r, in1, buf);
+        if (c + 3 < blocks) ortho_read_block<MODE>(p, t.b, row0, col0 + c * 32 + 96, in1);
+    }
+}
+// Blocks of 32 columns (an even number: sides are multiples of 64) from col0 on.
+template <int MODE>
+__device__ __forceinline__ int32_t ortho_block_count(const OrthoParams& p, int32_t row0, int32_t col0) {
+    const int32_t cols = MODE == kGram || MODE == kPoly ? p.np : p.mp;
+    return row0 >= p.np || col0 >= cols ? 0 : cols - col0 < 128 ? (cols - col0) >> 5 : 4;
 }
 
 __device__ __forceinline__ void ortho_give_up(const OrthoParams& p, volatile int* abort_flag) {
@@ -247,11 +351,10 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
     ortho_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ OrthoParams p) {
     constexpr bool kMN = MODE == kStep || MODE == kLast;
-    constexpr bool kSym = MODE == kGram || MODE == kPoly;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOrthoStages * kOrthoStage);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOrthoStages * kOrthoStage + kOrthoTurn);
     uint64_t* empty = full + kOrthoStages;
     uint64_t* acc_full = empty + kOrthoStages;
     uint64_t* acc_empty = acc_full + 2;
@@ -348,34 +451,25 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
+        float4* turn = reinterpret_cast<float4*>(smem + kOrthoStages * kOrthoStage) + (warp - 2) * 256;
         uint32_t acc_i = 0;
         for (int32_t item = mine; item < items; item += pairs, ++acc_i) {
             const OrthoTile t = ortho_tile<MODE>(p, item);
             const uint32_t buf = acc_i & 1u;
-            const int32_t row = t.i * 256 + static_cast<int32_t>(rank) * 128 + quarter * 32 + lane;
-            if (!ortho_wait(&acc_full[buf], (acc_i >> 1) & 1u, &abort_flag, p)) break;
-            tc_fence_after_sync();
-            const uint32_t taddr = tmem + buf * 256u + (static_cast<uint32_t>(quarter * 32) << 16);
-            #pragma unroll 1
-            for (int c = half * 128; c < half * 128 + 128; c += 32) {
-                __syncwarp();
-                const int32_t col = t.j * 256 + c;
-                OrthoIn<MODE> in[2];
-                #pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (ortho_inside<MODE>(p, row, col + 16 * q)) in[q] = ortho_read<MODE>(p, t.b, row, col + 16 * q);
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(taddr + c, r);
-                tmem_ld_wait();
-                #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    if (!ortho_inside<MODE>(p, row, col + 16 * q)) continue;
-                    float v[16];
-                    #pragma unroll
-                    for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[16 * q + k]);
-                    ortho_finish<MODE>(p, t.b, row, col + 16 * q, in[q], v, kSym && t.i != t.j);
-                }
+            const int32_t row0 = t.i * 256 + static_cast<int32_t>(rank) * 128 + quarter * 32;
+            const int32_t col0 = t.j * 256 + half * 128;
+            const int32_t blocks = ortho_block_count<MODE>(p, row0, col0);
+            OrthoIn<MODE> in0[4], in1[4];
+            if (blocks > 0) {
+                ortho_read_block<MODE>(p, t.b, row0, col0, in0);
+                ortho_read_block<MODE>(p, t.b, row0, col0 + 32, in1);
             }
+            if (!ortho_wait(&acc_full[buf], (acc_i >> 1) & 1u, &abort_flag, p)) break;
+            __syncwarp();
+            tc_fence_after_sync();
+            ortho_blocks<MODE>(p, t, row0, col0, blocks,
+                               tmem + buf * 256u + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128u, in0, in1,
+                               turn);
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&acc_empty[buf]), 0));
@@ -395,7 +489,6 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     ortho_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ OrthoParams p) {
     constexpr bool kMN = MODE == kStep || MODE == kLast;
-    constexpr bool kSym = MODE == kGram || MODE == kPoly;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -434,6 +527,34 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     grid_dependency_wait();
     grid_dependents_launch();
 
+    // The epilogue's place: 32 rows and the first two blocks of 32 columns, or with K
+    // split the first four units of 8 columns of a row among this CTA's columns.  Its
+    // inputs are on their way while the products run.
+    const int quarter = warp & 3;
+    const int32_t row0 = t.i * 128 + quarter * 32, log8 = p.log_width - 3;
+    const int32_t blocks = S > 1 ? 0 : ortho_block_count<MODE>(p, row0, t.j * 128);
+    const int32_t col_s = t.j * 128 + (static_cast<int32_t>(rank) << p.log_width);
+    auto unit = [&](int32_t k, int32_t& rr, int32_t& g) {       // (by rows)
+        const int32_t e = k * 128 + static_cast<int32_t>(threadIdx.x) - 64;
+        g = e & ((1 << log8) - 1);
+        rr = e >> log8;
+        return k < 1 << log8 && ortho_inside<MODE>(p, t.i * 128 + rr, col_s + g * 8);
+    };
+    OrthoIn<MODE> in0[4], in1[4];
+    if (warp >= 2) {
+        if (blocks > 0) {
+            ortho_read_block<MODE>(p, t.b, row0, t.j * 128, in0);
+            ortho_read_block<MODE>(p, t.b, row0, t.j * 128 + 32, in1);
+        }
+        if (S > 1) {
+            #pragma unroll
+            for (int32_t k = 0; k < 4; ++k) {
+                int32_t rr, g;
+                if (unit(k, rr, g)) in0[k] = ortho_read<MODE>(p, t.b, t.i * 128 + rr, col_s + g * 8);
+            }
+        }
+    }
+
     if (warp == 0) {
         if (lane == 0) {
             const uint64_t keep = l2_policy_evict_last();
@@ -471,18 +592,21 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         }
     }
     // Every CTA of the cluster is through with its stages: their memory becomes the
-    // exchange buffer [source][four columns of mine][row] of float4s.
+    // exchange buffer [source][four columns of mine][row] of float4s, the rows of
+    // different columns turned against each other, so that the units of eight lanes
+    // meet in no bank.
     tc_fence_before_sync();
     __syncthreads();
     if (S > 1) cluster_sync_all();
     tc_fence_after_sync();
-    const int quarter = warp & 3;
     const int r_in = quarter * 32 + lane;
-    const int32_t row = t.i * 128 + r_in;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     if (S > 1) {
         const int32_t log4 = p.log_width - 2;                // log2 of the fours of columns each CTA finishes
         float4* xbuf = reinterpret_cast<float4*>(smem);
+        auto at_of = [&](int32_t src, int32_t c4, int32_t rr) {
+            return xbuf + ((src << log4) + c4) * 128 + (rr ^ (((c4 >> 1) << (3 - log8)) & 7));
+        };
         if (warp >= 2) {
             const bool any = kb1 > kb0;                      // (a CTA without a K block adds zeros)
             #pragma unroll 1
@@ -494,7 +618,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                 for (int j = 0; j < 32; j += 4) {
                     const int32_t c4 = (c + j) >> 2;
                     const uint32_t q = static_cast<uint32_t>(c4 >> log4);
-                    float4* at = xbuf + ((static_cast<int32_t>(rank) << log4) + (c4 & ((1 << log4) - 1))) * 128 + r_in;
+                    float4* at = at_of(static_cast<int32_t>(rank), c4 & ((1 << log4) - 1), r_in);
                     const float4 v = any ? make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
                                                        __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]))
                                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -509,48 +633,59 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         }
         __syncthreads();
         cluster_sync_all();
-        if (warp >= 2 && !abort_flag) {
-            const int32_t col0 = t.j * 128 + (static_cast<int32_t>(rank) << p.log_width);
-            #pragma unroll 1
-            for (int32_t u = 0; u < (1 << p.log_width) / 16; ++u) {
-                const int32_t col = col0 + u * 16;
-                if (!ortho_inside<MODE>(p, row, col)) continue;
-                const OrthoIn<MODE> in = ortho_read<MODE>(p, t.b, row, col);
-                float v[16];
-                #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-                #pragma unroll 2
-                for (int32_t s = 0; s < S; ++s) {
+        if (!abort_flag) {
+            const bool again = ortho_again<MODE>(p, t);
+            if (warp >= 2) {
+                #pragma unroll 1
+                for (int32_t k0 = 0; k0 < 1 << log8; k0 += 4) {
                     #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float4 f = xbuf[((s << log4) + u * 4 + q) * 128 + r_in];
-                        v[4 * q] += f.x, v[4 * q + 1] += f.y, v[4 * q + 2] += f.z, v[4 * q + 3] += f.w;
+                    for (int32_t k = 0; k < 4; ++k) {
+                        int32_t rr, g;
+                        if (!unit(k0 + k, rr, g)) continue;
+                        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                        #pragma unroll 2
+                        for (int32_t s = 0; s < S; ++s) {
+                            const float4 a = *at_of(s, 2 * g, rr), b = *at_of(s, 2 * g + 1, rr);
+                            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+                            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+                        }
+                        ortho_finish<MODE>(p, t.b, t.i * 128 + rr, col_s + g * 8, in0[k], v);
+                        if (again) {
+                            // in the place of the first source's sums, which this thread alone reads
+                            *at_of(0, 2 * g, rr) = make_float4(v[0], v[1], v[2], v[3]);
+                            *at_of(0, 2 * g + 1, rr) = make_float4(v[4], v[5], v[6], v[7]);
+                        }
+                        if (unit(k0 + k + 4, rr, g)) in0[k] = ortho_read<MODE>(p, t.b, t.i * 128 + rr, col_s + g * 8);
                     }
                 }
-                ortho_finish<MODE>(p, t.b, row, col, in, v, kSym && t.i != t.j);
+            }
+            if (again) {
+                __syncthreads();
+                if (MODE == kLast && !p.tall) {
+                    if constexpr (MODE == kLast) {
+                        const int32_t width = 1 << p.log_width;
+                        #pragma unroll 1
+                        for (int32_t e = threadIdx.x; e < 128 * width; e += kOrthoTileThreads) {
+                            const int32_t rr = e >> p.log_width, cc = e & (width - 1);
+                            const int32_t row = t.i * 128 + rr, col = col_s + cc;
+                            if (row < p.n && col < p.m)
+                                p.O[t.b * p.stride_o + row * p.ldo + col] =
+                                    __float2bfloat16_rn(reinterpret_cast<const float*>(at_of(0, cc >> 2, rr))[cc & 3]);
+                        }
+                    }
+                } else {
+                    #pragma unroll 1
+                    for (int32_t e = threadIdx.x; e < 128 << log4; e += kOrthoTileThreads) {
+                        const int32_t rr = e & 127, c4 = e >> 7;
+                        if (ortho_inside<MODE>(p, t.i * 128 + rr, col_s + 4 * c4))
+                            ortho_mirror<MODE>(p, t.b, t.i * 128 + rr, col_s + 4 * c4, *at_of(0, c4, rr));
+                    }
+                }
             }
         }
     } else if (warp >= 2 && !abort_flag) {
-        #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-            __syncwarp();
-            const int32_t col = t.j * 128 + c;
-            OrthoIn<MODE> in[2];
-            #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                if (ortho_inside<MODE>(p, row, col + 16 * q)) in[q] = ortho_read<MODE>(p, t.b, row, col + 16 * q);
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(taddr + c, r);
-            tmem_ld_wait();
-            #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (!ortho_inside<MODE>(p, row, col + 16 * q)) continue;
-                float v[16];
-                #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[16 * q + k]);
-                ortho_finish<MODE>(p, t.b, row, col + 16 * q, in[q], v, kSym && t.i != t.j);
-            }
-        }
+        float4* turn = reinterpret_cast<float4*>(smem) + (warp - 2) * 256;      // the stages are free
+        ortho_blocks<MODE>(p, t, row0, t.j * 128, blocks, taddr, in0, in1, turn);
     }
     tc_fence_before_sync();
     __syncthreads();
