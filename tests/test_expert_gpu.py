@@ -55,7 +55,28 @@ def test_sort(lib, T, k, E, dtype):
     check_sort(lib, choices(T, k, E, drop=0.4, seed=T), E, dtype, pitch=3)
 
 
-@pytest.mark.parametrize("T,k,E", [(3000, 2, 50), (30000, 6, 300)])
+@pytest.mark.parametrize("T,k,E", [(131072, 1, 9), (131073, 1, 1024), (135167, 1, 500), (33792, 4, 64), (70000, 3, 2)])
+def test_sort_of_many_slots(lib, T, k, E):
+    """Around the border of the one-launch form and of its last CTA's share, against
+    torch's stable sort."""
+    for drop, dtype in ((0.0, torch.int64), (0.5, torch.int32)):
+        ids = choices(T, k, E, drop, seed=E)
+        if drop:
+            ids[:: 7] = E - 1
+        pos, offsets, order = (t.cpu().long() for t in lib.expert_sort(ids.to(dtype).cuda(), E))
+        key = torch.where((ids >= 0) & (ids < E), ids, E).flatten()
+        kept = int((key < E).sum())
+        want = torch.sort(key, stable=True)[1]
+        want[kept:] = -1
+        assert torch.equal(order, want)
+        counts = torch.bincount(key, minlength=E + 1)[:E].cumsum(0)
+        assert torch.equal(offsets, torch.cat([torch.zeros(1, dtype=torch.int64), counts]))
+        back = torch.full((T * k,), -1)
+        back[order[:kept]] = torch.arange(kept)
+        assert torch.equal(pos.flatten(), back)
+
+
+@pytest.mark.parametrize("T,k,E", [(3000, 2, 50), (30000, 6, 300), (140000, 1, 700)])
 def test_sort_extremes(lib, T, k, E):
     """All choices one expert's, the last expert's, none at all, ids at the types' ends."""
     for v in (0, E - 1, E, -1, 2 ** 31 - 1, -2 ** 31):
@@ -145,6 +166,46 @@ def check_rows(lib, pos, x, rows, w, pad=0, off=0, dw_type=None):
 def test_rows(lib, T, k, D, dtype):
     check_rows(lib, *problem(T, k, D, dtype, F32, 0.0))
     check_rows(lib, *problem(T, k, D, dtype, None, 0.3, seed=1))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP, F32], ids=IDS.get)
+@pytest.mark.parametrize("T,k,D", [(10000, 3, 256), (9777, 7, 320), (1300, 8, 2048), (1250, 2, 5000), (12000, 1, 264),
+                                   (1400, 4, 4104)])
+def test_many_tokens(lib, T, k, D, dtype):
+    """Enough tokens for the ring, against 64 bits on the GPU: the same bounds."""
+    pos, x, rows, w = problem(T, k, D, dtype, F32, 0.2)
+    p, on = pos.cuda(), (pos >= 0).cuda()
+    X, R, W = x.double(), rows.double(), torch.where(on, w.double(), 0.0)
+    at = p.long().clamp(min=0)
+    y, mag = torch.zeros_like(X), torch.zeros_like(X)
+    d, dmag = torch.zeros_like(W), torch.zeros_like(W)
+    for j in range(k):
+        r = R[at[:, j]] * on[:, j : j + 1]
+        y += r * W[:, j : j + 1]
+        mag += (r * W[:, j : j + 1]).abs()
+        d[:, j], dmag[:, j] = (X * r).sum(1), (X * r).abs().sum(1)
+    e = mag * (k * ref.U32)
+    tol = e + ref.rounding(y.abs() + e, dtype)
+    de = dmag * ((D / 32 + 22) * ref.U32)
+    dtol = de + ref.rounding(d.abs() + de, F32)
+    ref.check(lib.expert_combine(rows, p, w), y.cpu(), tol.cpu(), "Y")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    lib.expert_gather_backward(rows, p, w, x, dX=dx, dweight=dw)
+    ref.check(dx, y.cpu(), tol.cpu(), "dX")
+    ref.check(dw, d.cpu(), dtol.cpu(), "dweight")
+    out, otol = torch.full_like(R, 77.0), torch.zeros_like(R)
+    t, j = torch.nonzero(on, as_tuple=True)
+    v = X[t] * W[t, j][:, None]
+    out[at[t, j]] = v
+    otol[at[t, j]] = v.abs() * ref.U32 + ref.rounding(v.abs() * (1 + ref.U32), dtype)
+    got = torch.full_like(rows, 77.0)
+    lib.expert_combine_backward(x, p, w, rows, dYs=got, dweight=dw.zero_())
+    ref.check(got, out.cpu(), otol.cpu(), "dYs")
+    ref.check(dw, d.cpu(), dtol.cpu(), "dweight")
+    ref.check(lib.expert_gather(x, p, w, Xs=got.fill_(77.0)), out.cpu(), otol.cpu(), "Xs")
+    lib.expert_combine_backward(x, p, w, rows, dYs=rows, dweight=dw.zero_())
+    ref.check(dw, d.cpu(), dtol.cpu(), "dweight in place")
+    assert torch.equal(rows[at[t, j]], got[at[t, j]])
 
 
 @pytest.mark.parametrize("dtype", [BF, FP, F32], ids=IDS.get)
