@@ -22,6 +22,8 @@ struct PrepParams {
     int32_t vec;                             // G's rows are 16-byte vectors
     int32_t np, mp;                          // padded sides, wide
     double* sums;                            // [batch][parts]
+    int32_t* done;                           // [products][batch], zeroed for the products' kernel
+    int32_t products;
     float eps;
     __half *hi, *lo;
 };
@@ -64,6 +66,9 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_norm_kernel(const PrepPara
     __shared__ double red[kPrepThreads / 32];
     grid_dependency_wait();
     grid_dependents_launch();
+    if (blockIdx.x == 0)
+        for (int32_t i = threadIdx.x; i < p.products; i += kPrepThreads)
+            p.done[static_cast<int64_t>(i) * gridDim.y + blockIdx.y] = 0;
     const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
     const int32_t per_row = (p.cols + 7) >> 3;
     const int64_t total = static_cast<int64_t>(p.rows) * per_row;
@@ -204,7 +209,7 @@ int64_t up256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
 // Where things lie in the workspace, in bytes.
 struct Layout {
     int64_t np, mp;
-    int64_t hi[2], lo, a, b, sums, bytes;
+    int64_t hi[2], lo, a, b, sums, done, bytes;
 };
 Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     Layout l;
@@ -223,6 +228,7 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     l.a = take(s);
     l.b = take(s);
     l.sums = take(batch * kMostParts * 8);
+    l.done = take(batch * 3 * ORTHO_MAX_STEPS * 4);
     l.bytes = at;
     return l;
 }
@@ -258,19 +264,24 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
     return cfg;
 }
 
-template <int MODE>
-cudaError_t launch_pair(const OrthoCall& c, const CUtensorMap& a, const CUtensorMap& b, const OrthoParams& p) {
-    auto kern = ortho_pair_kernel<MODE>;
+struct Maps {
+    CUtensorMap x[2], a, b;
+};
+
+// Products [p.first, p.last) on CTA pairs.  More than one: a cooperative launch.
+cudaError_t launch_pair(const OrthoCall& c, const Maps& m, const OrthoParams& p) {
+    auto kern = ortho_pair_kernel;
     static DeviceLimits limit;
     cudaError_t e = limit.raise(kOrthoPairSmem, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoPairSmem));
     });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    int64_t pairs = static_cast<int64_t>(p.batch) * p.tiles;
+    const bool chain = p.last - p.first > 1;
+    int64_t pairs = static_cast<int64_t>(p.batch) * (p.tiles_step > p.tiles_sym ? p.tiles_step : p.tiles_sym);
     if (pairs > c.sms / 2) pairs = c.sms / 2;
-    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(2 * pairs), 1, 1), kOrthoPairThreads, kOrthoPairSmem, c.stream,
-                                    attr, 2);
+    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(2 * pairs), 1, 1), kOrthoPairThreads, kOrthoPairSmem,
+                                    c.stream, attr, 2);
     // no more pairs than can be resident at once: they take the tiles in turns
     static std::mutex mu;
     static PerDevice<int> known;
@@ -284,15 +295,18 @@ cudaError_t launch_pair(const OrthoCall& c, const CUtensorMap& a, const CUtensor
             q.gridDim = dim3(static_cast<unsigned>(c.sms / 2 * 2), 1, 1);
             q.attrs = &attr[1];
             q.numAttrs = 1;
-            if (cudaOccupancyMaxActiveClusters(&most, kern, &q) != cudaSuccess) {
-                cudaGetLastError();
-                most = 0;
-            }
+            e = cudaOccupancyMaxActiveClusters(&most, kern, &q);
+            if (e != cudaSuccess) return e;
+            if (most < 1) return cudaErrorInvalidConfiguration;
             if (k != nullptr) *k = most;
         }
     }
-    if (most > 0 && pairs > most) cfg.gridDim = dim3(static_cast<unsigned>(2 * most), 1, 1);
-    return cudaLaunchKernelEx(&cfg, kern, a, b, p);
+    if (pairs > most) cfg.gridDim = dim3(static_cast<unsigned>(2 * most), 1, 1);
+    if (chain) {
+        attr[0].id = cudaLaunchAttributeCooperative;
+        attr[0].val.cooperative = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, m.x[0], m.x[1], m.a, m.b, p);
 }
 
 template <int MODE>
@@ -304,7 +318,7 @@ cudaError_t launch_tile(const OrthoCall& c, const CUtensorMap& a, const CUtensor
     });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(p.batch * p.tiles * p.splits), 1, 1), kOrthoTileThreads,
+    cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(p.batch * (MODE < kStep ? p.tiles_sym : p.tiles_step) * p.splits), 1, 1), kOrthoTileThreads,
                                     kOrthoTileSmem, c.stream, attr, p.splits);
     return cudaLaunchKernelEx(&cfg, kern, a, b, p);
 }
@@ -349,12 +363,12 @@ Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols
 template <int MODE>
 cudaError_t product(const OrthoCall& c, const Schedule& s, const CUtensorMap& a, const CUtensorMap& b,
                     OrthoParams p) {
-    p.tiles = s.tiles;
-    p.tiles_i = s.tiles_i;
+    p.tiles_sym = p.tiles_step = s.tiles;
+    p.tiles_i_step = s.tiles_i;
     p.splits = s.splits;
     p.log_width = 7;
     for (int32_t n = s.splits; n > 1; n >>= 1) --p.log_width;
-    return s.pair ? launch_pair<MODE>(c, a, b, p) : launch_tile<MODE>(c, a, b, p);
+    return launch_tile<MODE>(c, a, b, p);
 }
 
 template <typename T>
@@ -403,46 +417,58 @@ cudaError_t run(const OrthoCall& c) {
     q.sums = reinterpret_cast<double*>(c.ws + l.sums);
     q.eps = c.opt->eps;
     q.hi = hi[0], q.lo = lo;
+    q.done = reinterpret_cast<int32_t*>(c.ws + l.done), q.products = 3 * c.opt->steps;
     cudaError_t e = c.g_dtype == GEMM_F32    ? prepare<float>(c, q)
                     : c.g_dtype == GEMM_BF16 ? prepare<__nv_bfloat16>(c, q)
                                              : prepare<__half>(c, q);
     if (e != cudaSuccess) return e;
 
-    CUtensorMap map_x[2], map_a, map_b;
-    bool ok = encode_map(c, &map_x[0], hi[0], l.np, l.mp) && encode_map(c, &map_a, a, l.np, l.np) &&
-              encode_map(c, &map_b, b, l.np, l.np);
-    if (c.opt->steps > 1) ok = ok && encode_map(c, &map_x[1], hi[1], l.np, l.mp);
-    if (!ok) return cudaErrorInvalidValue;
+    Maps m;
+    if (!encode_map(c, &m.x[0], hi[0], l.np, l.mp) || !encode_map(c, &m.x[1], hi[1], l.np, l.mp) ||
+        !encode_map(c, &m.a, a, l.np, l.np) || !encode_map(c, &m.b, b, l.np, l.np))
+        return cudaErrorInvalidValue;
 
     OrthoParams p = {};
     p.batch = static_cast<int32_t>(c.batch);
     p.np = q.np, p.mp = q.mp;
     p.n = static_cast<int32_t>(tall ? c.cols : c.rows), p.m = static_cast<int32_t>(tall ? c.rows : c.cols);
     p.tall = tall;
+    p.lo = lo;
     p.O = static_cast<__nv_bfloat16*>(c.O), p.ldo = c.ldo, p.stride_o = c.stride_o;
     p.vec = vector(c.O, c.ldo, c.stride_o, 2);
     p.scale = c.opt->scale;
     p.err = c.err, p.wait_limit_ns = c.wait_limit_ns;
-    const int32_t kx = static_cast<int32_t>((l.mp + 127) / 128), kn = static_cast<int32_t>((l.np + 127) / 128);
-    const Schedule gram = schedule(c, true, l.np, l.np, kx), poly = schedule(c, true, l.np, l.np, kn),
-                   step = schedule(c, false, l.np, l.mp, kn);
-    for (int32_t i = 0; i < c.opt->steps; ++i) {
-        const float* abc = c.opt->coefficients + 3 * i;
-        p.a = abc[0], p.b = abc[1], p.c = abc[2];
-        const int from = i & 1;
-        p.debug_flags = i == 0 ? c.debug_flags : 0;
-        p.k_blocks = kx;
-        p.out = a;
-        e = product<kGram>(c, gram, map_x[from], map_x[from], p);
-        if (e != cudaSuccess) return e;
-        p.debug_flags = 0;
-        p.k_blocks = kn;
-        p.ah = a, p.out = b;
-        e = product<kPoly>(c, poly, map_a, map_a, p);
-        if (e != cudaSuccess) return e;
-        p.hi = hi[from], p.lo = lo, p.hi_out = hi[from ^ 1];
-        e = i + 1 < c.opt->steps ? product<kStep>(c, step, map_b, map_x[from], p)
-                                 : product<kLast>(c, step, map_b, map_x[from], p);
+    const int32_t steps = c.opt->steps;
+    p.k_gram = static_cast<int32_t>((l.mp + 127) / 128), p.k_other = static_cast<int32_t>((l.np + 127) / 128);
+    const Schedule sched[3] = {schedule(c, true, l.np, l.np, p.k_gram), schedule(c, true, l.np, l.np, p.k_other),
+                               schedule(c, false, l.np, l.mp, p.k_other)};
+    p.steps = steps;
+    p.x[0] = hi[0], p.x[1] = hi[1], p.mat_a = a, p.mat_b = b, p.done = q.done;
+    std::memcpy(p.abc, c.opt->coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
+    auto square = [](int64_t side) { return (side + 255) / 256; };
+    p.tiles_sym = static_cast<int32_t>(square(l.np) * (square(l.np) + 1) / 2);
+    p.tiles_i_step = static_cast<int32_t>(square(l.np));
+    p.tiles_step = static_cast<int32_t>(square(l.np) * square(l.mp));
+    p.debug_flags = c.debug_flags;
+    if (sched[0].pair && sched[1].pair && sched[2].pair) {
+        p.first = 0, p.last = 3 * steps;
+        return launch_pair(c, m, p);
+    }
+    for (int32_t i = 0; i < 3 * steps; ++i) {
+        const int32_t s = i / 3, k = i % 3;
+        if (i > 0) p.debug_flags = 0;
+        if (sched[k].pair) {
+            p.first = i, p.last = i + 1;
+            e = launch_pair(c, m, p);
+        } else {
+            OrthoParams o = p;
+            o.first = i, o.last = i + 1;
+            const CUtensorMap& x = m.x[s & 1];
+            e = k == 0          ? product<kGram>(c, sched[k], x, x, o)
+                : k == 1        ? product<kPoly>(c, sched[k], m.a, m.a, o)
+                : s + 1 < steps ? product<kStep>(c, sched[k], m.b, x, o)
+                                : product<kLast>(c, sched[k], m.b, x, o);
+        }
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

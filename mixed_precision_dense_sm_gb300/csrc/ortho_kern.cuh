@@ -16,16 +16,20 @@
 // elements, rows, chunk, matrix).  In the first two both operands are K-major; in
 // kStep the right one is X with K along its rows (MN-major), a box of the same map.
 //
-// Two kernels.  ortho_pair_kernel: persistent, 256 x 256 tiles on CTA pairs, double-
-// buffered accumulators, for many tiles.  ortho_tile_kernel: one 128 x 128 tile per
-// cluster, whose 1 to 8 CTAs split K and add up through distributed shared memory,
-// for few tiles.
+// Two kernels.  ortho_pair_kernel: 256 x 256 tiles on CTA pairs, double-buffered
+// accumulators, for many tiles; it runs through a range of products, of all the steps
+// where all of them have many tiles.  A tile then waits for the tiles of its own
+// matrix in the product before, which others have done: those of a batch follow one
+// another without a gap (16 x 1023 x 777, 76 pairs: 38 rounds of tiles for 50, and one
+// launch for 15).  ortho_tile_kernel: one 128 x 128 tile per cluster, whose 1 to 8
+// CTAs split K and add up through distributed shared memory, for few tiles.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "ortho_sm103.h"
 #include "ptx.cuh"
 
 namespace gemm103 {
@@ -39,27 +43,34 @@ constexpr uint32_t kOrthoStage = 2 * kOrthoBox;      // A's and B's
 constexpr uint32_t kOrthoTurn = 32768;                // pairs: 4 KB per epilogue warp behind the stages
 constexpr uint32_t kOrthoTileSmem = kOrthoStages * kOrthoStage + 1024 + 256;
 constexpr uint32_t kOrthoPairSmem = kOrthoTileSmem + kOrthoTurn;
-constexpr int kOrthoPairThreads = 320;               // warp 0 TMA, 1 MMA, 2-9 epilogue
+constexpr int kOrthoPairThreads = 384;               // warp 0 TMA, 1 MMA, 4-11 epilogue
+// Registers per thread of the pairs' kernel: 168 at the launch, then as the roles
+// need them (128 x 40 + 256 x 232 of the launch's 384 x 168): with 168 the epilogues'
+// inputs ahead spill to memory that no cache has room for beside the stages, 8000
+// cycles a tile.
+constexpr int kOrthoFewRegs = 40, kOrthoManyRegs = 232;
+static_assert(128 * kOrthoFewRegs + 256 * kOrthoManyRegs <= 384 * 168, "the launch's registers");
 constexpr int kOrthoTileThreads = 192;               // warp 0 TMA, 1 MMA, 2-5 epilogue
 
+// Products [first, last): product 3 s of step s is kGram, 3 s + 1 kPoly, 3 s + 2 kStep,
+// or kLast in the last step.
 struct OrthoParams {
-    int32_t batch, tiles, tiles_i;      // matrices; tiles of each; tiles along its rows
-    int32_t k_blocks;                   // pairs of K chunks
+    int32_t batch;                      // matrices
     int32_t np, mp;                     // padded sides
+    int32_t k_gram, k_other;            // pairs of K chunks
+    int32_t steps, first, last;
+    int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; kStep's along its rows
     int32_t splits, log_width;          // ortho_tile_kernel: CTAs per tile; log2(128 / splits)
-    float a, b, c;
-    const __half* ah;                   // kPoly: A
-    __half* out;                        // kGram: A, kPoly: B
-    const __half* hi;                   // kStep, kLast
-    __half* lo;
-    __half* hi_out;                     // kStep
+    __half *x[2], *lo, *mat_a, *mat_b;  // X's first numbers before even and odd steps
     __nv_bfloat16* O;                   // kLast
     int64_t ldo, stride_o;
     int32_t n, m, tall, vec;            // true sides (wide); O transposed; O's rows are vectors
     float scale;
+    int32_t* done;                      // [product][matrix]: epilogue warps through with it
     int* err;
     uint64_t wait_limit_ns;
     uint32_t debug_flags;
+    float abc[3 * ORTHO_MAX_STEPS];
 };
 
 struct OrthoTile {
@@ -70,18 +81,19 @@ struct OrthoTile {
 // columns.  Others: by columns, so that the tiles of a wave share few columns of X.
 template <int MODE>
 __device__ __forceinline__ OrthoTile ortho_tile(const OrthoParams& p, int32_t item) {
+    const int32_t tiles = MODE < kStep ? p.tiles_sym : p.tiles_step;
     OrthoTile t;
-    t.b = item / p.tiles;
-    const int32_t k = item - t.b * p.tiles;
-    if constexpr (MODE == kGram || MODE == kPoly) {
+    t.b = item / tiles;
+    const int32_t k = item - t.b * tiles;
+    if constexpr (MODE < kStep) {
         int32_t j = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(k) + 1.0f) - 1.0f) * 0.5f);
         while (j * (j + 1) / 2 > k) --j;
         while ((j + 1) * (j + 2) / 2 <= k) ++j;
         t.j = j;
         t.i = k - j * (j + 1) / 2;
     } else {
-        t.j = k / p.tiles_i;
-        t.i = k - t.j * p.tiles_i;
+        t.j = k / p.tiles_i_step;
+        t.i = k - t.j * p.tiles_i_step;
     }
     return t;
 }
@@ -121,18 +133,18 @@ struct OrthoIn {
 // whole blocks of 32 do or do not.
 template <int MODE>
 __device__ __forceinline__ bool ortho_inside(const OrthoParams& p, int32_t row, int32_t col) {
-    return row < p.np && col < (MODE == kGram || MODE == kPoly ? p.np : p.mp);
+    return row < p.np && col < (MODE < kStep ? p.np : p.mp);
 }
 template <int MODE>
-__device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_t b, int32_t row, int32_t col) {
+__device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col) {
     OrthoIn<MODE> in;
     in.x = in.y = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (MODE == kPoly) {
-        in.x = *reinterpret_cast<const uint4*>(p.ah + (static_cast<int64_t>(b) * p.np + row) * p.np + col);
+        in.x = __ldcg(reinterpret_cast<const uint4*>(p.mat_a + (static_cast<int64_t>(b) * p.np + row) * p.np + col));
     } else if constexpr (MODE != kGram) {
         const int64_t at = (static_cast<int64_t>(b) * p.np + row) * p.mp + col;
-        in.x = *reinterpret_cast<const uint4*>(p.hi + at);
-        in.y = *reinterpret_cast<const uint4*>(p.lo + at);
+        in.x = __ldcg(reinterpret_cast<const uint4*>(p.x[s & 1] + at));
+        in.y = __ldcg(reinterpret_cast<const uint4*>(p.lo + at));
     }
     return in;
 }
@@ -140,39 +152,41 @@ __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_
 // Sums v (of scaled products) of 8 columns to the result, in v, and out to where it
 // is stored by rows.
 template <int MODE>
-__device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t b, int32_t row, int32_t col,
+__device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col,
                                              const OrthoIn<MODE>& in, float (&v)[8]) {
     constexpr float kDown = 1.0f / kOrthoScale;
-    if constexpr (MODE == kGram || MODE == kPoly) {
+    if constexpr (MODE < kStep) {
         if constexpr (MODE == kPoly) {
             float x[8];
             half8(in.x, x);
-            const float c = p.c * kDown;
+            const float c1 = p.abc[3 * s + 1], c2 = p.abc[3 * s + 2] * kDown;
             #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(p.b, x[i], c * v[i]);
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(c1, x[i], c2 * v[i]);
         } else {
             #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] *= kDown;
         }
-        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(b) * p.np + row) * p.np + col) = pack8(v);
+        __half* out = MODE == kGram ? p.mat_a : p.mat_b;
+        *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(b) * p.np + row) * p.np + col) = pack8(v);
     } else {
+        const float c0 = p.abc[3 * s];
         float x[8], y[8];
         half8(in.x, x);
         half8(in.y, y);
         #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(p.a, x[i] + y[i], v[i] * kDown);
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(c0, x[i] + y[i], v[i] * kDown);
         if constexpr (MODE == kStep) {
             const uint4 h = pack8(v);
             half8(h, x);
             #pragma unroll
             for (int i = 0; i < 8; ++i) y[i] = v[i] - x[i];
             const int64_t at = (static_cast<int64_t>(b) * p.np + row) * p.mp + col;
-            *reinterpret_cast<uint4*>(p.hi_out + at) = h;
+            *reinterpret_cast<uint4*>(p.x[(s & 1) ^ 1] + at) = h;
             *reinterpret_cast<uint4*>(p.lo + at) = pack8(y);
         } else {
-            const float s = p.scale * kDown;
+            const float scale = p.scale * kDown;
             #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= s;
+            for (int i = 0; i < 8; ++i) v[i] *= scale;
             if (!p.tall && p.vec && row < p.n && col < p.m) {
                 __nv_bfloat16* d = p.O + b * p.stride_o + row * p.ldo + col;
                 if (col + 8 <= p.m) {
@@ -197,7 +211,7 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t b, in
 // or as rows that are not vectors.
 template <int MODE>
 __device__ __forceinline__ bool ortho_again(const OrthoParams& p, const OrthoTile& t) {
-    if constexpr (MODE == kGram || MODE == kPoly) return t.i != t.j;
+    if constexpr (MODE < kStep) return t.i != t.j;
     else return MODE == kLast && (p.tall || !p.vec);
 }
 // Four columns of one row to the result's transpose (lanes: neighbouring rows).
@@ -211,7 +225,7 @@ __device__ __forceinline__ void ortho_mirror(const OrthoParams& p, int32_t b, in
         if (col + 2 < p.m) d[2 * p.ldo] = __float2bfloat16_rn(v.z);
         if (col + 3 < p.m) d[3 * p.ldo] = __float2bfloat16_rn(v.w);
     } else {
-        __half* d = p.out + (static_cast<int64_t>(b) * p.np + col) * p.np + row;
+        __half* d = (MODE == kGram ? p.mat_a : p.mat_b) + (static_cast<int64_t>(b) * p.np + col) * p.np + row;
         d[0] = __float2half_rn(v.x);
         d[p.np] = __float2half_rn(v.y);
         d[2 * p.np] = __float2half_rn(v.z);
@@ -223,7 +237,7 @@ __device__ __forceinline__ void ortho_mirror(const OrthoParams& p, int32_t b, in
 // tensor memory; `in` four of eight rows.  `buf` is 4 KB of its own: row r's float4 u
 // lies at u ^ (r & 7), which no access of 8 lanes meets twice in a bank.
 template <int MODE>
-__device__ __forceinline__ void ortho_block(const OrthoParams& p, const OrthoTile& t, int32_t row0, int32_t col0,
+__device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, const OrthoTile& t, int32_t row0, int32_t col0,
                                             const uint32_t (&r)[32], const OrthoIn<MODE> (&in)[4], float4* buf) {
     const int lane = threadIdx.x & 31, l7 = lane & 7, g = lane & 3, line = lane >> 2;
     __syncwarp();
@@ -238,7 +252,7 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, const OrthoTil
         float4* at = buf + (q * 8 + line) * 8;
         const float4 a = at[(2 * g) ^ line], b = at[(2 * g + 1) ^ line];
         float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-        ortho_finish<MODE>(p, t.b, row0 + q * 8 + line, col0 + g * 8, in[q], v);
+        ortho_finish<MODE>(p, s, t.b, row0 + q * 8 + line, col0 + g * 8, in[q], v);
         if (again) {
             at[(2 * g) ^ line] = make_float4(v[0], v[1], v[2], v[3]);
             at[(2 * g + 1) ^ line] = make_float4(v[4], v[5], v[6], v[7]);
@@ -265,11 +279,11 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, const OrthoTil
 
 // The inputs of such a block.
 template <int MODE>
-__device__ __forceinline__ void ortho_read_block(const OrthoParams& p, int32_t b, int32_t row0, int32_t col0,
+__device__ __forceinline__ void ortho_read_block(const OrthoParams& p, int32_t s, int32_t b, int32_t row0, int32_t col0,
                                                  OrthoIn<MODE> (&in)[4]) {
     const int lane = threadIdx.x & 31;
     #pragma unroll
-    for (int q = 0; q < 4; ++q) in[q] = ortho_read<MODE>(p, b, row0 + q * 8 + (lane >> 2), col0 + (lane & 3) * 8);
+    for (int q = 0; q < 4; ++q) in[q] = ortho_read<MODE>(p, s, b, row0 + q * 8 + (lane >> 2), col0 + (lane & 3) * 8);
 }
 
 // A warp's 32 rows by up to 128 columns of a tile: `taddr` their accumulator; `in0`
@@ -278,7 +292,7 @@ __device__ __forceinline__ void ortho_read_block(const OrthoParams& p, int32_t b
 // time, handed on, cost the latency of a load per block: 5 us of 10 a tile).  A loop,
 // and its body short: code that runs once per tile is bound by its fetching.
 template <int MODE>
-__device__ __forceinline__ void ortho_blocks(const OrthoParams& p, const OrthoTile& t, int32_t row0, int32_t col0,
+__device__ __forceinline__ void ortho_blocks(const OrthoParams& p, int32_t s, const OrthoTile& t, int32_t row0, int32_t col0,
                                              int32_t blocks, uint32_t taddr, OrthoIn<MODE> (&in0)[4],
                                              OrthoIn<MODE> (&in1)[4], float4* buf) {
     #pragma unroll 1
@@ -287,19 +301,19 @@ __device__ __forceinline__ void ortho_blocks(const OrthoParams& p, const OrthoTi
         __syncwarp();
         tmem_ld_32x32b_x32(taddr + c * 32, r);
         tmem_ld_wait();
-        ortho_block<MODE>(p, t, row0, col0 + c * 32, r, in0, buf);
-        if (c + 2 < blocks) ortho_read_block<MODE>(p, t.b, row0, col0 + c * 32 + 64, in0);
+        ortho_block<MODE>(p, s, t, row0, col0 + c * 32, r, in0, buf);
+        if (c + 2 < blocks) ortho_read_block<MODE>(p, s, t.b, row0, col0 + c * 32 + 64, in0);
         __syncwarp();
         tmem_ld_32x32b_x32(taddr + c * 32 + 32, r);
         tmem_ld_wait();
-        ortho_block<MODE>(p, t, row0, col0 + c * 32 + 32, r, in1, buf);
-        if (c + 3 < blocks) ortho_read_block<MODE>(p, t.b, row0, col0 + c * 32 + 96, in1);
+        ortho_block<MODE>(p, s, t, row0, col0 + c * 32 + 32, r, in1, buf);
+        if (c + 3 < blocks) ortho_read_block<MODE>(p, s, t.b, row0, col0 + c * 32 + 96, in1);
     }
 }
 // Blocks of 32 columns (an even number: sides are multiples of 64) from col0 on.
 template <int MODE>
 __device__ __forceinline__ int32_t ortho_block_count(const OrthoParams& p, int32_t row0, int32_t col0) {
-    const int32_t cols = MODE == kGram || MODE == kPoly ? p.np : p.mp;
+    const int32_t cols = MODE < kStep ? p.np : p.mp;
     return row0 >= p.np || col0 >= cols ? 0 : cols - col0 < 128 ? (cols - col0) >> 5 : 4;
 }
 
@@ -346,11 +360,69 @@ __device__ __forceinline__ void ortho_mma(uint32_t d, uint32_t sa, bool first) {
 
 // ------------------------------------------------------------------- CTA pairs
 
+// Product q: its mode, and its tiles of a matrix.
+__device__ __forceinline__ int ortho_mode(const OrthoParams& p, int32_t q) {
+    const int32_t s = q / 3, m = q - 3 * s;
+    return m < 2 ? m : s + 1 < p.steps ? kStep : kLast;
+}
+__device__ __forceinline__ int32_t ortho_tiles(const OrthoParams& p, int mode) {
+    return mode < kStep ? p.tiles_sym : p.tiles_step;
+}
+__device__ __forceinline__ OrthoTile ortho_tile_of(const OrthoParams& p, int mode, int32_t item) {
+    return mode < kStep ? ortho_tile<kGram>(p, item) : ortho_tile<kStep>(p, item);
+}
+// This pair's first tile of a product: tiles are numbered through the products.
+__device__ __forceinline__ int32_t ortho_first(int64_t before, int32_t mine, int32_t pairs) {
+    const int32_t at = static_cast<int32_t>(before % pairs);
+    return mine >= at ? mine - at : mine - at + pairs;
+}
+
+// Until the product before q is done for matrix b (bounded); one thread.  Tiles wait
+// for earlier tiles only, every pair takes its own in order, and all pairs are
+// resident (a cooperative launch), so some pair always can go on.
+__device__ __forceinline__ bool ortho_ready(const OrthoParams& p, int32_t q, int32_t b, volatile int* abort_flag) {
+    if (q == p.first) return true;
+    const int32_t want = ortho_tiles(p, ortho_mode(p, q - 1)) * 16;                // 8 warps, 2 CTAs
+    const int32_t* at = p.done + static_cast<int64_t>(q - 1) * p.batch + b;
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        int32_t v;
+        asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
+        if (v >= want) return true;
+        if ((i & 63u) == 63u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0) t0 = now;
+            if (*abort_flag || now - t0 > p.wait_limit_ns) break;
+        }
+    }
+    ortho_give_up(p, abort_flag);
+    return false;
+}
+// Between writes through the generic proxy and TMA's reads of them, on both sides.
+__device__ __forceinline__ void ortho_proxy_fence() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 template <int MODE>
+__device__ __forceinline__ bool ortho_epilogue(const OrthoParams& p, int32_t s, const OrthoTile& t, int32_t row0,
+                                               int32_t col0, uint32_t taddr, uint64_t* acc_full, uint32_t parity,
+                                               float4* turn, volatile int* abort_flag) {
+    const int32_t blocks = ortho_block_count<MODE>(p, row0, col0);
+    // inputs are on their way before the accumulator is there
+    OrthoIn<MODE> in0[4], in1[4];
+    if (blocks > 0) {
+        ortho_read_block<MODE>(p, s, t.b, row0, col0, in0);
+        ortho_read_block<MODE>(p, s, t.b, row0, col0 + 32, in1);
+    }
+    if (!ortho_wait(acc_full, parity, abort_flag, p)) return false;
+    __syncwarp();
+    tc_fence_after_sync();
+    ortho_blocks<MODE>(p, s, t, row0, col0, blocks, taddr, in0, in1, turn);
+    return true;
+}
+
 __global__ void __launch_bounds__(kOrthoPairThreads, 1)
-    ortho_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+    ortho_pair_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_x1,
+                      const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                       const __grid_constant__ OrthoParams p) {
-    constexpr bool kMN = MODE == kStep || MODE == kLast;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -364,8 +436,7 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
-    const int32_t pairs = static_cast<int32_t>(gridDim.x >> 1), items = p.batch * p.tiles;
-    const int32_t mine = static_cast<int32_t>(blockIdx.x >> 1);
+    const int32_t pairs = static_cast<int32_t>(gridDim.x >> 1), mine = static_cast<int32_t>(blockIdx.x >> 1);
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -379,8 +450,6 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
         }
         mbar_init(drain, 1);
         fence_barrier_init();
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -393,86 +462,141 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
     const uint32_t tmem = *tmem_slot;
     grid_dependency_wait();
 
-    if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_last();
-            uint32_t armed = 0;
-            bool ok = true;
-            for (int32_t item = mine; item < items && ok; item += pairs) {
-                const OrthoTile t = ortho_tile<MODE>(p, item);
-                const int32_t r0 = t.i * 256 + static_cast<int32_t>(rank) * 128;
-                const int32_t c0 = t.j * 256 + static_cast<int32_t>(rank) * 128;
-                for (int32_t kb = 0; kb < p.k_blocks; ++kb, ++armed) {
-                    const uint32_t s = armed % kOrthoStages, round = armed / kOrthoStages;
-                    ok = ortho_wait(&empty[s], (round & 1u) ^ 1u, &abort_flag, p);
-                    if (!ok) break;
-                    uint8_t* sa = smem + s * kOrthoStage;
-                    const uint32_t fb = map_to_rank(smem_addr(&full[s]), 0);
-                    // the even CTA's barrier counts the bytes of both
-                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kOrthoStage);
-                    if ((p.debug_flags & 1u) && armed == 0 && blockIdx.x == 0) continue;   // test hook: no load
-                    tma_load_4d_pair(sa, &tmA, fb, 0, r0, kb * 2, t.b, keep);
-                    if constexpr (kMN) tma_load_4d_pair(sa + kOrthoBox, &tmB, fb, 0, kb * 128, c0 >> 6, t.b, keep);
-                    else tma_load_4d_pair(sa + kOrthoBox, &tmB, fb, 0, c0, kb * 2, t.b, keep);
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOrthoFewRegs));
+        if (warp == 0) {
+            if (lane == 0) {
+                const uint64_t keep = l2_policy_evict_last();
+                uint32_t armed = 0;
+                bool ok = true;
+                int64_t before = 0;
+                for (int32_t q = p.first; q < p.last && ok; ++q) {
+                    const int mode = ortho_mode(p, q);
+                    const CUtensorMap* x = (q / 3) & 1 ? &map_x1 : &map_x0;
+                    const CUtensorMap* ma = mode == kGram ? x : mode == kPoly ? &map_a : &map_b;
+                    const CUtensorMap* mb = mode == kPoly ? &map_a : x;
+                    const int32_t items = p.batch * ortho_tiles(p, mode), k_blocks = mode == kGram ? p.k_gram : p.k_other;
+                    const int32_t item0 = ortho_first(before, mine, pairs);
+                    before += items;
+                    for (int32_t item = item0; item < items && ok; item += pairs) {
+                        const OrthoTile t = ortho_tile_of(p, mode, item);
+                        const int32_t r0 = t.i * 256 + static_cast<int32_t>(rank) * 128;
+                        const int32_t c0 = t.j * 256 + static_cast<int32_t>(rank) * 128;
+                        if (q > p.first) {
+                            ok = ortho_ready(p, q, t.b, &abort_flag);
+                            if (!ok) break;
+                            ortho_proxy_fence();
+                        }
+                        for (int32_t kb = 0; kb < k_blocks; ++kb, ++armed) {
+                            const uint32_t s = armed % kOrthoStages, round = armed / kOrthoStages;
+                            ok = ortho_wait(&empty[s], (round & 1u) ^ 1u, &abort_flag, p);
+                            if (!ok) break;
+                            uint8_t* sa = smem + s * kOrthoStage;
+                            const uint32_t fb = map_to_rank(smem_addr(&full[s]), 0);
+                            // the even CTA's barrier counts the bytes of both
+                            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kOrthoStage);
+                            if ((p.debug_flags & 1u) && armed == 0 && blockIdx.x == 0) continue;   // test hook: no load
+                            tma_load_4d_pair(sa, ma, fb, 0, r0, kb * 2, t.b, keep);
+                            if (mode >= kStep) tma_load_4d_pair(sa + kOrthoBox, mb, fb, 0, kb * 128, c0 >> 6, t.b, keep);
+                            else tma_load_4d_pair(sa + kOrthoBox, mb, fb, 0, c0, kb * 2, t.b, keep);
+                        }
+                    }
+                }
+                grid_dependents_launch();
+                // every load issued into the pair has landed before it ends
+                if (rank == 0) {
+                    for (uint32_t s = 0; s < kOrthoStages; ++s) {
+                        if (armed <= s) break;
+                        if (!mbar_wait(&full[s], ((armed - 1 - s) / kOrthoStages) & 1u, p.wait_limit_ns))
+                            ortho_give_up(p, &abort_flag);
+                    }
                 }
             }
-            grid_dependents_launch();
-            // every load issued into the pair has landed before it ends
-            if (rank == 0) {
-                for (uint32_t s = 0; s < kOrthoStages; ++s) {
-                    if (armed <= s) break;
-                    if (!mbar_wait(&full[s], ((armed - 1 - s) / kOrthoStages) & 1u, p.wait_limit_ns))
-                        ortho_give_up(p, &abort_flag);
+        } else if (warp == 1) {
+            if (lane == 0 && rank == 0) {
+                uint32_t used = 0, acc_i = 0;
+                bool ok = true;
+                const uint32_t base = smem_addr(smem);
+                int64_t before = 0;
+                for (int32_t q = p.first; q < p.last && ok; ++q) {
+                    const int mode = ortho_mode(p, q);
+                    const int32_t items = p.batch * ortho_tiles(p, mode), k_blocks = mode == kGram ? p.k_gram : p.k_other;
+                    const int32_t item0 = ortho_first(before, mine, pairs);
+                    before += items;
+                    for (int32_t item = item0; item < items && ok; item += pairs, ++acc_i) {
+                        const uint32_t buf = acc_i & 1u;
+                        ok = ortho_wait<true>(&acc_empty[buf], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, p);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        for (int32_t kb = 0; kb < k_blocks; ++kb, ++used) {
+                            const uint32_t s = used % kOrthoStages, round = used / kOrthoStages;
+                            ok = ortho_wait(&full[s], round & 1u, &abort_flag, p);
+                            if (!ok) break;
+                            tc_fence_after_sync();
+                            if (mode >= kStep) ortho_mma<kStep, true>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
+                            else ortho_mma<kGram, true>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
+                            tc_commit_pair_multicast(&empty[s], 3);
+                        }
+                        if (ok) tc_commit_pair_multicast(&acc_full[buf], 3);
+                    }
                 }
+                // all MMAs issued have completed, also when the loop was left early
+                tc_commit_pair(drain);
+                if (!mbar_wait(drain, 0, p.wait_limit_ns)) ortho_give_up(p, &abort_flag);
             }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            uint32_t used = 0, acc_i = 0;
-            bool ok = true;
-            const uint32_t base = smem_addr(smem);
-            for (int32_t item = mine; item < items && ok; item += pairs, ++acc_i) {
-                const uint32_t buf = acc_i & 1u;
-                if (!ortho_wait<true>(&acc_empty[buf], ((acc_i >> 1) & 1u) ^ 1u, &abort_flag, p)) break;
-                tc_fence_after_sync();
-                for (int32_t kb = 0; kb < p.k_blocks; ++kb, ++used) {
-                    const uint32_t s = used % kOrthoStages, round = used / kOrthoStages;
-                    ok = ortho_wait(&full[s], round & 1u, &abort_flag, p);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    ortho_mma<MODE, true>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
-                    tc_commit_pair_multicast(&empty[s], 3);
-                }
-                if (ok) tc_commit_pair_multicast(&acc_full[buf], 3);
-            }
-            // all MMAs issued have completed, also when the loop was left early
-            tc_commit_pair(drain);
-            if (!mbar_wait(drain, 0, p.wait_limit_ns)) ortho_give_up(p, &abort_flag);
         }
     } else {
-        const int quarter = warp & 3, half = (warp - 2) >> 2;
-        float4* turn = reinterpret_cast<float4*>(smem + kOrthoStages * kOrthoStage) + (warp - 2) * 256;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOrthoManyRegs));
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
+        float4* turn = reinterpret_cast<float4*>(smem + kOrthoStages * kOrthoStage) + (warp - 4) * 256;
         uint32_t acc_i = 0;
-        for (int32_t item = mine; item < items; item += pairs, ++acc_i) {
-            const OrthoTile t = ortho_tile<MODE>(p, item);
-            const uint32_t buf = acc_i & 1u;
-            const int32_t row0 = t.i * 256 + static_cast<int32_t>(rank) * 128 + quarter * 32;
-            const int32_t col0 = t.j * 256 + half * 128;
-            const int32_t blocks = ortho_block_count<MODE>(p, row0, col0);
-            OrthoIn<MODE> in0[4], in1[4];
-            if (blocks > 0) {
-                ortho_read_block<MODE>(p, t.b, row0, col0, in0);
-                ortho_read_block<MODE>(p, t.b, row0, col0 + 32, in1);
+        bool ok = true;
+        int64_t before = 0;
+        for (int32_t q = p.first; q < p.last && ok; ++q) {
+            const int mode = ortho_mode(p, q);
+            const int32_t items = p.batch * ortho_tiles(p, mode);
+            const int32_t item0 = ortho_first(before, mine, pairs);
+            before += items;
+            for (int32_t item = item0; item < items; item += pairs, ++acc_i) {
+                const OrthoTile t = ortho_tile_of(p, mode, item);
+                const uint32_t buf = acc_i & 1u, parity = (acc_i >> 1) & 1u;
+                const int32_t row0 = t.i * 256 + static_cast<int32_t>(rank) * 128 + quarter * 32;
+                const int32_t col0 = t.j * 256 + half * 128;
+                const uint32_t taddr = tmem + buf * 256u + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128u;
+                if (q > p.first) {
+                    int ready = 0;
+                    if (lane == 0) ready = ortho_ready(p, q, t.b, &abort_flag) ? 1 : 0;
+                    ok = __shfl_sync(0xffffffffu, ready, 0) != 0;
+                    if (!ok) break;
+                }
+                if (mode == kGram)
+                    ok = ortho_epilogue<kGram>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
+                                               &abort_flag);
+                else if (mode == kPoly)
+                    ok = ortho_epilogue<kPoly>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
+                                               &abort_flag);
+                else if (mode == kStep)
+                    ok = ortho_epilogue<kStep>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
+                                               &abort_flag);
+                else
+                    ok = ortho_epilogue<kLast>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
+                                               &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&acc_empty[buf]), 0));
+                if (q + 1 < p.last) {
+                    // what this warp wrote is there for the next product's loads
+                    ortho_proxy_fence();
+                    __threadfence();
+                    __syncwarp();
+                    if (lane == 0)
+                        asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(
+                                         p.done + static_cast<int64_t>(q) * p.batch + t.b)
+                                     : "memory");
+                }
             }
-            if (!ortho_wait(&acc_full[buf], (acc_i >> 1) & 1u, &abort_flag, p)) break;
-            __syncwarp();
-            tc_fence_after_sync();
-            ortho_blocks<MODE>(p, t, row0, col0, blocks,
-                               tmem + buf * 256u + (static_cast<uint32_t>(quarter * 32) << 16) + half * 128u, in0, in1,
-                               turn);
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&acc_empty[buf]), 0));
         }
     }
     tc_fence_before_sync();
@@ -502,8 +626,9 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     const int32_t S = p.splits;
     const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
     const OrthoTile t = ortho_tile<MODE>(p, static_cast<int32_t>(blockIdx.x) / S);
-    const int32_t kb0 = static_cast<int32_t>(rank) * p.k_blocks / S;
-    const int32_t kb1 = static_cast<int32_t>(rank + 1) * p.k_blocks / S;
+    const int32_t step = p.first / 3, k_blocks = MODE == kGram ? p.k_gram : p.k_other;
+    const int32_t kb0 = static_cast<int32_t>(rank) * k_blocks / S;
+    const int32_t kb1 = static_cast<int32_t>(rank + 1) * k_blocks / S;
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -543,14 +668,14 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     OrthoIn<MODE> in0[4], in1[4];
     if (warp >= 2) {
         if (blocks > 0) {
-            ortho_read_block<MODE>(p, t.b, row0, t.j * 128, in0);
-            ortho_read_block<MODE>(p, t.b, row0, t.j * 128 + 32, in1);
+            ortho_read_block<MODE>(p, step, t.b, row0, t.j * 128, in0);
+            ortho_read_block<MODE>(p, step, t.b, row0, t.j * 128 + 32, in1);
         }
         if (S > 1) {
             #pragma unroll
             for (int32_t k = 0; k < 4; ++k) {
                 int32_t rr, g;
-                if (unit(k, rr, g)) in0[k] = ortho_read<MODE>(p, t.b, t.i * 128 + rr, col_s + g * 8);
+                if (unit(k, rr, g)) in0[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
             }
         }
     }
@@ -649,13 +774,13 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                             v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
                             v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
                         }
-                        ortho_finish<MODE>(p, t.b, t.i * 128 + rr, col_s + g * 8, in0[k], v);
+                        ortho_finish<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8, in0[k], v);
                         if (again) {
                             // in the place of the first source's sums, which this thread alone reads
                             *at_of(0, 2 * g, rr) = make_float4(v[0], v[1], v[2], v[3]);
                             *at_of(0, 2 * g + 1, rr) = make_float4(v[4], v[5], v[6], v[7]);
                         }
-                        if (unit(k0 + k + 4, rr, g)) in0[k] = ortho_read<MODE>(p, t.b, t.i * 128 + rr, col_s + g * 8);
+                        if (unit(k0 + k + 4, rr, g)) in0[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
                     }
                 }
             }
@@ -685,7 +810,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         }
     } else if (warp >= 2 && !abort_flag) {
         float4* turn = reinterpret_cast<float4*>(smem) + (warp - 2) * 256;      // the stages are free
-        ortho_blocks<MODE>(p, t, row0, t.j * 128, blocks, taddr, in0, in1, turn);
+        ortho_blocks<MODE>(p, step, t, row0, t.j * 128, blocks, taddr, in0, in1, turn);
     }
     tc_fence_before_sync();
     __syncthreads();
