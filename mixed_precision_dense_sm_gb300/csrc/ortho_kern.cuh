@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "f32x2.cuh"
 #include "ortho_sm103.h"
 #include "ptx.cuh"
 
@@ -98,23 +99,12 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoParams& p, int32_t it
     return t;
 }
 
-__device__ __forceinline__ void half8(uint4 u, float* f) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-        f[2 * i] = v.x;
-        f[2 * i + 1] = v.y;
-    }
+// Eight FP16 numbers as four FP32 pairs, and back, rounded.
+__device__ __forceinline__ void half8(uint4 u, F2 (&f)[4]) {
+    f[0] = unpack2<__half>(u.x), f[1] = unpack2<__half>(u.y), f[2] = unpack2<__half>(u.z), f[3] = unpack2<__half>(u.w);
 }
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    uint32_t w[4];
-    #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
+    return make_uint4(pack2<__half>(f[0]), pack2<__half>(f[1]), pack2<__half>(f[2]), pack2<__half>(f[3]));
 }
 
 // The epilogue works on 8 columns of a row at a time, 8 rows by 32 columns a warp, four
@@ -153,58 +143,67 @@ __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_
 // is stored by rows.
 template <int MODE>
 __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col,
-                                             const OrthoIn<MODE>& in, float (&v)[8]) {
+                                             const OrthoIn<MODE>& in, F2 (&v)[4]) {
     constexpr float kDown = 1.0f / kOrthoScale;
+    F2 x[4];
     if constexpr (MODE < kStep) {
         if constexpr (MODE == kPoly) {
-            float x[8];
             half8(in.x, x);
-            const float c1 = p.abc[3 * s + 1], c2 = p.abc[3 * s + 2] * kDown;
+            const F2 c1 = mk2(p.abc[3 * s + 1]), c2 = mk2(p.abc[3 * s + 2] * kDown);
             #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(c1, x[i], c2 * v[i]);
+            for (int i = 0; i < 4; ++i) v[i] = fma2(c1, x[i], mul2(c2, v[i]));
         } else {
             #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= kDown;
+            for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], mk2(kDown));
         }
         __half* out = MODE == kGram ? p.mat_a : p.mat_b;
         *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(b) * p.np + row) * p.np + col) = pack8(v);
     } else {
-        const float c0 = p.abc[3 * s];
-        float x[8], y[8];
+        const F2 c0 = mk2(p.abc[3 * s]);
+        F2 y[4];
         half8(in.x, x);
         half8(in.y, y);
         #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = fmaf(c0, x[i] + y[i], v[i] * kDown);
+        for (int i = 0; i < 4; ++i) v[i] = fma2(c0, add2(x[i], y[i]), mul2(v[i], mk2(kDown)));
         if constexpr (MODE == kStep) {
             const uint4 h = pack8(v);
             half8(h, x);
             #pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = v[i] - x[i];
+            for (int i = 0; i < 4; ++i) y[i] = fma2(x[i], mk2(-1.0f), v[i]);
             const int64_t at = (static_cast<int64_t>(b) * p.np + row) * p.mp + col;
             *reinterpret_cast<uint4*>(p.x[(s & 1) ^ 1] + at) = h;
             *reinterpret_cast<uint4*>(p.lo + at) = pack8(y);
         } else {
-            const float scale = p.scale * kDown;
+            const F2 scale = mk2(p.scale);
             #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= scale;
+            for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], mk2(kDown)), scale);
             if (!p.tall && p.vec && row < p.n && col < p.m) {
                 __nv_bfloat16* d = p.O + b * p.stride_o + row * p.ldo + col;
                 if (col + 8 <= p.m) {
-                    uint32_t w[4];
-                    #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(d) = make_uint4(pack2<__nv_bfloat16>(v[0]), pack2<__nv_bfloat16>(v[1]),
+                                                              pack2<__nv_bfloat16>(v[2]), pack2<__nv_bfloat16>(v[3]));
                 } else {
                     #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (col + i < p.m) d[i] = __float2bfloat16_rn(v[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        float lo, hi;
+                        get2(v[i], lo, hi);
+                        if (col + 2 * i < p.m) d[2 * i] = __float2bfloat16_rn(lo);
+                        if (col + 2 * i + 1 < p.m) d[2 * i + 1] = __float2bfloat16_rn(hi);
+                    }
                 }
             }
         }
     }
+}
+// Eight sums as two float4s of shared memory.
+__device__ __forceinline__ void ortho_load8(const float4* a, const float4* b, F2 (&v)[4]) {
+    const float4 x = *a, y = *b;
+    v[0] = mk2(x.x, x.y), v[1] = mk2(x.z, x.w), v[2] = mk2(y.x, y.y), v[3] = mk2(y.z, y.w);
+}
+__device__ __forceinline__ void ortho_store8(float4* a, float4* b, const F2 (&v)[4]) {
+    float4 x, y;
+    get2(v[0], x.x, x.y), get2(v[1], x.z, x.w), get2(v[2], y.x, y.y), get2(v[3], y.z, y.w);
+    *a = x, *b = y;
 }
 
 // Whether the results are stored in another way too, or only: mirrored, transposed,
@@ -250,13 +249,10 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, con
     #pragma unroll
     for (int q = 0; q < 4; ++q) {
         float4* at = buf + (q * 8 + line) * 8;
-        const float4 a = at[(2 * g) ^ line], b = at[(2 * g + 1) ^ line];
-        float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        F2 v[4];
+        ortho_load8(at + ((2 * g) ^ line), at + ((2 * g + 1) ^ line), v);
         ortho_finish<MODE>(p, s, t.b, row0 + q * 8 + line, col0 + g * 8, in[q], v);
-        if (again) {
-            at[(2 * g) ^ line] = make_float4(v[0], v[1], v[2], v[3]);
-            at[(2 * g + 1) ^ line] = make_float4(v[4], v[5], v[6], v[7]);
-        }
+        if (again) ortho_store8(at + ((2 * g) ^ line), at + ((2 * g + 1) ^ line), v);
     }
     if (!again) return;
     __syncwarp();
@@ -389,6 +385,7 @@ __device__ __forceinline__ bool ortho_ready(const OrthoParams& p, int32_t q, int
         int32_t v;
         asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(at) : "memory");
         if (v >= want) return true;
+        __nanosleep(100);                // (1400 warps may be waiting at one address)
         if ((i & 63u) == 63u) {
             const uint64_t now = global_timer_ns();
             if (t0 == 0) t0 = now;
@@ -767,19 +764,18 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                     for (int32_t k = 0; k < 4; ++k) {
                         int32_t rr, g;
                         if (!unit(k0 + k, rr, g)) continue;
-                        float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                        F2 v[4];
+                        ortho_load8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
                         #pragma unroll 2
-                        for (int32_t s = 0; s < S; ++s) {
-                            const float4 a = *at_of(s, 2 * g, rr), b = *at_of(s, 2 * g + 1, rr);
-                            v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-                            v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+                        for (int32_t s = 1; s < S; ++s) {
+                            F2 o[4];
+                            ortho_load8(at_of(s, 2 * g, rr), at_of(s, 2 * g + 1, rr), o);
+                            #pragma unroll
+                            for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
                         }
                         ortho_finish<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8, in0[k], v);
-                        if (again) {
-                            // in the place of the first source's sums, which this thread alone reads
-                            *at_of(0, 2 * g, rr) = make_float4(v[0], v[1], v[2], v[3]);
-                            *at_of(0, 2 * g + 1, rr) = make_float4(v[4], v[5], v[6], v[7]);
-                        }
+                        // in the place of the first source's sums, which this thread alone reads
+                        if (again) ortho_store8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
                         if (unit(k0 + k + 4, rr, g)) in0[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
                     }
                 }
