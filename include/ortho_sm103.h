@@ -19,7 +19,7 @@
  * why O is BF16.  Values of X, A and b A + c A^2 up to 32 in magnitude are held:
  * coefficients that keep the singular values near 1 stay far below.
  * A and A^2 are symmetric: half their tiles are computed, the others mirrored.
- * The sum of squares is FP32 over up to 8 elements and FP64 from there on, in a fixed
+ * The sum of squares is FP32 over up to 32 elements and FP64 from there on, in a fixed
  * order: the same call gives the same bits.
  *
  * A matrix of zeros gives zeros (with eps > 0); one with an infinity or NaN gives

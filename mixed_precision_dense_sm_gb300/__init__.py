@@ -511,6 +511,7 @@ def norm_block_backward_workspace(M, N, gate_rows=1, num_sms=0) -> int:
 # The planner and the raw C calls need no torch: the first call that takes tensors imports it.
 torch = None
 _CODE = {}
+_DEVICES = {}
 
 
 def _need_torch():
@@ -574,7 +575,9 @@ def _empty(shape, dtype, dev, stream):
     """A new tensor of the caching allocator for a call on `stream` (None: the
     current one), from that stream's own memory: what another stream freed may
     still be in use there."""
-    where = torch.device("cuda", dev)
+    where = _DEVICES.get(dev)
+    if where is None:
+        where = _DEVICES[dev] = torch.device("cuda", dev)
     if stream is None or stream == _stream(dev):
         return torch.empty(shape, dtype=dtype, device=where)
     s = torch.cuda.ExternalStream(stream, where) if stream else torch.cuda.default_stream(where)

@@ -219,6 +219,13 @@ __device__ __forceinline__ void ortho_mirror(const OrthoParams& p, int32_t b, in
     if constexpr (MODE == kLast) {
         if (row >= p.n) return;
         __nv_bfloat16* d = p.O + b * p.stride_o + col * p.ldo + row;
+        if (col + 4 <= p.m) {
+            d[0] = __float2bfloat16_rn(v.x);
+            d[p.ldo] = __float2bfloat16_rn(v.y);
+            d[2 * p.ldo] = __float2bfloat16_rn(v.z);
+            d[3 * p.ldo] = __float2bfloat16_rn(v.w);
+            return;
+        }
         if (col < p.m) d[0] = __float2bfloat16_rn(v.x);
         if (col + 1 < p.m) d[p.ldo] = __float2bfloat16_rn(v.y);
         if (col + 2 < p.m) d[2 * p.ldo] = __float2bfloat16_rn(v.z);
@@ -584,9 +591,9 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_addr(&acc_empty[buf]), 0));
                 if (q + 1 < p.last) {
-                    // what this warp wrote is there for the next product's loads
+                    // what this warp wrote is there for the next product's loads (the
+                    // release is cumulative: it covers what the warp's barrier ordered)
                     ortho_proxy_fence();
-                    __threadfence();
                     __syncwarp();
                     if (lane == 0)
                         asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(
