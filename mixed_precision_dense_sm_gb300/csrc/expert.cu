@@ -461,7 +461,7 @@ __device__ __forceinline__ Place place_of(const RowsParams& p, int64_t unit) {
     a.live = a.t < p.T;
     a.step = a.group * V;
     const int32_t D = static_cast<int32_t>(p.D), whole = A ? D / V * V : D;
-    const int32_t per = ((D + p.chunks - 1) / p.chunks + a.step - 1) / a.step * a.step;
+    const int32_t per = ((whole + p.chunks - 1) / p.chunks + a.step - 1) / a.step * a.step;
     const int32_t first = chunk * per;
     a.c0 = first + a.g * (A ? V : 1);
     a.c1 = p.chunks > 1 && first + per < whole ? first + per : whole;
@@ -937,7 +937,7 @@ gemm_status_t rows_call(RowsKind kind, RowsParams& p, int32_t dtype, const exper
     auto vector = [&](const void* q, int64_t ld) { return q == nullptr || (aligned(q, 16) && ld % per == 0); };
     const bool vec = vector(p.tok_in, p.ld_tok_in) && vector(p.rows_in, p.ld_rows_in) &&
                      vector(p.tok_out, p.ld_tok_out) && vector(p.rows_out, p.ld_rows_out);
-    const int64_t nvec = p.D / (vec ? per : 4);
+    const int64_t nvec = vec ? p.D / per : (p.D + 3) / 4;
     // Threads per token: as many as it has vectors, up to a CTA's; whole warps
     // where they add up dot products.
     p.log_group = dot ? 5 : 2;

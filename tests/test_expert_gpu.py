@@ -162,7 +162,8 @@ def check_rows(lib, pos, x, rows, w, pad=0, off=0, dw_type=None):
 
 @pytest.mark.parametrize("dtype", [BF, FP, F32], ids=IDS.get)
 @pytest.mark.parametrize("T,k,D", [(1, 1, 1), (1, 8, 4096), (2, 3, 7), (5, 2, 8), (64, 8, 64), (7, 4, 1000),
-                                   (33, 9, 130), (3, 17, 520), (400, 2, 136), (10, 3, 5000), (700, 1, 24)])
+                                   (33, 9, 130), (3, 17, 520), (400, 2, 136), (10, 3, 5000), (700, 1, 24),
+                                   (4, 2, 2055), (6, 3, 1027)])
 def test_rows(lib, T, k, D, dtype):
     check_rows(lib, *problem(T, k, D, dtype, F32, 0.0))
     check_rows(lib, *problem(T, k, D, dtype, None, 0.3, seed=1))

@@ -184,7 +184,42 @@ def test_streams_and_capture(lib):
     graph_h.close()
 
 
-@pytest.mark.parametrize("r,c", [(64, 64), (512, 2048), (2048, 4096)])
+def test_one_launch_on_two_streams_and_captured(lib):
+    """Sizes whose products run in one launch: two handles at once, and a captured call
+    beside them, give the bits of a call alone."""
+    shapes = [(6, 900, 1500), (1, 4096, 4096)]
+    hs = [lib.Gemm() for _ in range(3)]
+    for n, shape in enumerate(shapes):
+        G = update(*shape, dtype=BF, scale=1.0, kind="few")
+        want = hs[0].orthogonalize(G)
+        torch.cuda.synchronize()
+        out = torch.empty_like(want)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            hs[2].orthogonalize(G, out)
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        got = [torch.empty_like(want) for _ in range(2)]
+        for _ in range(4):
+            for i in range(2):
+                with torch.cuda.stream(streams[i]):
+                    got[i].zero_()
+                    hs[i].orthogonalize(G, got[i])
+            with torch.cuda.stream(streams[2]):
+                out.zero_()
+                graph.replay()
+        torch.cuda.synchronize()
+        for h in hs:
+            h.sync()
+        assert torch.equal(got[0], want) and torch.equal(got[1], want) and torch.equal(out, want)
+        if n == 0:
+            ref = ortho.define(G[5], (3.4445, -4.7750, 2.0315))
+            assert float((want[5].double() - ref).norm()) <= 2.0 ** -8 * float(ref.norm())
+        del graph
+    for h in hs:
+        h.close()
+
+
+@pytest.mark.parametrize("r,c", [(64, 64), (512, 2048), (2048, 4096), (4096, 4096)])
 def test_a_wait_that_runs_out(lib, r, c):
     """A load that never comes: the call gives up, says so, and the next one is right."""
     h = lib.Gemm()
