@@ -258,12 +258,13 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
 }
 
 // batch matrices of `rows` x `cols` halves, cols a multiple of 64, one behind the
-// other: (64 elements, row, chunk, matrix), boxes of 128 rows by two chunks.
-bool encode_map(const OrthoCall& c, CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols) {
+// other: (64 elements, row, chunk, matrix), boxes of box_rows rows by box_chunks chunks.
+bool encode_map(const OrthoCall& c, CUtensorMap* map, const void* ptr, int64_t rows, int64_t cols,
+                uint32_t box_rows = 128, uint32_t box_chunks = 2) {
     const cuuint64_t dims[4] = {64u, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols / 64),
                                 static_cast<cuuint64_t>(c.batch)};
     const cuuint64_t strides[3] = {static_cast<cuuint64_t>(cols * 2), 128u, static_cast<cuuint64_t>(rows * cols * 2)};
-    const cuuint32_t box[4] = {64u, 128u, 2u, 1u};
+    const cuuint32_t box[4] = {64u, box_rows, box_chunks, 1u};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return c.encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -289,7 +290,9 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
 }
 
 struct Maps {
-    CUtensorMap x[2], a, b;
+    CUtensorMap x[2], a, b;              // boxes of 128 rows by two chunks
+    CUtensorMap x_few[2], a_few;         // for narrow tiles: of 32 rows, K-major
+    CUtensorMap x_narrow[2];             // of one chunk
 };
 
 // Products [p.first, p.last) on CTA pairs.  More than one: a cooperative launch.
@@ -333,9 +336,9 @@ cudaError_t launch_pair(const OrthoCall& c, const Maps& m, const OrthoParams& p)
     return cudaLaunchKernelEx(&cfg, kern, m.x[0], m.x[1], m.a, m.b, p);
 }
 
-template <int MODE>
+template <int MODE, int NB>
 cudaError_t launch_tile(const OrthoCall& c, const CUtensorMap& a, const CUtensorMap& b, const OrthoParams& p) {
-    auto kern = ortho_tile_kernel<MODE>;
+    auto kern = ortho_tile_kernel<MODE, NB>;
     static DeviceLimits limit;
     const cudaError_t e = limit.raise(kOrthoTileSmem, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoTileSmem));
@@ -349,50 +352,55 @@ cudaError_t launch_tile(const OrthoCall& c, const CUtensorMap& a, const CUtensor
 
 struct Schedule {
     bool pair;
+    bool narrow;                             // not pair: tiles of 32 or 64 columns
     int32_t tiles, tiles_i, splits;
 };
 
 // The faster schedule by a rough count of SM cycles.  A pair's 256 x 256 x 128 block
 // takes 1024 at the tensor core's rate, a tile's epilogue 9000 beside the next
 // tile's blocks.  A single CTA's 128 x 128 x 128 block takes as long, for it is bound
-// by the 64 KB that it loads; its epilogue 5000, the exchange of a split 2000.
+// by the 64 KB that it loads (64 a cycle); its epilogue 4500 and the exchange of a
+// split 7500, both as the columns, and 3000 until the first block is there.
 Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols, int64_t k_blocks) {
-    auto count = [&](int64_t side, int32_t& along) {
-        const int64_t i = (rows + side - 1) / side, j = (cols + side - 1) / side;
-        along = static_cast<int32_t>(i);
-        return symmetric ? i * (i + 1) / 2 : i * j;
-    };
-    Schedule s;
-    const int64_t big = count(256, s.tiles_i) * c.batch;
-    const int64_t pairs = c.sms / 2;
-    int64_t best = (big + pairs - 1) / pairs * (k_blocks * 1024 > 9000 ? k_blocks * 1024 : 9000) + 9000;
-    s.pair = true;
-    s.splits = 1;
-    int32_t along;
-    const int64_t small = count(128, along) * c.batch;
-    for (int32_t n = 1; n <= 8 && n <= k_blocks; n *= 2) {
-        const int64_t waves = (small * n + c.sms - 1) / c.sms;
-        const int64_t cost = waves * ((k_blocks + n - 1) / n * 1024 + 5000 + (n > 1 ? 2000 : 0));
-        if (cost < best) {
-            best = cost;
-            s.pair = false;
-            s.splits = n;
+    Schedule best = {};
+    int64_t least = INT64_MAX;
+    auto consider = [&](bool pair, bool narrow, int32_t splits) {
+        const int64_t side = pair ? 256 : 128, width = narrow ? (symmetric ? 32 : 64) : side;
+        const int64_t i = (rows + side - 1) / side, j = (cols + width - 1) / width;
+        const int64_t tiles = symmetric && !narrow ? i * (i + 1) / 2 : i * j;
+        int64_t cycles;
+        if (pair) {
+            const int64_t blocks = k_blocks * 1024, pairs = c.sms / 2;
+            cycles = (tiles * c.batch + pairs - 1) / pairs * (blocks > 9000 ? blocks : 9000) + 9000;
+        } else {
+            const int64_t block = (32768 + width * 256) / 64, waves = (tiles * c.batch * splits + c.sms - 1) / c.sms;
+            cycles = waves * ((k_blocks + splits - 1) / splits * block + 3000 + 4500 * width / 128 +
+                              (splits > 1 ? 2500 + 5000 * width / 128 : 0));
         }
+        if (cycles < least) {
+            least = cycles;
+            best = Schedule{pair, narrow, static_cast<int32_t>(tiles), static_cast<int32_t>(i), splits};
+        }
+    };
+    consider(true, false, 1);
+    for (int32_t n = 1; n <= 8 && n <= k_blocks; n *= 2) {
+        consider(false, false, n);
+        if (n <= 4) consider(false, true, n);        // (8 columns at least to finish)
     }
-    if (!s.pair) s.tiles_i = along;
-    s.tiles = static_cast<int32_t>((s.pair ? big : small) / c.batch);
-    return s;
+    return best;
 }
 
 template <int MODE>
 cudaError_t product(const OrthoCall& c, const Schedule& s, const CUtensorMap& a, const CUtensorMap& b,
-                    OrthoParams p) {
+                    const CUtensorMap& b_narrow, OrthoParams p) {
+    constexpr int kNarrow = MODE < kStep ? 32 : 64;
     p.tiles_sym = p.tiles_step = s.tiles;
     p.tiles_i_step = s.tiles_i;
+    p.full = s.narrow;
     p.splits = s.splits;
-    p.log_width = 7;
+    p.log_width = !s.narrow ? 7 : MODE < kStep ? 5 : 6;
     for (int32_t n = s.splits; n > 1; n >>= 1) --p.log_width;
-    return launch_tile<MODE>(c, a, b, p);
+    return s.narrow ? launch_tile<MODE, kNarrow>(c, a, b_narrow, p) : launch_tile<MODE, 128>(c, a, b, p);
 }
 
 template <typename T>
@@ -469,6 +477,13 @@ cudaError_t run(const OrthoCall& c) {
     p.steps = steps;
     p.x[0] = hi[0], p.x[1] = hi[1], p.mat_a = a, p.mat_b = b, p.done = q.done;
     std::memcpy(p.abc, c.opt->coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
+    bool ok = true;
+    for (int i = 0; i < 2; ++i) {
+        if (sched[0].narrow) ok = ok && encode_map(c, &m.x_few[i], hi[i], l.np, l.mp, 32, 2);
+        if (sched[2].narrow) ok = ok && encode_map(c, &m.x_narrow[i], hi[i], l.np, l.mp, 128, 1);
+    }
+    if (sched[1].narrow) ok = ok && encode_map(c, &m.a_few, a, l.np, l.np, 32, 2);
+    if (!ok) return cudaErrorInvalidValue;
     auto square = [](int64_t side) { return (side + 255) / 256; };
     p.tiles_sym = static_cast<int32_t>(square(l.np) * (square(l.np) + 1) / 2);
     p.tiles_i_step = static_cast<int32_t>(square(l.np));
@@ -488,10 +503,10 @@ cudaError_t run(const OrthoCall& c) {
             OrthoParams o = p;
             o.first = i, o.last = i + 1;
             const CUtensorMap& x = m.x[s & 1];
-            e = k == 0          ? product<kGram>(c, sched[k], x, x, o)
-                : k == 1        ? product<kPoly>(c, sched[k], m.a, m.a, o)
-                : s + 1 < steps ? product<kStep>(c, sched[k], m.b, x, o)
-                                : product<kLast>(c, sched[k], m.b, x, o);
+            e = k == 0          ? product<kGram>(c, sched[k], x, x, m.x_few[s & 1], o)
+                : k == 1        ? product<kPoly>(c, sched[k], m.a, m.a, m.a_few, o)
+                : s + 1 < steps ? product<kStep>(c, sched[k], m.b, x, m.x_narrow[s & 1], o)
+                                : product<kLast>(c, sched[k], m.b, x, m.x_narrow[s & 1], o);
         }
         if (e != cudaSuccess) return e;
     }

@@ -21,8 +21,10 @@
 // where all of them have many tiles.  A tile then waits for the tiles of its own
 // matrix in the product before, which others have done: those of a batch follow one
 // another without a gap (16 x 1023 x 777, 76 pairs: 38 rounds of tiles for 50, and one
-// launch for 15).  ortho_tile_kernel: one 128 x 128 tile per cluster, whose 1 to 8
-// CTAs split K and add up through distributed shared memory, for few tiles.
+// launch for 15).  ortho_tile_kernel: one tile of 128 rows and 128 columns per
+// cluster, whose 1 to 8 CTAs split K and add up through distributed shared memory, for
+// few tiles; for fewer still 64 columns (kStep, kLast) or 32, which shortens the
+// epilogue, and all tiles of the symmetric products, without mirroring.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -60,8 +62,9 @@ struct OrthoParams {
     int32_t np, mp;                     // padded sides
     int32_t k_gram, k_other;            // pairs of K chunks
     int32_t steps, first, last;
-    int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; kStep's along its rows
-    int32_t splits, log_width;          // ortho_tile_kernel: CTAs per tile; log2(128 / splits)
+    int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; along its rows
+    int32_t full;                       // symmetric products: all tiles, not the upper ones
+    int32_t splits, log_width;          // ortho_tile_kernel: CTAs per tile; log2(columns / splits)
     __half *x[2], *lo, *mat_a, *mat_b;  // X's first numbers before even and odd steps
     __nv_bfloat16* O;                   // kLast
     int64_t ldo, stride_o;
@@ -86,7 +89,7 @@ __device__ __forceinline__ OrthoTile ortho_tile(const OrthoParams& p, int32_t it
     OrthoTile t;
     t.b = item / tiles;
     const int32_t k = item - t.b * tiles;
-    if constexpr (MODE < kStep) {
+    if (MODE < kStep && !p.full) {
         int32_t j = static_cast<int32_t>((sqrtf(8.0f * static_cast<float>(k) + 1.0f) - 1.0f) * 0.5f);
         while (j * (j + 1) / 2 > k) --j;
         while ((j + 1) * (j + 2) / 2 <= k) ++j;
@@ -210,7 +213,7 @@ __device__ __forceinline__ void ortho_store8(float4* a, float4* b, const F2 (&v)
 // or as rows that are not vectors.
 template <int MODE>
 __device__ __forceinline__ bool ortho_again(const OrthoParams& p, const OrthoTile& t) {
-    if constexpr (MODE < kStep) return t.i != t.j;
+    if constexpr (MODE < kStep) return !p.full && t.i != t.j;
     else return MODE == kLast && (p.tall || !p.vec);
 }
 // Four columns of one row to the result's transpose (lanes: neighbouring rows).
@@ -305,6 +308,7 @@ __device__ __forceinline__ void ortho_blocks(const OrthoParams& p, int32_t s, co
         tmem_ld_32x32b_x32(taddr + c * 32, r);
         tmem_ld_wait();
         ortho_block<MODE>(p, s, t, row0, col0 + c * 32, r, in0, buf);
+        if (c + 1 >= blocks) break;
         if (c + 2 < blocks) ortho_read_block<MODE>(p, s, t.b, row0, col0 + c * 32 + 64, in0);
         __syncwarp();
         tmem_ld_32x32b_x32(taddr + c * 32 + 32, r);
@@ -313,11 +317,11 @@ __device__ __forceinline__ void ortho_blocks(const OrthoParams& p, int32_t s, co
         if (c + 3 < blocks) ortho_read_block<MODE>(p, s, t.b, row0, col0 + c * 32 + 96, in1);
     }
 }
-// Blocks of 32 columns (an even number: sides are multiples of 64) from col0 on.
+// Blocks of 32 columns from col0 on, of at most `most`.
 template <int MODE>
-__device__ __forceinline__ int32_t ortho_block_count(const OrthoParams& p, int32_t row0, int32_t col0) {
-    const int32_t cols = MODE < kStep ? p.np : p.mp;
-    return row0 >= p.np || col0 >= cols ? 0 : cols - col0 < 128 ? (cols - col0) >> 5 : 4;
+__device__ __forceinline__ int32_t ortho_block_count(const OrthoParams& p, int32_t row0, int32_t col0, int32_t most) {
+    const int32_t left = ((MODE < kStep ? p.np : p.mp) - col0) >> 5;
+    return row0 >= p.np || left <= 0 ? 0 : left < most ? left : most;
 }
 
 __device__ __forceinline__ void ortho_give_up(const OrthoParams& p, volatile int* abort_flag) {
@@ -342,19 +346,18 @@ __device__ __forceinline__ bool ortho_wait(uint64_t* bar, uint32_t parity, volat
     return false;
 }
 
-// The MMAs of one stage (128 of K) into d.
-template <int MODE, bool PAIR>
+// The MMAs of one stage (128 of K) into d: 256 x 256 on a pair, or 128 x NB.
+template <int MODE, bool PAIR, int NB>
 __device__ __forceinline__ void ortho_mma(uint32_t d, uint32_t sa, bool first) {
     constexpr bool kMN = MODE == kStep || MODE == kLast;      // B's K along its rows
-    constexpr uint32_t kSide = PAIR ? 256 : 128;
-    constexpr uint32_t idesc = instr_desc(0, false, kMN, kSide, kSide);
+    constexpr uint32_t idesc = instr_desc(0, false, kMN, PAIR ? 256 : 128, NB);
+    constexpr uint32_t kRows = PAIR ? NB / 2 : NB;            // of B in this CTA's memory
     const uint32_t sb = sa + kOrthoBox;
     #pragma unroll
     for (uint32_t kk = 0; kk < 8; ++kk) {
-        const uint32_t km = (kk >> 2) * 16384u + (kk & 3u) * 32u;
-        const uint64_t ad = smem_desc_sw128(sa + km, 16u, 1024u);
+        const uint64_t ad = smem_desc_sw128(sa + (kk >> 2) * 16384u + (kk & 3u) * 32u, 16u, 1024u);
         const uint64_t bd = kMN ? smem_desc_sw128(sb + kk * 2048u, 16384u, 1024u)
-                                : smem_desc_sw128(sb + km, 16u, 1024u);
+                                : smem_desc_sw128(sb + (kk >> 2) * (kRows * 128u) + (kk & 3u) * 32u, 16u, 1024u);
         const uint32_t acc = first && kk == 0 ? 0u : 1u;
         if constexpr (PAIR) tc_mma_f16_pair(d, ad, bd, idesc, acc);
         else tc_mma_f16(d, ad, bd, idesc, acc);
@@ -409,13 +412,11 @@ template <int MODE>
 __device__ __forceinline__ bool ortho_epilogue(const OrthoParams& p, int32_t s, const OrthoTile& t, int32_t row0,
                                                int32_t col0, uint32_t taddr, uint64_t* acc_full, uint32_t parity,
                                                float4* turn, volatile int* abort_flag) {
-    const int32_t blocks = ortho_block_count<MODE>(p, row0, col0);
+    const int32_t blocks = ortho_block_count<MODE>(p, row0, col0, 4);
     // inputs are on their way before the accumulator is there
     OrthoIn<MODE> in0[4], in1[4];
-    if (blocks > 0) {
-        ortho_read_block<MODE>(p, s, t.b, row0, col0, in0);
-        ortho_read_block<MODE>(p, s, t.b, row0, col0 + 32, in1);
-    }
+    if (blocks > 0) ortho_read_block<MODE>(p, s, t.b, row0, col0, in0);
+    if (blocks > 1) ortho_read_block<MODE>(p, s, t.b, row0, col0 + 32, in1);
     if (!ortho_wait(acc_full, parity, abort_flag, p)) return false;
     __syncwarp();
     tc_fence_after_sync();
@@ -537,8 +538,8 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                             ok = ortho_wait(&full[s], round & 1u, &abort_flag, p);
                             if (!ok) break;
                             tc_fence_after_sync();
-                            if (mode >= kStep) ortho_mma<kStep, true>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
-                            else ortho_mma<kGram, true>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
+                            if (mode >= kStep) ortho_mma<kStep, true, 256>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
+                            else ortho_mma<kGram, true, 256>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
                             tc_commit_pair_multicast(&empty[s], 3);
                         }
                         if (ok) tc_commit_pair_multicast(&acc_full[buf], 3);
@@ -612,11 +613,13 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
 
 // ------------------------------------------------------- one tile per cluster
 
-template <int MODE>
+// NB: its columns, 128, or 64 (kStep, kLast) or 32.
+template <int MODE, int NB>
 __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     ortho_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ OrthoParams p) {
     constexpr bool kMN = MODE == kStep || MODE == kLast;
+    static_assert(NB == 128 || NB == (kMN ? 64 : 32), "a K-major B has boxes of any rows, the other of 64 columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -646,7 +649,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         tma_prefetch_desc(&tmB);
     }
     if (warp == 1) {
-        tmem_alloc(tmem_slot, 128);
+        tmem_alloc(tmem_slot, NB);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -661,8 +664,8 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     // inputs are on their way while the products run.
     const int quarter = warp & 3;
     const int32_t row0 = t.i * 128 + quarter * 32, log8 = p.log_width - 3;
-    const int32_t blocks = S > 1 ? 0 : ortho_block_count<MODE>(p, row0, t.j * 128);
-    const int32_t col_s = t.j * 128 + (static_cast<int32_t>(rank) << p.log_width);
+    const int32_t blocks = S > 1 ? 0 : ortho_block_count<MODE>(p, row0, t.j * NB, NB / 32);
+    const int32_t col_s = t.j * NB + (static_cast<int32_t>(rank) << p.log_width);
     auto unit = [&](int32_t k, int32_t& rr, int32_t& g) {       // (by rows)
         const int32_t e = k * 128 + static_cast<int32_t>(threadIdx.x) - 64;
         g = e & ((1 << log8) - 1);
@@ -671,10 +674,8 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     };
     OrthoIn<MODE> in0[4], in1[4];
     if (warp >= 2) {
-        if (blocks > 0) {
-            ortho_read_block<MODE>(p, step, t.b, row0, t.j * 128, in0);
-            ortho_read_block<MODE>(p, step, t.b, row0, t.j * 128 + 32, in1);
-        }
+        if (blocks > 0) ortho_read_block<MODE>(p, step, t.b, row0, t.j * NB, in0);
+        if (blocks > 1) ortho_read_block<MODE>(p, step, t.b, row0, t.j * NB + 32, in1);
         if (S > 1) {
             #pragma unroll
             for (int32_t k = 0; k < 4; ++k) {
@@ -692,11 +693,11 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                 const uint32_t s = armed % kOrthoStages, round = armed / kOrthoStages;
                 if (!ortho_wait(&empty[s], (round & 1u) ^ 1u, &abort_flag, p)) break;
                 uint8_t* sa = smem + s * kOrthoStage;
-                mbar_arrive_expect_tx(&full[s], kOrthoStage);
+                mbar_arrive_expect_tx(&full[s], kOrthoBox + NB * 256u);
                 if ((p.debug_flags & 1u) && armed == 0 && blockIdx.x == 0) continue;   // test hook: no load
                 tma_load_4d(sa, &tmA, &full[s], 0, t.i * 128, kb * 2, t.b, keep);
-                if constexpr (kMN) tma_load_4d(sa + kOrthoBox, &tmB, &full[s], 0, kb * 128, t.j * 2, t.b, keep);
-                else tma_load_4d(sa + kOrthoBox, &tmB, &full[s], 0, t.j * 128, kb * 2, t.b, keep);
+                if constexpr (kMN) tma_load_4d(sa + kOrthoBox, &tmB, &full[s], 0, kb * 128, t.j * (NB / 64), t.b, keep);
+                else tma_load_4d(sa + kOrthoBox, &tmB, &full[s], 0, t.j * NB, kb * 2, t.b, keep);
             }
             // every load has landed before the memory is written again or the CTA ends
             for (uint32_t s = 0; s < kOrthoStages; ++s) {
@@ -713,7 +714,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                 const uint32_t s = used % kOrthoStages, round = used / kOrthoStages;
                 if (!ortho_wait(&full[s], round & 1u, &abort_flag, p)) break;
                 tc_fence_after_sync();
-                ortho_mma<MODE, false>(tmem, base + s * kOrthoStage, used == 0);
+                ortho_mma<MODE, false, NB>(tmem, base + s * kOrthoStage, used == 0);
                 tc_commit(&empty[s]);
             }
             tc_commit(done);
@@ -739,7 +740,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         if (warp >= 2) {
             const bool any = kb1 > kb0;                      // (a CTA without a K block adds zeros)
             #pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = 0; c < NB; c += 32) {
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(taddr + c, r);
                 tmem_ld_wait();
@@ -813,12 +814,12 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         }
     } else if (warp >= 2 && !abort_flag) {
         float4* turn = reinterpret_cast<float4*>(smem) + (warp - 2) * 256;      // the stages are free
-        ortho_blocks<MODE>(p, step, t, row0, t.j * 128, blocks, taddr, in0, in1, turn);
+        ortho_blocks<MODE>(p, step, t, row0, t.j * NB, blocks, taddr, in0, in1, turn);
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 1) tmem_dealloc(tmem, 128);
+    if (warp == 1) tmem_dealloc(tmem, NB);
 }
 
 }  // namespace gemm103
