@@ -291,8 +291,8 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
 
 struct Maps {
     CUtensorMap x[2], a, b;              // boxes of 128 rows by two chunks
-    CUtensorMap x_few[2], a_few;         // for narrow tiles: of 32 rows, K-major
-    CUtensorMap x_narrow[2];             // of one chunk
+    CUtensorMap x_few[2], a_few;         // narrow tiles' K-major B: of as many rows as columns
+    CUtensorMap x_narrow[2];             // kStep's: of one chunk
 };
 
 // Products [p.first, p.last) on CTA pairs.  More than one: a cooperative launch.
@@ -352,7 +352,7 @@ cudaError_t launch_tile(const OrthoCall& c, const CUtensorMap& a, const CUtensor
 
 struct Schedule {
     bool pair;
-    bool narrow;                             // not pair: tiles of 32 or 64 columns
+    int32_t width;                           // columns of a tile
     int32_t tiles, tiles_i, splits;
 };
 
@@ -364,10 +364,10 @@ struct Schedule {
 Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols, int64_t k_blocks) {
     Schedule best = {};
     int64_t least = INT64_MAX;
-    auto consider = [&](bool pair, bool narrow, int32_t splits) {
-        const int64_t side = pair ? 256 : 128, width = narrow ? (symmetric ? 32 : 64) : side;
+    auto consider = [&](bool pair, int32_t width, int32_t splits) {
+        const int64_t side = pair ? 256 : 128;
         const int64_t i = (rows + side - 1) / side, j = (cols + width - 1) / width;
-        const int64_t tiles = symmetric && !narrow ? i * (i + 1) / 2 : i * j;
+        const int64_t tiles = symmetric && width == side ? i * (i + 1) / 2 : i * j;
         int64_t cycles;
         if (pair) {
             const int64_t blocks = k_blocks * 1024, pairs = c.sms / 2;
@@ -379,28 +379,29 @@ Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols
         }
         if (cycles < least) {
             least = cycles;
-            best = Schedule{pair, narrow, static_cast<int32_t>(tiles), static_cast<int32_t>(i), splits};
+            best = Schedule{pair, width, static_cast<int32_t>(tiles), static_cast<int32_t>(i), splits};
         }
     };
-    consider(true, false, 1);
-    for (int32_t n = 1; n <= 8 && n <= k_blocks; n *= 2) {
-        consider(false, false, n);
-        if (n <= 4) consider(false, true, n);        // (8 columns at least to finish)
-    }
+    consider(true, 256, 1);
+    for (int32_t width = 128; width >= (symmetric ? 32 : 64); width /= 2)
+        for (int32_t n = 1; n <= 8 && n <= k_blocks && n * 8 <= width; n *= 2)       // (8 columns at least to finish)
+            consider(false, width, n);
     return best;
 }
 
 template <int MODE>
 cudaError_t product(const OrthoCall& c, const Schedule& s, const CUtensorMap& a, const CUtensorMap& b,
                     const CUtensorMap& b_narrow, OrthoParams p) {
-    constexpr int kNarrow = MODE < kStep ? 32 : 64;
     p.tiles_sym = p.tiles_step = s.tiles;
     p.tiles_i_step = s.tiles_i;
-    p.full = s.narrow;
+    p.full = s.width < 128;
     p.splits = s.splits;
-    p.log_width = !s.narrow ? 7 : MODE < kStep ? 5 : 6;
+    p.log_width = s.width == 128 ? 7 : s.width == 64 ? 6 : 5;
     for (int32_t n = s.splits; n > 1; n >>= 1) --p.log_width;
-    return s.narrow ? launch_tile<MODE, kNarrow>(c, a, b_narrow, p) : launch_tile<MODE, 128>(c, a, b, p);
+    if (s.width == 128) return launch_tile<MODE, 128>(c, a, b, p);
+    if constexpr (MODE < kStep)
+        if (s.width == 32) return launch_tile<MODE, 32>(c, a, b_narrow, p);
+    return launch_tile<MODE, 64>(c, a, b_narrow, p);
 }
 
 template <typename T>
@@ -479,10 +480,10 @@ cudaError_t run(const OrthoCall& c) {
     std::memcpy(p.abc, c.opt->coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
     bool ok = true;
     for (int i = 0; i < 2; ++i) {
-        if (sched[0].narrow) ok = ok && encode_map(c, &m.x_few[i], hi[i], l.np, l.mp, 32, 2);
-        if (sched[2].narrow) ok = ok && encode_map(c, &m.x_narrow[i], hi[i], l.np, l.mp, 128, 1);
+        if (sched[0].width < 128) ok = ok && encode_map(c, &m.x_few[i], hi[i], l.np, l.mp, sched[0].width, 2);
+        if (sched[2].width < 128) ok = ok && encode_map(c, &m.x_narrow[i], hi[i], l.np, l.mp, 128, 1);
     }
-    if (sched[1].narrow) ok = ok && encode_map(c, &m.a_few, a, l.np, l.np, 32, 2);
+    if (sched[1].width < 128) ok = ok && encode_map(c, &m.a_few, a, l.np, l.np, sched[1].width, 2);
     if (!ok) return cudaErrorInvalidValue;
     auto square = [](int64_t side) { return (side + 255) / 256; };
     p.tiles_sym = static_cast<int32_t>(square(l.np) * (square(l.np) + 1) / 2);

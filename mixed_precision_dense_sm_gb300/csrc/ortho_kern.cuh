@@ -23,8 +23,8 @@
 // another without a gap (16 x 1023 x 777, 76 pairs: 38 rounds of tiles for 50, and one
 // launch for 15).  ortho_tile_kernel: one tile of 128 rows and 128 columns per
 // cluster, whose 1 to 8 CTAs split K and add up through distributed shared memory, for
-// few tiles; for fewer still 64 columns (kStep, kLast) or 32, which shortens the
-// epilogue, and all tiles of the symmetric products, without mirroring.
+// few tiles; for fewer still 64 or 32 columns, which shortens the epilogue, and all
+// tiles of the symmetric products, without mirroring.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -613,13 +613,14 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
 
 // ------------------------------------------------------- one tile per cluster
 
-// NB: its columns, 128, or 64 (kStep, kLast) or 32.
+// NB: its columns, 32 (not for kStep and kLast, whose B has boxes of 64 columns), 64 or
+// 128.
 template <int MODE, int NB>
 __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     ortho_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ OrthoParams p) {
     constexpr bool kMN = MODE == kStep || MODE == kLast;
-    static_assert(NB == 128 || NB == (kMN ? 64 : 32), "a K-major B has boxes of any rows, the other of 64 columns");
+    static_assert(NB == 128 || NB == 64 || (NB == 32 && !kMN), "columns");
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
