@@ -20,7 +20,7 @@ struct PrepParams {
     int64_t ldg, stride_g;
     int32_t rows, cols, parts;               // as stored; CTAs that sum each matrix
     int32_t vec;                             // G's rows are 16-byte vectors
-    int32_t np, mp;                          // padded sides, wide
+    int32_t xr, xc;                          // padded sides
     double* sums;                            // [batch][parts]
     int32_t* done;                           // [products][batch], zeroed for the products' kernel
     int32_t products;
@@ -161,15 +161,15 @@ __device__ __forceinline__ void store_pair8(const PrepParams& p, int64_t at, con
 
 // X = G times the factor, as hi + lo, padded with zeros.
 template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) ortho_wide_kernel(const PrepParams p) {
+__global__ void __launch_bounds__(kPrepThreads) ortho_scale_kernel(const PrepParams p) {
     __shared__ double red[kPrepThreads / 32];
     grid_dependency_wait();
     grid_dependents_launch();
     const Factor f = split_factor(ortho_factor(p, red));
     const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
-    const int64_t base = static_cast<int64_t>(blockIdx.y) * p.np * p.mp;
-    const uint32_t per_row = static_cast<uint32_t>(p.mp) >> 3;
-    const int64_t total = static_cast<int64_t>(p.np) * per_row;
+    const int64_t base = static_cast<int64_t>(blockIdx.y) * p.xr * p.xc;
+    const uint32_t per_row = static_cast<uint32_t>(p.xc) >> 3;
+    const int64_t total = static_cast<int64_t>(p.xr) * per_row;
     for (int64_t q = static_cast<int64_t>(blockIdx.x) * kPrepThreads + threadIdx.x; q < total;
          q += static_cast<int64_t>(gridDim.x) * kPrepThreads) {
         const int32_t r = static_cast<int32_t>(static_cast<uint32_t>(q) / per_row);
@@ -190,62 +190,26 @@ __global__ void __launch_bounds__(kPrepThreads) ortho_wide_kernel(const PrepPara
     }
 }
 
-// The same, transposed, by tiles of 64 x 64.
-template <typename T>
-__global__ void __launch_bounds__(kPrepThreads) ortho_tall_kernel(const PrepParams p) {
-    __shared__ double red[kPrepThreads / 32];
-    __shared__ float tile[64][65];
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const Factor f = split_factor(ortho_factor(p, red));
-    const T* g = static_cast<const T*>(p.G) + blockIdx.y * p.stride_g;
-    const int64_t base = static_cast<int64_t>(blockIdx.y) * p.np * p.mp;
-    const int32_t across = p.np >> 6, tiles = across * (p.mp >> 6);
-    const int32_t sub = (static_cast<int32_t>(threadIdx.x) & 7) * 8, line = static_cast<int32_t>(threadIdx.x) >> 3;
-    for (int32_t k = blockIdx.x; k < tiles; k += gridDim.x) {
-        const int32_t r0 = k / across * 64, c0 = k % across * 64;       // of G
-        #pragma unroll
-        for (int h = 0; h < 64; h += 32) {
-            const int32_t r = r0 + h + line;
-            float x[8];
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-            if (r < p.rows && c0 + sub < p.cols) load8<T>(g + r * p.ldg, c0 + sub, p.cols, p.vec, x);
-            #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                tile[h + line][sub + i] = r < p.rows && c0 + sub + i < p.cols ? scaled(x[i], f) : 0.0f;
-        }
-        __syncthreads();
-        #pragma unroll
-        for (int h = 0; h < 64; h += 32) {
-            float x[8];
-            #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = tile[sub + i][h + line];
-            store_pair8(p, base + static_cast<int64_t>(c0 + h + line) * p.mp + r0 + sub, x);
-        }
-        __syncthreads();
-    }
-}
-
 int64_t pad64(int64_t v) { return (v + 63) & ~static_cast<int64_t>(63); }
 int64_t up256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
 
 // Where things lie in the workspace, in bytes.
 struct Layout {
-    int64_t np, mp;
+    int64_t np, xr, xc;
     int64_t hi[2], lo, a, b, sums, done, bytes;
 };
 Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     Layout l;
-    l.np = pad64(rows < cols ? rows : cols);
-    l.mp = pad64(rows < cols ? cols : rows);
+    l.xr = pad64(rows);
+    l.xc = pad64(cols);
+    l.np = rows < cols ? l.xr : l.xc;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
         at += up256(bytes);
         return here;
     };
-    const int64_t x = batch * l.np * l.mp * 2, s = batch * l.np * l.np * 2;
+    const int64_t x = batch * l.xr * l.xc * 2, s = batch * l.np * l.np * 2;
     l.hi[0] = take(x);
     l.hi[1] = take(x);
     l.lo = take(x);
@@ -291,8 +255,8 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
 
 struct Maps {
     CUtensorMap x[2], a, b;              // boxes of 128 rows by two chunks
-    CUtensorMap x_few[2], a_few;         // narrow tiles' K-major B: of as many rows as columns
-    CUtensorMap x_narrow[2];             // kStep's: of one chunk
+    CUtensorMap x_few[2], a_few, b_few;  // narrow tiles' K-major B: of as many rows as columns
+    CUtensorMap x_narrow[2];             // narrow tiles' MN-major B: of one chunk
 };
 
 // Products [p.first, p.last) on CTA pairs.  More than one: a cooperative launch.
@@ -361,7 +325,8 @@ struct Schedule {
 // tile's blocks.  A single CTA's 128 x 128 x 128 block takes as long, for it is bound
 // by the 64 KB that it loads (64 a cycle); its epilogue 4500 and the exchange of a
 // split 7500, both as the columns, and 3000 until the first block is there.
-Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols, int64_t k_blocks) {
+Schedule schedule(const OrthoCall& c, bool symmetric, int32_t least_width, int64_t rows, int64_t cols,
+                  int64_t k_blocks) {
     Schedule best = {};
     int64_t least = INT64_MAX;
     auto consider = [&](bool pair, int32_t width, int32_t splits) {
@@ -383,7 +348,7 @@ Schedule schedule(const OrthoCall& c, bool symmetric, int64_t rows, int64_t cols
         }
     };
     consider(true, 256, 1);
-    for (int32_t width = 128; width >= (symmetric ? 32 : 64); width /= 2)
+    for (int32_t width = 128; width >= least_width; width /= 2)
         for (int32_t n = 1; n <= 8 && n <= k_blocks && n * 8 <= width; n *= 2)       // (8 columns at least to finish)
             consider(false, width, n);
     return best;
@@ -417,16 +382,10 @@ cudaError_t prepare(const OrthoCall& c, PrepParams p) {
     cudaLaunchConfig_t cfg = config(dim3(static_cast<unsigned>(parts), batch, 1), kPrepThreads, 0, c.stream, attr, 1);
     cudaError_t e = cudaLaunchKernelEx(&cfg, ortho_norm_kernel<T>, p);
     if (e != cudaSuccess) return e;
-    if (p.rows > p.cols) {
-        int64_t grid = static_cast<int64_t>(p.np / 64) * (p.mp / 64);
-        if (grid > share) grid = share;
-        cfg.gridDim = dim3(static_cast<unsigned>(grid), batch, 1);
-        return cudaLaunchKernelEx(&cfg, ortho_tall_kernel<T>, p);
-    }
-    int64_t grid = (static_cast<int64_t>(p.np) * (p.mp / 8) + 2 * kPrepThreads - 1) / (2 * kPrepThreads);
+    int64_t grid = (static_cast<int64_t>(p.xr) * (p.xc / 8) + 2 * kPrepThreads - 1) / (2 * kPrepThreads);
     if (grid > share) grid = share;
     cfg.gridDim = dim3(static_cast<unsigned>(grid), batch, 1);
-    return cudaLaunchKernelEx(&cfg, ortho_wide_kernel<T>, p);
+    return cudaLaunchKernelEx(&cfg, ortho_scale_kernel<T>, p);
 }
 
 cudaError_t run(const OrthoCall& c) {
@@ -446,7 +405,7 @@ cudaError_t run(const OrthoCall& c) {
     q.G = c.G, q.ldg = c.ldg, q.stride_g = c.stride_g;
     q.rows = static_cast<int32_t>(c.rows), q.cols = static_cast<int32_t>(c.cols);
     q.vec = vector(c.G, c.ldg, c.stride_g, es);
-    q.np = static_cast<int32_t>(l.np), q.mp = static_cast<int32_t>(l.mp);
+    q.xr = static_cast<int32_t>(l.xr), q.xc = static_cast<int32_t>(l.xc);
     q.sums = reinterpret_cast<double*>(c.ws + l.sums);
     q.eps = c.opt->eps;
     q.hi = hi[0], q.lo = lo;
@@ -457,14 +416,14 @@ cudaError_t run(const OrthoCall& c) {
     if (e != cudaSuccess) return e;
 
     Maps m;
-    if (!encode_map(c, &m.x[0], hi[0], l.np, l.mp) || !encode_map(c, &m.x[1], hi[1], l.np, l.mp) ||
+    if (!encode_map(c, &m.x[0], hi[0], l.xr, l.xc) || !encode_map(c, &m.x[1], hi[1], l.xr, l.xc) ||
         !encode_map(c, &m.a, a, l.np, l.np) || !encode_map(c, &m.b, b, l.np, l.np))
         return cudaErrorInvalidValue;
 
     OrthoParams p = {};
     p.batch = static_cast<int32_t>(c.batch);
-    p.np = q.np, p.mp = q.mp;
-    p.n = static_cast<int32_t>(tall ? c.cols : c.rows), p.m = static_cast<int32_t>(tall ? c.rows : c.cols);
+    p.np = static_cast<int32_t>(l.np), p.xr = q.xr, p.xc = q.xc;
+    p.rows = q.rows, p.cols = q.cols;
     p.tall = tall;
     p.lo = lo;
     p.O = static_cast<__nv_bfloat16*>(c.O), p.ldo = c.ldo, p.stride_o = c.stride_o;
@@ -472,23 +431,27 @@ cudaError_t run(const OrthoCall& c) {
     p.scale = c.opt->scale;
     p.err = c.err, p.wait_limit_ns = c.wait_limit_ns;
     const int32_t steps = c.opt->steps;
-    p.k_gram = static_cast<int32_t>((l.mp + 127) / 128), p.k_other = static_cast<int32_t>((l.np + 127) / 128);
-    const Schedule sched[3] = {schedule(c, true, l.np, l.np, p.k_gram), schedule(c, true, l.np, l.np, p.k_other),
-                               schedule(c, false, l.np, l.mp, p.k_other)};
+    p.k_gram = static_cast<int32_t>(((tall ? l.xr : l.xc) + 127) / 128);
+    p.k_other = static_cast<int32_t>((l.np + 127) / 128);
+    // (an MN-major B comes in boxes of 64 columns)
+    const Schedule sched[3] = {schedule(c, true, tall ? 64 : 32, l.np, l.np, p.k_gram),
+                               schedule(c, true, 32, l.np, l.np, p.k_other),
+                               schedule(c, false, 64, l.xr, l.xc, p.k_other)};
     p.steps = steps;
     p.x[0] = hi[0], p.x[1] = hi[1], p.mat_a = a, p.mat_b = b, p.done = q.done;
     std::memcpy(p.abc, c.opt->coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
     bool ok = true;
     for (int i = 0; i < 2; ++i) {
-        if (sched[0].width < 128) ok = ok && encode_map(c, &m.x_few[i], hi[i], l.np, l.mp, sched[0].width, 2);
-        if (sched[2].width < 128) ok = ok && encode_map(c, &m.x_narrow[i], hi[i], l.np, l.mp, 128, 1);
+        if (sched[0].width < 128 && !tall) ok = ok && encode_map(c, &m.x_few[i], hi[i], l.xr, l.xc, sched[0].width, 2);
+        if (sched[tall ? 0 : 2].width < 128) ok = ok && encode_map(c, &m.x_narrow[i], hi[i], l.xr, l.xc, 128, 1);
     }
     if (sched[1].width < 128) ok = ok && encode_map(c, &m.a_few, a, l.np, l.np, sched[1].width, 2);
+    if (sched[2].width < 128 && tall) ok = ok && encode_map(c, &m.b_few, b, l.np, l.np, sched[2].width, 2);
     if (!ok) return cudaErrorInvalidValue;
     auto square = [](int64_t side) { return (side + 255) / 256; };
     p.tiles_sym = static_cast<int32_t>(square(l.np) * (square(l.np) + 1) / 2);
-    p.tiles_i_step = static_cast<int32_t>(square(l.np));
-    p.tiles_step = static_cast<int32_t>(square(l.np) * square(l.mp));
+    p.tiles_i_step = static_cast<int32_t>(square(l.xr));
+    p.tiles_step = static_cast<int32_t>(square(l.xr) * square(l.xc));
     p.debug_flags = c.debug_flags;
     if (sched[0].pair && sched[1].pair && sched[2].pair) {
         p.first = 0, p.last = 3 * steps;
@@ -503,11 +466,13 @@ cudaError_t run(const OrthoCall& c) {
         } else {
             OrthoParams o = p;
             o.first = i, o.last = i + 1;
-            const CUtensorMap& x = m.x[s & 1];
-            e = k == 0          ? product<kGram>(c, sched[k], x, x, m.x_few[s & 1], o)
-                : k == 1        ? product<kPoly>(c, sched[k], m.a, m.a, m.a_few, o)
-                : s + 1 < steps ? product<kStep>(c, sched[k], m.b, x, m.x_narrow[s & 1], o)
-                                : product<kLast>(c, sched[k], m.b, x, m.x_narrow[s & 1], o);
+            const CUtensorMap &x = m.x[s & 1], &xn = m.x_narrow[s & 1];
+            if (k == 0) e = product<kGram>(c, sched[k], x, x, tall ? xn : m.x_few[s & 1], o);
+            else if (k == 1) e = product<kPoly>(c, sched[k], m.a, m.a, m.a_few, o);
+            else if (s + 1 < steps)
+                e = tall ? product<kStep>(c, sched[k], x, m.b, m.b_few, o) : product<kStep>(c, sched[k], m.b, x, xn, o);
+            else
+                e = tall ? product<kLast>(c, sched[k], x, m.b, m.b_few, o) : product<kLast>(c, sched[k], m.b, x, xn, o);
         }
         if (e != cudaSuccess) return e;
     }

@@ -1,20 +1,21 @@
 // ortho_kern.cuh -- the products of the orthogonalised update
 // (include/ortho_sm103.h) on tcgen05, with their epilogues.
 //
-// The workspace holds every matrix in the wide orientation (n x m, n <= m), both
-// sides padded with zeros to multiples of 64: products of zeros are zeros, so the
-// padding keeps itself and only the last epilogue looks at the true sizes.
+// The workspace holds every matrix as it is stored (X, xr x xc), both sides padded with
+// zeros to multiples of 64: products of zeros are zeros, so the padding keeps itself
+// and only the last epilogue looks at the true sizes.  The short side, padded, is np.
 // Everything is FP16 times a power of two, kScale = 2^11: entries of X are as small
 // as 1 / sqrt(n m), near FP16's subnormals without it, and up to 32 is held.
 //
-// One step is three products:
-//   kGram  A = X X^T            upper tiles only; each is stored twice, as it is
-//   kPoly  B = b A + c A A      and mirrored
-//   kStep  X = a X + B X        X = hi + lo; the product reads hi, from one of two
-//   kLast  O = scale (...)      buffers to the other, lo stays in place
+// One step is three products (X wide; X tall):
+//   kGram  A = X X^T;  X^T X        upper tiles only; each is stored twice, as it is
+//   kPoly  B = b A + c A A          and mirrored
+//   kStep  X = a X + B X;  X B      X = hi + lo; the product reads hi, from one of two
+//   kLast  O = scale (...)          buffers to the other, lo stays in place
 // Operands come as boxes of 128 rows by two K chunks (32 KB) through 4-D maps (64
-// elements, rows, chunk, matrix).  In the first two both operands are K-major; in
-// kStep the right one is X with K along its rows (MN-major), a box of the same map.
+// elements, rows, chunk, matrix).  The same box is 128 rows of a K-major operand, or
+// 128 columns of one with K along its rows (MN-major): both in the tall kGram, the
+// right one in the wide kStep.
 //
 // Two kernels.  ortho_pair_kernel: 256 x 256 tiles on CTA pairs, double-buffered
 // accumulators, for many tiles; it runs through a range of products, of all the steps
@@ -59,7 +60,7 @@ constexpr int kOrthoTileThreads = 192;               // warp 0 TMA, 1 MMA, 2-5 e
 // or kLast in the last step.
 struct OrthoParams {
     int32_t batch;                      // matrices
-    int32_t np, mp;                     // padded sides
+    int32_t np, xr, xc;                 // padded: the short side; X's rows and columns
     int32_t k_gram, k_other;            // pairs of K chunks
     int32_t steps, first, last;
     int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; along its rows
@@ -68,7 +69,7 @@ struct OrthoParams {
     __half *x[2], *lo, *mat_a, *mat_b;  // X's first numbers before even and odd steps
     __nv_bfloat16* O;                   // kLast
     int64_t ldo, stride_o;
-    int32_t n, m, tall, vec;            // true sides (wide); O transposed; O's rows are vectors
+    int32_t rows, cols, tall, vec;      // true sides; rows > cols; O's rows are vectors
     float scale;
     int32_t* done;                      // [product][matrix]: epilogue warps through with it
     int* err;
@@ -122,11 +123,15 @@ template <int MODE>
 struct OrthoIn {
     uint4 x, y;
 };
-// Whether a row and a column lie in the padded matrix: with sides of multiples of 64,
-// whole blocks of 32 do or do not.
+// The padded sides of a product's result: multiples of 64, so that whole blocks of 32
+// lie in it or do not.
+template <int MODE>
+__device__ __forceinline__ int32_t ortho_rows(const OrthoParams& p) { return MODE < kStep ? p.np : p.xr; }
+template <int MODE>
+__device__ __forceinline__ int32_t ortho_cols(const OrthoParams& p) { return MODE < kStep ? p.np : p.xc; }
 template <int MODE>
 __device__ __forceinline__ bool ortho_inside(const OrthoParams& p, int32_t row, int32_t col) {
-    return row < p.np && col < (MODE < kStep ? p.np : p.mp);
+    return row < ortho_rows<MODE>(p) && col < ortho_cols<MODE>(p);
 }
 template <int MODE>
 __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col) {
@@ -135,7 +140,7 @@ __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_
     if constexpr (MODE == kPoly) {
         in.x = __ldcg(reinterpret_cast<const uint4*>(p.mat_a + (static_cast<int64_t>(b) * p.np + row) * p.np + col));
     } else if constexpr (MODE != kGram) {
-        const int64_t at = (static_cast<int64_t>(b) * p.np + row) * p.mp + col;
+        const int64_t at = (static_cast<int64_t>(b) * p.xr + row) * p.xc + col;
         in.x = __ldcg(reinterpret_cast<const uint4*>(p.x[s & 1] + at));
         in.y = __ldcg(reinterpret_cast<const uint4*>(p.lo + at));
     }
@@ -173,16 +178,16 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, in
             half8(h, x);
             #pragma unroll
             for (int i = 0; i < 4; ++i) y[i] = fma2(x[i], mk2(-1.0f), v[i]);
-            const int64_t at = (static_cast<int64_t>(b) * p.np + row) * p.mp + col;
+            const int64_t at = (static_cast<int64_t>(b) * p.xr + row) * p.xc + col;
             *reinterpret_cast<uint4*>(p.x[(s & 1) ^ 1] + at) = h;
             *reinterpret_cast<uint4*>(p.lo + at) = pack8(y);
         } else {
             const F2 scale = mk2(p.scale);
             #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], mk2(kDown)), scale);
-            if (!p.tall && p.vec && row < p.n && col < p.m) {
+            if (p.vec && row < p.rows && col < p.cols) {
                 __nv_bfloat16* d = p.O + b * p.stride_o + row * p.ldo + col;
-                if (col + 8 <= p.m) {
+                if (col + 8 <= p.cols) {
                     *reinterpret_cast<uint4*>(d) = make_uint4(pack2<__nv_bfloat16>(v[0]), pack2<__nv_bfloat16>(v[1]),
                                                               pack2<__nv_bfloat16>(v[2]), pack2<__nv_bfloat16>(v[3]));
                 } else {
@@ -190,8 +195,8 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, in
                     for (int i = 0; i < 4; ++i) {
                         float lo, hi;
                         get2(v[i], lo, hi);
-                        if (col + 2 * i < p.m) d[2 * i] = __float2bfloat16_rn(lo);
-                        if (col + 2 * i + 1 < p.m) d[2 * i + 1] = __float2bfloat16_rn(hi);
+                        if (col + 2 * i < p.cols) d[2 * i] = __float2bfloat16_rn(lo);
+                        if (col + 2 * i + 1 < p.cols) d[2 * i + 1] = __float2bfloat16_rn(hi);
                     }
                 }
             }
@@ -209,37 +214,21 @@ __device__ __forceinline__ void ortho_store8(float4* a, float4* b, const F2 (&v)
     *a = x, *b = y;
 }
 
-// Whether the results are stored in another way too, or only: mirrored, transposed,
-// or as rows that are not vectors.
+// Whether the results are stored in another way too, mirrored, or only in another,
+// as rows that are not vectors.
 template <int MODE>
 __device__ __forceinline__ bool ortho_again(const OrthoParams& p, const OrthoTile& t) {
     if constexpr (MODE < kStep) return !p.full && t.i != t.j;
-    else return MODE == kLast && (p.tall || !p.vec);
+    else return MODE == kLast && !p.vec;
 }
-// Four columns of one row to the result's transpose (lanes: neighbouring rows).
+// Four columns of one row to the mirrored place (lanes: neighbouring rows).
 template <int MODE>
 __device__ __forceinline__ void ortho_mirror(const OrthoParams& p, int32_t b, int32_t row, int32_t col, float4 v) {
-    if constexpr (MODE == kLast) {
-        if (row >= p.n) return;
-        __nv_bfloat16* d = p.O + b * p.stride_o + col * p.ldo + row;
-        if (col + 4 <= p.m) {
-            d[0] = __float2bfloat16_rn(v.x);
-            d[p.ldo] = __float2bfloat16_rn(v.y);
-            d[2 * p.ldo] = __float2bfloat16_rn(v.z);
-            d[3 * p.ldo] = __float2bfloat16_rn(v.w);
-            return;
-        }
-        if (col < p.m) d[0] = __float2bfloat16_rn(v.x);
-        if (col + 1 < p.m) d[p.ldo] = __float2bfloat16_rn(v.y);
-        if (col + 2 < p.m) d[2 * p.ldo] = __float2bfloat16_rn(v.z);
-        if (col + 3 < p.m) d[3 * p.ldo] = __float2bfloat16_rn(v.w);
-    } else {
-        __half* d = (MODE == kGram ? p.mat_a : p.mat_b) + (static_cast<int64_t>(b) * p.np + col) * p.np + row;
-        d[0] = __float2half_rn(v.x);
-        d[p.np] = __float2half_rn(v.y);
-        d[2 * p.np] = __float2half_rn(v.z);
-        d[3 * p.np] = __float2half_rn(v.w);
-    }
+    __half* d = (MODE == kGram ? p.mat_a : p.mat_b) + (static_cast<int64_t>(b) * p.np + col) * p.np + row;
+    d[0] = __float2half_rn(v.x);
+    d[p.np] = __float2half_rn(v.y);
+    d[2 * p.np] = __float2half_rn(v.z);
+    d[3 * p.np] = __float2half_rn(v.w);
 }
 
 // A warp's 32 rows (the first is row0) and 32 columns: `r` one row per lane, from
@@ -266,17 +255,15 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, con
     }
     if (!again) return;
     __syncwarp();
-    if (MODE == kLast && !p.tall) {
+    if constexpr (MODE == kLast) {
         // rows that are not vectors: a row at a time, one element per lane
-        if constexpr (MODE == kLast) {
-            const float* f = reinterpret_cast<const float*>(buf);
-            const int32_t col = col0 + lane;
-            __nv_bfloat16* d = p.O + t.b * p.stride_o + col;
-            #pragma unroll 4
-            for (int k = 0; k < 32; ++k)
-                if (row0 + k < p.n && col < p.m)
-                    d[(row0 + k) * p.ldo] = __float2bfloat16_rn(f[k * 32 + (((lane >> 2) ^ (k & 7)) << 2) + (lane & 3)]);
-        }
+        const float* f = reinterpret_cast<const float*>(buf);
+        const int32_t col = col0 + lane;
+        __nv_bfloat16* d = p.O + t.b * p.stride_o + col;
+        #pragma unroll 4
+        for (int k = 0; k < 32; ++k)
+            if (row0 + k < p.rows && col < p.cols)
+                d[(row0 + k) * p.ldo] = __float2bfloat16_rn(f[k * 32 + (((lane >> 2) ^ (k & 7)) << 2) + (lane & 3)]);
     } else {
         #pragma unroll 2
         for (int u = 0; u < 8; ++u) ortho_mirror<MODE>(p, t.b, row0 + lane, col0 + 4 * u, buf[lane * 8 + (u ^ l7)]);
@@ -320,8 +307,8 @@ __device__ __forceinline__ void ortho_blocks(const OrthoParams& p, int32_t s, co
 // Blocks of 32 columns from col0 on, of at most `most`.
 template <int MODE>
 __device__ __forceinline__ int32_t ortho_block_count(const OrthoParams& p, int32_t row0, int32_t col0, int32_t most) {
-    const int32_t left = ((MODE < kStep ? p.np : p.mp) - col0) >> 5;
-    return row0 >= p.np || left <= 0 ? 0 : left < most ? left : most;
+    const int32_t left = (ortho_cols<MODE>(p) - col0) >> 5;
+    return row0 >= ortho_rows<MODE>(p) || left <= 0 ? 0 : left < most ? left : most;
 }
 
 __device__ __forceinline__ void ortho_give_up(const OrthoParams& p, volatile int* abort_flag) {
@@ -346,22 +333,28 @@ __device__ __forceinline__ bool ortho_wait(uint64_t* bar, uint32_t parity, volat
     return false;
 }
 
-// The MMAs of one stage (128 of K) into d: 256 x 256 on a pair, or 128 x NB.
-template <int MODE, bool PAIR, int NB>
+// The MMAs of one stage (128 of K) into d: 256 x 256 on a pair, or 128 x NB.  AMN, BMN:
+// the operand's K is along its rows.
+template <bool AMN, bool BMN, bool PAIR, int NB>
 __device__ __forceinline__ void ortho_mma(uint32_t d, uint32_t sa, bool first) {
-    constexpr bool kMN = MODE == kStep || MODE == kLast;      // B's K along its rows
-    constexpr uint32_t idesc = instr_desc(0, false, kMN, PAIR ? 256 : 128, NB);
+    constexpr uint32_t idesc = instr_desc(0, AMN, BMN, PAIR ? 256 : 128, NB);
     constexpr uint32_t kRows = PAIR ? NB / 2 : NB;            // of B in this CTA's memory
     const uint32_t sb = sa + kOrthoBox;
     #pragma unroll
     for (uint32_t kk = 0; kk < 8; ++kk) {
-        const uint64_t ad = smem_desc_sw128(sa + (kk >> 2) * 16384u + (kk & 3u) * 32u, 16u, 1024u);
-        const uint64_t bd = kMN ? smem_desc_sw128(sb + kk * 2048u, 16384u, 1024u)
+        const uint64_t ad = AMN ? smem_desc_sw128(sa + kk * 2048u, 16384u, 1024u)
+                                : smem_desc_sw128(sa + (kk >> 2) * 16384u + (kk & 3u) * 32u, 16u, 1024u);
+        const uint64_t bd = BMN ? smem_desc_sw128(sb + kk * 2048u, 16384u, 1024u)
                                 : smem_desc_sw128(sb + (kk >> 2) * (kRows * 128u) + (kk & 3u) * 32u, 16u, 1024u);
         const uint32_t acc = first && kk == 0 ? 0u : 1u;
         if constexpr (PAIR) tc_mma_f16_pair(d, ad, bd, idesc, acc);
         else tc_mma_f16(d, ad, bd, idesc, acc);
     }
+}
+// How a product reads its operands.
+__device__ __forceinline__ bool ortho_a_mn(const OrthoParams& p, int mode) { return mode == kGram && p.tall; }
+__device__ __forceinline__ bool ortho_b_mn(const OrthoParams& p, int mode) {
+    return p.tall ? mode == kGram : mode >= kStep;
 }
 
 // ------------------------------------------------------------------- CTA pairs
@@ -478,8 +471,10 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                 for (int32_t q = p.first; q < p.last && ok; ++q) {
                     const int mode = ortho_mode(p, q);
                     const CUtensorMap* x = (q / 3) & 1 ? &map_x1 : &map_x0;
-                    const CUtensorMap* ma = mode == kGram ? x : mode == kPoly ? &map_a : &map_b;
                     const CUtensorMap* mb = mode == kPoly ? &map_a : x;
+                    const CUtensorMap* ma = mode >= kStep ? &map_b : mb;
+                    if (mode >= kStep && p.tall) ma = x, mb = &map_b;
+                    const bool amn = ortho_a_mn(p, mode), bmn = ortho_b_mn(p, mode);
                     const int32_t items = p.batch * ortho_tiles(p, mode), k_blocks = mode == kGram ? p.k_gram : p.k_other;
                     const int32_t item0 = ortho_first(before, mine, pairs);
                     before += items;
@@ -501,9 +496,9 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                             // the even CTA's barrier counts the bytes of both
                             if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kOrthoStage);
                             if ((p.debug_flags & 1u) && armed == 0 && blockIdx.x == 0) continue;   // test hook: no load
-                            tma_load_4d_pair(sa, ma, fb, 0, r0, kb * 2, t.b, keep);
-                            if (mode >= kStep) tma_load_4d_pair(sa + kOrthoBox, mb, fb, 0, kb * 128, c0 >> 6, t.b, keep);
-                            else tma_load_4d_pair(sa + kOrthoBox, mb, fb, 0, c0, kb * 2, t.b, keep);
+                            const int32_t k0 = kb * 128, kc = kb * 2;
+                            tma_load_4d_pair(sa, ma, fb, 0, amn ? k0 : r0, amn ? r0 >> 6 : kc, t.b, keep);
+                            tma_load_4d_pair(sa + kOrthoBox, mb, fb, 0, bmn ? k0 : c0, bmn ? c0 >> 6 : kc, t.b, keep);
                         }
                     }
                 }
@@ -526,6 +521,7 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                 for (int32_t q = p.first; q < p.last && ok; ++q) {
                     const int mode = ortho_mode(p, q);
                     const int32_t items = p.batch * ortho_tiles(p, mode), k_blocks = mode == kGram ? p.k_gram : p.k_other;
+                    const bool amn = ortho_a_mn(p, mode), bmn = ortho_b_mn(p, mode);
                     const int32_t item0 = ortho_first(before, mine, pairs);
                     before += items;
                     for (int32_t item = item0; item < items && ok; item += pairs, ++acc_i) {
@@ -538,8 +534,10 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                             ok = ortho_wait(&full[s], round & 1u, &abort_flag, p);
                             if (!ok) break;
                             tc_fence_after_sync();
-                            if (mode >= kStep) ortho_mma<kStep, true, 256>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
-                            else ortho_mma<kGram, true, 256>(tmem + buf * 256u, base + s * kOrthoStage, kb == 0);
+                            const uint32_t d = tmem + buf * 256u, sa = base + s * kOrthoStage;
+                            if (!bmn) ortho_mma<false, false, true, 256>(d, sa, kb == 0);
+                            else if (!amn) ortho_mma<false, true, true, 256>(d, sa, kb == 0);
+                            else ortho_mma<true, true, true, 256>(d, sa, kb == 0);
                             tc_commit_pair_multicast(&empty[s], 3);
                         }
                         if (ok) tc_commit_pair_multicast(&acc_full[buf], 3);
@@ -613,14 +611,13 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
 
 // ------------------------------------------------------- one tile per cluster
 
-// NB: its columns, 32 (not for kStep and kLast, whose B has boxes of 64 columns), 64 or
-// 128.
+// NB: its columns, 32 (not where B's boxes are of 64 columns: ortho_b_mn), 64 or 128.
 template <int MODE, int NB>
 __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     ortho_tile_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                       const __grid_constant__ OrthoParams p) {
-    constexpr bool kMN = MODE == kStep || MODE == kLast;
-    static_assert(NB == 128 || NB == 64 || (NB == 32 && !kMN), "columns");
+    static_assert(NB == 128 || NB == 64 || (NB == 32 && MODE < kStep), "columns");
+    const bool amn = ortho_a_mn(p, MODE), bmn = ortho_b_mn(p, MODE);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -696,9 +693,9 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                 uint8_t* sa = smem + s * kOrthoStage;
                 mbar_arrive_expect_tx(&full[s], kOrthoBox + NB * 256u);
                 if ((p.debug_flags & 1u) && armed == 0 && blockIdx.x == 0) continue;   // test hook: no load
-                tma_load_4d(sa, &tmA, &full[s], 0, t.i * 128, kb * 2, t.b, keep);
-                if constexpr (kMN) tma_load_4d(sa + kOrthoBox, &tmB, &full[s], 0, kb * 128, t.j * (NB / 64), t.b, keep);
-                else tma_load_4d(sa + kOrthoBox, &tmB, &full[s], 0, t.j * NB, kb * 2, t.b, keep);
+                const int32_t k0 = kb * 128, kc = kb * 2;
+                tma_load_4d(sa, &tmA, &full[s], 0, amn ? k0 : t.i * 128, amn ? t.i * 2 : kc, t.b, keep);
+                tma_load_4d(sa + kOrthoBox, &tmB, &full[s], 0, bmn ? k0 : t.j * NB, bmn ? t.j * (NB / 64) : kc, t.b, keep);
             }
             // every load has landed before the memory is written again or the CTA ends
             for (uint32_t s = 0; s < kOrthoStages; ++s) {
@@ -715,7 +712,16 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                 const uint32_t s = used % kOrthoStages, round = used / kOrthoStages;
                 if (!ortho_wait(&full[s], round & 1u, &abort_flag, p)) break;
                 tc_fence_after_sync();
-                ortho_mma<MODE, false, NB>(tmem, base + s * kOrthoStage, used == 0);
+                const uint32_t sa = base + s * kOrthoStage;
+                if constexpr (MODE == kGram && NB > 32) {
+                    if (bmn) ortho_mma<true, true, false, NB>(tmem, sa, used == 0);
+                    else ortho_mma<false, false, false, NB>(tmem, sa, used == 0);
+                } else if constexpr (MODE >= kStep) {
+                    if (bmn) ortho_mma<false, true, false, NB>(tmem, sa, used == 0);
+                    else ortho_mma<false, false, false, NB>(tmem, sa, used == 0);
+                } else {
+                    ortho_mma<false, false, false, NB>(tmem, sa, used == 0);
+                }
                 tc_commit(&empty[s]);
             }
             tc_commit(done);
@@ -791,17 +797,15 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
             }
             if (again) {
                 __syncthreads();
-                if (MODE == kLast && !p.tall) {
-                    if constexpr (MODE == kLast) {
-                        const int32_t width = 1 << p.log_width;
-                        #pragma unroll 1
-                        for (int32_t e = threadIdx.x; e < 128 * width; e += kOrthoTileThreads) {
-                            const int32_t rr = e >> p.log_width, cc = e & (width - 1);
-                            const int32_t row = t.i * 128 + rr, col = col_s + cc;
-                            if (row < p.n && col < p.m)
-                                p.O[t.b * p.stride_o + row * p.ldo + col] =
-                                    __float2bfloat16_rn(reinterpret_cast<const float*>(at_of(0, cc >> 2, rr))[cc & 3]);
-                        }
+                if constexpr (MODE == kLast) {
+                    const int32_t width = 1 << p.log_width;
+                    #pragma unroll 1
+                    for (int32_t e = threadIdx.x; e < 128 * width; e += kOrthoTileThreads) {
+                        const int32_t rr = e >> p.log_width, cc = e & (width - 1);
+                        const int32_t row = t.i * 128 + rr, col = col_s + cc;
+                        if (row < p.rows && col < p.cols)
+                            p.O[t.b * p.stride_o + row * p.ldo + col] =
+                                __float2bfloat16_rn(reinterpret_cast<const float*>(at_of(0, cc >> 2, rr))[cc & 3]);
                     }
                 } else {
                     #pragma unroll 1
