@@ -25,7 +25,8 @@ struct PrepParams {
     int32_t* done;                           // [products][batch], zeroed for the products' kernel
     int32_t products;
     float eps;
-    __half *hi, *lo;
+    __half* hi;
+    uint8_t* lo;
 };
 
 // Eight elements of a row as FP32, zeros behind its end.
@@ -149,14 +150,15 @@ __device__ __forceinline__ Factor split_factor(double f) {
 __device__ __forceinline__ float scaled(float x, const Factor& f) { return x * f.f * f.g; }
 
 __device__ __forceinline__ void store_pair8(const PrepParams& p, int64_t at, const float (&x)[8]) {
-    alignas(16) __half h[8], l[8];
+    F2 v[4], y[4];
     #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        h[i] = __float2half_rn(x[i]);
-        l[i] = __float2half_rn(x[i] - __half2float(h[i]));
-    }
-    *reinterpret_cast<uint4*>(p.hi + at) = *reinterpret_cast<const uint4*>(h);
-    *reinterpret_cast<uint4*>(p.lo + at) = *reinterpret_cast<const uint4*>(l);
+    for (int i = 0; i < 4; ++i) v[i] = mk2(x[2 * i], x[2 * i + 1]);
+    const uint4 h = pack8(v);
+    half8(h, y);
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = mul2(fma2(y[i], mk2(-1.0f), v[i]), mk2(kLoScale));
+    *reinterpret_cast<uint4*>(p.hi + at) = h;
+    *reinterpret_cast<uint2*>(p.lo + at) = pack_low8(y);
 }
 
 // X = G times the factor, as hi + lo, padded with zeros.
@@ -196,7 +198,7 @@ int64_t up256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
 // Where things lie in the workspace, in bytes.
 struct Layout {
     int64_t np, xr, xc;
-    int64_t hi[2], lo, a, b, sums, done, bytes;
+    int64_t hi[2], lo, a, b, diag, sums, done, bytes;
 };
 Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     Layout l;
@@ -212,9 +214,10 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     const int64_t x = batch * l.xr * l.xc * 2, s = batch * l.np * l.np * 2;
     l.hi[0] = take(x);
     l.hi[1] = take(x);
-    l.lo = take(x);
+    l.lo = take(x / 2);
     l.a = take(s);
     l.b = take(s);
+    l.diag = take(batch * l.np * 4);
     l.sums = take(batch * kMostParts * 8);
     l.done = take(batch * 3 * ORTHO_MAX_STEPS * 4);
     l.bytes = at;
@@ -391,7 +394,7 @@ cudaError_t prepare(const OrthoCall& c, PrepParams p) {
 cudaError_t run(const OrthoCall& c) {
     const Layout l = layout(c.batch, c.rows, c.cols);
     __half* hi[2] = {reinterpret_cast<__half*>(c.ws + l.hi[0]), reinterpret_cast<__half*>(c.ws + l.hi[1])};
-    __half* lo = reinterpret_cast<__half*>(c.ws + l.lo);
+    uint8_t* lo = c.ws + l.lo;
     __half* a = reinterpret_cast<__half*>(c.ws + l.a);
     __half* b = reinterpret_cast<__half*>(c.ws + l.b);
     const bool tall = c.rows > c.cols;
@@ -426,6 +429,7 @@ cudaError_t run(const OrthoCall& c) {
     p.rows = q.rows, p.cols = q.cols;
     p.tall = tall;
     p.lo = lo;
+    p.diag = reinterpret_cast<float*>(c.ws + l.diag);
     p.O = static_cast<__nv_bfloat16*>(c.O), p.ldo = c.ldo, p.stride_o = c.stride_o;
     p.vec = vector(c.O, c.ldo, c.stride_o, 2);
     p.scale = c.opt->scale;

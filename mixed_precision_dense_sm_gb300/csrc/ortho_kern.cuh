@@ -12,6 +12,11 @@
 //   kPoly  B = b A + c A A          and mirrored
 //   kStep  X = a X + B X;  X B      X = hi + lo; the product reads hi, from one of two
 //   kLast  O = scale (...)          buffers to the other, lo stays in place
+// lo, at most half a step of hi, is E5M2 times kLoScale: 2^-14 of X is enough for the
+// pair, and a quarter of what kStep reads and writes beside its operands is saved.
+// B is stored without its diagonal d, which is kept in FP32 and multiplies all of X:
+// (a + d) X + (B - d) X.  The diagonal is most of B, so the roundings of B and of hi
+// weigh half as much (0.0007 to 0.0014 of the norm of O, for 0.0015 to 0.0026).
 // Operands come as boxes of 128 rows by two K chunks (32 KB) through 4-D maps (64
 // elements, rows, chunk, matrix).  The same box is 128 rows of a K-major operand, or
 // 128 columns of one with K along its rows (MN-major): both in the tall kGram, the
@@ -41,6 +46,7 @@ namespace gemm103 {
 enum : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
 
 constexpr float kOrthoScale = 2048.0f;
+constexpr float kLoScale = 1024.0f;
 constexpr int kOrthoStages = 3;
 constexpr uint32_t kOrthoBox = 32768;                // 128 rows x 128 bytes x 2 chunks
 constexpr uint32_t kOrthoStage = 2 * kOrthoBox;      // A's and B's
@@ -66,7 +72,9 @@ struct OrthoParams {
     int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; along its rows
     int32_t full;                       // symmetric products: all tiles, not the upper ones
     int32_t splits, log_width;          // ortho_tile_kernel: CTAs per tile; log2(columns / splits)
-    __half *x[2], *lo, *mat_a, *mat_b;  // X's first numbers before even and odd steps
+    __half *x[2], *mat_a, *mat_b;       // X's first numbers before even and odd steps
+    uint8_t* lo;
+    float* diag;                        // B's
     __nv_bfloat16* O;                   // kLast
     int64_t ldo, stride_o;
     int32_t rows, cols, tall, vec;      // true sides; rows > cols; O's rows are vectors
@@ -118,10 +126,33 @@ __device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
 // than its products up to a K of 2500.)  The sums take a turn through shared memory to
 // get there.
 
+// Eight low numbers, times kLoScale, and back, rounded.  E5M2 is the upper half of FP16.
+__device__ __forceinline__ void low8(uint2 u, F2 (&f)[4]) {
+    f[0] = unpack2<__half>(__byte_perm(u.x, 0u, 0x1404)), f[1] = unpack2<__half>(__byte_perm(u.x, 0u, 0x3424));
+    f[2] = unpack2<__half>(__byte_perm(u.y, 0u, 0x1404)), f[3] = unpack2<__half>(__byte_perm(u.y, 0u, 0x3424));
+}
+__device__ __forceinline__ uint32_t pack_low(F2 a) {
+    float lo, hi;
+    get2(a, lo, hi);
+    uint16_t r;
+    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint2 pack_low8(const F2 (&f)[4]) {
+    return make_uint2(pack_low(f[0]) | pack_low(f[1]) << 16, pack_low(f[2]) | pack_low(f[3]) << 16);
+}
+
 // What it reads: A (kPoly), or hi and lo.
 template <int MODE>
 struct OrthoIn {
-    uint4 x, y;
+    uint4 x;
+    uint2 y;
+};
+// ... for 32 rows and 32 columns, with d of a row (wide) or a column (tall) per lane.
+template <int MODE>
+struct OrthoBlock {
+    OrthoIn<MODE> in[4];
+    float d;
 };
 // The padded sides of a product's result: multiples of 64, so that whole blocks of 32
 // lie in it or do not.
@@ -136,22 +167,41 @@ __device__ __forceinline__ bool ortho_inside(const OrthoParams& p, int32_t row, 
 template <int MODE>
 __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col) {
     OrthoIn<MODE> in;
-    in.x = in.y = make_uint4(0u, 0u, 0u, 0u);
+    in.x = make_uint4(0u, 0u, 0u, 0u);
+    in.y = make_uint2(0u, 0u);
     if constexpr (MODE == kPoly) {
         in.x = __ldcg(reinterpret_cast<const uint4*>(p.mat_a + (static_cast<int64_t>(b) * p.np + row) * p.np + col));
     } else if constexpr (MODE != kGram) {
         const int64_t at = (static_cast<int64_t>(b) * p.xr + row) * p.xc + col;
         in.x = __ldcg(reinterpret_cast<const uint4*>(p.x[s & 1] + at));
-        in.y = __ldcg(reinterpret_cast<const uint4*>(p.lo + at));
+        in.y = __ldcg(reinterpret_cast<const uint2*>(p.lo + at));
     }
     return in;
+}
+
+// kStep's factors of X in 8 columns of a row: a + d.
+template <int MODE>
+__device__ __forceinline__ void ortho_factors(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col,
+                                              F2 (&c0)[4]) {
+    if constexpr (MODE >= kStep) {
+        const float a = p.abc[3 * s];
+        const float* d = p.diag + static_cast<int64_t>(b) * p.np;
+        if (p.tall) {
+            const float4 d0 = __ldcg(reinterpret_cast<const float4*>(d + col));
+            const float4 d1 = __ldcg(reinterpret_cast<const float4*>(d + col + 4));
+            c0[0] = mk2(a + d0.x, a + d0.y), c0[1] = mk2(a + d0.z, a + d0.w);
+            c0[2] = mk2(a + d1.x, a + d1.y), c0[3] = mk2(a + d1.z, a + d1.w);
+        } else {
+            c0[0] = c0[1] = c0[2] = c0[3] = mk2(a + __ldcg(d + row));
+        }
+    }
 }
 
 // Sums v (of scaled products) of 8 columns to the result, in v, and out to where it
 // is stored by rows.
 template <int MODE>
 __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col,
-                                             const OrthoIn<MODE>& in, F2 (&v)[4]) {
+                                             const OrthoIn<MODE>& in, const F2 (&c0)[4], F2 (&v)[4]) {
     constexpr float kDown = 1.0f / kOrthoScale;
     F2 x[4];
     if constexpr (MODE < kStep) {
@@ -160,6 +210,20 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, in
             const F2 c1 = mk2(p.abc[3 * s + 1]), c2 = mk2(p.abc[3 * s + 2] * kDown);
             #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = fma2(c1, x[i], mul2(c2, v[i]));
+            if (col <= row && row < col + 8) {
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float e[2];
+                    get2(v[i], e[0], e[1]);
+                    #pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        if (col + 2 * i + k != row) continue;
+                        p.diag[static_cast<int64_t>(b) * p.np + row] = e[k] * kDown;
+                        e[k] = 0.0f;
+                    }
+                    v[i] = mk2(e[0], e[1]);
+                }
+            }
         } else {
             #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], mk2(kDown));
@@ -167,20 +231,20 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, in
         __half* out = MODE == kGram ? p.mat_a : p.mat_b;
         *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(b) * p.np + row) * p.np + col) = pack8(v);
     } else {
-        const F2 c0 = mk2(p.abc[3 * s]);
         F2 y[4];
         half8(in.x, x);
-        half8(in.y, y);
+        low8(in.y, y);
         #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = fma2(c0, add2(x[i], y[i]), mul2(v[i], mk2(kDown)));
+        for (int i = 0; i < 4; ++i)
+            v[i] = fma2(c0[i], fma2(y[i], mk2(1.0f / kLoScale), x[i]), mul2(v[i], mk2(kDown)));
         if constexpr (MODE == kStep) {
             const uint4 h = pack8(v);
             half8(h, x);
             #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = fma2(x[i], mk2(-1.0f), v[i]);
+            for (int i = 0; i < 4; ++i) y[i] = mul2(fma2(x[i], mk2(-1.0f), v[i]), mk2(kLoScale));
             const int64_t at = (static_cast<int64_t>(b) * p.xr + row) * p.xc + col;
             *reinterpret_cast<uint4*>(p.x[(s & 1) ^ 1] + at) = h;
-            *reinterpret_cast<uint4*>(p.lo + at) = pack8(y);
+            *reinterpret_cast<uint2*>(p.lo + at) = pack_low8(y);
         } else {
             const F2 scale = mk2(p.scale);
             #pragma unroll
@@ -236,7 +300,7 @@ __device__ __forceinline__ void ortho_mirror(const OrthoParams& p, int32_t b, in
 // lies at u ^ (r & 7), which no access of 8 lanes meets twice in a bank.
 template <int MODE>
 __device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, const OrthoTile& t, int32_t row0, int32_t col0,
-                                            const uint32_t (&r)[32], const OrthoIn<MODE> (&in)[4], float4* buf) {
+                                            const uint32_t (&r)[32], const OrthoBlock<MODE>& in, float4* buf) {
     const int lane = threadIdx.x & 31, l7 = lane & 7, g = lane & 3, line = lane >> 2;
     __syncwarp();
     #pragma unroll
@@ -245,12 +309,24 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, con
                                                __uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3]));
     __syncwarp();
     const bool again = ortho_again<MODE>(p, t);
+    F2 c0[4];
+    if constexpr (MODE >= kStep) {
+        if (p.tall) {
+            #pragma unroll
+            for (int i = 0; i < 4; ++i)
+                c0[i] = mk2(__shfl_sync(0xffffffffu, in.d, g * 8 + 2 * i), __shfl_sync(0xffffffffu, in.d, g * 8 + 2 * i + 1));
+        }
+    }
     #pragma unroll
     for (int q = 0; q < 4; ++q) {
         float4* at = buf + (q * 8 + line) * 8;
         F2 v[4];
         ortho_load8(at + ((2 * g) ^ line), at + ((2 * g + 1) ^ line), v);
-        ortho_finish<MODE>(p, s, t.b, row0 + q * 8 + line, col0 + g * 8, in[q], v);
+        if constexpr (MODE >= kStep) {
+            const float d = __shfl_sync(0xffffffffu, in.d, q * 8 + line);
+            if (!p.tall) c0[0] = c0[1] = c0[2] = c0[3] = mk2(d);
+        }
+        ortho_finish<MODE>(p, s, t.b, row0 + q * 8 + line, col0 + g * 8, in.in[q], c0, v);
         if (again) ortho_store8(at + ((2 * g) ^ line), at + ((2 * g + 1) ^ line), v);
     }
     if (!again) return;
@@ -273,10 +349,12 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, con
 // The inputs of such a block.
 template <int MODE>
 __device__ __forceinline__ void ortho_read_block(const OrthoParams& p, int32_t s, int32_t b, int32_t row0, int32_t col0,
-                                                 OrthoIn<MODE> (&in)[4]) {
+                                                 OrthoBlock<MODE>& in) {
     const int lane = threadIdx.x & 31;
     #pragma unroll
-    for (int q = 0; q < 4; ++q) in[q] = ortho_read<MODE>(p, s, b, row0 + q * 8 + (lane >> 2), col0 + (lane & 3) * 8);
+    for (int q = 0; q < 4; ++q) in.in[q] = ortho_read<MODE>(p, s, b, row0 + q * 8 + (lane >> 2), col0 + (lane & 3) * 8);
+    if constexpr (MODE >= kStep)
+        in.d = p.abc[3 * s] + __ldcg(p.diag + static_cast<int64_t>(b) * p.np + (p.tall ? col0 : row0) + lane);
 }
 
 // A warp's 32 rows by up to 128 columns of a tile: `taddr` their accumulator; `in0`
@@ -286,8 +364,8 @@ __device__ __forceinline__ void ortho_read_block(const OrthoParams& p, int32_t s
 // and its body short: code that runs once per tile is bound by its fetching.
 template <int MODE>
 __device__ __forceinline__ void ortho_blocks(const OrthoParams& p, int32_t s, const OrthoTile& t, int32_t row0, int32_t col0,
-                                             int32_t blocks, uint32_t taddr, OrthoIn<MODE> (&in0)[4],
-                                             OrthoIn<MODE> (&in1)[4], float4* buf) {
+                                             int32_t blocks, uint32_t taddr, OrthoBlock<MODE>& in0,
+                                             OrthoBlock<MODE>& in1, float4* buf) {
     #pragma unroll 1
     for (int32_t c = 0; c < blocks; c += 2) {
         uint32_t r[32];
@@ -407,7 +485,7 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoParams& p, int32_t s, 
                                                float4* turn, volatile int* abort_flag) {
     const int32_t blocks = ortho_block_count<MODE>(p, row0, col0, 4);
     // inputs are on their way before the accumulator is there
-    OrthoIn<MODE> in0[4], in1[4];
+    OrthoBlock<MODE> in0, in1;
     if (blocks > 0) ortho_read_block<MODE>(p, s, t.b, row0, col0, in0);
     if (blocks > 1) ortho_read_block<MODE>(p, s, t.b, row0, col0 + 32, in1);
     if (!ortho_wait(acc_full, parity, abort_flag, p)) return false;
@@ -670,7 +748,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         rr = e >> log8;
         return k < 1 << log8 && ortho_inside<MODE>(p, t.i * 128 + rr, col_s + g * 8);
     };
-    OrthoIn<MODE> in0[4], in1[4];
+    OrthoBlock<MODE> in0, in1;
     if (warp >= 2) {
         if (blocks > 0) ortho_read_block<MODE>(p, step, t.b, row0, t.j * NB, in0);
         if (blocks > 1) ortho_read_block<MODE>(p, step, t.b, row0, t.j * NB + 32, in1);
@@ -678,7 +756,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
             #pragma unroll
             for (int32_t k = 0; k < 4; ++k) {
                 int32_t rr, g;
-                if (unit(k, rr, g)) in0[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
+                if (unit(k, rr, g)) in0.in[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
             }
         }
     }
@@ -779,7 +857,8 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                     for (int32_t k = 0; k < 4; ++k) {
                         int32_t rr, g;
                         if (!unit(k0 + k, rr, g)) continue;
-                        F2 v[4];
+                        F2 c0[4], v[4];
+                        ortho_factors<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8, c0);
                         ortho_load8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
                         #pragma unroll 2
                         for (int32_t s = 1; s < S; ++s) {
@@ -788,10 +867,10 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
                             #pragma unroll
                             for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
                         }
-                        ortho_finish<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8, in0[k], v);
+                        ortho_finish<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8, in0.in[k], c0, v);
                         // in the place of the first source's sums, which this thread alone reads
                         if (again) ortho_store8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
-                        if (unit(k0 + k + 4, rr, g)) in0[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
+                        if (unit(k0 + k + 4, rr, g)) in0.in[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
                     }
                 }
             }

@@ -4,13 +4,15 @@ kernels' roundings to 16 bits, and the bounds its tests use.
 Notation of one step: A = X X^T, B = b A + c A^2, X' = a X + B X, f(s) = a s + b s^3
 + c s^5 on the singular values s of X.
 
-First-order bound, in Frobenius norms.  With u = 2^-11 (a rounding to FP16) and t the
+First-order bound, in Frobenius norms.  With u = 2^-11 (a rounding to FP16), 2^-14 for the
+pair (half a step of hi, 2^-11, and of E5M2 of that, 2^-3) and t the
 relative error of an FP32 sum of products of the tensor core (the products' tests
 allow 1e-5 of the sum of magnitudes, at most ||X||_F^2 for A, ||A||_F^2 for A^2 and
 ||B||_F ||X||_F for B X):
     dA <= 2 u |X| ||X|| + u ||A|| + t ||X||^2             |.| the largest singular value
     dB <= (|b| + 2 |c| |A|) dA + t |c| ||A||^2 + u ||B||
-    dX' <= |X| dB + u |B| ||X|| + t ||B|| ||X|| + 2^-21 ||X'||
+    dX' <= |X| dB + u |B| ||X|| + t ||B|| ||X|| + 2^-14 ||X'||
+(B's diagonal is not rounded, and multiplies all of X: the bound holds as it is.)
 A change E of X reaches the end through the steps that are left, g = f(f(...)): in the
 singular vectors' basis its parts are multiplied by (g(s) - g(s')) / (s - s') and
 (g(s) + g(s')) / (s + s'), so by at most the largest of these."""
@@ -42,17 +44,24 @@ def _half(x):
     return (x * SCALE).float().half().double() / SCALE
 
 
+def _low(x):
+    return (x * (SCALE * 1024)).float().to(torch.float8_e5m2).double() / (SCALE * 1024)
+
+
 def rounded(G, coefficients, eps=1e-7, scale=1.0, steps=5):
-    """The same with the kernels' roundings: A and B to FP16, X a pair of FP16
-    numbers whose first enters the products."""
+    """The same with the kernels' roundings: A and B but for its diagonal to FP16, X a
+    pair of an FP16 and an E5M2 number, of which the first enters the products."""
     abc = coefficients if hasattr(coefficients[0], "__len__") else [coefficients] * steps
     X = wide(G.double())
     X = X / (X.norm() + eps)
     for i, (a, b, c) in enumerate(abc):
         hi = _half(X)
-        X = hi + _half(X - hi)
+        X = hi + _low(X - hi)
         A = _half(hi @ hi.mT)
-        X = a * X + _half(b * A + c * (A @ A)) @ hi
+        B = b * A + c * (A @ A)
+        d = B.diagonal().clone()
+        B.diagonal().zero_()
+        X = (a + d)[:, None] * X + _half(B) @ hi
     X = scale * X
     return X.mT if G.shape[-2] > G.shape[-1] else X
 
@@ -78,7 +87,7 @@ def bound(G, coefficients, eps=1e-7, scale=1.0, steps=5):
     abc = coefficients if hasattr(coefficients[0], "__len__") else [coefficients] * steps
     s = torch.linalg.svdvals(wide(G.double().cpu()))
     s = s / (s.norm() + eps)
-    all_, half = 2.0 ** -21 * float(s.norm()) * _growth(s, abc), 0.0
+    all_, half = 2.0 ** -14 * float(s.norm()) * _growth(s, abc), 0.0
     for i, (a, b, c) in enumerate(abc):
         A, B = s ** 2, b * s ** 2 + c * s ** 4
         new = a * s + B * s
@@ -88,7 +97,7 @@ def bound(G, coefficients, eps=1e-7, scale=1.0, steps=5):
         def local(u, t):
             dA = 2 * u * m(s) * n(s) + u * n(A) + t * n(s) ** 2
             dB = (abs(b) + 2 * abs(c) * m(A)) * dA + t * abs(c) * n(A) ** 2 + u * n(B)
-            return m(s) * dB + u * m(B) * n(s) + t * n(B) * n(s) + 2.0 ** -21 * n(new)
+            return m(s) * dB + u * m(B) * n(s) + t * n(B) * n(s) + 2.0 ** -14 * n(new)
 
         grow = _growth(new.abs(), abc[i + 1:])
         all_ += grow * local(U16, TC)

@@ -12,17 +12,17 @@ def test_declared():
 
 
 def test_workspace():
-    """X twice and its low part, A and B in 16 bits on sides padded to 64; the same
+    """X twice, A and B in 16 bits and X's low part in 8 on sides padded to 64; the same
     for a matrix and its transpose."""
     assert lib.ortho_workspace(0, 5, 5) == lib.ortho_workspace(2, 0, 5) == lib.ortho_workspace(2, 5, 0) == 0
     for bad in ((-1, 4, 4), (1, -4, 4), (1, 4, -4), (65536, 4, 4), (1, 65537, 4), (1, 4, 65537)):
         assert lib.ortho_workspace(*bad) == -1
     for batch, r, c in ((1, 1, 1), (3, 64, 100), (16, 1023, 777), (1, 4096, 14336), (65535, 65536, 65536)):
         n, m = (-(-v // 64) * 64 for v in sorted((r, c)))
-        least = 2 * batch * (3 * n * m + 2 * n * n)
+        least = batch * (5 * n * m + 4 * n * n)
         got = lib.ortho_workspace(batch, r, c)
         assert got == lib.ortho_workspace(batch, c, r)
-        assert least <= got <= least + 8192 + 16384 * batch
+        assert least <= got <= least + 8192 + 4 * batch * n + 16384 * batch
 
 
 def test_needs_a_handle():
