@@ -12,10 +12,10 @@
  * is the optimiser's usual choice.
  *
  * Precision.  The products are the tensor core's: FP16 operands, FP32 sums.  A and
- * b A + c A^2 but for its diagonal are rounded to FP16; the diagonal is kept in FP32.
+ * b A + c A^2 are rounded to FP16 but for their diagonals, which are kept in FP32.
  * X is carried as a pair of numbers, FP16 and E5M2 (2^-14), of which the product takes
  * the first, so that the rounding of X does not grow along the directions of small
- * singular values, which the steps enlarge.  O is off by 0.0005 to 0.002 of its norm
+ * singular values, which the steps enlarge.  O is off by 0.0003 to 0.0015 of its norm
  * besides its own rounding (0.0017), which is why O is BF16.  Values of X, A and
  * b A + c A^2 up to 32 in magnitude are held: coefficients that keep the singular
  * values near 1 stay far below.

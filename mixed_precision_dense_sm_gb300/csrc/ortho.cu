@@ -198,7 +198,7 @@ int64_t up256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
 // Where things lie in the workspace, in bytes.
 struct Layout {
     int64_t np, xr, xc;
-    int64_t hi[2], lo, a, b, diag, sums, done, bytes;
+    int64_t hi[2], lo, a, b, diag_a, diag, sums, done, bytes;
 };
 Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     Layout l;
@@ -217,6 +217,7 @@ Layout layout(int64_t batch, int64_t rows, int64_t cols) {
     l.lo = take(x / 2);
     l.a = take(s);
     l.b = take(s);
+    l.diag_a = take(batch * l.np * 4);
     l.diag = take(batch * l.np * 4);
     l.sums = take(batch * kMostParts * 8);
     l.done = take(batch * 3 * ORTHO_MAX_STEPS * 4);
@@ -429,6 +430,7 @@ cudaError_t run(const OrthoCall& c) {
     p.rows = q.rows, p.cols = q.cols;
     p.tall = tall;
     p.lo = lo;
+    p.diag_a = reinterpret_cast<float*>(c.ws + l.diag_a);
     p.diag = reinterpret_cast<float*>(c.ws + l.diag);
     p.O = static_cast<__nv_bfloat16*>(c.O), p.ldo = c.ldo, p.stride_o = c.stride_o;
     p.vec = vector(c.O, c.ldo, c.stride_o, 2);

@@ -14,9 +14,10 @@
 //   kLast  O = scale (...)          buffers to the other, lo stays in place
 // lo, at most half a step of hi, is E5M2 times kLoScale: 2^-14 of X is enough for the
 // pair, and a quarter of what kStep reads and writes beside its operands is saved.
-// B is stored without its diagonal d, which is kept in FP32 and multiplies all of X:
-// (a + d) X + (B - d) X.  The diagonal is most of B, so the roundings of B and of hi
-// weigh half as much (0.0007 to 0.0014 of the norm of O, for 0.0015 to 0.0026).
+// A and B are stored without their diagonals D and d, which are most of them, and which
+// are kept in FP32: B = b A + c (A - D)^2 + c (D A + A D) - c D^2, and (a + d) X + (B - d) X
+// with all of X.  The roundings then weigh a third as much (0.0003 to 0.001 of the norm
+// of O, for 0.0015 to 0.0026).
 // Operands come as boxes of 128 rows by two K chunks (32 KB) through 4-D maps (64
 // elements, rows, chunk, matrix).  The same box is 128 rows of a K-major operand, or
 // 128 columns of one with K along its rows (MN-major): both in the tall kGram, the
@@ -74,7 +75,7 @@ struct OrthoParams {
     int32_t splits, log_width;          // ortho_tile_kernel: CTAs per tile; log2(columns / splits)
     __half *x[2], *mat_a, *mat_b;       // X's first numbers before even and odd steps
     uint8_t* lo;
-    float* diag;                        // B's
+    float *diag_a, *diag;               // A's and B's diagonals
     __nv_bfloat16* O;                   // kLast
     int64_t ldo, stride_o;
     int32_t rows, cols, tall, vec;      // true sides; rows > cols; O's rows are vectors
@@ -148,11 +149,12 @@ struct OrthoIn {
     uint4 x;
     uint2 y;
 };
-// ... for 32 rows and 32 columns, with d of a row (wide) or a column (tall) per lane.
+// ... for 32 rows and 32 columns, with a row's and a column's part of the factors
+// (ortho_factors) per lane.
 template <int MODE>
 struct OrthoBlock {
     OrthoIn<MODE> in[4];
-    float d;
+    float row, col;
 };
 // The padded sides of a product's result: multiples of 64, so that whole blocks of 32
 // lie in it or do not.
@@ -179,21 +181,37 @@ __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_
     return in;
 }
 
-// kStep's factors of X in 8 columns of a row: a + d.
+// The factors of what is read, in 8 columns of a row: a + d of X, b + c (D + D) of A.
 template <int MODE>
 __device__ __forceinline__ void ortho_factors(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col,
                                               F2 (&c0)[4]) {
-    if constexpr (MODE >= kStep) {
-        const float a = p.abc[3 * s];
-        const float* d = p.diag + static_cast<int64_t>(b) * p.np;
-        if (p.tall) {
-            const float4 d0 = __ldcg(reinterpret_cast<const float4*>(d + col));
-            const float4 d1 = __ldcg(reinterpret_cast<const float4*>(d + col + 4));
-            c0[0] = mk2(a + d0.x, a + d0.y), c0[1] = mk2(a + d0.z, a + d0.w);
-            c0[2] = mk2(a + d1.x, a + d1.y), c0[3] = mk2(a + d1.z, a + d1.w);
-        } else {
-            c0[0] = c0[1] = c0[2] = c0[3] = mk2(a + __ldcg(d + row));
-        }
+    if constexpr (MODE == kGram) return;
+    const float* d = (MODE == kPoly ? p.diag_a : p.diag) + static_cast<int64_t>(b) * p.np;
+    const float scale = MODE == kPoly ? p.abc[3 * s + 2] : 1.0f;
+    float base = MODE == kPoly ? p.abc[3 * s + 1] : p.abc[3 * s];
+    if (MODE == kPoly || !p.tall) base = fmaf(scale, __ldcg(d + row), base);
+    if (MODE == kPoly || p.tall) {
+        const float4 d0 = __ldcg(reinterpret_cast<const float4*>(d + col));
+        const float4 d1 = __ldcg(reinterpret_cast<const float4*>(d + col + 4));
+        c0[0] = mk2(fmaf(scale, d0.x, base), fmaf(scale, d0.y, base));
+        c0[1] = mk2(fmaf(scale, d0.z, base), fmaf(scale, d0.w, base));
+        c0[2] = mk2(fmaf(scale, d1.x, base), fmaf(scale, d1.y, base));
+        c0[3] = mk2(fmaf(scale, d1.z, base), fmaf(scale, d1.w, base));
+    } else {
+        c0[0] = c0[1] = c0[2] = c0[3] = mk2(base);
+    }
+}
+
+// An element of the diagonal, whose sum counts as 0 from here on (A's was read as 0).
+template <int MODE>
+__device__ __forceinline__ void ortho_diagonal(const OrthoParams& p, int32_t s, int32_t b, int32_t row, float sum) {
+    const int64_t at = static_cast<int64_t>(b) * p.np + row;
+    const float x = sum * (1.0f / (kOrthoScale * kOrthoScale));
+    if constexpr (MODE == kGram) {
+        p.diag_a[at] = x;
+    } else {
+        const float c = p.abc[3 * s + 2], d = __ldcg(p.diag_a + at);
+        p.diag[at] = fmaf(d, fmaf(c, d, p.abc[3 * s + 1]), c * x);
     }
 }
 
@@ -207,23 +225,9 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, in
     if constexpr (MODE < kStep) {
         if constexpr (MODE == kPoly) {
             half8(in.x, x);
-            const F2 c1 = mk2(p.abc[3 * s + 1]), c2 = mk2(p.abc[3 * s + 2] * kDown);
+            const F2 c2 = mk2(p.abc[3 * s + 2] * kDown);
             #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = fma2(c1, x[i], mul2(c2, v[i]));
-            if (col <= row && row < col + 8) {
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float e[2];
-                    get2(v[i], e[0], e[1]);
-                    #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (col + 2 * i + k != row) continue;
-                        p.diag[static_cast<int64_t>(b) * p.np + row] = e[k] * kDown;
-                        e[k] = 0.0f;
-                    }
-                    v[i] = mk2(e[0], e[1]);
-                }
-            }
+            for (int i = 0; i < 4; ++i) v[i] = fma2(c0[i], x[i], mul2(c2, v[i]));
         } else {
             #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], mk2(kDown));
@@ -308,13 +312,24 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, con
         buf[lane * 8 + (u ^ l7)] = make_float4(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1]),
                                                __uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3]));
     __syncwarp();
+    if constexpr (MODE < kStep) {
+        if (row0 == col0) {
+            float* e = reinterpret_cast<float*>(buf) + lane * 32 + (((lane >> 2) ^ l7) << 2) + (lane & 3);
+            ortho_diagonal<MODE>(p, s, t.b, row0 + lane, *e);
+            *e = 0.0f;
+            __syncwarp();
+        }
+    }
     const bool again = ortho_again<MODE>(p, t);
-    F2 c0[4];
-    if constexpr (MODE >= kStep) {
-        if (p.tall) {
+    F2 col[4];
+    if constexpr (MODE != kGram) {
+        if (MODE == kPoly || p.tall) {
             #pragma unroll
             for (int i = 0; i < 4; ++i)
-                c0[i] = mk2(__shfl_sync(0xffffffffu, in.d, g * 8 + 2 * i), __shfl_sync(0xffffffffu, in.d, g * 8 + 2 * i + 1));
+                col[i] = mk2(__shfl_sync(0xffffffffu, in.col, g * 8 + 2 * i),
+                             __shfl_sync(0xffffffffu, in.col, g * 8 + 2 * i + 1));
+        } else {
+            col[0] = col[1] = col[2] = col[3] = mk2(0.0f);
         }
     }
     #pragma unroll
@@ -322,9 +337,11 @@ __device__ __forceinline__ void ortho_block(const OrthoParams& p, int32_t s, con
         float4* at = buf + (q * 8 + line) * 8;
         F2 v[4];
         ortho_load8(at + ((2 * g) ^ line), at + ((2 * g + 1) ^ line), v);
-        if constexpr (MODE >= kStep) {
-            const float d = __shfl_sync(0xffffffffu, in.d, q * 8 + line);
-            if (!p.tall) c0[0] = c0[1] = c0[2] = c0[3] = mk2(d);
+        F2 c0[4];
+        if constexpr (MODE != kGram) {
+            const F2 r = mk2(__shfl_sync(0xffffffffu, in.row, q * 8 + line));
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) c0[i] = add2(r, col[i]);
         }
         ortho_finish<MODE>(p, s, t.b, row0 + q * 8 + line, col0 + g * 8, in.in[q], c0, v);
         if (again) ortho_store8(at + ((2 * g) ^ line), at + ((2 * g + 1) ^ line), v);
@@ -353,8 +370,18 @@ __device__ __forceinline__ void ortho_read_block(const OrthoParams& p, int32_t s
     const int lane = threadIdx.x & 31;
     #pragma unroll
     for (int q = 0; q < 4; ++q) in.in[q] = ortho_read<MODE>(p, s, b, row0 + q * 8 + (lane >> 2), col0 + (lane & 3) * 8);
-    if constexpr (MODE >= kStep)
-        in.d = p.abc[3 * s] + __ldcg(p.diag + static_cast<int64_t>(b) * p.np + (p.tall ? col0 : row0) + lane);
+    if constexpr (MODE == kPoly) {
+        const float* d = p.diag_a + static_cast<int64_t>(b) * p.np + lane;
+        const float c1 = p.abc[3 * s + 1], c2 = p.abc[3 * s + 2];
+        in.row = fmaf(c2, __ldcg(d + row0), c1);
+        in.col = c2 * __ldcg(d + col0);
+    } else if constexpr (MODE >= kStep) {
+        const float* d = p.diag + static_cast<int64_t>(b) * p.np + lane;
+        in.row = p.abc[3 * s];
+        in.col = 0.0f;
+        if (p.tall) in.col = __ldcg(d + col0);
+        else in.row += __ldcg(d + row0);
+    }
 }
 
 // A warp's 32 rows by up to 128 columns of a tile: `taddr` their accumulator; `in0`
@@ -850,6 +877,19 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
         cluster_sync_all();
         if (!abort_flag) {
             const bool again = ortho_again<MODE>(p, t);
+            if constexpr (MODE < kStep) {
+                const int32_t rr = static_cast<int32_t>(threadIdx.x), cc = t.i * 128 + rr - col_s;
+                if (rr < 128 && cc >= 0 && cc < 1 << p.log_width && t.i * 128 + rr < p.np) {
+                    float sum = 0.0f;
+                    for (int32_t s = 0; s < S; ++s) {
+                        float* e = reinterpret_cast<float*>(at_of(s, cc >> 2, rr)) + (cc & 3);
+                        sum += *e;
+                        *e = 0.0f;
+                    }
+                    ortho_diagonal<MODE>(p, step, t.b, t.i * 128 + rr, sum);
+                }
+                __syncthreads();
+            }
             if (warp >= 2) {
                 #pragma unroll 1
                 for (int32_t k0 = 0; k0 < 1 << log8; k0 += 4) {

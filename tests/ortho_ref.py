@@ -12,7 +12,8 @@ allow 1e-5 of the sum of magnitudes, at most ||X||_F^2 for A, ||A||_F^2 for A^2 
     dA <= 2 u |X| ||X|| + u ||A|| + t ||X||^2             |.| the largest singular value
     dB <= (|b| + 2 |c| |A|) dA + t |c| ||A||^2 + u ||B||
     dX' <= |X| dB + u |B| ||X|| + t ||B|| ||X|| + 2^-14 ||X'||
-(B's diagonal is not rounded, and multiplies all of X: the bound holds as it is.)
+(A's and B's diagonals are not rounded, and B's multiplies all of X: the bound holds as
+it is.)
 A change E of X reaches the end through the steps that are left, g = f(f(...)): in the
 singular vectors' basis its parts are multiplied by (g(s) - g(s')) / (s - s') and
 (g(s) + g(s')) / (s + s'), so by at most the largest of these."""
@@ -49,7 +50,7 @@ def _low(x):
 
 
 def rounded(G, coefficients, eps=1e-7, scale=1.0, steps=5):
-    """The same with the kernels' roundings: A and B but for its diagonal to FP16, X a
+    """The same with the kernels' roundings: A and B but for their diagonals to FP16, X a
     pair of an FP16 and an E5M2 number, of which the first enters the products."""
     abc = coefficients if hasattr(coefficients[0], "__len__") else [coefficients] * steps
     X = wide(G.double())
@@ -57,7 +58,9 @@ def rounded(G, coefficients, eps=1e-7, scale=1.0, steps=5):
     for i, (a, b, c) in enumerate(abc):
         hi = _half(X)
         X = hi + _low(X - hi)
-        A = _half(hi @ hi.mT)
+        A = hi @ hi.mT
+        d = A.diagonal().clone()
+        A = _half(A - torch.diag(d)) + torch.diag(d)
         B = b * A + c * (A @ A)
         d = B.diagonal().clone()
         B.diagonal().zero_()

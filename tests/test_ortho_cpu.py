@@ -22,7 +22,7 @@ def test_workspace():
         least = batch * (5 * n * m + 4 * n * n)
         got = lib.ortho_workspace(batch, r, c)
         assert got == lib.ortho_workspace(batch, c, r)
-        assert least <= got <= least + 8192 + 4 * batch * n + 16384 * batch
+        assert least <= got <= least + 8192 + 8 * batch * n + 16384 * batch
 
 
 def test_needs_a_handle():
