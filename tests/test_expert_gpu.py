@@ -55,7 +55,8 @@ def test_sort(lib, T, k, E, dtype):
     check_sort(lib, choices(T, k, E, drop=0.4, seed=T), E, dtype, pitch=3)
 
 
-@pytest.mark.parametrize("T,k,E", [(131072, 1, 9), (131073, 1, 1024), (135167, 1, 500), (33792, 4, 64), (70000, 3, 2)])
+@pytest.mark.parametrize("T,k,E", [(131072, 1, 9), (131073, 1, 1024), (135167, 1, 500), (33792, 4, 64), (70000, 3, 2),
+                                   (2 ** 20, 8, 1024)])
 def test_sort_of_many_slots(lib, T, k, E):
     """Around the border of the one-launch form and of its last CTA's share, against
     torch's stable sort."""

@@ -106,6 +106,18 @@ def test_large_on_pairs(g):
             assert float((got - near).abs().max()) <= 2.0 ** -8 * float(near.abs().max())
 
 
+def test_offsets_beyond_2_to_the_31(g):
+    """The last of 34 matrices of 2^26 elements gives the bits that it gives alone."""
+    G = torch.zeros(34, 8192, 8192, dtype=BF, device="cuda")
+    G[33] = update(8192, 8192, dtype=BF, scale=1.0)
+    G[0] = update(8192, 8192, dtype=BF, scale=0.5, seed=1)
+    O = g.orthogonalize(G, steps=2)
+    for i in (0, 33):
+        assert torch.equal(O[i], g.orthogonalize(G[i], steps=2))
+    assert not O[1:33].any() and bool(O[33].any())
+    g.sync()
+
+
 def test_coefficients_steps_and_scale(g):
     G = update(96, 160)
     for steps, abc in ((1, (1.5, -0.5, 0.0)), (8, (1.5, -0.5, 0.0)), (3, (2.0, -1.5, 0.5)), (32, (1.5, -0.5, 0.0)),
