@@ -528,9 +528,8 @@ __global__ void __launch_bounds__(kRowThreads, DOT ? 2 : 4) rows_out_kernel(cons
                         store_pack<T, V, A>(out + at[j] * p.ld_rows_out + col, a.group, left, r);
                 }
             }
-            // the elements behind the last vector
-            if (a.c1 + tail == D && a.g < tail) {
-                const int32_t col = a.c1 + a.g;
+            // the elements behind the last vector, which may be more than the group's threads
+            for (int32_t col = a.c1 + a.g; a.c1 + tail == D && col < D; col += a.group) {
                 const float f = to_f<T>(x[col]);
                 #pragma unroll
                 for (int j = 0; j < kTurn; ++j) {
@@ -604,9 +603,8 @@ __global__ void __launch_bounds__(kRowThreads, DOT ? 2 : 3) rows_in_kernel(const
             for (int i = 0; i < V; ++i) o.e[i] = from_f<T>(acc[i]);
             if (!DOT || y != nullptr) store_pack<T, V, A>(y + col, a.group, left, o);
         }
-        // the elements behind the last vector
-        if (a.c1 + tail == D && a.g < tail) {
-            const int32_t col = a.c1 + a.g;
+        // the elements behind the last vector, which may be more than the group's threads
+        for (int32_t col = a.c1 + a.g; a.c1 + tail == D && col < D; col += a.group) {
             const float xf = DOT ? to_f<T>(x[col]) : 0.0f;
             float acc = 0.0f;
             for (int64_t j0 = 0;;) {
