@@ -25,7 +25,7 @@ struct PrepParams {
     int32_t* done;                           // [products][batch], zeroed for the products' kernel
     int32_t products;
     float eps;
-    __half* hi;
+    __half *hi, *down;                       // down: lo's second bytes, 8 in the place of 8 halves, or NULL
     uint8_t* lo;
 };
 
@@ -156,9 +156,12 @@ __device__ __forceinline__ void store_pair8(const PrepParams& p, int64_t at, con
     const uint4 h = pack8(v);
     half8(h, y);
     #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = mul2(fma2(y[i], mk2(-1.0f), v[i]), mk2(kLoScale));
+    for (int i = 0; i < 4; ++i) v[i] = fma2(y[i], mk2(-1.0f), v[i]);
+    uint2 up, down;
+    pack_low8(y, v, up, down);
     *reinterpret_cast<uint4*>(p.hi + at) = h;
-    *reinterpret_cast<uint2*>(p.lo + at) = pack_low8(y);
+    *reinterpret_cast<uint2*>(p.lo + at) = up;
+    if (p.down != nullptr) *reinterpret_cast<uint2*>(p.down + at) = down;
 }
 
 // X = G times the factor, as hi + lo, padded with zeros.
@@ -264,8 +267,9 @@ struct Maps {
 };
 
 // Products [p.first, p.last) on CTA pairs.  More than one: a cooperative launch.
+template <bool FINE>
 cudaError_t launch_pair(const OrthoCall& c, const Maps& m, const OrthoParams& p) {
-    auto kern = ortho_pair_kernel;
+    auto kern = ortho_pair_kernel<FINE>;
     static DeviceLimits limit;
     cudaError_t e = limit.raise(kOrthoPairSmem, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kOrthoPairSmem));
@@ -392,6 +396,21 @@ cudaError_t prepare(const OrthoCall& c, PrepParams p) {
     return cudaLaunchKernelEx(&cfg, ortho_scale_kernel<T>, p);
 }
 
+// The first steps, in which lo has its second byte: those before which a rounding of X is
+// enlarged by more than kFineFrom by the steps that are left, of singular values near 0 by
+// their a.  Below that the first byte's 2^-20, of which half is the usual error, comes to at
+// most 0.0007 of the norm of O (512; the usual five steps: 484).
+constexpr float kFineFrom = 512.0f;
+int32_t fine_steps(const ortho_update_t& opt) {
+    int32_t s = opt.steps - 1;
+    float grow = fmaxf(1.0f, fabsf(opt.coefficients[3 * s]));
+    for (; s > 0; --s) {
+        grow *= fmaxf(1.0f, fabsf(opt.coefficients[3 * (s - 1)]));
+        if (grow > kFineFrom) break;
+    }
+    return s;                                // (0 of one step)
+}
+
 cudaError_t run(const OrthoCall& c) {
     const Layout l = layout(c.batch, c.rows, c.cols);
     __half* hi[2] = {reinterpret_cast<__half*>(c.ws + l.hi[0]), reinterpret_cast<__half*>(c.ws + l.hi[1])};
@@ -412,7 +431,8 @@ cudaError_t run(const OrthoCall& c) {
     q.xr = static_cast<int32_t>(l.xr), q.xc = static_cast<int32_t>(l.xc);
     q.sums = reinterpret_cast<double*>(c.ws + l.sums);
     q.eps = c.opt->eps;
-    q.hi = hi[0], q.lo = lo;
+    const int32_t fine = fine_steps(*c.opt);
+    q.hi = hi[0], q.lo = lo, q.down = fine > 0 ? hi[1] : nullptr;
     q.done = reinterpret_cast<int32_t*>(c.ws + l.done), q.products = 3 * c.opt->steps;
     cudaError_t e = c.g_dtype == GEMM_F32    ? prepare<float>(c, q)
                     : c.g_dtype == GEMM_BF16 ? prepare<__nv_bfloat16>(c, q)
@@ -443,7 +463,7 @@ cudaError_t run(const OrthoCall& c) {
     const Schedule sched[3] = {schedule(c, true, tall ? 64 : 32, l.np, l.np, p.k_gram),
                                schedule(c, true, 32, l.np, l.np, p.k_other),
                                schedule(c, false, 64, l.xr, l.xc, p.k_other)};
-    p.steps = steps;
+    p.steps = steps, p.fine = fine;
     p.x[0] = hi[0], p.x[1] = hi[1], p.mat_a = a, p.mat_b = b, p.done = q.done;
     std::memcpy(p.abc, c.opt->coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
     bool ok = true;
@@ -461,20 +481,22 @@ cudaError_t run(const OrthoCall& c) {
     p.debug_flags = c.debug_flags;
     if (sched[0].pair && sched[1].pair && sched[2].pair) {
         p.first = 0, p.last = 3 * steps;
-        return launch_pair(c, m, p);
+        return fine > 0 ? launch_pair<true>(c, m, p) : launch_pair<false>(c, m, p);
     }
     for (int32_t i = 0; i < 3 * steps; ++i) {
         const int32_t s = i / 3, k = i % 3;
         if (i > 0) p.debug_flags = 0;
         if (sched[k].pair) {
             p.first = i, p.last = i + 1;
-            e = launch_pair(c, m, p);
+            e = k == 2 && s < fine ? launch_pair<true>(c, m, p) : launch_pair<false>(c, m, p);
         } else {
             OrthoParams o = p;
             o.first = i, o.last = i + 1;
             const CUtensorMap &x = m.x[s & 1], &xn = m.x_narrow[s & 1];
             if (k == 0) e = product<kGram>(c, sched[k], x, x, tall ? xn : m.x_few[s & 1], o);
             else if (k == 1) e = product<kPoly>(c, sched[k], m.a, m.a, m.a_few, o);
+            else if (s + 1 < steps && s < fine)
+                e = tall ? product<kFine>(c, sched[k], x, m.b, m.b_few, o) : product<kFine>(c, sched[k], m.b, x, xn, o);
             else if (s + 1 < steps)
                 e = tall ? product<kStep>(c, sched[k], x, m.b, m.b_few, o) : product<kStep>(c, sched[k], m.b, x, xn, o);
             else

@@ -11,13 +11,22 @@
 //   kGram  A = X X^T;  X^T X        upper tiles only; each is stored twice, as it is
 //   kPoly  B = b A + c A A          and mirrored
 //   kStep  X = a X + B X;  X B      X = hi + lo; the product reads hi, from one of two
-//   kLast  O = scale (...)          buffers to the other, lo stays in place
-// lo, at most half a step of hi, is E5M2 times kLoScale: 2^-14 of X is enough for the
-// pair, and a quarter of what kStep reads and writes beside its operands is saved.
-// A and B are stored without their diagonals D and d, which are most of them, and which
-// are kept in FP32: B = b A + c (A - D)^2 + c (D A + A D) - c D^2, and (a + d) X + (B - d) X
-// with all of X.  The roundings then weigh a third as much (0.0003 to 0.001 of the norm
-// of O, for 0.0015 to 0.0026).
+//   kFine  the same, finer          buffers to the other, lo stays in place
+//   kLast  O = scale (...)
+// lo, at most half a step of hi, is a byte: a 254th of a step of its own hi, so that X is
+// rounded by 2^-20 (six more operations per element than an E5M2 lo, 439 us for 423,
+// which rounds X by 2^-14; FP16, 2^-22, would be half as much again of what kStep reads and
+// writes beside its operands).  It matters because every step enlarges what a rounding left
+// in the directions of small singular values by a (3.4): rank 1, five steps, 0.0007 of the
+// norm of O (E5M2 0.007).  Where the steps that are left enlarge it by more than 512, kFine
+// carries 8 more bits (eight steps of 16 x 1023 x 777: 884 us, 615 without, and 0.1 of the
+// norm of O for 0.002).  These lie where nothing else is: before step 0 in the second buffer
+// of hi (each thread reads its own before it writes hi there), from then on in O's rows, so
+// kLast, which writes O, has none.
+// A and B are stored without their diagonals D and d, which are kept in FP32: B = b A +
+// c (A - D)^2 + c (D A + A D) - c D^2, and X' = a X + d hi + (B - d) hi.  d multiplies what
+// the rest of B multiplies, for they may cancel (with d lo beside it rank 1 was off by 0.002
+// after five steps and 0.05 after eight); O of noise is off by 0.0012 (all in FP16: 0.0026).
 // Operands come as boxes of 128 rows by two K chunks (32 KB) through 4-D maps (64
 // elements, rows, chunk, matrix).  The same box is 128 rows of a K-major operand, or
 // 128 columns of one with K along its rows (MN-major): both in the tall kGram, the
@@ -44,10 +53,10 @@
 
 namespace gemm103 {
 
-enum : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3 };
+enum : int { kGram = 0, kPoly = 1, kStep = 2, kLast = 3, kFine = 4 };
 
 constexpr float kOrthoScale = 2048.0f;
-constexpr float kLoScale = 1024.0f;
+constexpr float kLoParts = 254.0f;                   // lo's byte: parts of a step of hi
 constexpr int kOrthoStages = 3;
 constexpr uint32_t kOrthoBox = 32768;                // 128 rows x 128 bytes x 2 chunks
 constexpr uint32_t kOrthoStage = 2 * kOrthoBox;      // A's and B's
@@ -63,13 +72,13 @@ constexpr int kOrthoFewRegs = 40, kOrthoManyRegs = 232;
 static_assert(128 * kOrthoFewRegs + 256 * kOrthoManyRegs <= 384 * 168, "the launch's registers");
 constexpr int kOrthoTileThreads = 192;               // warp 0 TMA, 1 MMA, 2-5 epilogue
 
-// Products [first, last): product 3 s of step s is kGram, 3 s + 1 kPoly, 3 s + 2 kStep,
-// or kLast in the last step.
+// Products [first, last): product 3 s of step s is kGram, 3 s + 1 kPoly, 3 s + 2 kFine in
+// the first `fine` steps, then kStep, and kLast in the last step.
 struct OrthoParams {
     int32_t batch;                      // matrices
     int32_t np, xr, xc;                 // padded: the short side; X's rows and columns
     int32_t k_gram, k_other;            // pairs of K chunks
-    int32_t steps, first, last;
+    int32_t steps, fine, first, last;
     int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; along its rows
     int32_t full;                       // symmetric products: all tiles, not the upper ones
     int32_t splits, log_width;          // ortho_tile_kernel: CTAs per tile; log2(columns / splits)
@@ -126,27 +135,69 @@ __device__ __forceinline__ uint4 pack8(const F2 (&f)[4]) {
 // lanes, eight: 33 wavefronts an access for 8; 16 x 1023 x 777 631 us for 536.)  The
 // sums take a turn through shared memory to get there.
 
-// Eight low numbers, times kLoScale, and back, rounded.  E5M2 is the upper half of FP16.
-__device__ __forceinline__ void low8(uint2 u, F2 (&f)[4]) {
-    f[0] = unpack2<__half>(__byte_perm(u.x, 0u, 0x1404)), f[1] = unpack2<__half>(__byte_perm(u.x, 0u, 0x3424));
-    f[2] = unpack2<__half>(__byte_perm(u.y, 0u, 0x1404)), f[3] = unpack2<__half>(__byte_perm(u.y, 0u, 0x3424));
+// lo in units of a step of its hi: a byte of kLoParts to the step, 128 for 0; with a second
+// byte of 256 parts to each of these, again 128 for 0.
+//
+// Times `scale`, the steps of eight FP16 numbers x, or one over them: 2^-10 of the power of
+// two below, at least FP16's smallest.
+template <bool INVERSE>
+__device__ __forceinline__ void low_unit(const F2 (&x)[4], float scale, F2 (&u)[4]) {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        get2(x[i], lo, hi);
+        lo = fmaxf(__uint_as_float(__float_as_uint(lo) & 0x7f800000u), 0x1p-14f);
+        hi = fmaxf(__uint_as_float(__float_as_uint(hi) & 0x7f800000u), 0x1p-14f);
+        if constexpr (INVERSE) {
+            lo = __uint_as_float(0x7f000000u - __float_as_uint(lo));
+            hi = __uint_as_float(0x7f000000u - __float_as_uint(hi));
+        }
+        u[i] = mul2(mk2(lo, hi), mk2(INVERSE ? scale * 0x1p10f : scale * 0x1p-10f));
+    }
 }
-__device__ __forceinline__ uint32_t pack_low(F2 a) {
-    float lo, hi;
-    get2(a, lo, hi);
-    uint16_t r;
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;
+// Whole numbers of 0 .. 65535 become FP32 and back as the low bits of 2^23 + them.
+constexpr uint32_t kWhole = 0x4b000000u;
+__device__ __forceinline__ void low8(uint2 up, F2 (&f)[4]) {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = i < 2 ? up.x : up.y;
+        f[i] = add2(mk2(__uint_as_float(__byte_perm(w, kWhole, i & 1 ? 0x7442 : 0x7440)),
+                        __uint_as_float(__byte_perm(w, kWhole, i & 1 ? 0x7443 : 0x7441))), mk2(-(0x1p23f + 128.0f)));
+    }
 }
-__device__ __forceinline__ uint2 pack_low8(const F2 (&f)[4]) {
-    return make_uint2(pack_low(f[0]) | pack_low(f[1]) << 16, pack_low(f[2]) | pack_low(f[3]) << 16);
+__device__ __forceinline__ void low16(uint2 up, uint2 down, F2 (&f)[4]) {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w = __byte_perm(i < 2 ? down.x : down.y, i < 2 ? up.x : up.y, i & 1 ? 0x7362 : 0x5140);
+        f[i] = add2(mk2(__uint_as_float(__byte_perm(w, kWhole, 0x7410)), __uint_as_float(__byte_perm(w, kWhole, 0x7432))),
+                    mk2(-(0x1p23f + 32768.0f + 128.0f)));
+    }
+}
+// lo as bytes; `up` alone is rounded to nearest as well.
+__device__ __forceinline__ void pack_low8(const F2 (&x)[4], const F2 (&lo)[4], uint2& up, uint2& down) {
+    F2 u[4];
+    low_unit<true>(x, kLoParts * 256.0f, u);
+    uint32_t w[4];
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        get2(fma2(lo[i], u[i], mk2(0x1p23f + 32768.0f + 128.0f)), a, b);
+        w[i] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5140);          // down, down, up, up
+    }
+    up = make_uint2(__byte_perm(w[0], w[1], 0x7632), __byte_perm(w[2], w[3], 0x7632));
+    down = make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
 }
 
-// What it reads: A (kPoly), or hi and lo.
+// What it reads: A (kPoly), or hi and lo, whose second byte only kFine has.
 template <int MODE>
 struct OrthoIn {
     uint4 x;
     uint2 y;
+};
+template <>
+struct OrthoIn<kFine> {
+    uint4 x;
+    uint2 y, z;
 };
 // ... for 32 rows and 32 columns, with a row's and a column's part of the factors
 // (ortho_factors) per lane.
@@ -165,6 +216,41 @@ template <int MODE>
 __device__ __forceinline__ bool ortho_inside(const OrthoParams& p, int32_t row, int32_t col) {
     return row < ortho_rows<MODE>(p) && col < ortho_cols<MODE>(p);
 }
+// lo's second bytes in 8 columns of a row before step s.  In O (s > 0) they lie at the
+// row's first multiple of 8 bytes: of a row's 2 cols bytes that takes up to 6, and the last
+// 8 up to 7 behind the last column, which from 16 columns on is never more than there
+// are.  Rows of fewer columns: from the first byte on, one at a time.
+__device__ __forceinline__ uint8_t* ortho_down(const OrthoParams& p, int32_t b, int32_t row, int32_t col) {
+    uint8_t* at = reinterpret_cast<uint8_t*>(p.O + b * p.stride_o + row * p.ldo);
+    if (p.cols >= 16) at += -reinterpret_cast<uintptr_t>(at) & 7;
+    return at + col;
+}
+__device__ __forceinline__ uint2 ortho_read_down(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col) {
+    uint2 z = make_uint2(0x80808080u, 0x80808080u);
+    if (row >= p.rows || col >= p.cols) return z;
+    if (s == 0) return __ldcg(reinterpret_cast<const uint2*>(p.x[1] + (static_cast<int64_t>(b) * p.xr + row) * p.xc + col));
+    const uint8_t* at = ortho_down(p, b, row, col);
+    if (p.cols >= 16) return __ldcg(reinterpret_cast<const uint2*>(at));
+    #pragma unroll 1
+    for (int32_t i = 0; i < 8 && col + i < p.cols; ++i) {
+        const uint32_t down = __ldcg(at + i), shift = (i & 3) * 8;
+        uint32_t& w = i < 4 ? z.x : z.y;
+        w = (w & ~(0xffu << shift)) | down << shift;
+    }
+    return z;
+}
+__device__ __forceinline__ void ortho_write_down(const OrthoParams& p, int32_t b, int32_t row, int32_t col, uint2 z) {
+    if (row >= p.rows || col >= p.cols) return;
+    uint8_t* at = ortho_down(p, b, row, col);
+    if (p.cols >= 16) {
+        *reinterpret_cast<uint2*>(at) = z;
+    } else {
+        #pragma unroll 1
+        for (int32_t i = 0; i < 8 && col + i < p.cols; ++i)
+            at[i] = static_cast<uint8_t>((i < 4 ? z.x : z.y) >> ((i & 3) * 8));
+    }
+}
+
 template <int MODE>
 __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col) {
     OrthoIn<MODE> in;
@@ -176,11 +262,12 @@ __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_
         const int64_t at = (static_cast<int64_t>(b) * p.xr + row) * p.xc + col;
         in.x = __ldcg(reinterpret_cast<const uint4*>(p.x[s & 1] + at));
         in.y = __ldcg(reinterpret_cast<const uint2*>(p.lo + at));
+        if constexpr (MODE == kFine) in.z = ortho_read_down(p, s, b, row, col);
     }
     return in;
 }
 
-// The factors of what is read, in 8 columns of a row: a + d of X, b + c (D + D) of A.
+// The factors of what is read, in 8 columns of a row: a + d of hi, b + c (D + D) of A.
 template <int MODE>
 __device__ __forceinline__ void ortho_factors(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col,
                                               F2 (&c0)[4]) {
@@ -234,20 +321,24 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, in
         __half* out = MODE == kGram ? p.mat_a : p.mat_b;
         *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(b) * p.np + row) * p.np + col) = pack8(v);
     } else {
-        F2 y[4];
+        F2 y[4], u[4];
         half8(in.x, x);
-        low8(in.y, y);
+        if constexpr (MODE == kFine) low16(in.y, in.z, y);
+        else low8(in.y, y);
+        low_unit<false>(x, p.abc[3 * s] * (MODE == kFine ? 1.0f / (kLoParts * 256.0f) : 1.0f / kLoParts), u);
         #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = fma2(c0[i], fma2(y[i], mk2(1.0f / kLoScale), x[i]), mul2(v[i], mk2(kDown)));
-        if constexpr (MODE == kStep) {
+        for (int i = 0; i < 4; ++i) v[i] = fma2(c0[i], x[i], fma2(u[i], y[i], mul2(v[i], mk2(kDown))));
+        if constexpr (MODE != kLast) {
             const uint4 h = pack8(v);
             half8(h, x);
             #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = mul2(fma2(x[i], mk2(-1.0f), v[i]), mk2(kLoScale));
+            for (int i = 0; i < 4; ++i) y[i] = fma2(x[i], mk2(-1.0f), v[i]);
             const int64_t at = (static_cast<int64_t>(b) * p.xr + row) * p.xc + col;
             *reinterpret_cast<uint4*>(p.x[(s & 1) ^ 1] + at) = h;
-            *reinterpret_cast<uint2*>(p.lo + at) = pack_low8(y);
+            uint2 up, down;
+            pack_low8(x, y, up, down);
+            *reinterpret_cast<uint2*>(p.lo + at) = up;
+            if (MODE == kFine && s + 1 < p.fine) ortho_write_down(p, b, row, col, down);
         } else {
             const F2 scale = mk2(p.scale);
             #pragma unroll
@@ -466,7 +557,7 @@ __device__ __forceinline__ bool ortho_b_mn(const OrthoParams& p, int mode) {
 // Product q: its mode, and its tiles of a matrix.
 __device__ __forceinline__ int ortho_mode(const OrthoParams& p, int32_t q) {
     const int32_t s = q / 3, m = q - 3 * s;
-    return m < 2 ? m : s + 1 < p.steps ? kStep : kLast;
+    return m < 2 ? m : s + 1 == p.steps ? kLast : s < p.fine ? kFine : kStep;
 }
 __device__ __forceinline__ int32_t ortho_tiles(const OrthoParams& p, int mode) {
     return mode < kStep ? p.tiles_sym : p.tiles_step;
@@ -521,6 +612,9 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoParams& p, int32_t s, 
     return true;
 }
 
+// FINE: some products are kFine.  (Their code in the same kernel costs all others their
+// registers: 16 x 1023 x 777, five steps, 519 us for 434.)
+template <bool FINE>
 __global__ void __launch_bounds__(kOrthoPairThreads, 1)
     ortho_pair_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_x1,
                       const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
@@ -684,6 +778,9 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                                                &abort_flag);
                 else if (mode == kStep)
                     ok = ortho_epilogue<kStep>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
+                                               &abort_flag);
+                else if (FINE && mode == kFine)
+                    ok = ortho_epilogue<kFine>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
                                                &abort_flag);
                 else
                     ok = ortho_epilogue<kLast>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
