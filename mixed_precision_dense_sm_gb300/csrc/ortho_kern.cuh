@@ -605,8 +605,9 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoParams& p, int32_t s, 
     OrthoBlock<MODE> in0, in1;
     if (blocks > 0) ortho_read_block<MODE>(p, s, t.b, row0, col0, in0);
     if (blocks > 1) ortho_read_block<MODE>(p, s, t.b, row0, col0 + 32, in1);
-    if (!ortho_wait(acc_full, parity, abort_flag, p)) return false;
-    __syncwarp();
+    // each lane waits for itself, and the warp goes on together or not at all: what follows
+    // is collective
+    if (!__all_sync(0xffffffffu, ortho_wait(acc_full, parity, abort_flag, p))) return false;
     tc_fence_after_sync();
     ortho_blocks<MODE>(p, s, t, row0, col0, blocks, taddr, in0, in1, turn);
     return true;
@@ -785,7 +786,6 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                 else
                     ok = ortho_epilogue<kLast>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,
                                                &abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 tc_fence_before_sync();
                 __syncwarp();

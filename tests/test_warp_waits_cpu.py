@@ -1,0 +1,29 @@
+"""Warps that wait and then act together (no GPU: the sources are looked at).
+
+A bounded wait may end differently for two lanes of a warp, at the limit.  Where
+all lanes wait, they vote before anything collective (a load from tensor memory, a
+full-mask barrier): a lane that left alone would leave the others waiting."""
+import os
+import re
+
+import mixed_precision_dense_sm_gb300 as lib
+
+
+def body(text, head):
+    """The block that follows the first `head`."""
+    start = text.index("{", text.index(head))
+    depth, i = 1, start + 1
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[i], 0)
+        i += 1
+    return text[start:i]
+
+
+def source(name):
+    return re.sub(r"//[^\n]*", "", open(os.path.join(lib.HERE, "csrc", name)).read())
+
+
+def test_the_updates_epilogue_votes():
+    text = body(source("ortho_kern.cuh"), "bool ortho_epilogue(")
+    assert len(re.findall(r"\bortho_wait\(", text)) == 1
+    assert re.search(r"if \(!__all_sync\(0xffffffffu, ortho_wait\([^;]*\)\)\) return false;", text)
