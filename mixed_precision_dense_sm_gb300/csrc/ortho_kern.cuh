@@ -770,6 +770,7 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
                     if (lane == 0) ready = ortho_ready(p, q, t.b, &abort_flag) ? 1 : 0;
                     ok = __shfl_sync(0xffffffffu, ready, 0) != 0;
                     if (!ok) break;
+                    __syncwarp();        // all lanes read behind the acquire of one (a shuffle orders nothing)
                 }
                 if (mode == kGram)
                     ok = ortho_epilogue<kGram>(p, q / 3, t, row0, col0, taddr, &acc_full[buf], parity, turn,

@@ -27,3 +27,14 @@ def test_the_updates_epilogue_votes():
     text = body(source("ortho_kern.cuh"), "bool ortho_epilogue(")
     assert len(re.findall(r"\bortho_wait\(", text)) == 1
     assert re.search(r"if \(!__all_sync\(0xffffffffu, ortho_wait\([^;]*\)\)\) return false;", text)
+
+
+def test_what_one_lane_acquired_the_warp_reads_behind_a_barrier():
+    """ortho_ready acquires with one lane; a shuffle hands its answer on and orders no
+    memory, __syncwarp does."""
+    text = source("ortho_kern.cuh")
+    calls = [m for m in re.finditer(r"if \(lane == 0\) \w+ = ortho_ready\(", text)]
+    assert len(calls) == 1
+    rest = text[calls[0].end():]
+    between = rest[:rest.index("ortho_epilogue<")]
+    assert re.search(r"__shfl_sync\(.*__syncwarp\(\);", between, flags=re.S)
