@@ -1513,8 +1513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ok = ok && wait_or_abort(&acc_full[buf], (acc_i >> 1) & 1u, &abort_flag, p.wait_limit_ns);
             // stream-K, the LayerNorm and gated epilogues and the TMA store of C
-            // use named barriers below
+            // use named barriers below; without them the warp's lanes, which waited
+            // each for itself, still go on together or not at all
             if (p.stream_k || EPI != kEpiPlain || p.c_tma) ok = epilogue_all(ok);
+            else ok = __all_sync(0xffffffffu, ok);
             if (!ok) {
                 record_error(p, kErrTimeoutEpilogue, &abort_flag);
                 break;

@@ -38,3 +38,14 @@ def test_what_one_lane_acquired_the_warp_reads_behind_a_barrier():
     rest = text[calls[0].end():]
     between = rest[:rest.index("ortho_epilogue<")]
     assert re.search(r"__shfl_sync\(.*__syncwarp\(\);", between, flags=re.S)
+
+
+def test_the_gemm_epilogue_votes():
+    """Between the wait for the accumulator and the collective loads: over all epilogue
+    warps where they share barriers, else over the warp."""
+    text = source("gemm_tc.cuh")
+    waits = [m for m in re.finditer(r"wait_or_abort\(&acc_full", text)]
+    assert len(waits) == 1
+    rest = text[waits[0].start():]
+    assert re.search(r"ok = epilogue_all\(ok\);\s*else ok = __all_sync\(0xffffffffu, ok\);\s*if \(!ok\)",
+                     rest[:rest.index("tc_fence_after_sync")])
