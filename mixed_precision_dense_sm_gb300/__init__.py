@@ -913,6 +913,8 @@ def ortho_update(h, batch, rows, cols, G, ldg, stride_g, g_dtype, O, ldo, stride
     """Raw C-ABI call (include/ortho_sm103.h); coefficients: 3 floats per step.
     Returns the gemm_status_t code."""
     abc = array.array("f", coefficients)
+    if len(abc) % 3:
+        raise ValueError("coefficients: three for each step")
     o = OrthoUpdate(len(abc) // 3, abc.buffer_info()[0], eps, scale)
     return lib.ortho_update(h, batch, rows, cols, G or None, ldg, stride_g, g_dtype, O or None, ldo,
                             stride_o, ctypes.byref(o), stream)
@@ -1101,7 +1103,7 @@ class Gemm:
         op, ldo = _mat(o, "O", rows, cols, torch.bfloat16, dev)
         if len(coefficients) == 3 and not hasattr(coefficients[0], "__len__"):
             abc = tuple(coefficients) * steps
-        elif len(coefficients) == steps:
+        elif len(coefficients) == steps and all(hasattr(c, "__len__") and len(c) == 3 for c in coefficients):
             abc = [v for step in coefficients for v in step]
         else:
             raise ValueError("coefficients: one (a, b, c), or one for each step")
