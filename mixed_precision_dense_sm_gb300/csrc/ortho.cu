@@ -332,8 +332,10 @@ struct Schedule {
 // takes 1024 at the tensor core's rate, a tile's epilogue 9000 beside the next
 // tile's blocks.  A single CTA's 128 x 128 x 128 block takes as long, for it is bound
 // by the 64 KB that it loads (64 a cycle); its epilogue 4500 and the exchange of a
-// split 7500, both as the columns, and 3000 until the first block is there.
-Schedule schedule(const OrthoCall& c, bool symmetric, int32_t least_width, int64_t rows, int64_t cols,
+// split 7500, both as the columns, and 3000 until the first block is there.  K is split
+// up to `most_splits` (the first product alone: of the others, on 64 to 65536 rows and
+// columns, this count never finds a split faster).
+Schedule schedule(const OrthoCall& c, bool symmetric, int32_t least_width, int32_t most_splits, int64_t rows, int64_t cols,
                   int64_t k_blocks) {
     Schedule best = {};
     int64_t least = INT64_MAX;
@@ -357,7 +359,7 @@ Schedule schedule(const OrthoCall& c, bool symmetric, int32_t least_width, int64
     };
     consider(true, 256, 1);
     for (int32_t width = 128; width >= least_width; width /= 2)
-        for (int32_t n = 1; n <= 8 && n <= k_blocks && n * 8 <= width; n *= 2)       // (8 columns at least to finish)
+        for (int32_t n = 1; n <= most_splits && n <= k_blocks && n * 8 <= width; n *= 2)       // (8 columns at least to finish)
             consider(false, width, n);
     return best;
 }
@@ -370,7 +372,7 @@ cudaError_t product(const OrthoCall& c, const Schedule& s, const CUtensorMap& a,
     p.full = s.width < 128;
     p.splits = s.splits;
     p.log_width = s.width == 128 ? 7 : s.width == 64 ? 6 : 5;
-    for (int32_t n = s.splits; n > 1; n >>= 1) --p.log_width;
+    for (int32_t n = s.splits; n > 1; n >>= 1) --p.log_width;               // (kGram)
     if (s.width == 128) return launch_tile<MODE, 128>(c, a, b, p);
     if constexpr (MODE < kStep)
         if (s.width == 32) return launch_tile<MODE, 32>(c, a, b_narrow, p);
@@ -460,9 +462,9 @@ cudaError_t run(const OrthoCall& c) {
     p.k_gram = static_cast<int32_t>(((tall ? l.xr : l.xc) + 127) / 128);
     p.k_other = static_cast<int32_t>((l.np + 127) / 128);
     // (an MN-major B comes in boxes of 64 columns)
-    const Schedule sched[3] = {schedule(c, true, tall ? 64 : 32, l.np, l.np, p.k_gram),
-                               schedule(c, true, 32, l.np, l.np, p.k_other),
-                               schedule(c, false, 64, l.xr, l.xc, p.k_other)};
+    const Schedule sched[3] = {schedule(c, true, tall ? 64 : 32, 8, l.np, l.np, p.k_gram),
+                               schedule(c, true, 32, 1, l.np, l.np, p.k_other),
+                               schedule(c, false, 64, 1, l.xr, l.xc, p.k_other)};
     p.steps = steps, p.fine = fine;
     p.x[0] = hi[0], p.x[1] = hi[1], p.mat_a = a, p.mat_b = b, p.done = q.done;
     std::memcpy(p.abc, c.opt->coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));

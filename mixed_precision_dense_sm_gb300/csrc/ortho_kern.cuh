@@ -37,10 +37,11 @@
 // where all of them have many tiles.  A tile then waits for the tiles of its own
 // matrix in the product before, which others have done: those of a batch follow one
 // another without a gap (16 x 1023 x 777, 76 pairs: 38 rounds of tiles for 50, and one
-// launch for 15).  ortho_tile_kernel: one tile of 128 rows and 128 columns per
-// cluster, whose 1 to 8 CTAs split K and add up through distributed shared memory, for
-// few tiles; for fewer still 64 or 32 columns, which shortens the epilogue, and all
-// tiles of the symmetric products, without mirroring.
+// launch for 15).  ortho_tile_kernel: one tile of 128 rows and 128 columns per CTA, for few
+// tiles; for fewer still 64 or 32 columns, which shortens the epilogue, and all tiles of
+// the symmetric products, without mirroring.  Of kGram, whose K is the long side, the tile is
+// a cluster's, whose 1 to 8 CTAs split K and add up through distributed shared memory; the
+// others' K is the short side, short where tiles are few.
 #pragma once
 #include <cstdint>
 #include <cuda.h>
@@ -81,7 +82,7 @@ struct OrthoParams {
     int32_t steps, fine, first, last;
     int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; along its rows
     int32_t full;                       // symmetric products: all tiles, not the upper ones
-    int32_t splits, log_width;          // ortho_tile_kernel: CTAs per tile; log2(columns / splits)
+    int32_t splits, log_width;          // ortho_tile_kernel, kGram: CTAs per tile; log2(columns / splits)
     __half *x[2], *mat_a, *mat_b;       // X's first numbers before even and odd steps
     uint8_t* lo;
     float *diag_a, *diag;               // A's and B's diagonals
@@ -265,27 +266,6 @@ __device__ __forceinline__ OrthoIn<MODE> ortho_read(const OrthoParams& p, int32_
         if constexpr (MODE == kFine) in.z = ortho_read_down(p, s, b, row, col);
     }
     return in;
-}
-
-// The factors of what is read, in 8 columns of a row: a + d of hi, b + c (D + D) of A.
-template <int MODE>
-__device__ __forceinline__ void ortho_factors(const OrthoParams& p, int32_t s, int32_t b, int32_t row, int32_t col,
-                                              F2 (&c0)[4]) {
-    if constexpr (MODE == kGram) return;
-    const float* d = (MODE == kPoly ? p.diag_a : p.diag) + static_cast<int64_t>(b) * p.np;
-    const float scale = MODE == kPoly ? p.abc[3 * s + 2] : 1.0f;
-    float base = MODE == kPoly ? p.abc[3 * s + 1] : p.abc[3 * s];
-    if (MODE == kPoly || !p.tall) base = fmaf(scale, __ldcg(d + row), base);
-    if (MODE == kPoly || p.tall) {
-        const float4 d0 = __ldcg(reinterpret_cast<const float4*>(d + col));
-        const float4 d1 = __ldcg(reinterpret_cast<const float4*>(d + col + 4));
-        c0[0] = mk2(fmaf(scale, d0.x, base), fmaf(scale, d0.y, base));
-        c0[1] = mk2(fmaf(scale, d0.z, base), fmaf(scale, d0.w, base));
-        c0[2] = mk2(fmaf(scale, d1.x, base), fmaf(scale, d1.y, base));
-        c0[3] = mk2(fmaf(scale, d1.z, base), fmaf(scale, d1.w, base));
-    } else {
-        c0[0] = c0[1] = c0[2] = c0[3] = mk2(base);
-    }
 }
 
 // An element of the diagonal, whose sum counts as 0 from here on (A's was read as 0).
@@ -813,6 +793,89 @@ __global__ void __launch_bounds__(kOrthoPairThreads, 1)
 
 // ------------------------------------------------------- one tile per cluster
 
+// kGram with K split: the sums of S CTAs, each of which finishes 128 rows and its part of
+// the tile's columns, in units of 8 columns of a row.
+template <int NB>
+__device__ __forceinline__ void ortho_join(const OrthoParams& p, const OrthoTile& t, int32_t S, uint32_t rank, uint32_t taddr,
+                                           uint8_t* smem, volatile int* abort_flag) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t log4 = p.log_width - 2, log8 = p.log_width - 3;            // log2 of the fours and eights of columns
+    const int32_t first_row = t.i * 128, first_col = t.j * NB + (static_cast<int32_t>(rank) << p.log_width);
+    float4* xbuf = reinterpret_cast<float4*>(smem);
+    auto at_of = [&](int32_t src, int32_t c4, int32_t rr) {
+        return xbuf + ((src << log4) + c4) * 128 + (rr ^ (((c4 >> 1) << (3 - log8)) & 7));
+    };
+    if (warp >= 2) {
+        const int r_in = (warp & 3) * 32 + lane;
+        #pragma unroll 1
+        for (int c = 0; c < NB; c += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(taddr + c, r);
+            tmem_ld_wait();
+            #pragma unroll
+            for (int j = 0; j < 32; j += 4) {
+                const int32_t c4 = (c + j) >> 2;
+                const uint32_t q = static_cast<uint32_t>(c4 >> log4);
+                float4* at = at_of(static_cast<int32_t>(rank), c4 & ((1 << log4) - 1), r_in);
+                const float4 v = make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
+                                             __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]));
+                if (q == rank) *at = v;
+                else
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     map_to_rank(smem_addr(at), q)),
+                                 "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                                 : "memory");
+            }
+        }
+    }
+    __syncthreads();
+    cluster_sync_all();
+    if (*abort_flag) return;
+    {
+        const int32_t rr = static_cast<int32_t>(threadIdx.x), cc = first_row + rr - first_col;
+        if (rr < 128 && cc >= 0 && cc < 1 << p.log_width && first_row + rr < p.np) {
+            float sum = 0.0f;
+            for (int32_t s = 0; s < S; ++s) {
+                float* e = reinterpret_cast<float*>(at_of(s, cc >> 2, rr)) + (cc & 3);
+                sum += *e;
+                *e = 0.0f;
+            }
+            ortho_diagonal<kGram>(p, 0, t.b, first_row + rr, sum);
+        }
+        __syncthreads();
+    }
+    const bool again = ortho_again<kGram>(p, t);
+    if (warp >= 2) {
+        #pragma unroll 4
+        for (int32_t k = 0; k < 1 << log8; ++k) {
+            const int32_t e = k * 128 + static_cast<int32_t>(threadIdx.x) - 64;          // (by rows)
+            const int32_t g = e & ((1 << log8) - 1), rr = e >> log8;
+            if (!ortho_inside<kGram>(p, first_row + rr, first_col + g * 8)) continue;
+            F2 v[4];
+            ortho_load8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
+            #pragma unroll 2
+            for (int32_t s = 1; s < S; ++s) {
+                F2 o[4];
+                ortho_load8(at_of(s, 2 * g, rr), at_of(s, 2 * g + 1, rr), o);
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
+            }
+            const F2 none[4] = {};
+            ortho_finish<kGram>(p, 0, t.b, first_row + rr, first_col + g * 8, OrthoIn<kGram>{}, none, v);
+            // in the place of the first source's sums, which this thread alone reads
+            if (again) ortho_store8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
+        }
+    }
+    if (!again) return;
+    __syncthreads();
+    #pragma unroll 1
+    for (int32_t e = threadIdx.x; e < 128 << log4; e += kOrthoTileThreads) {
+        const int32_t rr = e & 127, c4 = e >> 7;
+        if (ortho_inside<kGram>(p, first_row + rr, first_col + 4 * c4))
+            ortho_mirror<kGram>(p, t.b, first_row + rr, first_col + 4 * c4, *at_of(0, c4, rr));
+    }
+}
+
 // NB: its columns, 32 (not where B's boxes are of 64 columns: ortho_b_mn), 64 or 128.
 template <int MODE, int NB>
 __global__ void __launch_bounds__(kOrthoTileThreads, 1)
@@ -830,7 +893,7 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     __shared__ volatile int abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t S = p.splits;
+    const int32_t S = MODE == kGram ? p.splits : 1;
     const uint32_t rank = S > 1 ? cluster_ctarank() : 0u;
     const OrthoTile t = ortho_tile<MODE>(p, static_cast<int32_t>(blockIdx.x) / S);
     const int32_t step = p.first / 3, k_blocks = MODE == kGram ? p.k_gram : p.k_other;
@@ -859,30 +922,15 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // The epilogue's place: 32 rows and the first two blocks of 32 columns, or with K
-    // split the first four units of 8 columns of a row among this CTA's columns.  Its
-    // inputs are on their way while the products run.
+    // The epilogue's place: 32 rows and, unless K is split, blocks of 32 columns, of which
+    // the first two's inputs are on their way while the products run.
     const int quarter = warp & 3;
-    const int32_t row0 = t.i * 128 + quarter * 32, log8 = p.log_width - 3;
+    const int32_t row0 = t.i * 128 + quarter * 32;
     const int32_t blocks = S > 1 ? 0 : ortho_block_count<MODE>(p, row0, t.j * NB, NB / 32);
-    const int32_t col_s = t.j * NB + (static_cast<int32_t>(rank) << p.log_width);
-    auto unit = [&](int32_t k, int32_t& rr, int32_t& g) {       // (by rows)
-        const int32_t e = k * 128 + static_cast<int32_t>(threadIdx.x) - 64;
-        g = e & ((1 << log8) - 1);
-        rr = e >> log8;
-        return k < 1 << log8 && ortho_inside<MODE>(p, t.i * 128 + rr, col_s + g * 8);
-    };
     OrthoBlock<MODE> in0, in1;
     if (warp >= 2) {
         if (blocks > 0) ortho_read_block<MODE>(p, step, t.b, row0, t.j * NB, in0);
         if (blocks > 1) ortho_read_block<MODE>(p, step, t.b, row0, t.j * NB + 32, in1);
-        if (S > 1) {
-            #pragma unroll
-            for (int32_t k = 0; k < 4; ++k) {
-                int32_t rr, g;
-                if (unit(k, rr, g)) in0.in[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
-            }
-        }
     }
 
     if (warp == 0) {
@@ -930,109 +978,17 @@ __global__ void __launch_bounds__(kOrthoTileThreads, 1)
             if (!mbar_wait(done, 0, p.wait_limit_ns)) ortho_give_up(p, &abort_flag);
         }
     }
-    // Every CTA of the cluster is through with its stages: their memory becomes the
-    // exchange buffer [source][four columns of mine][row] of float4s, the rows of
-    // different columns turned against each other, so that the units of eight lanes
-    // meet in no bank.
     tc_fence_before_sync();
     __syncthreads();
     if (S > 1) cluster_sync_all();
     tc_fence_after_sync();
-    const int r_in = quarter * 32 + lane;
     const uint32_t taddr = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     if (S > 1) {
-        const int32_t log4 = p.log_width - 2;                // log2 of the fours of columns each CTA finishes
-        float4* xbuf = reinterpret_cast<float4*>(smem);
-        auto at_of = [&](int32_t src, int32_t c4, int32_t rr) {
-            return xbuf + ((src << log4) + c4) * 128 + (rr ^ (((c4 >> 1) << (3 - log8)) & 7));
-        };
-        if (warp >= 2) {
-            const bool any = kb1 > kb0;                      // (a CTA without a K block adds zeros)
-            #pragma unroll 1
-            for (int c = 0; c < NB; c += 32) {
-                uint32_t r[32];
-                tmem_ld_32x32b_x32(taddr + c, r);
-                tmem_ld_wait();
-                #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const int32_t c4 = (c + j) >> 2;
-                    const uint32_t q = static_cast<uint32_t>(c4 >> log4);
-                    float4* at = at_of(static_cast<int32_t>(rank), c4 & ((1 << log4) - 1), r_in);
-                    const float4 v = any ? make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
-                                                       __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]))
-                                         : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (q == rank) *at = v;
-                    else
-                        asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         map_to_rank(smem_addr(at), q)),
-                                     "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                                     : "memory");
-                }
-            }
-        }
-        __syncthreads();
-        cluster_sync_all();
-        if (!abort_flag) {
-            const bool again = ortho_again<MODE>(p, t);
-            if constexpr (MODE < kStep) {
-                const int32_t rr = static_cast<int32_t>(threadIdx.x), cc = t.i * 128 + rr - col_s;
-                if (rr < 128 && cc >= 0 && cc < 1 << p.log_width && t.i * 128 + rr < p.np) {
-                    float sum = 0.0f;
-                    for (int32_t s = 0; s < S; ++s) {
-                        float* e = reinterpret_cast<float*>(at_of(s, cc >> 2, rr)) + (cc & 3);
-                        sum += *e;
-                        *e = 0.0f;
-                    }
-                    ortho_diagonal<MODE>(p, step, t.b, t.i * 128 + rr, sum);
-                }
-                __syncthreads();
-            }
-            if (warp >= 2) {
-                #pragma unroll 1
-                for (int32_t k0 = 0; k0 < 1 << log8; k0 += 4) {
-                    #pragma unroll
-                    for (int32_t k = 0; k < 4; ++k) {
-                        int32_t rr, g;
-                        if (!unit(k0 + k, rr, g)) continue;
-                        F2 c0[4], v[4];
-                        ortho_factors<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8, c0);
-                        ortho_load8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
-                        #pragma unroll 2
-                        for (int32_t s = 1; s < S; ++s) {
-                            F2 o[4];
-                            ortho_load8(at_of(s, 2 * g, rr), at_of(s, 2 * g + 1, rr), o);
-                            #pragma unroll
-                            for (int i = 0; i < 4; ++i) v[i] = add2(v[i], o[i]);
-                        }
-                        ortho_finish<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8, in0.in[k], c0, v);
-                        // in the place of the first source's sums, which this thread alone reads
-                        if (again) ortho_store8(at_of(0, 2 * g, rr), at_of(0, 2 * g + 1, rr), v);
-                        if (unit(k0 + k + 4, rr, g)) in0.in[k] = ortho_read<MODE>(p, step, t.b, t.i * 128 + rr, col_s + g * 8);
-                    }
-                }
-            }
-            if (again) {
-                __syncthreads();
-                if constexpr (MODE == kLast) {
-                    const int32_t width = 1 << p.log_width;
-                    #pragma unroll 1
-                    for (int32_t e = threadIdx.x; e < 128 * width; e += kOrthoTileThreads) {
-                        const int32_t rr = e >> p.log_width, cc = e & (width - 1);
-                        const int32_t row = t.i * 128 + rr, col = col_s + cc;
-                        if (row < p.rows && col < p.cols)
-                            p.O[t.b * p.stride_o + row * p.ldo + col] =
-                                __float2bfloat16_rn(reinterpret_cast<const float*>(at_of(0, cc >> 2, rr))[cc & 3]);
-                    }
-                } else {
-                    #pragma unroll 1
-                    for (int32_t e = threadIdx.x; e < 128 << log4; e += kOrthoTileThreads) {
-                        const int32_t rr = e & 127, c4 = e >> 7;
-                        if (ortho_inside<MODE>(p, t.i * 128 + rr, col_s + 4 * c4))
-                            ortho_mirror<MODE>(p, t.b, t.i * 128 + rr, col_s + 4 * c4, *at_of(0, c4, rr));
-                    }
-                }
-            }
-        }
+        // Every CTA of the cluster is through with its stages: their memory becomes the
+        // exchange buffer [source][four columns of mine][row] of float4s, the rows of
+        // different columns turned against each other, so that the units of eight lanes
+        // meet in no bank.
+        if constexpr (MODE == kGram) ortho_join<NB>(p, t, S, rank, taddr, smem, &abort_flag);
     } else if (warp >= 2 && !abort_flag) {
         float4* turn = reinterpret_cast<float4*>(smem) + (warp - 2) * 256;      // the stages are free
         ortho_blocks<MODE>(p, step, t, row0, t.j * NB, blocks, taddr, in0, in1, turn);
