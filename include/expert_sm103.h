@@ -34,8 +34,8 @@
  * A position outside 0 .. rows - 1 counts as none.
  *
  * Positions that are not -1 must differ where rows are written (as expert_sort's
- * do).  Outputs must not overlap inputs or each other, but for dYs, which may be
- * Ys (same leading dimension).
+ * do).  Outputs must not overlap inputs or each other, element by element (columns of one
+ * buffer are apart), but for dYs, which may be Ys (same leading dimension).
  *
  * No handle and no workspace: asynchronous on `stream`, nothing allocated, can be
  * captured.  The same call gives the same bits.
@@ -43,7 +43,7 @@
  * Errors: GEMM_ERR_INVALID_VALUE (a negative size, T k, D or rows
  * above 2^30, E below 1 or
  * above EXPERT_MAX, a leading dimension below its row's length, an unknown type,
- * NULL or misaligned pointers of what is not empty; nothing is enqueued),
+ * NULL or misaligned pointers of what is not empty, overlap; nothing is enqueued),
  * GEMM_ERR_NOT_SUPPORTED (not sm_103), GEMM_ERR_LAUNCH.
  */
 #ifndef EXPERT_SM103_H_

@@ -29,6 +29,7 @@
 #include "epilogue_ops.cuh"
 #include "expert_sm103.h"
 #include "f32x2.cuh"
+#include "overlap.h"
 #include "ptx.cuh"
 
 namespace {
@@ -897,6 +898,18 @@ bool matrix_ok(const void* p, int64_t ld, int64_t rows, int64_t cols, int32_t es
     return ld >= (cols > 0 ? cols : 1) && ld <= (1ll << 40) && aligned(p, es);
 }
 
+// CTAs write outputs while others still read inputs: each output has to be apart from
+// every input, and from the others.
+template <int INS, int OUTS>
+bool outputs_apart(const Region (&in)[INS], const Region (&out)[OUTS]) {
+    for (int o = 0; o < OUTS; ++o) {
+        for (int i = 0; i < INS; ++i)
+            if (overlap(out[o], in[i])) return false;
+        for (int i = 0; i < o; ++i)
+            if (overlap(out[o], out[i])) return false;
+    }
+    return true;
+}
 
 gemm_status_t rows_call(RowsKind kind, RowsParams& p, int32_t dtype, const expert_weights_t* w,
                         cudaStream_t stream) {
@@ -929,6 +942,18 @@ gemm_status_t rows_call(RowsKind kind, RowsParams& p, int32_t dtype, const exper
     if (sms < 0) return GEMM_ERR_LAUNCH;
     if (sms == 0) return GEMM_ERR_NOT_SUPPORTED;
     if (p.T == 0 || (p.D == 0 && !dot)) return GEMM_OK;
+    auto matrix = [](const void* q, int64_t rows, int64_t ld, int64_t cols, int64_t bytes) {
+        return Region{q, rows, ld * bytes, cols * bytes};
+    };
+    // (dYs may be Ys: a row's elements are read before they are written, by the same thread)
+    const bool in_place = p.rows_in == p.rows_out && (p.ld_rows_in == p.ld_rows_out || p.rows <= 1);
+    const Region in[] = {matrix(p.tok_in, p.T, p.ld_tok_in, p.D, es),
+                         matrix(in_place ? nullptr : p.rows_in, p.rows, p.ld_rows_in, p.D, es),
+                         matrix(p.pos, p.T, p.k, p.k, 4), matrix(p.weight, p.T, p.ldw, p.k, esize(p.wtype))};
+    const Region out_of[] = {matrix(p.tok_out, p.T, p.ld_tok_out, p.D, es),
+                             matrix(p.rows_out, p.rows, p.ld_rows_out, p.D, es),
+                             matrix(p.dweight, p.T, p.lddw, p.k, esize(p.dwtype))};
+    if (!outputs_apart(in, out_of)) return GEMM_ERR_INVALID_VALUE;
 
     // 16-byte vectors where every row of every matrix starts on one
     const int32_t per = 16 / es;
@@ -1000,6 +1025,9 @@ gemm_status_t expert_sort(int64_t T, int64_t k, int64_t E, const void* ids, int6
     const int sms = device_sms();
     if (sms < 0) return GEMM_ERR_LAUNCH;
     if (sms == 0) return GEMM_ERR_NOT_SUPPORTED;
+    const Region in[] = {{ids, T, ldids * id_bytes, k * id_bytes}};
+    const Region out[] = {{pos, 1, T * k * 4, T * k * 4}, {offsets, 1, (E + 1) * 4, (E + 1) * 4}, {order, 1, T * k * 4, T * k * 4}};
+    if (!outputs_apart(in, out)) return GEMM_ERR_INVALID_VALUE;
     SortParams p = {};
     p.ids = ids, p.ldids = T == 1 ? k : ldids;
     p.n = static_cast<int32_t>(T * k), p.k = static_cast<int32_t>(k), p.E = static_cast<int32_t>(E);
