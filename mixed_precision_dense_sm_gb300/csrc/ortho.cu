@@ -413,6 +413,17 @@ int32_t fine_steps(const ortho_update_t& opt) {
     return s;                                // (0 of one step)
 }
 
+// The first of the last steps, behind each of which a rounding is enlarged by up to 4.
+constexpr float kLateFrom = 4.0f;
+int32_t late_step(const ortho_update_t& opt) {
+    int32_t s = opt.steps - 1;
+    for (float grow = 1.0f; s > 0; --s) {
+        grow *= fmaxf(1.0f, fabsf(opt.coefficients[3 * s]));
+        if (grow > kLateFrom) break;
+    }
+    return s;
+}
+
 cudaError_t run(const OrthoCall& c) {
     const Layout l = layout(c.batch, c.rows, c.cols);
     __half* hi[2] = {reinterpret_cast<__half*>(c.ws + l.hi[0]), reinterpret_cast<__half*>(c.ws + l.hi[1])};
@@ -465,7 +476,7 @@ cudaError_t run(const OrthoCall& c) {
     const Schedule sched[3] = {schedule(c, true, tall ? 64 : 32, 8, l.np, l.np, p.k_gram),
                                schedule(c, true, 32, 1, l.np, l.np, p.k_other),
                                schedule(c, false, 64, 1, l.xr, l.xc, p.k_other)};
-    p.steps = steps, p.fine = fine;
+    p.steps = steps, p.fine = fine, p.late = late_step(*c.opt);
     p.x[0] = hi[0], p.x[1] = hi[1], p.mat_a = a, p.mat_b = b, p.done = q.done;
     std::memcpy(p.abc, c.opt->coefficients, static_cast<size_t>(steps) * 3 * sizeof(float));
     bool ok = true;

@@ -14,19 +14,21 @@
 //   kFine  the same, finer          buffers to the other, lo stays in place
 //   kLast  O = scale (...)
 // lo, at most half a step of hi, is a byte: a 254th of a step of its own hi, so that X is
-// rounded by 2^-20 (six more operations per element than an E5M2 lo, 439 us for 423,
+// rounded by 2^-20 (eight more operations per element than an E5M2 lo, 446 us for 423,
 // which rounds X by 2^-14; FP16, 2^-22, would be half as much again of what kStep reads and
 // writes beside its operands).  It matters because every step enlarges what a rounding left
 // in the directions of small singular values by a (3.4): rank 1, five steps, 0.0007 of the
 // norm of O (E5M2 0.007).  Where the steps that are left enlarge it by more than 512, kFine
-// carries 8 more bits (eight steps of 16 x 1023 x 777: 884 us, 615 without, and 0.1 of the
+// carries 8 more bits (eight steps of 16 x 1023 x 777: 892 us, 615 without, and 0.1 of the
 // norm of O for 0.002).  These lie where nothing else is: before step 0 in the second buffer
 // of hi (each thread reads its own before it writes hi there), from then on in O's rows, so
 // kLast, which writes O, has none.
 // A and B are stored without their diagonals D and d, which are kept in FP32: B = b A +
 // c (A - D)^2 + c (D A + A D) - c D^2, and X' = a X + d hi + (B - d) hi.  d multiplies what
-// the rest of B multiplies, for they may cancel (with d lo beside it rank 1 was off by 0.002
-// after five steps and 0.05 after eight); O of noise is off by 0.0012 (all in FP16: 0.0026).
+// the rest of B multiplies, for they may cancel (with d lo beside it O of rank 1 is off by
+// 0.002 after five steps and 0.05 after eight), but where little more enlarges what does not,
+// in the last two steps usually: there d is most of B if G is noise, of which O is off by
+// 0.0007 for 0.0012 (all in FP16: 0.0026).
 // Operands come as boxes of 128 rows by two K chunks (32 KB) through 4-D maps (64
 // elements, rows, chunk, matrix).  The same box is 128 rows of a K-major operand, or
 // 128 columns of one with K along its rows (MN-major): both in the tall kGram, the
@@ -74,12 +76,13 @@ static_assert(128 * kOrthoFewRegs + 256 * kOrthoManyRegs <= 384 * 168, "the laun
 constexpr int kOrthoTileThreads = 192;               // warp 0 TMA, 1 MMA, 2-5 epilogue
 
 // Products [first, last): product 3 s of step s is kGram, 3 s + 1 kPoly, 3 s + 2 kFine in
-// the first `fine` steps, then kStep, and kLast in the last step.
+// the first `fine` steps, then kStep, and kLast in the last step.  From step `late` on B's
+// diagonal multiplies lo too.
 struct OrthoParams {
     int32_t batch;                      // matrices
     int32_t np, xr, xc;                 // padded: the short side; X's rows and columns
     int32_t k_gram, k_other;            // pairs of K chunks
-    int32_t steps, fine, first, last;
+    int32_t steps, fine, late, first, last;
     int32_t tiles_sym, tiles_step, tiles_i_step;    // tiles of a matrix; along its rows
     int32_t full;                       // symmetric products: all tiles, not the upper ones
     int32_t splits, log_width;          // ortho_tile_kernel, kGram: CTAs per tile; log2(columns / splits)
@@ -305,9 +308,17 @@ __device__ __forceinline__ void ortho_finish(const OrthoParams& p, int32_t s, in
         half8(in.x, x);
         if constexpr (MODE == kFine) low16(in.y, in.z, y);
         else low8(in.y, y);
-        low_unit<false>(x, p.abc[3 * s] * (MODE == kFine ? 1.0f / (kLoParts * 256.0f) : 1.0f / kLoParts), u);
+        low_unit<false>(x, MODE == kFine ? 1.0f / (kLoParts * 256.0f) : 1.0f / kLoParts, u);
+        // lo counts to hi, or apart from it: times a alone
+        const bool late = MODE == kLast || s >= p.late;
+        const F2 to_hi = mk2(late ? 1.0f : 0.0f), apart = mk2(late ? 0.0f : p.abc[3 * s]);
         #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = fma2(c0[i], x[i], fma2(u[i], y[i], mul2(v[i], mk2(kDown))));
+        for (int i = 0; i < 4; ++i) {
+            y[i] = mul2(u[i], y[i]);
+            v[i] = mul2(v[i], mk2(kDown));
+            if constexpr (MODE != kLast) v[i] = fma2(apart, y[i], v[i]);
+            v[i] = fma2(c0[i], fma2(to_hi, y[i], x[i]), v[i]);
+        }
         if constexpr (MODE != kLast) {
             const uint4 h = pack8(v);
             half8(h, x);
@@ -594,7 +605,7 @@ __device__ __forceinline__ bool ortho_epilogue(const OrthoParams& p, int32_t s, 
 }
 
 // FINE: some products are kFine.  (Their code in the same kernel costs all others their
-// registers: 16 x 1023 x 777, five steps, 519 us for 434.)
+// registers: 16 x 1023 x 777, five steps, 519 us for 439.)
 template <bool FINE>
 __global__ void __launch_bounds__(kOrthoPairThreads, 1)
     ortho_pair_kernel(const __grid_constant__ CUtensorMap map_x0, const __grid_constant__ CUtensorMap map_x1,

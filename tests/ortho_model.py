@@ -3,7 +3,7 @@ of the kernels' roundings in 64 bits, and a check that sees a tenth of BF16's ro
 
 Roundings: X is hi + lo, FP16 (times 2^11) and a byte of 254 parts to a step of hi, two
 bytes (254 * 256 parts) before the first `fine` steps; A and B but for their diagonals
-FP16.  X' = a (hi + lo) + d hi + (B - d) hi.
+FP16.  X' = a (hi + lo) + d hi + (B - d) hi, from step `late` on with d lo as well.
 
 Beside them the kernels have FP32's errors, small themselves, but what a rounding does to
 a number next to its border they change altogether, and what the steps enlarge they
@@ -30,7 +30,7 @@ import ffn_ref as ref
 import ortho_ref as ortho
 
 MUON = (3.4445, -4.7750, 2.0315)
-SCALE, PARTS, FINE_FROM = 2048.0, 254, 512.0
+SCALE, PARTS, FINE_FROM, LATE_FROM = 2048.0, 254, 512.0, 4.0
 
 
 def steps_of(coefficients, steps):
@@ -47,6 +47,18 @@ def fine_steps(abc):
             break
         n -= 1
     return n
+
+
+def late_step(abc):
+    """The first of the last steps, behind each of which a rounding is enlarged by up to
+    LATE_FROM."""
+    s, grow = len(abc) - 1, 1.0
+    while s > 0:
+        grow *= max(1.0, abs(abc[s][0]))
+        if grow > LATE_FROM:
+            break
+        s -= 1
+    return s
 
 
 def half(x):
@@ -67,7 +79,7 @@ def parts_of(s, fine):
 def model(G, coefficients=MUON, eps=1e-7, scale=1.0, steps=5, gen=None):
     """scale * X with the kernels' roundings; gen: a generator of disturbances."""
     abc = steps_of(coefficients, steps)
-    fine = fine_steps(abc)
+    fine, late = fine_steps(abc), late_step(abc)
     X = ortho.wide(G.double())
     X = X / (X.norm() + eps)
 
@@ -95,7 +107,7 @@ def model(G, coefficients=MUON, eps=1e-7, scale=1.0, steps=5, gen=None):
             B = B + c * off(A, A)
         d = B.diagonal().clone()
         B = half(B - torch.diag(d))
-        X = a * (hi + lo) + d[:, None] * hi + B @ hi + off(B, hi, False)
+        X = a * (hi + lo) + d[:, None] * (hi + lo if s >= late else hi) + B @ hi + off(B, hi, False)
         if gen is not None:
             X = X * (1 + 2.0 ** -24 * rand(X.shape))
     X = scale * X

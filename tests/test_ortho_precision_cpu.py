@@ -26,6 +26,12 @@ def test_fine_steps():
     assert om.fine_steps([(0.1, 0.0, 0.0)] * 3 + [om.MUON] * 6) == 4
 
 
+def test_late_step():
+    assert [om.late_step([om.MUON] * n) for n in (1, 2, 3, 5, 8)] == [0, 0, 1, 3, 6]
+    assert om.late_step([(1.5, -0.5, 0.0)] * 9) == 5 and om.late_step([(0.5, 0.0, 0.0)] * 9) == 0
+    assert om.late_step([om.MUON] * 3 + [(5.0, 0.0, 0.0)]) == 3
+
+
 def planted(kind, G, steps):
     X = ortho.wide(G.double())
     X = X / (X.norm() + 1e-7)
@@ -50,17 +56,17 @@ def planted(kind, G, steps):
     return X
 
 
-# Where each is seen.  (Without lo noise is as exact as with it: a lo without B lo beside it
-# is no gain there.  b off by 0.2 % weighs less than FP32's errors at rank 1 after eight steps.)
+# Where each is seen.  (After eight steps noise is as exact without lo: a lo without B lo
+# beside it is no gain there.  b off by 0.2 % weighs less than FP32's errors at rank 1 after eight steps.)
 LOW = ("rank1", "rank4")
 NOT_NOISE = tuple(k for k in om.KINDS if k != "noise")
 CAUGHT = {
-    "no lo": {5: NOT_NOISE, 8: NOT_NOISE},
+    "no lo": {5: om.KINDS, 8: NOT_NOISE},
     "fp16": {5: om.KINDS, 8: om.KINDS},
     "bf16": {5: om.KINDS, 8: om.KINDS},
     "b": {5: om.KINDS, 8: om.KINDS[1:]},
-    "e5m2": {5: LOW + ("decay6",), 8: LOW + ("decay4", "decay6")},
-    "d lo": {5: LOW + ("decay4", "decay6"), 8: LOW + ("decay4", "decay6")},
+    "e5m2": {5: LOW + ("noise", "few", "decay6"), 8: LOW + ("decay4", "decay6")},
+    "d lo": {5: LOW + ("noise", "decay4", "decay6"), 8: LOW + ("decay4", "decay6")},
 }
 
 
