@@ -13,7 +13,11 @@ the largest of them and cuts them off behind 24 bits (Fasi, Higham, Mikaitis and
 Numerical behavior of NVIDIA tensor cores, 2021): K products are cut off, each by up to
 2^-23 of a binade that is up to twice the sum, evenly, so by 2 * 2^-23 / sqrt(12) usually,
 and all of them by sqrt(K) times that, sqrt(K) 2^-23.8 of a sum that is the sum of the
-magnitudes at most: sqrt(K) 2^-24 of the latter are taken.  (2^-21 for any K, as if only
+magnitudes at most: sqrt(K) 2^-24 of the latter are taken.  What is cut off is cut off
+towards zero, so where the products have one sign it adds up: up to K times half of 2^-23 of
+the sum so far, which is half the sum usually, in a binade of up to twice that: K 2^-24 of
+the sum at most (a side of 65536: 2^-8; A of one column: 2^-11 in eight parts of K, seen),
+of which each product of a run takes a part between none and all.  (2^-21 for any K, as if only
 sums were cut off, is a sixth of it at K = 2048 and falls short.)  X' is disturbed by 2^-24,
 the factor of G by 2^-22 (the norm's FP32 part, the quotient, the product) and each of its
 products by a rounding.  A disturbed run stands for the kernels': its distance
@@ -90,8 +94,10 @@ def model(G, coefficients=MUON, eps=1e-7, scale=1.0, steps=5, gen=None):
         if gen is None:
             return 0.0
         magnitudes = x.abs() @ y.abs()
-        n = x.shape[1] ** 0.5 * 2.0 ** -24 * rand(magnitudes.shape) * magnitudes
-        return (n + n.mT) / 2 ** 0.5 if symmetric else n
+        k = x.shape[1]
+        n = k ** 0.5 * 2.0 ** -24 * rand(magnitudes.shape) * magnitudes
+        cut = k * 2.0 ** -24 * float(torch.rand(1, generator=gen)) * (x @ y)
+        return ((n + n.mT) / 2 ** 0.5 if symmetric else n) - cut
 
     if gen is not None:
         X = (X * (1 + 2.0 ** -22 * float(rand((1,))))).float().double()
