@@ -17,8 +17,9 @@
  * (2^-28) before steps that with those behind them enlarge a rounding by more than 512
  * (the product of their a); the products take the FP16 part.
  * Besides its own rounding to BF16 (0.0017 of its norm) O is off by
- *   five usual steps: 0.0002 to 0.0015 of its norm, on spectra from rank 1 to noise (the
- *     most where rank 1 to 4 meets sides of thousands);
+ *   five usual steps: 0.0002 to 0.0016 of its norm, on spectra from rank 1 to noise (the
+ *     most where rank 1 to 4 meets sides of thousands, and of noise on sides of tens; a
+ *     handful of elements can be off by 0.006);
  *   eight: 0.001 to 0.002 where no singular value is far below 10^-6 of the largest.
  * An error in the directions of singular values near 0 grows by a (3.4) in every step,
  * and the sums' FP32 errors, sqrt(sides) 2^-25, are one: of rank 1 to 4 O is off by 0.002
